@@ -677,6 +677,111 @@ CF_API cf_status cf_unfused_gemm_rowsoftmax(const void *X, const void *W, const 
                                             void *workspace, size_t workspace_bytes,
                                             cf_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Grouped GEMM: every group of rows has its own weights                     */
+/* ------------------------------------------------------------------------ */
+typedef enum { CF_BF16 = 0, CF_FP16 = 1 } cf_dtype;  /* 16-bit operand types */
+
+/* Y[r, :] = act(X[r, :] . W[e]) for the rows r in [offsets[e], offsets[e+1])
+ *
+ * The products of a mixture of experts, its rows sorted by expert, in the
+ * directions that training and serving need; the activation is one more
+ * stage-1 node on the accumulator ([sass2mlir] "Epilogue fusion - the core
+ * technique").  The pages have no grouped product: this stands beside
+ * cf_gemm_fused_*, in which every row shares W.
+ *   X       (device) `dtype` [T, K]            W  (device) `dtype` [E, K, N]
+ *   offsets (device) int32 [E + 1], not decreasing, within [0, T]: the sizes
+ *           are read on the device, so no host copy of them is needed.  A
+ *           group may be empty.  Rows before offsets[0] and from offsets[E] on
+ *           belong to no group: they are not written.
+ *   Y       (device) `dtype` [T, N], written (round to nearest even)
+ *   Z       (device) `dtype` [T, N] or NULL: receives X . W[e], rounded, for
+ *           the gradient; the activation is applied to the unrounded product
+ * cf_grouped_gemm_dgrad: dX[r, :] = (dY[r, :] . W[e]^T) * act'(Z[r, :]) with
+ *   dY [T, N], Z and dX [T, K]; Z is the pre-activation of the layer that made
+ *   the rows X (act GELU(tanh)), or NULL for none.  dX may be Z.
+ * cf_grouped_gemm_wgrad: dW[e] = sum of X[r, :]^T dY[r, :] over the group's
+ *   rows, [E, K, N]; an empty group's dW is written as zeros.
+ * Accumulation is fp32 in tensor memory, in an order that depends on the
+ * sizes alone: equal calls give equal bits.  An infinity or NaN in one group
+ * reaches no other, in rows of no group none.
+ * Supported: T >= 0, E in 0..1024 (either 0 is a no-op; wgrad with T = 0
+ * writes zeros), N and K positive multiples of 8, no matrix aliasing an input
+ * (but dX = Z); 16-byte aligned matrices and workspace.  Offsets that decrease
+ * or leave [0, T] are clamped, and reported as CF_ERR_DEVICE_BOUNDS.
+ * workspace (device) >= cf_grouped_gemm_workspace_size() bytes, any of the
+ * three directions; zeroed once, one launch at a time, as for every call.
+ * Tuning fields used (_ex): n_slice (accumulator columns: 32, 64, 128, 256;
+ * wgrad from 64 on), stages, max_clusters (cap on CTAs), timeout_us, disable_pdl. */
+CF_API size_t cf_grouped_gemm_workspace_size(int64_t T, int64_t N, int64_t K, int64_t E);
+
+CF_API cf_status cf_grouped_gemm(const void *X, const void *W, const int32_t *offsets, void *Y, void *Z,
+                                 int64_t T, int64_t N, int64_t K, int64_t E, cf_dtype dtype,
+                                 cf_activation act, void *workspace, size_t workspace_bytes,
+                                 cf_stream_t stream);
+
+CF_API cf_status cf_grouped_gemm_ex(const void *X, const void *W, const int32_t *offsets, void *Y, void *Z,
+                                    int64_t T, int64_t N, int64_t K, int64_t E, cf_dtype dtype,
+                                    cf_activation act, void *workspace, size_t workspace_bytes,
+                                    cf_stream_t stream, const cf_tuning *tuning);
+
+CF_API cf_status cf_grouped_gemm_dgrad(const void *dY, const void *W, const int32_t *offsets,
+                                       const void *Z, void *dX, int64_t T, int64_t N, int64_t K, int64_t E,
+                                       cf_dtype dtype, void *workspace, size_t workspace_bytes,
+                                       cf_stream_t stream);
+
+CF_API cf_status cf_grouped_gemm_dgrad_ex(const void *dY, const void *W, const int32_t *offsets,
+                                          const void *Z, void *dX, int64_t T, int64_t N, int64_t K,
+                                          int64_t E, cf_dtype dtype, void *workspace,
+                                          size_t workspace_bytes, cf_stream_t stream,
+                                          const cf_tuning *tuning);
+
+CF_API cf_status cf_grouped_gemm_wgrad(const void *X, const void *dY, const int32_t *offsets, void *dW,
+                                       int64_t T, int64_t N, int64_t K, int64_t E, cf_dtype dtype,
+                                       void *workspace, size_t workspace_bytes, cf_stream_t stream);
+
+CF_API cf_status cf_grouped_gemm_wgrad_ex(const void *X, const void *dY, const int32_t *offsets, void *dW,
+                                          int64_t T, int64_t N, int64_t K, int64_t E, cf_dtype dtype,
+                                          void *workspace, size_t workspace_bytes, cf_stream_t stream,
+                                          const cf_tuning *tuning);
+
+/* ------------------------------------------------------------------------ */
+/* Shared projection with the low-rank adapters of many requests             */
+/* ------------------------------------------------------------------------ */
+/* Y[r, :] = X[r, :] . W + bias + scale[a] * (X[r, :] . A[a]) . B[a]
+ *
+ * with a = adapters[s] for the rows r of request s, [offsets[s],
+ * offsets[s+1]): one batch in which each request has its own fine-tuned
+ * weights, a low-rank term beside the projection that all share.  The
+ * [T, R] product in the middle is two small GEMMs back to back ([ComFuse]
+ * B2BGEMM) and is held in fp32; the second is an epilogue of the projection.
+ *   X (device) `dtype` [T, K]      W (device) `dtype` [K, N]
+ *   bias (device) fp32 [N] or NULL
+ *   A (device) `dtype` [L, K, R]   B (device) `dtype` [L, R, N]
+ *   offsets  (device) int32 [S + 1] as for cf_grouped_gemm
+ *   adapters (device) int32 [S], each in 0..L-1, or -1 for the projection alone
+ *   scale    (device) fp32 [L], or NULL for 1
+ *   Y (device) `dtype` [T, N], written; rows of no request are not
+ * Supported: T >= 0, S in 0..1024 (either 0 is a no-op), L >= 0, N and K
+ * positive multiples of 8, R a multiple of 8 up to 128 (a smaller rank is
+ * padded with zeros); Y not an input; 16-byte aligned.  An infinity or NaN in
+ * an adapter reaches the rows of its own requests only.  Indices outside -1..L-1 are
+ * taken as -1 and reported as CF_ERR_DEVICE_BOUNDS, as are bad offsets.
+ * workspace (device) >= cf_gemm_lora_workspace_size() bytes.
+ * Tuning fields used (_ex): those of cf_grouped_gemm_ex, for the projection. */
+CF_API size_t cf_gemm_lora_workspace_size(int64_t T, int64_t N, int64_t K, int64_t S, int64_t R);
+
+CF_API cf_status cf_gemm_lora(const void *X, const void *W, const float *bias, const void *A, const void *B,
+                              const int32_t *offsets, const int32_t *adapters, const float *scale, void *Y,
+                              int64_t T, int64_t N, int64_t K, int64_t S, int64_t L, int64_t R,
+                              cf_dtype dtype, void *workspace, size_t workspace_bytes, cf_stream_t stream);
+
+CF_API cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *bias, const void *A,
+                                 const void *B, const int32_t *offsets, const int32_t *adapters,
+                                 const float *scale, void *Y, int64_t T, int64_t N, int64_t K, int64_t S,
+                                 int64_t L, int64_t R, cf_dtype dtype, void *workspace,
+                                 size_t workspace_bytes, cf_stream_t stream, const cf_tuning *tuning);
+
 #ifdef __cplusplus
 }
 #endif

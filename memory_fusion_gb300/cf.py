@@ -7,6 +7,7 @@ fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -154,6 +155,21 @@ _SIGS = {
     "cf_stitch_rowreduce_broadcast": (_ST, [_P, _P, _P, _I64, _I64, _P, _SZ, _P]),
     "cf_stitch_rowreduce_broadcast_ex": (_ST, [_P, _P, _P, _I64, _I64, _P, _SZ, _P,
                                                ctypes.POINTER(cf_tuning)]),
+    "cf_grouped_gemm_workspace_size": (_SZ, [_I64, _I64, _I64, _I64]),
+    "cf_grouped_gemm": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _P, _SZ, _P]),
+    "cf_grouped_gemm_ex": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _P, _SZ, _P,
+                                 ctypes.POINTER(cf_tuning)]),
+    "cf_grouped_gemm_dgrad": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, ctypes.c_int, _P, _SZ, _P]),
+    "cf_grouped_gemm_dgrad_ex": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, ctypes.c_int, _P, _SZ, _P,
+                                       ctypes.POINTER(cf_tuning)]),
+    "cf_grouped_gemm_wgrad": (_ST, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, ctypes.c_int, _P, _SZ, _P]),
+    "cf_grouped_gemm_wgrad_ex": (_ST, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, ctypes.c_int, _P, _SZ, _P,
+                                       ctypes.POINTER(cf_tuning)]),
+    "cf_gemm_lora_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "cf_gemm_lora": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_int, _P,
+                           _SZ, _P]),
+    "cf_gemm_lora_ex": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_int,
+                              _P, _SZ, _P, ctypes.POINTER(cf_tuning)]),
     "cf_stitch_powadd_softmax": (_ST, [_P, _P, _F, _P, _I64, _I64, _P, _SZ, _P]),
     "cf_stitch_powadd_softmax_ex": (_ST, [_P, _P, _F, _P, _I64, _I64, _P, _SZ, _P, ctypes.POINTER(cf_tuning)]),
 }
@@ -630,3 +646,204 @@ def stitch_powadd_softmax(A, w, p, *, out=None, workspace=None, stream=None, tun
     check(cf_stitch_powadd_softmax(A, w, float(p), O, rows, cols, ws, ws.numel(), stream, tuning),
           "cf_stitch_powadd_softmax")
     return O
+
+
+# ---------------------------------------------------------------------------
+# grouped GEMM and low-rank adapters
+# ---------------------------------------------------------------------------
+CF_BF16 = 0
+CF_FP16 = 1
+
+
+def cf_grouped_gemm_workspace_size(T, N, K, E) -> int:
+    return lib().cf_grouped_gemm_workspace_size(T, N, K, E)
+
+
+def cf_grouped_gemm(X, W, offsets, Y, Z, T, N, K, E, dtype, act, workspace, workspace_bytes, stream=None,
+                    tuning=None) -> int:
+    """Y = act(X . W[e]) for the rows of each group e; Z (or None) receives the pre-activation."""
+    L = lib()
+    if tuning is None:
+        return L.cf_grouped_gemm(_ptr(X), _ptr(W), _ptr(offsets), _ptr(Y), _ptr(Z), T, N, K, E, dtype, act,
+                                 _ptr(workspace), workspace_bytes, _stream(stream))
+    return L.cf_grouped_gemm_ex(_ptr(X), _ptr(W), _ptr(offsets), _ptr(Y), _ptr(Z), T, N, K, E, dtype, act,
+                                _ptr(workspace), workspace_bytes, _stream(stream), _tun(tuning))
+
+
+def cf_grouped_gemm_dgrad(dY, W, offsets, Z, dX, T, N, K, E, dtype, workspace, workspace_bytes, stream=None,
+                          tuning=None) -> int:
+    """dX = (dY . W[e]^T) * act'(Z) for the rows of each group e (Z may be None)."""
+    L = lib()
+    if tuning is None:
+        return L.cf_grouped_gemm_dgrad(_ptr(dY), _ptr(W), _ptr(offsets), _ptr(Z), _ptr(dX), T, N, K, E, dtype,
+                                       _ptr(workspace), workspace_bytes, _stream(stream))
+    return L.cf_grouped_gemm_dgrad_ex(_ptr(dY), _ptr(W), _ptr(offsets), _ptr(Z), _ptr(dX), T, N, K, E, dtype,
+                                      _ptr(workspace), workspace_bytes, _stream(stream), _tun(tuning))
+
+
+def cf_grouped_gemm_wgrad(X, dY, offsets, dW, T, N, K, E, dtype, workspace, workspace_bytes, stream=None,
+                          tuning=None) -> int:
+    """dW[e] = X^T . dY over the rows of each group e."""
+    L = lib()
+    if tuning is None:
+        return L.cf_grouped_gemm_wgrad(_ptr(X), _ptr(dY), _ptr(offsets), _ptr(dW), T, N, K, E, dtype,
+                                       _ptr(workspace), workspace_bytes, _stream(stream))
+    return L.cf_grouped_gemm_wgrad_ex(_ptr(X), _ptr(dY), _ptr(offsets), _ptr(dW), T, N, K, E, dtype,
+                                      _ptr(workspace), workspace_bytes, _stream(stream), _tun(tuning))
+
+
+def cf_gemm_lora_workspace_size(T, N, K, S, R) -> int:
+    return lib().cf_gemm_lora_workspace_size(T, N, K, S, R)
+
+
+def cf_gemm_lora(X, W, bias, A, B, offsets, adapters, scale, Y, T, N, K, S, L, R, dtype, workspace, workspace_bytes,
+                 stream=None, tuning=None) -> int:
+    """Y = X . W + bias + scale[a] * (X . A[a]) . B[a], a the adapter of the row's request (-1: none)."""
+    lb = lib()
+    if tuning is None:
+        return lb.cf_gemm_lora(_ptr(X), _ptr(W), _ptr(bias), _ptr(A), _ptr(B), _ptr(offsets), _ptr(adapters),
+                               _ptr(scale), _ptr(Y), T, N, K, S, L, R, dtype, _ptr(workspace), workspace_bytes,
+                               _stream(stream))
+    return lb.cf_gemm_lora_ex(_ptr(X), _ptr(W), _ptr(bias), _ptr(A), _ptr(B), _ptr(offsets), _ptr(adapters),
+                              _ptr(scale), _ptr(Y), T, N, K, S, L, R, dtype, _ptr(workspace), workspace_bytes,
+                              _stream(stream), _tun(tuning))
+
+
+def _operand(name, t, shape, dtype, device):
+    """Check one tensor argument; sizes of None in `shape` are free."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
+    if t.dim() != len(shape) or any(n is not None and int(s) != int(n) for s, n in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple('*' if n is None else n for n in shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+def _grouped_dtype(name, t):
+    import torch
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} is on {t.device}, not on a CUDA device")
+    if t.dtype == torch.bfloat16:
+        return CF_BF16
+    if t.dtype == torch.float16:
+        return CF_FP16
+    raise ValueError(f"{name} has dtype {t.dtype}, not bfloat16 or float16")
+
+
+@contextlib.contextmanager
+def _launch_on(device, stream):
+    """The operands' device, and `stream` (a torch stream or a handle; None = the device's current one), made current:
+    outputs and workspaces allocated inside belong to the stream that uses them."""
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+            with torch.cuda.stream(s):
+                yield
+
+
+def _act(act):
+    acts = {"none": CF_ACT_NONE, "gelu_tanh": CF_ACT_GELU_TANH}
+    if act not in acts:
+        raise ValueError(f"unknown activation {act!r}")
+    return acts[act]
+
+
+def grouped_gemm(X, W, offsets, *, act="none", preact=None, out=None, workspace=None, stream=None, tuning=None):
+    """Y[r] = act(X[r] @ W[e]) for the rows r in [offsets[e], offsets[e+1]); X [T, K] and W [E, K, N] bf16 or fp16
+    CUDA tensors, offsets int32 [E + 1] on the same device.  `preact` ([T, N]) receives the unactivated product for
+    grouped_gemm_dgrad.  Rows of no group are not written: in a new output they hold anything."""
+    import torch
+    dt, dev = _grouped_dtype("X", X), X.device
+    a = _act(act)
+    _operand("X", X, (None, None), X.dtype, dev)
+    T, K = X.shape
+    _operand("W", W, (None, K, None), X.dtype, dev)
+    E, _, N = W.shape
+    _operand("offsets", offsets, (E + 1,), torch.int32, dev)
+    for name, t in (("preact", preact), ("out", out)):
+        if t is not None:
+            _operand(name, t, (T, N), X.dtype, dev)
+    with _launch_on(dev, stream):
+        Y = out if out is not None else torch.empty((T, N), dtype=X.dtype, device=dev)
+        ws = workspace if workspace is not None else new_workspace(cf_grouped_gemm_workspace_size(T, N, K, E), dev)
+        check(cf_grouped_gemm(X, W, offsets, Y, preact, T, N, K, E, dt, a, ws, ws.numel(), None, tuning),
+              "cf_grouped_gemm")
+    return Y
+
+
+def grouped_gemm_dgrad(dY, W, offsets, *, preact=None, out=None, workspace=None, stream=None, tuning=None):
+    """dX[r] = (dY[r] @ W[e].T) * gelu_tanh'(preact[r]) for the rows of each group; dY [T, N], W [E, K, N],
+    preact [T, K] or None (no activation before these rows).  out may be preact."""
+    import torch
+    dt, dev = _grouped_dtype("dY", dY), dY.device
+    _operand("dY", dY, (None, None), dY.dtype, dev)
+    T, N = dY.shape
+    _operand("W", W, (None, None, N), dY.dtype, dev)
+    E, K, _ = W.shape
+    _operand("offsets", offsets, (E + 1,), torch.int32, dev)
+    for name, t in (("preact", preact), ("out", out)):
+        if t is not None:
+            _operand(name, t, (T, K), dY.dtype, dev)
+    with _launch_on(dev, stream):
+        dX = out if out is not None else torch.empty((T, K), dtype=dY.dtype, device=dev)
+        ws = workspace if workspace is not None else new_workspace(cf_grouped_gemm_workspace_size(T, N, K, E), dev)
+        check(cf_grouped_gemm_dgrad(dY, W, offsets, preact, dX, T, N, K, E, dt, ws, ws.numel(), None, tuning),
+              "cf_grouped_gemm_dgrad")
+    return dX
+
+
+def grouped_gemm_wgrad(X, dY, offsets, *, out=None, workspace=None, stream=None, tuning=None):
+    """dW[e] = X[rows of e].T @ dY[rows of e] (zeros for an empty group), [E, K, N]; X [T, K], dY [T, N]."""
+    import torch
+    dt, dev = _grouped_dtype("X", X), X.device
+    _operand("X", X, (None, None), X.dtype, dev)
+    T, K = X.shape
+    _operand("dY", dY, (T, None), X.dtype, dev)
+    N = dY.shape[1]
+    _operand("offsets", offsets, (None,), torch.int32, dev)
+    E = offsets.shape[0] - 1
+    if E < 0:
+        raise ValueError("offsets is empty: it has one entry more than there are groups")
+    if out is not None:
+        _operand("out", out, (E, K, N), X.dtype, dev)
+    with _launch_on(dev, stream):
+        dW = out if out is not None else torch.empty((E, K, N), dtype=X.dtype, device=dev)
+        ws = workspace if workspace is not None else new_workspace(cf_grouped_gemm_workspace_size(T, N, K, E), dev)
+        check(cf_grouped_gemm_wgrad(X, dY, offsets, dW, T, N, K, E, dt, ws, ws.numel(), None, tuning),
+              "cf_grouped_gemm_wgrad")
+    return dW
+
+
+def gemm_lora(X, W, bias, A, B, offsets, adapters, *, scale=None, out=None, workspace=None, stream=None, tuning=None):
+    """Y[r] = X[r] @ W + bias + scale[a] * (X[r] @ A[a]) @ B[a] for the rows r of request s,
+    [offsets[s], offsets[s+1]), with a = adapters[s] (-1: no adapter).  X [T, K], W [K, N], A [L, K, R], B [L, R, N]
+    bf16 or fp16; bias fp32 [N] or None; offsets int32 [S + 1], adapters int32 [S], scale fp32 [L] or None (1)."""
+    import torch
+    dt, dev = _grouped_dtype("X", X), X.device
+    _operand("X", X, (None, None), X.dtype, dev)
+    T, K = X.shape
+    _operand("W", W, (K, None), X.dtype, dev)
+    N = W.shape[1]
+    _operand("A", A, (None, K, None), X.dtype, dev)
+    L, _, R = A.shape
+    _operand("B", B, (L, R, N), X.dtype, dev)
+    _operand("adapters", adapters, (None,), torch.int32, dev)
+    S = adapters.shape[0]
+    _operand("offsets", offsets, (S + 1,), torch.int32, dev)
+    if bias is not None:
+        _operand("bias", bias, (N,), torch.float32, dev)
+    if scale is not None:
+        _operand("scale", scale, (L,), torch.float32, dev)
+    if out is not None:
+        _operand("out", out, (T, N), X.dtype, dev)
+    with _launch_on(dev, stream):
+        Y = out if out is not None else torch.empty((T, N), dtype=X.dtype, device=dev)
+        ws = workspace if workspace is not None else new_workspace(cf_gemm_lora_workspace_size(T, N, K, S, R), dev)
+        check(cf_gemm_lora(X, W, bias, A, B, offsets, adapters, scale, Y, T, N, K, S, L, R, dt, ws, ws.numel(), None,
+                           tuning), "cf_gemm_lora")
+    return Y

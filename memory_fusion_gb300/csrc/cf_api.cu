@@ -1319,3 +1319,294 @@ extern "C" cf_status cf_unfused_gemm_rowsoftmax(const void *X, const void *W, co
     return unfused_common(2, X, W, bias, nullptr, nullptr, Y, M, N, K, scale, 0.f, workspace, workspace_bytes,
                           stream);
 }
+
+// =========================================================================
+// Grouped GEMM and low-rank adapters
+// =========================================================================
+namespace {
+
+// weights [count, rows, cols] 16-bit, cols contiguous, as a 3-D tensor; outside reads as zero
+bool make_tmap_weights(CUtensorMap *m, const void *ptr, uint64_t count, uint64_t rows, uint64_t cols,
+                       uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {cols, rows, count};
+    cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
+    cuuint32_t box[3] = {64, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+constexpr int64_t kGroupedMaxDim = int64_t(1) << 24;
+
+// sizes every grouped call checks before it looks at a pointer
+cf_status grouped_sizes(int64_t T, int64_t N, int64_t K, int64_t groups, int dtype) {
+    if (T < 0 || N <= 0 || K <= 0 || groups < 0) return CF_ERR_INVALID_ARG;
+    if (dtype != CF_BF16 && dtype != CF_FP16) return CF_ERR_INVALID_ARG;
+    if (N % 8 != 0 || K % 8 != 0) return CF_ERR_UNSUPPORTED;  // TMA rows are multiples of 16 bytes
+    if (N > kGroupedMaxDim || K > kGroupedMaxDim || N * K >= (int64_t(1) << 39)) return CF_ERR_UNSUPPORTED;
+    if (T > (int64_t(1) << 31) - 512 || groups > cf::kGroupedMaxGroups) return CF_ERR_UNSUPPORTED;
+    return CF_OK;
+}
+
+// Accumulator columns, ring depth and grid of one grouped launch.
+// Columns (rows of the batch; WGRAD: columns of dW): four times the mean group,
+// so that an uneven group still reads its weights once, between 32 and 256.
+cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t N, int64_t groups, int64_t rank, const cf_tuning &t,
+                       const cf::DeviceInfo &dev, cf::GroupedArgs *a, int *ctas, int *smem) {
+    int64_t want;
+    if (kind == cf::GR_WGRAD) want = N;
+    else if (kind == cf::GR_LORA) want = T;
+    else want = std::min<int64_t>(T, 4 * ((T + groups - 1) / groups));
+    const int least = kind == cf::GR_WGRAD ? 64 : 32;  // WGRAD stages dY in 64-column blocks
+    int bn = least;
+    while (bn < 256 && bn < want) bn *= 2;
+    if (t.n_slice != 0) {
+        if (t.n_slice != 32 && t.n_slice != 64 && t.n_slice != 128 && t.n_slice != 256) return CF_ERR_UNSUPPORTED;
+        if (t.n_slice < least) return CF_ERR_UNSUPPORTED;
+        bn = t.n_slice;
+    }
+    if (t.stages < 0 || t.stages > 12) return CF_ERR_UNSUPPORTED;
+    int stages = t.stages > 0 ? t.stages : 12;
+    while (stages > 2 && cf::grouped_smem_bytes(kind, stages, bn, int(groups), int(rank)) > kMaxSmem) --stages;
+    *smem = cf::grouped_smem_bytes(kind, stages, bn, int(groups), int(rank));
+    if (*smem > kMaxSmem || *smem > dev.max_smem_optin) return CF_ERR_UNSUPPORTED;
+    const int64_t ft = (F + 127) / 128;
+    const int64_t tiles = kind == cf::GR_WGRAD ? groups * ft * ((N + bn - 1) / bn)
+                                               : ft * std::min<int64_t>(T, T / bn + groups);
+    if (tiles >= (int64_t(1) << 31) - 65536) return CF_ERR_UNSUPPORTED;
+    int64_t c = std::min<int64_t>(tiles, dev.sm_count);
+    if (t.max_clusters > 0) c = std::min<int64_t>(c, t.max_clusters);
+    *ctas = int(std::max<int64_t>(c, 1));
+    a->bn = bn;
+    a->stages = stages;
+    return CF_OK;
+}
+
+// the fields every kind shares
+void grouped_args(cf::GroupedArgs *a, int64_t T, int64_t F, int64_t C, int64_t N, int64_t groups, int dtype,
+                  const int32_t *offsets, void *ws, const cf_tuning &t) {
+    std::memset(a, 0, sizeof(*a));
+    a->offsets = offsets;
+    a->err = static_cast<uint32_t *>(ws);
+    a->T = int(T);
+    a->F = int(F);
+    a->C = int(C);
+    a->N = int(N);
+    a->groups = int(groups);
+    a->fp16 = dtype == CF_FP16;
+    a->timeout_ns = 1000ull * (t.timeout_us ? t.timeout_us : kDefaultTimeoutUs);
+}
+
+cf_status launch_grouped_checked(int kind, const cf::GroupedArgs &a, int ctas, int smem, const cf_tuning &t,
+                                 cf_stream_t stream) {
+    cudaError_t e =
+        cf::launch_grouped(kind, a, ctas, smem, t.disable_pdl == 0, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CF_OK : cuda_fail(e);
+}
+
+// forward (rows X [T,K], features N) and input gradient (rows dY [T,N], features K)
+cf_status grouped_rows(int kind, const void *rows, const void *W, const int32_t *offsets, void *out, void *preact,
+                       int64_t T, int64_t N, int64_t K, int64_t E, int dtype, cf_activation act, void *ws,
+                       size_t ws_bytes, cf_stream_t stream, const cf_tuning *tuning) {
+    cf_status st = grouped_sizes(T, N, K, E, dtype);
+    if (st != CF_OK) return st;
+    if (act != CF_ACT_NONE && act != CF_ACT_GELU_TANH) return CF_ERR_INVALID_ARG;
+    if (!ws) return CF_ERR_INVALID_ARG;
+    if (T == 0 || E == 0) return CF_OK;  // no row belongs to a group
+    if (!rows || !W || !offsets || !out) return CF_ERR_INVALID_ARG;
+    if (!aligned16(rows) || !aligned16(W) || !aligned16(out) || !aligned16(ws) || (preact && !aligned16(preact)) ||
+        (reinterpret_cast<uintptr_t>(offsets) & 3u) != 0)
+        return CF_ERR_MISALIGNED;
+    if (out == rows || out == W) return CF_ERR_INVALID_ARG;
+    if (preact && (preact == W || preact == rows || (kind == cf::GR_FORWARD && preact == out)))
+        return CF_ERR_INVALID_ARG;
+    if (ws_bytes < cf_grouped_gemm_workspace_size(T, N, K, E)) return CF_ERR_WORKSPACE_TOO_SMALL;
+    cf_tuning tz;
+    cf_tuning_default(&tz);
+    const cf_tuning &t = tuning ? *tuning : tz;
+    cf::DeviceInfo dev;
+    if (!cf::current_device_info(&dev)) return CF_ERR_NO_DEVICE;
+    if (dev.cc_major != 10 || dev.cc_minor != 3) return CF_ERR_NO_DEVICE;
+    const bool fwd = kind == cf::GR_FORWARD;
+    const int64_t F = fwd ? N : K, C = fwd ? K : N;
+    cf::GroupedArgs a;
+    grouped_args(&a, T, F, C, 0, E, dtype, offsets, ws, t);
+    int ctas, smem;
+    st = plan_grouped(kind, T, F, 0, E, 0, t, dev, &a, &ctas, &smem);
+    if (st != CF_OK) return st;
+    if (!make_tmap_weights(&a.tmap_a, W, uint64_t(E), uint64_t(K), uint64_t(N), fwd ? 64 : 128) ||
+        !make_tmap_bf16(&a.tmap_b, rows, uint64_t(T), uint64_t(C), 64, 64) ||
+        !make_tmap_bf16(&a.tmap_b16, rows, uint64_t(T), uint64_t(C), 64, 16))
+        return CF_ERR_CUDA;
+    a.out = out;
+    a.preact = preact;
+    a.act = act == CF_ACT_GELU_TANH;
+    return launch_grouped_checked(kind, a, ctas, smem, t, stream);
+}
+
+}  // namespace
+
+extern "C" size_t cf_grouped_gemm_workspace_size(int64_t T, int64_t N, int64_t K, int64_t E) {
+    (void)T;
+    (void)N;
+    (void)K;
+    (void)E;
+    return cf::kErrBytes;
+}
+
+extern "C" cf_status cf_grouped_gemm_ex(const void *X, const void *W, const int32_t *offsets, void *Y, void *Z,
+                                        int64_t T, int64_t N, int64_t K, int64_t E, cf_dtype dtype, cf_activation act,
+                                        void *workspace, size_t workspace_bytes, cf_stream_t stream,
+                                        const cf_tuning *tuning) {
+    return grouped_rows(cf::GR_FORWARD, X, W, offsets, Y, Z, T, N, K, E, int(dtype), act, workspace, workspace_bytes,
+                        stream, tuning);
+}
+
+extern "C" cf_status cf_grouped_gemm(const void *X, const void *W, const int32_t *offsets, void *Y, void *Z, int64_t T,
+                                     int64_t N, int64_t K, int64_t E, cf_dtype dtype, cf_activation act,
+                                     void *workspace, size_t workspace_bytes, cf_stream_t stream) {
+    return cf_grouped_gemm_ex(X, W, offsets, Y, Z, T, N, K, E, dtype, act, workspace, workspace_bytes, stream, nullptr);
+}
+
+extern "C" cf_status cf_grouped_gemm_dgrad_ex(const void *dY, const void *W, const int32_t *offsets, const void *Z,
+                                              void *dX, int64_t T, int64_t N, int64_t K, int64_t E, cf_dtype dtype,
+                                              void *workspace, size_t workspace_bytes, cf_stream_t stream,
+                                              const cf_tuning *tuning) {
+    return grouped_rows(cf::GR_DGRAD, dY, W, offsets, dX, const_cast<void *>(Z), T, N, K, E, int(dtype),
+                        Z ? CF_ACT_GELU_TANH : CF_ACT_NONE, workspace, workspace_bytes, stream, tuning);
+}
+
+extern "C" cf_status cf_grouped_gemm_dgrad(const void *dY, const void *W, const int32_t *offsets, const void *Z,
+                                           void *dX, int64_t T, int64_t N, int64_t K, int64_t E, cf_dtype dtype,
+                                           void *workspace, size_t workspace_bytes, cf_stream_t stream) {
+    return cf_grouped_gemm_dgrad_ex(dY, W, offsets, Z, dX, T, N, K, E, dtype, workspace, workspace_bytes, stream,
+                                    nullptr);
+}
+
+extern "C" cf_status cf_grouped_gemm_wgrad_ex(const void *X, const void *dY, const int32_t *offsets, void *dW,
+                                              int64_t T, int64_t N, int64_t K, int64_t E, cf_dtype dtype,
+                                              void *workspace, size_t workspace_bytes, cf_stream_t stream,
+                                              const cf_tuning *tuning) {
+    cf_status st = grouped_sizes(T, N, K, E, int(dtype));
+    if (st != CF_OK) return st;
+    if (!workspace) return CF_ERR_INVALID_ARG;
+    if (E == 0) return CF_OK;
+    if (!dW || (T > 0 && (!X || !dY || !offsets))) return CF_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(dY) || !aligned16(dW) || !aligned16(workspace) ||
+        (reinterpret_cast<uintptr_t>(offsets) & 3u) != 0)
+        return CF_ERR_MISALIGNED;
+    if (dW == X || dW == dY) return CF_ERR_INVALID_ARG;
+    if (workspace_bytes < cf_grouped_gemm_workspace_size(T, N, K, E)) return CF_ERR_WORKSPACE_TOO_SMALL;
+    cf_tuning tz;
+    cf_tuning_default(&tz);
+    const cf_tuning &t = tuning ? *tuning : tz;
+    cf::DeviceInfo dev;
+    if (!cf::current_device_info(&dev)) return CF_ERR_NO_DEVICE;
+    if (dev.cc_major != 10 || dev.cc_minor != 3) return CF_ERR_NO_DEVICE;
+    if (T == 0) {  // every sum is empty
+        cudaError_t e = cudaMemsetAsync(dW, 0, size_t(E) * size_t(K) * size_t(N) * 2,
+                                        reinterpret_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? CF_OK : cuda_fail(e);
+    }
+    cf::GroupedArgs a;
+    grouped_args(&a, T, K, 0, N, E, int(dtype), offsets, workspace, t);
+    int ctas, smem;
+    st = plan_grouped(cf::GR_WGRAD, T, K, N, E, 0, t, dev, &a, &ctas, &smem);
+    if (st != CF_OK) return st;
+    if (!make_tmap_bf16(&a.tmap_a, X, uint64_t(T), uint64_t(K), 64, 64) ||
+        !make_tmap_bf16(&a.tmap_b, dY, uint64_t(T), uint64_t(N), 64, 64))
+        return CF_ERR_CUDA;
+    a.tmap_b16 = a.tmap_b;
+    a.out = dW;
+    return launch_grouped_checked(cf::GR_WGRAD, a, ctas, smem, t, stream);
+}
+
+extern "C" cf_status cf_grouped_gemm_wgrad(const void *X, const void *dY, const int32_t *offsets, void *dW, int64_t T,
+                                           int64_t N, int64_t K, int64_t E, cf_dtype dtype, void *workspace,
+                                           size_t workspace_bytes, cf_stream_t stream) {
+    return cf_grouped_gemm_wgrad_ex(X, dY, offsets, dW, T, N, K, E, dtype, workspace, workspace_bytes, stream, nullptr);
+}
+
+// workspace: error word, then H [T, R] fp32
+extern "C" size_t cf_gemm_lora_workspace_size(int64_t T, int64_t N, int64_t K, int64_t S, int64_t R) {
+    (void)N;
+    (void)K;
+    (void)S;
+    if (T < 0 || R < 0) return cf::kErrBytes;
+    return cf::kErrBytes + cf::align_up(size_t(T) * size_t(R) * 4, 256);
+}
+
+extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *bias, const void *A, const void *B,
+                                     const int32_t *offsets, const int32_t *adapters, const float *scale, void *Y,
+                                     int64_t T, int64_t N, int64_t K, int64_t S, int64_t L, int64_t R, cf_dtype dtype,
+                                     void *workspace, size_t workspace_bytes, cf_stream_t stream,
+                                     const cf_tuning *tuning) {
+    cf_status st = grouped_sizes(T, N, K, S, int(dtype));
+    if (st != CF_OK) return st;
+    if (L < 0 || R <= 0) return CF_ERR_INVALID_ARG;
+    if (R % 8 != 0 || R > cf::kLoraMaxRank || L > (int64_t(1) << 24)) return CF_ERR_UNSUPPORTED;
+    if (!workspace) return CF_ERR_INVALID_ARG;
+    if (T == 0 || S == 0) return CF_OK;
+    if (!X || !W || !offsets || !adapters || !Y || (L > 0 && (!A || !B))) return CF_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(W) || !aligned16(A) || !aligned16(B) || !aligned16(Y) || !aligned16(workspace) ||
+        (bias && !aligned16(bias)) || (reinterpret_cast<uintptr_t>(offsets) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(adapters) & 3u) != 0 || (reinterpret_cast<uintptr_t>(scale) & 3u) != 0)
+        return CF_ERR_MISALIGNED;
+    if (Y == X || Y == W || (L > 0 && (Y == A || Y == B))) return CF_ERR_INVALID_ARG;
+    if (workspace_bytes < cf_gemm_lora_workspace_size(T, N, K, S, R)) return CF_ERR_WORKSPACE_TOO_SMALL;
+    cf_tuning tz;
+    cf_tuning_default(&tz);
+    const cf_tuning &t = tuning ? *tuning : tz;
+    cf::DeviceInfo dev;
+    if (!cf::current_device_info(&dev)) return CF_ERR_NO_DEVICE;
+    if (dev.cc_major != 10 || dev.cc_minor != 3) return CF_ERR_NO_DEVICE;
+    float *H = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + cf::kErrBytes);
+    cf::GroupedArgs sh, a;
+    int sh_ctas = 0, sh_smem = 0, ctas, smem;
+    if (L > 0) {
+        cf_tuning ts = t;
+        ts.n_slice = ts.stages = 0;  // the knobs are the main product's
+        grouped_args(&sh, T, R, K, 0, S, int(dtype), offsets, workspace, t);
+        st = plan_grouped(cf::GR_SHRINK, T, R, 0, S, 0, ts, dev, &sh, &sh_ctas, &sh_smem);
+        if (st != CF_OK) return st;
+        if (!make_tmap_weights(&sh.tmap_a, A, uint64_t(L), uint64_t(K), uint64_t(R), 64) ||
+            !make_tmap_bf16(&sh.tmap_b, X, uint64_t(T), uint64_t(K), 64, 64) ||
+            !make_tmap_bf16(&sh.tmap_b16, X, uint64_t(T), uint64_t(K), 64, 16))
+            return CF_ERR_CUDA;
+        sh.windex = adapters;
+        sh.nweights = int(L);
+        sh.scale = scale;
+        sh.out = H;
+    }
+    grouped_args(&a, T, N, K, 0, S, int(dtype), offsets, workspace, t);
+    a.rank = int(R);
+    st = plan_grouped(cf::GR_LORA, T, N, 0, S, R, t, dev, &a, &ctas, &smem);
+    if (st != CF_OK) return st;
+    if (!make_tmap_weights(&a.tmap_a, W, 1, uint64_t(K), uint64_t(N), 64) ||
+        !make_tmap_bf16(&a.tmap_b, X, uint64_t(T), uint64_t(K), 64, 64) ||
+        !make_tmap_bf16(&a.tmap_b16, X, uint64_t(T), uint64_t(K), 64, 16))
+        return CF_ERR_CUDA;
+    a.windex = adapters;
+    a.nweights = int(L);
+    a.bias = bias;
+    a.low = H;
+    a.lora_b = B;
+    a.out = Y;
+    if (L > 0) {
+        st = launch_grouped_checked(cf::GR_SHRINK, sh, sh_ctas, sh_smem, t, stream);
+        if (st != CF_OK) return st;
+    }
+    return launch_grouped_checked(cf::GR_LORA, a, ctas, smem, t, stream);
+}
+
+extern "C" cf_status cf_gemm_lora(const void *X, const void *W, const float *bias, const void *A, const void *B,
+                                  const int32_t *offsets, const int32_t *adapters, const float *scale, void *Y,
+                                  int64_t T, int64_t N, int64_t K, int64_t S, int64_t L, int64_t R, cf_dtype dtype,
+                                  void *workspace, size_t workspace_bytes, cf_stream_t stream) {
+    return cf_gemm_lora_ex(X, W, bias, A, B, offsets, adapters, scale, Y, T, N, K, S, L, R, dtype, workspace,
+                           workspace_bytes, stream, nullptr);
+}

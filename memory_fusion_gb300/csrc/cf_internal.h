@@ -221,4 +221,48 @@ constexpr size_t kB2bWorkspaceBytes = kB2bFoldPartialsOff + size_t(kB2bFoldSplit
 cudaError_t launch_b2b_ln_fold(const void *W2, const float *gamma1, const float *beta1, int N1, int N2,
                                unsigned char *ws, bool pdl, cudaStream_t stream);
 
+// --------------------------------------------------------------------------
+// grouped GEMM and low-rank adapters (gemm_grouped.cu)
+// --------------------------------------------------------------------------
+enum GroupedKind : int {
+    GR_FORWARD = 0,  // Y = act(X_g . W_g), optionally keeping the pre-activation
+    GR_DGRAD = 1,    // dX = (dY_g . W_g^T) (* act'(Z))
+    GR_WGRAD = 2,    // dW_g = X_g^T . dY_g
+    GR_SHRINK = 3,   // H = scale[a] * X_g . A_a in fp32 (adapters: groups are requests)
+    GR_LORA = 4,     // Y = X . W + bias + H . B_a, one group of all the requests' rows
+};
+
+constexpr int kGroupedMaxGroups = 1024;  // the group table lives in shared memory
+constexpr int kLoraMaxRank = 128;        // one tile of features in the first product
+
+struct GroupedArgs {
+    CUtensorMap tmap_a;    // the operand whose features become accumulator lanes: W (WGRAD: X)
+    CUtensorMap tmap_b;    // the operand whose rows become accumulator columns: X or dY, box 64 rows (WGRAD: dY)
+    CUtensorMap tmap_b16;  // the same in boxes of 16 rows
+    const int32_t *offsets;  // [groups + 1] rows of each group (LORA: of each request)
+    const int32_t *windex;   // SHRINK, LORA: [groups] adapter of each request, -1 for none
+    void *out;               // Y / dX / dW / H
+    void *preact;            // FORWARD: Z written; DGRAD: Z read; or null
+    const float *bias;       // LORA: [F] or null
+    const float *scale;      // SHRINK: [nweights] or null
+    const float *low;        // LORA: H [T, rank]
+    const void *lora_b;      // LORA: B [nweights, rank, F]
+    uint32_t *err;
+    int T;                   // rows of X / dY
+    int F;                   // features: length of the accumulator-lane axis of the result
+    int C;                   // contraction length (WGRAD: the groups' rows instead)
+    int N;                   // WGRAD: columns of dW
+    int groups;
+    int nweights;            // weights that windex may name
+    int rank;                // LORA
+    int fp16;                // 16-bit type of every operand: 0 bf16, 1 fp16
+    int act;                 // FORWARD, DGRAD: 1 = GELU(tanh)
+    int bn;                  // columns of one accumulator tile (32, 64, 128 or 256)
+    int stages;
+    unsigned long long timeout_ns;
+};
+
+int grouped_smem_bytes(int kind, int stages, int bn, int groups, int rank);
+cudaError_t launch_grouped(int kind, const GroupedArgs &a, int ctas, int smem, bool pdl, cudaStream_t stream);
+
 }  // namespace cf

@@ -1,0 +1,584 @@
+// gemm_grouped.cu -- products whose rows choose their weights, on tcgen05:
+//     FORWARD  Y = act(X_g . W_g)             rows [offsets[g], offsets[g+1]) of X with W[g]
+//     DGRAD    dX = (dY_g . W_g^T) * act'(Z)
+//     WGRAD    dW_g = X_g^T . dY_g            a sum over the group's rows
+//     SHRINK   H = scale[a] * X_g . A[a]      groups are requests, a their adapter
+//     LORA     Y = X . W + bias + H . B[a]    the shared projection with the adapters' second product
+//
+// Design:
+//  * Features are the accumulator's lanes and rows of the batch its columns:
+//    D^T[128 features, n rows] = W^T . X^T.  A group of a few rows then costs an
+//    MMA of N = 16 and a 2 KB row tile instead of a 128-row tile that is mostly
+//    padding: a decode batch reads weights and little else.  The last tile of a
+//    group takes the N it needs (multiples of 16), and a group's tiles are cut
+//    evenly.  Columns behind a group's rows hold its neighbour's products: a
+//    column depends on its own row alone, so they are not stored and nothing
+//    of them (a NaN, say) can reach the group.
+//  * WGRAD sums over rows, so there the neighbour's rows must not take part:
+//    the last block of a group issues the MMAs that hold its rows and zeroes, in
+//    shared memory, what is left of the last 16.
+//  * Group sizes are device data.  Every CTA scans the offsets into a table in
+//    shared memory and walks the same tile list; no host synchronisation.
+//    Offsets that decrease or pass T are clamped and reported
+//    (CF_ERR_DEVICE_BOUNDS), so no read or write leaves its array.
+//  * Warp roles as in the fused GEMM: warp 0 issues TMA loads into a ring,
+//    warp 1 the MMAs into one of two accumulators, warps 2..9 the epilogue of
+//    tile i while tile i + 1 is multiplied; every wait is bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/cf.h"
+#include "cf_internal.h"
+#include "ptx.cuh"
+#include "umma.cuh"
+
+namespace cf {
+namespace {
+
+constexpr int kThreads = 320;   // 10 warps
+constexpr int kEpiWarps = 8;    // warps 2..9: two halves of 4 warps (128 lanes each)
+constexpr int kHalfThreads = 128;
+constexpr int kBK = 64;         // contraction per stage (128 bytes: one swizzle atom)
+constexpr int kFB = 128;        // features per tile (accumulator lanes)
+constexpr int kABytes = kFB * kBK * 2;
+constexpr int kRasterRows = 16;  // row tiles walked before the next feature tile
+constexpr int kRankChunk = 32;   // LORA: ranks of B held in registers at once
+
+constexpr uint32_t kInfoProducer = 0x10000000u;
+constexpr uint32_t kInfoMma = 0x20000000u;
+constexpr uint32_t kInfoEpi = 0x30000000u;
+constexpr uint32_t kInfoTable = 0x70000000u;
+
+struct GrLayout {
+    uint32_t stage_bytes, table, stg, low, bars, total;
+};
+
+__host__ __device__ inline GrLayout gr_layout(int kind, int stages, int bn, int groups, int rank) {
+    GrLayout L;
+    L.stage_bytes = uint32_t(kABytes + bn * kBK * 2);
+    uint32_t off = uint32_t(stages) * L.stage_bytes;
+    L.table = off;  // int off[groups + 1], int pre[groups + 1]
+    off += (uint32_t(2 * (groups + 1)) * 4u + 15u) & ~15u;
+    L.stg = off;    // LORA: fp32 [32 rows][33] per epilogue warp
+    off += kind == GR_LORA ? uint32_t(kEpiWarps) * 32u * 33u * 4u : 0u;
+    L.low = off;    // LORA: fp32 [32 rows][rank] per half
+    off += kind == GR_LORA ? 2u * 32u * uint32_t(rank) * 4u : 0u;
+    L.bars = (off + 15u) & ~15u;
+    L.total = L.bars + 256u;
+    return L;
+}
+
+struct GrBars {
+    uint32_t full0, empty0, tmem_full0, tmem_empty0, mma_done, misc;
+};
+__device__ __forceinline__ GrBars gr_bars(uint32_t base, int stages) {
+    GrBars b;
+    b.full0 = base;
+    b.empty0 = base + 8 * stages;
+    b.tmem_full0 = base + 16 * stages;
+    b.tmem_empty0 = b.tmem_full0 + 16;
+    b.mma_done = b.tmem_empty0 + 16;
+    b.misc = b.mma_done + 8;
+    return b;
+}
+static_assert(16 * 12 + 16 + 16 + 8 + 8 <= 256, "barrier area");
+
+// one tile of work
+struct Tile {
+    int g;      // group
+    int w;      // its weights
+    int f0;     // first feature
+    int col0;   // first accumulator column's row of the batch (WGRAD: column of dW)
+    int n;      // columns that exist
+    int nm;     // columns multiplied (n rounded up to 16)
+    int nk;     // 64-deep blocks of the contraction
+    int row0;   // WGRAD: first row of the group
+    int rows;   // WGRAD: rows of the group
+};
+
+template <int KIND>
+struct Walk {
+    const int *off, *pre;
+    const GroupedArgs &a;
+    int ft;      // feature tiles
+    int g;       // group of the current tile (tiles are visited in ascending order)
+
+    __device__ Walk(const int *off_, const int *pre_, const GroupedArgs &a_) : off(off_), pre(pre_), a(a_), g(0) {
+        ft = (a.F + kFB - 1) / kFB;
+    }
+    __device__ int total() const { return pre[groups()]; }
+    __device__ int groups() const { return KIND == GR_LORA ? 1 : a.groups; }
+    __device__ Tile at(int t) {
+        while (t >= pre[g + 1]) ++g;
+        Tile r;
+        r.g = g;
+        r.w = KIND == GR_SHRINK ? a.windex[g] : (KIND == GR_LORA ? 0 : g);
+        const int local = t - pre[g];
+        const int lo = off[KIND == GR_LORA ? 0 : g];
+        const int rows = off[KIND == GR_LORA ? a.groups : g + 1] - lo;
+        if constexpr (KIND == GR_WGRAD) {
+            const int nt = (a.N + a.bn - 1) / a.bn;
+            r.f0 = (local / nt) * kFB;
+            r.col0 = (local % nt) * a.bn;
+            r.n = min(a.bn, a.N - r.col0);
+            r.row0 = lo;
+            r.rows = rows;
+            r.nk = (rows + kBK - 1) / kBK;
+        } else {
+            const int rt = (rows + a.bn - 1) / a.bn;              // row tiles of the group,
+            const int per = (((rows + rt - 1) / rt) + 15) & ~15;  // cut evenly
+            const int chunk = local / (kRasterRows * ft);
+            const int wide = min(kRasterRows, rt - chunk * kRasterRows);
+            const int in = local - chunk * kRasterRows * ft;
+            const int rtile = chunk * kRasterRows + in % wide;
+            r.f0 = (in / wide) * kFB;
+            r.col0 = lo + rtile * per;
+            r.n = min(per, rows - rtile * per);
+            r.row0 = r.rows = 0;
+            r.nk = (a.C + kBK - 1) / kBK;
+        }
+        r.nm = (r.n + 15) & ~15;
+        return r;
+    }
+};
+
+// GELU in the tanh form is z * p with p = 1 / (1 + exp(-2u)), u = sqrt(2/pi)(z + 0.044715 z^3):
+// no cancellation in the left tail, where 1 + tanh(u) would lose every digit
+__device__ __forceinline__ float gelu_p(float z) {
+    const float u = 0.7978845608028654f * fmaf(0.044715f * z, z * z, z);
+    return __fdividef(1.f, 1.f + ptx::ex2_approx(-2.885390081777927f * u));
+}
+__device__ __forceinline__ float gelu(float z) { return z * gelu_p(z); }
+// d/dz of that: p + 2 z p (1 - p) u'.  Beyond |z| = 12, p is 0 or 1 to fp32 and the second term
+// vanishes; the clamp keeps z^2 finite there (and a NaN stays one)
+__device__ __forceinline__ float gelu_slope(float z) {
+    const float c = fabsf(z) > 12.f ? copysignf(12.f, z) : z;
+    const float p = gelu_p(c);
+    const float du = 0.7978845608028654f * fmaf(0.134145f * c, c, 1.f);
+    return fmaf(2.f * c * p * (1.f - p), du, p);
+}
+
+__device__ __forceinline__ uint16_t to16(float v, bool fp16) {
+    return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
+    return uint32_t(to16(lo, fp16)) | (uint32_t(to16(hi, fp16)) << 16);
+}
+__device__ __forceinline__ float from16(uint16_t v, bool fp16) {
+    return fp16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(uint32_t(v) << 16);
+}
+
+// Group table: off[i] = offsets[i] clamped to [0, T] and to not decrease, pre[i] = tiles of the groups
+// before i.  One warp, after the raw offsets are in off[].
+template <int KIND>
+__device__ void scan_table(int *off, int *pre, const GroupedArgs &a, uint32_t *err) {
+    const int lane = threadIdx.x & 31;
+    const int n = a.groups + 1;
+    const int ft = (a.F + kFB - 1) / kFB;
+    bool bad = false;
+    int run_max = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        const int raw = i < n ? off[i] : 0;
+        int v = min(max(raw, 0), a.T);
+        const int own = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, v, d);
+            if (lane >= d) v = max(v, o);
+        }
+        v = max(v, run_max);
+        if (i < n) {
+            bad |= v != own || own != raw;
+            off[i] = v;
+        }
+        run_max = __shfl_sync(0xffffffffu, v, 31);
+    }
+    __syncwarp();
+    const int groups = KIND == GR_LORA ? 1 : a.groups;
+    int carry = 0;
+    for (int i0 = 0; i0 < groups; i0 += 32) {
+        const int i = i0 + lane;
+        int tiles = 0;
+        if (i < groups) {
+            const int rows = off[KIND == GR_LORA ? a.groups : i + 1] - off[i];
+            if constexpr (KIND == GR_WGRAD) {
+                tiles = ft * ((a.N + a.bn - 1) / a.bn);
+            } else {
+                tiles = ft * ((rows + a.bn - 1) / a.bn);
+                if constexpr (KIND == GR_SHRINK) {
+                    const int w = a.windex[i];
+                    bad |= w < -1 || w >= a.nweights;
+                    if (w < 0 || w >= a.nweights) tiles = 0;
+                }
+            }
+        }
+        int s = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += o;
+        }
+        if (i < groups) pre[i + 1] = carry + s;
+        carry += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) pre[0] = 0;
+    if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
+        ptx::record_error(err, 8u /*CF_ERR_DEVICE_BOUNDS*/, kInfoTable);
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_constant__ GroupedArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t base = ptx::smem_u32(smem_raw);
+    if ((base & 1023u) != 0u) {  // the swizzled operand tiles need it; see the fused GEMM
+        ptx::griddep_wait();
+        if (threadIdx.x == 0) ptx::record_error(a.err, 8u, 0x60000000u | (base & 1023u));
+        return;
+    }
+    constexpr bool kAMn = KIND != GR_DGRAD;  // features contiguous in memory: A is MN-major
+    constexpr bool kBMn = KIND == GR_WGRAD;
+    const int stages = a.stages;
+    const GrLayout L = gr_layout(KIND, stages, a.bn, a.groups, a.rank);
+    const GrBars B = gr_bars(base + L.bars, stages);
+    int *const off = reinterpret_cast<int *>(smem_raw + L.table);
+    int *const pre = off + a.groups + 1;
+    volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem_raw + (B.misc - base));
+    volatile uint32_t *abort = misc + 1;
+    const uint64_t tmo = a.timeout_ns;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t tmem_cols = uint32_t(2 * a.bn);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            ptx::mbar_init(B.full0 + 8 * s, 1);
+            ptx::mbar_init(B.empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(B.tmem_full0 + 8 * b, 1);
+            ptx::mbar_init(B.tmem_empty0 + 8 * b, kEpiWarps);
+        }
+        ptx::mbar_init(B.mma_done, 1);
+        misc[1] = 0u;
+        ptx::fence_mbarrier_init_cluster();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(B.misc, tmem_cols);
+        ptx::tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        ptx::prefetch_tensormap(&a.tmap_a);
+        ptx::prefetch_tensormap(&a.tmap_b);
+        ptx::prefetch_tensormap(&a.tmap_b16);
+    }
+    // The next grid may start only once this CTA holds its tensor memory: a dependent CTA that took it first
+    // would wait for this grid while this grid waited for the columns.
+    __syncthreads();
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    for (int i = threadIdx.x; i <= a.groups; i += kThreads) off[i] = a.offsets[i];
+    __syncthreads();
+    if (warp == 0) scan_table<KIND>(off, pre, a, a.err);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = misc[0];
+    Walk<KIND> walk(off, pre, a);
+    const int total = walk.total();
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            uint32_t it = 0, s = 0, ph = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                const Tile w = walk.at(t);
+                const int ablocks = kAMn ? (a.F - w.f0 > 64 ? 2 : 1) : 1;
+                // columns: whole 64s, then 16s (WGRAD: 64-column blocks)
+                const int b64 = kBMn ? (w.n + 63) / 64 : w.nm / 64;
+                const int b16 = kBMn ? 0 : (w.nm % 64) / 16;
+                const uint32_t tx = uint32_t(kAMn ? ablocks * 8192 : kABytes) + uint32_t(b64 * 8192 + b16 * 2048);
+                for (int kb = 0; kb < w.nk; ++kb) {
+                    ok = ptx::mbar_wait_bounded(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
+                    if (!ok) break;
+                    const uint32_t sa = base + s * L.stage_bytes;
+                    const uint32_t sb = sa + kABytes;
+                    const uint32_t fb = B.full0 + 8 * s;
+                    ptx::mbar_arrive_expect_tx(fb, tx);
+                    if constexpr (KIND == GR_WGRAD) {
+                        const int y = w.row0 + kb * kBK;
+                        for (int i = 0; i < ablocks; ++i)
+                            ptx::tma_load_2d(sa + i * 8192, &a.tmap_a, fb, w.f0 + 64 * i, y);
+                        for (int i = 0; i < b64; ++i)
+                            ptx::tma_load_2d(sb + i * 8192, &a.tmap_b, fb, w.col0 + 64 * i, y);
+                    } else {
+                        if constexpr (kAMn) {
+                            for (int i = 0; i < ablocks; ++i)
+                                ptx::tma_load_3d(sa + i * 8192, &a.tmap_a, fb, w.f0 + 64 * i, kb * kBK, w.w);
+                        } else {
+                            ptx::tma_load_3d(sa, &a.tmap_a, fb, kb * kBK, w.f0, w.w);
+                        }
+                        for (int i = 0; i < b64; ++i)
+                            ptx::tma_load_2d(sb + i * 8192, &a.tmap_b, fb, kb * kBK, w.col0 + 64 * i);
+                        for (int i = 0; i < b16; ++i)
+                            ptx::tma_load_2d(sb + b64 * 8192 + i * 2048, &a.tmap_b16, fb, kb * kBK,
+                                             w.col0 + 64 * b64 + 16 * i);
+                    }
+                    ++it;
+                    if (++s == uint32_t(stages)) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            // every load has landed and been read before the CTA may leave
+            const uint32_t first = it > uint32_t(stages) ? it - uint32_t(stages) : 0u;
+            for (uint32_t i = first; i < it; ++i) {
+                volatile uint32_t local_abort = 0;
+                ptx::mbar_wait_bounded(B.empty0 + 8 * (i % uint32_t(stages)), (i / uint32_t(stages)) & 1u, tmo,
+                                       &local_abort, nullptr, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        // (WGRAD: the whole warp, which zeroes the rows behind a group in its last block)
+        if (lane == 0 || KIND == GR_WGRAD) {
+            const uint64_t ad0 = kAMn ? sw128_desc(base, 8192, 1024) : sw128_desc(base, 16, 1024);
+            const uint64_t bd0 = kBMn ? sw128_desc(base + kABytes, 8192, 1024) : sw128_desc(base + kABytes, 16, 1024);
+            uint32_t s = 0, ph = 0;
+            int tile = 0;
+            for (int t = blockIdx.x; t < total; t += gridDim.x, ++tile) {
+                const Tile w = walk.at(t);
+                const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
+                bool ok = ptx::mbar_wait_bounded(B.tmem_empty0 + 8 * buf, tph ^ 1u, tmo, abort, a.err, kInfoMma | buf);
+                if constexpr (KIND == GR_WGRAD) ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint32_t d = tmem_base + buf * uint32_t(a.bn);
+                const uint32_t idesc = idesc_f16(kFB, w.nm, a.fp16 != 0, kAMn, kBMn);
+                for (int kb = 0; kb < w.nk; ++kb) {
+                    ok = ptx::mbar_wait_bounded(B.full0 + 8 * s, ph, tmo, abort, a.err, kInfoMma | 0x100u | s);
+                    if constexpr (KIND == GR_WGRAD) ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const int left = (KIND == GR_WGRAD ? w.rows : a.C) - kb * kBK;
+                    const int steps = left >= kBK ? kBK / 16 : (left + 15) / 16;
+                    if constexpr (KIND == GR_WGRAD) {
+                        if (left < kBK && (left & 15) != 0) {
+                            // rows left .. 16*steps - 1 of every 64-column block (a row is 128 bytes of it)
+                            uint8_t *const st = smem_raw + s * L.stage_bytes;
+                            const int blocks = 2 + (w.n + 63) / 64;
+                            const int per = (16 * steps - left) * 8;  // 16-byte pieces per block
+                            for (int i = lane; i < blocks * per; i += 32) {
+                                const int blk = i / per, p = i % per;
+                                uint8_t *q = st + (blk < 2 ? blk * 8192 : kABytes + (blk - 2) * 8192) + left * 128 + p * 16;
+                                *reinterpret_cast<uint4 *>(q) = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                            ptx::fence_proxy_async_smem();
+                        }
+                        __syncwarp();
+                    }
+                    ptx::tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t so = uint64_t((s * L.stage_bytes) >> 4);
+                        for (int k = 0; k < steps; ++k)
+                            ptx::mma_bf16(d, ad0 + so + uint64_t(k * (kAMn ? 128 : 2)),
+                                          bd0 + so + uint64_t(k * (kBMn ? 128 : 2)), idesc, (kb | k) != 0 ? 1u : 0u);
+                        ptx::mma_commit(B.empty0 + 8 * s);
+                    }
+                    if (++s == uint32_t(stages)) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (lane == 0) ptx::mma_commit(B.tmem_full0 + 8 * buf);
+            }
+            if (lane == 0) {
+                ptx::mma_commit(B.mma_done);
+                volatile uint32_t local_abort = 0;
+                ptx::mbar_wait_bounded(B.mma_done, 0, tmo, &local_abort, nullptr, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ epilogue
+        // thread = one feature (TMEM lane); the two halves of 4 warps take alternate 32-column fragments
+        const int e = warp - 2;
+        const int half = e >> 2;
+        const int q = warp & 3;
+        const bool fp16 = a.fp16 != 0;
+        int tile = 0;
+        for (int t = blockIdx.x; t < total; t += gridDim.x, ++tile) {
+            const Tile w = walk.at(t);
+            const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
+            const bool ok = ptx::mbar_wait_bounded(B.tmem_full0 + 8 * buf, tph, tmo, abort, a.err, kInfoEpi | buf);
+            ptx::tc_fence_after();
+            const uint32_t tacc = tmem_base + (uint32_t(q * 32) << 16) + buf * uint32_t(a.bn);
+            const int f = w.f0 + q * 32 + lane;
+            const bool live = f < a.F && ok;
+            for (int c = half * 32; c < w.n; c += 64) {
+                uint32_t v[32];
+                ptx::tmem_ld32(tacc + uint32_t(c), v);
+                ptx::tmem_ld_wait();
+                const int cols = min(32, w.n - c);
+                if constexpr (KIND == GR_FORWARD || KIND == GR_DGRAD) {
+                    uint16_t *y = static_cast<uint16_t *>(a.out) + size_t(w.col0 + c) * a.F + f;
+                    uint16_t *z = a.preact ? static_cast<uint16_t *>(a.preact) + size_t(w.col0 + c) * a.F + f : nullptr;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (live && j < cols) {
+                            float x = __uint_as_float(v[j]);
+                            if constexpr (KIND == GR_FORWARD) {
+                                if (z) z[size_t(j) * a.F] = to16(x, fp16);
+                                if (a.act) x = gelu(x);
+                            } else if (z) {
+                                x *= gelu_slope(from16(z[size_t(j) * a.F], fp16));
+                            }
+                            y[size_t(j) * a.F] = to16(x, fp16);
+                        }
+                    }
+                } else if constexpr (KIND == GR_SHRINK) {
+                    const float sc = a.scale ? a.scale[w.w] : 1.f;
+                    float *y = static_cast<float *>(a.out) + size_t(w.col0 + c) * a.F + f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (live && j < cols) y[size_t(j) * a.F] = sc * __uint_as_float(v[j]);
+                } else if constexpr (KIND == GR_WGRAD) {
+                    if (live) {
+                        uint16_t *y = static_cast<uint16_t *>(a.out) + (size_t(w.g) * a.F + f) * a.N + w.col0 + c;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            if (j < cols) {  // N is a multiple of 8
+                                uint32_t p[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)  // an empty group's sum is zero
+                                    p[i] = w.nk == 0 ? 0u
+                                                     : pack16(__uint_as_float(v[j + 2 * i]),
+                                                              __uint_as_float(v[j + 2 * i + 1]), fp16);
+                                *reinterpret_cast<uint4 *>(y + j) = make_uint4(p[0], p[1], p[2], p[3]);
+                            }
+                        }
+                    }
+                } else {  // GR_LORA
+                    // The adapters' second product on the CUDA cores, in fp32, one row after another: rows of
+                    // different requests never share an instruction, so a NaN in one adapter stays with its
+                    // own requests.
+                    float *const stg = reinterpret_cast<float *>(smem_raw + L.stg) + e * (32 * 33);
+                    float *const low = reinterpret_cast<float *>(smem_raw + L.low) + half * 32 * a.rank;
+                    const int rank = a.rank;
+                    const int row0 = w.col0 + c;
+                    ptx::named_bar_sync(1 + half, kHalfThreads);  // the half is done with the last fragment's rows
+                    {
+                        const int tid = (e & 3) * 32 + lane;
+                        const float4 *src = reinterpret_cast<const float4 *>(a.low + size_t(row0) * rank);
+                        for (int i = tid; i < cols * rank / 4; i += kHalfThreads)
+                            reinterpret_cast<float4 *>(low)[i] = src[i];
+                    }
+                    const float bv = (a.bias && live) ? a.bias[f] : 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) stg[j * 33 + lane] = __uint_as_float(v[j]) + bv;
+                    ptx::named_bar_sync(1 + half, kHalfThreads);
+                    // the request of the first row: the last one that starts at or before it
+                    int lo = 0, hi = a.groups - 1;
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (off[mid] <= row0) lo = mid;
+                        else hi = mid - 1;
+                    }
+                    int j0 = 0;
+                    for (int sgm = lo; sgm < a.groups && j0 < cols; ++sgm) {
+                        const int j1 = min(cols, off[sgm + 1] - row0);
+                        const int ad = a.windex[sgm];
+                        if (j1 > j0 && ad >= 0 && ad < a.nweights && live) {
+                            const uint16_t *bp = static_cast<const uint16_t *>(a.lora_b) + (size_t(ad) * rank) * a.F + f;
+                            for (int r0 = 0; r0 < rank; r0 += kRankChunk) {
+                                float b[kRankChunk];
+#pragma unroll
+                                for (int r = 0; r < kRankChunk; ++r)
+                                    b[r] = r0 + r < rank ? from16(__ldg(bp + size_t(r0 + r) * a.F), fp16) : 0.f;
+                                for (int j = j0; j < j1; ++j) {
+                                    const float4 *h = reinterpret_cast<const float4 *>(low + j * rank + r0);
+                                    float s0 = stg[j * 33 + lane], s1 = 0.f;
+#pragma unroll
+                                    for (int r = 0; r < kRankChunk; r += 8) {
+                                        if (r0 + r < rank) {  // rank is a multiple of 8
+                                            const float4 h0 = h[r / 4], h1 = h[r / 4 + 1];
+                                            ptx::fma2(s0, s1, h0.x, h0.y, b[r], b[r + 1], s0, s1);
+                                            ptx::fma2(s0, s1, h0.z, h0.w, b[r + 2], b[r + 3], s0, s1);
+                                            ptx::fma2(s0, s1, h1.x, h1.y, b[r + 4], b[r + 5], s0, s1);
+                                            ptx::fma2(s0, s1, h1.z, h1.w, b[r + 6], b[r + 7], s0, s1);
+                                        }
+                                    }
+                                    stg[j * 33 + lane] = s0 + s1;
+                                }
+                            }
+                        }
+                        j0 = max(j0, j1);
+                    }
+                    uint16_t *y = static_cast<uint16_t *>(a.out) + size_t(row0) * a.F + f;
+                    if (live)
+                        for (int j = 0; j < cols; ++j) y[size_t(j) * a.F] = to16(stg[j * 33 + lane], fp16);
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(B.tmem_empty0 + 8 * buf);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc(tmem_base, tmem_cols);
+}
+
+void *kernel_for(int kind) {
+    switch (kind) {
+        case GR_FORWARD: return reinterpret_cast<void *>(&grouped_kernel<GR_FORWARD>);
+        case GR_DGRAD: return reinterpret_cast<void *>(&grouped_kernel<GR_DGRAD>);
+        case GR_WGRAD: return reinterpret_cast<void *>(&grouped_kernel<GR_WGRAD>);
+        case GR_SHRINK: return reinterpret_cast<void *>(&grouped_kernel<GR_SHRINK>);
+        case GR_LORA: return reinterpret_cast<void *>(&grouped_kernel<GR_LORA>);
+        default: return nullptr;
+    }
+}
+
+}  // namespace
+
+int grouped_smem_bytes(int kind, int stages, int bn, int groups, int rank) {
+    return int(gr_layout(kind, stages, bn, groups, rank).total);
+}
+
+cudaError_t launch_grouped(int kind, const GroupedArgs &a, int ctas, int smem, bool pdl, cudaStream_t stream) {
+    void *fn = kernel_for(kind);
+    if (!fn) return cudaErrorInvalidValue;
+    static int set_smem[64][8] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidValue;
+    if (smem > set_smem[dev][kind]) {  // once per device and kernel, to the largest size: none under capture later
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        set_smem[dev][kind] = smem;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    void *args[] = {(void *)&a};
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace cf

@@ -76,6 +76,11 @@ import math
 import numpy as np
 
 __all__ = [
+    "gelu_tanh_slope",
+    "grouped_gemm",
+    "grouped_gemm_dgrad",
+    "grouped_gemm_wgrad",
+    "gemm_lora",
     "gemm",
     "gemm_naive",
     "gelu_tanh",
@@ -440,3 +445,55 @@ def stitch_powadd_softmax(A, w, p: float, rows=None) -> np.ndarray:
         out[o:o + idx.size] = softmax_rows(y)
         o += idx.size
     return out
+
+
+def gelu_tanh_slope(x) -> np.ndarray:
+    """d/dx of gelu_tanh: (1 + t)/2 + x (1 - t^2)/2 * s (1 + 3*0.044715 x^2), t = tanh(s (x + 0.044715 x^3))."""
+    x = _f64(x)
+    s = math.sqrt(2.0 / math.pi)
+    t = np.tanh(s * (x + 0.044715 * x ** 3))
+    return 0.5 * (1.0 + t) + 0.5 * x * (1.0 - t * t) * s * (1.0 + 3.0 * 0.044715 * x * x)
+
+
+def grouped_gemm(X, W, offsets, *, act: str = "none"):
+    """(Y, Z): for the rows r in [offsets[e], offsets[e+1]), Z[r] = X[r].W[e] and Y[r] = act(Z[r]).
+
+    Rows of no group are zero in both."""
+    X, W = _f64(X), _f64(W)
+    Z = np.zeros((X.shape[0], W.shape[2]))
+    for e in range(W.shape[0]):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        Z[lo:hi] = X[lo:hi] @ W[e]
+    return (gelu_tanh(Z) if act == "gelu_tanh" else Z.copy()), Z
+
+
+def grouped_gemm_dgrad(dY, W, offsets, *, preact=None) -> np.ndarray:
+    """dX[r] = (dY[r].W[e]^T) * gelu_tanh'(preact[r]) for the rows of each group; rows of no group are zero."""
+    dY, W = _f64(dY), _f64(W)
+    dX = np.zeros((dY.shape[0], W.shape[1]))
+    for e in range(W.shape[0]):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        dX[lo:hi] = dY[lo:hi] @ W[e].T
+        if preact is not None:
+            dX[lo:hi] *= gelu_tanh_slope(preact[lo:hi])
+    return dX
+
+
+def grouped_gemm_wgrad(X, dY, offsets) -> np.ndarray:
+    """dW[e] = X[rows of e]^T.dY[rows of e]; zero for an empty group."""
+    X, dY = _f64(X), _f64(dY)
+    return np.stack([X[int(lo):int(hi)].T @ dY[int(lo):int(hi)] for lo, hi in zip(offsets[:-1], offsets[1:])])
+
+
+def gemm_lora(X, W, bias, A, B, offsets, adapters, scale=None) -> np.ndarray:
+    """Y[r] = X[r].W + bias + scale[a] (X[r].A[a]).B[a], a the adapter of the row's request (-1: none).
+
+    Rows of no request are zero."""
+    X, W = _f64(X), _f64(W)
+    Y = np.zeros((X.shape[0], W.shape[1]))
+    for s in range(len(adapters)):
+        lo, hi, a = int(offsets[s]), int(offsets[s + 1]), int(adapters[s])
+        Y[lo:hi] = X[lo:hi] @ W + (0.0 if bias is None else _f64(bias))
+        if a >= 0:
+            Y[lo:hi] += (1.0 if scale is None else float(scale[a])) * ((X[lo:hi] @ _f64(A[a])) @ _f64(B[a]))
+    return Y
