@@ -63,8 +63,9 @@ __host__ __device__ inline GrLayout gr_layout(int kind, int stages, int bn, int 
     uint32_t off = uint32_t(stages) * L.stage_bytes;
     L.table = off;  // int off[groups + 1], int pre[groups + 1]
     off += (uint32_t(2 * (groups + 1)) * 4u + 15u) & ~15u;
-    L.stg = off;    // LORA: fp32 [32 rows][33] per epilogue warp
-    off += kind == GR_LORA ? uint32_t(kEpiWarps) * 32u * 33u * 4u : 0u;
+    L.stg = off;    // per epilogue warp: 16-bit [32 rows][32 features]; LORA: fp32 [32 rows][33]
+    off += kind == GR_LORA ? uint32_t(kEpiWarps) * 32u * 33u * 4u
+                           : (kind == GR_FORWARD || kind == GR_DGRAD) ? uint32_t(kEpiWarps) * 2048u : 0u;
     L.low = off;    // LORA: fp32 [32 rows][rank] per half
     off += kind == GR_LORA ? 2u * 32u * uint32_t(rank) * 4u : 0u;
     L.bars = (off + 15u) & ~15u;
@@ -170,6 +171,40 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
 }
 __device__ __forceinline__ float from16(uint16_t v, bool fp16) {
     return fp16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(uint32_t(v) << 16);
+}
+
+// A warp's fragment, 32 rows x 32 features, in its 2 KB of shared memory (64 bytes a row): lane l holds the 16-byte
+// piece l % 4 of rows l / 4, + 8, + 16, + 24.
+struct Fragment {
+    uint8_t *stg;
+    int lane, cols;
+    bool live;        // the piece's features exist
+    size_t at, step;  // element of the first piece, and from a piece to the next
+    __device__ void put(const uint4 (&z)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(stg + i * 512 + lane * 16) = z[i];
+        __syncwarp();
+    }
+    __device__ void out(void *p) const {
+        __syncwarp();
+        uint16_t *y = static_cast<uint16_t *>(p) + at;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (live && (lane >> 2) + 8 * i < cols)
+                *reinterpret_cast<uint4 *>(y + i * step) = *reinterpret_cast<const uint4 *>(stg + i * 512 + lane * 16);
+        __syncwarp();
+    }
+};
+
+// the pieces of the pre-activation's fragment at column c of the tile (zeros outside)
+__device__ __forceinline__ void load_fragment(uint4 (&z)[4], const GroupedArgs &a, const Tile &w, int c, int q, int lane,
+                                              bool ok) {
+    const int f = w.f0 + q * 32 + (lane & 3) * 8;
+    const uint16_t *p = static_cast<const uint16_t *>(a.preact) + size_t(w.col0 + c + (lane >> 2)) * a.F + f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        z[i] = ok && f < a.F && c + (lane >> 2) + 8 * i < w.n
+                   ? *reinterpret_cast<const uint4 *>(p + size_t(8 * i) * a.F) : make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Group table: off[i] = offsets[i] clamped to [0, T] and to not decrease, pre[i] = tiles of the groups
@@ -417,6 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         for (int t = blockIdx.x; t < total; t += gridDim.x, ++tile) {
             const Tile w = walk.at(t);
             const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
+            uint4 zv[4];  // DGRAD: the next fragment's pre-activations, on their way before the accumulator is ready
+            if constexpr (KIND == GR_DGRAD)
+                if (a.preact && half * 32 < w.n) load_fragment(zv, a, w, half * 32, q, lane, true);
             const bool ok = ptx::mbar_wait_bounded(B.tmem_full0 + 8 * buf, tph, tmo, abort, a.err, kInfoEpi | buf);
             ptx::tc_fence_after();
             const uint32_t tacc = tmem_base + (uint32_t(q * 32) << 16) + buf * uint32_t(a.bn);
@@ -428,21 +466,38 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                 ptx::tmem_ld_wait();
                 const int cols = min(32, w.n - c);
                 if constexpr (KIND == GR_FORWARD || KIND == GR_DGRAD) {
-                    uint16_t *y = static_cast<uint16_t *>(a.out) + size_t(w.col0 + c) * a.F + f;
-                    uint16_t *z = a.preact ? static_cast<uint16_t *>(a.preact) + size_t(w.col0 + c) * a.F + f : nullptr;
+                    // The fragment is turned in shared memory (a lane's feature column in, whole rows out), so that
+                    // global memory is read and written in 16-byte pieces, 64 bytes a row.
+                    uint8_t *const stg = smem_raw + L.stg + e * 2048;
+                    const Fragment fr{stg, lane, cols, (w.f0 + q * 32 + (lane & 3) * 8) < a.F && ok,
+                                      size_t(w.col0 + c + (lane >> 2)) * a.F + w.f0 + q * 32 + (lane & 3) * 8,
+                                      size_t(8) * a.F};
+                    uint16_t *const mine = reinterpret_cast<uint16_t *>(stg) + lane;
+                    if constexpr (KIND == GR_DGRAD) {
+                        if (a.preact) {
+                            fr.put(zv);
+                            if (c + 64 < w.n)  // the next fragment's, while this one is worked on
+                                load_fragment(zv, a, w, c + 64, q, lane, ok);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (live && j < cols) {
-                            float x = __uint_as_float(v[j]);
-                            if constexpr (KIND == GR_FORWARD) {
-                                if (z) z[size_t(j) * a.F] = to16(x, fp16);
-                                if (a.act) x = gelu(x);
-                            } else if (z) {
-                                x *= gelu_slope(from16(z[size_t(j) * a.F], fp16));
-                            }
-                            y[size_t(j) * a.F] = to16(x, fp16);
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = __float_as_uint(__uint_as_float(v[j]) * gelu_slope(from16(mine[j * 32], fp16)));
+                            __syncwarp();
                         }
                     }
+                    if constexpr (KIND == GR_FORWARD) {
+                        if (a.preact) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) mine[j * 32] = to16(__uint_as_float(v[j]), fp16);
+                            fr.out(a.preact);
+                        }
+                        if (a.act) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(gelu(__uint_as_float(v[j])));
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) mine[j * 32] = to16(__uint_as_float(v[j]), fp16);
+                    fr.out(a.out);
                 } else if constexpr (KIND == GR_SHRINK) {
                     const float sc = a.scale ? a.scale[w.w] : 1.f;
                     float *y = static_cast<float *>(a.out) + size_t(w.col0 + c) * a.F + f;
