@@ -711,8 +711,10 @@ typedef enum { CF_BF16 = 0, CF_FP16 = 1 } cf_dtype;  /* 16-bit operand types */
  * or leave [0, T] are clamped, and reported as CF_ERR_DEVICE_BOUNDS.
  * workspace (device) >= cf_grouped_gemm_workspace_size() bytes, any of the
  * three directions; zeroed once, one launch at a time, as for every call.
- * Tuning fields used (_ex): n_slice (accumulator columns: 32, 64, 128, 256;
- * wgrad from 64 on), stages, max_clusters (cap on CTAs), timeout_us, disable_pdl. */
+ * Tuning fields used (_ex): n_slice (accumulator columns: 16, 32, 64, 128, 256;
+ * wgrad from 64 on), cluster_m (2: CTA pairs on tiles of 256 features, with
+ * n_slice 128 or 256; 1: single CTAs), stages, max_clusters (cap on CTAs or
+ * pairs), timeout_us, disable_pdl. */
 CF_API size_t cf_grouped_gemm_workspace_size(int64_t T, int64_t N, int64_t K, int64_t E);
 
 CF_API cf_status cf_grouped_gemm(const void *X, const void *W, const int32_t *offsets, void *Y, void *Z,

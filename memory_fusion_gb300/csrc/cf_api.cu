@@ -1325,19 +1325,44 @@ extern "C" cf_status cf_unfused_gemm_rowsoftmax(const void *X, const void *W, co
 // =========================================================================
 namespace {
 
-// weights [count, rows, cols] 16-bit, cols contiguous, as a 3-D tensor; outside reads as zero
-bool make_tmap_weights(CUtensorMap *m, const void *ptr, uint64_t count, uint64_t rows, uint64_t cols,
-                       uint32_t box_rows) {
+// 16-bit tensor map of up to four dimensions, 128B swizzle, zeros outside; strides in bytes
+bool make_tmap_nd(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                  const cuuint32_t *box) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[3] = {cols, rows, count};
-    cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
-    cuuint32_t box[3] = {64, box_rows, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void *>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Feature operand of FORWARD, SHRINK and LORA: weights [count, K, F], features contiguous.  Two 64-feature blocks of 64
+// rows a copy where the rows consist of whole blocks, one otherwise.
+bool make_tmap_features(CUtensorMap *m, int *split, const void *ptr, uint64_t count, uint64_t K, uint64_t F) {
+    *split = F % 64 != 0;
+    if (*split) {
+        const cuuint64_t dims[3] = {F, K, count}, strides[2] = {F * 2, K * F * 2};
+        const cuuint32_t box[3] = {64, 64, 1};
+        return make_tmap_nd(m, ptr, 3, dims, strides, box);
+    }
+    const cuuint64_t dims[4] = {64, K, F / 64, count}, strides[3] = {F * 2, 128, K * F * 2};
+    const cuuint32_t box[4] = {64, 64, 2, 1};
+    return make_tmap_nd(m, ptr, 4, dims, strides, box);
+}
+
+// Feature operand of DGRAD: the same weights [count, K, N] with rows K as the features, 128 of them a copy.
+bool make_tmap_features_t(CUtensorMap *m, const void *ptr, uint64_t count, uint64_t K, uint64_t N) {
+    const cuuint64_t dims[3] = {N, K, count}, strides[2] = {N * 2, K * N * 2};
+    const cuuint32_t box[3] = {64, 128, 1};
+    return make_tmap_nd(m, ptr, 3, dims, strides, box);
+}
+
+// Operand of WGRAD: a row-major [rows, cols] matrix in blocks of 64 rows x 64 columns, `blocks` of them a copy where the
+// rows consist of whole blocks, one otherwise.
+bool make_tmap_blocks(CUtensorMap *m, int *split, const void *ptr, uint64_t rows, uint64_t cols, uint32_t blocks) {
+    *split = cols % 64 != 0;
+    if (*split) return make_tmap_bf16(m, ptr, rows, cols, 64, 64);
+    return make_tmap_w(m, ptr, rows, cols, blocks);
 }
 
 constexpr int64_t kGroupedMaxDim = int64_t(1) << 24;
@@ -1354,37 +1379,47 @@ cf_status grouped_sizes(int64_t T, int64_t N, int64_t K, int64_t groups, int dty
 
 // Accumulator columns, ring depth and grid of one grouped launch.
 // Columns (rows of the batch; WGRAD: columns of dW): four times the mean group,
-// so that an uneven group still reads its weights once, between 32 and 256.
+// so that an uneven group still reads its weights once, between 16 and 256.
 cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t N, int64_t groups, int64_t rank, const cf_tuning &t,
                        const cf::DeviceInfo &dev, cf::GroupedArgs *a, int *ctas, int *smem) {
     int64_t want;
     if (kind == cf::GR_WGRAD) want = N;
     else if (kind == cf::GR_LORA) want = T;
     else want = std::min<int64_t>(T, 4 * ((T + groups - 1) / groups));
-    const int least = kind == cf::GR_WGRAD ? 64 : 32;  // WGRAD stages dY in 64-column blocks
+    const int least = kind == cf::GR_WGRAD ? 64 : 16;  // WGRAD stages dY in 64-column blocks
     int bn = least;
     while (bn < 256 && bn < want) bn *= 2;
     if (t.n_slice != 0) {
-        if (t.n_slice != 32 && t.n_slice != 64 && t.n_slice != 128 && t.n_slice != 256) return CF_ERR_UNSUPPORTED;
+        if (t.n_slice != 16 && t.n_slice != 32 && t.n_slice != 64 && t.n_slice != 128 && t.n_slice != 256) return CF_ERR_UNSUPPORTED;
         if (t.n_slice < least) return CF_ERR_UNSUPPORTED;
         bn = t.n_slice;
     }
     if (t.stages < 0 || t.stages > 12) return CF_ERR_UNSUPPORTED;
+    // CTA pairs where the tiles are full
+    if (t.cluster_m < 0 || t.cluster_m > 2) return CF_ERR_UNSUPPORTED;
+    bool pair = kind != cf::GR_SHRINK && bn == 256 && F > 128;
+    if (t.cluster_m != 0) pair = t.cluster_m == 2;
+    if (pair && (kind == cf::GR_SHRINK || bn < 128)) return CF_ERR_UNSUPPORTED;
     int stages = t.stages > 0 ? t.stages : 12;
-    while (stages > 2 && cf::grouped_smem_bytes(kind, stages, bn, int(groups), int(rank)) > kMaxSmem) --stages;
-    *smem = cf::grouped_smem_bytes(kind, stages, bn, int(groups), int(rank));
+    while (stages > 2 && cf::grouped_smem_bytes(kind, pair, stages, bn, int(groups), int(rank)) > kMaxSmem) --stages;
+    *smem = cf::grouped_smem_bytes(kind, pair, stages, bn, int(groups), int(rank));
     if (*smem > kMaxSmem || *smem > dev.max_smem_optin) return CF_ERR_UNSUPPORTED;
-    const int64_t ft = (F + 127) / 128;
+    const int per = pair ? 256 : 128, width = pair ? 2 : 1;
+    const int64_t ft = (F + per - 1) / per;
     const int64_t tiles = kind == cf::GR_WGRAD ? groups * ft * ((N + bn - 1) / bn)
                                                : ft * std::min<int64_t>(T, T / bn + groups);
     if (tiles >= (int64_t(1) << 31) - 65536) return CF_ERR_UNSUPPORTED;
-    int64_t c = std::min<int64_t>(tiles, dev.sm_count);
+    int64_t c = std::min<int64_t>(tiles, dev.sm_count / width);
     if (t.max_clusters > 0) c = std::min<int64_t>(c, t.max_clusters);
-    *ctas = int(std::max<int64_t>(c, 1));
+    *ctas = int(std::max<int64_t>(c, 1)) * width;
     a->bn = bn;
+    a->pair = pair;
     a->stages = stages;
     return CF_OK;
 }
+
+// columns of a tile that one CTA stages: rows of the batch in one copy's box
+uint32_t staged_columns(const cf::GroupedArgs &a) { return uint32_t(a.pair ? a.bn / 2 : a.bn); }
 
 // the fields every kind shares
 void grouped_args(cf::GroupedArgs *a, int64_t T, int64_t F, int64_t C, int64_t N, int64_t groups, int dtype,
@@ -1438,9 +1473,9 @@ cf_status grouped_rows(int kind, const void *rows, const void *W, const int32_t 
     int ctas, smem;
     st = plan_grouped(kind, T, F, 0, E, 0, t, dev, &a, &ctas, &smem);
     if (st != CF_OK) return st;
-    if (!make_tmap_weights(&a.tmap_a, W, uint64_t(E), uint64_t(K), uint64_t(N), fwd ? 64 : 128) ||
-        !make_tmap_bf16(&a.tmap_b, rows, uint64_t(T), uint64_t(C), 64, 64) ||
-        !make_tmap_bf16(&a.tmap_b16, rows, uint64_t(T), uint64_t(C), 64, 16))
+    if (!(fwd ? make_tmap_features(&a.tmap_a, &a.a_split, W, uint64_t(E), uint64_t(K), uint64_t(N))
+              : make_tmap_features_t(&a.tmap_a, W, uint64_t(E), uint64_t(K), uint64_t(N))) ||
+        !make_tmap_bf16(&a.tmap_b, rows, uint64_t(T), uint64_t(C), 64, staged_columns(a)))
         return CF_ERR_CUDA;
     a.out = out;
     a.preact = preact;
@@ -1517,10 +1552,9 @@ extern "C" cf_status cf_grouped_gemm_wgrad_ex(const void *X, const void *dY, con
     int ctas, smem;
     st = plan_grouped(cf::GR_WGRAD, T, K, N, E, 0, t, dev, &a, &ctas, &smem);
     if (st != CF_OK) return st;
-    if (!make_tmap_bf16(&a.tmap_a, X, uint64_t(T), uint64_t(K), 64, 64) ||
-        !make_tmap_bf16(&a.tmap_b, dY, uint64_t(T), uint64_t(N), 64, 64))
+    if (!make_tmap_blocks(&a.tmap_a, &a.a_split, X, uint64_t(T), uint64_t(K), 2) ||
+        !make_tmap_blocks(&a.tmap_b, &a.b_split, dY, uint64_t(T), uint64_t(N), staged_columns(a) / 64))
         return CF_ERR_CUDA;
-    a.tmap_b16 = a.tmap_b;
     a.out = dW;
     return launch_grouped_checked(cf::GR_WGRAD, a, ctas, smem, t, stream);
 }
@@ -1569,13 +1603,12 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
     int sh_ctas = 0, sh_smem = 0, ctas, smem;
     if (L > 0) {
         cf_tuning ts = t;
-        ts.n_slice = ts.stages = 0;  // the knobs are the main product's
+        ts.n_slice = ts.stages = ts.cluster_m = 0;  // the knobs are the main product's
         grouped_args(&sh, T, R, K, 0, S, int(dtype), offsets, workspace, t);
         st = plan_grouped(cf::GR_SHRINK, T, R, 0, S, 0, ts, dev, &sh, &sh_ctas, &sh_smem);
         if (st != CF_OK) return st;
-        if (!make_tmap_weights(&sh.tmap_a, A, uint64_t(L), uint64_t(K), uint64_t(R), 64) ||
-            !make_tmap_bf16(&sh.tmap_b, X, uint64_t(T), uint64_t(K), 64, 64) ||
-            !make_tmap_bf16(&sh.tmap_b16, X, uint64_t(T), uint64_t(K), 64, 16))
+        if (!make_tmap_features(&sh.tmap_a, &sh.a_split, A, uint64_t(L), uint64_t(K), uint64_t(R)) ||
+            !make_tmap_bf16(&sh.tmap_b, X, uint64_t(T), uint64_t(K), 64, staged_columns(sh)))
             return CF_ERR_CUDA;
         sh.windex = adapters;
         sh.nweights = int(L);
@@ -1586,9 +1619,8 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
     a.rank = int(R);
     st = plan_grouped(cf::GR_LORA, T, N, 0, S, R, t, dev, &a, &ctas, &smem);
     if (st != CF_OK) return st;
-    if (!make_tmap_weights(&a.tmap_a, W, 1, uint64_t(K), uint64_t(N), 64) ||
-        !make_tmap_bf16(&a.tmap_b, X, uint64_t(T), uint64_t(K), 64, 64) ||
-        !make_tmap_bf16(&a.tmap_b16, X, uint64_t(T), uint64_t(K), 64, 16))
+    if (!make_tmap_features(&a.tmap_a, &a.a_split, W, 1, uint64_t(K), uint64_t(N)) ||
+        !make_tmap_bf16(&a.tmap_b, X, uint64_t(T), uint64_t(K), 64, staged_columns(a)))
         return CF_ERR_CUDA;
     a.windex = adapters;
     a.nweights = int(L);

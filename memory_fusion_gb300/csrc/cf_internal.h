@@ -237,8 +237,8 @@ constexpr int kLoraMaxRank = 128;        // one tile of features in the first pr
 
 struct GroupedArgs {
     CUtensorMap tmap_a;    // the operand whose features become accumulator lanes: W (WGRAD: X)
-    CUtensorMap tmap_b;    // the operand whose rows become accumulator columns: X or dY, box 64 rows (WGRAD: dY)
-    CUtensorMap tmap_b16;  // the same in boxes of 16 rows
+    CUtensorMap tmap_b;    // the operand whose rows become accumulator columns: X or dY (WGRAD: dY)
+    int a_split, b_split;  // 1: rows of 64-column blocks do not tile the matrix, so one block a copy (a length % 64)
     const int32_t *offsets;  // [groups + 1] rows of each group (LORA: of each request)
     const int32_t *windex;   // SHRINK, LORA: [groups] adapter of each request, -1 for none
     void *out;               // Y / dX / dW / H
@@ -259,10 +259,11 @@ struct GroupedArgs {
     int act;                 // FORWARD, DGRAD: 1 = GELU(tanh)
     int bn;                  // columns of one accumulator tile (32, 64, 128 or 256)
     int stages;
+    int pair;                // CTA pairs, one cta_group::2 MMA stream over 256 features (not SHRINK)
     unsigned long long timeout_ns;
 };
 
-int grouped_smem_bytes(int kind, int stages, int bn, int groups, int rank);
+int grouped_smem_bytes(int kind, bool pair, int stages, int bn, int groups, int rank);
 cudaError_t launch_grouped(int kind, const GroupedArgs &a, int ctas, int smem, bool pdl, cudaStream_t stream);
 
 }  // namespace cf

@@ -57,9 +57,10 @@ struct GrLayout {
     uint32_t stage_bytes, table, stg, low, bars, total;
 };
 
-__host__ __device__ inline GrLayout gr_layout(int kind, int stages, int bn, int groups, int rank) {
+__host__ __device__ inline GrLayout gr_layout(int kind, bool pair, int stages, int bn, int groups, int rank) {
     GrLayout L;
-    L.stage_bytes = uint32_t(kABytes + bn * kBK * 2);
+    // a CTA of a pair stages its own 128 features and half of the tile's columns
+    L.stage_bytes = uint32_t(kABytes + (pair ? bn / 2 : bn) * kBK * 2);
     uint32_t off = uint32_t(stages) * L.stage_bytes;
     L.table = off;  // int off[groups + 1], int pre[groups + 1]
     off += (uint32_t(2 * (groups + 1)) * 4u + 15u) & ~15u;
@@ -88,29 +89,39 @@ __device__ __forceinline__ GrBars gr_bars(uint32_t base, int stages) {
 }
 static_assert(16 * 12 + 16 + 16 + 8 + 8 <= 256, "barrier area");
 
+template <bool kPair>
+__device__ __forceinline__ int feature_tiles(const GroupedArgs &a) {
+    return kPair ? (a.F + 2 * kFB - 1) / (2 * kFB) : (a.F + kFB - 1) / kFB;
+}
+
 // one tile of work
 struct Tile {
     int g;      // group
     int w;      // its weights
-    int f0;     // first feature
+    int f0;     // first feature of this CTA
     int col0;   // first accumulator column's row of the batch (WGRAD: column of dW)
     int n;      // columns that exist
-    int nm;     // columns multiplied (n rounded up to 16)
+    int nm;     // columns multiplied (n rounded up; a pair: half of them staged by each CTA)
     int nk;     // 64-deep blocks of the contraction
     int row0;   // WGRAD: first row of the group
     int rows;   // WGRAD: rows of the group
 };
 
-template <int KIND>
+template <int KIND, bool kPair>
 struct Walk {
     const int *off, *pre;
     const GroupedArgs &a;
     int ft;      // feature tiles
     int g;       // group of the current tile (tiles are visited in ascending order)
+    int half;    // features of this CTA behind the tile's first: 0, or 128 in the second CTA of a pair
 
-    __device__ Walk(const int *off_, const int *pre_, const GroupedArgs &a_) : off(off_), pre(pre_), a(a_), g(0) {
-        ft = (a.F + kFB - 1) / kFB;
+    __device__ Walk(const int *off_, const int *pre_, const GroupedArgs &a_, int half_)
+        : off(off_), pre(pre_), a(a_), g(0), half(half_) {
+        ft = feature_tiles<kPair>(a);
     }
+    static constexpr int kTileF = kPair ? 2 * kFB : kFB;
+    // columns are multiplied in 16s; each half of a pair's in 16s (WGRAD: whole 64-column blocks)
+    static constexpr int kGran = kPair ? (KIND == GR_WGRAD ? 128 : 32) : 16;
     __device__ int total() const { return pre[groups()]; }
     __device__ int groups() const { return KIND == GR_LORA ? 1 : a.groups; }
     __device__ Tile at(int t) {
@@ -123,7 +134,7 @@ struct Walk {
         const int rows = off[KIND == GR_LORA ? a.groups : g + 1] - lo;
         if constexpr (KIND == GR_WGRAD) {
             const int nt = (a.N + a.bn - 1) / a.bn;
-            r.f0 = (local / nt) * kFB;
+            r.f0 = (local / nt) * kTileF + half;
             r.col0 = (local % nt) * a.bn;
             r.n = min(a.bn, a.N - r.col0);
             r.row0 = lo;
@@ -131,18 +142,18 @@ struct Walk {
             r.nk = (rows + kBK - 1) / kBK;
         } else {
             const int rt = (rows + a.bn - 1) / a.bn;              // row tiles of the group,
-            const int per = (((rows + rt - 1) / rt) + 15) & ~15;  // cut evenly
+            const int per = ((rows + rt - 1) / rt + kGran - 1) & ~(kGran - 1);  // cut evenly
             const int chunk = local / (kRasterRows * ft);
             const int wide = min(kRasterRows, rt - chunk * kRasterRows);
             const int in = local - chunk * kRasterRows * ft;
             const int rtile = chunk * kRasterRows + in % wide;
-            r.f0 = (in / wide) * kFB;
+            r.f0 = (in / wide) * kTileF + half;
             r.col0 = lo + rtile * per;
             r.n = min(per, rows - rtile * per);
             r.row0 = r.rows = 0;
             r.nk = (a.C + kBK - 1) / kBK;
         }
-        r.nm = (r.n + 15) & ~15;
+        r.nm = (r.n + kGran - 1) & ~(kGran - 1);
         return r;
     }
 };
@@ -209,11 +220,11 @@ __device__ __forceinline__ void load_fragment(uint4 (&z)[4], const GroupedArgs &
 
 // Group table: off[i] = offsets[i] clamped to [0, T] and to not decrease, pre[i] = tiles of the groups
 // before i.  One warp, after the raw offsets are in off[].
-template <int KIND>
+template <int KIND, bool kPair>
 __device__ void scan_table(int *off, int *pre, const GroupedArgs &a, uint32_t *err) {
     const int lane = threadIdx.x & 31;
     const int n = a.groups + 1;
-    const int ft = (a.F + kFB - 1) / kFB;
+    const int ft = feature_tiles<kPair>(a);
     bool bad = false;
     int run_max = 0;
     for (int i0 = 0; i0 < n; i0 += 32) {
@@ -266,7 +277,87 @@ __device__ void scan_table(int *off, int *pre, const GroupedArgs &a, uint32_t *e
         ptx::record_error(err, 8u /*CF_ERR_DEVICE_BOUNDS*/, kInfoTable);
 }
 
-template <int KIND>
+// A block of the contraction stages 16 KB of the feature operand (features behind the last are zeros, or stale where
+// a copy would hold none: those lanes are never stored) and, of the columns, what the CTA multiplies, rounded up to
+// whole boxes.  Rows of a box behind the tile's are the neighbour's, in columns that are not multiplied or not stored.
+template <int KIND, bool kPair>
+__device__ __forceinline__ int b_blocks(const GroupedArgs &a, const Tile &w) {  // WGRAD: 64-column blocks to fill
+    const int cols = kPair ? w.nm / 2 : w.nm;
+    return KIND == GR_WGRAD ? (a.b_split ? (cols + 63) / 64 : (kPair ? a.bn / 2 : a.bn) / 64) : 1;
+}
+template <int KIND, bool kPair>
+__device__ __forceinline__ uint32_t b_bytes(const GroupedArgs &a, const Tile &w) {
+    return KIND == GR_WGRAD ? uint32_t(b_blocks<KIND, kPair>(a, w)) * 8192u : uint32_t(kPair ? a.bn / 2 : a.bn) * 128u;
+}
+
+// WGRAD: rows left .. 16*steps - 1 of every 64-column block of the stage (a row is 128 bytes of a block) become
+// zeros, by one warp; then the async proxy may read them
+__device__ __forceinline__ void zero_tail(uint8_t *st, int left, int steps, int bblocks, int lane) {
+    const int per = (16 * steps - left) * 8;  // 16-byte pieces per block
+    for (int i = lane; i < (2 + bblocks) * per; i += 32) {
+        const int blk = i / per, p = i % per;
+        uint8_t *q = st + (blk < 2 ? blk * 8192 : kABytes + (blk - 2) * 8192) + left * 128 + p * 16;
+        *reinterpret_cast<uint4 *>(q) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+}
+
+template <bool kPair>
+__device__ __forceinline__ void issue_mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (kPair) ptx::mma_bf16_pair(d, ad, bd, idesc, accumulate);
+    else ptx::mma_bf16(d, ad, bd, idesc, accumulate);
+}
+// arrive when the MMAs issued so far are complete (a pair: on both CTAs' barrier)
+template <bool kPair>
+__device__ __forceinline__ void issue_commit(uint32_t bar) {
+    if constexpr (kPair) ptx::mma_commit_pair_mc(bar, 3);
+    else ptx::mma_commit(bar);
+}
+// The copies of block kb into a stage, completing on `bar` (kShared: a barrier of either CTA of the pair)
+template <int KIND, bool kShared>
+__device__ __forceinline__ void stage_loads(const GroupedArgs &a, const Tile &w, uint32_t sa, uint32_t sb, uint32_t bar,
+                                            int kb, int col0, int bblk) {
+    const int k0 = kb * kBK;
+    if constexpr (KIND == GR_WGRAD) {
+        const int y = w.row0 + k0;
+        if (a.a_split) {
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (kShared) ptx::tma_load_2d_pair(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, y);
+                else ptx::tma_load_2d(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, y);
+            }
+        } else {
+            if constexpr (kShared) ptx::tma_load_3d_pair(sa, &a.tmap_a, bar, 0, y, w.f0 / 64);
+            else ptx::tma_load_3d(sa, &a.tmap_a, bar, 0, y, w.f0 / 64);
+        }
+        if (a.b_split) {
+            for (int i = 0; i < bblk; ++i) {
+                if constexpr (kShared) ptx::tma_load_2d_pair(sb + i * 8192, &a.tmap_b, bar, col0 + 64 * i, y);
+                else ptx::tma_load_2d(sb + i * 8192, &a.tmap_b, bar, col0 + 64 * i, y);
+            }
+        } else {
+            if constexpr (kShared) ptx::tma_load_3d_pair(sb, &a.tmap_b, bar, 0, y, col0 / 64);
+            else ptx::tma_load_3d(sb, &a.tmap_b, bar, 0, y, col0 / 64);
+        }
+    } else {
+        if constexpr (KIND == GR_DGRAD) {
+            if constexpr (kShared) ptx::tma_load_3d_pair(sa, &a.tmap_a, bar, k0, w.f0, w.w);
+            else ptx::tma_load_3d(sa, &a.tmap_a, bar, k0, w.f0, w.w);
+        } else if (a.a_split) {
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (kShared) ptx::tma_load_3d_pair(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, k0, w.w);
+                else ptx::tma_load_3d(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, k0, w.w);
+            }
+        } else {
+            if constexpr (kShared) ptx::tma_load_4d_pair(sa, &a.tmap_a, bar, 0, k0, w.f0 / 64, w.w);
+            else ptx::tma_load_4d(sa, &a.tmap_a, bar, 0, k0, w.f0 / 64, w.w);
+        }
+        if constexpr (kShared) ptx::tma_load_2d_pair(sb, &a.tmap_b, bar, k0, col0);
+        else ptx::tma_load_2d(sb, &a.tmap_b, bar, k0, col0);
+    }
+}
+
+template <int KIND, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_constant__ GroupedArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = ptx::smem_u32(smem_raw);
@@ -278,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     constexpr bool kAMn = KIND != GR_DGRAD;  // features contiguous in memory: A is MN-major
     constexpr bool kBMn = KIND == GR_WGRAD;
     const int stages = a.stages;
-    const GrLayout L = gr_layout(KIND, stages, a.bn, a.groups, a.rank);
+    const GrLayout L = gr_layout(KIND, kPair, stages, a.bn, a.groups, a.rank);
     const GrBars B = gr_bars(base + L.bars, stages);
     int *const off = reinterpret_cast<int *>(smem_raw + L.table);
     int *const pre = off + a.groups + 1;
@@ -288,28 +379,38 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t tmem_cols = uint32_t(2 * a.bn);
+    // A pair (two CTAs of a cluster) works on one tile of 256 features: the even CTA issues MMAs of M = 256 that
+    // read both CTAs' shared memory and write both tensor memories (128 features each).
+    const uint32_t crank = kPair ? ptx::cluster_ctarank() : 0u;
+    const bool leader = crank == 0u;
+    const int worker = int(blockIdx.x) / (kPair ? 2 : 1), workers = int(gridDim.x) / (kPair ? 2 : 1);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
-            ptx::mbar_init(B.full0 + 8 * s, 1);
+            // WGRAD pairs: the second CTA arrives too, when its part of the stage is ready
+            ptx::mbar_init(B.full0 + 8 * s, kPair && KIND == GR_WGRAD && leader ? 2 : 1);
             ptx::mbar_init(B.empty0 + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(B.tmem_full0 + 8 * b, 1);
-            ptx::mbar_init(B.tmem_empty0 + 8 * b, kEpiWarps);
+            ptx::mbar_init(B.tmem_empty0 + 8 * b, kPair ? 2 * kEpiWarps : kEpiWarps);
         }
         ptx::mbar_init(B.mma_done, 1);
         misc[1] = 0u;
         ptx::fence_mbarrier_init_cluster();
     }
     if (warp == 1) {
-        ptx::tmem_alloc(B.misc, tmem_cols);
-        ptx::tmem_relinquish();
+        if constexpr (kPair) {
+            ptx::tmem_alloc_pair(B.misc, tmem_cols);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(B.misc, tmem_cols);
+            ptx::tmem_relinquish();
+        }
     }
     if (threadIdx.x == 0) {
         ptx::prefetch_tensormap(&a.tmap_a);
         ptx::prefetch_tensormap(&a.tmap_b);
-        ptx::prefetch_tensormap(&a.tmap_b16);
     }
     // The next grid may start only once this CTA holds its tensor memory: a dependent CTA that took it first
     // would wait for this grid while this grid waited for the columns.
@@ -318,12 +419,13 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     ptx::griddep_wait();
     for (int i = threadIdx.x; i <= a.groups; i += kThreads) off[i] = a.offsets[i];
     __syncthreads();
-    if (warp == 0) scan_table<KIND>(off, pre, a, a.err);
+    if (warp == 0) scan_table<KIND, kPair>(off, pre, a, a.err);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
+    if constexpr (kPair) ptx::cluster_sync();  // the peer's barriers are initialised before anything signals them
     const uint32_t tmem_base = misc[0];
-    Walk<KIND> walk(off, pre, a);
+    Walk<KIND, kPair> walk(off, pre, a, int(crank) * kFB);
     const int total = walk.total();
 
     if (warp == 0) {
@@ -331,39 +433,33 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         if (lane == 0) {
             uint32_t it = 0, s = 0, ph = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            const uint32_t full_lead = kPair ? ptx::mapa(B.full0, 0u) : B.full0;
+            for (int t = worker; t < total && ok; t += workers) {
                 const Tile w = walk.at(t);
-                const int ablocks = kAMn ? (a.F - w.f0 > 64 ? 2 : 1) : 1;
-                // columns: whole 64s, then 16s (WGRAD: 64-column blocks)
-                const int b64 = kBMn ? (w.n + 63) / 64 : w.nm / 64;
-                const int b16 = kBMn ? 0 : (w.nm % 64) / 16;
-                const uint32_t tx = uint32_t(kAMn ? ablocks * 8192 : kABytes) + uint32_t(b64 * 8192 + b16 * 2048);
+                const int cols = kPair ? w.nm / 2 : w.nm;  // columns this CTA stages
+                const int col0 = w.col0 + int(crank) * cols;
+                const int bblk = b_blocks<KIND, kPair>(a, w);
+                const uint32_t own = uint32_t(kABytes) + b_bytes<KIND, kPair>(a, w);
                 for (int kb = 0; kb < w.nk; ++kb) {
-                    ok = ptx::mbar_wait_bounded(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
-                    if (!ok) break;
+                    if (!ptx::mbar_try_wait(B.empty0 + 8 * s, ph ^ 1u)) {
+                        ok = ptx::mbar_wait_bounded(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
+                        if (!ok) break;
+                    }
                     const uint32_t sa = base + s * L.stage_bytes;
                     const uint32_t sb = sa + kABytes;
-                    const uint32_t fb = B.full0 + 8 * s;
-                    ptx::mbar_arrive_expect_tx(fb, tx);
-                    if constexpr (KIND == GR_WGRAD) {
-                        const int y = w.row0 + kb * kBK;
-                        for (int i = 0; i < ablocks; ++i)
-                            ptx::tma_load_2d(sa + i * 8192, &a.tmap_a, fb, w.f0 + 64 * i, y);
-                        for (int i = 0; i < b64; ++i)
-                            ptx::tma_load_2d(sb + i * 8192, &a.tmap_b, fb, w.col0 + 64 * i, y);
-                    } else {
-                        if constexpr (kAMn) {
-                            for (int i = 0; i < ablocks; ++i)
-                                ptx::tma_load_3d(sa + i * 8192, &a.tmap_a, fb, w.f0 + 64 * i, kb * kBK, w.w);
-                        } else {
-                            ptx::tma_load_3d(sa, &a.tmap_a, fb, kb * kBK, w.f0, w.w);
-                        }
-                        for (int i = 0; i < b64; ++i)
-                            ptx::tma_load_2d(sb + i * 8192, &a.tmap_b, fb, kb * kBK, w.col0 + 64 * i);
-                        for (int i = 0; i < b16; ++i)
-                            ptx::tma_load_2d(sb + b64 * 8192 + i * 2048, &a.tmap_b16, fb, kb * kBK,
-                                             w.col0 + 64 * b64 + 16 * i);
+                    // A pair's loads complete on the leader's barrier.  (WGRAD: but for a group's last block where it
+                    // has to be zeroed behind the rows; the second CTA's part then completes on its own barrier, its
+                    // warp 1 zeroes and arrives.)
+                    const bool tail = kPair && KIND == GR_WGRAD && kb == w.nk - 1 && (w.rows & 15) != 0;
+                    if (!kPair || leader) {
+                        ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, kPair && !tail ? 2 * own : own);
+                    } else if (KIND == GR_WGRAD) {
+                        if (tail) ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, own);
+                        else ptx::mbar_arrive_cluster_relaxed(full_lead + 8 * s);  // the loads count bytes
                     }
+                    if (kPair && !(tail && !leader))
+                        stage_loads<KIND, true>(a, w, sa, sb, full_lead + 8 * s, kb, col0, bblk);
+                    else stage_loads<KIND, false>(a, w, sa, sb, B.full0 + 8 * s, kb, col0, bblk);
                     ++it;
                     if (++s == uint32_t(stages)) {
                         s = 0;
@@ -383,48 +479,88 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         // (WGRAD: the whole warp, which zeroes the rows behind a group in its last block)
-        if (lane == 0 || KIND == GR_WGRAD) {
+        if (!leader) {
+            if constexpr (kPair && KIND == GR_WGRAD) {
+                // the second CTA of a pair: zero its part of each group's last block
+                uint32_t s = 0, ph = 0;  // ring position of the tile's first block; a phase bit per stage
+                for (int t = worker; t < total; t += workers) {
+                    const Tile w = walk.at(t);
+                    if (w.nk > 0 && (w.rows & 15) != 0) {
+                        const uint32_t at = (s + uint32_t(w.nk) - 1u) % uint32_t(stages);
+                        const bool ok = ptx::mbar_wait_bounded(B.full0 + 8 * at, (ph >> at) & 1u, tmo, abort, a.err,
+                                                               kInfoMma | 0x200u | at);
+                        if (!__all_sync(0xffffffffu, ok)) break;
+                        ph ^= 1u << at;
+                        const int left = w.rows - (w.nk - 1) * kBK;
+                        zero_tail(smem_raw + at * L.stage_bytes, left, (left + 15) / 16, (w.nm / 2 + 63) / 64, lane);
+                        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(B.full0 + 8 * at, 0u));
+                    }
+                    s = (s + uint32_t(w.nk)) % uint32_t(stages);
+                }
+            }
+        } else if (lane == 0 || KIND == GR_WGRAD) {
             const uint64_t ad0 = kAMn ? sw128_desc(base, 8192, 1024) : sw128_desc(base, 16, 1024);
             const uint64_t bd0 = kBMn ? sw128_desc(base + kABytes, 8192, 1024) : sw128_desc(base + kABytes, 16, 1024);
             uint32_t s = 0, ph = 0;
             int tile = 0;
-            for (int t = blockIdx.x; t < total; t += gridDim.x, ++tile) {
+            for (int t = worker; t < total; t += workers, ++tile) {
                 const Tile w = walk.at(t);
                 const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
-                bool ok = ptx::mbar_wait_bounded(B.tmem_empty0 + 8 * buf, tph ^ 1u, tmo, abort, a.err, kInfoMma | buf);
-                if constexpr (KIND == GR_WGRAD) ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                ptx::tc_fence_after();
                 const uint32_t d = tmem_base + buf * uint32_t(a.bn);
-                const uint32_t idesc = idesc_f16(kFB, w.nm, a.fp16 != 0, kAMn, kBMn);
-                for (int kb = 0; kb < w.nk; ++kb) {
-                    ok = ptx::mbar_wait_bounded(B.full0 + 8 * s, ph, tmo, abort, a.err, kInfoMma | 0x100u | s);
-                    if constexpr (KIND == GR_WGRAD) ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    const int left = (KIND == GR_WGRAD ? w.rows : a.C) - kb * kBK;
-                    const int steps = left >= kBK ? kBK / 16 : (left + 15) / 16;
-                    if constexpr (KIND == GR_WGRAD) {
-                        if (left < kBK && (left & 15) != 0) {
-                            // rows left .. 16*steps - 1 of every 64-column block (a row is 128 bytes of it)
-                            uint8_t *const st = smem_raw + s * L.stage_bytes;
-                            const int blocks = 2 + (w.n + 63) / 64;
-                            const int per = (16 * steps - left) * 8;  // 16-byte pieces per block
-                            for (int i = lane; i < blocks * per; i += 32) {
-                                const int blk = i / per, p = i % per;
-                                uint8_t *q = st + (blk < 2 ? blk * 8192 : kABytes + (blk - 2) * 8192) + left * 128 + p * 16;
-                                *reinterpret_cast<uint4 *>(q) = make_uint4(0u, 0u, 0u, 0u);
-                            }
-                            ptx::fence_proxy_async_smem();
-                        }
-                        __syncwarp();
-                    }
+                const uint32_t idesc = idesc_f16(kPair ? 2 * kFB : kFB, w.nm, a.fp16 != 0, kAMn, kBMn);
+                const int length = KIND == GR_WGRAD ? w.rows : a.C;
+                const int whole = length / kBK;  // blocks of 64; the rest of the contraction is one shorter block
+                const int left = length - whole * kBK;
+                bool ok = true;
+                if (lane == 0) {
+                    ok = ptx::mbar_wait_bounded(B.tmem_empty0 + 8 * buf, tph ^ 1u, tmo, abort, a.err, kInfoMma | buf);
                     ptx::tc_fence_after();
-                    if (lane == 0) {
+                    // The one issuing thread's work between MMA groups is kept short, so that the tensor pipe's
+                    // queue does not run dry: fixed steps, descriptors by addition.
+                    for (int kb = 0; kb < whole && ok; ++kb) {
+                        const uint32_t fb = B.full0 + 8 * s;
+                        if (!ptx::mbar_try_wait(fb, ph)) {
+                            ok = ptx::mbar_wait_bounded(fb, ph, tmo, abort, a.err, kInfoMma | 0x100u | s);
+                            if (!ok) break;
+                        }
+                        ptx::tc_fence_after();
+                        const uint64_t so = uint64_t((s * L.stage_bytes) >> 4);
+#pragma unroll
+                        for (int k = 0; k < kBK / 16; ++k)
+                            issue_mma<kPair>(d, ad0 + so + uint64_t(k * (kAMn ? 128 : 2)),
+                                             bd0 + so + uint64_t(k * (kBMn ? 128 : 2)), idesc, (kb | k) != 0 ? 1u : 0u);
+                        issue_commit<kPair>(B.empty0 + 8 * s);
+                        if (++s == uint32_t(stages)) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+                if constexpr (KIND == GR_WGRAD) {
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    s = __shfl_sync(0xffffffffu, s, 0);
+                    ph = __shfl_sync(0xffffffffu, ph, 0);
+                }
+                if (ok && left > 0) {
+                    const uint32_t fb = B.full0 + 8 * s;
+                    const int steps = (left + 15) / 16;
+                    // (a WGRAD pair: the peer's zeroes are behind its arrival)
+                    ok = ptx::mbar_wait_bounded<kPair && KIND == GR_WGRAD>(fb, ph, tmo, abort, a.err,
+                                                                           kInfoMma | 0x100u | s);
+                    if constexpr (KIND == GR_WGRAD) {
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (ok && (left & 15) != 0)
+                            zero_tail(smem_raw + s * L.stage_bytes, left, steps,
+                                      ((kPair ? w.nm / 2 : w.nm) + 63) / 64, lane);
+                    }
+                    if (ok && lane == 0) {
+                        ptx::tc_fence_after();
                         const uint64_t so = uint64_t((s * L.stage_bytes) >> 4);
                         for (int k = 0; k < steps; ++k)
-                            ptx::mma_bf16(d, ad0 + so + uint64_t(k * (kAMn ? 128 : 2)),
-                                          bd0 + so + uint64_t(k * (kBMn ? 128 : 2)), idesc, (kb | k) != 0 ? 1u : 0u);
-                        ptx::mma_commit(B.empty0 + 8 * s);
+                            issue_mma<kPair>(d, ad0 + so + uint64_t(k * (kAMn ? 128 : 2)),
+                                             bd0 + so + uint64_t(k * (kBMn ? 128 : 2)), idesc,
+                                             (whole | k) != 0 ? 1u : 0u);
+                        issue_commit<kPair>(B.empty0 + 8 * s);
                     }
                     if (++s == uint32_t(stages)) {
                         s = 0;
@@ -432,10 +568,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                     }
                 }
                 if (!ok) break;
-                if (lane == 0) ptx::mma_commit(B.tmem_full0 + 8 * buf);
+                if (lane == 0) issue_commit<kPair>(B.tmem_full0 + 8 * buf);
             }
             if (lane == 0) {
-                ptx::mma_commit(B.mma_done);
+                if constexpr (kPair) ptx::mma_commit_pair_mc(B.mma_done, 1);
+                else ptx::mma_commit(B.mma_done);
                 volatile uint32_t local_abort = 0;
                 ptx::mbar_wait_bounded(B.mma_done, 0, tmo, &local_abort, nullptr, 0);
             }
@@ -449,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         const int q = warp & 3;
         const bool fp16 = a.fp16 != 0;
         int tile = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x, ++tile) {
+        for (int t = worker; t < total; t += workers, ++tile) {
             const Tile w = walk.at(t);
             const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
             uint4 zv[4];  // DGRAD: the next fragment's pre-activations, on their way before the accumulator is ready
@@ -583,55 +720,74 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(B.tmem_empty0 + 8 * buf);
+            if (lane == 0) {
+                if constexpr (kPair) ptx::mbar_arrive_cluster(ptx::mapa(B.tmem_empty0 + 8 * buf, 0u));
+                else ptx::mbar_arrive(B.tmem_empty0 + 8 * buf);
+            }
         }
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == 1) ptx::tmem_dealloc(tmem_base, tmem_cols);
+    if constexpr (kPair) ptx::cluster_sync();  // no CTA leaves while its peer may still reach its shared memory
+    if (warp == 1) {
+        if constexpr (kPair) ptx::tmem_dealloc_pair(tmem_base, tmem_cols);
+        else ptx::tmem_dealloc(tmem_base, tmem_cols);
+    }
 }
 
+template <bool kPair>
 void *kernel_for(int kind) {
     switch (kind) {
-        case GR_FORWARD: return reinterpret_cast<void *>(&grouped_kernel<GR_FORWARD>);
-        case GR_DGRAD: return reinterpret_cast<void *>(&grouped_kernel<GR_DGRAD>);
-        case GR_WGRAD: return reinterpret_cast<void *>(&grouped_kernel<GR_WGRAD>);
-        case GR_SHRINK: return reinterpret_cast<void *>(&grouped_kernel<GR_SHRINK>);
-        case GR_LORA: return reinterpret_cast<void *>(&grouped_kernel<GR_LORA>);
+        case GR_FORWARD: return reinterpret_cast<void *>(&grouped_kernel<GR_FORWARD, kPair>);
+        case GR_DGRAD: return reinterpret_cast<void *>(&grouped_kernel<GR_DGRAD, kPair>);
+        case GR_WGRAD: return reinterpret_cast<void *>(&grouped_kernel<GR_WGRAD, kPair>);
+        case GR_SHRINK: return kPair ? nullptr : reinterpret_cast<void *>(&grouped_kernel<GR_SHRINK, false>);
+        case GR_LORA: return reinterpret_cast<void *>(&grouped_kernel<GR_LORA, kPair>);
         default: return nullptr;
     }
 }
 
 }  // namespace
 
-int grouped_smem_bytes(int kind, int stages, int bn, int groups, int rank) {
-    return int(gr_layout(kind, stages, bn, groups, rank).total);
+int grouped_smem_bytes(int kind, bool pair, int stages, int bn, int groups, int rank) {
+    return int(gr_layout(kind, pair, stages, bn, groups, rank).total);
 }
 
 cudaError_t launch_grouped(int kind, const GroupedArgs &a, int ctas, int smem, bool pdl, cudaStream_t stream) {
-    void *fn = kernel_for(kind);
+    const bool pair = a.pair != 0;
+    void *fn = pair ? kernel_for<true>(kind) : kernel_for<false>(kind);
     if (!fn) return cudaErrorInvalidValue;
-    static int set_smem[64][8] = {};
+    static int set_smem[64][16] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidValue;
-    if (smem > set_smem[dev][kind]) {  // once per device and kernel, to the largest size: none under capture later
+    int &set = set_smem[dev][2 * kind + (pair ? 1 : 0)];
+    if (smem > set) {  // once per device and kernel, to the largest size: none under capture later
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        set_smem[dev][kind] = smem;
+        set = smem;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (pair) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = 2;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = n;
     void *args[] = {(void *)&a};
     return cudaLaunchKernelExC(&cfg, fn, args);
 }

@@ -82,8 +82,18 @@ SHAPES = [
     ([3] * 40, 0, 0, 256, 72),
     ([1, 700, 2], 1, 1, 8, 8),
     ([300, 300, 300], 0, 0, 1024, 384),
+    ([70, 33, 300], 0, 0, 192, 448),
 ]
 IDS = [f"{len(s[0])}g{sum(s[0])}r{s[3]}x{s[4]}" for s in SHAPES]
+
+
+# automatic, and forced: narrow and wide tiles, a shallow ring, few CTAs (several tiles each), CTA pairs
+TUNINGS = {"auto": {}, "n16": dict(n_slice=16), "n64": dict(n_slice=64, cluster_m=1, stages=2), "n256": dict(n_slice=256, cluster_m=1, max_clusters=3),
+           "pair128": dict(n_slice=128, cluster_m=2, max_clusters=2), "pair256": dict(n_slice=256, cluster_m=2, stages=3)}
+
+
+def _tuning(name):
+    return cf.tuning(**TUNINGS[name]) if TUNINGS[name] else None
 
 
 def _forward_case(shape, dt, seed=0):
@@ -102,14 +112,15 @@ def _gelu_slack(ref, z_slack):
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=IDS)
 @pytest.mark.parametrize("act", ["none", "gelu_tanh"])
-def test_forward(shape, dt, act):
+@pytest.mark.parametrize("tun", TUNINGS)
+def test_forward(shape, dt, act, tun):
     torch = torch_cuda()
     X, W, off, T, K, N = _forward_case(shape, dt)
     Xd = _dev(X, dt)
     out = torch.full((T, N), SENTINEL, dtype=Xd.dtype, device="cuda")
     z = torch.full((T, N), SENTINEL, dtype=Xd.dtype, device="cuda")
     ws = cf.new_workspace(cf.cf_grouped_gemm_workspace_size(T, N, K, W.shape[0]))
-    cf.grouped_gemm(Xd, _dev(W, dt), _i32(off), act=act, preact=z, out=out, workspace=ws)
+    cf.grouped_gemm(Xd, _dev(W, dt), _i32(off), act=act, preact=z, out=out, workspace=ws, tuning=_tuning(tun))
     _status(ws)
     Y, Z = oracle.grouped_gemm(X, W, off, act=act)
     mag = oracle.grouped_gemm(np.abs(X), np.abs(W), off)[0]
@@ -122,14 +133,15 @@ def test_forward(shape, dt, act):
         assert np.all(rest == SENTINEL), "rows of no group were written"
     # without the pre-activation the output is the same bits
     out2 = torch.full((T, N), SENTINEL, dtype=Xd.dtype, device="cuda")
-    cf.grouped_gemm(Xd, _dev(W, dt), _i32(off), act=act, out=out2, workspace=ws)
+    cf.grouped_gemm(Xd, _dev(W, dt), _i32(off), act=act, out=out2, workspace=ws, tuning=_tuning(tun))
     assert torch.equal(out, out2)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=IDS)
 @pytest.mark.parametrize("act", ["none", "gelu_tanh"])
-def test_dgrad(shape, dt, act):
+@pytest.mark.parametrize("tun", TUNINGS)
+def test_dgrad(shape, dt, act, tun):
     torch = torch_cuda()
     sizes, before, behind, K, N = shape
     X, W, off, T, K, N = _forward_case(shape, dt, seed=1)
@@ -139,7 +151,8 @@ def test_dgrad(shape, dt, act):
     out = torch.full((T, K), SENTINEL, dtype=_dev([0.0], dt).dtype, device="cuda")
     ws = cf.new_workspace(cf.cf_grouped_gemm_workspace_size(T, N, K, W.shape[0]))
     zd = _dev(Z, dt) if Z is not None else None
-    cf.grouped_gemm_dgrad(_dev(dY, dt), _dev(W, dt), _i32(off), preact=zd, out=out, workspace=ws)
+    cf.grouped_gemm_dgrad(_dev(dY, dt), _dev(W, dt), _i32(off), preact=zd, out=out, workspace=ws,
+                          tuning=_tuning(tun))
     _status(ws)
     ref = oracle.grouped_gemm_dgrad(dY, W, off, preact=Z)
     plain = np.abs(oracle.grouped_gemm_dgrad(dY, W, off))
@@ -151,13 +164,15 @@ def test_dgrad(shape, dt, act):
     assert np.all(np.delete(_host(out), np.arange(off[0], off[-1]), axis=0) == SENTINEL)
     if zd is not None:  # in place of the pre-activation
         out_rows = out[off[0]:off[-1]].clone()
-        cf.grouped_gemm_dgrad(_dev(dY, dt), _dev(W, dt), _i32(off), preact=zd, out=zd, workspace=ws)
+        cf.grouped_gemm_dgrad(_dev(dY, dt), _dev(W, dt), _i32(off), preact=zd, out=zd, workspace=ws,
+                              tuning=_tuning(tun))
         assert torch.equal(zd[off[0]:off[-1]], out_rows)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("shape", SHAPES, ids=IDS)
-def test_wgrad(shape, dt):
+@pytest.mark.parametrize("tun", [t for t in TUNINGS if t != "n16"])
+def test_wgrad(shape, dt, tun):
     torch = torch_cuda()
     sizes, before, behind, K, N = shape
     rng = _rng(3)
@@ -170,7 +185,7 @@ def test_wgrad(shape, dt):
         a[off[-1]:] = np.inf
     out = torch.full((len(sizes), K, N), SENTINEL, dtype=_dev([0.0], dt).dtype, device="cuda")
     ws = cf.new_workspace(cf.cf_grouped_gemm_workspace_size(T, N, K, len(sizes)))
-    cf.grouped_gemm_wgrad(_dev(X, dt), _dev(dY, dt), _i32(off), out=out, workspace=ws)
+    cf.grouped_gemm_wgrad(_dev(X, dt), _dev(dY, dt), _i32(off), out=out, workspace=ws, tuning=_tuning(tun))
     _status(ws)
     ref = oracle.grouped_gemm_wgrad(X, dY, off)
     mag = oracle.grouped_gemm_wgrad(np.abs(X), np.abs(dY), off)
@@ -179,7 +194,10 @@ def test_wgrad(shape, dt):
 
 
 @pytest.mark.parametrize("direction", ["forward", "dgrad", "wgrad"])
-def test_nan_stays_in_its_group(direction):
+@pytest.mark.parametrize("tun", TUNINGS)
+def test_nan_stays_in_its_group(direction, tun):
+    if direction == "wgrad" and tun == "n16":
+        pytest.skip("refused: 64 columns at least")
     """One group's rows and weights are NaN: the other groups' results are the same bits as without."""
     torch = torch_cuda()
     shape = ([20, 37, 5, 70], 0, 0, 136, 264)
@@ -188,10 +206,10 @@ def test_nan_stays_in_its_group(direction):
 
     def run(x, dy, w):
         if direction == "forward":
-            return cf.grouped_gemm(_dev(x, "bf16"), _dev(w, "bf16"), _i32(off))
+            return cf.grouped_gemm(_dev(x, "bf16"), _dev(w, "bf16"), _i32(off), tuning=_tuning(tun))
         if direction == "dgrad":
-            return cf.grouped_gemm_dgrad(_dev(dy, "bf16"), _dev(w, "bf16"), _i32(off))
-        return cf.grouped_gemm_wgrad(_dev(x, "bf16"), _dev(dy, "bf16"), _i32(off))
+            return cf.grouped_gemm_dgrad(_dev(dy, "bf16"), _dev(w, "bf16"), _i32(off), tuning=_tuning(tun))
+        return cf.grouped_gemm_wgrad(_dev(x, "bf16"), _dev(dy, "bf16"), _i32(off), tuning=_tuning(tun))
 
     clean = run(X, dY, W)
     bad = 2
@@ -248,9 +266,10 @@ def _lora_run(c, dt, bias=True, scale=True, **kw):
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("shape", LORA_SHAPES, ids=[f"{len(s[0])}s{sum(s[0])}r{s[3]}x{s[4]}R{s[6]}" for s in LORA_SHAPES])
 @pytest.mark.parametrize("extras", [True, False])
-def test_lora(shape, dt, extras):
+@pytest.mark.parametrize("tun", TUNINGS)
+def test_lora(shape, dt, extras, tun):
     c = _lora_case(shape, dt)
-    out = _host(_lora_run(c, dt, extras, extras))
+    out = _host(_lora_run(c, dt, extras, extras, tuning=_tuning(tun)))
     bias, scale = (c["bias"], c["scale"]) if extras else (None, None)
     ref = oracle.gemm_lora(c["X"], c["W"], bias, c["A"], c["B"], c["off"], c["ad"], scale)
     ab = {k: np.abs(c[k]) for k in ("X", "W", "A", "B")}
