@@ -1377,44 +1377,69 @@ cf_status grouped_sizes(int64_t T, int64_t N, int64_t K, int64_t groups, int dty
     return CF_OK;
 }
 
-// Accumulator columns, ring depth and grid of one grouped launch.
-// Columns (rows of the batch; WGRAD: columns of dW): four times the mean group,
-// so that an uneven group still reads its weights once, between 16 and 256.
-cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t N, int64_t groups, int64_t rank, const cf_tuning &t,
-                       const cf::DeviceInfo &dev, cf::GroupedArgs *a, int *ctas, int *smem) {
+// Accumulator columns where none are asked for.  Columns are rows of the batch (WGRAD: columns of dW): four times
+// the mean group, so that an uneven group still reads its weights once, between 16 and 256.
+int grouped_columns(int kind, int64_t T, int64_t N, int64_t groups) {
     int64_t want;
     if (kind == cf::GR_WGRAD) want = N;
     else if (kind == cf::GR_LORA) want = T;
     else want = std::min<int64_t>(T, 4 * ((T + groups - 1) / groups));
-    const int least = kind == cf::GR_WGRAD ? 64 : 16;  // WGRAD stages dY in 64-column blocks
-    int bn = least;
+    int bn = kind == cf::GR_WGRAD ? 64 : 16;  // WGRAD stages dY in 64-column blocks
     while (bn < 256 && bn < want) bn *= 2;
+    return bn;
+}
+
+// pieces of tiles: two for each CTA
+size_t grouped_partial_bytes(int bn) { return size_t(2 * cf::kGroupedWorkers) * 128 * size_t(bn) * 4; }
+constexpr size_t kGroupedCounterBytes = size_t(cf::kGroupedSplitTiles) * 4;
+// Head of a workspace, the same for every grouped and adapter call and all sizes, so that one workspace may serve
+// them in turn: the error word and two sets of counters, zero between launches (the adapters' two launches may
+// overlap).  Behind it, data that no launch expects to find.
+constexpr size_t kGroupedHead = cf::kErrBytes + 2 * kGroupedCounterBytes;
+
+// Ring depth, grid and workspace of one grouped launch: counter set 0 or 1, `room` bytes of partials at `part`.
+cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int64_t groups, int64_t rank,
+                       const cf_tuning &t, const cf::DeviceInfo &dev, void *ws, int set, unsigned char *part,
+                       size_t room, cf::GroupedArgs *a, int *ctas, int *smem) {
+    const bool wgrad = kind == cf::GR_WGRAD;
+    int bn = grouped_columns(kind, T, N, groups);
     if (t.n_slice != 0) {
-        if (t.n_slice != 16 && t.n_slice != 32 && t.n_slice != 64 && t.n_slice != 128 && t.n_slice != 256) return CF_ERR_UNSUPPORTED;
-        if (t.n_slice < least) return CF_ERR_UNSUPPORTED;
+        if (t.n_slice != 16 && t.n_slice != 32 && t.n_slice != 64 && t.n_slice != 128 && t.n_slice != 256)
+            return CF_ERR_UNSUPPORTED;
+        if (wgrad && t.n_slice < 64) return CF_ERR_UNSUPPORTED;
         bn = t.n_slice;
     }
     if (t.stages < 0 || t.stages > 12) return CF_ERR_UNSUPPORTED;
-    // CTA pairs where the tiles are full
+    // the most tiles there can be, for tiles of `features`
+    auto tiles_of = [&](int64_t features) {
+        const int64_t ft = (F + features - 1) / features;
+        return wgrad ? groups * ft * ((N + bn - 1) / bn) : ft * std::min<int64_t>(T, T / bn + groups);
+    };
+    // CTA pairs where there are full tiles for all of them; a smaller launch is better off dividing its tiles
     if (t.cluster_m < 0 || t.cluster_m > 2) return CF_ERR_UNSUPPORTED;
-    bool pair = kind != cf::GR_SHRINK && bn == 256 && F > 128;
+    bool pair = kind != cf::GR_SHRINK && bn == 256 && F > 128 && tiles_of(256) >= dev.sm_count;
     if (t.cluster_m != 0) pair = t.cluster_m == 2;
     if (pair && (kind == cf::GR_SHRINK || bn < 128)) return CF_ERR_UNSUPPORTED;
     int stages = t.stages > 0 ? t.stages : 12;
     while (stages > 2 && cf::grouped_smem_bytes(kind, pair, stages, bn, int(groups), int(rank)) > kMaxSmem) --stages;
     *smem = cf::grouped_smem_bytes(kind, pair, stages, bn, int(groups), int(rank));
     if (*smem > kMaxSmem || *smem > dev.max_smem_optin) return CF_ERR_UNSUPPORTED;
-    const int per = pair ? 256 : 128, width = pair ? 2 : 1;
-    const int64_t ft = (F + per - 1) / per;
-    const int64_t tiles = kind == cf::GR_WGRAD ? groups * ft * ((N + bn - 1) / bn)
-                                               : ft * std::min<int64_t>(T, T / bn + groups);
+    const int width = pair ? 2 : 1;
+    const int64_t tiles = tiles_of(128 * width);
     if (tiles >= (int64_t(1) << 31) - 65536) return CF_ERR_UNSUPPORTED;
-    int64_t c = std::min<int64_t>(tiles, dev.sm_count / width);
+    // a worker takes whole tiles or, divided, at least a few blocks of the contraction
+    const int64_t blocks = wgrad ? T / 64 + 1 : (C + 63) / 64;
+    int64_t c = pair ? tiles : std::min<int64_t>(tiles, dev.sm_count) * blocks;
+    c = std::min<int64_t>(c, std::min(dev.sm_count, cf::kGroupedWorkers) / width);
     if (t.max_clusters > 0) c = std::min<int64_t>(c, t.max_clusters);
     *ctas = int(std::max<int64_t>(c, 1)) * width;
     a->bn = bn;
     a->pair = pair;
     a->stages = stages;
+    a->counters = reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(ws) + cf::kErrBytes +
+                                               size_t(set) * kGroupedCounterBytes);
+    // (a forced tile wider than the workspace was sized for: whole tiles only)
+    a->partials = grouped_partial_bytes(bn) <= room ? reinterpret_cast<float *>(part) : nullptr;
     return CF_OK;
 }
 
@@ -1471,7 +1496,8 @@ cf_status grouped_rows(int kind, const void *rows, const void *W, const int32_t 
     cf::GroupedArgs a;
     grouped_args(&a, T, F, C, 0, E, dtype, offsets, ws, t);
     int ctas, smem;
-    st = plan_grouped(kind, T, F, 0, E, 0, t, dev, &a, &ctas, &smem);
+    st = plan_grouped(kind, T, F, C, 0, E, 0, t, dev, ws, 0, static_cast<unsigned char *>(ws) + kGroupedHead,
+                      ws_bytes - kGroupedHead, &a, &ctas, &smem);
     if (st != CF_OK) return st;
     if (!(fwd ? make_tmap_features(&a.tmap_a, &a.a_split, W, uint64_t(E), uint64_t(K), uint64_t(N))
               : make_tmap_features_t(&a.tmap_a, W, uint64_t(E), uint64_t(K), uint64_t(N))) ||
@@ -1486,11 +1512,11 @@ cf_status grouped_rows(int kind, const void *rows, const void *W, const int32_t 
 }  // namespace
 
 extern "C" size_t cf_grouped_gemm_workspace_size(int64_t T, int64_t N, int64_t K, int64_t E) {
-    (void)T;
-    (void)N;
     (void)K;
-    (void)E;
-    return cf::kErrBytes;
+    if (T < 0 || N <= 0 || E <= 0) return kGroupedHead;
+    return kGroupedHead +
+           grouped_partial_bytes(std::max(grouped_columns(cf::GR_FORWARD, T, N, E),
+                                          grouped_columns(cf::GR_WGRAD, T, N, E)));
 }
 
 extern "C" cf_status cf_grouped_gemm_ex(const void *X, const void *W, const int32_t *offsets, void *Y, void *Z,
@@ -1550,7 +1576,9 @@ extern "C" cf_status cf_grouped_gemm_wgrad_ex(const void *X, const void *dY, con
     cf::GroupedArgs a;
     grouped_args(&a, T, K, 0, N, E, int(dtype), offsets, workspace, t);
     int ctas, smem;
-    st = plan_grouped(cf::GR_WGRAD, T, K, N, E, 0, t, dev, &a, &ctas, &smem);
+    st = plan_grouped(cf::GR_WGRAD, T, K, 0, N, E, 0, t, dev, workspace, 0,
+                      static_cast<unsigned char *>(workspace) + kGroupedHead, workspace_bytes - kGroupedHead, &a,
+                      &ctas, &smem);
     if (st != CF_OK) return st;
     if (!make_tmap_blocks(&a.tmap_a, &a.a_split, X, uint64_t(T), uint64_t(K), 2) ||
         !make_tmap_blocks(&a.tmap_b, &a.b_split, dY, uint64_t(T), uint64_t(N), staged_columns(a) / 64))
@@ -1565,13 +1593,14 @@ extern "C" cf_status cf_grouped_gemm_wgrad(const void *X, const void *dY, const 
     return cf_grouped_gemm_wgrad_ex(X, dY, offsets, dW, T, N, K, E, dtype, workspace, workspace_bytes, stream, nullptr);
 }
 
-// workspace: error word, then H [T, R] fp32
+// workspace: head; partials of the first product; of the second (which may start while the first ends); H [T, R] fp32
 extern "C" size_t cf_gemm_lora_workspace_size(int64_t T, int64_t N, int64_t K, int64_t S, int64_t R) {
     (void)N;
     (void)K;
-    (void)S;
-    if (T < 0 || R < 0) return cf::kErrBytes;
-    return cf::kErrBytes + cf::align_up(size_t(T) * size_t(R) * 4, 256);
+    if (T < 0 || R < 0 || S <= 0) return kGroupedHead;
+    return kGroupedHead + grouped_partial_bytes(grouped_columns(cf::GR_SHRINK, T, 0, S)) +
+           grouped_partial_bytes(grouped_columns(cf::GR_LORA, T, 0, S)) +
+           cf::align_up(size_t(T) * size_t(R) * 4, 256);
 }
 
 extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *bias, const void *A, const void *B,
@@ -1598,14 +1627,18 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
     cf::DeviceInfo dev;
     if (!cf::current_device_info(&dev)) return CF_ERR_NO_DEVICE;
     if (dev.cc_major != 10 || dev.cc_minor != 3) return CF_ERR_NO_DEVICE;
-    float *H = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + cf::kErrBytes);
+    const size_t room_sh = grouped_partial_bytes(grouped_columns(cf::GR_SHRINK, T, 0, S));
+    const size_t room = grouped_partial_bytes(grouped_columns(cf::GR_LORA, T, 0, S));
+    unsigned char *const part_sh = static_cast<unsigned char *>(workspace) + kGroupedHead;
+    unsigned char *const part = part_sh + room_sh;
+    float *H = reinterpret_cast<float *>(part + room);
     cf::GroupedArgs sh, a;
     int sh_ctas = 0, sh_smem = 0, ctas, smem;
     if (L > 0) {
         cf_tuning ts = t;
         ts.n_slice = ts.stages = ts.cluster_m = 0;  // the knobs are the main product's
         grouped_args(&sh, T, R, K, 0, S, int(dtype), offsets, workspace, t);
-        st = plan_grouped(cf::GR_SHRINK, T, R, 0, S, 0, ts, dev, &sh, &sh_ctas, &sh_smem);
+        st = plan_grouped(cf::GR_SHRINK, T, R, K, 0, S, 0, ts, dev, workspace, 0, part_sh, room_sh, &sh, &sh_ctas, &sh_smem);
         if (st != CF_OK) return st;
         if (!make_tmap_features(&sh.tmap_a, &sh.a_split, A, uint64_t(L), uint64_t(K), uint64_t(R)) ||
             !make_tmap_bf16(&sh.tmap_b, X, uint64_t(T), uint64_t(K), 64, staged_columns(sh)))
@@ -1617,7 +1650,7 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
     }
     grouped_args(&a, T, N, K, 0, S, int(dtype), offsets, workspace, t);
     a.rank = int(R);
-    st = plan_grouped(cf::GR_LORA, T, N, 0, S, R, t, dev, &a, &ctas, &smem);
+    st = plan_grouped(cf::GR_LORA, T, N, K, 0, S, R, t, dev, workspace, 1, part, room, &a, &ctas, &smem);
     if (st != CF_OK) return st;
     if (!make_tmap_features(&a.tmap_a, &a.a_split, W, 1, uint64_t(K), uint64_t(N)) ||
         !make_tmap_bf16(&a.tmap_b, X, uint64_t(T), uint64_t(K), 64, staged_columns(a)))

@@ -233,6 +233,8 @@ enum GroupedKind : int {
 };
 
 constexpr int kGroupedMaxGroups = 1024;  // the group table lives in shared memory
+constexpr int kGroupedSplitTiles = 1024; // tiles whose contraction may be divided among CTAs
+constexpr int kGroupedWorkers = 160;     // CTAs that may hold a piece of a tile (a GB300 has 152 SMs)
 constexpr int kLoraMaxRank = 128;        // one tile of features in the first product
 
 struct GroupedArgs {
@@ -248,6 +250,8 @@ struct GroupedArgs {
     const float *low;        // LORA: H [T, rank]
     const void *lora_b;      // LORA: B [nweights, rank, F]
     uint32_t *err;
+    uint32_t *counters;      // [kGroupedSplitTiles] pieces arrived, zero between launches
+    float *partials;         // [2 * kGroupedWorkers][bn][128] pieces of tiles, or null: whole tiles only
     int T;                   // rows of X / dY
     int F;                   // features: length of the accumulator-lane axis of the result
     int C;                   // contraction length (WGRAD: the groups' rows instead)
@@ -257,7 +261,7 @@ struct GroupedArgs {
     int rank;                // LORA
     int fp16;                // 16-bit type of every operand: 0 bf16, 1 fp16
     int act;                 // FORWARD, DGRAD: 1 = GELU(tanh)
-    int bn;                  // columns of one accumulator tile (32, 64, 128 or 256)
+    int bn;                  // columns of one accumulator tile (16, 32, 64, 128 or 256)
     int stages;
     int pair;                // CTA pairs, one cta_group::2 MMA stream over 256 features (not SHRINK)
     unsigned long long timeout_ns;

@@ -46,6 +46,7 @@ constexpr int kBK = 64;         // contraction per stage (128 bytes: one swizzle
 constexpr int kFB = 128;        // features per tile (accumulator lanes)
 constexpr int kABytes = kFB * kBK * 2;
 constexpr int kRasterRows = 16;  // row tiles walked before the next feature tile
+constexpr int kMinStretch = 4;   // blocks a worker takes at least
 constexpr int kRankChunk = 32;   // LORA: ranks of B held in registers at once
 
 constexpr uint32_t kInfoProducer = 0x10000000u;
@@ -62,8 +63,8 @@ __host__ __device__ inline GrLayout gr_layout(int kind, bool pair, int stages, i
     // a CTA of a pair stages its own 128 features and half of the tile's columns
     L.stage_bytes = uint32_t(kABytes + (pair ? bn / 2 : bn) * kBK * 2);
     uint32_t off = uint32_t(stages) * L.stage_bytes;
-    L.table = off;  // int off[groups + 1], int pre[groups + 1]
-    off += (uint32_t(2 * (groups + 1)) * 4u + 15u) & ~15u;
+    L.table = off;  // Plan, int off[groups + 1], int pre[groups + 1]
+    off += (16u + uint32_t(2 * (groups + 1)) * 4u + 15u) & ~15u;
     L.stg = off;    // per epilogue warp: 16-bit [32 rows][32 features]; LORA: fp32 [32 rows][33]
     off += kind == GR_LORA ? uint32_t(kEpiWarps) * 32u * 33u * 4u
                            : (kind == GR_FORWARD || kind == GR_DGRAD) ? uint32_t(kEpiWarps) * 2048u : 0u;
@@ -87,51 +88,103 @@ __device__ __forceinline__ GrBars gr_bars(uint32_t base, int stages) {
     b.misc = b.mma_done + 8;
     return b;
 }
-static_assert(16 * 12 + 16 + 16 + 8 + 8 <= 256, "barrier area");
+static_assert(16 * 12 + 16 + 16 + 8 + 16 <= 256, "barrier area");
 
 template <bool kPair>
 __device__ __forceinline__ int feature_tiles(const GroupedArgs &a) {
     return kPair ? (a.F + 2 * kFB - 1) / (2 * kFB) : (a.F + kFB - 1) / kFB;
 }
 
-// one tile of work
+// one piece of work: a tile, or the part of its contraction that falls to this CTA
 struct Tile {
+    int id;     // tile number
     int g;      // group
     int w;      // its weights
     int f0;     // first feature of this CTA
     int col0;   // first accumulator column's row of the batch (WGRAD: column of dW)
     int n;      // columns that exist
     int nm;     // columns multiplied (n rounded up; a pair: half of them staged by each CTA)
-    int nk;     // 64-deep blocks of the contraction
+    int nk;     // 64-deep blocks of the tile's contraction
+    int kb0, kb1;  // the blocks of this piece
     int row0;   // WGRAD: first row of the group
     int rows;   // WGRAD: rows of the group
+    int first, last;  // workers that hold pieces of the tile
+    int slot;   // which of its two workspace slots this worker's piece goes to
+    __device__ bool whole() const { return first == last; }
+};
+
+// How the launch divides its work, decided on the device once the sizes are known (every CTA decides alike).
+// Whole tiles dealt out in turn; or, where the tiles are few or their last round is poorly filled, the blocks of all
+// tiles in one row, cut into equal stretches: a worker's stretch starts and ends inside a tile at most once each.
+// The pieces of a tile are added in the workspace in worker order (so equal calls give equal bits) by the
+// worker whose piece arrives last; nobody waits.
+struct Plan {
+    int split;    // stretches
+    int workers;  // that take part
+    int tiles;
+    int units;    // split: blocks of all tiles
 };
 
 template <int KIND, bool kPair>
 struct Walk {
     const int *off, *pre;
     const GroupedArgs &a;
+    const Plan plan;
     int ft;      // feature tiles
+    int per_group;  // WGRAD: tiles of a group
     int g;       // group of the current tile (tiles are visited in ascending order)
     int half;    // features of this CTA behind the tile's first: 0, or 128 in the second CTA of a pair
+    int worker, cur, begin, end;  // tile, or unit and this worker's stretch
 
-    __device__ Walk(const int *off_, const int *pre_, const GroupedArgs &a_, int half_)
-        : off(off_), pre(pre_), a(a_), g(0), half(half_) {
+    __device__ Walk(const int *off_, const int *pre_, const GroupedArgs &a_, const Plan &p, int worker_, int half_)
+        : off(off_), pre(pre_), a(a_), plan(p), g(0), half(half_), worker(worker_) {
         ft = feature_tiles<kPair>(a);
+        per_group = KIND == GR_WGRAD ? ft * ((a.N + a.bn - 1) / a.bn) : 0;
+        cur = worker;
+        begin = 0;
+        end = plan.tiles;
+        if (!kPair && plan.split) {
+            begin = cur = unit_of(worker);
+            end = worker < plan.workers ? unit_of(worker + 1) : cur;
+        }
     }
     static constexpr int kTileF = kPair ? 2 * kFB : kFB;
     // columns are multiplied in 16s; each half of a pair's in 16s (WGRAD: whole 64-column blocks)
     static constexpr int kGran = kPair ? (KIND == GR_WGRAD ? 128 : 32) : 16;
-    __device__ int total() const { return pre[groups()]; }
-    __device__ int groups() const { return KIND == GR_LORA ? 1 : a.groups; }
-    __device__ Tile at(int t) {
-        while (t >= pre[g + 1]) ++g;
-        Tile r;
+    __device__ int unit_of(int w) const { return int((long long)plan.units * w / plan.workers); }
+    __device__ int worker_of(int u) const { return int(((long long)(u + 1) * plan.workers - 1) / plan.units); }
+
+    __device__ bool next(Tile &r) {
+        if (cur >= end) return false;
+        int local, kb = 0, u0 = 0;
+        if constexpr (KIND == GR_WGRAD) {
+            // pre: blocks of the groups before, of one tile (an empty group counts one, which holds no rows)
+            if (!kPair && plan.split) {
+                while (cur >= per_group * pre[g + 1]) ++g;
+                const int nk = pre[g + 1] - pre[g], at = cur - per_group * pre[g];
+                local = at / nk;
+                kb = at % nk;
+            } else {
+                g = cur / per_group;
+                local = cur % per_group;
+            }
+            r.id = g * per_group + local;
+        } else {
+            // pre: tiles of the groups before
+            const int nk = (a.C + kBK - 1) / kBK;
+            r.id = cur;
+            if (!kPair && plan.split) {
+                r.id = cur / nk;
+                kb = cur % nk;
+            }
+            while (r.id >= pre[g + 1]) ++g;
+            local = r.id - pre[g];
+        }
         r.g = g;
         r.w = KIND == GR_SHRINK ? a.windex[g] : (KIND == GR_LORA ? 0 : g);
-        const int local = t - pre[g];
         const int lo = off[KIND == GR_LORA ? 0 : g];
         const int rows = off[KIND == GR_LORA ? a.groups : g + 1] - lo;
+        int blocks;  // of the tile, one at least
         if constexpr (KIND == GR_WGRAD) {
             const int nt = (a.N + a.bn - 1) / a.bn;
             r.f0 = (local / nt) * kTileF + half;
@@ -140,6 +193,7 @@ struct Walk {
             r.row0 = lo;
             r.rows = rows;
             r.nk = (rows + kBK - 1) / kBK;
+            blocks = max(r.nk, 1);
         } else {
             const int rt = (rows + a.bn - 1) / a.bn;              // row tiles of the group,
             const int per = ((rows + rt - 1) / rt + kGran - 1) & ~(kGran - 1);  // cut evenly
@@ -151,11 +205,30 @@ struct Walk {
             r.col0 = lo + rtile * per;
             r.n = min(per, rows - rtile * per);
             r.row0 = r.rows = 0;
-            r.nk = (a.C + kBK - 1) / kBK;
+            r.nk = blocks = (a.C + kBK - 1) / kBK;
         }
         r.nm = (r.n + kGran - 1) & ~(kGran - 1);
-        return r;
+        r.kb0 = kb;
+        r.kb1 = r.nk;
+        r.first = r.last = worker;
+        r.slot = 0;
+        if (!kPair && plan.split) {
+            u0 = cur - kb;  // the tile's first unit
+            const int take = min(blocks - kb, end - cur);
+            r.kb1 = min(kb + take, r.nk);
+            if (take < blocks) {
+                r.first = worker_of(u0);
+                r.last = worker_of(u0 + blocks - 1);
+                r.slot = slot_of(worker, u0);
+            }
+            cur += take;
+        } else {
+            cur += plan.workers;
+        }
+        return true;
     }
+    // a worker's first piece goes to its slot 0 unless its stretch began in an earlier tile
+    __device__ int slot_of(int w, int u0) const { return unit_of(w) >= u0 ? 0 : 1; }
 };
 
 // GELU in the tanh form is z * p with p = 1 / (1 + exp(-2u)), u = sqrt(2/pi)(z + 0.044715 z^3):
@@ -219,9 +292,9 @@ __device__ __forceinline__ void load_fragment(uint4 (&z)[4], const GroupedArgs &
 }
 
 // Group table: off[i] = offsets[i] clamped to [0, T] and to not decrease, pre[i] = tiles of the groups
-// before i.  One warp, after the raw offsets are in off[].
+// before i (WGRAD: blocks of one tile of each), and the plan.  One warp, after the raw offsets are in off[].
 template <int KIND, bool kPair>
-__device__ void scan_table(int *off, int *pre, const GroupedArgs &a, uint32_t *err) {
+__device__ void scan_table(int *off, int *pre, Plan *plan, const GroupedArgs &a, int workers, uint32_t *err) {
     const int lane = threadIdx.x & 31;
     const int n = a.groups + 1;
     const int ft = feature_tiles<kPair>(a);
@@ -246,14 +319,15 @@ __device__ void scan_table(int *off, int *pre, const GroupedArgs &a, uint32_t *e
     }
     __syncwarp();
     const int groups = KIND == GR_LORA ? 1 : a.groups;
-    int carry = 0;
+    int carry = 0, longest = 0;
     for (int i0 = 0; i0 < groups; i0 += 32) {
         const int i = i0 + lane;
         int tiles = 0;
         if (i < groups) {
             const int rows = off[KIND == GR_LORA ? a.groups : i + 1] - off[i];
             if constexpr (KIND == GR_WGRAD) {
-                tiles = ft * ((a.N + a.bn - 1) / a.bn);
+                tiles = max((rows + kBK - 1) / kBK, 1);
+                longest = max(longest, tiles);
             } else {
                 tiles = ft * ((rows + a.bn - 1) / a.bn);
                 if constexpr (KIND == GR_SHRINK) {
@@ -272,7 +346,34 @@ __device__ void scan_table(int *off, int *pre, const GroupedArgs &a, uint32_t *e
         if (i < groups) pre[i + 1] = carry + s;
         carry += __shfl_sync(0xffffffffu, s, 31);
     }
-    if (lane == 0) pre[0] = 0;
+    if constexpr (KIND == GR_WGRAD) longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) {
+        pre[0] = 0;
+        // Rounds of whole tiles against equal stretches, in blocks (of about 0.36 us each: 16 KB of weights at an
+        // SM's share of HBM, or MMAs of 256 columns).  Adding pieces costs about 6 blocks, and another for each 32
+        // columns written and read back.
+        const long long each = KIND == GR_WGRAD ? 0 : (a.C + kBK - 1) / kBK;
+        const long long tiles = KIND == GR_WGRAD ? (long long)groups * ft * ((a.N + a.bn - 1) / a.bn) : carry;
+        const long long units = KIND == GR_WGRAD ? (long long)ft * ((a.N + a.bn - 1) / a.bn) * carry : tiles * each;
+        Plan p;
+        p.split = 0;
+        p.workers = workers;
+        p.tiles = int(tiles);
+        p.units = 0;
+        if (!kPair && a.partials != nullptr && tiles > 0 && tiles <= kGroupedSplitTiles && units < (1ll << 30)) {
+            const long long share = (units + workers - 1) / workers;
+            const long long stretch = share > kMinStretch ? share : kMinStretch;
+            const long long rounds = (tiles + workers - 1) / workers;
+            long long whole = rounds * units / tiles;  // WGRAD: of mean tiles, or the longest one
+            if (longest > whole) whole = longest;
+            if (whole > stretch + 6 + a.bn / 32) {
+                p.split = 1;
+                p.workers = int((units + stretch - 1) / stretch);
+                p.units = int(units);
+            }
+        }
+        *plan = p;
+    }
     if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
         ptx::record_error(err, 8u /*CF_ERR_DEVICE_BOUNDS*/, kInfoTable);
 }
@@ -301,6 +402,26 @@ __device__ __forceinline__ void zero_tail(uint8_t *st, int left, int steps, int 
     }
     ptx::fence_proxy_async_smem();
     __syncwarp();
+}
+
+// the tile's pieces at columns c .. c + 31 of one lane, added in worker order
+template <int KIND, bool kPair>
+__device__ __forceinline__ void sum_pieces(uint32_t (&v)[32], const GroupedArgs &a, const Walk<KIND, kPair> &walk,
+                                           const Tile &w, int c, int l) {
+    float s[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) s[j] = 0.f;
+    const int cols = min(32, w.n - c);
+    const int u0 = KIND == GR_WGRAD ? walk.per_group * walk.pre[w.g] + (w.id - w.g * walk.per_group) * max(w.nk, 1)
+                                    : w.id * w.nk;
+    for (int k = w.first; k <= w.last; ++k) {
+        const float *p = a.partials + size_t(2 * k + walk.slot_of(k, u0)) * size_t(kFB * a.bn) + size_t(c) * kFB + l;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < cols) s[j] += __ldcg(p + j * kFB);
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(s[j]);
 }
 
 template <bool kPair>
@@ -371,7 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     const int stages = a.stages;
     const GrLayout L = gr_layout(KIND, kPair, stages, a.bn, a.groups, a.rank);
     const GrBars B = gr_bars(base + L.bars, stages);
-    int *const off = reinterpret_cast<int *>(smem_raw + L.table);
+    Plan *const plan = reinterpret_cast<Plan *>(smem_raw + L.table);
+    int *const off = reinterpret_cast<int *>(smem_raw + L.table + sizeof(Plan));
     int *const pre = off + a.groups + 1;
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem_raw + (B.misc - base));
     volatile uint32_t *abort = misc + 1;
@@ -419,14 +541,14 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     ptx::griddep_wait();
     for (int i = threadIdx.x; i <= a.groups; i += kThreads) off[i] = a.offsets[i];
     __syncthreads();
-    if (warp == 0) scan_table<KIND, kPair>(off, pre, a, a.err);
+    if (warp == 0) scan_table<KIND, kPair>(off, pre, plan, a, workers, a.err);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     if constexpr (kPair) ptx::cluster_sync();  // the peer's barriers are initialised before anything signals them
     const uint32_t tmem_base = misc[0];
-    Walk<KIND, kPair> walk(off, pre, a, int(crank) * kFB);
-    const int total = walk.total();
+    Walk<KIND, kPair> walk(off, pre, a, *plan, worker, int(crank) * kFB);
+    Tile w;
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -434,13 +556,12 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             uint32_t it = 0, s = 0, ph = 0;
             bool ok = true;
             const uint32_t full_lead = kPair ? ptx::mapa(B.full0, 0u) : B.full0;
-            for (int t = worker; t < total && ok; t += workers) {
-                const Tile w = walk.at(t);
+            while (ok && walk.next(w)) {
                 const int cols = kPair ? w.nm / 2 : w.nm;  // columns this CTA stages
                 const int col0 = w.col0 + int(crank) * cols;
                 const int bblk = b_blocks<KIND, kPair>(a, w);
                 const uint32_t own = uint32_t(kABytes) + b_bytes<KIND, kPair>(a, w);
-                for (int kb = 0; kb < w.nk; ++kb) {
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     if (!ptx::mbar_try_wait(B.empty0 + 8 * s, ph ^ 1u)) {
                         ok = ptx::mbar_wait_bounded(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
                         if (!ok) break;
@@ -483,8 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             if constexpr (kPair && KIND == GR_WGRAD) {
                 // the second CTA of a pair: zero its part of each group's last block
                 uint32_t s = 0, ph = 0;  // ring position of the tile's first block; a phase bit per stage
-                for (int t = worker; t < total; t += workers) {
-                    const Tile w = walk.at(t);
+                while (walk.next(w)) {
                     if (w.nk > 0 && (w.rows & 15) != 0) {
                         const uint32_t at = (s + uint32_t(w.nk) - 1u) % uint32_t(stages);
                         const bool ok = ptx::mbar_wait_bounded(B.full0 + 8 * at, (ph >> at) & 1u, tmo, abort, a.err,
@@ -502,22 +622,21 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             const uint64_t ad0 = kAMn ? sw128_desc(base, 8192, 1024) : sw128_desc(base, 16, 1024);
             const uint64_t bd0 = kBMn ? sw128_desc(base + kABytes, 8192, 1024) : sw128_desc(base + kABytes, 16, 1024);
             uint32_t s = 0, ph = 0;
-            int tile = 0;
-            for (int t = worker; t < total; t += workers, ++tile) {
-                const Tile w = walk.at(t);
+            for (int tile = 0; walk.next(w); ++tile) {
                 const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
                 const uint32_t d = tmem_base + buf * uint32_t(a.bn);
                 const uint32_t idesc = idesc_f16(kPair ? 2 * kFB : kFB, w.nm, a.fp16 != 0, kAMn, kBMn);
                 const int length = KIND == GR_WGRAD ? w.rows : a.C;
-                const int whole = length / kBK;  // blocks of 64; the rest of the contraction is one shorter block
-                const int left = length - whole * kBK;
+                // blocks of 64, and where the piece ends with the contraction the shorter one behind them
+                const int whole = min(w.kb1, length / kBK);
+                const int left = w.kb1 > whole ? length - whole * kBK : 0;
                 bool ok = true;
                 if (lane == 0) {
                     ok = ptx::mbar_wait_bounded(B.tmem_empty0 + 8 * buf, tph ^ 1u, tmo, abort, a.err, kInfoMma | buf);
                     ptx::tc_fence_after();
                     // The one issuing thread's work between MMA groups is kept short, so that the tensor pipe's
                     // queue does not run dry: fixed steps, descriptors by addition.
-                    for (int kb = 0; kb < whole && ok; ++kb) {
+                    for (int kb = w.kb0; kb < whole && ok; ++kb) {
                         const uint32_t fb = B.full0 + 8 * s;
                         if (!ptx::mbar_try_wait(fb, ph)) {
                             ok = ptx::mbar_wait_bounded(fb, ph, tmo, abort, a.err, kInfoMma | 0x100u | s);
@@ -528,7 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
 #pragma unroll
                         for (int k = 0; k < kBK / 16; ++k)
                             issue_mma<kPair>(d, ad0 + so + uint64_t(k * (kAMn ? 128 : 2)),
-                                             bd0 + so + uint64_t(k * (kBMn ? 128 : 2)), idesc, (kb | k) != 0 ? 1u : 0u);
+                                             bd0 + so + uint64_t(k * (kBMn ? 128 : 2)), idesc,
+                                             kb > w.kb0 || k > 0 ? 1u : 0u);
                         issue_commit<kPair>(B.empty0 + 8 * s);
                         if (++s == uint32_t(stages)) {
                             s = 0;
@@ -559,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                         for (int k = 0; k < steps; ++k)
                             issue_mma<kPair>(d, ad0 + so + uint64_t(k * (kAMn ? 128 : 2)),
                                              bd0 + so + uint64_t(k * (kBMn ? 128 : 2)), idesc,
-                                             (whole | k) != 0 ? 1u : 0u);
+                                             whole > w.kb0 || k > 0 ? 1u : 0u);
                         issue_commit<kPair>(B.empty0 + 8 * s);
                     }
                     if (++s == uint32_t(stages)) {
@@ -585,22 +705,57 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         const int half = e >> 2;
         const int q = warp & 3;
         const bool fp16 = a.fp16 != 0;
-        int tile = 0;
-        for (int t = worker; t < total; t += workers, ++tile) {
-            const Tile w = walk.at(t);
+        for (int tile = 0; walk.next(w); ++tile) {
             const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
             uint4 zv[4];  // DGRAD: the next fragment's pre-activations, on their way before the accumulator is ready
             if constexpr (KIND == GR_DGRAD)
-                if (a.preact && half * 32 < w.n) load_fragment(zv, a, w, half * 32, q, lane, true);
+                if (a.preact && half * 32 < w.n && w.whole()) load_fragment(zv, a, w, half * 32, q, lane, true);
             const bool ok = ptx::mbar_wait_bounded(B.tmem_full0 + 8 * buf, tph, tmo, abort, a.err, kInfoEpi | buf);
             ptx::tc_fence_after();
             const uint32_t tacc = tmem_base + (uint32_t(q * 32) << 16) + buf * uint32_t(a.bn);
             const int f = w.f0 + q * 32 + lane;
             const bool live = f < a.F && ok;
+            bool held = true;  // the accumulator is still this tile's
+            if (!kPair && !w.whole()) {
+                // a piece of the tile: to the workspace, [column][lane]; the last to arrive goes on with the sum
+                float *const mine = a.partials + size_t(2 * worker + w.slot) * size_t(kFB * a.bn) + q * 32 + lane;
+                for (int c = half * 32; c < w.n; c += 64) {
+                    uint32_t v[32];
+                    ptx::tmem_ld32(tacc + uint32_t(c), v);
+                    ptx::tmem_ld_wait();
+                    const int cols = min(32, w.n - c);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < cols) __stcg(mine + (c + j) * kFB, __uint_as_float(v[j]));
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(B.tmem_empty0 + 8 * buf);
+                held = false;
+                __threadfence();
+                ptx::named_bar_sync(3, kEpiWarps * 32);
+                if (threadIdx.x == 64) {
+                    const uint32_t before = ptx::atom_add_acq_rel_gpu(a.counters + w.id, 1u);
+                    const bool last = before == uint32_t(w.last - w.first);
+                    if (last) ptx::st_relaxed_gpu(a.counters + w.id, 0u);  // for the next launch
+                    misc[2] = last;
+                }
+                ptx::named_bar_sync(3, kEpiWarps * 32);
+                const bool last = misc[2] != 0u;
+                ptx::named_bar_sync(3, kEpiWarps * 32);  // read before the next piece's verdict is written
+                if (!last) continue;
+                __threadfence();
+                if constexpr (KIND == GR_DGRAD)
+                    if (a.preact && half * 32 < w.n) load_fragment(zv, a, w, half * 32, q, lane, true);
+            }
             for (int c = half * 32; c < w.n; c += 64) {
                 uint32_t v[32];
-                ptx::tmem_ld32(tacc + uint32_t(c), v);
-                ptx::tmem_ld_wait();
+                if (kPair || w.whole()) {
+                    ptx::tmem_ld32(tacc + uint32_t(c), v);
+                    ptx::tmem_ld_wait();
+                } else {
+                    sum_pieces(v, a, walk, w, c, q * 32 + lane);
+                }
                 const int cols = min(32, w.n - c);
                 if constexpr (KIND == GR_FORWARD || KIND == GR_DGRAD) {
                     // The fragment is turned in shared memory (a lane's feature column in, whole rows out), so that
@@ -720,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
+            if (held && lane == 0) {
                 if constexpr (kPair) ptx::mbar_arrive_cluster(ptx::mapa(B.tmem_empty0 + 8 * buf, 0u));
                 else ptx::mbar_arrive(B.tmem_empty0 + 8 * buf);
             }

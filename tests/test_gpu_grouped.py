@@ -351,3 +351,64 @@ def test_bad_adapters_are_none_and_reported():
                      scale=torch.from_numpy(c["scale"]).cuda(), workspace=ws)
     assert cf.cf_get_device_status(ws)[0] == cf.CF_ERR_DEVICE_BOUNDS
     assert torch.equal(good, y)
+
+
+SPLIT = [  # few tiles, long contractions: the tiles' contractions are divided among CTAs
+    ([2, 1], 0, 0, 4096, 128), ([1, 0, 40], 1, 2, 2056, 264), ([200, 7], 0, 0, 1992, 128), ([16], 0, 0, 8192, 8)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("shape", SPLIT, ids=[f"{sum(s[0])}r{s[3]}x{s[4]}" for s in SPLIT])
+@pytest.mark.parametrize("tun", ["auto", "n256", "n16"])
+def test_divided_contraction(shape, dt, tun):
+    """forward over a long K, input gradient over a long N, weight gradient over many rows; twice on one workspace
+    (its counters return to zero), equal bits."""
+    torch = torch_cuda()
+    X, W, off, T, K, N = _forward_case(shape, dt, seed=7)
+    E = W.shape[0]
+    ws = cf.new_workspace(cf.cf_grouped_gemm_workspace_size(T, max(N, K), max(N, K), E))
+    live = slice(off[0], off[-1])
+    Xd, Wd, Wt = _dev(X, dt), _dev(W, dt), _dev(np.swapaxes(W, 1, 2), dt)
+    ref, Z = oracle.grouped_gemm(X, W, off, act="gelu_tanh")
+    mag = oracle.grouped_gemm(np.abs(X), np.abs(W), off)[0]
+    kw = dict(workspace=ws, tuning=_tuning(tun))
+    y = cf.grouped_gemm(Xd, Wd, _i32(off), act="gelu_tanh", **kw)
+    _status(ws)
+    _check(_host(y)[live], ref[live], _gelu_slack(ref[live], K * ACC * mag[live]), dt, "Y")
+    pre = _dev(2.0 * _rng(8).standard_normal((T, N)), dt)
+    dx = cf.grouped_gemm_dgrad(Xd, Wt, _i32(off), preact=pre, **kw)  # rows of length K, "features" N
+    _status(ws)
+    slope = oracle.gelu_tanh_slope(_host(pre))
+    _check(_host(dx)[live], (Z * slope)[live], (1.13 * K * ACC * mag + 2.0 ** -16 * np.abs(Z))[live], dt, "dX")
+    rows = _offsets([3 * K // 2, 0, 1], 1)
+    A, D = _round(_rng(9).standard_normal((rows[-1] + 2, 72)), dt), _round(_rng(10).standard_normal((rows[-1] + 2, N)) / 64, dt)
+    A[rows[-1]:] = np.nan
+    if tun != "n16":
+        ws2 = cf.new_workspace(cf.cf_grouped_gemm_workspace_size(A.shape[0], N, 72, 3))
+        dw = cf.grouped_gemm_wgrad(_dev(A, dt), _dev(D, dt), _i32(rows), workspace=ws2, tuning=_tuning(tun))
+        _status(ws2)
+        want, wmag = oracle.grouped_gemm_wgrad(A, D, rows), oracle.grouped_gemm_wgrad(np.abs(A), np.abs(D), rows)
+        _check(_host(dw), want, np.diff(rows)[:, None, None] * ACC * wmag, dt, "dW")
+        assert torch.equal(dw, cf.grouped_gemm_wgrad(_dev(A, dt), _dev(D, dt), _i32(rows), workspace=ws2,
+                                                     tuning=_tuning(tun)))
+    y2 = cf.grouped_gemm(Xd, Wd, _i32(off), act="gelu_tanh", **kw)
+    assert torch.equal(y[live], y2[live])
+
+
+def test_one_workspace_serves_calls_of_many_sizes():
+    """Grouped and adapter calls of different sizes in turn on one workspace give what fresh ones give."""
+    torch = torch_cuda()
+    ws = cf.new_workspace(1 << 26)
+    for _ in range(2):
+        for shape in LORA_SHAPES[:4] + [([2, 1], 0, 0, 4096, 128, 2, 16, [1, 0])]:
+            c = _lora_case(shape, "bf16")
+            X, off = _dev(c["X"], "bf16"), _i32(c["off"])
+            args = (X, _dev(c["W"], "bf16"), None, _dev(c["A"], "bf16"), _dev(c["B"], "bf16"), off, _i32(c["ad"]))
+            live = slice(c["off"][0], c["off"][-1])
+            assert torch.equal(cf.gemm_lora(*args, workspace=ws)[live], cf.gemm_lora(*args)[live])
+            W = _dev(np.stack([c["W"]] * len(c["ad"])), "bf16")
+            y, fresh = (cf.grouped_gemm(X, W, off, workspace=w) for w in (ws, None))
+            assert torch.equal(y[live], fresh[live])
+            assert torch.equal(cf.grouped_gemm_wgrad(X[live], y[live], off - off[0], workspace=ws),
+                               cf.grouped_gemm_wgrad(X[live], y[live], off - off[0]))
+    _status(ws)
