@@ -1338,7 +1338,8 @@ bool make_tmap_nd(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *d
 
 // Feature operand of FORWARD, SHRINK and LORA: weights [count, K, F], features contiguous.  Two 64-feature blocks of 64
 // rows a copy where the rows consist of whole blocks, one otherwise.
-bool make_tmap_features(CUtensorMap *m, int *split, const void *ptr, uint64_t count, uint64_t K, uint64_t F) {
+bool make_tmap_features(CUtensorMap *m, int *split, const void *ptr, uint64_t count, uint64_t K, uint64_t F,
+                        int blocks) {
     *split = F % 64 != 0;
     if (*split) {
         const cuuint64_t dims[3] = {F, K, count}, strides[2] = {F * 2, K * F * 2};
@@ -1346,7 +1347,7 @@ bool make_tmap_features(CUtensorMap *m, int *split, const void *ptr, uint64_t co
         return make_tmap_nd(m, ptr, 3, dims, strides, box);
     }
     const cuuint64_t dims[4] = {64, K, F / 64, count}, strides[3] = {F * 2, 128, K * F * 2};
-    const cuuint32_t box[4] = {64, 64, 2, 1};
+    const cuuint32_t box[4] = {64, 64, cuuint32_t(blocks), 1};
     return make_tmap_nd(m, ptr, 4, dims, strides, box);
 }
 
@@ -1421,7 +1422,12 @@ cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int
     if (t.cluster_m != 0) pair = t.cluster_m == 2;
     if (pair && (kind == cf::GR_SHRINK || bn < 128)) return CF_ERR_UNSUPPORTED;
     int stages = t.stages > 0 ? t.stages : 12;
-    while (stages > 2 && cf::grouped_smem_bytes(kind, pair, stages, bn, int(groups), int(rank)) > kMaxSmem) --stages;
+    // a decode batch's two adapter products share the SMs: the second reads its weights while the first runs
+    const int shrink_room = 98 * 1024, room_smem = bn > 64                ? kMaxSmem
+                                                   : kind == cf::GR_SHRINK ? shrink_room
+                                                   : kind == cf::GR_LORA   ? kMaxSmem - shrink_room - 2048
+                                                                           : kMaxSmem;
+    while (stages > 2 && cf::grouped_smem_bytes(kind, pair, stages, bn, int(groups), int(rank)) > room_smem) --stages;
     *smem = cf::grouped_smem_bytes(kind, pair, stages, bn, int(groups), int(rank));
     if (*smem > kMaxSmem || *smem > dev.max_smem_optin) return CF_ERR_UNSUPPORTED;
     const int width = pair ? 2 : 1;
@@ -1435,6 +1441,7 @@ cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int
     *ctas = int(std::max<int64_t>(c, 1)) * width;
     a->bn = bn;
     a->pair = pair;
+    a->a_blocks = F <= 64 && kind != cf::GR_DGRAD && !pair ? 1 : 2;
     a->stages = stages;
     a->counters = reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(ws) + cf::kErrBytes +
                                                size_t(set) * kGroupedCounterBytes);
@@ -1499,7 +1506,8 @@ cf_status grouped_rows(int kind, const void *rows, const void *W, const int32_t 
     st = plan_grouped(kind, T, F, C, 0, E, 0, t, dev, ws, 0, static_cast<unsigned char *>(ws) + kGroupedHead,
                       ws_bytes - kGroupedHead, &a, &ctas, &smem);
     if (st != CF_OK) return st;
-    if (!(fwd ? make_tmap_features(&a.tmap_a, &a.a_split, W, uint64_t(E), uint64_t(K), uint64_t(N))
+    if (!(fwd ? make_tmap_features(&a.tmap_a, &a.a_split, W, uint64_t(E), uint64_t(K), uint64_t(N),
+                                 a.a_blocks)
               : make_tmap_features_t(&a.tmap_a, W, uint64_t(E), uint64_t(K), uint64_t(N))) ||
         !make_tmap_bf16(&a.tmap_b, rows, uint64_t(T), uint64_t(C), 64, staged_columns(a)))
         return CF_ERR_CUDA;
@@ -1580,7 +1588,7 @@ extern "C" cf_status cf_grouped_gemm_wgrad_ex(const void *X, const void *dY, con
                       static_cast<unsigned char *>(workspace) + kGroupedHead, workspace_bytes - kGroupedHead, &a,
                       &ctas, &smem);
     if (st != CF_OK) return st;
-    if (!make_tmap_blocks(&a.tmap_a, &a.a_split, X, uint64_t(T), uint64_t(K), 2) ||
+    if (!make_tmap_blocks(&a.tmap_a, &a.a_split, X, uint64_t(T), uint64_t(K), uint32_t(a.a_blocks)) ||
         !make_tmap_blocks(&a.tmap_b, &a.b_split, dY, uint64_t(T), uint64_t(N), staged_columns(a) / 64))
         return CF_ERR_CUDA;
     a.out = dW;
@@ -1593,7 +1601,7 @@ extern "C" cf_status cf_grouped_gemm_wgrad(const void *X, const void *dY, const 
     return cf_grouped_gemm_wgrad_ex(X, dY, offsets, dW, T, N, K, E, dtype, workspace, workspace_bytes, stream, nullptr);
 }
 
-// workspace: head; partials of the first product; of the second (which may start while the first ends); H [T, R] fp32
+// workspace: head; partials of the first product; of the second (which may start while the first ends); H [T, 2, R] 16-bit
 extern "C" size_t cf_gemm_lora_workspace_size(int64_t T, int64_t N, int64_t K, int64_t S, int64_t R) {
     (void)N;
     (void)K;
@@ -1631,7 +1639,7 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
     const size_t room = grouped_partial_bytes(grouped_columns(cf::GR_LORA, T, 0, S));
     unsigned char *const part_sh = static_cast<unsigned char *>(workspace) + kGroupedHead;
     unsigned char *const part = part_sh + room_sh;
-    float *H = reinterpret_cast<float *>(part + room);
+    void *H = part + room;
     cf::GroupedArgs sh, a;
     int sh_ctas = 0, sh_smem = 0, ctas, smem;
     if (L > 0) {
@@ -1640,7 +1648,7 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
         grouped_args(&sh, T, R, K, 0, S, int(dtype), offsets, workspace, t);
         st = plan_grouped(cf::GR_SHRINK, T, R, K, 0, S, 0, ts, dev, workspace, 0, part_sh, room_sh, &sh, &sh_ctas, &sh_smem);
         if (st != CF_OK) return st;
-        if (!make_tmap_features(&sh.tmap_a, &sh.a_split, A, uint64_t(L), uint64_t(K), uint64_t(R)) ||
+        if (!make_tmap_features(&sh.tmap_a, &sh.a_split, A, uint64_t(L), uint64_t(K), uint64_t(R), sh.a_blocks) ||
             !make_tmap_bf16(&sh.tmap_b, X, uint64_t(T), uint64_t(K), 64, staged_columns(sh)))
             return CF_ERR_CUDA;
         sh.windex = adapters;
@@ -1652,9 +1660,13 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
     a.rank = int(R);
     st = plan_grouped(cf::GR_LORA, T, N, K, 0, S, R, t, dev, workspace, 1, part, room, &a, &ctas, &smem);
     if (st != CF_OK) return st;
-    if (!make_tmap_features(&a.tmap_a, &a.a_split, W, 1, uint64_t(K), uint64_t(N)) ||
+    if (!make_tmap_features(&a.tmap_a, &a.a_split, W, 1, uint64_t(K), uint64_t(N), a.a_blocks) ||
         !make_tmap_bf16(&a.tmap_b, X, uint64_t(T), uint64_t(K), 64, staged_columns(a)))
         return CF_ERR_CUDA;
+    if (L > 0 && (!make_tmap_features(&a.tmap_lb, &a.a_split, B, uint64_t(L), uint64_t(R), uint64_t(N), a.a_blocks) ||
+                  !make_tmap_bf16(&a.tmap_h, H, uint64_t(T), uint64_t(2 * R), 64, staged_columns(a))))
+        return CF_ERR_CUDA;
+    a.after_shrink = L > 0 && t.disable_pdl == 0;
     a.windex = adapters;
     a.nweights = int(L);
     a.bias = bias;

@@ -228,8 +228,8 @@ enum GroupedKind : int {
     GR_FORWARD = 0,  // Y = act(X_g . W_g), optionally keeping the pre-activation
     GR_DGRAD = 1,    // dX = (dY_g . W_g^T) (* act'(Z))
     GR_WGRAD = 2,    // dW_g = X_g^T . dY_g
-    GR_SHRINK = 3,   // H = scale[a] * X_g . A_a in fp32 (adapters: groups are requests)
-    GR_LORA = 4,     // Y = X . W + bias + H . B_a, one group of all the requests' rows
+    GR_SHRINK = 3,   // H = scale[a] * X_g . A_a (adapters: groups are requests), as two 16-bit parts
+    GR_LORA = 4,     // Y = X . W + bias + H . B_a
 };
 
 constexpr int kGroupedMaxGroups = 1024;  // the group table lives in shared memory
@@ -240,14 +240,18 @@ constexpr int kLoraMaxRank = 128;        // one tile of features in the first pr
 struct GroupedArgs {
     CUtensorMap tmap_a;    // the operand whose features become accumulator lanes: W (WGRAD: X)
     CUtensorMap tmap_b;    // the operand whose rows become accumulator columns: X or dY (WGRAD: dY)
+    CUtensorMap tmap_lb;   // LORA: B of the adapters, as tmap_a
+    CUtensorMap tmap_h;    // LORA: H, as tmap_b
+    int a_blocks;          // 64-feature blocks staged: 1 where there are no more than 64 features, else 2
     int a_split, b_split;  // 1: rows of 64-column blocks do not tile the matrix, so one block a copy (a length % 64)
     const int32_t *offsets;  // [groups + 1] rows of each group (LORA: of each request)
     const int32_t *windex;   // SHRINK, LORA: [groups] adapter of each request, -1 for none
-    void *out;               // Y / dX / dW / H
+    void *out;               // Y / dX / dW / H [T, 2, rank]
     void *preact;            // FORWARD: Z written; DGRAD: Z read; or null
     const float *bias;       // LORA: [F] or null
     const float *scale;      // SHRINK: [nweights] or null
-    const float *low;        // LORA: H [T, rank]
+    const void *low;         // LORA: H [T, 2, rank] 16-bit, upper parts and rests
+    int after_shrink;        // LORA: the launch before is the SHRINK that makes H (it waits for what came before it)
     const void *lora_b;      // LORA: B [nweights, rank, F]
     uint32_t *err;
     uint32_t *counters;      // [kGroupedSplitTiles] pieces arrived, zero between launches

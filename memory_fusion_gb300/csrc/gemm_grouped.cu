@@ -47,29 +47,42 @@ constexpr int kFB = 128;        // features per tile (accumulator lanes)
 constexpr int kABytes = kFB * kBK * 2;
 constexpr int kRasterRows = 16;  // row tiles walked before the next feature tile
 constexpr int kMinStretch = 4;   // blocks a worker takes at least
-constexpr int kRankChunk = 32;   // LORA: ranks of B held in registers at once
+constexpr int kLongRows = 64;    // LORA: rows from which a request has tiles of its own
+constexpr int kRankChunk = 16;   // LORA, mixed tiles: ranks of B in registers at once
 
 constexpr uint32_t kInfoProducer = 0x10000000u;
 constexpr uint32_t kInfoMma = 0x20000000u;
 constexpr uint32_t kInfoEpi = 0x30000000u;
 constexpr uint32_t kInfoTable = 0x70000000u;
 
+__host__ __device__ constexpr uint32_t slice_bytes(int rank) {
+    return uint32_t(rank < kRankChunk ? rank : kRankChunk) * 64u;
+}
+
 struct GrLayout {
-    uint32_t stage_bytes, table, stg, low, bars, total;
+    uint32_t stage_bytes, table, stg, low, ring, bars, total;
 };
+
+// LORA, mixed tiles: slices of B in flight per epilogue warp
+__host__ __device__ constexpr int slice_depth(bool pair) { return pair ? 2 : 4; }
+
+// int32 arrays of the group table behind the Plan, groups + 1 long
+__host__ __device__ constexpr int table_arrays(int kind) { return kind == GR_LORA ? 5 : kind == GR_SHRINK ? 3 : 2; }
 
 __host__ __device__ inline GrLayout gr_layout(int kind, bool pair, int stages, int bn, int groups, int rank) {
     GrLayout L;
     // a CTA of a pair stages its own 128 features and half of the tile's columns
     L.stage_bytes = uint32_t(kABytes + (pair ? bn / 2 : bn) * kBK * 2);
     uint32_t off = uint32_t(stages) * L.stage_bytes;
-    L.table = off;  // Plan, int off[groups + 1], int pre[groups + 1]
-    off += (16u + uint32_t(2 * (groups + 1)) * 4u + 15u) & ~15u;
-    L.stg = off;    // per epilogue warp: 16-bit [32 rows][32 features]; LORA: fp32 [32 rows][33]
-    off += kind == GR_LORA ? uint32_t(kEpiWarps) * 32u * 33u * 4u
+    L.table = off;
+    off += (32u + uint32_t(table_arrays(kind) * (groups + 1)) * 4u + 15u) & ~15u;
+    L.stg = off;    // per epilogue warp: 16-bit [32 rows][32 features]; LORA: fp32 [32 rows][32 features]
+    off += kind == GR_LORA ? uint32_t(kEpiWarps) * 4096u
                            : (kind == GR_FORWARD || kind == GR_DGRAD) ? uint32_t(kEpiWarps) * 2048u : 0u;
-    L.low = off;    // LORA: fp32 [32 rows][rank] per half
+    L.low = off;    // LORA: fp32 H [32 rows][rank] per half
     off += kind == GR_LORA ? 2u * 32u * uint32_t(rank) * 4u : 0u;
+    L.ring = off;   // LORA: 16-bit slices of B [ranks][32 features], slice_depth per epilogue warp
+    off += kind == GR_LORA ? uint32_t(kEpiWarps * slice_depth(pair)) * slice_bytes(rank) : 0u;
     L.bars = (off + 15u) & ~15u;
     L.total = L.bars + 256u;
     return L;
@@ -108,6 +121,8 @@ struct Tile {
     int kb0, kb1;  // the blocks of this piece
     int row0;   // WGRAD: first row of the group
     int rows;   // WGRAD: rows of the group
+    int extra;  // LORA: blocks of the low-rank product behind the tile's own (pieces: with the last)
+    int ad;     // LORA: the adapter of all the tile's rows, -1 none, -2 rows of several requests
     int first, last;  // workers that hold pieces of the tile
     int slot;   // which of its two workspace slots this worker's piece goes to
     __device__ bool whole() const { return first == last; }
@@ -119,49 +134,76 @@ struct Tile {
 // The pieces of a tile are added in the workspace in worker order (so equal calls give equal bits) by the
 // worker whose piece arrives last; nobody waits.
 struct Plan {
-    int split;    // stretches
-    int workers;  // that take part
+    int split;      // stretches
+    int workers;    // that take part
     int tiles;
-    int units;    // split: blocks of all tiles
+    int units;      // split: blocks of all tiles
+    int base, rem;  // split: a worker's stretch is base blocks, of the first rem workers one more
+    int groups;     // LORA: long requests and runs of short ones; else the groups
+};
+static_assert(sizeof(Plan) <= 32, "table layout");
+
+// The group table in shared memory.
+struct Table {
+    Plan *plan;
+    int *off;   // [groups + 1] first row of each group (LORA: request)
+    int *pre;   // [plan groups + 1] tiles of the groups before (WGRAD: blocks of one tile of each)
+    int *ad;    // SHRINK, LORA: adapter of each request, -1 for none
+    int *goff;  // LORA: [plan groups + 1] first row of each plan group
+    int *gad;   // LORA: its adapter, -1 none, -2 a run of short requests
+    __device__ Table(uint8_t *p, int kind, int groups) {
+        plan = reinterpret_cast<Plan *>(p);
+        off = reinterpret_cast<int *>(p + 32);
+        pre = off + groups + 1;
+        ad = pre + groups + 1;
+        goff = kind == GR_LORA ? ad + groups + 1 : off;
+        gad = goff + groups + 1;
+    }
 };
 
 template <int KIND, bool kPair>
 struct Walk {
-    const int *off, *pre;
+    const Table tab;
     const GroupedArgs &a;
     const Plan plan;
     int ft;      // feature tiles
     int per_group;  // WGRAD: tiles of a group
+    int shift;   // log2(a.bn)
+    int nkc;     // blocks of C
     int g;       // group of the current tile (tiles are visited in ascending order)
     int half;    // features of this CTA behind the tile's first: 0, or 128 in the second CTA of a pair
-    int worker, cur, begin, end;  // tile, or unit and this worker's stretch
+    int worker, cur, end;  // tile, or unit and the end of this worker's stretch
 
-    __device__ Walk(const int *off_, const int *pre_, const GroupedArgs &a_, const Plan &p, int worker_, int half_)
-        : off(off_), pre(pre_), a(a_), plan(p), g(0), half(half_), worker(worker_) {
+    __device__ Walk(const Table &t, const GroupedArgs &a_, int worker_, int half_)
+        : tab(t), a(a_), plan(*t.plan), g(0), half(half_), worker(worker_) {
         ft = feature_tiles<kPair>(a);
-        per_group = KIND == GR_WGRAD ? ft * ((a.N + a.bn - 1) / a.bn) : 0;
+        shift = 31 - __clz(a.bn);
+        nkc = (a.C + kBK - 1) / kBK;
+        per_group = KIND == GR_WGRAD ? ft * ((a.N + a.bn - 1) >> shift) : 0;
         cur = worker;
-        begin = 0;
         end = plan.tiles;
         if (!kPair && plan.split) {
-            begin = cur = unit_of(worker);
+            cur = unit_of(worker);
             end = worker < plan.workers ? unit_of(worker + 1) : cur;
         }
     }
     static constexpr int kTileF = kPair ? 2 * kFB : kFB;
     // columns are multiplied in 16s; each half of a pair's in 16s (WGRAD: whole 64-column blocks)
     static constexpr int kGran = kPair ? (KIND == GR_WGRAD ? 128 : 32) : 16;
-    __device__ int unit_of(int w) const { return int((long long)plan.units * w / plan.workers); }
-    __device__ int worker_of(int u) const { return int(((long long)(u + 1) * plan.workers - 1) / plan.units); }
+    __device__ int unit_of(int w) const { return w * plan.base + min(w, plan.rem); }
+    __device__ int worker_of(int u) const {
+        const int wide = plan.rem * (plan.base + 1);
+        return u < wide ? u / (plan.base + 1) : plan.rem + (u - wide) / plan.base;
+    }
 
     __device__ bool next(Tile &r) {
         if (cur >= end) return false;
-        int local, kb = 0, u0 = 0;
+        int local, kb = 0;
         if constexpr (KIND == GR_WGRAD) {
-            // pre: blocks of the groups before, of one tile (an empty group counts one, which holds no rows)
+            // (an empty group counts one block a tile, which holds no rows)
             if (!kPair && plan.split) {
-                while (cur >= per_group * pre[g + 1]) ++g;
-                const int nk = pre[g + 1] - pre[g], at = cur - per_group * pre[g];
+                while (cur >= per_group * tab.pre[g + 1]) ++g;
+                const int nk = tab.pre[g + 1] - tab.pre[g], at = cur - per_group * tab.pre[g];
                 local = at / nk;
                 kb = at % nk;
             } else {
@@ -170,23 +212,22 @@ struct Walk {
             }
             r.id = g * per_group + local;
         } else {
-            // pre: tiles of the groups before
-            const int nk = (a.C + kBK - 1) / kBK;
             r.id = cur;
             if (!kPair && plan.split) {
-                r.id = cur / nk;
-                kb = cur % nk;
+                r.id = cur / nkc;
+                kb = cur % nkc;
             }
-            while (r.id >= pre[g + 1]) ++g;
-            local = r.id - pre[g];
+            while (r.id >= tab.pre[g + 1]) ++g;
+            local = r.id - tab.pre[g];
         }
         r.g = g;
-        r.w = KIND == GR_SHRINK ? a.windex[g] : (KIND == GR_LORA ? 0 : g);
-        const int lo = off[KIND == GR_LORA ? 0 : g];
-        const int rows = off[KIND == GR_LORA ? a.groups : g + 1] - lo;
+        r.w = KIND == GR_SHRINK ? tab.ad[g] : (KIND == GR_LORA ? 0 : g);
+        const int lo = tab.goff[g];
+        const int rows = tab.goff[g + 1] - lo;
+        r.ad = KIND == GR_LORA ? tab.gad[g] : -1;
         int blocks;  // of the tile, one at least
         if constexpr (KIND == GR_WGRAD) {
-            const int nt = (a.N + a.bn - 1) / a.bn;
+            const int nt = (a.N + a.bn - 1) >> shift;
             r.f0 = (local / nt) * kTileF + half;
             r.col0 = (local % nt) * a.bn;
             r.n = min(a.bn, a.N - r.col0);
@@ -195,17 +236,24 @@ struct Walk {
             r.nk = (rows + kBK - 1) / kBK;
             blocks = max(r.nk, 1);
         } else {
-            const int rt = (rows + a.bn - 1) / a.bn;              // row tiles of the group,
-            const int per = ((rows + rt - 1) / rt + kGran - 1) & ~(kGran - 1);  // cut evenly
-            const int chunk = local / (kRasterRows * ft);
-            const int wide = min(kRasterRows, rt - chunk * kRasterRows);
-            const int in = local - chunk * kRasterRows * ft;
-            const int rtile = chunk * kRasterRows + in % wide;
-            r.f0 = (in / wide) * kTileF + half;
-            r.col0 = lo + rtile * per;
-            r.n = min(per, rows - rtile * per);
+            const int rt = (rows + a.bn - 1) >> shift;  // row tiles of the group, cut evenly
+            if (rt == 1) {
+                r.f0 = local * kTileF + half;
+                r.col0 = lo;
+                r.n = rows;
+            } else {
+                const int per = ((rows + rt - 1) / rt + kGran - 1) & ~(kGran - 1);
+                const int chunk = local / (kRasterRows * ft);
+                const int wide = min(kRasterRows, rt - chunk * kRasterRows);
+                const int in = local - chunk * kRasterRows * ft;
+                const int ftile = in / wide;
+                const int rtile = chunk * kRasterRows + in - ftile * wide;
+                r.f0 = ftile * kTileF + half;
+                r.col0 = lo + rtile * per;
+                r.n = min(per, rows - rtile * per);
+            }
             r.row0 = r.rows = 0;
-            r.nk = blocks = (a.C + kBK - 1) / kBK;
+            r.nk = blocks = nkc;
         }
         r.nm = (r.n + kGran - 1) & ~(kGran - 1);
         r.kb0 = kb;
@@ -213,7 +261,7 @@ struct Walk {
         r.first = r.last = worker;
         r.slot = 0;
         if (!kPair && plan.split) {
-            u0 = cur - kb;  // the tile's first unit
+            const int u0 = cur - kb;  // the tile's first unit
             const int take = min(blocks - kb, end - cur);
             r.kb1 = min(kb + take, r.nk);
             if (take < blocks) {
@@ -225,6 +273,7 @@ struct Walk {
         } else {
             cur += plan.workers;
         }
+        r.extra = KIND == GR_LORA && r.ad >= 0 && r.kb1 == r.nk ? 2 * ((a.rank + kBK - 1) / kBK) : 0;
         return true;
     }
     // a worker's first piece goes to its slot 0 unless its stretch began in an earlier tile
@@ -255,6 +304,12 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
 }
 __device__ __forceinline__ float from16(uint16_t v, bool fp16) {
     return fp16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(uint32_t(v) << 16);
+}
+
+// 16-bit part of H: rounded; fp16 saturates (an infinity stays one), the rest goes to the other part
+__device__ __forceinline__ uint16_t low_part(float h, bool fp16) {
+    if (fp16 && fabsf(h) > 65504.f && isfinite(h)) h = copysignf(65504.f, h);
+    return to16(h, fp16);
 }
 
 // A warp's fragment, 32 rows x 32 features, in its 2 KB of shared memory (64 bytes a row): lane l holds the 16-byte
@@ -291,96 +346,138 @@ __device__ __forceinline__ void load_fragment(uint4 (&z)[4], const GroupedArgs &
                    ? *reinterpret_cast<const uint4 *>(p + size_t(8 * i) * a.F) : make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Group table: off[i] = offsets[i] clamped to [0, T] and to not decrease, pre[i] = tiles of the groups
-// before i (WGRAD: blocks of one tile of each), and the plan.  One warp, after the raw offsets are in off[].
+// The group table from the raw offsets (in off[]) and adapters (in ad[]), by one warp: offsets clamped to [0, T] and
+// to not decrease, adapters outside -1 .. L-1 made -1, the running numbers of tiles, the plan.  It stands between the
+// offsets' arrival and the first copy, so it is short: one pass of 32 groups at a time, no 64-bit division.
 template <int KIND, bool kPair>
-__device__ void scan_table(int *off, int *pre, Plan *plan, const GroupedArgs &a, int workers, uint32_t *err) {
+__device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, uint32_t *err) {
     const int lane = threadIdx.x & 31;
-    const int n = a.groups + 1;
     const int ft = feature_tiles<kPair>(a);
-    bool bad = false;
-    int run_max = 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
+    const int shift = 31 - __clz(a.bn);
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int raw0 = tab.off[0];
+    int lo_all = min(max(raw0, 0), a.T);  // end of the groups before, clamped
+    bool bad = raw0 != lo_all;
+    const int first = lo_all;
+    int carry = 0, longest = 0, ngroups = 0;
+    bool long_before = true;
+    __syncwarp();
+    if (lane == 0) tab.off[0] = first;
+    for (int i0 = 0; i0 < a.groups; i0 += 32) {
         const int i = i0 + lane;
-        const int raw = i < n ? off[i] : 0;
-        int v = min(max(raw, 0), a.T);
-        const int own = v;
+        const int raw = i < a.groups ? tab.off[i + 1] : 0;
+        int v = min(max(raw, lo_all), a.T);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, v, d);
+            const int o = __shfl_up_sync(kAll, v, d);
             if (lane >= d) v = max(v, o);
         }
-        v = max(v, run_max);
-        if (i < n) {
-            bad |= v != own || own != raw;
-            off[i] = v;
-        }
-        run_max = __shfl_sync(0xffffffffu, v, 31);
-    }
-    __syncwarp();
-    const int groups = KIND == GR_LORA ? 1 : a.groups;
-    int carry = 0, longest = 0;
-    for (int i0 = 0; i0 < groups; i0 += 32) {
-        const int i = i0 + lane;
-        int tiles = 0;
-        if (i < groups) {
-            const int rows = off[KIND == GR_LORA ? a.groups : i + 1] - off[i];
+        int lo = __shfl_up_sync(kAll, v, 1);
+        if (lane == 0) lo = lo_all;
+        lo_all = __shfl_sync(kAll, v, 31);
+        const int rows = v - lo;
+        int count = 0;
+        if (i < a.groups) {
+            bad |= v != raw;
+            tab.off[i + 1] = v;
             if constexpr (KIND == GR_WGRAD) {
-                tiles = max((rows + kBK - 1) / kBK, 1);
-                longest = max(longest, tiles);
+                count = max((rows + kBK - 1) / kBK, 1);
+                longest = max(longest, count);
             } else {
-                tiles = ft * ((rows + a.bn - 1) / a.bn);
-                if constexpr (KIND == GR_SHRINK) {
-                    const int w = a.windex[i];
-                    bad |= w < -1 || w >= a.nweights;
-                    if (w < 0 || w >= a.nweights) tiles = 0;
+                count = ft * ((rows + a.bn - 1) >> shift);
+            }
+            if constexpr (KIND == GR_SHRINK || KIND == GR_LORA) {
+                const int w = tab.ad[i];
+                if (w < -1 || w >= a.nweights) {
+                    bad = true;
+                    tab.ad[i] = -1;
                 }
+                if (KIND == GR_SHRINK && (w < 0 || w >= a.nweights)) count = 0;
             }
         }
-        int s = tiles;
+        if constexpr (KIND == GR_LORA) {
+            // a long request is a group of its own, a run of short ones another
+            const bool is_long = i < a.groups && rows >= kLongRows;
+            bool before = __shfl_up_sync(kAll, is_long, 1);
+            if (lane == 0) before = long_before;
+            long_before = __shfl_sync(kAll, is_long, 31);
+            const bool start = i < a.groups && (is_long || before);
+            const uint32_t m = __ballot_sync(kAll, start);
+            if (start) {
+                const int gi = ngroups + __popc(m & ((1u << lane) - 1u));
+                tab.goff[gi] = lo;
+                tab.gad[gi] = is_long ? tab.ad[i] : -2;
+            }
+            ngroups += __popc(m);
+        } else {
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, s, d);
-            if (lane >= d) s += o;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(kAll, count, d);
+                if (lane >= d) count += o;
+            }
+            if (i < a.groups) tab.pre[i + 1] = carry + count;
+            carry += __shfl_sync(kAll, count, 31);
         }
-        if (i < groups) pre[i + 1] = carry + s;
-        carry += __shfl_sync(0xffffffffu, s, 31);
     }
-    if constexpr (KIND == GR_WGRAD) longest = __reduce_max_sync(0xffffffffu, longest);
+    if constexpr (KIND == GR_LORA) {
+        if (lane == 0) tab.goff[ngroups] = lo_all;
+        __syncwarp();
+        for (int i0 = 0; i0 < ngroups; i0 += 32) {
+            const int i = i0 + lane;
+            int count = i < ngroups ? ft * ((tab.goff[i + 1] - tab.goff[i] + a.bn - 1) >> shift) : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(kAll, count, d);
+                if (lane >= d) count += o;
+            }
+            if (i < ngroups) tab.pre[i + 1] = carry + count;
+            carry += __shfl_sync(kAll, count, 31);
+        }
+    } else {
+        ngroups = a.groups;
+    }
+    if constexpr (KIND == GR_WGRAD) longest = __reduce_max_sync(kAll, longest);
     if (lane == 0) {
-        pre[0] = 0;
+        tab.pre[0] = 0;
         // Rounds of whole tiles against equal stretches, in blocks (of about 0.36 us each: 16 KB of weights at an
-        // SM's share of HBM, or MMAs of 256 columns).  Adding pieces costs about 6 blocks, and another for each 32
+        // SM's share of HBM, or MMAs of 256 columns).  Adding pieces costs about 8 blocks, and another for each 32
         // columns written and read back.
-        const long long each = KIND == GR_WGRAD ? 0 : (a.C + kBK - 1) / kBK;
-        const long long tiles = KIND == GR_WGRAD ? (long long)groups * ft * ((a.N + a.bn - 1) / a.bn) : carry;
-        const long long units = KIND == GR_WGRAD ? (long long)ft * ((a.N + a.bn - 1) / a.bn) * carry : tiles * each;
+        constexpr int kMost = 1 << 20;  // blocks of a contraction, tiles x blocks then fit 30 bits
+        const int per_tile = KIND == GR_WGRAD ? ft * ((a.N + a.bn - 1) >> shift) : 1;
+        const int nkc = (a.C + kBK - 1) / kBK;
         Plan p;
         p.split = 0;
         p.workers = workers;
-        p.tiles = int(tiles);
-        p.units = 0;
-        if (!kPair && a.partials != nullptr && tiles > 0 && tiles <= kGroupedSplitTiles && units < (1ll << 30)) {
-            const long long share = (units + workers - 1) / workers;
-            const long long stretch = share > kMinStretch ? share : kMinStretch;
-            const long long rounds = (tiles + workers - 1) / workers;
-            long long whole = rounds * units / tiles;  // WGRAD: of mean tiles, or the longest one
-            if (longest > whole) whole = longest;
-            if (whole > stretch + 6 + a.bn / 32) {
+        p.tiles = KIND == GR_WGRAD ? ngroups * per_tile : carry;
+        p.units = p.base = p.rem = 0;
+        p.groups = ngroups;
+        const bool few = KIND == GR_WGRAD ? ngroups <= kGroupedSplitTiles && per_tile <= kGroupedSplitTiles &&
+                                                p.tiles <= kGroupedSplitTiles && carry <= kMost
+                                          : carry <= kGroupedSplitTiles && nkc <= kMost;
+        if (!kPair && a.partials != nullptr && few && p.tiles > 0) {
+            const int units = KIND == GR_WGRAD ? per_tile * carry : p.tiles * nkc;
+            const int share = (units + workers - 1) / workers;
+            const int stretch = max(share, kMinStretch);
+            const int rounds = (p.tiles + workers - 1) / workers;
+            // WGRAD: of mean tiles, or the longest one
+            const int whole = KIND == GR_WGRAD ? max(rounds * ((units + p.tiles - 1) / p.tiles), longest) : rounds * nkc;
+            if (whole > stretch + 8 + a.bn / 32) {
                 p.split = 1;
-                p.workers = int((units + stretch - 1) / stretch);
-                p.units = int(units);
+                p.workers = stretch == share ? workers : max(units / stretch, 1);
+                p.units = units;
+                p.base = units / p.workers;
+                p.rem = units - p.base * p.workers;
             }
         }
-        *plan = p;
+        *tab.plan = p;
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0)
+    if (__any_sync(kAll, bad) && lane == 0 && blockIdx.x == 0)
         ptx::record_error(err, 8u /*CF_ERR_DEVICE_BOUNDS*/, kInfoTable);
 }
 
-// A block of the contraction stages 16 KB of the feature operand (features behind the last are zeros, or stale where
-// a copy would hold none: those lanes are never stored) and, of the columns, what the CTA multiplies, rounded up to
-// whole boxes.  Rows of a box behind the tile's are the neighbour's, in columns that are not multiplied or not stored.
+// A block of the contraction stages 16 KB of the feature operand (8 KB where there are no more than 64 features;
+// what is behind the last feature is zero or stale, in lanes that are never stored) and, of the columns, what the CTA
+// multiplies, rounded up to whole boxes.  Rows of a box behind the tile's are the neighbour's, in columns that are not multiplied or not stored.
 template <int KIND, bool kPair>
 __device__ __forceinline__ int b_blocks(const GroupedArgs &a, const Tile &w) {  // WGRAD: 64-column blocks to fill
     const int cols = kPair ? w.nm / 2 : w.nm;
@@ -404,24 +501,166 @@ __device__ __forceinline__ void zero_tail(uint8_t *st, int left, int steps, int 
     __syncwarp();
 }
 
-// the tile's pieces at columns c .. c + 31 of one lane, added in worker order
+// the tile's pieces at columns c .. c + 31 of one lane, added in worker order; several pieces' loads in flight
 template <int KIND, bool kPair>
 __device__ __forceinline__ void sum_pieces(uint32_t (&v)[32], const GroupedArgs &a, const Walk<KIND, kPair> &walk,
                                            const Tile &w, int c, int l) {
-    float s[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) s[j] = 0.f;
     const int cols = min(32, w.n - c);
-    const int u0 = KIND == GR_WGRAD ? walk.per_group * walk.pre[w.g] + (w.id - w.g * walk.per_group) * max(w.nk, 1)
-                                    : w.id * w.nk;
-    for (int k = w.first; k <= w.last; ++k) {
-        const float *p = a.partials + size_t(2 * k + walk.slot_of(k, u0)) * size_t(kFB * a.bn) + size_t(c) * kFB + l;
+    const int u0 = KIND == GR_WGRAD
+                       ? walk.per_group * walk.tab.pre[w.g] + (w.id - w.g * walk.per_group) * max(w.nk, 1)
+                       : w.id * w.nk;
+    const size_t piece = size_t(kFB) * a.bn;
+    // the first piece may be the second slot of its worker; every later one starts its worker's stretch
+    const float *p0 = a.partials + size_t(2 * w.first + walk.slot_of(w.first, u0)) * piece + size_t(c) * kFB + l;
+    const float *p = a.partials + size_t(2 * (w.first + 1)) * piece + size_t(c) * kFB + l;
+    const int more = w.last - w.first;
+    constexpr int kFly = KIND == GR_LORA || KIND == GR_SHRINK ? 2 : 4;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < cols) s[j] += __ldcg(p + j * kFB);
+    for (int jb = 0; jb < 32; jb += 8) {
+        if (jb < cols) {
+            float s[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = jb + j < cols ? __ldcg(p0 + (jb + j) * kFB) : 0.f;
+            for (int k = 0; k < more; k += kFly) {
+                float x[kFly][8];
+#pragma unroll
+                for (int i = 0; i < kFly; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        x[i][j] = k + i < more && jb + j < cols ? __ldcg(p + (k + i) * (2 * piece) + (jb + j) * kFB) : 0.f;
+#pragma unroll
+                for (int i = 0; i < kFly; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[j] += x[i][j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[jb + j] = __float_as_uint(s[j]);
+        }
     }
+}
+
+// LORA, a tile with rows of several requests: the adapters' second product on the CUDA cores, in fp32.  Each row takes
+// its own adapter's B and nothing of another's, so a NaN in an adapter stays with its requests.  stg holds the warp's 32 rows
+// x 32 features; rows [j_lo, j_hi) of them, at row0 of the batch, are added to.  Slices of B ([16 ranks][32 features])
+// arrive by cp.async a few items ahead: an item is a run of one request's rows and one slice.
+struct Runs {
+    const Table &tab;
+    int groups, rank, row0, j_lo, j_hi;
+    int seg, j0, j1, r0;
+    __device__ bool next() {  // the next item
+        r0 += kRankChunk;
+        if (r0 < rank) return true;
+        r0 = 0;
+        while (++seg < groups) {
+            j0 = max(tab.off[seg] - row0, j_lo);
+            if (j0 >= j_hi) break;
+            j1 = min(tab.off[seg + 1] - row0, j_hi);
+            if (j1 > j0 && tab.ad[seg] >= 0) return true;
+        }
+        seg = groups;
+        return false;
+    }
+};
+
+// (Not inlined: its registers would push the kernel's above what two CTAs an SM may have.)
+template <bool kPair>
+__device__ __noinline__ void add_low_rank(const GroupedArgs &a, const Table tab, float *stg, float *low, uint32_t ring,
+                                          int half, int q, int f0, int row0, int j_lo, int j_hi) {
+    const int lane = threadIdx.x & 31;
+    constexpr int kDepth = slice_depth(kPair);
+    const int rank = a.rank;
+    const bool fp16 = a.fp16 != 0;
+    const uint32_t slot_bytes = slice_bytes(rank);
+    Runs issue{tab, a.groups, rank, row0, j_lo, j_hi, 0, 0, 0, rank};
+    {  // the request of the first row: the last one that starts at or before it
+        int lo = 0, hi = a.groups - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (tab.off[mid] <= row0 + j_lo) lo = mid;
+            else hi = mid - 1;
+        }
+        issue.seg = lo - 1;
+    }
+    Runs work = issue;
+    const int piece = (lane & 3) * 8;
+    const bool have = f0 + q * 32 + piece < a.F;
+    auto fetch = [&](int slot) {
+        if (issue.seg < a.groups && issue.next()) {
+            const uint16_t *src = static_cast<const uint16_t *>(a.lora_b) +
+                                  (size_t(tab.ad[issue.seg]) * rank + issue.r0) * a.F + (have ? f0 + q * 32 + piece : 0);
+            const int ranks = min(kRankChunk, rank - issue.r0);
+            for (int r = lane >> 2; r < ranks; r += 8)
+                ptx::cp_async16(ring + uint32_t(slot) * slot_bytes + uint32_t(r * 64 + (lane & 3) * 16),
+                                src + size_t(r) * a.F, have);
+        }
+        ptx::cp_async_commit();
+    };
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(s[j]);
+    for (int i = 0; i < kDepth - 1; ++i) fetch(i);
+    ptx::named_bar_sync(1 + half, kHalfThreads);  // the half is done with the last fragment's H
+    {
+        const uint16_t *src = static_cast<const uint16_t *>(a.low) + size_t(row0) * (2 * rank);
+        const int pieces = rank / 8;
+        for (int i = q * 32 + lane; i < (j_hi - j_lo) * pieces; i += kHalfThreads) {
+            const int j = j_lo + i / pieces, r = (i % pieces) * 8;
+            const uint4 h = *reinterpret_cast<const uint4 *>(src + size_t(j) * (2 * rank) + r);
+            const uint4 l = *reinterpret_cast<const uint4 *>(src + size_t(j) * (2 * rank) + rank + r);
+            float *d = low + j * rank + r;
+            const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                d[2 * k] = from16(uint16_t(hw[k]), fp16) + from16(uint16_t(lw[k]), fp16);
+                d[2 * k + 1] = from16(uint16_t(hw[k] >> 16), fp16) + from16(uint16_t(lw[k] >> 16), fp16);
+            }
+        }
+    }
+    ptx::named_bar_sync(1 + half, kHalfThreads);
+    int slot = 0;
+    while (work.next()) {
+        fetch(slot == 0 ? kDepth - 1 : slot - 1);
+        ptx::cp_async_wait<kDepth - 1>();
+        __syncwarp();
+        const int ranks = min(kRankChunk, rank - work.r0);
+        float b[kRankChunk];
+#pragma unroll
+        for (int r = 0; r < kRankChunk; ++r)
+            if (r < ranks) {
+                uint16_t x;
+                ptx::ld_shared_u16(x, ring + uint32_t(slot) * slot_bytes + uint32_t(r * 64 + lane * 2));
+                b[r] = from16(x, fp16);
+            }
+        __syncwarp();  // the slot is free for the fetch of the next turn
+        for (int j = work.j0; j < work.j1; ++j) {
+            const float4 *h = reinterpret_cast<const float4 *>(low + j * rank + work.r0);
+            float s0 = stg[j * 32 + lane], s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+            for (int r = 0; r < kRankChunk; r += 8) {
+                if (r < ranks) {  // a multiple of 8
+                    const float4 h0 = h[r / 4], h1 = h[r / 4 + 1];
+                    ptx::fma2(s0, s1, h0.x, h0.y, b[r], b[r + 1], s0, s1);
+                    ptx::fma2(s2, s3, h0.z, h0.w, b[r + 2], b[r + 3], s2, s3);
+                    ptx::fma2(s0, s1, h1.x, h1.y, b[r + 4], b[r + 5], s0, s1);
+                    ptx::fma2(s2, s3, h1.z, h1.w, b[r + 6], b[r + 7], s2, s3);
+                }
+            }
+            stg[j * 32 + lane] = (s0 + s1) + (s2 + s3);
+        }
+        slot = slot + 1 == kDepth ? 0 : slot + 1;
+    }
+    ptx::cp_async_wait<0>();
+    __syncwarp();
+}
+// the same on a fragment in registers (32 rows of this lane's feature)
+template <bool kPair>
+__device__ __forceinline__ void add_low_rank(uint32_t (&v)[32], const GroupedArgs &a, const Table &tab, float *stg,
+                                             float *low, uint32_t ring, int half, int q, int lane, int f0, int row0,
+                                             int j_lo, int j_hi) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) stg[j * 32 + lane] = __uint_as_float(v[j]);
+    add_low_rank<kPair>(a, tab, stg, low, ring, half, q, f0, row0, j_lo, j_hi);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(stg[j * 32 + lane]);
+    __syncwarp();
 }
 
 template <bool kPair>
@@ -443,7 +682,7 @@ __device__ __forceinline__ void stage_loads(const GroupedArgs &a, const Tile &w,
     if constexpr (KIND == GR_WGRAD) {
         const int y = w.row0 + k0;
         if (a.a_split) {
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < a.a_blocks; ++i) {
                 if constexpr (kShared) ptx::tma_load_2d_pair(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, y);
                 else ptx::tma_load_2d(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, y);
             }
@@ -465,7 +704,7 @@ __device__ __forceinline__ void stage_loads(const GroupedArgs &a, const Tile &w,
             if constexpr (kShared) ptx::tma_load_3d_pair(sa, &a.tmap_a, bar, k0, w.f0, w.w);
             else ptx::tma_load_3d(sa, &a.tmap_a, bar, k0, w.f0, w.w);
         } else if (a.a_split) {
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < a.a_blocks; ++i) {
                 if constexpr (kShared) ptx::tma_load_3d_pair(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, k0, w.w);
                 else ptx::tma_load_3d(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, k0, w.w);
             }
@@ -478,8 +717,9 @@ __device__ __forceinline__ void stage_loads(const GroupedArgs &a, const Tile &w,
     }
 }
 
+// (a decode batch's SHRINK and LORA share the SMs, two CTAs each)
 template <int KIND, bool kPair>
-__global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_constant__ GroupedArgs a) {
+__global__ void __launch_bounds__(kThreads, KIND == GR_SHRINK || (KIND == GR_LORA && !kPair) ? 2 : 1) grouped_kernel(const __grid_constant__ GroupedArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = ptx::smem_u32(smem_raw);
     if ((base & 1023u) != 0u) {  // the swizzled operand tiles need it; see the fused GEMM
@@ -492,9 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     const int stages = a.stages;
     const GrLayout L = gr_layout(KIND, kPair, stages, a.bn, a.groups, a.rank);
     const GrBars B = gr_bars(base + L.bars, stages);
-    Plan *const plan = reinterpret_cast<Plan *>(smem_raw + L.table);
-    int *const off = reinterpret_cast<int *>(smem_raw + L.table + sizeof(Plan));
-    int *const pre = off + a.groups + 1;
+    const Table tab(smem_raw + L.table, KIND, a.groups);
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem_raw + (B.misc - base));
     volatile uint32_t *abort = misc + 1;
     const uint64_t tmo = a.timeout_ns;
@@ -537,17 +775,27 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
     // The next grid may start only once this CTA holds its tensor memory: a dependent CTA that took it first
     // would wait for this grid while this grid waited for the columns.
     __syncthreads();
-    ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    for (int i = threadIdx.x; i <= a.groups; i += kThreads) off[i] = a.offsets[i];
+    if constexpr (KIND == GR_SHRINK) {
+        // LORA, launched next, reads what came before this grid without waiting: it must not start earlier
+        ptx::griddep_wait();
+        ptx::griddep_launch_dependents();
+    } else {
+        ptx::griddep_launch_dependents();
+        if (KIND != GR_LORA || !a.after_shrink) ptx::griddep_wait();
+    }
+    for (int i = threadIdx.x; i <= a.groups; i += kThreads) {
+        tab.off[i] = a.offsets[i];
+        if constexpr (KIND == GR_SHRINK || KIND == GR_LORA)
+            if (i < a.groups) tab.ad[i] = a.windex[i];
+    }
     __syncthreads();
-    if (warp == 0) scan_table<KIND, kPair>(off, pre, plan, a, workers, a.err);
+    if (warp == 0) scan_table<KIND, kPair>(tab, a, workers, a.err);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     if constexpr (kPair) ptx::cluster_sync();  // the peer's barriers are initialised before anything signals them
     const uint32_t tmem_base = misc[0];
-    Walk<KIND, kPair> walk(off, pre, a, *plan, worker, int(crank) * kFB);
+    Walk<KIND, kPair> walk(tab, a, worker, int(crank) * kFB);
     Tile w;
 
     if (warp == 0) {
@@ -560,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                 const int cols = kPair ? w.nm / 2 : w.nm;  // columns this CTA stages
                 const int col0 = w.col0 + int(crank) * cols;
                 const int bblk = b_blocks<KIND, kPair>(a, w);
-                const uint32_t own = uint32_t(kABytes) + b_bytes<KIND, kPair>(a, w);
+                const uint32_t own = uint32_t(a.a_blocks) * 8192u + b_bytes<KIND, kPair>(a, w);
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     if (!ptx::mbar_try_wait(B.empty0 + 8 * s, ph ^ 1u)) {
                         ok = ptx::mbar_wait_bounded(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
@@ -585,6 +833,36 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                     if (++s == uint32_t(stages)) {
                         s = 0;
                         ph ^= 1u;
+                    }
+                }
+                if constexpr (KIND == GR_LORA) {
+                    // the low-rank product of a tile with one adapter: blocks of 64 ranks, H's upper parts, then its
+                    // lower ones, against the same rows of B
+                    if (w.extra > 0) ptx::griddep_wait();  // H is the previous grid's
+                    for (int x = 0; x < w.extra && ok; ++x) {
+                        ok = ptx::mbar_wait_bounded(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
+                        if (!ok) break;
+                        const int r0 = (x >> 1) * kBK;
+                        const uint32_t sa = base + s * L.stage_bytes;
+                        const uint32_t bar = full_lead + 8 * s;
+                        if (leader) ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, kPair ? 2 * own : own);
+                        if (a.a_split) {
+                            for (int i = 0; i < a.a_blocks; ++i) {
+                                if constexpr (kPair) ptx::tma_load_3d_pair(sa + i * 8192, &a.tmap_lb, bar, w.f0 + 64 * i, r0, w.ad);
+                                else ptx::tma_load_3d(sa + i * 8192, &a.tmap_lb, bar, w.f0 + 64 * i, r0, w.ad);
+                            }
+                        } else {
+                            if constexpr (kPair) ptx::tma_load_4d_pair(sa, &a.tmap_lb, bar, 0, r0, w.f0 / 64, w.ad);
+                            else ptx::tma_load_4d(sa, &a.tmap_lb, bar, 0, r0, w.f0 / 64, w.ad);
+                        }
+                        const int xh = (x & 1) * a.rank + r0;
+                        if constexpr (kPair) ptx::tma_load_2d_pair(sa + kABytes, &a.tmap_h, bar, xh, col0);
+                        else ptx::tma_load_2d(sa + kABytes, &a.tmap_h, bar, xh, col0);
+                        ++it;
+                        if (++s == uint32_t(stages)) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
                     }
                 }
             }
@@ -687,6 +965,23 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                         ph ^= 1u;
                     }
                 }
+                if constexpr (KIND == GR_LORA) {
+                    for (int x = 0; x < w.extra && ok; ++x) {
+                        ok = ptx::mbar_wait_bounded(B.full0 + 8 * s, ph, tmo, abort, a.err, kInfoMma | 0x400u | s);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        const int ranks = a.rank - (x >> 1) * kBK;
+                        const int steps = ranks >= kBK ? kBK / 16 : (ranks + 15) / 16;
+                        const uint64_t so = uint64_t((s * L.stage_bytes) >> 4);
+                        for (int k = 0; k < steps; ++k)
+                            issue_mma<kPair>(d, ad0 + so + uint64_t(k * 128), bd0 + so + uint64_t(k * 2), idesc, 1u);
+                        issue_commit<kPair>(B.empty0 + 8 * s);
+                        if (++s == uint32_t(stages)) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
                 if (!ok) break;
                 if (lane == 0) issue_commit<kPair>(B.tmem_full0 + 8 * buf);
             }
@@ -705,6 +1000,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
         const int half = e >> 2;
         const int q = warp & 3;
         const bool fp16 = a.fp16 != 0;
+        float *const low_stg = reinterpret_cast<float *>(smem_raw + L.stg) + e * 1024;
+        float *const low = reinterpret_cast<float *>(smem_raw + L.low) + half * 32 * a.rank;
+        const uint32_t low_ring = base + L.ring + uint32_t(e * slice_depth(kPair)) * slice_bytes(a.rank);
         for (int tile = 0; walk.next(w); ++tile) {
             const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
             uint4 zv[4];  // DGRAD: the next fragment's pre-activations, on their way before the accumulator is ready
@@ -716,7 +1014,16 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             const int f = w.f0 + q * 32 + lane;
             const bool live = f < a.F && ok;
             bool held = true;  // the accumulator is still this tile's
+            // rows whose low-rank product falls to this worker (LORA, a tile of several requests): all of them, or its
+            // share of a divided tile's
+            int low_lo = 0, low_hi = KIND == GR_LORA && w.ad == -2 && a.nweights > 0 ? w.n : 0;
             if (!kPair && !w.whole()) {
+                if constexpr (KIND == GR_LORA) {
+                    const int parts = w.last - w.first + 1, mine = worker - w.first;
+                    low_lo = low_hi * mine / parts;
+                    low_hi = low_hi * (mine + 1) / parts;
+                    if (low_hi > low_lo) ptx::griddep_wait();
+                }
                 // a piece of the tile: to the workspace, [column][lane]; the last to arrive goes on with the sum
                 float *const mine = a.partials + size_t(2 * worker + w.slot) * size_t(kFB * a.bn) + q * 32 + lane;
                 for (int c = half * 32; c < w.n; c += 64) {
@@ -724,30 +1031,37 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                     ptx::tmem_ld32(tacc + uint32_t(c), v);
                     ptx::tmem_ld_wait();
                     const int cols = min(32, w.n - c);
+                    if constexpr (KIND == GR_LORA) {
+                        const int j_lo = max(low_lo - c, 0), j_hi = min(low_hi - c, 32);
+                        if (j_lo < j_hi)
+                            add_low_rank<kPair>(v, a, tab, low_stg, low, low_ring, half, q, lane, w.f0, w.col0 + c, j_lo,
+                                                j_hi);
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (j < cols) __stcg(mine + (c + j) * kFB, __uint_as_float(v[j]));
+                        if (j < cols && live) __stcg(mine + (c + j) * kFB, __uint_as_float(v[j]));
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(B.tmem_empty0 + 8 * buf);
                 held = false;
-                __threadfence();
+                // thread 64's release covers what the others wrote before the barrier, its acquire what they read after
                 ptx::named_bar_sync(3, kEpiWarps * 32);
+                volatile uint32_t *const verdict = misc + 2 + (tile & 1);  // read before the one after next is written
                 if (threadIdx.x == 64) {
                     const uint32_t before = ptx::atom_add_acq_rel_gpu(a.counters + w.id, 1u);
                     const bool last = before == uint32_t(w.last - w.first);
                     if (last) ptx::st_relaxed_gpu(a.counters + w.id, 0u);  // for the next launch
-                    misc[2] = last;
+                    *verdict = last;
                 }
                 ptx::named_bar_sync(3, kEpiWarps * 32);
-                const bool last = misc[2] != 0u;
-                ptx::named_bar_sync(3, kEpiWarps * 32);  // read before the next piece's verdict is written
-                if (!last) continue;
-                __threadfence();
+                if (*verdict == 0u) continue;
+                low_hi = 0;
                 if constexpr (KIND == GR_DGRAD)
                     if (a.preact && half * 32 < w.n) load_fragment(zv, a, w, half * 32, q, lane, true);
             }
+            if constexpr (KIND == GR_LORA)
+                if (low_hi > low_lo) ptx::griddep_wait();
             for (int c = half * 32; c < w.n; c += 64) {
                 uint32_t v[32];
                 if (kPair || w.whole()) {
@@ -757,10 +1071,19 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                     sum_pieces(v, a, walk, w, c, q * 32 + lane);
                 }
                 const int cols = min(32, w.n - c);
-                if constexpr (KIND == GR_FORWARD || KIND == GR_DGRAD) {
+                if constexpr (KIND == GR_LORA) {
+                    if (low_hi > low_lo)
+                        add_low_rank<kPair>(v, a, tab, low_stg, low, low_ring, half, q, lane, w.f0, w.col0 + c, 0, cols);
+                    if (a.bias) {
+                        const float bv = f < a.F ? __ldg(a.bias + f) : 0.f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + bv);
+                    }
+                }
+                if constexpr (KIND == GR_FORWARD || KIND == GR_DGRAD || KIND == GR_LORA) {
                     // The fragment is turned in shared memory (a lane's feature column in, whole rows out), so that
                     // global memory is read and written in 16-byte pieces, 64 bytes a row.
-                    uint8_t *const stg = smem_raw + L.stg + e * 2048;
+                    uint8_t *const stg = smem_raw + L.stg + e * (KIND == GR_LORA ? 4096 : 2048);
                     const Fragment fr{stg, lane, cols, (w.f0 + q * 32 + (lane & 3) * 8) < a.F && ok,
                                       size_t(w.col0 + c + (lane >> 2)) * a.F + w.f0 + q * 32 + (lane & 3) * 8,
                                       size_t(8) * a.F};
@@ -791,11 +1114,20 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                     for (int j = 0; j < 32; ++j) mine[j * 32] = to16(__uint_as_float(v[j]), fp16);
                     fr.out(a.out);
                 } else if constexpr (KIND == GR_SHRINK) {
-                    const float sc = a.scale ? a.scale[w.w] : 1.f;
-                    float *y = static_cast<float *>(a.out) + size_t(w.col0 + c) * a.F + f;
+                    // H in two 16-bit parts, upper and rest: 16 bits and more of mantissa (fp16: 22, within twice its
+                    // range, behind which H saturates), so that the second product can run on the tensor cores
+                    const float sc = a.scale ? __ldg(a.scale + w.w) : 1.f;
+                    uint16_t *y = static_cast<uint16_t *>(a.out) + size_t(w.col0 + c) * (2 * a.F) + f;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (live && j < cols) y[size_t(j) * a.F] = sc * __uint_as_float(v[j]);
+                    for (int j = 0; j < 32; ++j) {
+                        if (live && j < cols) {
+                            const float h = sc * __uint_as_float(v[j]);
+                            const uint16_t up = low_part(h, fp16);
+                            const float rest = h - from16(up, fp16);
+                            y[size_t(j) * (2 * a.F)] = up;
+                            y[size_t(j) * (2 * a.F) + a.F] = isfinite(h) ? low_part(rest, fp16) : uint16_t(0);
+                        }
+                    }
                 } else if constexpr (KIND == GR_WGRAD) {
                     if (live) {
                         uint16_t *y = static_cast<uint16_t *>(a.out) + (size_t(w.g) * a.F + f) * a.N + w.col0 + c;
@@ -812,65 +1144,6 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
                             }
                         }
                     }
-                } else {  // GR_LORA
-                    // The adapters' second product on the CUDA cores, in fp32, one row after another: rows of
-                    // different requests never share an instruction, so a NaN in one adapter stays with its
-                    // own requests.
-                    float *const stg = reinterpret_cast<float *>(smem_raw + L.stg) + e * (32 * 33);
-                    float *const low = reinterpret_cast<float *>(smem_raw + L.low) + half * 32 * a.rank;
-                    const int rank = a.rank;
-                    const int row0 = w.col0 + c;
-                    ptx::named_bar_sync(1 + half, kHalfThreads);  // the half is done with the last fragment's rows
-                    {
-                        const int tid = (e & 3) * 32 + lane;
-                        const float4 *src = reinterpret_cast<const float4 *>(a.low + size_t(row0) * rank);
-                        for (int i = tid; i < cols * rank / 4; i += kHalfThreads)
-                            reinterpret_cast<float4 *>(low)[i] = src[i];
-                    }
-                    const float bv = (a.bias && live) ? a.bias[f] : 0.f;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) stg[j * 33 + lane] = __uint_as_float(v[j]) + bv;
-                    ptx::named_bar_sync(1 + half, kHalfThreads);
-                    // the request of the first row: the last one that starts at or before it
-                    int lo = 0, hi = a.groups - 1;
-                    while (lo < hi) {
-                        const int mid = (lo + hi + 1) >> 1;
-                        if (off[mid] <= row0) lo = mid;
-                        else hi = mid - 1;
-                    }
-                    int j0 = 0;
-                    for (int sgm = lo; sgm < a.groups && j0 < cols; ++sgm) {
-                        const int j1 = min(cols, off[sgm + 1] - row0);
-                        const int ad = a.windex[sgm];
-                        if (j1 > j0 && ad >= 0 && ad < a.nweights && live) {
-                            const uint16_t *bp = static_cast<const uint16_t *>(a.lora_b) + (size_t(ad) * rank) * a.F + f;
-                            for (int r0 = 0; r0 < rank; r0 += kRankChunk) {
-                                float b[kRankChunk];
-#pragma unroll
-                                for (int r = 0; r < kRankChunk; ++r)
-                                    b[r] = r0 + r < rank ? from16(__ldg(bp + size_t(r0 + r) * a.F), fp16) : 0.f;
-                                for (int j = j0; j < j1; ++j) {
-                                    const float4 *h = reinterpret_cast<const float4 *>(low + j * rank + r0);
-                                    float s0 = stg[j * 33 + lane], s1 = 0.f;
-#pragma unroll
-                                    for (int r = 0; r < kRankChunk; r += 8) {
-                                        if (r0 + r < rank) {  // rank is a multiple of 8
-                                            const float4 h0 = h[r / 4], h1 = h[r / 4 + 1];
-                                            ptx::fma2(s0, s1, h0.x, h0.y, b[r], b[r + 1], s0, s1);
-                                            ptx::fma2(s0, s1, h0.z, h0.w, b[r + 2], b[r + 3], s0, s1);
-                                            ptx::fma2(s0, s1, h1.x, h1.y, b[r + 4], b[r + 5], s0, s1);
-                                            ptx::fma2(s0, s1, h1.z, h1.w, b[r + 6], b[r + 7], s0, s1);
-                                        }
-                                    }
-                                    stg[j * 33 + lane] = s0 + s1;
-                                }
-                            }
-                        }
-                        j0 = max(j0, j1);
-                    }
-                    uint16_t *y = static_cast<uint16_t *>(a.out) + size_t(row0) * a.F + f;
-                    if (live)
-                        for (int j = 0; j < cols; ++j) y[size_t(j) * a.F] = to16(stg[j * 33 + lane], fp16);
                 }
             }
             ptx::tc_fence_before();
@@ -881,6 +1154,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const __grid_const
             }
         }
     }
+    // this grid's end is the end of the one before it, too
+    if constexpr (KIND == GR_LORA) ptx::griddep_wait();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
