@@ -1384,6 +1384,7 @@ int grouped_columns(int kind, int64_t T, int64_t N, int64_t groups) {
     int64_t want;
     if (kind == cf::GR_WGRAD) want = N;
     else if (kind == cf::GR_LORA) want = T;
+    else if (kind == cf::GR_SHRINK) want = T / cf::kGroupedWorkers;  // one tile of features: row tiles for every SM
     else want = std::min<int64_t>(T, 4 * ((T + groups - 1) / groups));
     int bn = kind == cf::GR_WGRAD ? 64 : 16;  // WGRAD stages dY in 64-column blocks
     while (bn < 256 && bn < want) bn *= 2;
@@ -1601,14 +1602,15 @@ extern "C" cf_status cf_grouped_gemm_wgrad(const void *X, const void *dY, const 
     return cf_grouped_gemm_wgrad_ex(X, dY, offsets, dW, T, N, K, E, dtype, workspace, workspace_bytes, stream, nullptr);
 }
 
-// workspace: head; partials of the first product; of the second (which may start while the first ends); H [T, 2, R] 16-bit
+// workspace: head; partials of the first product; of the second (which may start while the first ends); H [T, 2, R] 16-bit;
+// the adapter of each row [T] int32
 extern "C" size_t cf_gemm_lora_workspace_size(int64_t T, int64_t N, int64_t K, int64_t S, int64_t R) {
     (void)N;
     (void)K;
     if (T < 0 || R < 0 || S <= 0) return kGroupedHead;
     return kGroupedHead + grouped_partial_bytes(grouped_columns(cf::GR_SHRINK, T, 0, S)) +
            grouped_partial_bytes(grouped_columns(cf::GR_LORA, T, 0, S)) +
-           cf::align_up(size_t(T) * size_t(R) * 4, 256);
+           cf::align_up(size_t(T) * size_t(R) * 4, 256) + size_t(T) * 4;
 }
 
 extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *bias, const void *A, const void *B,
@@ -1640,6 +1642,7 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
     unsigned char *const part_sh = static_cast<unsigned char *>(workspace) + kGroupedHead;
     unsigned char *const part = part_sh + room_sh;
     void *H = part + room;
+    int *row_adapter = reinterpret_cast<int *>(part + room + cf::align_up(size_t(T) * size_t(R) * 4, 256));
     cf::GroupedArgs sh, a;
     int sh_ctas = 0, sh_smem = 0, ctas, smem;
     if (L > 0) {
@@ -1655,6 +1658,11 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
         sh.nweights = int(L);
         sh.scale = scale;
         sh.out = H;
+        sh.x = X;
+        sh.lora_a = A;
+        sh.row_adapter = row_adapter;
+        // (short requests are spread over the CTAs too: a unit for each of them and 8 ranks)
+        sh_ctas = int(std::min<int64_t>(std::max<int64_t>(sh_ctas, S * (R / 8)), std::min(dev.sm_count, cf::kGroupedWorkers)));
     }
     grouped_args(&a, T, N, K, 0, S, int(dtype), offsets, workspace, t);
     a.rank = int(R);
@@ -1671,6 +1679,7 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
     a.nweights = int(L);
     a.bias = bias;
     a.low = H;
+    a.row_adapter = row_adapter;
     a.lora_b = B;
     a.out = Y;
     if (L > 0) {

@@ -252,6 +252,8 @@ struct GroupedArgs {
     const float *scale;      // SHRINK: [nweights] or null
     const void *low;         // LORA: H [T, 2, rank] 16-bit, upper parts and rests
     int after_shrink;        // LORA: the launch before is the SHRINK that makes H (it waits for what came before it)
+    const void *x, *lora_a;  // SHRINK: X [T, C], A [nweights, C, F]
+    int *row_adapter;        // SHRINK writes, LORA reads: [T] adapter of each row, -1 for none
     const void *lora_b;      // LORA: B [nweights, rank, F]
     uint32_t *err;
     uint32_t *counters;      // [kGroupedSplitTiles] pieces arrived, zero between launches

@@ -39,32 +39,31 @@
 namespace cf {
 namespace {
 
-constexpr int kThreads = 320;   // 10 warps
-constexpr int kEpiWarps = 8;    // warps 2..9: two halves of 4 warps (128 lanes each)
-constexpr int kHalfThreads = 128;
+// Epilogue warps, from warp 2 on: two halves of 4 (128 lanes each); SHRINK one, and two more warps that only help
+// with its short requests.  A decode batch's SHRINK and LORA share the SMs, one CTA of each: 256 threads of 96
+// registers and 320 of 128 are what an SM has.
+__host__ __device__ constexpr int epi_warps(int kind) { return kind == GR_SHRINK ? 4 : 8; }
+__host__ __device__ constexpr int threads_of(int kind) { return kind == GR_SHRINK ? 256 : 320; }
+__host__ __device__ constexpr int registers_of(int kind, bool pair) {
+    return kind == GR_SHRINK ? 96 : kind == GR_LORA && !pair ? 128 : 200;
+}
+constexpr int kShortWarps = 6;
 constexpr int kBK = 64;         // contraction per stage (128 bytes: one swizzle atom)
 constexpr int kFB = 128;        // features per tile (accumulator lanes)
 constexpr int kABytes = kFB * kBK * 2;
 constexpr int kRasterRows = 16;  // row tiles walked before the next feature tile
 constexpr int kMinStretch = 4;   // blocks a worker takes at least
 constexpr int kLongRows = 64;    // LORA: rows from which a request has tiles of its own
-constexpr int kRankChunk = 16;   // LORA, mixed tiles: ranks of B in registers at once
+constexpr int kShortRows = 8;    // SHRINK: rows up to which a request's product runs on the CUDA cores
 
 constexpr uint32_t kInfoProducer = 0x10000000u;
 constexpr uint32_t kInfoMma = 0x20000000u;
 constexpr uint32_t kInfoEpi = 0x30000000u;
 constexpr uint32_t kInfoTable = 0x70000000u;
 
-__host__ __device__ constexpr uint32_t slice_bytes(int rank) {
-    return uint32_t(rank < kRankChunk ? rank : kRankChunk) * 64u;
-}
-
 struct GrLayout {
-    uint32_t stage_bytes, table, stg, low, ring, bars, total;
+    uint32_t stage_bytes, table, stg, bars, total;
 };
-
-// LORA, mixed tiles: slices of B in flight per epilogue warp
-__host__ __device__ constexpr int slice_depth(bool pair) { return pair ? 2 : 4; }
 
 // int32 arrays of the group table behind the Plan, groups + 1 long
 __host__ __device__ constexpr int table_arrays(int kind) { return kind == GR_LORA ? 5 : kind == GR_SHRINK ? 3 : 2; }
@@ -76,13 +75,10 @@ __host__ __device__ inline GrLayout gr_layout(int kind, bool pair, int stages, i
     uint32_t off = uint32_t(stages) * L.stage_bytes;
     L.table = off;
     off += (32u + uint32_t(table_arrays(kind) * (groups + 1)) * 4u + 15u) & ~15u;
-    L.stg = off;    // per epilogue warp: 16-bit [32 rows][32 features]; LORA: fp32 [32 rows][32 features]
-    off += kind == GR_LORA ? uint32_t(kEpiWarps) * 4096u
-                           : (kind == GR_FORWARD || kind == GR_DGRAD) ? uint32_t(kEpiWarps) * 2048u : 0u;
-    L.low = off;    // LORA: fp32 H [32 rows][rank] per half
-    off += kind == GR_LORA ? 2u * 32u * uint32_t(rank) * 4u : 0u;
-    L.ring = off;   // LORA: 16-bit slices of B [ranks][32 features], slice_depth per epilogue warp
-    off += kind == GR_LORA ? uint32_t(kEpiWarps * slice_depth(pair)) * slice_bytes(rank) : 0u;
+    // per epilogue warp: 16-bit [32 rows][32 features]; LORA: fp32; SHRINK: sums of the warps
+    L.stg = off;
+    off += kind == GR_LORA ? 8u * 4096u
+                           : (kind == GR_FORWARD || kind == GR_DGRAD) ? 8u * 2048u : uint32_t(kShortWarps) * 128u;
     L.bars = (off + 15u) & ~15u;
     L.total = L.bars + 256u;
     return L;
@@ -312,6 +308,16 @@ __device__ __forceinline__ uint16_t low_part(float h, bool fp16) {
     return to16(h, fp16);
 }
 
+// H in two 16-bit parts, upper and rest: 16 bits and more of mantissa (fp16: 22, within twice its range, behind which H
+// saturates), so that the second product can run on the tensor cores
+__device__ __forceinline__ void store_low(const GroupedArgs &a, int row, int r, float h) {
+    const bool fp16 = a.fp16 != 0;
+    uint16_t *y = static_cast<uint16_t *>(a.out) + size_t(row) * (2 * a.F) + r;
+    const uint16_t up = low_part(h, fp16);
+    y[0] = up;
+    y[a.F] = isfinite(h) ? low_part(h - from16(up, fp16), fp16) : uint16_t(0);
+}
+
 // A warp's fragment, 32 rows x 32 features, in its 2 KB of shared memory (64 bytes a row): lane l holds the 16-byte
 // piece l % 4 of rows l / 4, + 8, + 16, + 24.
 struct Fragment {
@@ -334,6 +340,21 @@ struct Fragment {
         __syncwarp();
     }
 };
+
+// a fragment in registers (32 rows of this lane's feature) turned in the warp's 4 KB of shared memory ...
+__device__ __forceinline__ void turn(const uint32_t (&v)[32], float *stg, int lane) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) stg[j * 32 + lane] = __uint_as_float(v[j]);
+    __syncwarp();
+}
+// ... and read back as 8 features of row lane / 4 + 8i, features (lane % 4) * 8 and on
+__device__ __forceinline__ void turned(float (&x)[8], const float *stg, int lane, int i) {
+    const float4 *s = reinterpret_cast<const float4 *>(stg + ((lane >> 2) + 8 * i) * 32 + (lane & 3) * 8);
+    const float4 l = s[0], h = s[1];
+    x[0] = l.x, x[1] = l.y, x[2] = l.z, x[3] = l.w;
+    x[4] = h.x, x[5] = h.y, x[6] = h.z, x[7] = h.w;
+}
 
 // the pieces of the pre-activation's fragment at column c of the tile (zeros outside)
 __device__ __forceinline__ void load_fragment(uint4 (&z)[4], const GroupedArgs &a, const Tile &w, int c, int q, int lane,
@@ -360,77 +381,77 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
     bool bad = raw0 != lo_all;
     const int first = lo_all;
     int carry = 0, longest = 0, ngroups = 0;
-    bool long_before = true;
-    __syncwarp();
-    if (lane == 0) tab.off[0] = first;
+    uint32_t long_before = 1u;
+    // No branches on the lane from here to the plan: lanes behind the last group repeat its end, count nothing and
+    // store what is stored there anyway.  (With branches between them the shuffles took 2000 cycles and more.)
+    tab.off[0] = first;
     for (int i0 = 0; i0 < a.groups; i0 += 32) {
         const int i = i0 + lane;
-        const int raw = i < a.groups ? tab.off[i + 1] : 0;
+        const bool in = i < a.groups;
+        const int at = in ? i : a.groups - 1;
+        const int raw = tab.off[at + 1];
         int v = min(max(raw, lo_all), a.T);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(kAll, v, d);
-            if (lane >= d) v = max(v, o);
+            v = lane >= d ? max(v, o) : v;
         }
-        int lo = __shfl_up_sync(kAll, v, 1);
-        if (lane == 0) lo = lo_all;
+        const int up = __shfl_up_sync(kAll, v, 1);
+        const int lo = lane == 0 ? lo_all : up;
         lo_all = __shfl_sync(kAll, v, 31);
-        const int rows = v - lo;
-        int count = 0;
-        if (i < a.groups) {
-            bad |= v != raw;
-            tab.off[i + 1] = v;
-            if constexpr (KIND == GR_WGRAD) {
-                count = max((rows + kBK - 1) / kBK, 1);
-                longest = max(longest, count);
-            } else {
-                count = ft * ((rows + a.bn - 1) >> shift);
-            }
-            if constexpr (KIND == GR_SHRINK || KIND == GR_LORA) {
-                const int w = tab.ad[i];
-                if (w < -1 || w >= a.nweights) {
-                    bad = true;
-                    tab.ad[i] = -1;
-                }
-                if (KIND == GR_SHRINK && (w < 0 || w >= a.nweights)) count = 0;
+        const int rows = in ? v - lo : 0;
+        bad |= in && v != raw;
+        tab.off[at + 1] = v;
+        int count;
+        if constexpr (KIND == GR_WGRAD) {
+            count = in ? max((rows + kBK - 1) / kBK, 1) : 0;
+            longest = max(longest, count);
+        } else {
+            count = ft * ((rows + a.bn - 1) >> shift);
+        }
+        if constexpr (KIND == GR_SHRINK || KIND == GR_LORA) {
+            int w = tab.ad[at];
+            const bool wrong = w < -1 || w >= a.nweights;
+            bad |= in && wrong;
+            w = wrong ? -1 : w;
+            tab.ad[at] = w;
+            count = KIND == GR_SHRINK && (w < 0 || rows <= kShortRows) ? 0 : count;
+            if constexpr (KIND == GR_LORA) {
+                // a long request is a group of its own, a run of short ones another
+                const uint32_t longs = __ballot_sync(kAll, rows >= kLongRows);
+                const uint32_t some = __ballot_sync(kAll, in);
+                const uint32_t m = (longs | (longs << 1) | long_before) & some;  // groups start here
+                long_before = longs >> 31;
+                const int gi = m >> lane & 1u ? ngroups + __popc(m & ((1u << lane) - 1u)) : a.groups;
+                tab.goff[gi] = lo;  // (the last entry is a dummy, or written below)
+                tab.gad[gi] = rows >= kLongRows ? w : -2;
+                ngroups += __popc(m);
             }
         }
-        if constexpr (KIND == GR_LORA) {
-            // a long request is a group of its own, a run of short ones another
-            const bool is_long = i < a.groups && rows >= kLongRows;
-            bool before = __shfl_up_sync(kAll, is_long, 1);
-            if (lane == 0) before = long_before;
-            long_before = __shfl_sync(kAll, is_long, 31);
-            const bool start = i < a.groups && (is_long || before);
-            const uint32_t m = __ballot_sync(kAll, start);
-            if (start) {
-                const int gi = ngroups + __popc(m & ((1u << lane) - 1u));
-                tab.goff[gi] = lo;
-                tab.gad[gi] = is_long ? tab.ad[i] : -2;
-            }
-            ngroups += __popc(m);
-        } else {
+        if constexpr (KIND != GR_LORA) {
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int o = __shfl_up_sync(kAll, count, d);
-                if (lane >= d) count += o;
+                count += lane >= d ? o : 0;
             }
-            if (i < a.groups) tab.pre[i + 1] = carry + count;
+            tab.pre[at + 1] = carry + count;
             carry += __shfl_sync(kAll, count, 31);
         }
     }
     if constexpr (KIND == GR_LORA) {
-        if (lane == 0) tab.goff[ngroups] = lo_all;
         __syncwarp();
-        for (int i0 = 0; i0 < ngroups; i0 += 32) {
+        tab.goff[ngroups] = lo_all;
+        __syncwarp();
+        for (int i0 = 0; i0 < a.groups; i0 += 32) {
             const int i = i0 + lane;
-            int count = i < ngroups ? ft * ((tab.goff[i + 1] - tab.goff[i] + a.bn - 1) >> shift) : 0;
+            const int at = i < ngroups ? i : ngroups - 1;
+            int count = i < ngroups ? ft * ((tab.goff[at + 1] - tab.goff[at] + a.bn - 1) >> shift) : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int o = __shfl_up_sync(kAll, count, d);
-                if (lane >= d) count += o;
+                count += lane >= d ? o : 0;
             }
-            if (i < ngroups) tab.pre[i + 1] = carry + count;
+            tab.pre[at + 1] = carry + count;
             carry += __shfl_sync(kAll, count, 31);
         }
     } else {
@@ -501,6 +522,26 @@ __device__ __forceinline__ void zero_tail(uint8_t *st, int left, int steps, int 
     __syncwarp();
 }
 
+// kCols columns of the first piece (p0) and `more` further ones (p, `step` apart), kFly of them in flight
+template <int kFly, int kCols>
+__device__ __forceinline__ void sum_columns(float (&s)[kCols], const float *p0, const float *p, size_t step, int more,
+                                            int cols) {
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) s[j] = j < cols ? __ldcg(p0 + j * kFB) : 0.f;
+    for (int k = 0; k < more; k += kFly) {
+        float x[kFly][kCols];
+#pragma unroll
+        for (int i = 0; i < kFly; ++i)
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+                x[i][j] = k + i < more && j < cols ? __ldcg(p + (k + i) * step + j * kFB) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kFly; ++i)
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) s[j] += x[i][j];
+    }
+}
+
 // the tile's pieces at columns c .. c + 31 of one lane, added in worker order; several pieces' loads in flight
 template <int KIND, bool kPair>
 __device__ __forceinline__ void sum_pieces(uint32_t (&v)[32], const GroupedArgs &a, const Walk<KIND, kPair> &walk,
@@ -514,25 +555,18 @@ __device__ __forceinline__ void sum_pieces(uint32_t (&v)[32], const GroupedArgs 
     const float *p0 = a.partials + size_t(2 * w.first + walk.slot_of(w.first, u0)) * piece + size_t(c) * kFB + l;
     const float *p = a.partials + size_t(2 * (w.first + 1)) * piece + size_t(c) * kFB + l;
     const int more = w.last - w.first;
-    constexpr int kFly = KIND == GR_LORA || KIND == GR_SHRINK ? 2 : 4;
+    if (cols <= 2) {  // a row or two: many pieces at once instead of many columns
+        float s[2];
+        sum_columns<16, 2>(s, p0, p, 2 * piece, more, cols);
+        v[0] = __float_as_uint(s[0]);
+        v[1] = __float_as_uint(s[1]);
+        return;
+    }
 #pragma unroll
     for (int jb = 0; jb < 32; jb += 8) {
         if (jb < cols) {
             float s[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] = jb + j < cols ? __ldcg(p0 + (jb + j) * kFB) : 0.f;
-            for (int k = 0; k < more; k += kFly) {
-                float x[kFly][8];
-#pragma unroll
-                for (int i = 0; i < kFly; ++i)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        x[i][j] = k + i < more && jb + j < cols ? __ldcg(p + (k + i) * (2 * piece) + (jb + j) * kFB) : 0.f;
-#pragma unroll
-                for (int i = 0; i < kFly; ++i)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) s[j] += x[i][j];
-            }
+            sum_columns<KIND == GR_LORA ? 2 : 4, 8>(s, p0 + jb * kFB, p + jb * kFB, 2 * piece, more, cols - jb);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[jb + j] = __float_as_uint(s[j]);
         }
@@ -540,127 +574,104 @@ __device__ __forceinline__ void sum_pieces(uint32_t (&v)[32], const GroupedArgs 
 }
 
 // LORA, a tile with rows of several requests: the adapters' second product on the CUDA cores, in fp32.  Each row takes
-// its own adapter's B and nothing of another's, so a NaN in an adapter stays with its requests.  stg holds the warp's 32 rows
-// x 32 features; rows [j_lo, j_hi) of them, at row0 of the batch, are added to.  Slices of B ([16 ranks][32 features])
-// arrive by cp.async a few items ahead: an item is a run of one request's rows and one slice.
-struct Runs {
-    const Table &tab;
-    int groups, rank, row0, j_lo, j_hi;
-    int seg, j0, j1, r0;
-    __device__ bool next() {  // the next item
-        r0 += kRankChunk;
-        if (r0 < rank) return true;
-        r0 = 0;
-        while (++seg < groups) {
-            j0 = max(tab.off[seg] - row0, j_lo);
-            if (j0 >= j_hi) break;
-            j1 = min(tab.off[seg + 1] - row0, j_hi);
-            if (j1 > j0 && tab.ad[seg] >= 0) return true;
-        }
-        seg = groups;
-        return false;
-    }
-};
-
-// (Not inlined: its registers would push the kernel's above what two CTAs an SM may have.)
-template <bool kPair>
-__device__ __noinline__ void add_low_rank(const GroupedArgs &a, const Table tab, float *stg, float *low, uint32_t ring,
-                                          int half, int q, int f0, int row0, int j_lo, int j_hi) {
-    const int lane = threadIdx.x & 31;
-    constexpr int kDepth = slice_depth(kPair);
+// its own adapter's B and nothing of another's, so a NaN in an adapter stays with its requests.
+// x: this lane's 8 features (from f on) of one row; four lanes cover a row's 32 features, eight rows go side by side
+// with an adapter each, and lanes of one adapter read the same addresses.
+template <int kFly>  // ranks of B in flight
+__device__ __forceinline__ void add_low_rank(float (&x)[8], const GroupedArgs &a, int row, int f) {
     const int rank = a.rank;
     const bool fp16 = a.fp16 != 0;
-    const uint32_t slot_bytes = slice_bytes(rank);
-    Runs issue{tab, a.groups, rank, row0, j_lo, j_hi, 0, 0, 0, rank};
-    {  // the request of the first row: the last one that starts at or before it
-        int lo = 0, hi = a.groups - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (tab.off[mid] <= row0 + j_lo) lo = mid;
-            else hi = mid - 1;
-        }
-        issue.seg = lo - 1;
-    }
-    Runs work = issue;
-    const int piece = (lane & 3) * 8;
-    const bool have = f0 + q * 32 + piece < a.F;
-    auto fetch = [&](int slot) {
-        if (issue.seg < a.groups && issue.next()) {
-            const uint16_t *src = static_cast<const uint16_t *>(a.lora_b) +
-                                  (size_t(tab.ad[issue.seg]) * rank + issue.r0) * a.F + (have ? f0 + q * 32 + piece : 0);
-            const int ranks = min(kRankChunk, rank - issue.r0);
-            for (int r = lane >> 2; r < ranks; r += 8)
-                ptx::cp_async16(ring + uint32_t(slot) * slot_bytes + uint32_t(r * 64 + (lane & 3) * 16),
-                                src + size_t(r) * a.F, have);
-        }
-        ptx::cp_async_commit();
-    };
+    const int ad = __ldcg(a.row_adapter + row);
+    if (ad < 0) return;
+    const uint16_t *h = static_cast<const uint16_t *>(a.low) + size_t(row) * (2 * rank);
+    const uint16_t *b = static_cast<const uint16_t *>(a.lora_b) + size_t(ad) * rank * a.F + f;
+    for (int r = 0; r < rank; r += 8) {
+        const uint4 up = __ldcg(reinterpret_cast<const uint4 *>(h + r));
+        const uint4 rest = __ldcg(reinterpret_cast<const uint4 *>(h + rank + r));
+        const uint32_t uw[4] = {up.x, up.y, up.z, up.w}, lw[4] = {rest.x, rest.y, rest.z, rest.w};
+        uint4 bv[kFly];
 #pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) fetch(i);
-    ptx::named_bar_sync(1 + half, kHalfThreads);  // the half is done with the last fragment's H
-    {
-        const uint16_t *src = static_cast<const uint16_t *>(a.low) + size_t(row0) * (2 * rank);
-        const int pieces = rank / 8;
-        for (int i = q * 32 + lane; i < (j_hi - j_lo) * pieces; i += kHalfThreads) {
-            const int j = j_lo + i / pieces, r = (i % pieces) * 8;
-            const uint4 h = *reinterpret_cast<const uint4 *>(src + size_t(j) * (2 * rank) + r);
-            const uint4 l = *reinterpret_cast<const uint4 *>(src + size_t(j) * (2 * rank) + rank + r);
-            float *d = low + j * rank + r;
-            const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+        for (int k = 0; k < 8; ++k) {
+            if (k % kFly == 0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                d[2 * k] = from16(uint16_t(hw[k]), fp16) + from16(uint16_t(lw[k]), fp16);
-                d[2 * k + 1] = from16(uint16_t(hw[k] >> 16), fp16) + from16(uint16_t(lw[k] >> 16), fp16);
+                for (int l = 0; l < kFly; ++l)
+                    bv[l] = __ldg(reinterpret_cast<const uint4 *>(b + size_t(r + k + l) * a.F));
             }
+            const uint32_t sh = (k & 1) * 16;
+            const float hk = from16(uint16_t(uw[k / 2] >> sh), fp16) + from16(uint16_t(lw[k / 2] >> sh), fp16);
+            const uint32_t w[4] = {bv[k % kFly].x, bv[k % kFly].y, bv[k % kFly].z, bv[k % kFly].w};
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                ptx::fma2(x[2 * p], x[2 * p + 1], hk, hk, from16(uint16_t(w[p]), fp16),
+                          from16(uint16_t(w[p] >> 16), fp16), x[2 * p], x[2 * p + 1]);
         }
     }
-    ptx::named_bar_sync(1 + half, kHalfThreads);
-    int slot = 0;
-    while (work.next()) {
-        fetch(slot == 0 ? kDepth - 1 : slot - 1);
-        ptx::cp_async_wait<kDepth - 1>();
-        __syncwarp();
-        const int ranks = min(kRankChunk, rank - work.r0);
-        float b[kRankChunk];
+}
+
+// SHRINK, short requests: H on the CUDA cores, by the warps from 2 on (192 threads).  A unit is a request and 8 ranks:
+// a thread takes 8 rows of A at a time for up to 4 rows of X, the sums are folded over the warp, then over the warps,
+// in a fixed order.  (As tiles, a request of one row took a copy of 64 rows of 32 bytes per block at rank 16, some 640
+// cycles of copy engine each.)
+__device__ void shrink_short(const GroupedArgs &a, const Table &tab, float *sums) {
+    const int tid = threadIdx.x - 64, lane = tid & 31, warp = tid >> 5;
+    const int chunks = a.F / 8;
+    const bool fp16 = a.fp16 != 0;
+    for (int u = blockIdx.x; u < a.groups * chunks; u += gridDim.x) {
+        const int s = u / chunks, r0 = (u - s * chunks) * 8;
+        const int lo = tab.off[s], rows = tab.off[s + 1] - lo, ad = tab.ad[s];
+        if (ad < 0 || rows == 0 || rows > kShortRows) continue;
+        const uint16_t *wa = static_cast<const uint16_t *>(a.lora_a) + size_t(ad) * a.C * a.F + r0;
+        for (int t0 = 0; t0 < rows; t0 += 4) {
+            const uint16_t *x = static_cast<const uint16_t *>(a.x) + size_t(lo + t0) * a.C;
+            float acc[32];  // [row][rank]
 #pragma unroll
-        for (int r = 0; r < kRankChunk; ++r)
-            if (r < ranks) {
-                uint16_t x;
-                ptx::ld_shared_u16(x, ring + uint32_t(slot) * slot_bytes + uint32_t(r * 64 + lane * 2));
-                b[r] = from16(x, fp16);
-            }
-        __syncwarp();  // the slot is free for the fetch of the next turn
-        for (int j = work.j0; j < work.j1; ++j) {
-            const float4 *h = reinterpret_cast<const float4 *>(low + j * rank + work.r0);
-            float s0 = stg[j * 32 + lane], s1 = 0.f, s2 = 0.f, s3 = 0.f;
+            for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+            for (int k = tid * 8; k < a.C; k += kShortWarps * 32 * 8) {
+                uint4 w[8];
 #pragma unroll
-            for (int r = 0; r < kRankChunk; r += 8) {
-                if (r < ranks) {  // a multiple of 8
-                    const float4 h0 = h[r / 4], h1 = h[r / 4 + 1];
-                    ptx::fma2(s0, s1, h0.x, h0.y, b[r], b[r + 1], s0, s1);
-                    ptx::fma2(s2, s3, h0.z, h0.w, b[r + 2], b[r + 3], s2, s3);
-                    ptx::fma2(s0, s1, h1.x, h1.y, b[r + 4], b[r + 5], s0, s1);
-                    ptx::fma2(s2, s3, h1.z, h1.w, b[r + 6], b[r + 7], s2, s3);
+                for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(wa + size_t(k + i) * a.F));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (t0 + j >= rows) continue;
+                    const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(x + size_t(j) * a.C + k));
+                    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float xs = from16(uint16_t(xw[i / 2] >> ((i & 1) * 16)), fp16);
+                        const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            ptx::fma2(acc[8 * j + 2 * p], acc[8 * j + 2 * p + 1], xs, xs, from16(uint16_t(ww[p]), fp16),
+                                      from16(uint16_t(ww[p] >> 16), fp16), acc[8 * j + 2 * p], acc[8 * j + 2 * p + 1]);
+                    }
                 }
             }
-            stg[j * 32 + lane] = (s0 + s1) + (s2 + s3);
+            // fold over the lanes: each step halves the values a lane keeps, lane l ends with value l
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) {
+#pragma unroll
+                for (int i = 0; i < d; ++i) {
+                    const bool upper = lane & d;
+                    const float give = upper ? acc[i] : acc[i + d];
+                    const float keep = upper ? acc[i + d] : acc[i];
+                    acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+                }
+            }
+            sums[warp * 32 + lane] = acc[0];
+            ptx::named_bar_sync(4, kShortWarps * 32);
+            if (warp == 0 && t0 + (lane >> 3) < rows) {
+                float h = 0.f;
+#pragma unroll
+                for (int i = 0; i < kShortWarps; ++i) h += sums[i * 32 + lane];
+                if (a.scale) h *= __ldg(a.scale + ad);
+                store_low(a, lo + t0 + (lane >> 3), r0 + (lane & 7), h);
+            }
+            ptx::named_bar_sync(4, kShortWarps * 32);
         }
-        slot = slot + 1 == kDepth ? 0 : slot + 1;
     }
-    ptx::cp_async_wait<0>();
-    __syncwarp();
-}
-// the same on a fragment in registers (32 rows of this lane's feature)
-template <bool kPair>
-__device__ __forceinline__ void add_low_rank(uint32_t (&v)[32], const GroupedArgs &a, const Table &tab, float *stg,
-                                             float *low, uint32_t ring, int half, int q, int lane, int f0, int row0,
-                                             int j_lo, int j_hi) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) stg[j * 32 + lane] = __uint_as_float(v[j]);
-    add_low_rank<kPair>(a, tab, stg, low, ring, half, q, f0, row0, j_lo, j_hi);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(stg[j * 32 + lane]);
-    __syncwarp();
+    // the adapter of each row, for the tiles of several requests
+    for (int s = blockIdx.x; s < a.groups; s += gridDim.x)
+        for (int r = tab.off[s] + tid; r < tab.off[s + 1]; r += kShortWarps * 32) a.row_adapter[r] = tab.ad[s];
 }
 
 template <bool kPair>
@@ -717,9 +728,8 @@ __device__ __forceinline__ void stage_loads(const GroupedArgs &a, const Tile &w,
     }
 }
 
-// (a decode batch's SHRINK and LORA share the SMs, two CTAs each)
 template <int KIND, bool kPair>
-__global__ void __launch_bounds__(kThreads, KIND == GR_SHRINK || (KIND == GR_LORA && !kPair) ? 2 : 1) grouped_kernel(const __grid_constant__ GroupedArgs a) {
+__global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __grid_constant__ GroupedArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = ptx::smem_u32(smem_raw);
     if ((base & 1023u) != 0u) {  // the swizzled operand tiles need it; see the fused GEMM
@@ -727,6 +737,7 @@ __global__ void __launch_bounds__(kThreads, KIND == GR_SHRINK || (KIND == GR_LOR
         if (threadIdx.x == 0) ptx::record_error(a.err, 8u, 0x60000000u | (base & 1023u));
         return;
     }
+    constexpr int kEpiWarps = epi_warps(KIND), kThreads = threads_of(KIND), kHalves = kEpiWarps / 4;
     constexpr bool kAMn = KIND != GR_DGRAD;  // features contiguous in memory: A is MN-major
     constexpr bool kBMn = KIND == GR_WGRAD;
     const int stages = a.stages;
@@ -736,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, KIND == GR_SHRINK || (KIND == GR_LOR
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem_raw + (B.misc - base));
     volatile uint32_t *abort = misc + 1;
     const uint64_t tmo = a.timeout_ns;
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // one for the warp, and known to be
     const int lane = threadIdx.x & 31;
     const uint32_t tmem_cols = uint32_t(2 * a.bn);
     // A pair (two CTAs of a cluster) works on one tile of 256 features: the even CTA issues MMAs of M = 256 that
@@ -1000,10 +1011,8 @@ __global__ void __launch_bounds__(kThreads, KIND == GR_SHRINK || (KIND == GR_LOR
         const int half = e >> 2;
         const int q = warp & 3;
         const bool fp16 = a.fp16 != 0;
-        float *const low_stg = reinterpret_cast<float *>(smem_raw + L.stg) + e * 1024;
-        float *const low = reinterpret_cast<float *>(smem_raw + L.low) + half * 32 * a.rank;
-        const uint32_t low_ring = base + L.ring + uint32_t(e * slice_depth(kPair)) * slice_bytes(a.rank);
-        for (int tile = 0; walk.next(w); ++tile) {
+        if constexpr (KIND == GR_SHRINK) shrink_short(a, tab, reinterpret_cast<float *>(smem_raw + L.stg));
+        for (int tile = 0; e < kEpiWarps && walk.next(w); ++tile) {
             const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
             uint4 zv[4];  // DGRAD: the next fragment's pre-activations, on their way before the accumulator is ready
             if constexpr (KIND == GR_DGRAD)
@@ -1014,28 +1023,43 @@ __global__ void __launch_bounds__(kThreads, KIND == GR_SHRINK || (KIND == GR_LOR
             const int f = w.f0 + q * 32 + lane;
             const bool live = f < a.F && ok;
             bool held = true;  // the accumulator is still this tile's
-            // rows whose low-rank product falls to this worker (LORA, a tile of several requests): all of them, or its
-            // share of a divided tile's
-            int low_lo = 0, low_hi = KIND == GR_LORA && w.ad == -2 && a.nweights > 0 ? w.n : 0;
-            if (!kPair && !w.whole()) {
-                if constexpr (KIND == GR_LORA) {
-                    const int parts = w.last - w.first + 1, mine = worker - w.first;
-                    low_lo = low_hi * mine / parts;
-                    low_hi = low_hi * (mine + 1) / parts;
-                    if (low_hi > low_lo) ptx::griddep_wait();
+            // LORA, a tile of several requests: this worker adds the low-rank product of every parts-th eight rows
+            int parts = 0, part = 0;
+            if constexpr (KIND == GR_LORA) {
+                if (w.ad == -2 && a.nweights > 0) {
+                    parts = w.last - w.first + 1;
+                    part = worker - w.first;
+                    ptx::griddep_wait();  // H is the previous grid's
                 }
+            }
+            if (!kPair && !w.whole()) {
                 // a piece of the tile: to the workspace, [column][lane]; the last to arrive goes on with the sum
                 float *const mine = a.partials + size_t(2 * worker + w.slot) * size_t(kFB * a.bn) + q * 32 + lane;
-                for (int c = half * 32; c < w.n; c += 64) {
+                for (int c = half * 32; c < w.n; c += 32 * kHalves) {
                     uint32_t v[32];
                     ptx::tmem_ld32(tacc + uint32_t(c), v);
                     ptx::tmem_ld_wait();
                     const int cols = min(32, w.n - c);
                     if constexpr (KIND == GR_LORA) {
-                        const int j_lo = max(low_lo - c, 0), j_hi = min(low_hi - c, 32);
-                        if (j_lo < j_hi)
-                            add_low_rank<kPair>(v, a, tab, low_stg, low, low_ring, half, q, lane, w.f0, w.col0 + c, j_lo,
-                                                j_hi);
+                        if (parts > 0) {
+                            float *const stg = reinterpret_cast<float *>(smem_raw + L.stg) + e * 1024;
+                            turn(v, stg, lane);
+                            const int f8 = w.f0 + q * 32 + (lane & 3) * 8;
+                            float *p = a.partials + size_t(2 * worker + w.slot) * size_t(kFB * a.bn) +
+                                       size_t(c + (lane >> 2)) * kFB + q * 32 + (lane & 3) * 8;
+#pragma unroll 1
+                            for (int i = 0; i < 4; ++i, p += 8 * kFB) {
+                                if ((lane >> 2) + 8 * i >= cols || f8 >= a.F) continue;
+                                float x[8];
+                                turned(x, stg, lane, i);
+                                if ((c / 8 + i) % parts == part)
+                                    add_low_rank<8>(x, a, w.col0 + c + (lane >> 2) + 8 * i, f8);
+                                float4 *d = reinterpret_cast<float4 *>(p);
+                                __stcg(d, make_float4(x[0], x[1], x[2], x[3]));
+                                __stcg(d + 1, make_float4(x[4], x[5], x[6], x[7]));
+                            }
+                            continue;
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -1056,13 +1080,11 @@ __global__ void __launch_bounds__(kThreads, KIND == GR_SHRINK || (KIND == GR_LOR
                 }
                 ptx::named_bar_sync(3, kEpiWarps * 32);
                 if (*verdict == 0u) continue;
-                low_hi = 0;
+                parts = 0;  // the pieces hold it
                 if constexpr (KIND == GR_DGRAD)
                     if (a.preact && half * 32 < w.n) load_fragment(zv, a, w, half * 32, q, lane, true);
             }
-            if constexpr (KIND == GR_LORA)
-                if (low_hi > low_lo) ptx::griddep_wait();
-            for (int c = half * 32; c < w.n; c += 64) {
+            for (int c = half * 32; c < w.n; c += 32 * kHalves) {
                 uint32_t v[32];
                 if (kPair || w.whole()) {
                     ptx::tmem_ld32(tacc + uint32_t(c), v);
@@ -1072,18 +1094,34 @@ __global__ void __launch_bounds__(kThreads, KIND == GR_SHRINK || (KIND == GR_LOR
                 }
                 const int cols = min(32, w.n - c);
                 if constexpr (KIND == GR_LORA) {
-                    if (low_hi > low_lo)
-                        add_low_rank<kPair>(v, a, tab, low_stg, low, low_ring, half, q, lane, w.f0, w.col0 + c, 0, cols);
-                    if (a.bias) {
-                        const float bv = f < a.F ? __ldg(a.bias + f) : 0.f;
+                    float *const stg = reinterpret_cast<float *>(smem_raw + L.stg) + e * 1024;
+                    turn(v, stg, lane);
+                    const int f8 = w.f0 + q * 32 + (lane & 3) * 8;
+                    float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    if (a.bias && f8 < a.F) {
+                        const float4 b0 = __ldg(reinterpret_cast<const float4 *>(a.bias + f8));
+                        const float4 b1 = __ldg(reinterpret_cast<const float4 *>(a.bias + f8) + 1);
+                        bias[0] = b0.x, bias[1] = b0.y, bias[2] = b0.z, bias[3] = b0.w;
+                        bias[4] = b1.x, bias[5] = b1.y, bias[6] = b1.z, bias[7] = b1.w;
+                    }
+                    uint16_t *y = static_cast<uint16_t *>(a.out) + size_t(w.col0 + c + (lane >> 2)) * a.F + f8;
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i, y += size_t(8) * a.F) {
+                        if ((lane >> 2) + 8 * i >= cols || f8 >= a.F || !ok) continue;
+                        float x[8];
+                        turned(x, stg, lane, i);
+                        if (parts > 0) add_low_rank<8>(x, a, w.col0 + c + (lane >> 2) + 8 * i, f8);
+                        uint32_t p[4];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + bv);
+                        for (int k = 0; k < 4; ++k)
+                            p[k] = pack16(x[2 * k] + bias[2 * k], x[2 * k + 1] + bias[2 * k + 1], fp16);
+                        *reinterpret_cast<uint4 *>(y) = make_uint4(p[0], p[1], p[2], p[3]);
                     }
                 }
-                if constexpr (KIND == GR_FORWARD || KIND == GR_DGRAD || KIND == GR_LORA) {
+                if constexpr (KIND == GR_FORWARD || KIND == GR_DGRAD) {
                     // The fragment is turned in shared memory (a lane's feature column in, whole rows out), so that
                     // global memory is read and written in 16-byte pieces, 64 bytes a row.
-                    uint8_t *const stg = smem_raw + L.stg + e * (KIND == GR_LORA ? 4096 : 2048);
+                    uint8_t *const stg = smem_raw + L.stg + e * 2048;
                     const Fragment fr{stg, lane, cols, (w.f0 + q * 32 + (lane & 3) * 8) < a.F && ok,
                                       size_t(w.col0 + c + (lane >> 2)) * a.F + w.f0 + q * 32 + (lane & 3) * 8,
                                       size_t(8) * a.F};
@@ -1114,20 +1152,10 @@ __global__ void __launch_bounds__(kThreads, KIND == GR_SHRINK || (KIND == GR_LOR
                     for (int j = 0; j < 32; ++j) mine[j * 32] = to16(__uint_as_float(v[j]), fp16);
                     fr.out(a.out);
                 } else if constexpr (KIND == GR_SHRINK) {
-                    // H in two 16-bit parts, upper and rest: 16 bits and more of mantissa (fp16: 22, within twice its
-                    // range, behind which H saturates), so that the second product can run on the tensor cores
                     const float sc = a.scale ? __ldg(a.scale + w.w) : 1.f;
-                    uint16_t *y = static_cast<uint16_t *>(a.out) + size_t(w.col0 + c) * (2 * a.F) + f;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (live && j < cols) {
-                            const float h = sc * __uint_as_float(v[j]);
-                            const uint16_t up = low_part(h, fp16);
-                            const float rest = h - from16(up, fp16);
-                            y[size_t(j) * (2 * a.F)] = up;
-                            y[size_t(j) * (2 * a.F) + a.F] = isfinite(h) ? low_part(rest, fp16) : uint16_t(0);
-                        }
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        if (live && j < cols) store_low(a, w.col0 + c + j, f, sc * __uint_as_float(v[j]));
                 } else if constexpr (KIND == GR_WGRAD) {
                     if (live) {
                         uint16_t *y = static_cast<uint16_t *>(a.out) + (size_t(w.g) * a.F + f) * a.N + w.col0 + c;
@@ -1201,7 +1229,7 @@ cudaError_t launch_grouped(int kind, const GroupedArgs &a, int ctas, int smem, b
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads_of(kind));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

@@ -334,22 +334,6 @@ __device__ __forceinline__ void bulk_copy_s2cluster(uint32_t remote_dst, uint32_
         : "memory");
 }
 
-// 16-byte asynchronous copy global -> shared of one thread; zeros where !have (nothing is read then)
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool have) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
-                 "r"(have ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// at most N of this thread's committed groups are still on their way
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void ld_shared_u16(uint16_t &v, uint32_t addr) {
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-}
-
 // 2-D tiled TMA store from this CTA's shared memory (bulk-group completion)
 __device__ __forceinline__ void tma_store_2d(const void *tmap, uint32_t src, int32_t x, int32_t y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
