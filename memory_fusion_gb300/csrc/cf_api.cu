@@ -1378,16 +1378,17 @@ cf_status grouped_sizes(int64_t T, int64_t N, int64_t K, int64_t groups, int dty
     return CF_OK;
 }
 
-// Accumulator columns where none are asked for.  Columns are rows of the batch (WGRAD: columns of dW): four times
-// the mean group, so that an uneven group still reads its weights once, between 16 and 256.
+// Accumulator columns where none are asked for.  Columns are rows of the batch (WGRAD: columns of dW): twice
+// the mean group, so that most uneven groups read their weights once, between 16 and 256.  (4099 rows over 64 groups:
+// 128 columns 49 us, 256 57 us, 64 68 us.)
 int grouped_columns(int kind, int64_t T, int64_t N, int64_t groups) {
     int64_t want;
     if (kind == cf::GR_WGRAD) want = N;
     else if (kind == cf::GR_LORA) want = T;
     else if (kind == cf::GR_SHRINK) want = T / cf::kGroupedWorkers;  // one tile of features: row tiles for every SM
-    else want = std::min<int64_t>(T, 4 * ((T + groups - 1) / groups));
+    else want = std::min<int64_t>(T, 2 * ((T + groups - 1) / groups));
     int bn = kind == cf::GR_WGRAD ? 64 : 16;  // WGRAD stages dY in 64-column blocks
-    while (bn < 256 && bn < want) bn *= 2;
+    while (bn < 256 && 5 * bn < 4 * want) bn *= 2;
     return bn;
 }
 
@@ -1395,9 +1396,10 @@ int grouped_columns(int kind, int64_t T, int64_t N, int64_t groups) {
 size_t grouped_partial_bytes(int bn) { return size_t(2 * cf::kGroupedWorkers) * 128 * size_t(bn) * 4; }
 constexpr size_t kGroupedCounterBytes = size_t(cf::kGroupedSplitTiles) * 4;
 // Head of a workspace, the same for every grouped and adapter call and all sizes, so that one workspace may serve
-// them in turn: the error word and two sets of counters, zero between launches (the adapters' two launches may
-// overlap).  Behind it, data that no launch expects to find.
-constexpr size_t kGroupedHead = cf::kErrBytes + 2 * kGroupedCounterBytes;
+// them in turn: the error word and three sets of counters, zero between launches (tiles of either of the adapters'
+// two launches, which may overlap, and their short requests).  Behind it, data that no launch expects to find.
+constexpr size_t kGroupedHead = cf::kErrBytes + 3 * kGroupedCounterBytes;
+static_assert(cf::kGroupedWorkers <= cf::kGroupedSplitTiles, "one counter for each unit with parts");
 
 // Ring depth, grid and workspace of one grouped launch: counter set 0 or 1, `room` bytes of partials at `part`.
 cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int64_t groups, int64_t rank,
@@ -1419,10 +1421,13 @@ cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int
     };
     // CTA pairs where there are full tiles for all of them; a smaller launch is better off dividing its tiles
     if (t.cluster_m < 0 || t.cluster_m > 2) return CF_ERR_UNSUPPORTED;
-    bool pair = kind != cf::GR_SHRINK && bn == 256 && F > 128 && tiles_of(256) >= dev.sm_count;
+    // and where rounding the features up to 256 costs less than a tenth more than to 128
+    bool pair = kind != cf::GR_SHRINK && bn >= 128 && !(wgrad && bn < 256) && tiles_of(256) >= dev.sm_count &&
+                20 * ((F + 255) / 256) <= 11 * ((F + 127) / 128);
     if (t.cluster_m != 0) pair = t.cluster_m == 2;
     if (pair && (kind == cf::GR_SHRINK || bn < 128)) return CF_ERR_UNSUPPORTED;
-    int stages = t.stages > 0 ? t.stages : 12;
+    int stages = t.stages > 0 ? t.stages : 8;  // (deeper rings of small stages were slower: 250 rows over 32 groups, 12
+                                               // stages 76.9 us, 8 stages 73.2)
     // a decode batch's two adapter products share the SMs: the second reads its weights while the first runs
     const int shrink_room = 98 * 1024, room_smem = bn > 64                ? kMaxSmem
                                                    : kind == cf::GR_SHRINK ? shrink_room
@@ -1602,15 +1607,27 @@ extern "C" cf_status cf_grouped_gemm_wgrad(const void *X, const void *dY, const 
     return cf_grouped_gemm_wgrad_ex(X, dY, offsets, dW, T, N, K, E, dtype, workspace, workspace_bytes, stream, nullptr);
 }
 
+// parts of a short request's first contraction: few requests are spread over the SMs
+static int lora_split(int64_t S, int64_t R) {
+    const int64_t units = S * ((R + 63) / 64);
+    return int(std::max<int64_t>(1, std::min<int64_t>(cf::kLoraMaxSplit, cf::kGroupedWorkers / std::max<int64_t>(units, 1))));
+}
+
+// (no parts, no scratch; with parts there are few units)
+static size_t lora_part_bytes(int64_t S, int64_t R) {
+    const int n = lora_split(S, R);
+    return n > 1 ? size_t(S) * size_t((R + 63) / 64) * size_t(n) * cf::kLoraShortRows * 64 * 4 : 0;
+}
+
 // workspace: head; partials of the first product; of the second (which may start while the first ends); H [T, 2, R] 16-bit;
-// the adapter of each row [T] int32
+// parts of the short requests' first product
 extern "C" size_t cf_gemm_lora_workspace_size(int64_t T, int64_t N, int64_t K, int64_t S, int64_t R) {
     (void)N;
     (void)K;
     if (T < 0 || R < 0 || S <= 0) return kGroupedHead;
     return kGroupedHead + grouped_partial_bytes(grouped_columns(cf::GR_SHRINK, T, 0, S)) +
            grouped_partial_bytes(grouped_columns(cf::GR_LORA, T, 0, S)) +
-           cf::align_up(size_t(T) * size_t(R) * 4, 256) + size_t(T) * 4;
+           cf::align_up(size_t(T) * size_t(R) * 4, 256) + lora_part_bytes(S, R);
 }
 
 extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *bias, const void *A, const void *B,
@@ -1642,7 +1659,7 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
     unsigned char *const part_sh = static_cast<unsigned char *>(workspace) + kGroupedHead;
     unsigned char *const part = part_sh + room_sh;
     void *H = part + room;
-    int *row_adapter = reinterpret_cast<int *>(part + room + cf::align_up(size_t(T) * size_t(R) * 4, 256));
+    float *const low_parts = reinterpret_cast<float *>(part + room + cf::align_up(size_t(T) * size_t(R) * 4, 256));
     cf::GroupedArgs sh, a;
     int sh_ctas = 0, sh_smem = 0, ctas, smem;
     if (L > 0) {
@@ -1660,9 +1677,12 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
         sh.out = H;
         sh.x = X;
         sh.lora_a = A;
-        sh.row_adapter = row_adapter;
-        // (short requests are spread over the CTAs too: a unit for each of them and 8 ranks)
-        sh_ctas = int(std::min<int64_t>(std::max<int64_t>(sh_ctas, S * (R / 8)), std::min(dev.sm_count, cf::kGroupedWorkers)));
+        sh.low_counters = reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(workspace) + cf::kErrBytes +
+                                                       2 * kGroupedCounterBytes);
+        sh.low_parts = low_parts;
+        sh.low_split = lora_split(S, R);
+        sh_ctas = int(std::min<int64_t>(std::max<int64_t>(sh_ctas, S * ((R + 63) / 64) * sh.low_split),
+                                        std::min(dev.sm_count, cf::kGroupedWorkers)));
     }
     grouped_args(&a, T, N, K, 0, S, int(dtype), offsets, workspace, t);
     a.rank = int(R);
@@ -1679,7 +1699,6 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
     a.nweights = int(L);
     a.bias = bias;
     a.low = H;
-    a.row_adapter = row_adapter;
     a.lora_b = B;
     a.out = Y;
     if (L > 0) {

@@ -235,6 +235,8 @@ enum GroupedKind : int {
 constexpr int kGroupedMaxGroups = 1024;  // the group table lives in shared memory
 constexpr int kGroupedSplitTiles = 1024; // tiles whose contraction may be divided among CTAs
 constexpr int kGroupedWorkers = 160;     // CTAs that may hold a piece of a tile (a GB300 has 152 SMs)
+constexpr int kLoraShortRows = 8;        // rows up to which a request's X . A runs on the CUDA cores
+constexpr int kLoraMaxSplit = 8;         // parts of their contraction
 constexpr int kLoraMaxRank = 128;        // one tile of features in the first product
 
 struct GroupedArgs {
@@ -253,7 +255,9 @@ struct GroupedArgs {
     const void *low;         // LORA: H [T, 2, rank] 16-bit, upper parts and rests
     int after_shrink;        // LORA: the launch before is the SHRINK that makes H (it waits for what came before it)
     const void *x, *lora_a;  // SHRINK: X [T, C], A [nweights, C, F]
-    int *row_adapter;        // SHRINK writes, LORA reads: [T] adapter of each row, -1 for none
+    float *low_parts;        // SHRINK: [request and 64 ranks][low_split][kLoraShortRows][64] parts of short requests' H
+    uint32_t *low_counters;  // SHRINK: parts arrived, zero between launches
+    int low_split;           // SHRINK: parts of a short request's contraction
     const void *lora_b;      // LORA: B [nweights, rank, F]
     uint32_t *err;
     uint32_t *counters;      // [kGroupedSplitTiles] pieces arrived, zero between launches

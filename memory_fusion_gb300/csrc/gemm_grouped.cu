@@ -54,7 +54,7 @@ constexpr int kABytes = kFB * kBK * 2;
 constexpr int kRasterRows = 16;  // row tiles walked before the next feature tile
 constexpr int kMinStretch = 4;   // blocks a worker takes at least
 constexpr int kLongRows = 64;    // LORA: rows from which a request has tiles of its own
-constexpr int kShortRows = 8;    // SHRINK: rows up to which a request's product runs on the CUDA cores
+constexpr int kShortRows = kLoraShortRows;
 
 constexpr uint32_t kInfoProducer = 0x10000000u;
 constexpr uint32_t kInfoMma = 0x20000000u;
@@ -75,10 +75,12 @@ __host__ __device__ inline GrLayout gr_layout(int kind, bool pair, int stages, i
     uint32_t off = uint32_t(stages) * L.stage_bytes;
     L.table = off;
     off += (32u + uint32_t(table_arrays(kind) * (groups + 1)) * 4u + 15u) & ~15u;
-    // per epilogue warp: 16-bit [32 rows][32 features]; LORA: fp32; SHRINK: sums of the warps
+    // per epilogue warp: 16-bit [32 rows][32 features]; LORA: fp32; WGRAD: 16-bit [32 features][64 columns];
+    // SHRINK: the warps' sums of 4 rows x 64 ranks
     L.stg = off;
     off += kind == GR_LORA ? 8u * 4096u
-                           : (kind == GR_FORWARD || kind == GR_DGRAD) ? 8u * 2048u : uint32_t(kShortWarps) * 128u;
+                           : (kind == GR_FORWARD || kind == GR_DGRAD) ? 8u * 2048u
+           : kind == GR_WGRAD ? 8u * 4096u : uint32_t(kShortWarps) * 4u * 64u * 4u;
     L.bars = (off + 15u) & ~15u;
     L.total = L.bars + 256u;
     return L;
@@ -97,7 +99,7 @@ __device__ __forceinline__ GrBars gr_bars(uint32_t base, int stages) {
     b.misc = b.mma_done + 8;
     return b;
 }
-static_assert(16 * 12 + 16 + 16 + 8 + 16 <= 256, "barrier area");
+static_assert(16 * 12 + 16 + 16 + 8 + 20 <= 256, "barrier area");
 
 template <bool kPair>
 __device__ __forceinline__ int feature_tiles(const GroupedArgs &a) {
@@ -341,6 +343,36 @@ struct Fragment {
     }
 };
 
+// WGRAD: 32 columns of this lane's row of dW.  Rows go out in whole 128 bytes: the first call of a 64-column block
+// (c % 64 == 0) leaves its half in the warp's 4 KB of shared memory, the second sends both (pieces of 16 bytes, at
+// piece ^ row % 8 so that neither side of the turn meets bank conflicts).
+__device__ __forceinline__ void store_columns(const uint32_t (&v)[32], const GroupedArgs &a, const Tile &w, int c,
+                                              uint4 *stg, int q, int lane, bool ok) {
+    const bool fp16 = a.fp16 != 0;
+    const int hi = (c & 32) / 8;  // pieces 0..3 or 4..7 of the block
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // an empty group's sum is zero
+            p[i] = w.nk == 0 ? 0u
+                             : pack16(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]), fp16);
+        stg[lane * 8 + ((hi + j) ^ (lane & 7))] = make_uint4(p[0], p[1], p[2], p[3]);
+    }
+    if (hi == 0 && c + 32 < w.n) return;
+    __syncwarp();
+    const int c0 = c & ~63, piece = lane & 7;
+    const int f0 = w.f0 + q * 32 + (lane >> 3);
+    uint16_t *y = static_cast<uint16_t *>(a.out) + (size_t(w.g) * a.F + f0) * a.N + w.col0 + c0 + piece * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = (lane >> 3) + 4 * i;
+        if (ok && f0 + 4 * i < a.F && c0 + piece * 8 < w.n)  // N is a multiple of 8
+            *reinterpret_cast<uint4 *>(y + size_t(4 * i) * a.N) = stg[row * 8 + (piece ^ (row & 7))];
+    }
+    __syncwarp();
+}
+
 // a fragment in registers (32 rows of this lane's feature) turned in the warp's 4 KB of shared memory ...
 __device__ __forceinline__ void turn(const uint32_t (&v)[32], float *stg, int lane) {
     __syncwarp();
@@ -522,156 +554,266 @@ __device__ __forceinline__ void zero_tail(uint8_t *st, int left, int steps, int 
     __syncwarp();
 }
 
-// kCols columns of the first piece (p0) and `more` further ones (p, `step` apart), kFly of them in flight
-template <int kFly, int kCols>
-__device__ __forceinline__ void sum_columns(float (&s)[kCols], const float *p0, const float *p, size_t step, int more,
-                                            int cols) {
-#pragma unroll
-    for (int j = 0; j < kCols; ++j) s[j] = j < cols ? __ldcg(p0 + j * kFB) : 0.f;
-    for (int k = 0; k < more; k += kFly) {
-        float x[kFly][kCols];
-#pragma unroll
-        for (int i = 0; i < kFly; ++i)
-#pragma unroll
-            for (int j = 0; j < kCols; ++j)
-                x[i][j] = k + i < more && j < cols ? __ldcg(p + (k + i) * step + j * kFB) : 0.f;
-#pragma unroll
-        for (int i = 0; i < kFly; ++i)
-#pragma unroll
-            for (int j = 0; j < kCols; ++j) s[j] += x[i][j];
-    }
-}
-
-// the tile's pieces at columns c .. c + 31 of one lane, added in worker order; several pieces' loads in flight
+// Where the pieces of a divided tile lie: the first may be the second slot of its worker, every later one starts its
+// worker's stretch.
+struct Pieces {
+    const float *p0, *p;  // of the first piece, of the second
+    size_t step;          // from the second on
+    int more;             // pieces behind the first
+};
 template <int KIND, bool kPair>
-__device__ __forceinline__ void sum_pieces(uint32_t (&v)[32], const GroupedArgs &a, const Walk<KIND, kPair> &walk,
-                                           const Tile &w, int c, int l) {
-    const int cols = min(32, w.n - c);
+__device__ __forceinline__ Pieces pieces_of(const GroupedArgs &a, const Walk<KIND, kPair> &walk, const Tile &w) {
     const int u0 = KIND == GR_WGRAD
                        ? walk.per_group * walk.tab.pre[w.g] + (w.id - w.g * walk.per_group) * max(w.nk, 1)
                        : w.id * w.nk;
     const size_t piece = size_t(kFB) * a.bn;
-    // the first piece may be the second slot of its worker; every later one starts its worker's stretch
-    const float *p0 = a.partials + size_t(2 * w.first + walk.slot_of(w.first, u0)) * piece + size_t(c) * kFB + l;
-    const float *p = a.partials + size_t(2 * (w.first + 1)) * piece + size_t(c) * kFB + l;
-    const int more = w.last - w.first;
-    if (cols <= 2) {  // a row or two: many pieces at once instead of many columns
-        float s[2];
-        sum_columns<16, 2>(s, p0, p, 2 * piece, more, cols);
-        v[0] = __float_as_uint(s[0]);
-        v[1] = __float_as_uint(s[1]);
-        return;
+    return Pieces{a.partials + size_t(2 * w.first + walk.slot_of(w.first, u0)) * piece,
+                  a.partials + size_t(2 * (w.first + 1)) * piece, 2 * piece, w.last - w.first};
+}
+
+// WGRAD: the pieces at 32 columns from c on of one lane, added in worker order
+__device__ __forceinline__ void sum_pieces(uint32_t (&v)[32], const Pieces &pc, int c, int n, int l) {
+    const int cols = min(32, n - c);
+    const size_t at = size_t(c) * kFB + l;
+    float s[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) s[j] = j < cols ? __ldcg(pc.p0 + at + j * kFB) : 0.f;
+    for (int k = 0; k < pc.more; k += 2) {  // two pieces' loads in flight
+        float x[2][32];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                x[i][j] = k + i < pc.more && j < cols ? __ldcg(pc.p + (k + i) * pc.step + at + j * kFB) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] += x[i][j];
     }
 #pragma unroll
-    for (int jb = 0; jb < 32; jb += 8) {
-        if (jb < cols) {
-            float s[8];
-            sum_columns<KIND == GR_LORA ? 2 : 4, 8>(s, p0 + jb * kFB, p + jb * kFB, 2 * piece, more, cols - jb);
+    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(s[j]);
+}
+
+// Four features of one row, finished and stored: s holds the products.
+template <int KIND>
+__device__ __forceinline__ void finish_row(const GroupedArgs &a, const Tile &w, int row, int f, float4 s4) {
+    const bool fp16 = a.fp16 != 0;
+    float s[4] = {s4.x, s4.y, s4.z, s4.w};
+    if constexpr (KIND == GR_SHRINK) {
+        const float sc = a.scale ? __ldg(a.scale + w.w) : 1.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[jb + j] = __float_as_uint(s[j]);
+        for (int i = 0; i < 4; ++i) store_low(a, row, f + i, sc * s[i]);
+        return;
+    }
+    const size_t at = size_t(row) * a.F + f;
+    if (KIND == GR_FORWARD && a.preact)
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.preact) + at) =
+            make_uint2(pack16(s[0], s[1], fp16), pack16(s[2], s[3], fp16));
+    if (KIND == GR_FORWARD && a.act) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = gelu(s[i]);
+    }
+    if (KIND == GR_DGRAD && a.preact) {
+        const uint2 z = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.preact) + at);
+        const uint32_t zw[2] = {z.x, z.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] *= gelu_slope(from16(uint16_t(zw[i / 2] >> ((i & 1) * 16)), fp16));
+    }
+    if (KIND == GR_LORA && a.bias) {
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(a.bias + f));
+        s[0] += b.x, s[1] += b.y, s[2] += b.z, s[3] += b.w;
+    }
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+        make_uint2(pack16(s[0], s[1], fp16), pack16(s[2], s[3], fp16));
+}
+
+// The pieces of a divided tile added in worker order and finished (all kinds but WGRAD).  A warp takes whole columns,
+// that is rows of the batch: a lane 4 neighbouring features, so the loads are 512 bytes a warp and the stores whole
+// rows, and nothing needs turning.  Two columns of several pieces are in flight.
+template <int KIND>
+__device__ __forceinline__ void finish_pieces(const GroupedArgs &a, const Tile &w, const Pieces &pc, int e, int lane) {
+    constexpr int kWarps = epi_warps(KIND), kFly = KIND == GR_SHRINK ? 4 : 6;
+    const int f = w.f0 + 4 * lane;
+    if (f >= a.F) return;
+    for (int j = e; j < w.n; j += 2 * kWarps) {
+        const size_t at = size_t(j) * kFB + 4 * lane;
+        const bool two = j + kWarps < w.n;
+        float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int k = 0; k <= pc.more; k += kFly) {
+            float4 x[kFly][2];
+#pragma unroll
+            for (int i = 0; i < kFly; ++i) {
+                const float *p = (k + i == 0 ? pc.p0 : pc.p + (k + i - 1) * pc.step) + at;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    x[i][h] = k + i <= pc.more && (h == 0 || two)
+                                  ? __ldcg(reinterpret_cast<const float4 *>(p + h * kWarps * kFB))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < kFly; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    s[h].x += x[i][h].x, s[h].y += x[i][h].y, s[h].z += x[i][h].z, s[h].w += x[i][h].w;
         }
+        finish_row<KIND>(a, w, w.col0 + j, f, s[0]);
+        if (two) finish_row<KIND>(a, w, w.col0 + j + kWarps, f, s[1]);
     }
 }
 
 // LORA, a tile with rows of several requests: the adapters' second product on the CUDA cores, in fp32.  Each row takes
 // its own adapter's B and nothing of another's, so a NaN in an adapter stays with its requests.
+// The adapter of a row of the batch: its request is the last that starts at or before it.
+__device__ __forceinline__ int adapter_of(const Table &tab, int groups, int row) {
+    int lo = 0, hi = groups - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tab.off[mid] <= row) lo = mid;
+        else hi = mid - 1;
+    }
+    return tab.ad[lo];
+}
 // x: this lane's 8 features (from f on) of one row; four lanes cover a row's 32 features, eight rows go side by side
 // with an adapter each, and lanes of one adapter read the same addresses.
-template <int kFly>  // ranks of B in flight
-__device__ __forceinline__ void add_low_rank(float (&x)[8], const GroupedArgs &a, int row, int f) {
+__device__ __forceinline__ void add_low_rank(float (&x)[8], const GroupedArgs &a, int ad, int row, int f) {
+    if (ad < 0) return;
     const int rank = a.rank;
     const bool fp16 = a.fp16 != 0;
-    const int ad = __ldcg(a.row_adapter + row);
-    if (ad < 0) return;
-    const uint16_t *h = static_cast<const uint16_t *>(a.low) + size_t(row) * (2 * rank);
     const uint16_t *b = static_cast<const uint16_t *>(a.lora_b) + size_t(ad) * rank * a.F + f;
+    const uint16_t *h = static_cast<const uint16_t *>(a.low) + size_t(row) * (2 * rank);
+#pragma unroll 1
     for (int r = 0; r < rank; r += 8) {
+        uint4 bv[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) bv[k] = __ldg(reinterpret_cast<const uint4 *>(b + size_t(r + k) * a.F));
+        float hk[8];
         const uint4 up = __ldcg(reinterpret_cast<const uint4 *>(h + r));
         const uint4 rest = __ldcg(reinterpret_cast<const uint4 *>(h + rank + r));
         const uint32_t uw[4] = {up.x, up.y, up.z, up.w}, lw[4] = {rest.x, rest.y, rest.z, rest.w};
-        uint4 bv[kFly];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            hk[k] = from16(uint16_t(uw[k / 2] >> ((k & 1) * 16)), fp16) +
+                    from16(uint16_t(lw[k / 2] >> ((k & 1) * 16)), fp16);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            if (k % kFly == 0) {
-#pragma unroll
-                for (int l = 0; l < kFly; ++l)
-                    bv[l] = __ldg(reinterpret_cast<const uint4 *>(b + size_t(r + k + l) * a.F));
-            }
-            const uint32_t sh = (k & 1) * 16;
-            const float hk = from16(uint16_t(uw[k / 2] >> sh), fp16) + from16(uint16_t(lw[k / 2] >> sh), fp16);
-            const uint32_t w[4] = {bv[k % kFly].x, bv[k % kFly].y, bv[k % kFly].z, bv[k % kFly].w};
+            const uint32_t w[4] = {bv[k].x, bv[k].y, bv[k].z, bv[k].w};
 #pragma unroll
             for (int p = 0; p < 4; ++p)
-                ptx::fma2(x[2 * p], x[2 * p + 1], hk, hk, from16(uint16_t(w[p]), fp16),
+                ptx::fma2(x[2 * p], x[2 * p + 1], hk[k], hk[k], from16(uint16_t(w[p]), fp16),
                           from16(uint16_t(w[p] >> 16), fp16), x[2 * p], x[2 * p + 1]);
         }
     }
 }
 
-// SHRINK, short requests: H on the CUDA cores, by the warps from 2 on (192 threads).  A unit is a request and 8 ranks:
-// a thread takes 8 rows of A at a time for up to 4 rows of X, the sums are folded over the warp, then over the warps,
-// in a fixed order.  (As tiles, a request of one row took a copy of 64 rows of 32 bytes per block at rank 16, some 640
-// cycles of copy engine each.)
-__device__ void shrink_short(const GroupedArgs &a, const Table &tab, float *sums) {
+// SHRINK, short requests: H on the CUDA cores, in fp32, by the warps from 2 on (192 threads).  A unit is a request, up
+// to 64 ranks and one of low_split parts of the contraction (added by the last to arrive): neighbouring lanes take
+// neighbouring 16-byte pieces of A's rows, six of them in flight, for up to 4 rows of X at a time; the sums are
+// folded over the lanes of equal ranks, then over the warps, in a fixed order.  (As tiles, a request of one row took
+// a copy of 64 rows of 32 bytes per block at rank 16, some 640 cycles of copy engine each.)
+__device__ void shrink_short(const GroupedArgs &a, const Table &tab, float *sums, volatile uint32_t *verdict) {
     const int tid = threadIdx.x - 64, lane = tid & 31, warp = tid >> 5;
-    const int chunks = a.F / 8;
+    const int chunks = (a.F + 63) / 64;
     const bool fp16 = a.fp16 != 0;
-    for (int u = blockIdx.x; u < a.groups * chunks; u += gridDim.x) {
-        const int s = u / chunks, r0 = (u - s * chunks) * 8;
-        const int lo = tab.off[s], rows = tab.off[s + 1] - lo, ad = tab.ad[s];
+    const int span = ((a.C / 8 + a.low_split - 1) / a.low_split) * 8;
+    for (int u = blockIdx.x; u < a.groups * chunks * a.low_split; u += gridDim.x) {
+        const int part = u % a.low_split, uc = u / a.low_split;
+        const int s = uc / chunks, r0 = (uc - s * chunks) * 64;
+        const int lo = tab.off[s];
+        // (one for the warp, and known to be: see the group table on shuffles)
+        const int rows = __shfl_sync(0xffffffffu, tab.off[s + 1] - lo, 0), ad = __shfl_sync(0xffffffffu, tab.ad[s], 0);
         if (ad < 0 || rows == 0 || rows > kShortRows) continue;
-        const uint16_t *wa = static_cast<const uint16_t *>(a.lora_a) + size_t(ad) * a.C * a.F + r0;
+        // pieces of 8 ranks in a row of the unit: lane = (row of A) * 2^shift + piece
+        const int pieces = min(a.F - r0, 64) / 8;
+        const int shift = pieces > 4 ? 3 : pieces > 2 ? 2 : pieces - 1;
+        const int piece = lane & ((1 << shift) - 1);
+        const bool live = piece < pieces;
+        const int step = (kShortWarps * 32) >> shift;  // rows of A side by side
+        const uint16_t *wa = static_cast<const uint16_t *>(a.lora_a) + size_t(ad) * a.C * a.F + r0 + (live ? piece * 8 : 0);
+        const int k_end = min(a.C, (part + 1) * span);
         for (int t0 = 0; t0 < rows; t0 += 4) {
             const uint16_t *x = static_cast<const uint16_t *>(a.x) + size_t(lo + t0) * a.C;
             float acc[32];  // [row][rank]
 #pragma unroll
             for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-            for (int k = tid * 8; k < a.C; k += kShortWarps * 32 * 8) {
-                uint4 w[8];
+            constexpr int kFly = 6;
+#pragma unroll 1
+            for (int k = part * span + (tid >> shift); k < k_end; k += kFly * step) {
+                uint4 w[kFly];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(wa + size_t(k + i) * a.F));
+                for (int i = 0; i < kFly; ++i)
+                    w[i] = k + i * step < k_end ? __ldg(reinterpret_cast<const uint4 *>(wa + size_t(k + i * step) * a.F))
+                                                : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (t0 + j >= rows) continue;
-                    const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(x + size_t(j) * a.C + k));
-                    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                    uint16_t xs[kFly];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float xs = from16(uint16_t(xw[i / 2] >> ((i & 1) * 16)), fp16);
+                    for (int i = 0; i < kFly; ++i)
+                        xs[i] = k + i * step < k_end ? __ldg(x + size_t(j) * a.C + k + i * step) : uint16_t(0);
+#pragma unroll
+                    for (int i = 0; i < kFly; ++i) {
+                        const float xv = from16(xs[i], fp16);
                         const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
                         for (int p = 0; p < 4; ++p)
-                            ptx::fma2(acc[8 * j + 2 * p], acc[8 * j + 2 * p + 1], xs, xs, from16(uint16_t(ww[p]), fp16),
+                            ptx::fma2(acc[8 * j + 2 * p], acc[8 * j + 2 * p + 1], xv, xv, from16(uint16_t(ww[p]), fp16),
                                       from16(uint16_t(ww[p] >> 16), fp16), acc[8 * j + 2 * p], acc[8 * j + 2 * p + 1]);
                     }
                 }
             }
-            // fold over the lanes: each step halves the values a lane keeps, lane l ends with value l
+            // lanes of one piece, then the warps: sums[warp][row][rank of the unit]
+            __syncwarp();
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) {
+            for (int d = 16; d >= 1; d >>= 1) {
 #pragma unroll
-                for (int i = 0; i < d; ++i) {
-                    const bool upper = lane & d;
-                    const float give = upper ? acc[i] : acc[i + d];
-                    const float keep = upper ? acc[i + d] : acc[i];
-                    acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+                for (int i = 0; i < 32; ++i) {
+                    const float o = __shfl_xor_sync(0xffffffffu, acc[i], d);
+                    acc[i] = d >= (1 << shift) ? acc[i] + o : acc[i];
                 }
             }
-            sums[warp * 32 + lane] = acc[0];
-            ptx::named_bar_sync(4, kShortWarps * 32);
-            if (warp == 0 && t0 + (lane >> 3) < rows) {
-                float h = 0.f;
+            if (lane < (1 << shift) && live) {
 #pragma unroll
-                for (int i = 0; i < kShortWarps; ++i) h += sums[i * 32 + lane];
-                if (a.scale) h *= __ldg(a.scale + ad);
-                store_low(a, lo + t0 + (lane >> 3), r0 + (lane & 7), h);
+                for (int i = 0; i < 32; ++i) sums[(warp * 4 + i / 8) * 64 + piece * 8 + (i & 7)] = acc[i];
+            }
+            ptx::named_bar_sync(4, kShortWarps * 32);
+            for (int i = tid; i < 4 * pieces * 8; i += kShortWarps * 32) {
+                const int j = i / (pieces * 8), r = i - j * pieces * 8;
+                if (t0 + j < rows) {
+                    float h = 0.f;
+#pragma unroll
+                    for (int g = 0; g < kShortWarps; ++g) h += sums[(g * 4 + j) * 64 + r];
+                    if (a.low_split > 1)
+                        __stcg(a.low_parts + (size_t(uc) * a.low_split + part) * (kShortRows * 64) + (t0 + j) * 64 + r, h);
+                    else
+                        store_low(a, lo + t0 + j, r0 + r, a.scale ? h * __ldg(a.scale + ad) : h);
+                }
+            }
+            ptx::named_bar_sync(4, kShortWarps * 32);
+        }
+        if (a.low_split > 1) {  // the parts, added in order by whoever comes last
+            if (tid == 0) {
+                const bool last = ptx::atom_add_acq_rel_gpu(a.low_counters + uc, 1u) == uint32_t(a.low_split - 1);
+                if (last) ptx::st_relaxed_gpu(a.low_counters + uc, 0u);
+                *verdict = last;
+            }
+            ptx::named_bar_sync(4, kShortWarps * 32);
+            if (*verdict != 0u) {
+                const float sc = a.scale ? __ldg(a.scale + ad) : 1.f;
+                for (int i = tid; i < rows * pieces * 8; i += kShortWarps * 32) {
+                    const int j = i / (pieces * 8), r = i - j * pieces * 8;
+                    const float *p = a.low_parts + size_t(uc) * a.low_split * (kShortRows * 64) + j * 64 + r;
+                    float x[kLoraMaxSplit], h = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kLoraMaxSplit; ++k)
+                        x[k] = k < a.low_split ? __ldcg(p + k * (kShortRows * 64)) : 0.f;
+#pragma unroll
+                    for (int k = 0; k < kLoraMaxSplit; ++k) h += x[k];
+                    store_low(a, lo + j, r0 + r, h * sc);
+                }
             }
             ptx::named_bar_sync(4, kShortWarps * 32);
         }
     }
-    // the adapter of each row, for the tiles of several requests
-    for (int s = blockIdx.x; s < a.groups; s += gridDim.x)
-        for (int r = tab.off[s] + tid; r < tab.off[s + 1]; r += kShortWarps * 32) a.row_adapter[r] = tab.ad[s];
 }
 
 template <bool kPair>
@@ -685,6 +827,12 @@ __device__ __forceinline__ void issue_commit(uint32_t bar) {
     if constexpr (kPair) ptx::mma_commit_pair_mc(bar, 3);
     else ptx::mma_commit(bar);
 }
+// the 32-column fragment behind c of those that a half takes: spans of kSpan columns, one of kHalves
+template <int kSpan, int kHalves>
+__device__ __forceinline__ int next_fragment(int c) {
+    return kSpan == 64 && (c & 32) == 0 ? c + 32 : c + 32 + (kHalves - 1) * kSpan;
+}
+
 // The copies of block kb into a stage, completing on `bar` (kShared: a barrier of either CTA of the pair)
 template <int KIND, bool kShared>
 __device__ __forceinline__ void stage_loads(const GroupedArgs &a, const Tile &w, uint32_t sa, uint32_t sb, uint32_t bar,
@@ -737,7 +885,8 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
         if (threadIdx.x == 0) ptx::record_error(a.err, 8u, 0x60000000u | (base & 1023u));
         return;
     }
-    constexpr int kEpiWarps = epi_warps(KIND), kThreads = threads_of(KIND), kHalves = kEpiWarps / 4;
+    constexpr int kEpiWarps = epi_warps(KIND), kThreads = threads_of(KIND), kHalves = kEpiWarps / 4,
+                  kSpan = KIND == GR_WGRAD ? 64 : 32;
     constexpr bool kAMn = KIND != GR_DGRAD;  // features contiguous in memory: A is MN-major
     constexpr bool kBMn = KIND == GR_WGRAD;
     const int stages = a.stages;
@@ -1011,31 +1160,44 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
         const int half = e >> 2;
         const int q = warp & 3;
         const bool fp16 = a.fp16 != 0;
-        if constexpr (KIND == GR_SHRINK) shrink_short(a, tab, reinterpret_cast<float *>(smem_raw + L.stg));
+        if constexpr (KIND == GR_SHRINK) shrink_short(a, tab, reinterpret_cast<float *>(smem_raw + L.stg), misc + 4);
         for (int tile = 0; e < kEpiWarps && walk.next(w); ++tile) {
             const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
             uint4 zv[4];  // DGRAD: the next fragment's pre-activations, on their way before the accumulator is ready
             if constexpr (KIND == GR_DGRAD)
                 if (a.preact && half * 32 < w.n && w.whole()) load_fragment(zv, a, w, half * 32, q, lane, true);
-            const bool ok = ptx::mbar_wait_bounded(B.tmem_full0 + 8 * buf, tph, tmo, abort, a.err, kInfoEpi | buf);
-            ptx::tc_fence_after();
-            const uint32_t tacc = tmem_base + (uint32_t(q * 32) << 16) + buf * uint32_t(a.bn);
-            const int f = w.f0 + q * 32 + lane;
-            const bool live = f < a.F && ok;
-            bool held = true;  // the accumulator is still this tile's
             // LORA, a tile of several requests: this worker adds the low-rank product of every parts-th eight rows
             int parts = 0, part = 0;
             if constexpr (KIND == GR_LORA) {
                 if (w.ad == -2 && a.nweights > 0) {
                     parts = w.last - w.first + 1;
                     part = worker - w.first;
-                    ptx::griddep_wait();  // H is the previous grid's
+                    // B's slices on their way to L2 while the projection is multiplied
+                    for (int c = half * 32; c < w.n; c += 64) {
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = c + (lane >> 2) + 8 * i;
+                            if ((c / 8 + i) % parts != part || j >= w.n) continue;
+                            const int ad = adapter_of(tab, a.groups, w.col0 + j);
+                            const int f8 = w.f0 + q * 32 + (lane & 3) * 8;
+                            if (ad < 0 || f8 >= a.F) continue;
+                            const uint16_t *b = static_cast<const uint16_t *>(a.lora_b) + size_t(ad) * a.rank * a.F + f8;
+                            for (int r = lane & 3; r < a.rank; r += 4)
+                                ptx::prefetch_l2(b + size_t(r) * a.F - (lane & 3) * 8);
+                        }
+                    }
                 }
             }
+            const bool ok = ptx::mbar_wait_bounded(B.tmem_full0 + 8 * buf, tph, tmo, abort, a.err, kInfoEpi | buf);
+            ptx::tc_fence_after();
+            if (KIND == GR_LORA && parts > 0) ptx::griddep_wait();  // H is the previous grid's
+            const uint32_t tacc = tmem_base + (uint32_t(q * 32) << 16) + buf * uint32_t(a.bn);
+            const int f = w.f0 + q * 32 + lane;
+            const bool live = f < a.F && ok;
+            bool held = true;  // the accumulator is still this tile's
             if (!kPair && !w.whole()) {
                 // a piece of the tile: to the workspace, [column][lane]; the last to arrive goes on with the sum
                 float *const mine = a.partials + size_t(2 * worker + w.slot) * size_t(kFB * a.bn) + q * 32 + lane;
-                for (int c = half * 32; c < w.n; c += 32 * kHalves) {
+                for (int c = half * kSpan; c < w.n; c = next_fragment<kSpan, kHalves>(c)) {
                     uint32_t v[32];
                     ptx::tmem_ld32(tacc + uint32_t(c), v);
                     ptx::tmem_ld_wait();
@@ -1052,8 +1214,9 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                                 if ((lane >> 2) + 8 * i >= cols || f8 >= a.F) continue;
                                 float x[8];
                                 turned(x, stg, lane, i);
+                                const int row = w.col0 + c + (lane >> 2) + 8 * i;
                                 if ((c / 8 + i) % parts == part)
-                                    add_low_rank<8>(x, a, w.col0 + c + (lane >> 2) + 8 * i, f8);
+                                    add_low_rank(x, a, adapter_of(tab, a.groups, row), row, f8);
                                 float4 *d = reinterpret_cast<float4 *>(p);
                                 __stcg(d, make_float4(x[0], x[1], x[2], x[3]));
                                 __stcg(d + 1, make_float4(x[4], x[5], x[6], x[7]));
@@ -1080,17 +1243,19 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                 }
                 ptx::named_bar_sync(3, kEpiWarps * 32);
                 if (*verdict == 0u) continue;
-                parts = 0;  // the pieces hold it
-                if constexpr (KIND == GR_DGRAD)
-                    if (a.preact && half * 32 < w.n) load_fragment(zv, a, w, half * 32, q, lane, true);
+                if constexpr (KIND != GR_WGRAD) {
+                    finish_pieces<KIND>(a, w, pieces_of(a, walk, w), e, lane);
+                    continue;
+                }
             }
-            for (int c = half * 32; c < w.n; c += 32 * kHalves) {
+            // (WGRAD: the halves take alternate 64-column blocks)
+            for (int c = half * kSpan; c < w.n; c = next_fragment<kSpan, kHalves>(c)) {
                 uint32_t v[32];
-                if (kPair || w.whole()) {
+                if (kPair || KIND != GR_WGRAD || w.whole()) {
                     ptx::tmem_ld32(tacc + uint32_t(c), v);
                     ptx::tmem_ld_wait();
                 } else {
-                    sum_pieces(v, a, walk, w, c, q * 32 + lane);
+                    sum_pieces(v, pieces_of(a, walk, w), c, w.n, q * 32 + lane);
                 }
                 const int cols = min(32, w.n - c);
                 if constexpr (KIND == GR_LORA) {
@@ -1110,7 +1275,8 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                         if ((lane >> 2) + 8 * i >= cols || f8 >= a.F || !ok) continue;
                         float x[8];
                         turned(x, stg, lane, i);
-                        if (parts > 0) add_low_rank<8>(x, a, w.col0 + c + (lane >> 2) + 8 * i, f8);
+                        const int row = w.col0 + c + (lane >> 2) + 8 * i;
+                        if (parts > 0) add_low_rank(x, a, adapter_of(tab, a.groups, row), row, f8);
                         uint32_t p[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -1157,21 +1323,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                     for (int j = 0; j < 32; ++j)
                         if (live && j < cols) store_low(a, w.col0 + c + j, f, sc * __uint_as_float(v[j]));
                 } else if constexpr (KIND == GR_WGRAD) {
-                    if (live) {
-                        uint16_t *y = static_cast<uint16_t *>(a.out) + (size_t(w.g) * a.F + f) * a.N + w.col0 + c;
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            if (j < cols) {  // N is a multiple of 8
-                                uint32_t p[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)  // an empty group's sum is zero
-                                    p[i] = w.nk == 0 ? 0u
-                                                     : pack16(__uint_as_float(v[j + 2 * i]),
-                                                              __uint_as_float(v[j + 2 * i + 1]), fp16);
-                                *reinterpret_cast<uint4 *>(y + j) = make_uint4(p[0], p[1], p[2], p[3]);
-                            }
-                        }
-                    }
+                    store_columns(v, a, w, c, reinterpret_cast<uint4 *>(smem_raw + L.stg + e * 4096), q, lane, ok);
                 }
             }
             ptx::tc_fence_before();
