@@ -136,7 +136,8 @@ struct Plan {
     int workers;    // that take part
     int tiles;
     int units;      // split: blocks of all tiles
-    int base, rem;  // split: a worker's stretch is base blocks, of the first rem workers one more
+    int ways;       // split: stretches of each tile, or 0 where they run over tiles:
+    int base, rem;  // then a worker's stretch is base blocks, of the first rem workers one more
     int groups;     // LORA: long requests and runs of short ones; else the groups
 };
 static_assert(sizeof(Plan) <= 32, "table layout");
@@ -188,8 +189,18 @@ struct Walk {
     static constexpr int kTileF = kPair ? 2 * kFB : kFB;
     // columns are multiplied in 16s; each half of a pair's in 16s (WGRAD: whole 64-column blocks)
     static constexpr int kGran = kPair ? (KIND == GR_WGRAD ? 128 : 32) : 16;
-    __device__ int unit_of(int w) const { return w * plan.base + min(w, plan.rem); }
+    __device__ int unit_of(int w) const {
+        if (plan.ways != 0) {
+            const int t = w / plan.ways;
+            return t * nkc + (w - t * plan.ways) * nkc / plan.ways;
+        }
+        return w * plan.base + min(w, plan.rem);
+    }
     __device__ int worker_of(int u) const {
+        if (plan.ways != 0) {
+            const int t = u / nkc;
+            return t * plan.ways + ((u - t * nkc + 1) * plan.ways - 1) / nkc;
+        }
         const int wide = plan.rem * (plan.base + 1);
         return u < wide ? u / (plan.base + 1) : plan.rem + (u - wide) / plan.base;
     }
@@ -502,7 +513,7 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
         p.split = 0;
         p.workers = workers;
         p.tiles = KIND == GR_WGRAD ? ngroups * per_tile : carry;
-        p.units = p.base = p.rem = 0;
+        p.units = p.ways = p.base = p.rem = 0;
         p.groups = ngroups;
         const bool few = KIND == GR_WGRAD ? ngroups <= kGroupedSplitTiles && per_tile <= kGroupedSplitTiles &&
                                                 p.tiles <= kGroupedSplitTiles && carry <= kMost
@@ -514,12 +525,23 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
             const int rounds = (p.tiles + workers - 1) / workers;
             // WGRAD: of mean tiles, or the longest one
             const int whole = KIND == GR_WGRAD ? max(rounds * ((units + p.tiles - 1) / p.tiles), longest) : rounds * nkc;
-            if (whole > stretch + 8 + a.bn / 32) {
+            // Equal parts of every tile, where there are workers for two at least: a worker then has one piece, not the
+            // end of one tile and the start of another, each of which costs what adding a piece costs.
+            const int most = KIND == GR_WGRAD ? 0 : min(workers / p.tiles, nkc / kMinStretch);
+            const int adding = 8 + a.bn / 32;
+            const int even = most >= 2 ? (nkc + most - 1) / most + adding : 1 << 30;
+            const int mixed = stretch + adding + adding / 2;
+            if (whole > min(even, mixed)) {
                 p.split = 1;
-                p.workers = stretch == share ? workers : max(units / stretch, 1);
                 p.units = units;
-                p.base = units / p.workers;
-                p.rem = units - p.base * p.workers;
+                if (even <= mixed) {
+                    p.ways = most;
+                    p.workers = p.tiles * most;
+                } else {
+                    p.workers = stretch == share ? workers : max(units / stretch, 1);
+                    p.base = units / p.workers;
+                    p.rem = units - p.base * p.workers;
+                }
             }
         }
         *tab.plan = p;
@@ -705,11 +727,66 @@ __device__ __forceinline__ void add_low_rank(float (&x)[8], const GroupedArgs &a
     }
 }
 
+// One lane's share of a short request: rows of A (8 ranks, a 16-byte piece) `step` apart, `left` rows until the end,
+// against up to kRows rows of X; the lanes of a warp that hold the same ranks are then added, in a fixed order, into
+// sums[row][64].  kFly pieces in flight: one row takes fewer registers for its sums, so more loads (beside the
+// projection, which saturates HBM at the same time, each turn of the loop costs about 2000 cycles).
+template <int kRows, int kFly>
+__device__ __forceinline__ void short_sums(const GroupedArgs &a, const uint16_t *wa, const uint16_t *x, int left, int step,
+                                           int rows, int shift, int lane, float *sums, bool live) {
+    const bool fp16 = a.fp16 != 0;
+    float acc[8 * kRows];
+#pragma unroll
+    for (int i = 0; i < 8 * kRows; ++i) acc[i] = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < left; k += kFly * step) {
+        uint4 w[kFly];
+        uint16_t xs[kFly];
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) {
+            const bool in = k + i * step < left;
+            w[i] = in ? __ldg(reinterpret_cast<const uint4 *>(wa + size_t(k + i * step) * a.F)) : make_uint4(0u, 0u, 0u, 0u);
+            xs[i] = in ? __ldg(x + k + i * step) : uint16_t(0);
+        }
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            if (j >= rows) break;
+            if (j > 0) {
+#pragma unroll
+                for (int i = 0; i < kFly; ++i)
+                    xs[i] = k + i * step < left ? __ldg(x + size_t(j) * a.C + k + i * step) : uint16_t(0);
+            }
+#pragma unroll
+            for (int i = 0; i < kFly; ++i) {
+                const float xv = from16(xs[i], fp16);
+                const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    ptx::fma2(acc[8 * j + 2 * p], acc[8 * j + 2 * p + 1], xv, xv, from16(uint16_t(ww[p]), fp16),
+                              from16(uint16_t(ww[p] >> 16), fp16), acc[8 * j + 2 * p], acc[8 * j + 2 * p + 1]);
+            }
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+#pragma unroll
+        for (int i = 0; i < 8 * kRows; ++i) {
+            const float o = __shfl_xor_sync(0xffffffffu, acc[i], d);
+            acc[i] = d >= (1 << shift) ? acc[i] + o : acc[i];
+        }
+    }
+    if (lane < (1 << shift) && live) {
+#pragma unroll
+        for (int i = 0; i < 8 * kRows; ++i) sums[(i / 8) * 64 + (i & 7)] = acc[i];
+    }
+}
+
 // SHRINK, short requests: H on the CUDA cores, in fp32, by the warps from 2 on (192 threads).  A unit is a request, up
 // to 64 ranks and one of low_split parts of the contraction (added by the last to arrive): neighbouring lanes take
-// neighbouring 16-byte pieces of A's rows, six of them in flight, for up to 4 rows of X at a time; the sums are
-// folded over the lanes of equal ranks, then over the warps, in a fixed order.  (As tiles, a request of one row took
-// a copy of 64 rows of 32 bytes per block at rank 16, some 640 cycles of copy engine each.)
+// neighbouring 16-byte pieces of A's rows, for up to 4 rows of X at a time; the sums are folded over the lanes of equal
+// ranks, then over the warps.  (As tiles, a request of one row took a copy of 64 rows of 32 bytes per block at rank
+// 16, some 640 cycles of copy engine each.)
 __device__ void shrink_short(const GroupedArgs &a, const Table &tab, float *sums, volatile uint32_t *verdict) {
     const int tid = threadIdx.x - 64, lane = tid & 31, warp = tid >> 5;
     const int chunks = (a.F + 63) / 64;
@@ -732,49 +809,10 @@ __device__ void shrink_short(const GroupedArgs &a, const Table &tab, float *sums
         const int k_end = min(a.C, (part + 1) * span);
         for (int t0 = 0; t0 < rows; t0 += 4) {
             const uint16_t *x = static_cast<const uint16_t *>(a.x) + size_t(lo + t0) * a.C;
-            float acc[32];  // [row][rank]
-#pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-            constexpr int kFly = 6;
-#pragma unroll 1
-            for (int k = part * span + (tid >> shift); k < k_end; k += kFly * step) {
-                uint4 w[kFly];
-#pragma unroll
-                for (int i = 0; i < kFly; ++i)
-                    w[i] = k + i * step < k_end ? __ldg(reinterpret_cast<const uint4 *>(wa + size_t(k + i * step) * a.F))
-                                                : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (t0 + j >= rows) continue;
-                    uint16_t xs[kFly];
-#pragma unroll
-                    for (int i = 0; i < kFly; ++i)
-                        xs[i] = k + i * step < k_end ? __ldg(x + size_t(j) * a.C + k + i * step) : uint16_t(0);
-#pragma unroll
-                    for (int i = 0; i < kFly; ++i) {
-                        const float xv = from16(xs[i], fp16);
-                        const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                        for (int p = 0; p < 4; ++p)
-                            ptx::fma2(acc[8 * j + 2 * p], acc[8 * j + 2 * p + 1], xv, xv, from16(uint16_t(ww[p]), fp16),
-                                      from16(uint16_t(ww[p] >> 16), fp16), acc[8 * j + 2 * p], acc[8 * j + 2 * p + 1]);
-                    }
-                }
-            }
-            // lanes of one piece, then the warps: sums[warp][row][rank of the unit]
-            __syncwarp();
-#pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float o = __shfl_xor_sync(0xffffffffu, acc[i], d);
-                    acc[i] = d >= (1 << shift) ? acc[i] + o : acc[i];
-                }
-            }
-            if (lane < (1 << shift) && live) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) sums[(warp * 4 + i / 8) * 64 + piece * 8 + (i & 7)] = acc[i];
-            }
+            const int k0 = part * span + (tid >> shift);
+            const uint16_t *row = wa + size_t(k0) * a.F;
+            if (rows == 1) short_sums<1, 12>(a, row, x + k0, k_end - k0, step, 1, shift, lane, sums + warp * 256 + piece * 8, live);
+            else short_sums<4, 6>(a, row, x + k0, k_end - k0, step, rows - t0, shift, lane, sums + warp * 256 + piece * 8, live);
             ptx::named_bar_sync(4, kShortWarps * 32);
             for (int i = tid; i < 4 * pieces * 8; i += kShortWarps * 32) {
                 const int j = i / (pieces * 8), r = i - j * pieces * 8;
