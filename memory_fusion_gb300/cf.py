@@ -207,8 +207,9 @@ def _ptr(x):
         return None
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
+    f = getattr(x, "data_ptr", None)
+    if f is not None:
+        return f()
     raise TypeError(f"cannot pass {type(x)} as a pointer")
 
 
@@ -710,24 +711,32 @@ def cf_gemm_lora(X, W, bias, A, B, offsets, adapters, scale, Y, T, N, K, S, L, R
 
 
 def _operand(name, t, shape, dtype, device):
-    """Check one tensor argument; sizes of None in `shape` are free."""
+    """Check one tensor argument against its whole shape."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
-    if t.dim() != len(shape) or any(n is not None and int(s) != int(n) for s, n in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple('*' if n is None else n for n in shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    raise ValueError(f"{name} is not contiguous")
+
+
+def _sizes(name, t, dims):
+    """The sizes of a tensor that has to have `dims` of them."""
+    if t.dim() != dims:
+        raise ValueError(f"{name} has {t.dim()} dimensions, not {dims}")
+    return t.shape
 
 
 def _grouped_dtype(name, t):
     import torch
     if t.device.type != "cuda":
         raise ValueError(f"{name} is on {t.device}, not on a CUDA device")
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return CF_BF16
-    if t.dtype == torch.float16:
+    if t.dtype is torch.float16:
         return CF_FP16
     raise ValueError(f"{name} has dtype {t.dtype}, not bfloat16 or float16")
 
@@ -746,6 +755,23 @@ def _launch_on(device, stream):
                 yield
 
 
+def _run(what, call, device, stream, out, shape, dtype, workspace, nbytes):
+    """call(out, workspace, its bytes, stream handle) on the operands' device, with the output and the workspace made
+    where none are given; the output."""
+    import torch
+    index = device.index
+    if stream is None and index == torch.cuda.current_device():  # nothing to switch: the decode step's path
+        Y = out if out is not None else torch.empty(shape, dtype=dtype, device=device)
+        ws = workspace if workspace is not None else new_workspace(nbytes(), device)
+        check(call(Y, ws, ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(index)), what)
+        return Y
+    with _launch_on(device, stream):
+        Y = out if out is not None else torch.empty(shape, dtype=dtype, device=device)
+        ws = workspace if workspace is not None else new_workspace(nbytes(), device)
+        check(call(Y, ws, ws.numel() * ws.element_size(), torch.cuda.current_stream().cuda_stream), what)
+    return Y
+
+
 def _act(act):
     acts = {"none": CF_ACT_NONE, "gelu_tanh": CF_ACT_GELU_TANH}
     if act not in acts:
@@ -758,65 +784,58 @@ def grouped_gemm(X, W, offsets, *, act="none", preact=None, out=None, workspace=
     CUDA tensors, offsets int32 [E + 1] on the same device.  `preact` ([T, N]) receives the unactivated product for
     grouped_gemm_dgrad.  Rows of no group are not written: in a new output they hold anything."""
     import torch
-    dt, dev = _grouped_dtype("X", X), X.device
+    dt, dev, dtype = _grouped_dtype("X", X), X.device, X.dtype
     a = _act(act)
-    _operand("X", X, (None, None), X.dtype, dev)
-    T, K = X.shape
-    _operand("W", W, (None, K, None), X.dtype, dev)
-    E, _, N = W.shape
+    T, K = _sizes("X", X, 2)
+    E, _, N = _sizes("W", W, 3)
+    _operand("X", X, (T, K), dtype, dev)
+    _operand("W", W, (E, K, N), dtype, dev)
     _operand("offsets", offsets, (E + 1,), torch.int32, dev)
-    for name, t in (("preact", preact), ("out", out)):
-        if t is not None:
-            _operand(name, t, (T, N), X.dtype, dev)
-    with _launch_on(dev, stream):
-        Y = out if out is not None else torch.empty((T, N), dtype=X.dtype, device=dev)
-        ws = workspace if workspace is not None else new_workspace(cf_grouped_gemm_workspace_size(T, N, K, E), dev)
-        check(cf_grouped_gemm(X, W, offsets, Y, preact, T, N, K, E, dt, a, ws, ws.numel(), None, tuning),
-              "cf_grouped_gemm")
-    return Y
+    if preact is not None:
+        _operand("preact", preact, (T, N), dtype, dev)
+    if out is not None:
+        _operand("out", out, (T, N), dtype, dev)
+    return _run("cf_grouped_gemm",
+                lambda Y, ws, n, s: cf_grouped_gemm(X, W, offsets, Y, preact, T, N, K, E, dt, a, ws, n, s, tuning),
+                dev, stream, out, (T, N), dtype, workspace, lambda: cf_grouped_gemm_workspace_size(T, N, K, E))
 
 
 def grouped_gemm_dgrad(dY, W, offsets, *, preact=None, out=None, workspace=None, stream=None, tuning=None):
     """dX[r] = (dY[r] @ W[e].T) * gelu_tanh'(preact[r]) for the rows of each group; dY [T, N], W [E, K, N],
     preact [T, K] or None (no activation before these rows).  out may be preact."""
     import torch
-    dt, dev = _grouped_dtype("dY", dY), dY.device
-    _operand("dY", dY, (None, None), dY.dtype, dev)
-    T, N = dY.shape
-    _operand("W", W, (None, None, N), dY.dtype, dev)
-    E, K, _ = W.shape
+    dt, dev, dtype = _grouped_dtype("dY", dY), dY.device, dY.dtype
+    T, N = _sizes("dY", dY, 2)
+    E, K, _ = _sizes("W", W, 3)
+    _operand("dY", dY, (T, N), dtype, dev)
+    _operand("W", W, (E, K, N), dtype, dev)
     _operand("offsets", offsets, (E + 1,), torch.int32, dev)
-    for name, t in (("preact", preact), ("out", out)):
-        if t is not None:
-            _operand(name, t, (T, K), dY.dtype, dev)
-    with _launch_on(dev, stream):
-        dX = out if out is not None else torch.empty((T, K), dtype=dY.dtype, device=dev)
-        ws = workspace if workspace is not None else new_workspace(cf_grouped_gemm_workspace_size(T, N, K, E), dev)
-        check(cf_grouped_gemm_dgrad(dY, W, offsets, preact, dX, T, N, K, E, dt, ws, ws.numel(), None, tuning),
-              "cf_grouped_gemm_dgrad")
-    return dX
+    if preact is not None:
+        _operand("preact", preact, (T, K), dtype, dev)
+    if out is not None:
+        _operand("out", out, (T, K), dtype, dev)
+    return _run("cf_grouped_gemm_dgrad",
+                lambda dX, ws, n, s: cf_grouped_gemm_dgrad(dY, W, offsets, preact, dX, T, N, K, E, dt, ws, n, s, tuning),
+                dev, stream, out, (T, K), dtype, workspace, lambda: cf_grouped_gemm_workspace_size(T, N, K, E))
 
 
 def grouped_gemm_wgrad(X, dY, offsets, *, out=None, workspace=None, stream=None, tuning=None):
     """dW[e] = X[rows of e].T @ dY[rows of e] (zeros for an empty group), [E, K, N]; X [T, K], dY [T, N]."""
     import torch
-    dt, dev = _grouped_dtype("X", X), X.device
-    _operand("X", X, (None, None), X.dtype, dev)
-    T, K = X.shape
-    _operand("dY", dY, (T, None), X.dtype, dev)
-    N = dY.shape[1]
-    _operand("offsets", offsets, (None,), torch.int32, dev)
-    E = offsets.shape[0] - 1
+    dt, dev, dtype = _grouped_dtype("X", X), X.device, X.dtype
+    T, K = _sizes("X", X, 2)
+    N = _sizes("dY", dY, 2)[1]
+    E = _sizes("offsets", offsets, 1)[0] - 1
     if E < 0:
         raise ValueError("offsets is empty: it has one entry more than there are groups")
+    _operand("X", X, (T, K), dtype, dev)
+    _operand("dY", dY, (T, N), dtype, dev)
+    _operand("offsets", offsets, (E + 1,), torch.int32, dev)
     if out is not None:
-        _operand("out", out, (E, K, N), X.dtype, dev)
-    with _launch_on(dev, stream):
-        dW = out if out is not None else torch.empty((E, K, N), dtype=X.dtype, device=dev)
-        ws = workspace if workspace is not None else new_workspace(cf_grouped_gemm_workspace_size(T, N, K, E), dev)
-        check(cf_grouped_gemm_wgrad(X, dY, offsets, dW, T, N, K, E, dt, ws, ws.numel(), None, tuning),
-              "cf_grouped_gemm_wgrad")
-    return dW
+        _operand("out", out, (E, K, N), dtype, dev)
+    return _run("cf_grouped_gemm_wgrad",
+                lambda dW, ws, n, s: cf_grouped_gemm_wgrad(X, dY, offsets, dW, T, N, K, E, dt, ws, n, s, tuning),
+                dev, stream, out, (E, K, N), dtype, workspace, lambda: cf_grouped_gemm_workspace_size(T, N, K, E))
 
 
 def gemm_lora(X, W, bias, A, B, offsets, adapters, *, scale=None, out=None, workspace=None, stream=None, tuning=None):
@@ -824,26 +843,24 @@ def gemm_lora(X, W, bias, A, B, offsets, adapters, *, scale=None, out=None, work
     [offsets[s], offsets[s+1]), with a = adapters[s] (-1: no adapter).  X [T, K], W [K, N], A [L, K, R], B [L, R, N]
     bf16 or fp16; bias fp32 [N] or None; offsets int32 [S + 1], adapters int32 [S], scale fp32 [L] or None (1)."""
     import torch
-    dt, dev = _grouped_dtype("X", X), X.device
-    _operand("X", X, (None, None), X.dtype, dev)
-    T, K = X.shape
-    _operand("W", W, (K, None), X.dtype, dev)
-    N = W.shape[1]
-    _operand("A", A, (None, K, None), X.dtype, dev)
-    L, _, R = A.shape
-    _operand("B", B, (L, R, N), X.dtype, dev)
-    _operand("adapters", adapters, (None,), torch.int32, dev)
-    S = adapters.shape[0]
+    dt, dev, dtype = _grouped_dtype("X", X), X.device, X.dtype
+    T, K = _sizes("X", X, 2)
+    N = _sizes("W", W, 2)[1]
+    L, _, R = _sizes("A", A, 3)
+    S = _sizes("adapters", adapters, 1)[0]
+    _operand("X", X, (T, K), dtype, dev)
+    _operand("W", W, (K, N), dtype, dev)
+    _operand("A", A, (L, K, R), dtype, dev)
+    _operand("B", B, (L, R, N), dtype, dev)
+    _operand("adapters", adapters, (S,), torch.int32, dev)
     _operand("offsets", offsets, (S + 1,), torch.int32, dev)
     if bias is not None:
         _operand("bias", bias, (N,), torch.float32, dev)
     if scale is not None:
         _operand("scale", scale, (L,), torch.float32, dev)
     if out is not None:
-        _operand("out", out, (T, N), X.dtype, dev)
-    with _launch_on(dev, stream):
-        Y = out if out is not None else torch.empty((T, N), dtype=X.dtype, device=dev)
-        ws = workspace if workspace is not None else new_workspace(cf_gemm_lora_workspace_size(T, N, K, S, R), dev)
-        check(cf_gemm_lora(X, W, bias, A, B, offsets, adapters, scale, Y, T, N, K, S, L, R, dt, ws, ws.numel(), None,
-                           tuning), "cf_gemm_lora")
-    return Y
+        _operand("out", out, (T, N), dtype, dev)
+    return _run("cf_gemm_lora",
+                lambda Y, ws, n, s: cf_gemm_lora(X, W, bias, A, B, offsets, adapters, scale, Y, T, N, K, S, L, R, dt, ws,
+                                                 n, s, tuning),
+                dev, stream, out, (T, N), dtype, workspace, lambda: cf_gemm_lora_workspace_size(T, N, K, S, R))

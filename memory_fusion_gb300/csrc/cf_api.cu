@@ -1426,15 +1426,16 @@ cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int
                 20 * ((F + 255) / 256) <= 11 * ((F + 127) / 128);
     if (t.cluster_m != 0) pair = t.cluster_m == 2;
     if (pair && (kind == cf::GR_SHRINK || bn < 128)) return CF_ERR_UNSUPPORTED;
-    int stages = t.stages > 0 ? t.stages : 8;  // (deeper rings of small stages were slower: 250 rows over 32 groups, 12
+    const int a_blocks = F <= 64 && kind != cf::GR_DGRAD && !pair ? 1 : 2;
+    int stages = t.stages > 0 ? t.stages : kind == cf::GR_SHRINK ? 12 : 8;  // (deeper rings of small stages were slower: 250 rows over 32 groups, 12
                                                // stages 76.9 us, 8 stages 73.2)
     // a decode batch's two adapter products share the SMs: the second reads its weights while the first runs
     const int shrink_room = 98 * 1024, room_smem = bn > 64                ? kMaxSmem
                                                    : kind == cf::GR_SHRINK ? shrink_room
                                                    : kind == cf::GR_LORA   ? kMaxSmem - shrink_room - 2048
                                                                            : kMaxSmem;
-    while (stages > 2 && cf::grouped_smem_bytes(kind, pair, stages, bn, int(groups), int(rank)) > room_smem) --stages;
-    *smem = cf::grouped_smem_bytes(kind, pair, stages, bn, int(groups), int(rank));
+    while (stages > 2 && cf::grouped_smem_bytes(kind, pair, stages, bn, int(groups), int(rank), a_blocks) > room_smem) --stages;
+    *smem = cf::grouped_smem_bytes(kind, pair, stages, bn, int(groups), int(rank), a_blocks);
     if (*smem > kMaxSmem || *smem > dev.max_smem_optin) return CF_ERR_UNSUPPORTED;
     const int width = pair ? 2 : 1;
     const int64_t tiles = tiles_of(128 * width);
@@ -1447,7 +1448,7 @@ cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int
     *ctas = int(std::max<int64_t>(c, 1)) * width;
     a->bn = bn;
     a->pair = pair;
-    a->a_blocks = F <= 64 && kind != cf::GR_DGRAD && !pair ? 1 : 2;
+    a->a_blocks = a_blocks;
     a->stages = stages;
     a->counters = reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(ws) + cf::kErrBytes +
                                                size_t(set) * kGroupedCounterBytes);

@@ -277,7 +277,7 @@ struct GroupedArgs {
     unsigned long long timeout_ns;
 };
 
-int grouped_smem_bytes(int kind, bool pair, int stages, int bn, int groups, int rank);
+int grouped_smem_bytes(int kind, bool pair, int stages, int bn, int groups, int rank, int a_blocks);
 cudaError_t launch_grouped(int kind, const GroupedArgs &a, int ctas, int smem, bool pdl, cudaStream_t stream);
 
 }  // namespace cf

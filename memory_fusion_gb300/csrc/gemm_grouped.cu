@@ -50,7 +50,6 @@ __host__ __device__ constexpr int registers_of(int kind, bool pair) {
 constexpr int kShortWarps = 6;
 constexpr int kBK = 64;         // contraction per stage (128 bytes: one swizzle atom)
 constexpr int kFB = 128;        // features per tile (accumulator lanes)
-constexpr int kABytes = kFB * kBK * 2;
 constexpr int kRasterRows = 16;  // row tiles walked before the next feature tile
 constexpr int kMinStretch = 4;   // blocks a worker takes at least
 constexpr int kLongRows = 64;    // LORA: rows from which a request has tiles of its own
@@ -62,17 +61,21 @@ constexpr uint32_t kInfoEpi = 0x30000000u;
 constexpr uint32_t kInfoTable = 0x70000000u;
 
 struct GrLayout {
-    uint32_t stage_bytes, table, stg, bars, total;
+    uint32_t a_bytes, stage_bytes, table, stg, bars, total;
 };
 
 // int32 arrays of the group table behind the Plan, groups + 1 long
 __host__ __device__ constexpr int table_arrays(int kind) { return kind == GR_LORA ? 5 : kind == GR_SHRINK ? 3 : 2; }
 
-__host__ __device__ inline GrLayout gr_layout(int kind, bool pair, int stages, int bn, int groups, int rank) {
+__host__ __device__ inline GrLayout gr_layout(int kind, bool pair, int stages, int bn, int groups, int rank,
+                                              int a_blocks) {
     GrLayout L;
     // a CTA of a pair stages its own 128 features and half of the tile's columns
-    L.stage_bytes = uint32_t(kABytes + (pair ? bn / 2 : bn) * kBK * 2);
+    L.a_bytes = uint32_t(a_blocks) * 8192u;
+    L.stage_bytes = L.a_bytes + uint32_t((pair ? bn / 2 : bn) * kBK * 2);
     uint32_t off = uint32_t(stages) * L.stage_bytes;
+    // (with one block of features the MMA reads another 8 KB behind it, into lanes that nobody stores)
+    if (a_blocks == 1 && L.stage_bytes < 16384u) off += 16384u - L.stage_bytes;
     L.table = off;
     off += (32u + uint32_t(table_arrays(kind) * (groups + 1)) * 4u + 15u) & ~15u;
     // per epilogue warp: 16-bit [32 rows][32 features]; LORA: fp32; WGRAD: 16-bit [32 features][64 columns];
@@ -565,12 +568,11 @@ __device__ __forceinline__ uint32_t b_bytes(const GroupedArgs &a, const Tile &w)
 
 // WGRAD: rows left .. 16*steps - 1 of every 64-column block of the stage (a row is 128 bytes of a block) become
 // zeros, by one warp; then the async proxy may read them
-__device__ __forceinline__ void zero_tail(uint8_t *st, int left, int steps, int bblocks, int lane) {
-    const int per = (16 * steps - left) * 8;  // 16-byte pieces per block
-    for (int i = lane; i < (2 + bblocks) * per; i += 32) {
+__device__ __forceinline__ void zero_tail(uint8_t *st, int left, int steps, int blocks, int lane) {
+    const int per = (16 * steps - left) * 8;  // 16-byte pieces per block; the blocks of X, then those of dY
+    for (int i = lane; i < blocks * per; i += 32) {
         const int blk = i / per, p = i % per;
-        uint8_t *q = st + (blk < 2 ? blk * 8192 : kABytes + (blk - 2) * 8192) + left * 128 + p * 16;
-        *reinterpret_cast<uint4 *>(q) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(st + blk * 8192 + left * 128 + p * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
     ptx::fence_proxy_async_smem();
     __syncwarp();
@@ -654,7 +656,27 @@ __device__ __forceinline__ void finish_row(const GroupedArgs &a, const Tile &w, 
 // rows, and nothing needs turning.  Two columns of several pieces are in flight.
 template <int KIND>
 __device__ __forceinline__ void finish_pieces(const GroupedArgs &a, const Tile &w, const Pieces &pc, int e, int lane) {
-    constexpr int kWarps = epi_warps(KIND), kFly = KIND == GR_SHRINK ? 4 : 6;
+    if constexpr (KIND == GR_SHRINK) {  // few features: lanes go over rows and features alike
+        const int nf = a.F / 4;
+        for (int i = e * 32 + lane; i < w.n * nf; i += 128) {
+            const int j = i / nf, f = (i - j * nf) * 4;
+            const size_t at = size_t(j) * kFB + f;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k <= pc.more; k += 8) {
+                float4 x[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    x[q] = k + q <= pc.more ? __ldcg(reinterpret_cast<const float4 *>(
+                                                  (k + q == 0 ? pc.p0 : pc.p + (k + q - 1) * pc.step) + at))
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) s.x += x[q].x, s.y += x[q].y, s.z += x[q].z, s.w += x[q].w;
+            }
+            finish_row<KIND>(a, w, w.col0 + j, f, s);
+        }
+        return;
+    }
+    constexpr int kWarps = epi_warps(KIND), kFly = 6;
     const int f = w.f0 + 4 * lane;
     if (f >= a.F) return;
     for (int j = e; j < w.n; j += 2 * kWarps) {
@@ -928,7 +950,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
     constexpr bool kAMn = KIND != GR_DGRAD;  // features contiguous in memory: A is MN-major
     constexpr bool kBMn = KIND == GR_WGRAD;
     const int stages = a.stages;
-    const GrLayout L = gr_layout(KIND, kPair, stages, a.bn, a.groups, a.rank);
+    const GrLayout L = gr_layout(KIND, kPair, stages, a.bn, a.groups, a.rank, a.a_blocks);
     const GrBars B = gr_bars(base + L.bars, stages);
     const Table tab(smem_raw + L.table, KIND, a.groups);
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem_raw + (B.misc - base));
@@ -1013,7 +1035,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                         if (!ok) break;
                     }
                     const uint32_t sa = base + s * L.stage_bytes;
-                    const uint32_t sb = sa + kABytes;
+                    const uint32_t sb = sa + L.a_bytes;
                     // A pair's loads complete on the leader's barrier.  (WGRAD: but for a group's last block where it
                     // has to be zeroed behind the rows; the second CTA's part then completes on its own barrier, its
                     // warp 1 zeroes and arrives.)
@@ -1054,8 +1076,8 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                             else ptx::tma_load_4d(sa, &a.tmap_lb, bar, 0, r0, w.f0 / 64, w.ad);
                         }
                         const int xh = (x & 1) * a.rank + r0;
-                        if constexpr (kPair) ptx::tma_load_2d_pair(sa + kABytes, &a.tmap_h, bar, xh, col0);
-                        else ptx::tma_load_2d(sa + kABytes, &a.tmap_h, bar, xh, col0);
+                        if constexpr (kPair) ptx::tma_load_2d_pair(sa + L.a_bytes, &a.tmap_h, bar, xh, col0);
+                        else ptx::tma_load_2d(sa + L.a_bytes, &a.tmap_h, bar, xh, col0);
                         ++it;
                         if (++s == uint32_t(stages)) {
                             s = 0;
@@ -1088,7 +1110,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                         if (!__all_sync(0xffffffffu, ok)) break;
                         ph ^= 1u << at;
                         const int left = w.rows - (w.nk - 1) * kBK;
-                        zero_tail(smem_raw + at * L.stage_bytes, left, (left + 15) / 16, (w.nm / 2 + 63) / 64, lane);
+                        zero_tail(smem_raw + at * L.stage_bytes, left, (left + 15) / 16, a.a_blocks + (w.nm / 2 + 63) / 64, lane);
                         if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(B.full0 + 8 * at, 0u));
                     }
                     s = (s + uint32_t(w.nk)) % uint32_t(stages);
@@ -1096,7 +1118,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
             }
         } else if (lane == 0 || KIND == GR_WGRAD) {
             const uint64_t ad0 = kAMn ? sw128_desc(base, 8192, 1024) : sw128_desc(base, 16, 1024);
-            const uint64_t bd0 = kBMn ? sw128_desc(base + kABytes, 8192, 1024) : sw128_desc(base + kABytes, 16, 1024);
+            const uint64_t bd0 = kBMn ? sw128_desc(base + L.a_bytes, 8192, 1024) : sw128_desc(base + L.a_bytes, 16, 1024);
             uint32_t s = 0, ph = 0;
             for (int tile = 0; walk.next(w); ++tile) {
                 const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
@@ -1147,7 +1169,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                         ok = __all_sync(0xffffffffu, ok);
                         if (ok && (left & 15) != 0)
                             zero_tail(smem_raw + s * L.stage_bytes, left, steps,
-                                      ((kPair ? w.nm / 2 : w.nm) + 63) / 64, lane);
+                                      a.a_blocks + ((kPair ? w.nm / 2 : w.nm) + 63) / 64, lane);
                     }
                     if (ok && lane == 0) {
                         ptx::tc_fence_after();
@@ -1398,8 +1420,8 @@ void *kernel_for(int kind) {
 
 }  // namespace
 
-int grouped_smem_bytes(int kind, bool pair, int stages, int bn, int groups, int rank) {
-    return int(gr_layout(kind, pair, stages, bn, groups, rank).total);
+int grouped_smem_bytes(int kind, bool pair, int stages, int bn, int groups, int rank, int a_blocks) {
+    return int(gr_layout(kind, pair, stages, bn, groups, rank, a_blocks).total);
 }
 
 cudaError_t launch_grouped(int kind, const GroupedArgs &a, int ctas, int smem, bool pdl, cudaStream_t stream) {
