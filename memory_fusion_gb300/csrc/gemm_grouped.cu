@@ -185,25 +185,19 @@ struct Walk {
         cur = worker;
         end = plan.tiles;
         if (!kPair && plan.split) {
-            cur = unit_of(worker);
-            end = worker < plan.workers ? unit_of(worker + 1) : cur;
+            if (plan.ways != 0) {  // one piece: of tile worker / ways
+                end = cur + (worker < plan.workers ? 1 : 0);
+            } else {
+                cur = unit_of(worker);
+                end = worker < plan.workers ? unit_of(worker + 1) : cur;
+            }
         }
     }
     static constexpr int kTileF = kPair ? 2 * kFB : kFB;
     // columns are multiplied in 16s; each half of a pair's in 16s (WGRAD: whole 64-column blocks)
     static constexpr int kGran = kPair ? (KIND == GR_WGRAD ? 128 : 32) : 16;
-    __device__ int unit_of(int w) const {
-        if (plan.ways != 0) {
-            const int t = w / plan.ways;
-            return t * nkc + (w - t * plan.ways) * nkc / plan.ways;
-        }
-        return w * plan.base + min(w, plan.rem);
-    }
+    __device__ int unit_of(int w) const { return w * plan.base + min(w, plan.rem); }
     __device__ int worker_of(int u) const {
-        if (plan.ways != 0) {
-            const int t = u / nkc;
-            return t * plan.ways + ((u - t * nkc + 1) * plan.ways - 1) / nkc;
-        }
         const int wide = plan.rem * (plan.base + 1);
         return u < wide ? u / (plan.base + 1) : plan.rem + (u - wide) / plan.base;
     }
@@ -226,8 +220,12 @@ struct Walk {
         } else {
             r.id = cur;
             if (!kPair && plan.split) {
-                r.id = cur / nkc;
-                kb = cur % nkc;
+                if (plan.ways != 0) {
+                    r.id = cur / plan.ways;
+                } else {
+                    r.id = cur / nkc;
+                    kb = cur - r.id * nkc;
+                }
             }
             while (r.id >= tab.pre[g + 1]) ++g;
             local = r.id - tab.pre[g];
@@ -272,7 +270,13 @@ struct Walk {
         r.kb1 = r.nk;
         r.first = r.last = worker;
         r.slot = 0;
-        if (!kPair && plan.split) {
+        if (!kPair && plan.split && plan.ways != 0) {
+            r.first = r.id * plan.ways;
+            r.last = r.first + plan.ways - 1;
+            r.kb0 = (worker - r.first) * nkc / plan.ways;
+            r.kb1 = (worker - r.first + 1) * nkc / plan.ways;
+            ++cur;
+        } else if (!kPair && plan.split) {
             const int u0 = cur - kb;  // the tile's first unit
             const int take = min(blocks - kb, end - cur);
             r.kb1 = min(kb + take, r.nk);
@@ -289,7 +293,7 @@ struct Walk {
         return true;
     }
     // a worker's first piece goes to its slot 0 unless its stretch began in an earlier tile
-    __device__ int slot_of(int w, int u0) const { return unit_of(w) >= u0 ? 0 : 1; }
+    __device__ int slot_of(int w, int u0) const { return plan.ways != 0 || unit_of(w) >= u0 ? 0 : 1; }
 };
 
 // GELU in the tanh form is z * p with p = 1 / (1 + exp(-2u)), u = sqrt(2/pi)(z + 0.044715 z^3):
@@ -653,7 +657,7 @@ __device__ __forceinline__ void finish_row(const GroupedArgs &a, const Tile &w, 
 
 // The pieces of a divided tile added in worker order and finished (all kinds but WGRAD).  A warp takes whole columns,
 // that is rows of the batch: a lane 4 neighbouring features, so the loads are 512 bytes a warp and the stores whole
-// rows, and nothing needs turning.  Two columns of several pieces are in flight.
+// rows, and nothing needs turning.  Four columns of four pieces are in flight.
 template <int KIND>
 __device__ __forceinline__ void finish_pieces(const GroupedArgs &a, const Tile &w, const Pieces &pc, int e, int lane) {
     if constexpr (KIND == GR_SHRINK) {  // few features: lanes go over rows and features alike
@@ -676,32 +680,34 @@ __device__ __forceinline__ void finish_pieces(const GroupedArgs &a, const Tile &
         }
         return;
     }
-    constexpr int kWarps = epi_warps(KIND), kFly = 6;
+    constexpr int kWarps = epi_warps(KIND), kFly = 4, kCols = 4;
     const int f = w.f0 + 4 * lane;
     if (f >= a.F) return;
-    for (int j = e; j < w.n; j += 2 * kWarps) {
+    for (int j = e; j < w.n; j += kCols * kWarps) {
         const size_t at = size_t(j) * kFB + 4 * lane;
-        const bool two = j + kWarps < w.n;
-        float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        float4 s[kCols];
+#pragma unroll
+        for (int h = 0; h < kCols; ++h) s[h] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k <= pc.more; k += kFly) {
-            float4 x[kFly][2];
+            float4 x[kFly][kCols];
 #pragma unroll
             for (int i = 0; i < kFly; ++i) {
                 const float *p = (k + i == 0 ? pc.p0 : pc.p + (k + i - 1) * pc.step) + at;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    x[i][h] = k + i <= pc.more && (h == 0 || two)
+                for (int h = 0; h < kCols; ++h)
+                    x[i][h] = k + i <= pc.more && j + h * kWarps < w.n
                                   ? __ldcg(reinterpret_cast<const float4 *>(p + h * kWarps * kFB))
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
             for (int i = 0; i < kFly; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < kCols; ++h)
                     s[h].x += x[i][h].x, s[h].y += x[i][h].y, s[h].z += x[i][h].z, s[h].w += x[i][h].w;
         }
-        finish_row<KIND>(a, w, w.col0 + j, f, s[0]);
-        if (two) finish_row<KIND>(a, w, w.col0 + j + kWarps, f, s[1]);
+#pragma unroll
+        for (int h = 0; h < kCols; ++h)
+            if (j + h * kWarps < w.n) finish_row<KIND>(a, w, w.col0 + j + h * kWarps, f, s[h]);
     }
 }
 
@@ -1232,7 +1238,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                 if (w.ad == -2 && a.nweights > 0) {
                     parts = w.last - w.first + 1;
                     part = worker - w.first;
-                    // B's slices on their way to L2 while the projection is multiplied
+                    // the other rows' slices of B on their way to L2 while the projection is multiplied
                     for (int c = half * 32; c < w.n; c += 64) {
                         for (int i = 0; i < 4; ++i) {
                             const int j = c + (lane >> 2) + 8 * i;
@@ -1247,9 +1253,27 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                     }
                 }
             }
+            // The first eight of those rows in the warp's first fragment are worked out now, while the projection is
+            // multiplied.
+            int early = -1;  // their place in it
+            float low[8];
+            if constexpr (KIND == GR_LORA) {
+                if (parts > 0) {
+                    ptx::griddep_wait();  // H is the previous grid's
+                    const int c = half * 32;
+                    const int i = parts == 1 ? 0 : (part + parts - c / 8 % parts) % parts;
+                    if (i < 4 && c + 8 * i < w.n) {
+                        early = i;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) low[k] = 0.f;
+                        const int j = c + (lane >> 2) + 8 * i, f8 = w.f0 + q * 32 + (lane & 3) * 8;
+                        if (j < w.n && f8 < a.F)
+                            add_low_rank(low, a, adapter_of(tab, a.groups, w.col0 + j), w.col0 + j, f8);
+                    }
+                }
+            }
             const bool ok = ptx::mbar_wait_bounded(B.tmem_full0 + 8 * buf, tph, tmo, abort, a.err, kInfoEpi | buf);
             ptx::tc_fence_after();
-            if (KIND == GR_LORA && parts > 0) ptx::griddep_wait();  // H is the previous grid's
             const uint32_t tacc = tmem_base + (uint32_t(q * 32) << 16) + buf * uint32_t(a.bn);
             const int f = w.f0 + q * 32 + lane;
             const bool live = f < a.F && ok;
@@ -1275,8 +1299,12 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                                 float x[8];
                                 turned(x, stg, lane, i);
                                 const int row = w.col0 + c + (lane >> 2) + 8 * i;
-                                if ((c / 8 + i) % parts == part)
+                                if (c == half * 32 && i == early) {
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k) x[k] += low[k];
+                                } else if ((c / 8 + i) % parts == part) {
                                     add_low_rank(x, a, adapter_of(tab, a.groups, row), row, f8);
+                                }
                                 float4 *d = reinterpret_cast<float4 *>(p);
                                 __stcg(d, make_float4(x[0], x[1], x[2], x[3]));
                                 __stcg(d + 1, make_float4(x[4], x[5], x[6], x[7]));
@@ -1336,7 +1364,12 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                         float x[8];
                         turned(x, stg, lane, i);
                         const int row = w.col0 + c + (lane >> 2) + 8 * i;
-                        if (parts > 0) add_low_rank(x, a, adapter_of(tab, a.groups, row), row, f8);
+                        if (c == half * 32 && i == early) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) x[k] += low[k];
+                        } else if (parts > 0) {
+                            add_low_rank(x, a, adapter_of(tab, a.groups, row), row, f8);
+                        }
                         uint32_t p[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
