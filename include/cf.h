@@ -107,7 +107,8 @@ typedef struct cf_tuning {
     uint32_t timeout_us;    /* bound of every device spin (0 = 200000 us)          */
     int32_t extra_arrivals; /* TEST HOOK: added to the arrival count the global
                                barrier waits for (B2B stream kernel: the
-                               per-chunk P-ready barrier); > 0 makes that wait
+                               per-chunk P-ready barrier; grouped kernels: the
+                               accumulator-ready barrier); > 0 makes that wait
                                run out (CF_ERR_DEVICE_TIMEOUT) without
                                faulting.  0 in normal use.                        */
     int32_t cluster_m;      /* GEMM: row blocks per cluster (1 or 2); 2 pairs the
@@ -714,7 +715,8 @@ typedef enum { CF_BF16 = 0, CF_FP16 = 1 } cf_dtype;  /* 16-bit operand types */
  * Tuning fields used (_ex): n_slice (accumulator columns: 16, 32, 64, 128, 256;
  * wgrad from 64 on), cluster_m (2: CTA pairs on tiles of 256 features, with
  * n_slice 128 or 256; 1: single CTAs), stages, max_clusters (cap on CTAs or
- * pairs), timeout_us, disable_pdl. */
+ * pairs), timeout_us, disable_pdl, extra_arrivals (TEST HOOK: > 0 makes the
+ * wait for the accumulator run out). */
 CF_API size_t cf_grouped_gemm_workspace_size(int64_t T, int64_t N, int64_t K, int64_t E);
 
 CF_API cf_status cf_grouped_gemm(const void *X, const void *W, const int32_t *offsets, void *Y, void *Z,

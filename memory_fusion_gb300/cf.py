@@ -181,6 +181,8 @@ _lock = threading.Lock()
 def lib() -> ctypes.CDLL:
     """Load libcf.so (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -203,14 +205,12 @@ def declared_symbols():
 # raw entry points (same names and argument order as the C ABI)
 # ---------------------------------------------------------------------------
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
-    f = getattr(x, "data_ptr", None)
-    if f is not None:
-        return f()
-    raise TypeError(f"cannot pass {type(x)} as a pointer")
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        raise TypeError(f"cannot pass {type(x)} as a pointer") from None
 
 
 def _stream(s):
@@ -763,12 +763,12 @@ def _run(what, call, device, stream, out, shape, dtype, workspace, nbytes):
     if stream is None and index == torch.cuda.current_device():  # nothing to switch: the decode step's path
         Y = out if out is not None else torch.empty(shape, dtype=dtype, device=device)
         ws = workspace if workspace is not None else new_workspace(nbytes(), device)
-        check(call(Y, ws, ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(index)), what)
+        check(call(Y, ws, ws.nbytes, torch._C._cuda_getCurrentRawStream(index)), what)
         return Y
     with _launch_on(device, stream):
         Y = out if out is not None else torch.empty(shape, dtype=dtype, device=device)
         ws = workspace if workspace is not None else new_workspace(nbytes(), device)
-        check(call(Y, ws, ws.numel() * ws.element_size(), torch.cuda.current_stream().cuda_stream), what)
+        check(call(Y, ws, ws.nbytes, torch.cuda.current_stream().cuda_stream), what)
     return Y
 
 

@@ -15,6 +15,7 @@
 
 #include "../../include/cf.h"
 #include "cf_internal.h"
+#include "grouped_internal.h"
 
 namespace {
 
@@ -1472,6 +1473,7 @@ void grouped_args(cf::GroupedArgs *a, int64_t T, int64_t F, int64_t C, int64_t N
     a->N = int(N);
     a->groups = int(groups);
     a->fp16 = dtype == CF_FP16;
+    a->extra_arrivals = t.extra_arrivals > 0 ? t.extra_arrivals : 0;
     a->timeout_ns = 1000ull * (t.timeout_us ? t.timeout_us : kDefaultTimeoutUs);
 }
 

@@ -29,15 +29,76 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/cf.h"
 #include "cf_internal.h"
+#include "grouped_internal.h"
 #include "ptx.cuh"
 #include "umma.cuh"
 
 namespace cf {
+
+// ---------------------------------------------------------------------------
+// Primitives that only these kernels use (the shared ones are in ptx.cuh)
+// ---------------------------------------------------------------------------
+namespace ptx {
+
+// bring the line holding p into L2
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(p)));
+}
+// 3-D and 4-D tiled TMA loads without a cache policy; _pair: completing on an mbarrier of either CTA of the pair
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *tmap, uint32_t bar_cluster, int32_t x,
+                                                 int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z, int32_t w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void *tmap, uint32_t bar_cluster, int32_t x,
+                                                 int32_t y, int32_t z, int32_t w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+// arrive on an mbarrier of another CTA of the cluster without release semantics: nothing this thread wrote is handed
+// over.  (A release per pipeline stage waits for the thread's own copies: the weight gradient ran at half the speed.)
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+}  // namespace ptx
+
 namespace {
+
+// instruction descriptor: kind::f16, A and B both bf16 or both fp16, D = fp32, either operand MN-major or K-major,
+// M = m, N = n
+__device__ __forceinline__ uint32_t idesc_f16(int m, int n, bool fp16, bool a_mn, bool b_mn) {
+    return (1u << 4) | (fp16 ? 0u : (1u << 7) | (1u << 10)) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
+           (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+
 
 // Epilogue warps, from warp 2 on: two halves of 4 (128 lanes each); SHRINK one, and two more warps that only help
 // with its short requests.  A decode batch's SHRINK and LORA share the SMs, one CTA of each: 256 threads of 96
@@ -978,7 +1039,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
             ptx::mbar_init(B.empty0 + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
-            ptx::mbar_init(B.tmem_full0 + 8 * b, 1);
+            ptx::mbar_init(B.tmem_full0 + 8 * b, 1 + uint32_t(a.extra_arrivals));
             ptx::mbar_init(B.tmem_empty0 + 8 * b, kPair ? 2 * kEpiWarps : kEpiWarps);
         }
         ptx::mbar_init(B.mma_done, 1);
@@ -1461,16 +1522,18 @@ cudaError_t launch_grouped(int kind, const GroupedArgs &a, int ctas, int smem, b
     const bool pair = a.pair != 0;
     void *fn = pair ? kernel_for<true>(kind) : kernel_for<false>(kind);
     if (!fn) return cudaErrorInvalidValue;
-    static int set_smem[64][16] = {};
+    // Once per device and kernel, to the most a launch may ask for: launches from several threads set the same value,
+    // and none is set under a capture later.
+    static std::atomic<bool> set[64][16];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidValue;
-    int &set = set_smem[dev][2 * kind + (pair ? 1 : 0)];
-    if (smem > set) {  // once per device and kernel, to the largest size: none under capture later
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    std::atomic<bool> &done = set[dev][2 * kind + (pair ? 1 : 0)];
+    if (!done.load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kGroupedMaxSmem);
         if (e != cudaSuccess) return e;
-        set = smem;
+        done.store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);

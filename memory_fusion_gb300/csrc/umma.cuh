@@ -25,11 +25,5 @@ __device__ __forceinline__ uint32_t idesc_bf16(int m, int n) {
            (uint32_t(m >> 4) << 24);
 }
 
-// instruction descriptor of the grouped kernels: kind::f16, A and B both bf16 or
-// both fp16, D = fp32, either operand MN-major or K-major, M = m, N = n
-__device__ __forceinline__ uint32_t idesc_f16(int m, int n, bool fp16, bool a_mn, bool b_mn) {
-    return (1u << 4) | (fp16 ? 0u : (1u << 7) | (1u << 10)) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
-           (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
-}
 
 }  // namespace cf
