@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <map>
@@ -1379,18 +1380,89 @@ cf_status grouped_sizes(int64_t T, int64_t N, int64_t K, int64_t groups, int dty
     return CF_OK;
 }
 
-// Accumulator columns where none are asked for.  Columns are rows of the batch (WGRAD: columns of dW): twice
-// the mean group, so that most uneven groups read their weights once, between 16 and 256.  (4099 rows over 64 groups:
-// 128 columns 49 us, 256 57 us, 64 68 us.)
-int grouped_columns(int kind, int64_t T, int64_t N, int64_t groups) {
-    int64_t want;
-    if (kind == cf::GR_WGRAD) want = N;
-    else if (kind == cf::GR_LORA) want = T;
-    else if (kind == cf::GR_SHRINK) want = T / cf::kGroupedWorkers;  // one tile of features: row tiles for every SM
-    else want = std::min<int64_t>(T, 2 * ((T + groups - 1) / groups));
-    int bn = kind == cf::GR_WGRAD ? 64 : 16;  // WGRAD stages dY in 64-column blocks
-    while (bn < 256 && 5 * bn < 4 * want) bn *= 2;
-    return bn;
+// -------------------------------------------------------------------------
+// Tile width (accumulator columns) and CTA pairs, from the sizes the host knows: a model of a launch's cycles,
+// minimised over the widths.  Group sizes are device data, so groups are taken as equal, with half a tile of waste
+// where they are wider than a tile.  Measured on a GB300 (about 1.8 GHz under load): an MMA block of n columns takes
+// 2.7 n cycles (690 at 256), copies arrive at 56 B per cycle and SM, HBM gives the chip 3770 B per cycle; an epilogue
+// takes 600 cycles and 25 a column; dividing tiles costs 1500 cycles and 70 a column (writing, adding, finishing); the
+// low-rank product of rows with adapters of their own 1000 cycles for 8 rows and 8 ranks.
+// -------------------------------------------------------------------------
+constexpr double kPlanSms = 152;  // a GB300's, whatever device is current: the workspace size follows from this plan
+
+struct GroupedShape {
+    int kind;
+    int64_t T, F, C, N, groups, rank;
+};
+
+double grouped_cycles(const GroupedShape &s, int bn, bool pair) {
+    const bool wgrad = s.kind == cf::GR_WGRAD;
+    const double sms = pair ? kPlanSms / 2 : kPlanSms;
+    const double groups = double(std::max<int64_t>(1, std::min(s.groups, s.T)));
+    const double mean = double(s.T) / groups;
+    const double ft = double((s.F + (pair ? 255 : 127)) / (pair ? 256 : 128));
+    double tiles, n, blocks, bytes, low = 0.0;
+    if (wgrad) {
+        tiles = double(s.groups) * ft * double((s.N + bn - 1) / bn);
+        n = double(std::min<int64_t>(bn, s.N));
+        blocks = std::max(1.0, mean / 64);
+        bytes = 2.0 * (double(s.T) * double(s.F + s.N) + double(s.groups) * double(s.F) * double(s.N));
+    } else {
+        const bool lora = s.kind == cf::GR_LORA;
+        double row_tiles;
+        if (lora) {  // long requests have tiles of their own, runs of short ones share tiles
+            row_tiles = double((s.T + bn - 1) / bn) + 0.5 * double(std::min<int64_t>(s.groups, s.T / 64));
+            n = std::min(double(bn), double(s.T) / row_tiles);
+        } else {
+            row_tiles = mean <= bn / 1.5 ? groups : double(s.T) / bn + 0.5 * groups;
+            n = std::min(double(bn), std::max(16.0, mean));
+        }
+        tiles = ft * row_tiles;
+        blocks = double((s.C + 63) / 64);
+        bytes = 2.0 * (double(s.T) * double(s.F + s.C) + (lora ? 1.0 : groups) * double(s.F) * double(s.C));
+        if (lora) {  // eight rows each of the requests, at most, are short
+            const double share = std::min(1.0, 8.0 * double(s.groups) / double(s.T));
+            low = 600 + 15 * n + share * (n > 32 ? 0.5 : 1.0) * std::ceil(n / 8) * double(s.rank / 8) * 1000;
+            blocks += (1.0 - share) * 2.0 * double((s.rank + 63) / 64);
+        }
+    }
+    // (a copy brings the tile's full width, a narrower group's or not)
+    const double block = std::max(2.7 * n, (16384 + (pair ? 64.0 : 128.0) * bn) / 56);
+    const double main = blocks * block + 400, epilogue = 600 + 25 * n + low, hbm = bytes / 3770;
+    // two things that go on at once hardly ever overlap quite
+    auto both = [](double a, double b) { return std::max(a, b) + 0.3 * std::min(a, b); };
+    const double rounds = std::ceil(tiles / sms - 1e-9);
+    const double whole = both(rounds * std::max(main, epilogue) + std::min(main, epilogue), hbm);
+    if (pair || tiles > double(cf::kGroupedSplitTiles)) return whole;
+    const double each = std::max(tiles * main / sms, 4 * block);
+    const double parts = std::max(1.0, sms / tiles);
+    const double split = both(each, hbm) + 1500 + 70 * n + 600 + 25 * n + low / parts;
+    return std::min(whole, split);
+}
+
+bool grouped_may_pair(int kind, int bn, int64_t F) { return kind != cf::GR_SHRINK && bn >= 128 && F > 128; }
+
+// the tile width where none is asked for, and whether CTA pairs work on it
+int grouped_columns(const GroupedShape &s, bool *pair) {
+    *pair = false;
+    if (s.kind == cf::GR_SHRINK) {  // one tile of features: row tiles for every SM
+        int bn = 16;
+        while (bn < 256 && bn * cf::kGroupedWorkers < s.T) bn *= 2;
+        return bn;
+    }
+    int best = 256;
+    double cycles = 1e300;
+    for (int bn = 256; bn >= (s.kind == cf::GR_WGRAD ? 64 : 16); bn /= 2) {  // WGRAD stages dY in 64-column blocks
+        for (int p = grouped_may_pair(s.kind, bn, s.F) ? 1 : 0; p >= 0; --p) {
+            const double c = grouped_cycles(s, bn, p == 1);
+            if (c < cycles) {
+                cycles = c;
+                best = bn;
+                *pair = p == 1;
+            }
+        }
+    }
+    return best;
 }
 
 // pieces of tiles: two for each CTA
@@ -1407,7 +1479,9 @@ cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int
                        const cf_tuning &t, const cf::DeviceInfo &dev, void *ws, int set, unsigned char *part,
                        size_t room, cf::GroupedArgs *a, int *ctas, int *smem) {
     const bool wgrad = kind == cf::GR_WGRAD;
-    int bn = grouped_columns(kind, T, N, groups);
+    const GroupedShape shape{kind, T, F, C, N, groups, rank};
+    bool pair;
+    int bn = grouped_columns(shape, &pair);
     if (t.n_slice != 0) {
         if (t.n_slice != 16 && t.n_slice != 32 && t.n_slice != 64 && t.n_slice != 128 && t.n_slice != 256)
             return CF_ERR_UNSUPPORTED;
@@ -1420,23 +1494,22 @@ cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int
         const int64_t ft = (F + features - 1) / features;
         return wgrad ? groups * ft * ((N + bn - 1) / bn) : ft * std::min<int64_t>(T, T / bn + groups);
     };
-    // CTA pairs where there are full tiles for all of them; a smaller launch is better off dividing its tiles
     if (t.cluster_m < 0 || t.cluster_m > 2) return CF_ERR_UNSUPPORTED;
-    // and where rounding the features up to 256 costs less than a tenth more than to 128
-    bool pair = kind != cf::GR_SHRINK && bn >= 128 && !(wgrad && bn < 256) && tiles_of(256) >= dev.sm_count &&
-                20 * ((F + 255) / 256) <= 11 * ((F + 127) / 128);
+    if (t.n_slice != 0)
+        pair = grouped_may_pair(kind, bn, F) && grouped_cycles(shape, bn, true) <= grouped_cycles(shape, bn, false);
     if (t.cluster_m != 0) pair = t.cluster_m == 2;
     if (pair && (kind == cf::GR_SHRINK || bn < 128)) return CF_ERR_UNSUPPORTED;
     const int a_blocks = F <= 64 && kind != cf::GR_DGRAD && !pair ? 1 : 2;
-    int stages = t.stages > 0 ? t.stages : kind == cf::GR_SHRINK ? 12 : 8;  // (deeper rings of small stages were slower: 250 rows over 32 groups, 12
-                                               // stages 76.9 us, 8 stages 73.2)
+    // (deeper rings of small stages were slower: 250 rows over 32 groups of 2048 x 4096, 12 stages 76.9 us, 8 73.2)
+    int stages = t.stages > 0 ? t.stages : kind == cf::GR_SHRINK ? 12 : 8;
     // a decode batch's two adapter products share the SMs: the second reads its weights while the first runs
     const int shrink_room = 98 * 1024, room_smem = bn > 64                ? kMaxSmem
                                                    : kind == cf::GR_SHRINK ? shrink_room
                                                    : kind == cf::GR_LORA   ? kMaxSmem - shrink_room - 2048
                                                                            : kMaxSmem;
-    while (stages > 2 && cf::grouped_smem_bytes(kind, pair, stages, bn, int(groups), int(rank), a_blocks) > room_smem) --stages;
-    *smem = cf::grouped_smem_bytes(kind, pair, stages, bn, int(groups), int(rank), a_blocks);
+    auto bytes = [&](int n) { return cf::grouped_smem_bytes(kind, pair, n, bn, int(groups), int(rank), a_blocks); };
+    while (stages > 2 && bytes(stages) > room_smem) --stages;
+    *smem = bytes(stages);
     if (*smem > kMaxSmem || *smem > dev.max_smem_optin) return CF_ERR_UNSUPPORTED;
     const int width = pair ? 2 : 1;
     const int64_t tiles = tiles_of(128 * width);
@@ -1529,11 +1602,12 @@ cf_status grouped_rows(int kind, const void *rows, const void *W, const int32_t 
 }  // namespace
 
 extern "C" size_t cf_grouped_gemm_workspace_size(int64_t T, int64_t N, int64_t K, int64_t E) {
-    (void)K;
-    if (T < 0 || N <= 0 || E <= 0) return kGroupedHead;
-    return kGroupedHead +
-           grouped_partial_bytes(std::max(grouped_columns(cf::GR_FORWARD, T, N, E),
-                                          grouped_columns(cf::GR_WGRAD, T, N, E)));
+    if (T < 0 || N <= 0 || K <= 0 || E <= 0) return kGroupedHead;
+    bool pair;
+    const int fwd = grouped_columns({cf::GR_FORWARD, T, N, K, 0, E, 0}, &pair);
+    const int dgrad = grouped_columns({cf::GR_DGRAD, T, K, N, 0, E, 0}, &pair);
+    const int wgrad = grouped_columns({cf::GR_WGRAD, T, K, 0, N, E, 0}, &pair);
+    return kGroupedHead + grouped_partial_bytes(std::max(fwd, std::max(dgrad, wgrad)));
 }
 
 extern "C" cf_status cf_grouped_gemm_ex(const void *X, const void *W, const int32_t *offsets, void *Y, void *Z,
@@ -1625,11 +1699,10 @@ static size_t lora_part_bytes(int64_t S, int64_t R) {
 // workspace: head; partials of the first product; of the second (which may start while the first ends); H [T, 2, R] 16-bit;
 // parts of the short requests' first product
 extern "C" size_t cf_gemm_lora_workspace_size(int64_t T, int64_t N, int64_t K, int64_t S, int64_t R) {
-    (void)N;
-    (void)K;
-    if (T < 0 || R < 0 || S <= 0) return kGroupedHead;
-    return kGroupedHead + grouped_partial_bytes(grouped_columns(cf::GR_SHRINK, T, 0, S)) +
-           grouped_partial_bytes(grouped_columns(cf::GR_LORA, T, 0, S)) +
+    if (T < 0 || N <= 0 || K <= 0 || R <= 0 || S <= 0) return kGroupedHead;
+    bool pair;
+    return kGroupedHead + grouped_partial_bytes(grouped_columns({cf::GR_SHRINK, T, R, K, 0, S, 0}, &pair)) +
+           grouped_partial_bytes(grouped_columns({cf::GR_LORA, T, N, K, 0, S, R}, &pair)) +
            cf::align_up(size_t(T) * size_t(R) * 4, 256) + lora_part_bytes(S, R);
 }
 
@@ -1657,8 +1730,9 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
     cf::DeviceInfo dev;
     if (!cf::current_device_info(&dev)) return CF_ERR_NO_DEVICE;
     if (dev.cc_major != 10 || dev.cc_minor != 3) return CF_ERR_NO_DEVICE;
-    const size_t room_sh = grouped_partial_bytes(grouped_columns(cf::GR_SHRINK, T, 0, S));
-    const size_t room = grouped_partial_bytes(grouped_columns(cf::GR_LORA, T, 0, S));
+    bool pair;
+    const size_t room_sh = grouped_partial_bytes(grouped_columns({cf::GR_SHRINK, T, R, K, 0, S, 0}, &pair));
+    const size_t room = grouped_partial_bytes(grouped_columns({cf::GR_LORA, T, N, K, 0, S, R}, &pair));
     unsigned char *const part_sh = static_cast<unsigned char *>(workspace) + kGroupedHead;
     unsigned char *const part = part_sh + room_sh;
     void *H = part + room;

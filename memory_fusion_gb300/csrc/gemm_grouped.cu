@@ -126,7 +126,7 @@ struct GrLayout {
 };
 
 // int32 arrays of the group table behind the Plan, groups + 1 long
-__host__ __device__ constexpr int table_arrays(int kind) { return kind == GR_LORA ? 5 : kind == GR_SHRINK ? 3 : 2; }
+__host__ __device__ constexpr int table_arrays(int kind) { return kind == GR_LORA ? 6 : kind == GR_SHRINK ? 3 : 2; }
 
 __host__ __device__ inline GrLayout gr_layout(int kind, bool pair, int stages, int bn, int groups, int rank,
                                               int a_blocks) {
@@ -214,6 +214,7 @@ struct Table {
     int *ad;    // SHRINK, LORA: adapter of each request, -1 for none
     int *goff;  // LORA: [plan groups + 1] first row of each plan group
     int *gad;   // LORA: its adapter, -1 none, -2 a run of short requests
+    int *turn;  // LORA: [groups] changes of the adapter up to each request
     __device__ Table(uint8_t *p, int kind, int groups) {
         plan = reinterpret_cast<Plan *>(p);
         off = reinterpret_cast<int *>(p + 32);
@@ -221,8 +222,20 @@ struct Table {
         ad = pre + groups + 1;
         goff = kind == GR_LORA ? ad + groups + 1 : off;
         gad = goff + groups + 1;
+        turn = gad + groups + 1;
     }
 };
+
+// The request of a row of the batch: the last that starts at or before it.
+__device__ __forceinline__ int request_of(const Table &tab, int groups, int row) {
+    int lo = 0, hi = groups - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tab.off[mid] <= row) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
 
 template <int KIND, bool kPair>
 struct Walk {
@@ -325,6 +338,12 @@ struct Walk {
             }
             r.row0 = r.rows = 0;
             r.nk = blocks = nkc;
+        }
+        if constexpr (KIND == GR_LORA) {  // requests in a row may share an adapter
+            if (r.ad == -2) {
+                const int s0 = request_of(tab, a.groups, r.col0), s1 = request_of(tab, a.groups, r.col0 + r.n - 1);
+                if (tab.turn[s0] == tab.turn[s1]) r.ad = tab.ad[s0];
+            }
         }
         r.nm = (r.n + kGran - 1) & ~(kGran - 1);
         r.kb0 = kb;
@@ -493,6 +512,7 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
     const int first = lo_all;
     int carry = 0, longest = 0, ngroups = 0;
     uint32_t long_before = 1u;
+    int turns = 0, last_ad = -1;  // LORA
     // No branches on the lane from here to the plan: lanes behind the last group repeat its end, count nothing and
     // store what is stored there anyway.  (With branches between them the shuffles took 2000 cycles and more.)
     tab.off[0] = first;
@@ -537,6 +557,11 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
                 tab.goff[gi] = lo;  // (the last entry is a dummy, or written below)
                 tab.gad[gi] = rows >= kLongRows ? w : -2;
                 ngroups += __popc(m);
+                const int left = __shfl_up_sync(kAll, w, 1);
+                const uint32_t changes = __ballot_sync(kAll, w != (lane == 0 ? last_ad : left));
+                tab.turn[at] = turns + __popc(changes & (0xffffffffu >> (31 - lane)));
+                turns += __popc(changes);
+                last_ad = __shfl_sync(kAll, w, 31);
             }
         }
         if constexpr (KIND != GR_LORA) {
@@ -571,9 +596,9 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
     if constexpr (KIND == GR_WGRAD) longest = __reduce_max_sync(kAll, longest);
     if (lane == 0) {
         tab.pre[0] = 0;
-        // Rounds of whole tiles against equal stretches, in blocks (of about 0.36 us each: 16 KB of weights at an
-        // SM's share of HBM, or MMAs of 256 columns).  Adding pieces costs about 8 blocks, and another for each 32
-        // columns written and read back.
+        const int rows_all = lo_all - first;
+        // Rounds of whole tiles against equal stretches, in blocks; what adding pieces costs is in the host's plan
+        // (grouped_cycles), which chose the tiles.
         constexpr int kMost = 1 << 20;  // blocks of a contraction, tiles x blocks then fit 30 bits
         const int per_tile = KIND == GR_WGRAD ? ft * ((a.N + a.bn - 1) >> shift) : 1;
         const int nkc = (a.C + kBK - 1) / kBK;
@@ -596,7 +621,10 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
             // Equal parts of every tile, where there are workers for two at least: a worker then has one piece, not the
             // end of one tile and the start of another, each of which costs what adding a piece costs.
             const int most = KIND == GR_WGRAD ? 0 : min(workers / p.tiles, nkc / kMinStretch);
-            const int adding = 8 + a.bn / 32;
+            const int n = min(a.bn, (rows_all + ngroups - 1) / ngroups + 15);  // columns of a tile, about
+            const int cols = KIND == GR_WGRAD ? a.bn : n;
+            const int block = max(27 * cols / 10, (16384 + 128 * a.bn) / 56);
+            const int adding = (1500 + 70 * cols) / block + 1;
             const int even = most >= 2 ? (nkc + most - 1) / most + adding : 1 << 30;
             const int mixed = stretch + adding + adding / 2;
             if (whole > min(even, mixed)) {
@@ -627,18 +655,17 @@ __device__ __forceinline__ int b_blocks(const GroupedArgs &a, const Tile &w) {  
     return KIND == GR_WGRAD ? (a.b_split ? (cols + 63) / 64 : (kPair ? a.bn / 2 : a.bn) / 64) : 1;
 }
 template <int KIND, bool kPair>
-__device__ __forceinline__ uint32_t b_bytes(const GroupedArgs &a, const Tile &w) {
-    return KIND == GR_WGRAD ? uint32_t(b_blocks<KIND, kPair>(a, w)) * 8192u : uint32_t(kPair ? a.bn / 2 : a.bn) * 128u;
+__device__ __forceinline__ uint32_t b_bytes(const GroupedArgs &a, int blocks) {
+    return KIND == GR_WGRAD ? uint32_t(blocks) * 8192u : uint32_t(kPair ? a.bn / 2 : a.bn) * 128u;
 }
 
 // WGRAD: rows left .. 16*steps - 1 of every 64-column block of the stage (a row is 128 bytes of a block) become
 // zeros, by one warp; then the async proxy may read them
 __device__ __forceinline__ void zero_tail(uint8_t *st, int left, int steps, int blocks, int lane) {
     const int per = (16 * steps - left) * 8;  // 16-byte pieces per block; the blocks of X, then those of dY
-    for (int i = lane; i < blocks * per; i += 32) {
-        const int blk = i / per, p = i % per;
-        *reinterpret_cast<uint4 *>(st + blk * 8192 + left * 128 + p * 16) = make_uint4(0u, 0u, 0u, 0u);
-    }
+    for (int blk = 0; blk < blocks; ++blk)
+        for (int p = lane; p < per; p += 32)
+            *reinterpret_cast<uint4 *>(st + blk * 8192 + left * 128 + p * 16) = make_uint4(0u, 0u, 0u, 0u);
     ptx::fence_proxy_async_smem();
     __syncwarp();
 }
@@ -774,16 +801,6 @@ __device__ __forceinline__ void finish_pieces(const GroupedArgs &a, const Tile &
 
 // LORA, a tile with rows of several requests: the adapters' second product on the CUDA cores, in fp32.  Each row takes
 // its own adapter's B and nothing of another's, so a NaN in an adapter stays with its requests.
-// The adapter of a row of the batch: its request is the last that starts at or before it.
-__device__ __forceinline__ int adapter_of(const Table &tab, int groups, int row) {
-    int lo = 0, hi = groups - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (tab.off[mid] <= row) lo = mid;
-        else hi = mid - 1;
-    }
-    return tab.ad[lo];
-}
 // x: this lane's 8 features (from f on) of one row; four lanes cover a row's 32 features, eight rows go side by side
 // with an adapter each, and lanes of one adapter read the same addresses.
 __device__ __forceinline__ void add_low_rank(float (&x)[8], const GroupedArgs &a, int ad, int row, int f) {
@@ -963,7 +980,7 @@ __device__ __forceinline__ int next_fragment(int c) {
 // The copies of block kb into a stage, completing on `bar` (kShared: a barrier of either CTA of the pair)
 template <int KIND, bool kShared>
 __device__ __forceinline__ void stage_loads(const GroupedArgs &a, const Tile &w, uint32_t sa, uint32_t sb, uint32_t bar,
-                                            int kb, int col0, int bblk) {
+                                            int kb, int col0, int blocks) {
     const int k0 = kb * kBK;
     if constexpr (KIND == GR_WGRAD) {
         const int y = w.row0 + k0;
@@ -977,7 +994,7 @@ __device__ __forceinline__ void stage_loads(const GroupedArgs &a, const Tile &w,
             else ptx::tma_load_3d(sa, &a.tmap_a, bar, 0, y, w.f0 / 64);
         }
         if (a.b_split) {
-            for (int i = 0; i < bblk; ++i) {
+            for (int i = 0; i < blocks; ++i) {
                 if constexpr (kShared) ptx::tma_load_2d_pair(sb + i * 8192, &a.tmap_b, bar, col0 + 64 * i, y);
                 else ptx::tma_load_2d(sb + i * 8192, &a.tmap_b, bar, col0 + 64 * i, y);
             }
@@ -1094,8 +1111,8 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
             while (ok && walk.next(w)) {
                 const int cols = kPair ? w.nm / 2 : w.nm;  // columns this CTA stages
                 const int col0 = w.col0 + int(crank) * cols;
-                const int bblk = b_blocks<KIND, kPair>(a, w);
-                const uint32_t own = uint32_t(a.a_blocks) * 8192u + b_bytes<KIND, kPair>(a, w);
+                const int blocks = b_blocks<KIND, kPair>(a, w);
+                const uint32_t own = uint32_t(a.a_blocks) * 8192u + b_bytes<KIND, kPair>(a, blocks);
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     if (!ptx::mbar_try_wait(B.empty0 + 8 * s, ph ^ 1u)) {
                         ok = ptx::mbar_wait_bounded(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
@@ -1114,8 +1131,8 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                         else ptx::mbar_arrive_cluster_relaxed(full_lead + 8 * s);  // the loads count bytes
                     }
                     if (kPair && !(tail && !leader))
-                        stage_loads<KIND, true>(a, w, sa, sb, full_lead + 8 * s, kb, col0, bblk);
-                    else stage_loads<KIND, false>(a, w, sa, sb, B.full0 + 8 * s, kb, col0, bblk);
+                        stage_loads<KIND, true>(a, w, sa, sb, full_lead + 8 * s, kb, col0, blocks);
+                    else stage_loads<KIND, false>(a, w, sa, sb, B.full0 + 8 * s, kb, col0, blocks);
                     ++it;
                     if (++s == uint32_t(stages)) {
                         s = 0;
@@ -1304,7 +1321,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                         for (int i = 0; i < 4; ++i) {
                             const int j = c + (lane >> 2) + 8 * i;
                             if ((c / 8 + i) % parts != part || j >= w.n) continue;
-                            const int ad = adapter_of(tab, a.groups, w.col0 + j);
+                            const int ad = tab.ad[request_of(tab, a.groups, w.col0 + j)];
                             const int f8 = w.f0 + q * 32 + (lane & 3) * 8;
                             if (ad < 0 || f8 >= a.F) continue;
                             const uint16_t *b = static_cast<const uint16_t *>(a.lora_b) + size_t(ad) * a.rank * a.F + f8;
@@ -1329,7 +1346,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                         for (int k = 0; k < 8; ++k) low[k] = 0.f;
                         const int j = c + (lane >> 2) + 8 * i, f8 = w.f0 + q * 32 + (lane & 3) * 8;
                         if (j < w.n && f8 < a.F)
-                            add_low_rank(low, a, adapter_of(tab, a.groups, w.col0 + j), w.col0 + j, f8);
+                            add_low_rank(low, a, tab.ad[request_of(tab, a.groups, w.col0 + j)], w.col0 + j, f8);
                     }
                 }
             }
@@ -1364,7 +1381,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
 #pragma unroll
                                     for (int k = 0; k < 8; ++k) x[k] += low[k];
                                 } else if ((c / 8 + i) % parts == part) {
-                                    add_low_rank(x, a, adapter_of(tab, a.groups, row), row, f8);
+                                    add_low_rank(x, a, tab.ad[request_of(tab, a.groups, row)], row, f8);
                                 }
                                 float4 *d = reinterpret_cast<float4 *>(p);
                                 __stcg(d, make_float4(x[0], x[1], x[2], x[3]));
@@ -1429,7 +1446,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
 #pragma unroll
                             for (int k = 0; k < 8; ++k) x[k] += low[k];
                         } else if (parts > 0) {
-                            add_low_rank(x, a, adapter_of(tab, a.groups, row), row, f8);
+                            add_low_rank(x, a, tab.ad[request_of(tab, a.groups, row)], row, f8);
                         }
                         uint32_t p[4];
 #pragma unroll

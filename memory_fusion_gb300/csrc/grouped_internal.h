@@ -21,7 +21,7 @@ constexpr int kGroupedMaxSmem = 232448;   // dynamic shared memory of a CTA (227
 constexpr int kGroupedMaxGroups = 1024;  // the group table lives in shared memory
 constexpr int kGroupedSplitTiles = 1024; // tiles whose contraction may be divided among CTAs
 constexpr int kGroupedWorkers = 160;     // CTAs that may hold a piece of a tile (a GB300 has 152 SMs)
-constexpr int kLoraShortRows = 8;        // rows up to which a request's X . A runs on the CUDA cores
+constexpr int kLoraShortRows = 4;        // rows up to which a request's X . A runs on the CUDA cores
 constexpr int kLoraMaxSplit = 8;         // parts of their contraction
 constexpr int kLoraMaxRank = 128;        // one tile of features in the first product
 
