@@ -88,6 +88,13 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
+// one lane of a converged warp, the same one every time
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0u;
+}
+
 }  // namespace ptx
 
 namespace {
@@ -104,9 +111,14 @@ __device__ __forceinline__ uint32_t idesc_f16(int m, int n, bool fp16, bool a_mn
 // with its short requests.  A decode batch's SHRINK and LORA share the SMs, one CTA of each: 256 threads of 96
 // registers and 320 of 128 are what an SM has.
 __host__ __device__ constexpr int epi_warps(int kind) { return kind == GR_SHRINK ? 4 : 8; }
-__host__ __device__ constexpr int threads_of(int kind) { return kind == GR_SHRINK ? 256 : 320; }
+__host__ __device__ constexpr bool two_producers(int kind, bool pair) {
+    return kind != GR_SHRINK && (kind != GR_LORA || pair);
+}
+__host__ __device__ constexpr int threads_of(int kind, bool pair) {
+    return kind == GR_SHRINK ? 256 : two_producers(kind, pair) ? 352 : 320;
+}
 __host__ __device__ constexpr int registers_of(int kind, bool pair) {
-    return kind == GR_SHRINK ? 96 : kind == GR_LORA && !pair ? 128 : 200;
+    return kind == GR_SHRINK ? 96 : kind == GR_LORA && !pair ? 128 : 184;
 }
 constexpr int kShortWarps = 6;
 constexpr int kBK = 64;         // contraction per stage (128 bytes: one swizzle atom)
@@ -971,52 +983,203 @@ __device__ __forceinline__ void issue_commit(uint32_t bar) {
     if constexpr (kPair) ptx::mma_commit_pair_mc(bar, 3);
     else ptx::mma_commit(bar);
 }
+// A value that every lane of the warp holds alike, known to be.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// The bounded wait of a whole warp, one verdict.
+template <bool kClusterScope = false>
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_t tmo, volatile uint32_t *abort,
+                                          uint32_t *err, uint32_t info) {
+    const bool now = kClusterScope ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, now)) return true;
+    return __all_sync(0xffffffffu, ptx::mbar_wait_bounded<kClusterScope>(bar, parity, tmo, abort, err, info)) != 0;
+}
+
+// The four MMAs of a 64-deep block and the commit that frees its stage (pair: in both CTAs), issued by one elected lane
+// of a converged warp.  kA, kB: from 16 of the contraction to the next, in descriptor units.
+template <bool kPair, int kA, int kB>
+__device__ __forceinline__ void mma_block(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate,
+                                          uint32_t bar) {
+    if constexpr (kPair) {
+        asm volatile(
+            "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a, b;\n\t.reg .b16 m;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\tmov.b16 m, 3;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+            "add.s64 a, %1, %6;\n\tadd.s64 b, %2, %7;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, %1, %8;\n\tadd.s64 b, %2, %9;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, %1, %10;\n\tadd.s64 b, %2, %11;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n\t"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], m;\n\t}"
+            ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(bar), "n"(kA), "n"(kB), "n"(2 * kA), "n"(2 * kB),
+            "n"(3 * kA), "n"(3 * kB)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a, b;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+            "add.s64 a, %1, %6;\n\tadd.s64 b, %2, %7;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, %1, %8;\n\tadd.s64 b, %2, %9;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, %1, %10;\n\tadd.s64 b, %2, %11;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
+            ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(bar), "n"(kA), "n"(kB), "n"(2 * kA), "n"(2 * kB),
+            "n"(3 * kA), "n"(3 * kB)
+            : "memory");
+    }
+}
+
 // the 32-column fragment behind c of those that a half takes: spans of kSpan columns, one of kHalves
 template <int kSpan, int kHalves>
 __device__ __forceinline__ int next_fragment(int c) {
     return kSpan == 64 && (c & 32) == 0 ? c + 32 : c + 32 + (kHalves - 1) * kSpan;
 }
 
-// The copies of block kb into a stage, completing on `bar` (kShared: a barrier of either CTA of the pair)
-template <int KIND, bool kShared>
+// The copies of block kb into a stage, completing on `bar` (kShared: a barrier of either CTA of the pair): the feature
+// operand, the column operand, or both
+template <int KIND, bool kShared, bool kFeatures, bool kColumns>
 __device__ __forceinline__ void stage_loads(const GroupedArgs &a, const Tile &w, uint32_t sa, uint32_t sb, uint32_t bar,
                                             int kb, int col0, int blocks) {
     const int k0 = kb * kBK;
     if constexpr (KIND == GR_WGRAD) {
         const int y = w.row0 + k0;
-        if (a.a_split) {
-            for (int i = 0; i < a.a_blocks; ++i) {
-                if constexpr (kShared) ptx::tma_load_2d_pair(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, y);
-                else ptx::tma_load_2d(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, y);
+        if constexpr (kFeatures) {
+            if (a.a_split) {
+                for (int i = 0; i < a.a_blocks; ++i) {
+                    if constexpr (kShared) ptx::tma_load_2d_pair(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, y);
+                    else ptx::tma_load_2d(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, y);
+                }
+            } else {
+                if constexpr (kShared) ptx::tma_load_3d_pair(sa, &a.tmap_a, bar, 0, y, w.f0 / 64);
+                else ptx::tma_load_3d(sa, &a.tmap_a, bar, 0, y, w.f0 / 64);
             }
-        } else {
-            if constexpr (kShared) ptx::tma_load_3d_pair(sa, &a.tmap_a, bar, 0, y, w.f0 / 64);
-            else ptx::tma_load_3d(sa, &a.tmap_a, bar, 0, y, w.f0 / 64);
         }
-        if (a.b_split) {
-            for (int i = 0; i < blocks; ++i) {
-                if constexpr (kShared) ptx::tma_load_2d_pair(sb + i * 8192, &a.tmap_b, bar, col0 + 64 * i, y);
-                else ptx::tma_load_2d(sb + i * 8192, &a.tmap_b, bar, col0 + 64 * i, y);
+        if constexpr (kColumns) {
+            if (a.b_split) {
+                for (int i = 0; i < blocks; ++i) {
+                    if constexpr (kShared) ptx::tma_load_2d_pair(sb + i * 8192, &a.tmap_b, bar, col0 + 64 * i, y);
+                    else ptx::tma_load_2d(sb + i * 8192, &a.tmap_b, bar, col0 + 64 * i, y);
+                }
+            } else {
+                if constexpr (kShared) ptx::tma_load_3d_pair(sb, &a.tmap_b, bar, 0, y, col0 / 64);
+                else ptx::tma_load_3d(sb, &a.tmap_b, bar, 0, y, col0 / 64);
             }
-        } else {
-            if constexpr (kShared) ptx::tma_load_3d_pair(sb, &a.tmap_b, bar, 0, y, col0 / 64);
-            else ptx::tma_load_3d(sb, &a.tmap_b, bar, 0, y, col0 / 64);
         }
     } else {
-        if constexpr (KIND == GR_DGRAD) {
-            if constexpr (kShared) ptx::tma_load_3d_pair(sa, &a.tmap_a, bar, k0, w.f0, w.w);
-            else ptx::tma_load_3d(sa, &a.tmap_a, bar, k0, w.f0, w.w);
-        } else if (a.a_split) {
-            for (int i = 0; i < a.a_blocks; ++i) {
-                if constexpr (kShared) ptx::tma_load_3d_pair(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, k0, w.w);
-                else ptx::tma_load_3d(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, k0, w.w);
+        if constexpr (kFeatures) {
+            if constexpr (KIND == GR_DGRAD) {
+                if constexpr (kShared) ptx::tma_load_3d_pair(sa, &a.tmap_a, bar, k0, w.f0, w.w);
+                else ptx::tma_load_3d(sa, &a.tmap_a, bar, k0, w.f0, w.w);
+            } else if (a.a_split) {
+                for (int i = 0; i < a.a_blocks; ++i) {
+                    if constexpr (kShared) ptx::tma_load_3d_pair(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, k0, w.w);
+                    else ptx::tma_load_3d(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, k0, w.w);
+                }
+            } else {
+                if constexpr (kShared) ptx::tma_load_4d_pair(sa, &a.tmap_a, bar, 0, k0, w.f0 / 64, w.w);
+                else ptx::tma_load_4d(sa, &a.tmap_a, bar, 0, k0, w.f0 / 64, w.w);
             }
-        } else {
-            if constexpr (kShared) ptx::tma_load_4d_pair(sa, &a.tmap_a, bar, 0, k0, w.f0 / 64, w.w);
-            else ptx::tma_load_4d(sa, &a.tmap_a, bar, 0, k0, w.f0 / 64, w.w);
         }
-        if constexpr (kShared) ptx::tma_load_2d_pair(sb, &a.tmap_b, bar, k0, col0);
-        else ptx::tma_load_2d(sb, &a.tmap_b, bar, k0, col0);
+        if constexpr (kColumns) {
+            if constexpr (kShared) ptx::tma_load_2d_pair(sb, &a.tmap_b, bar, k0, col0);
+            else ptx::tma_load_2d(sb, &a.tmap_b, bar, k0, col0);
+        }
+    }
+}
+
+// The producer loop of one thread.  Two threads of different warps share the work where there are two (each copy
+// instruction keeps its thread busy for some 250 cycles): one stages the feature operand and speaks for the stage,
+// the other the column operand.
+template <int KIND, bool kPair, bool kFeatures, bool kColumns>
+__device__ __forceinline__ void produce(const GroupedArgs &a, Walk<KIND, kPair> &walk, const GrLayout &L, const GrBars &B,
+                                        uint32_t base, uint32_t crank, uint64_t tmo, volatile uint32_t *abort) {
+    const int stages = a.stages;
+    const bool leader = crank == 0u;
+    const uint32_t full_lead = kPair ? ptx::mapa(B.full0, 0u) : B.full0;
+    uint32_t it = 0, s = 0, ph = 0;
+    bool ok = true;
+    Tile w;
+    while (ok && walk.next(w)) {
+        const int cols = kPair ? w.nm / 2 : w.nm;  // columns this CTA stages
+        const int col0 = w.col0 + int(crank) * cols;
+        const int blocks = b_blocks<KIND, kPair>(a, w);
+        const uint32_t own = uint32_t(a.a_blocks) * 8192u + b_bytes<KIND, kPair>(a, blocks);
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+            if (!ptx::mbar_try_wait(B.empty0 + 8 * s, ph ^ 1u)) {
+                ok = ptx::mbar_wait_bounded(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
+                if (!ok) break;
+            }
+            const uint32_t sa = base + s * L.stage_bytes;
+            const uint32_t sb = sa + L.a_bytes;
+            // A pair's loads complete on the leader's barrier.  (WGRAD: but for a group's last block where it
+            // has to be zeroed behind the rows; the second CTA's part then completes on its own barrier, its
+            // warp 1 zeroes and arrives.)
+            const bool tail = kPair && KIND == GR_WGRAD && kb == w.nk - 1 && (w.rows & 15) != 0;
+            if constexpr (kFeatures) {
+                if (!kPair || leader) {
+                    ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, kPair && !tail ? 2 * own : own);
+                } else if (KIND == GR_WGRAD) {
+                    if (tail) ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, own);
+                    else ptx::mbar_arrive_cluster_relaxed(full_lead + 8 * s);  // the loads count bytes
+                }
+            }
+            if (kPair && !(tail && !leader))
+                stage_loads<KIND, true, kFeatures, kColumns>(a, w, sa, sb, full_lead + 8 * s, kb, col0, blocks);
+            else stage_loads<KIND, false, kFeatures, kColumns>(a, w, sa, sb, B.full0 + 8 * s, kb, col0, blocks);
+            ++it;
+            if (++s == uint32_t(stages)) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        if constexpr (KIND == GR_LORA) {
+            // the low-rank product of a tile with one adapter: blocks of 64 ranks, H's upper parts, then its
+            // lower ones, against the same rows of B
+            if (w.extra > 0) ptx::griddep_wait();  // H is the previous grid's
+            for (int x = 0; x < w.extra && ok; ++x) {
+                ok = ptx::mbar_wait_bounded(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
+                if (!ok) break;
+                const int r0 = (x >> 1) * kBK;
+                const uint32_t sa = base + s * L.stage_bytes;
+                const uint32_t bar = full_lead + 8 * s;
+                if constexpr (kFeatures) {
+                    if (leader) ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, kPair ? 2 * own : own);
+                    if (a.a_split) {
+                        for (int i = 0; i < a.a_blocks; ++i) {
+                            if constexpr (kPair)
+                                ptx::tma_load_3d_pair(sa + i * 8192, &a.tmap_lb, bar, w.f0 + 64 * i, r0, w.ad);
+                            else ptx::tma_load_3d(sa + i * 8192, &a.tmap_lb, bar, w.f0 + 64 * i, r0, w.ad);
+                        }
+                    } else {
+                        if constexpr (kPair) ptx::tma_load_4d_pair(sa, &a.tmap_lb, bar, 0, r0, w.f0 / 64, w.ad);
+                        else ptx::tma_load_4d(sa, &a.tmap_lb, bar, 0, r0, w.f0 / 64, w.ad);
+                    }
+                }
+                if constexpr (kColumns) {
+                    const int xh = (x & 1) * a.rank + r0;
+                    if constexpr (kPair) ptx::tma_load_2d_pair(sa + L.a_bytes, &a.tmap_h, bar, xh, col0);
+                    else ptx::tma_load_2d(sa + L.a_bytes, &a.tmap_h, bar, xh, col0);
+                }
+                ++it;
+                if (++s == uint32_t(stages)) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+    }
+    // every load has landed and been read before the CTA may leave
+    const uint32_t first = it > uint32_t(stages) ? it - uint32_t(stages) : 0u;
+    for (uint32_t i = first; i < it; ++i) {
+        volatile uint32_t local_abort = 0;
+        ptx::mbar_wait_bounded(B.empty0 + 8 * (i % uint32_t(stages)), (i / uint32_t(stages)) & 1u, tmo, &local_abort,
+                               nullptr, 0);
     }
 }
 
@@ -1029,8 +1192,9 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
         if (threadIdx.x == 0) ptx::record_error(a.err, 8u, 0x60000000u | (base & 1023u));
         return;
     }
-    constexpr int kEpiWarps = epi_warps(KIND), kThreads = threads_of(KIND), kHalves = kEpiWarps / 4,
+    constexpr int kEpiWarps = epi_warps(KIND), kThreads = threads_of(KIND, kPair), kHalves = kEpiWarps / 4,
                   kSpan = KIND == GR_WGRAD ? 64 : 32;
+    constexpr bool kTwo = two_producers(KIND, kPair);
     constexpr bool kAMn = KIND != GR_DGRAD;  // features contiguous in memory: A is MN-major
     constexpr bool kBMn = KIND == GR_WGRAD;
     const int stages = a.stages;
@@ -1104,80 +1268,10 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            uint32_t it = 0, s = 0, ph = 0;
-            bool ok = true;
-            const uint32_t full_lead = kPair ? ptx::mapa(B.full0, 0u) : B.full0;
-            while (ok && walk.next(w)) {
-                const int cols = kPair ? w.nm / 2 : w.nm;  // columns this CTA stages
-                const int col0 = w.col0 + int(crank) * cols;
-                const int blocks = b_blocks<KIND, kPair>(a, w);
-                const uint32_t own = uint32_t(a.a_blocks) * 8192u + b_bytes<KIND, kPair>(a, blocks);
-                for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                    if (!ptx::mbar_try_wait(B.empty0 + 8 * s, ph ^ 1u)) {
-                        ok = ptx::mbar_wait_bounded(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
-                        if (!ok) break;
-                    }
-                    const uint32_t sa = base + s * L.stage_bytes;
-                    const uint32_t sb = sa + L.a_bytes;
-                    // A pair's loads complete on the leader's barrier.  (WGRAD: but for a group's last block where it
-                    // has to be zeroed behind the rows; the second CTA's part then completes on its own barrier, its
-                    // warp 1 zeroes and arrives.)
-                    const bool tail = kPair && KIND == GR_WGRAD && kb == w.nk - 1 && (w.rows & 15) != 0;
-                    if (!kPair || leader) {
-                        ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, kPair && !tail ? 2 * own : own);
-                    } else if (KIND == GR_WGRAD) {
-                        if (tail) ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, own);
-                        else ptx::mbar_arrive_cluster_relaxed(full_lead + 8 * s);  // the loads count bytes
-                    }
-                    if (kPair && !(tail && !leader))
-                        stage_loads<KIND, true>(a, w, sa, sb, full_lead + 8 * s, kb, col0, blocks);
-                    else stage_loads<KIND, false>(a, w, sa, sb, B.full0 + 8 * s, kb, col0, blocks);
-                    ++it;
-                    if (++s == uint32_t(stages)) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
-                }
-                if constexpr (KIND == GR_LORA) {
-                    // the low-rank product of a tile with one adapter: blocks of 64 ranks, H's upper parts, then its
-                    // lower ones, against the same rows of B
-                    if (w.extra > 0) ptx::griddep_wait();  // H is the previous grid's
-                    for (int x = 0; x < w.extra && ok; ++x) {
-                        ok = ptx::mbar_wait_bounded(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
-                        if (!ok) break;
-                        const int r0 = (x >> 1) * kBK;
-                        const uint32_t sa = base + s * L.stage_bytes;
-                        const uint32_t bar = full_lead + 8 * s;
-                        if (leader) ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, kPair ? 2 * own : own);
-                        if (a.a_split) {
-                            for (int i = 0; i < a.a_blocks; ++i) {
-                                if constexpr (kPair) ptx::tma_load_3d_pair(sa + i * 8192, &a.tmap_lb, bar, w.f0 + 64 * i, r0, w.ad);
-                                else ptx::tma_load_3d(sa + i * 8192, &a.tmap_lb, bar, w.f0 + 64 * i, r0, w.ad);
-                            }
-                        } else {
-                            if constexpr (kPair) ptx::tma_load_4d_pair(sa, &a.tmap_lb, bar, 0, r0, w.f0 / 64, w.ad);
-                            else ptx::tma_load_4d(sa, &a.tmap_lb, bar, 0, r0, w.f0 / 64, w.ad);
-                        }
-                        const int xh = (x & 1) * a.rank + r0;
-                        if constexpr (kPair) ptx::tma_load_2d_pair(sa + L.a_bytes, &a.tmap_h, bar, xh, col0);
-                        else ptx::tma_load_2d(sa + L.a_bytes, &a.tmap_h, bar, xh, col0);
-                        ++it;
-                        if (++s == uint32_t(stages)) {
-                            s = 0;
-                            ph ^= 1u;
-                        }
-                    }
-                }
-            }
-            // every load has landed and been read before the CTA may leave
-            const uint32_t first = it > uint32_t(stages) ? it - uint32_t(stages) : 0u;
-            for (uint32_t i = first; i < it; ++i) {
-                volatile uint32_t local_abort = 0;
-                ptx::mbar_wait_bounded(B.empty0 + 8 * (i % uint32_t(stages)), (i / uint32_t(stages)) & 1u, tmo,
-                                       &local_abort, nullptr, 0);
-            }
-        }
+        if (lane == 0) produce<KIND, kPair, true, !kTwo>(a, walk, L, B, base, crank, tmo, abort);
+        __syncwarp();
+    } else if (kTwo && warp == kThreads / 32 - 1) {
+        if (lane == 0) produce<KIND, kPair, false, true>(a, walk, L, B, base, crank, tmo, abort);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
@@ -1200,69 +1294,58 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                     s = (s + uint32_t(w.nk)) % uint32_t(stages);
                 }
             }
-        } else if (lane == 0 || KIND == GR_WGRAD) {
+        } else {
+            // The whole warp runs the loop, and one lane of it issues: control flow and descriptors that are the warp's
+            // own keep the work between MMA groups short, so that the tensor pipe's queue does not run dry.
             const uint64_t ad0 = kAMn ? sw128_desc(base, 8192, 1024) : sw128_desc(base, 16, 1024);
             const uint64_t bd0 = kBMn ? sw128_desc(base + L.a_bytes, 8192, 1024) : sw128_desc(base + L.a_bytes, 16, 1024);
+            constexpr int kAStep = kAMn ? 128 : 2, kBStep = kBMn ? 128 : 2;  // of 16 in the contraction, descriptor units
+            const uint32_t stage_step = L.stage_bytes >> 4;
+            const bool elected = ptx::elect_one();  // the same lane as in mma_block: commits cover their thread's MMAs
             uint32_t s = 0, ph = 0;
             for (int tile = 0; walk.next(w); ++tile) {
                 const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
                 const uint32_t d = tmem_base + buf * uint32_t(a.bn);
-                const uint32_t idesc = idesc_f16(kPair ? 2 * kFB : kFB, w.nm, a.fp16 != 0, kAMn, kBMn);
-                const int length = KIND == GR_WGRAD ? w.rows : a.C;
+                const uint32_t idesc = idesc_f16(kPair ? 2 * kFB : kFB, uniform(w.nm), a.fp16 != 0, kAMn, kBMn);
+                const int length = KIND == GR_WGRAD ? uniform(w.rows) : a.C;
+                const int kb0 = uniform(w.kb0), kb1 = uniform(w.kb1);
                 // blocks of 64, and where the piece ends with the contraction the shorter one behind them
-                const int whole = min(w.kb1, length / kBK);
-                const int left = w.kb1 > whole ? length - whole * kBK : 0;
+                const int whole = min(kb1, length / kBK);
+                const int left = kb1 > whole ? length - whole * kBK : 0;
+                if (!wait_warp(B.tmem_empty0 + 8 * buf, tph ^ 1u, tmo, abort, a.err, kInfoMma | buf)) break;
+                ptx::tc_fence_after();
                 bool ok = true;
-                if (lane == 0) {
-                    ok = ptx::mbar_wait_bounded(B.tmem_empty0 + 8 * buf, tph ^ 1u, tmo, abort, a.err, kInfoMma | buf);
+                for (int kb = kb0; kb < whole; ++kb) {
+                    ok = wait_warp(B.full0 + 8 * s, ph, tmo, abort, a.err, kInfoMma | 0x100u | s);
+                    if (!ok) break;
                     ptx::tc_fence_after();
-                    // The one issuing thread's work between MMA groups is kept short, so that the tensor pipe's
-                    // queue does not run dry: fixed steps, descriptors by addition.
-                    for (int kb = w.kb0; kb < whole && ok; ++kb) {
-                        const uint32_t fb = B.full0 + 8 * s;
-                        if (!ptx::mbar_try_wait(fb, ph)) {
-                            ok = ptx::mbar_wait_bounded(fb, ph, tmo, abort, a.err, kInfoMma | 0x100u | s);
-                            if (!ok) break;
-                        }
-                        ptx::tc_fence_after();
-                        const uint64_t so = uint64_t((s * L.stage_bytes) >> 4);
-#pragma unroll
-                        for (int k = 0; k < kBK / 16; ++k)
-                            issue_mma<kPair>(d, ad0 + so + uint64_t(k * (kAMn ? 128 : 2)),
-                                             bd0 + so + uint64_t(k * (kBMn ? 128 : 2)), idesc,
-                                             kb > w.kb0 || k > 0 ? 1u : 0u);
-                        issue_commit<kPair>(B.empty0 + 8 * s);
-                        if (++s == uint32_t(stages)) {
-                            s = 0;
-                            ph ^= 1u;
-                        }
+                    const uint64_t so = uint64_t(s * stage_step);
+                    mma_block<kPair, kAStep, kBStep>(d, ad0 + so, bd0 + so, idesc, kb > kb0 ? 1u : 0u, B.empty0 + 8 * s);
+                    if (++s == uint32_t(stages)) {
+                        s = 0;
+                        ph ^= 1u;
                     }
-                }
-                if constexpr (KIND == GR_WGRAD) {
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    s = __shfl_sync(0xffffffffu, s, 0);
-                    ph = __shfl_sync(0xffffffffu, ph, 0);
                 }
                 if (ok && left > 0) {
-                    const uint32_t fb = B.full0 + 8 * s;
                     const int steps = (left + 15) / 16;
                     // (a WGRAD pair: the peer's zeroes are behind its arrival)
-                    ok = ptx::mbar_wait_bounded<kPair && KIND == GR_WGRAD>(fb, ph, tmo, abort, a.err,
-                                                                           kInfoMma | 0x100u | s);
-                    if constexpr (KIND == GR_WGRAD) {
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (ok && (left & 15) != 0)
-                            zero_tail(smem_raw + s * L.stage_bytes, left, steps,
-                                      a.a_blocks + ((kPair ? w.nm / 2 : w.nm) + 63) / 64, lane);
-                    }
-                    if (ok && lane == 0) {
+                    ok = wait_warp<kPair && KIND == GR_WGRAD>(B.full0 + 8 * s, ph, tmo, abort, a.err,
+                                                              kInfoMma | 0x100u | s);
+                    if (ok) {
+                        if constexpr (KIND == GR_WGRAD) {
+                            if ((left & 15) != 0)
+                                zero_tail(smem_raw + s * L.stage_bytes, left, steps,
+                                          a.a_blocks + ((kPair ? w.nm / 2 : w.nm) + 63) / 64, lane);
+                        }
                         ptx::tc_fence_after();
-                        const uint64_t so = uint64_t((s * L.stage_bytes) >> 4);
-                        for (int k = 0; k < steps; ++k)
-                            issue_mma<kPair>(d, ad0 + so + uint64_t(k * (kAMn ? 128 : 2)),
-                                             bd0 + so + uint64_t(k * (kBMn ? 128 : 2)), idesc,
-                                             whole > w.kb0 || k > 0 ? 1u : 0u);
-                        issue_commit<kPair>(B.empty0 + 8 * s);
+                        const uint64_t so = uint64_t(s * stage_step);
+                        if (elected) {
+                            for (int k = 0; k < steps; ++k)
+                                issue_mma<kPair>(d, ad0 + so + uint64_t(k * kAStep), bd0 + so + uint64_t(k * kBStep), idesc,
+                                                 whole > kb0 || k > 0 ? 1u : 0u);
+                            issue_commit<kPair>(B.empty0 + 8 * s);
+                        }
+                        __syncwarp();
                     }
                     if (++s == uint32_t(stages)) {
                         s = 0;
@@ -1270,16 +1353,21 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                     }
                 }
                 if constexpr (KIND == GR_LORA) {
-                    for (int x = 0; x < w.extra && ok; ++x) {
-                        ok = ptx::mbar_wait_bounded(B.full0 + 8 * s, ph, tmo, abort, a.err, kInfoMma | 0x400u | s);
+                    const int extra = uniform(w.extra);
+                    for (int x = 0; x < extra && ok; ++x) {
+                        ok = wait_warp(B.full0 + 8 * s, ph, tmo, abort, a.err, kInfoMma | 0x400u | s);
                         if (!ok) break;
                         ptx::tc_fence_after();
                         const int ranks = a.rank - (x >> 1) * kBK;
                         const int steps = ranks >= kBK ? kBK / 16 : (ranks + 15) / 16;
-                        const uint64_t so = uint64_t((s * L.stage_bytes) >> 4);
-                        for (int k = 0; k < steps; ++k)
-                            issue_mma<kPair>(d, ad0 + so + uint64_t(k * 128), bd0 + so + uint64_t(k * 2), idesc, 1u);
-                        issue_commit<kPair>(B.empty0 + 8 * s);
+                        const uint64_t so = uint64_t(s * stage_step);
+                        if (elected) {
+                            for (int k = 0; k < steps; ++k)
+                                issue_mma<kPair>(d, ad0 + so + uint64_t(k * kAStep), bd0 + so + uint64_t(k * kBStep), idesc,
+                                                 1u);
+                            issue_commit<kPair>(B.empty0 + 8 * s);
+                        }
+                        __syncwarp();
                         if (++s == uint32_t(stages)) {
                             s = 0;
                             ph ^= 1u;
@@ -1287,9 +1375,10 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                     }
                 }
                 if (!ok) break;
-                if (lane == 0) issue_commit<kPair>(B.tmem_full0 + 8 * buf);
+                if (elected) issue_commit<kPair>(B.tmem_full0 + 8 * buf);
+                __syncwarp();
             }
-            if (lane == 0) {
+            if (elected) {
                 if constexpr (kPair) ptx::mma_commit_pair_mc(B.mma_done, 1);
                 else ptx::mma_commit(B.mma_done);
                 volatile uint32_t local_abort = 0;
@@ -1554,7 +1643,7 @@ cudaError_t launch_grouped(int kind, const GroupedArgs &a, int ctas, int smem, b
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(threads_of(kind));
+    cfg.blockDim = dim3(threads_of(kind, pair));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
