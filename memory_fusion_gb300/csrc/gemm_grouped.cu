@@ -111,14 +111,9 @@ __device__ __forceinline__ uint32_t idesc_f16(int m, int n, bool fp16, bool a_mn
 // with its short requests.  A decode batch's SHRINK and LORA share the SMs, one CTA of each: 256 threads of 96
 // registers and 320 of 128 are what an SM has.
 __host__ __device__ constexpr int epi_warps(int kind) { return kind == GR_SHRINK ? 4 : 8; }
-__host__ __device__ constexpr bool two_producers(int kind, bool pair) {
-    return kind != GR_SHRINK && (kind != GR_LORA || pair);
-}
-__host__ __device__ constexpr int threads_of(int kind, bool pair) {
-    return kind == GR_SHRINK ? 256 : two_producers(kind, pair) ? 352 : 320;
-}
+__host__ __device__ constexpr int threads_of(int kind) { return kind == GR_SHRINK ? 256 : 320; }
 __host__ __device__ constexpr int registers_of(int kind, bool pair) {
-    return kind == GR_SHRINK ? 96 : kind == GR_LORA && !pair ? 128 : 184;
+    return kind == GR_SHRINK ? 96 : kind == GR_LORA && !pair ? 128 : 200;
 }
 constexpr int kShortWarps = 6;
 constexpr int kBK = 64;         // contraction per stage (128 bytes: one swizzle atom)
@@ -983,18 +978,6 @@ __device__ __forceinline__ void issue_commit(uint32_t bar) {
     if constexpr (kPair) ptx::mma_commit_pair_mc(bar, 3);
     else ptx::mma_commit(bar);
 }
-// A value that every lane of the warp holds alike, known to be.
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
-
-// The bounded wait of a whole warp, one verdict.
-template <bool kClusterScope = false>
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_t tmo, volatile uint32_t *abort,
-                                          uint32_t *err, uint32_t info) {
-    const bool now = kClusterScope ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
-    if (__all_sync(0xffffffffu, now)) return true;
-    return __all_sync(0xffffffffu, ptx::mbar_wait_bounded<kClusterScope>(bar, parity, tmo, abort, err, info)) != 0;
-}
-
 // The four MMAs of a 64-deep block and the commit that frees its stage (pair: in both CTAs), issued by one elected lane
 // of a converged warp.  kA, kB: from 16 of the contraction to the next, in descriptor units.
 template <bool kPair, int kA, int kB>
@@ -1041,97 +1024,99 @@ __device__ __forceinline__ int next_fragment(int c) {
     return kSpan == 64 && (c & 32) == 0 ? c + 32 : c + 32 + (kHalves - 1) * kSpan;
 }
 
-// The copies of block kb into a stage, completing on `bar` (kShared: a barrier of either CTA of the pair): the feature
-// operand, the column operand, or both
-template <int KIND, bool kShared, bool kFeatures, bool kColumns>
+// The copies of block kb into a stage, completing on `bar` (kShared: a barrier of either CTA of the pair)
+template <int KIND, bool kShared>
 __device__ __forceinline__ void stage_loads(const GroupedArgs &a, const Tile &w, uint32_t sa, uint32_t sb, uint32_t bar,
                                             int kb, int col0, int blocks) {
     const int k0 = kb * kBK;
     if constexpr (KIND == GR_WGRAD) {
         const int y = w.row0 + k0;
-        if constexpr (kFeatures) {
-            if (a.a_split) {
-                for (int i = 0; i < a.a_blocks; ++i) {
-                    if constexpr (kShared) ptx::tma_load_2d_pair(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, y);
-                    else ptx::tma_load_2d(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, y);
-                }
-            } else {
-                if constexpr (kShared) ptx::tma_load_3d_pair(sa, &a.tmap_a, bar, 0, y, w.f0 / 64);
-                else ptx::tma_load_3d(sa, &a.tmap_a, bar, 0, y, w.f0 / 64);
+        if (a.a_split) {
+            for (int i = 0; i < a.a_blocks; ++i) {
+                if constexpr (kShared) ptx::tma_load_2d_pair(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, y);
+                else ptx::tma_load_2d(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, y);
             }
+        } else {
+            if constexpr (kShared) ptx::tma_load_3d_pair(sa, &a.tmap_a, bar, 0, y, w.f0 / 64);
+            else ptx::tma_load_3d(sa, &a.tmap_a, bar, 0, y, w.f0 / 64);
         }
-        if constexpr (kColumns) {
-            if (a.b_split) {
-                for (int i = 0; i < blocks; ++i) {
-                    if constexpr (kShared) ptx::tma_load_2d_pair(sb + i * 8192, &a.tmap_b, bar, col0 + 64 * i, y);
-                    else ptx::tma_load_2d(sb + i * 8192, &a.tmap_b, bar, col0 + 64 * i, y);
-                }
-            } else {
-                if constexpr (kShared) ptx::tma_load_3d_pair(sb, &a.tmap_b, bar, 0, y, col0 / 64);
-                else ptx::tma_load_3d(sb, &a.tmap_b, bar, 0, y, col0 / 64);
+        if (a.b_split) {
+            for (int i = 0; i < blocks; ++i) {
+                if constexpr (kShared) ptx::tma_load_2d_pair(sb + i * 8192, &a.tmap_b, bar, col0 + 64 * i, y);
+                else ptx::tma_load_2d(sb + i * 8192, &a.tmap_b, bar, col0 + 64 * i, y);
             }
+        } else {
+            if constexpr (kShared) ptx::tma_load_3d_pair(sb, &a.tmap_b, bar, 0, y, col0 / 64);
+            else ptx::tma_load_3d(sb, &a.tmap_b, bar, 0, y, col0 / 64);
         }
     } else {
-        if constexpr (kFeatures) {
-            if constexpr (KIND == GR_DGRAD) {
-                if constexpr (kShared) ptx::tma_load_3d_pair(sa, &a.tmap_a, bar, k0, w.f0, w.w);
-                else ptx::tma_load_3d(sa, &a.tmap_a, bar, k0, w.f0, w.w);
-            } else if (a.a_split) {
-                for (int i = 0; i < a.a_blocks; ++i) {
-                    if constexpr (kShared) ptx::tma_load_3d_pair(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, k0, w.w);
-                    else ptx::tma_load_3d(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, k0, w.w);
-                }
-            } else {
-                if constexpr (kShared) ptx::tma_load_4d_pair(sa, &a.tmap_a, bar, 0, k0, w.f0 / 64, w.w);
-                else ptx::tma_load_4d(sa, &a.tmap_a, bar, 0, k0, w.f0 / 64, w.w);
+        if constexpr (KIND == GR_DGRAD) {
+            if constexpr (kShared) ptx::tma_load_3d_pair(sa, &a.tmap_a, bar, k0, w.f0, w.w);
+            else ptx::tma_load_3d(sa, &a.tmap_a, bar, k0, w.f0, w.w);
+        } else if (a.a_split) {
+            for (int i = 0; i < a.a_blocks; ++i) {
+                if constexpr (kShared) ptx::tma_load_3d_pair(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, k0, w.w);
+                else ptx::tma_load_3d(sa + i * 8192, &a.tmap_a, bar, w.f0 + 64 * i, k0, w.w);
             }
+        } else {
+            if constexpr (kShared) ptx::tma_load_4d_pair(sa, &a.tmap_a, bar, 0, k0, w.f0 / 64, w.w);
+            else ptx::tma_load_4d(sa, &a.tmap_a, bar, 0, k0, w.f0 / 64, w.w);
         }
-        if constexpr (kColumns) {
-            if constexpr (kShared) ptx::tma_load_2d_pair(sb, &a.tmap_b, bar, k0, col0);
-            else ptx::tma_load_2d(sb, &a.tmap_b, bar, k0, col0);
-        }
+        if constexpr (kShared) ptx::tma_load_2d_pair(sb, &a.tmap_b, bar, k0, col0);
+        else ptx::tma_load_2d(sb, &a.tmap_b, bar, k0, col0);
     }
 }
 
-// The producer loop of one thread.  Two threads of different warps share the work where there are two (each copy
-// instruction keeps its thread busy for some 250 cycles): one stages the feature operand and speaks for the stage,
-// the other the column operand.
-template <int KIND, bool kPair, bool kFeatures, bool kColumns>
+// A value that every lane of the warp holds alike, known to be.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// The bounded wait of a whole warp, one verdict.
+template <bool kClusterScope = false>
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_t tmo, volatile uint32_t *abort,
+                                          uint32_t *err, uint32_t info) {
+    const bool now = kClusterScope ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, now)) return true;
+    return __all_sync(0xffffffffu, ptx::mbar_wait_bounded<kClusterScope>(bar, parity, tmo, abort, err, info)) != 0;
+}
+
+// The producer loop, of a whole warp with an elected lane that issues (as in the MMA loop).
+template <int KIND, bool kPair>
 __device__ __forceinline__ void produce(const GroupedArgs &a, Walk<KIND, kPair> &walk, const GrLayout &L, const GrBars &B,
                                         uint32_t base, uint32_t crank, uint64_t tmo, volatile uint32_t *abort) {
     const int stages = a.stages;
     const bool leader = crank == 0u;
     const uint32_t full_lead = kPair ? ptx::mapa(B.full0, 0u) : B.full0;
+    const bool elected = ptx::elect_one();
     uint32_t it = 0, s = 0, ph = 0;
     bool ok = true;
     Tile w;
     while (ok && walk.next(w)) {
+        const int kb0 = uniform(w.kb0), kb1 = uniform(w.kb1), extra = KIND == GR_LORA ? uniform(w.extra) : 0;
         const int cols = kPair ? w.nm / 2 : w.nm;  // columns this CTA stages
         const int col0 = w.col0 + int(crank) * cols;
         const int blocks = b_blocks<KIND, kPair>(a, w);
         const uint32_t own = uint32_t(a.a_blocks) * 8192u + b_bytes<KIND, kPair>(a, blocks);
-        for (int kb = w.kb0; kb < w.kb1; ++kb) {
-            if (!ptx::mbar_try_wait(B.empty0 + 8 * s, ph ^ 1u)) {
-                ok = ptx::mbar_wait_bounded(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
-                if (!ok) break;
-            }
+        for (int kb = kb0; kb < kb1; ++kb) {
+            ok = wait_warp(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
+            if (!ok) break;
             const uint32_t sa = base + s * L.stage_bytes;
             const uint32_t sb = sa + L.a_bytes;
-            // A pair's loads complete on the leader's barrier.  (WGRAD: but for a group's last block where it
-            // has to be zeroed behind the rows; the second CTA's part then completes on its own barrier, its
-            // warp 1 zeroes and arrives.)
-            const bool tail = kPair && KIND == GR_WGRAD && kb == w.nk - 1 && (w.rows & 15) != 0;
-            if constexpr (kFeatures) {
+            if (elected) {
+                // A pair's loads complete on the leader's barrier.  (WGRAD: but for a group's last block where it
+                // has to be zeroed behind the rows; the second CTA's part then completes on its own barrier, its
+                // warp 1 zeroes and arrives.)
+                const bool tail = kPair && KIND == GR_WGRAD && kb == w.nk - 1 && (w.rows & 15) != 0;
                 if (!kPair || leader) {
                     ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, kPair && !tail ? 2 * own : own);
                 } else if (KIND == GR_WGRAD) {
                     if (tail) ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, own);
                     else ptx::mbar_arrive_cluster_relaxed(full_lead + 8 * s);  // the loads count bytes
                 }
+                if (kPair && !(tail && !leader))
+                    stage_loads<KIND, true>(a, w, sa, sb, full_lead + 8 * s, kb, col0, blocks);
+                else stage_loads<KIND, false>(a, w, sa, sb, B.full0 + 8 * s, kb, col0, blocks);
             }
-            if (kPair && !(tail && !leader))
-                stage_loads<KIND, true, kFeatures, kColumns>(a, w, sa, sb, full_lead + 8 * s, kb, col0, blocks);
-            else stage_loads<KIND, false, kFeatures, kColumns>(a, w, sa, sb, B.full0 + 8 * s, kb, col0, blocks);
+            __syncwarp();
             ++it;
             if (++s == uint32_t(stages)) {
                 s = 0;
@@ -1141,14 +1126,14 @@ __device__ __forceinline__ void produce(const GroupedArgs &a, Walk<KIND, kPair> 
         if constexpr (KIND == GR_LORA) {
             // the low-rank product of a tile with one adapter: blocks of 64 ranks, H's upper parts, then its
             // lower ones, against the same rows of B
-            if (w.extra > 0) ptx::griddep_wait();  // H is the previous grid's
-            for (int x = 0; x < w.extra && ok; ++x) {
-                ok = ptx::mbar_wait_bounded(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
+            if (extra > 0) ptx::griddep_wait();  // H is the previous grid's
+            for (int x = 0; x < extra && ok; ++x) {
+                ok = wait_warp(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
                 if (!ok) break;
                 const int r0 = (x >> 1) * kBK;
                 const uint32_t sa = base + s * L.stage_bytes;
                 const uint32_t bar = full_lead + 8 * s;
-                if constexpr (kFeatures) {
+                if (elected) {
                     if (leader) ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, kPair ? 2 * own : own);
                     if (a.a_split) {
                         for (int i = 0; i < a.a_blocks; ++i) {
@@ -1160,12 +1145,11 @@ __device__ __forceinline__ void produce(const GroupedArgs &a, Walk<KIND, kPair> 
                         if constexpr (kPair) ptx::tma_load_4d_pair(sa, &a.tmap_lb, bar, 0, r0, w.f0 / 64, w.ad);
                         else ptx::tma_load_4d(sa, &a.tmap_lb, bar, 0, r0, w.f0 / 64, w.ad);
                     }
-                }
-                if constexpr (kColumns) {
                     const int xh = (x & 1) * a.rank + r0;
                     if constexpr (kPair) ptx::tma_load_2d_pair(sa + L.a_bytes, &a.tmap_h, bar, xh, col0);
                     else ptx::tma_load_2d(sa + L.a_bytes, &a.tmap_h, bar, xh, col0);
                 }
+                __syncwarp();
                 ++it;
                 if (++s == uint32_t(stages)) {
                     s = 0;
@@ -1192,9 +1176,8 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
         if (threadIdx.x == 0) ptx::record_error(a.err, 8u, 0x60000000u | (base & 1023u));
         return;
     }
-    constexpr int kEpiWarps = epi_warps(KIND), kThreads = threads_of(KIND, kPair), kHalves = kEpiWarps / 4,
+    constexpr int kEpiWarps = epi_warps(KIND), kThreads = threads_of(KIND), kHalves = kEpiWarps / 4,
                   kSpan = KIND == GR_WGRAD ? 64 : 32;
-    constexpr bool kTwo = two_producers(KIND, kPair);
     constexpr bool kAMn = KIND != GR_DGRAD;  // features contiguous in memory: A is MN-major
     constexpr bool kBMn = KIND == GR_WGRAD;
     const int stages = a.stages;
@@ -1268,10 +1251,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) produce<KIND, kPair, true, !kTwo>(a, walk, L, B, base, crank, tmo, abort);
-        __syncwarp();
-    } else if (kTwo && warp == kThreads / 32 - 1) {
-        if (lane == 0) produce<KIND, kPair, false, true>(a, walk, L, B, base, crank, tmo, abort);
+        produce<KIND, kPair>(a, walk, L, B, base, crank, tmo, abort);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
@@ -1643,7 +1623,7 @@ cudaError_t launch_grouped(int kind, const GroupedArgs &a, int ctas, int smem, b
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(threads_of(kind, pair));
+    cfg.blockDim = dim3(threads_of(kind));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
