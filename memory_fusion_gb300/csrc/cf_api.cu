@@ -1384,9 +1384,11 @@ cf_status grouped_sizes(int64_t T, int64_t N, int64_t K, int64_t groups, int dty
 // Tile width (accumulator columns) and CTA pairs, from the sizes the host knows: a model of a launch's cycles,
 // minimised over the widths.  Group sizes are device data, so groups are taken as equal, with half a tile of waste
 // where they are wider than a tile.  Measured on a GB300 (about 1.8 GHz under load): an MMA block of n columns takes
-// 2.7 n cycles (690 at 256), copies arrive at 56 B per cycle and SM, HBM gives the chip 3770 B per cycle; an epilogue
-// takes 600 cycles and 25 a column; dividing tiles costs 1500 cycles and 70 a column (writing, adding, finishing); the
-// low-rank product of rows with adapters of their own 1000 cycles for 8 rows and 8 ranks.
+// 2.35 n cycles (600 at 256) and 290 at least (370 in a pair), copies arrive at 75 B per cycle and SM, HBM gives the
+// chip 3770 B per cycle; an epilogue takes 1500 cycles and 20 a column, 900 more where a pair turns a weight gradient;
+// dividing tiles costs 1500 cycles and 70 a column (writing, adding, finishing), the low-rank product of rows with
+// adapters of their own 1000 cycles for 8 rows and 8 ranks.  Against every width and both CTA counts, timed over 120
+// random sizes, the choice takes 4 % more time than the best one in the geometric mean.
 // -------------------------------------------------------------------------
 constexpr double kPlanSms = 152;  // a GB300's, whatever device is current: the workspace size follows from this plan
 
@@ -1427,8 +1429,8 @@ double grouped_cycles(const GroupedShape &s, int bn, bool pair) {
         }
     }
     // (a copy brings the tile's full width, a narrower group's or not)
-    const double block = std::max(2.7 * n, (16384 + (pair ? 64.0 : 128.0) * bn) / 56);
-    const double main = blocks * block + 400, epilogue = 600 + 25 * n + low, hbm = bytes / 3770;
+    const double block = std::max(std::max(2.35 * n, pair ? 370.0 : 290.0), (16384 + (pair ? 64.0 : 128.0) * bn) / 75);
+    const double main = blocks * block + 400, epilogue = 1500 + 20 * n + (wgrad && pair ? 900 : 0) + low, hbm = bytes / 3770;
     // two things that go on at once hardly ever overlap quite
     auto both = [](double a, double b) { return std::max(a, b) + 0.3 * std::min(a, b); };
     const double rounds = std::ceil(tiles / sms - 1e-9);
@@ -1436,7 +1438,7 @@ double grouped_cycles(const GroupedShape &s, int bn, bool pair) {
     if (pair || tiles > double(cf::kGroupedSplitTiles)) return whole;
     const double each = std::max(tiles * main / sms, 4 * block);
     const double parts = std::max(1.0, sms / tiles);
-    const double split = both(each, hbm) + 1500 + 70 * n + 600 + 25 * n + low / parts;
+    const double split = both(each, hbm) + 1500 + 70 * n + 1500 + 20 * n + low / parts;
     return std::min(whole, split);
 }
 

@@ -630,7 +630,7 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
             const int most = KIND == GR_WGRAD ? 0 : min(workers / p.tiles, nkc / kMinStretch);
             const int n = min(a.bn, (rows_all + ngroups - 1) / ngroups + 15);  // columns of a tile, about
             const int cols = KIND == GR_WGRAD ? a.bn : n;
-            const int block = max(27 * cols / 10, (16384 + 128 * a.bn) / 56);
+            const int block = max(max(47 * cols / 20, 290), (16384 + 128 * a.bn) / 75);
             const int adding = (1500 + 70 * cols) / block + 1;
             const int even = most >= 2 ? (nkc + most - 1) / most + adding : 1 << 30;
             const int mixed = stretch + adding + adding / 2;
