@@ -1329,12 +1329,12 @@ namespace {
 
 // 16-bit tensor map of up to four dimensions, 128B swizzle, zeros outside; strides in bytes
 bool make_tmap_nd(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-                  const cuuint32_t *box) {
+                  const cuuint32_t *box, CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
     auto fn = encode_fn();
     if (!fn) return false;
     cuuint32_t estr[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void *>(ptr), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1343,14 +1343,20 @@ bool make_tmap_nd(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *d
 bool make_tmap_features(CUtensorMap *m, int *split, const void *ptr, uint64_t count, uint64_t K, uint64_t F,
                         int blocks) {
     *split = F % 64 != 0;
+    // A CTA takes 256 bytes of a row, another one what is next to them, much later: where those 256 bytes are no whole
+    // aligned piece, fetching whole pieces brings up to twice what is used (55 rows over 12 groups of 5464 x 3320: 96 us
+    // with 256-byte fetches, 84 without; of 5464 x 3392: 77 and 64).
+    const bool whole = F % 128 == 0 && reinterpret_cast<uintptr_t>(ptr) % 256 == 0;
+    const CUtensorMapL2promotion promotion =
+        whole ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE;
     if (*split) {
         const cuuint64_t dims[3] = {F, K, count}, strides[2] = {F * 2, K * F * 2};
         const cuuint32_t box[3] = {64, 64, 1};
-        return make_tmap_nd(m, ptr, 3, dims, strides, box);
+        return make_tmap_nd(m, ptr, 3, dims, strides, box, promotion);
     }
     const cuuint64_t dims[4] = {64, K, F / 64, count}, strides[3] = {F * 2, 128, K * F * 2};
     const cuuint32_t box[4] = {64, 64, cuuint32_t(blocks), 1};
-    return make_tmap_nd(m, ptr, 4, dims, strides, box);
+    return make_tmap_nd(m, ptr, 4, dims, strides, box, promotion);
 }
 
 // Feature operand of DGRAD: the same weights [count, K, N] with rows K as the features, 128 of them a copy.
@@ -1384,8 +1390,8 @@ cf_status grouped_sizes(int64_t T, int64_t N, int64_t K, int64_t groups, int dty
 // Tile width (accumulator columns) and CTA pairs, from the sizes the host knows: a model of a launch's cycles,
 // minimised over the widths.  Group sizes are device data, so groups are taken as equal, with half a tile of waste
 // where they are wider than a tile.  Measured on a GB300 (about 1.8 GHz under load): an MMA block of n columns takes
-// 2.35 n cycles (600 at 256) and 290 at least (370 in a pair), copies arrive at 75 B per cycle and SM, HBM gives the
-// chip 3770 B per cycle; an epilogue takes 1500 cycles and 20 a column, 900 more where a pair turns a weight gradient;
+// 2.35 n cycles (600 at 256) and 290 at least (370 in a pair), copies arrive at 75 B per cycle and SM (43 where the
+// matrix's rows are no multiples of 128 bytes: 2048 features 17.4 us, 2056 21.9), HBM gives the chip 3770 B per cycle; an epilogue takes 1500 cycles and 20 a column, 900 more where a pair turns a weight gradient;
 // dividing tiles costs 1500 cycles and 70 a column (writing, adding, finishing), the low-rank product of rows with
 // adapters of their own 1000 cycles for 8 rows and 8 ranks.  Against every width and both CTA counts, timed over 120
 // random sizes, the choice takes 4 % more time than the best one in the geometric mean.
@@ -1396,6 +1402,13 @@ struct GroupedShape {
     int kind;
     int64_t T, F, C, N, groups, rank;
 };
+
+// cycles that the copies of a block take
+double copy_cycles(const GroupedShape &s, int bn, bool pair) {
+    const bool wgrad = s.kind == cf::GR_WGRAD;
+    const int64_t a_row = s.kind == cf::GR_DGRAD ? s.C : s.F, b_row = wgrad ? s.N : s.C;
+    return 16384 * (a_row % 64 ? 1.75 : 1.0) / 75 + (pair ? 64.0 : 128.0) * bn * (b_row % 64 ? 1.75 : 1.0) / 75;
+}
 
 double grouped_cycles(const GroupedShape &s, int bn, bool pair) {
     const bool wgrad = s.kind == cf::GR_WGRAD;
@@ -1428,8 +1441,9 @@ double grouped_cycles(const GroupedShape &s, int bn, bool pair) {
             blocks += (1.0 - share) * 2.0 * double((s.rank + 63) / 64);
         }
     }
-    // (a copy brings the tile's full width, a narrower group's or not)
-    const double block = std::max(std::max(2.35 * n, pair ? 370.0 : 290.0), (16384 + (pair ? 64.0 : 128.0) * bn) / 75);
+    // (where half of the tile's width holds its columns, a copy brings only that half)
+    const double copies = copy_cycles(s, !wgrad && 2 * n <= bn ? bn / 2 : bn, pair);
+    const double block = std::max(std::max(2.35 * n, pair ? 370.0 : 290.0), copies);
     const double main = blocks * block + 400, epilogue = 1500 + 20 * n + (wgrad && pair ? 900 : 0) + low, hbm = bytes / 3770;
     // two things that go on at once hardly ever overlap quite
     auto both = [](double a, double b) { return std::max(a, b) + 0.3 * std::min(a, b); };
@@ -1526,6 +1540,7 @@ cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int
     a->pair = pair;
     a->a_blocks = a_blocks;
     a->stages = stages;
+    a->copy_cycles = int(copy_cycles(shape, bn, pair));
     a->counters = reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(ws) + cf::kErrBytes +
                                                size_t(set) * kGroupedCounterBytes);
     // (a forced tile wider than the workspace was sized for: whole tiles only)
@@ -1550,6 +1565,13 @@ void grouped_args(cf::GroupedArgs *a, int64_t T, int64_t F, int64_t C, int64_t N
     a->fp16 = dtype == CF_FP16;
     a->extra_arrivals = t.extra_arrivals > 0 ? t.extra_arrivals : 0;
     a->timeout_ns = 1000ull * (t.timeout_us ? t.timeout_us : kDefaultTimeoutUs);
+}
+
+// the rows [T, C] that become accumulator columns, in boxes of what a CTA stages and of half of it
+bool make_tmap_rows(cf::GroupedArgs *a, const void *rows, int64_t T, int64_t C) {
+    const uint32_t box = staged_columns(*a);
+    return make_tmap_bf16(&a->tmap_b, rows, uint64_t(T), uint64_t(C), 64, box) &&
+           make_tmap_bf16(&a->tmap_b2, rows, uint64_t(T), uint64_t(C), 64, box / 2);
 }
 
 cf_status launch_grouped_checked(int kind, const cf::GroupedArgs &a, int ctas, int smem, const cf_tuning &t,
@@ -1593,7 +1615,7 @@ cf_status grouped_rows(int kind, const void *rows, const void *W, const int32_t 
     if (!(fwd ? make_tmap_features(&a.tmap_a, &a.a_split, W, uint64_t(E), uint64_t(K), uint64_t(N),
                                  a.a_blocks)
               : make_tmap_features_t(&a.tmap_a, W, uint64_t(E), uint64_t(K), uint64_t(N))) ||
-        !make_tmap_bf16(&a.tmap_b, rows, uint64_t(T), uint64_t(C), 64, staged_columns(a)))
+        !make_tmap_rows(&a, rows, T, C))
         return CF_ERR_CUDA;
     a.out = out;
     a.preact = preact;
@@ -1748,7 +1770,7 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
         st = plan_grouped(cf::GR_SHRINK, T, R, K, 0, S, 0, ts, dev, workspace, 0, part_sh, room_sh, &sh, &sh_ctas, &sh_smem);
         if (st != CF_OK) return st;
         if (!make_tmap_features(&sh.tmap_a, &sh.a_split, A, uint64_t(L), uint64_t(K), uint64_t(R), sh.a_blocks) ||
-            !make_tmap_bf16(&sh.tmap_b, X, uint64_t(T), uint64_t(K), 64, staged_columns(sh)))
+            !make_tmap_rows(&sh, X, T, K))
             return CF_ERR_CUDA;
         sh.windex = adapters;
         sh.nweights = int(L);
@@ -1768,7 +1790,7 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
     st = plan_grouped(cf::GR_LORA, T, N, K, 0, S, R, t, dev, workspace, 1, part, room, &a, &ctas, &smem);
     if (st != CF_OK) return st;
     if (!make_tmap_features(&a.tmap_a, &a.a_split, W, 1, uint64_t(K), uint64_t(N), a.a_blocks) ||
-        !make_tmap_bf16(&a.tmap_b, X, uint64_t(T), uint64_t(K), 64, staged_columns(a)))
+        !make_tmap_rows(&a, X, T, K))
         return CF_ERR_CUDA;
     if (L > 0 && (!make_tmap_features(&a.tmap_lb, &a.a_split, B, uint64_t(L), uint64_t(R), uint64_t(N), a.a_blocks) ||
                   !make_tmap_bf16(&a.tmap_h, H, uint64_t(T), uint64_t(2 * R), 64, staged_columns(a))))

@@ -88,6 +88,13 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
+// 8 columns of 32 lanes of tensor memory
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr)
+                 : "memory");
+}
 // one lane of a converged warp, the same one every time
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
@@ -120,7 +127,8 @@ constexpr int kBK = 64;         // contraction per stage (128 bytes: one swizzle
 constexpr int kFB = 128;        // features per tile (accumulator lanes)
 constexpr int kRasterRows = 16;  // row tiles walked before the next feature tile
 constexpr int kMinStretch = 4;   // blocks a worker takes at least
-constexpr int kLongRows = 64;    // LORA: rows from which a request has tiles of its own
+constexpr int kLongRows = 32;    // LORA: rows from which a request has tiles of its own
+constexpr int kRunRows = 32;     // LORA: rows up to which a run of shorter requests joins the long one before it
 constexpr int kShortRows = kLoraShortRows;
 
 constexpr uint32_t kInfoProducer = 0x10000000u;
@@ -191,7 +199,10 @@ struct Tile {
     int row0;   // WGRAD: first row of the group
     int rows;   // WGRAD: rows of the group
     int extra;  // LORA: blocks of the low-rank product behind the tile's own (pieces: with the last)
-    int ad;     // LORA: the adapter of all the tile's rows, -1 none, -2 rows of several requests
+    int ad;     // LORA: the adapter of the first nx columns' rows, -1 none
+    int nx;     // LORA: columns whose low-rank product runs on the tensor cores: all of the tile (nm), or a long
+                // request's in whole 16s (a pair: 32s)
+    bool mixed; // LORA: the columns behind them are of several requests
     int first, last;  // workers that hold pieces of the tile
     int slot;   // which of its two workspace slots this worker's piece goes to
     __device__ bool whole() const { return first == last; }
@@ -242,6 +253,13 @@ __device__ __forceinline__ int request_of(const Table &tab, int groups, int row)
         else hi = mid - 1;
     }
     return lo;
+}
+
+// LORA: rows of the run of short requests behind plan group g that join it
+__device__ __forceinline__ int joined_rows(const Table &tab, int ngroups, int g) {
+    if (tab.gad[g] == -2 || g + 1 >= ngroups || tab.gad[g + 1] != -2) return 0;
+    const int rows = tab.goff[g + 2] - tab.goff[g + 1];
+    return rows <= kRunRows ? rows : 0;
 }
 
 template <int KIND, bool kPair>
@@ -308,14 +326,18 @@ struct Walk {
                     kb = cur - r.id * nkc;
                 }
             }
-            while (r.id >= tab.pre[g + 1]) ++g;
+            // the last group that starts at or before the tile: 32 at a time, by the whole warp
+            for (int passed = 32; passed == 32;) {
+                const int at = min(g + 1 + int(threadIdx.x & 31), plan.groups);  // (pre of the last is above any tile)
+                passed = __popc(__ballot_sync(0xffffffffu, r.id >= tab.pre[at]));
+                g += passed;
+            }
             local = r.id - tab.pre[g];
         }
         r.g = g;
         r.w = KIND == GR_SHRINK ? tab.ad[g] : (KIND == GR_LORA ? 0 : g);
         const int lo = tab.goff[g];
-        const int rows = tab.goff[g + 1] - lo;
-        r.ad = KIND == GR_LORA ? tab.gad[g] : -1;
+        const int rows = tab.goff[g + 1] - lo + (KIND == GR_LORA ? joined_rows(tab, plan.groups, g) : 0);
         int blocks;  // of the tile, one at least
         if constexpr (KIND == GR_WGRAD) {
             const int nt = (a.N + a.bn - 1) >> shift;
@@ -346,13 +368,22 @@ struct Walk {
             r.row0 = r.rows = 0;
             r.nk = blocks = nkc;
         }
-        if constexpr (KIND == GR_LORA) {  // requests in a row may share an adapter
-            if (r.ad == -2) {
+        r.nm = (r.n + kGran - 1) & ~(kGran - 1);
+        r.ad = -1;
+        r.nx = 0;
+        r.mixed = false;
+        if constexpr (KIND == GR_LORA) {
+            const int own = tab.gad[g] == -2 ? 0 : min(max(tab.goff[g + 1] - r.col0, 0), r.n);  // a long request's rows
+            if (own == r.n) {
+                r.ad = tab.gad[g];
+                r.nx = r.nm;
+            } else {  // requests in a row may share an adapter
                 const int s0 = request_of(tab, a.groups, r.col0), s1 = request_of(tab, a.groups, r.col0 + r.n - 1);
-                if (tab.turn[s0] == tab.turn[s1]) r.ad = tab.ad[s0];
+                r.mixed = tab.turn[s0] != tab.turn[s1];
+                r.nx = r.mixed ? own & ~(kGran - 1) : r.nm;
+                if (r.nx > 0) r.ad = tab.ad[s0];
             }
         }
-        r.nm = (r.n + kGran - 1) & ~(kGran - 1);
         r.kb0 = kb;
         r.kb1 = r.nk;
         r.first = r.last = worker;
@@ -588,7 +619,13 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
         for (int i0 = 0; i0 < a.groups; i0 += 32) {
             const int i = i0 + lane;
             const int at = i < ngroups ? i : ngroups - 1;
-            int count = i < ngroups ? ft * ((tab.goff[at + 1] - tab.goff[at] + a.bn - 1) >> shift) : 0;
+            // a run that joins the long request before it (there is one, but for the first group) has no tiles
+            const int here = tab.gad[at], behind = tab.gad[min(at + 1, ngroups - 1)];
+            const int own = tab.goff[at + 1] - tab.goff[at], run = tab.goff[min(at + 2, ngroups)] - tab.goff[at + 1];
+            const bool joins = here == -2 && at > 0 && own <= kRunRows;
+            const bool takes = here != -2 && behind == -2 && run <= kRunRows;
+            const int rows = (joins ? 0 : own) + (takes ? run : 0);
+            int count = i < ngroups ? ft * ((rows + a.bn - 1) >> shift) : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int o = __shfl_up_sync(kAll, count, d);
@@ -630,7 +667,7 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
             const int most = KIND == GR_WGRAD ? 0 : min(workers / p.tiles, nkc / kMinStretch);
             const int n = min(a.bn, (rows_all + ngroups - 1) / ngroups + 15);  // columns of a tile, about
             const int cols = KIND == GR_WGRAD ? a.bn : n;
-            const int block = max(max(47 * cols / 20, 290), (16384 + 128 * a.bn) / 75);
+            const int block = max(max(47 * cols / 20, 290), a.copy_cycles);
             const int adding = (1500 + 70 * cols) / block + 1;
             const int even = most >= 2 ? (nkc + most - 1) / most + adding : 1 << 30;
             const int mixed = stretch + adding + adding / 2;
@@ -653,17 +690,23 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
         ptx::record_error(err, 8u /*CF_ERR_DEVICE_BOUNDS*/, kInfoTable);
 }
 
-// A block of the contraction stages 16 KB of the feature operand (8 KB where there are no more than 64 features;
-// what is behind the last feature is zero or stale, in lanes that are never stored) and, of the columns, what the CTA
-// multiplies, rounded up to whole boxes.  Rows of a box behind the tile's are the neighbour's, in columns that are not multiplied or not stored.
+// A block of the contraction stages 16 KB of the feature operand (8 KB where there are no more than 64 features; what
+// is behind the last feature is zero or stale, in lanes that are never stored) and the tile's columns: one box of rows,
+// of the full width or of half of it.  (An SM takes 75 B of copies a cycle, so a narrow tile that brings a full box pays
+// for it: 120 rows a group at 256 columns took 650 cycles a block, not 440.)  Rows of a box behind the tile's are its
+// neighbour's, in columns that are not multiplied or not stored.  WGRAD: 64-column blocks to fill.
+template <bool kPair>
+__device__ __forceinline__ bool half_box(const GroupedArgs &a, const Tile &w) {
+    return kPair ? w.nm <= a.bn / 2 : 2 * w.nm <= a.bn;
+}
 template <int KIND, bool kPair>
-__device__ __forceinline__ int b_blocks(const GroupedArgs &a, const Tile &w) {  // WGRAD: 64-column blocks to fill
+__device__ __forceinline__ int b_blocks(const GroupedArgs &a, const Tile &w) {
     const int cols = kPair ? w.nm / 2 : w.nm;
     return KIND == GR_WGRAD ? (a.b_split ? (cols + 63) / 64 : (kPair ? a.bn / 2 : a.bn) / 64) : 1;
 }
 template <int KIND, bool kPair>
-__device__ __forceinline__ uint32_t b_bytes(const GroupedArgs &a, int blocks) {
-    return KIND == GR_WGRAD ? uint32_t(blocks) * 8192u : uint32_t(kPair ? a.bn / 2 : a.bn) * 128u;
+__device__ __forceinline__ uint32_t b_bytes(const GroupedArgs &a, int blocks, bool half) {
+    return KIND == GR_WGRAD ? uint32_t(blocks) * 8192u : uint32_t(kPair ? a.bn / 2 : a.bn) * (half ? 64u : 128u);
 }
 
 // WGRAD: rows left .. 16*steps - 1 of every 64-column block of the stage (a row is 128 bytes of a block) become
@@ -1027,7 +1070,7 @@ __device__ __forceinline__ int next_fragment(int c) {
 // The copies of block kb into a stage, completing on `bar` (kShared: a barrier of either CTA of the pair)
 template <int KIND, bool kShared>
 __device__ __forceinline__ void stage_loads(const GroupedArgs &a, const Tile &w, uint32_t sa, uint32_t sb, uint32_t bar,
-                                            int kb, int col0, int blocks) {
+                                            int kb, int col0, int blocks, bool half) {
     const int k0 = kb * kBK;
     if constexpr (KIND == GR_WGRAD) {
         const int y = w.row0 + k0;
@@ -1062,8 +1105,9 @@ __device__ __forceinline__ void stage_loads(const GroupedArgs &a, const Tile &w,
             if constexpr (kShared) ptx::tma_load_4d_pair(sa, &a.tmap_a, bar, 0, k0, w.f0 / 64, w.w);
             else ptx::tma_load_4d(sa, &a.tmap_a, bar, 0, k0, w.f0 / 64, w.w);
         }
-        if constexpr (kShared) ptx::tma_load_2d_pair(sb, &a.tmap_b, bar, k0, col0);
-        else ptx::tma_load_2d(sb, &a.tmap_b, bar, k0, col0);
+        const CUtensorMap *const rows = half ? &a.tmap_b2 : &a.tmap_b;
+        if constexpr (kShared) ptx::tma_load_2d_pair(sb, rows, bar, k0, col0);
+        else ptx::tma_load_2d(sb, rows, bar, k0, col0);
     }
 }
 
@@ -1089,13 +1133,50 @@ __device__ __forceinline__ void produce(const GroupedArgs &a, Walk<KIND, kPair> 
     const bool elected = ptx::elect_one();
     uint32_t it = 0, s = 0, ph = 0;
     bool ok = true;
+    // the low-rank product of a tile's first nx columns, of one adapter: blocks of 64 ranks, H's upper parts, then its
+    // lower ones, against the same rows of B
+    auto load_low_rank = [&](const Tile &t) {
+        const int extra = uniform(t.extra);
+        if (extra > 0) ptx::griddep_wait();  // H is the previous grid's
+        for (int x = 0; x < extra && ok; ++x) {
+            ok = wait_warp(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
+            if (!ok) break;
+            const int r0 = (x >> 1) * kBK;
+            const uint32_t sa = base + s * L.stage_bytes;
+            const uint32_t bar = full_lead + 8 * s;
+            if (elected) {
+                const uint32_t own = uint32_t(a.a_blocks) * 8192u + b_bytes<KIND, kPair>(a, 1, false);
+                if (leader) ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, kPair ? 2 * own : own);
+                if (a.a_split) {
+                    for (int i = 0; i < a.a_blocks; ++i) {
+                        if constexpr (kPair)
+                            ptx::tma_load_3d_pair(sa + i * 8192, &a.tmap_lb, bar, t.f0 + 64 * i, r0, t.ad);
+                        else ptx::tma_load_3d(sa + i * 8192, &a.tmap_lb, bar, t.f0 + 64 * i, r0, t.ad);
+                    }
+                } else {
+                    if constexpr (kPair) ptx::tma_load_4d_pair(sa, &a.tmap_lb, bar, 0, r0, t.f0 / 64, t.ad);
+                    else ptx::tma_load_4d(sa, &a.tmap_lb, bar, 0, r0, t.f0 / 64, t.ad);
+                }
+                const int xh = (x & 1) * a.rank + r0, y = t.col0 + (kPair ? int(crank) * (t.nx / 2) : 0);
+                if constexpr (kPair) ptx::tma_load_2d_pair(sa + L.a_bytes, &a.tmap_h, bar, xh, y);
+                else ptx::tma_load_2d(sa + L.a_bytes, &a.tmap_h, bar, xh, y);
+            }
+            __syncwarp();
+            ++it;
+            if (++s == uint32_t(stages)) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+    };
     Tile w;
     while (ok && walk.next(w)) {
-        const int kb0 = uniform(w.kb0), kb1 = uniform(w.kb1), extra = KIND == GR_LORA ? uniform(w.extra) : 0;
+        const int kb0 = uniform(w.kb0), kb1 = uniform(w.kb1);
         const int cols = kPair ? w.nm / 2 : w.nm;  // columns this CTA stages
         const int col0 = w.col0 + int(crank) * cols;
         const int blocks = b_blocks<KIND, kPair>(a, w);
-        const uint32_t own = uint32_t(a.a_blocks) * 8192u + b_bytes<KIND, kPair>(a, blocks);
+        const bool half = KIND != GR_WGRAD && half_box<kPair>(a, w);
+        const uint32_t own = uint32_t(a.a_blocks) * 8192u + b_bytes<KIND, kPair>(a, blocks, half);
         for (int kb = kb0; kb < kb1; ++kb) {
             ok = wait_warp(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
             if (!ok) break;
@@ -1113,8 +1194,8 @@ __device__ __forceinline__ void produce(const GroupedArgs &a, Walk<KIND, kPair> 
                     else ptx::mbar_arrive_cluster_relaxed(full_lead + 8 * s);  // the loads count bytes
                 }
                 if (kPair && !(tail && !leader))
-                    stage_loads<KIND, true>(a, w, sa, sb, full_lead + 8 * s, kb, col0, blocks);
-                else stage_loads<KIND, false>(a, w, sa, sb, B.full0 + 8 * s, kb, col0, blocks);
+                    stage_loads<KIND, true>(a, w, sa, sb, full_lead + 8 * s, kb, col0, blocks, half);
+                else stage_loads<KIND, false>(a, w, sa, sb, B.full0 + 8 * s, kb, col0, blocks, half);
             }
             __syncwarp();
             ++it;
@@ -1123,40 +1204,7 @@ __device__ __forceinline__ void produce(const GroupedArgs &a, Walk<KIND, kPair> 
                 ph ^= 1u;
             }
         }
-        if constexpr (KIND == GR_LORA) {
-            // the low-rank product of a tile with one adapter: blocks of 64 ranks, H's upper parts, then its
-            // lower ones, against the same rows of B
-            if (extra > 0) ptx::griddep_wait();  // H is the previous grid's
-            for (int x = 0; x < extra && ok; ++x) {
-                ok = wait_warp(B.empty0 + 8 * s, ph ^ 1u, tmo, abort, a.err, kInfoProducer | s);
-                if (!ok) break;
-                const int r0 = (x >> 1) * kBK;
-                const uint32_t sa = base + s * L.stage_bytes;
-                const uint32_t bar = full_lead + 8 * s;
-                if (elected) {
-                    if (leader) ptx::mbar_arrive_expect_tx(B.full0 + 8 * s, kPair ? 2 * own : own);
-                    if (a.a_split) {
-                        for (int i = 0; i < a.a_blocks; ++i) {
-                            if constexpr (kPair)
-                                ptx::tma_load_3d_pair(sa + i * 8192, &a.tmap_lb, bar, w.f0 + 64 * i, r0, w.ad);
-                            else ptx::tma_load_3d(sa + i * 8192, &a.tmap_lb, bar, w.f0 + 64 * i, r0, w.ad);
-                        }
-                    } else {
-                        if constexpr (kPair) ptx::tma_load_4d_pair(sa, &a.tmap_lb, bar, 0, r0, w.f0 / 64, w.ad);
-                        else ptx::tma_load_4d(sa, &a.tmap_lb, bar, 0, r0, w.f0 / 64, w.ad);
-                    }
-                    const int xh = (x & 1) * a.rank + r0;
-                    if constexpr (kPair) ptx::tma_load_2d_pair(sa + L.a_bytes, &a.tmap_h, bar, xh, col0);
-                    else ptx::tma_load_2d(sa + L.a_bytes, &a.tmap_h, bar, xh, col0);
-                }
-                __syncwarp();
-                ++it;
-                if (++s == uint32_t(stages)) {
-                    s = 0;
-                    ph ^= 1u;
-                }
-            }
-        }
+        if constexpr (KIND == GR_LORA) load_low_rank(w);
     }
     // every load has landed and been read before the CTA may leave
     const uint32_t first = it > uint32_t(stages) ? it - uint32_t(stages) : 0u;
@@ -1283,6 +1331,33 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
             const uint32_t stage_step = L.stage_bytes >> 4;
             const bool elected = ptx::elect_one();  // the same lane as in mma_block: commits cover their thread's MMAs
             uint32_t s = 0, ph = 0;
+            // the low-rank product of a tile's first nx columns, and the commit that hands the accumulator over
+            auto finish = [&](const Tile &t, uint32_t buf) {
+                const int extra = uniform(t.extra);
+                const uint32_t d = tmem_base + buf * uint32_t(a.bn);
+                const uint32_t idesc = idesc_f16(kPair ? 2 * kFB : kFB, uniform(t.nx), a.fp16 != 0, kAMn, kBMn);
+                for (int x = 0; KIND == GR_LORA && x < extra; ++x) {
+                    if (!wait_warp(B.full0 + 8 * s, ph, tmo, abort, a.err, kInfoMma | 0x400u | s)) return false;
+                    ptx::tc_fence_after();
+                    const int ranks = a.rank - (x >> 1) * kBK;
+                    const int steps = ranks >= kBK ? kBK / 16 : (ranks + 15) / 16;
+                    const uint64_t so = uint64_t(s * stage_step);
+                    if (elected) {
+                        for (int k = 0; k < steps; ++k)
+                            issue_mma<kPair>(d, ad0 + so + uint64_t(k * kAStep), bd0 + so + uint64_t(k * kBStep), idesc,
+                                             1u);
+                        issue_commit<kPair>(B.empty0 + 8 * s);
+                    }
+                    __syncwarp();
+                    if (++s == uint32_t(stages)) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (elected) issue_commit<kPair>(B.tmem_full0 + 8 * buf);
+                __syncwarp();
+                return true;
+            };
             for (int tile = 0; walk.next(w); ++tile) {
                 const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
                 const uint32_t d = tmem_base + buf * uint32_t(a.bn);
@@ -1332,31 +1407,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                         ph ^= 1u;
                     }
                 }
-                if constexpr (KIND == GR_LORA) {
-                    const int extra = uniform(w.extra);
-                    for (int x = 0; x < extra && ok; ++x) {
-                        ok = wait_warp(B.full0 + 8 * s, ph, tmo, abort, a.err, kInfoMma | 0x400u | s);
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-                        const int ranks = a.rank - (x >> 1) * kBK;
-                        const int steps = ranks >= kBK ? kBK / 16 : (ranks + 15) / 16;
-                        const uint64_t so = uint64_t(s * stage_step);
-                        if (elected) {
-                            for (int k = 0; k < steps; ++k)
-                                issue_mma<kPair>(d, ad0 + so + uint64_t(k * kAStep), bd0 + so + uint64_t(k * kBStep), idesc,
-                                                 1u);
-                            issue_commit<kPair>(B.empty0 + 8 * s);
-                        }
-                        __syncwarp();
-                        if (++s == uint32_t(stages)) {
-                            s = 0;
-                            ph ^= 1u;
-                        }
-                    }
-                }
-                if (!ok) break;
-                if (elected) issue_commit<kPair>(B.tmem_full0 + 8 * buf);
-                __syncwarp();
+                if (!ok || !finish(w, buf)) break;
             }
             if (elected) {
                 if constexpr (kPair) ptx::mma_commit_pair_mc(B.mma_done, 1);
@@ -1382,14 +1433,14 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
             // LORA, a tile of several requests: this worker adds the low-rank product of every parts-th eight rows
             int parts = 0, part = 0;
             if constexpr (KIND == GR_LORA) {
-                if (w.ad == -2 && a.nweights > 0) {
+                if (w.mixed) {
                     parts = w.last - w.first + 1;
                     part = worker - w.first;
                     // the other rows' slices of B on their way to L2 while the projection is multiplied
                     for (int c = half * 32; c < w.n; c += 64) {
                         for (int i = 0; i < 4; ++i) {
                             const int j = c + (lane >> 2) + 8 * i;
-                            if ((c / 8 + i) % parts != part || j >= w.n) continue;
+                            if (c + 8 * i < w.nx || (c / 8 + i) % parts != part || j >= w.n) continue;
                             const int ad = tab.ad[request_of(tab, a.groups, w.col0 + j)];
                             const int f8 = w.f0 + q * 32 + (lane & 3) * 8;
                             if (ad < 0 || f8 >= a.F) continue;
@@ -1400,20 +1451,21 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                     }
                 }
             }
-            // The first eight of those rows in the warp's first fragment are worked out now, while the projection is
+            // The first eight of those rows that fall to this warp are worked out now, while the projection is
             // multiplied.
-            int early = -1;  // their place in it
+            int early = -1;  // which eight of the tile's
             float low[8];
             if constexpr (KIND == GR_LORA) {
                 if (parts > 0) {
                     ptx::griddep_wait();  // H is the previous grid's
-                    const int c = half * 32;
-                    const int i = parts == 1 ? 0 : (part + parts - c / 8 % parts) % parts;
-                    if (i < 4 && c + 8 * i < w.n) {
-                        early = i;
+                    int c = half * 32;
+                    while (c + 32 <= w.nx) c += 64;
+                    for (int i = 3; i >= 0; --i)
+                        if (c + 8 * i >= w.nx && c + 8 * i < w.n && (c / 8 + i) % parts == part) early = c / 8 + i;
+                    if (early >= 0) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k) low[k] = 0.f;
-                        const int j = c + (lane >> 2) + 8 * i, f8 = w.f0 + q * 32 + (lane & 3) * 8;
+                        const int j = early * 8 + (lane >> 2), f8 = w.f0 + q * 32 + (lane & 3) * 8;
                         if (j < w.n && f8 < a.F)
                             add_low_rank(low, a, tab.ad[request_of(tab, a.groups, w.col0 + j)], w.col0 + j, f8);
                     }
@@ -1446,10 +1498,10 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                                 float x[8];
                                 turned(x, stg, lane, i);
                                 const int row = w.col0 + c + (lane >> 2) + 8 * i;
-                                if (c == half * 32 && i == early) {
+                                if (c / 8 + i == early) {
 #pragma unroll
                                     for (int k = 0; k < 8; ++k) x[k] += low[k];
-                                } else if ((c / 8 + i) % parts == part) {
+                                } else if (c + 8 * i >= w.nx && (c / 8 + i) % parts == part) {
                                     add_low_rank(x, a, tab.ad[request_of(tab, a.groups, row)], row, f8);
                                 }
                                 float4 *d = reinterpret_cast<float4 *>(p);
@@ -1483,8 +1535,22 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                     continue;
                 }
             }
+            if constexpr (KIND == GR_SHRINK) {
+                // (a short loop: this runs once or twice a CTA, and 32 columns' worth of unrolled code took 7000 cycles
+                // to fetch, of a launch of 30000)
+                const float sc = a.scale ? __ldg(a.scale + w.w) : 1.f;
+#pragma unroll 1
+                for (int c = 0; c < w.n; c += 8) {
+                    uint32_t v[8];
+                    ptx::tmem_ld8(tacc + uint32_t(c), v);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (live && c + j < w.n) store_low(a, w.col0 + c + j, f, sc * __uint_as_float(v[j]));
+                }
+            }
             // (WGRAD: the halves take alternate 64-column blocks)
-            for (int c = half * kSpan; c < w.n; c = next_fragment<kSpan, kHalves>(c)) {
+            for (int c = half * kSpan; KIND != GR_SHRINK && c < w.n; c = next_fragment<kSpan, kHalves>(c)) {
                 uint32_t v[32];
                 if (kPair || KIND != GR_WGRAD || w.whole()) {
                     ptx::tmem_ld32(tacc + uint32_t(c), v);
@@ -1511,10 +1577,10 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                         float x[8];
                         turned(x, stg, lane, i);
                         const int row = w.col0 + c + (lane >> 2) + 8 * i;
-                        if (c == half * 32 && i == early) {
+                        if (c / 8 + i == early) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k) x[k] += low[k];
-                        } else if (parts > 0) {
+                        } else if (parts > 0 && c + 8 * i >= w.nx) {
                             add_low_rank(x, a, tab.ad[request_of(tab, a.groups, row)], row, f8);
                         }
                         uint32_t p[4];
@@ -1557,11 +1623,6 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
 #pragma unroll
                     for (int j = 0; j < 32; ++j) mine[j * 32] = to16(__uint_as_float(v[j]), fp16);
                     fr.out(a.out);
-                } else if constexpr (KIND == GR_SHRINK) {
-                    const float sc = a.scale ? __ldg(a.scale + w.w) : 1.f;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (live && j < cols) store_low(a, w.col0 + c + j, f, sc * __uint_as_float(v[j]));
                 } else if constexpr (KIND == GR_WGRAD) {
                     store_columns(v, a, w, c, reinterpret_cast<uint4 *>(smem_raw + L.stg + e * 4096), q, lane, ok);
                 }

@@ -28,6 +28,7 @@ constexpr int kLoraMaxRank = 128;        // one tile of features in the first pr
 struct GroupedArgs {
     CUtensorMap tmap_a;    // the operand whose features become accumulator lanes: W (WGRAD: X)
     CUtensorMap tmap_b;    // the operand whose rows become accumulator columns: X or dY (WGRAD: dY)
+    CUtensorMap tmap_b2;   // the same with boxes of half the rows (not WGRAD)
     CUtensorMap tmap_lb;   // LORA: B of the adapters, as tmap_a
     CUtensorMap tmap_h;    // LORA: H, as tmap_b
     int a_blocks;          // 64-feature blocks staged: 1 where there are no more than 64 features, else 2
@@ -59,6 +60,7 @@ struct GroupedArgs {
     int act;                 // FORWARD, DGRAD: 1 = GELU(tanh)
     int bn;                  // columns of one accumulator tile (16, 32, 64, 128 or 256)
     int stages;
+    int copy_cycles;         // what a block's copies take
     int pair;                // CTA pairs, one cta_group::2 MMA stream over 256 features (not SHRINK)
     int extra_arrivals;      // test hook: arrivals that the accumulator-ready barriers wait for in vain
     unsigned long long timeout_ns;
