@@ -56,6 +56,7 @@ struct GroupedArgs {
     int groups;
     int nweights;            // weights that windex may name
     int rank;                // LORA
+    int long_rows;           // LORA: rows from which a request has tiles of its own
     int fp16;                // 16-bit type of every operand: 0 bf16, 1 fp16
     int act;                 // FORWARD, DGRAD: 1 = GELU(tanh)
     int bn;                  // columns of one accumulator tile (16, 32, 64, 128 or 256)
