@@ -756,9 +756,12 @@ CF_API cf_status cf_grouped_gemm_wgrad_ex(const void *X, const void *dY, const i
  *
  * with a = adapters[s] for the rows r of request s, [offsets[s],
  * offsets[s+1]): one batch in which each request has its own fine-tuned
- * weights, a low-rank term beside the projection that all share.  The
- * [T, R] product in the middle is two small GEMMs back to back ([ComFuse]
- * B2BGEMM) and is held in fp32; the second is an epilogue of the projection.
+ * weights, a low-rank term beside the projection that all share.  The term is
+ * two small GEMMs back to back ([ComFuse] B2BGEMM), the second an epilogue of
+ * the projection.  Sums are fp32; the scaled [T, R] product between the two is
+ * held as the sum of two `dtype` numbers: to 2^-16 of its value in bf16; in
+ * fp16 to 2^-22 or 2^-25, whichever is more, and a finite value beyond
+ * +-131,008 counts as that.
  *   X (device) `dtype` [T, K]      W (device) `dtype` [K, N]
  *   bias (device) fp32 [N] or NULL
  *   A (device) `dtype` [L, K, R]   B (device) `dtype` [L, R, N]
@@ -769,9 +772,11 @@ CF_API cf_status cf_grouped_gemm_wgrad_ex(const void *X, const void *dY, const i
  * Supported: T >= 0, S in 0..1024 (either 0 is a no-op), L >= 0, N and K
  * positive multiples of 8, R a multiple of 8 up to 128 (a smaller rank is
  * padded with zeros); Y not an input; 16-byte aligned.  An infinity or NaN in
- * an adapter reaches the rows of its own requests only.  Indices outside -1..L-1 are
- * taken as -1 and reported as CF_ERR_DEVICE_BOUNDS, as are bad offsets.
- * workspace (device) >= cf_gemm_lora_workspace_size() bytes.
+ * an adapter reaches the rows of its own requests only (an infinity in B as an
+ * infinity or a NaN).  Indices outside -1..L-1 are taken as -1 and reported as
+ * CF_ERR_DEVICE_BOUNDS, as are bad offsets.  Equal calls give equal bits.
+ * workspace (device) >= cf_gemm_lora_workspace_size() bytes; one workspace may
+ * serve grouped and adapter calls of any sizes in turn.
  * Tuning fields used (_ex): those of cf_grouped_gemm_ex, for the projection. */
 CF_API size_t cf_gemm_lora_workspace_size(int64_t T, int64_t N, int64_t K, int64_t S, int64_t R);
 

@@ -760,7 +760,7 @@ def _run(what, call, device, stream, out, shape, dtype, workspace, nbytes):
     where none are given; the output."""
     import torch
     index = device.index
-    if stream is None and index == torch.cuda.current_device():  # nothing to switch: the decode step's path
+    if stream is None and index == torch._C._cuda_getDevice():  # nothing to switch: the decode step's path
         Y = out if out is not None else torch.empty(shape, dtype=dtype, device=device)
         ws = workspace if workspace is not None else new_workspace(nbytes(), device)
         check(call(Y, ws, ws.nbytes, torch._C._cuda_getCurrentRawStream(index)), what)
@@ -815,7 +815,8 @@ def grouped_gemm_dgrad(dY, W, offsets, *, preact=None, out=None, workspace=None,
     if out is not None:
         _operand("out", out, (T, K), dtype, dev)
     return _run("cf_grouped_gemm_dgrad",
-                lambda dX, ws, n, s: cf_grouped_gemm_dgrad(dY, W, offsets, preact, dX, T, N, K, E, dt, ws, n, s, tuning),
+                lambda dX, ws, n, s: cf_grouped_gemm_dgrad(dY, W, offsets, preact, dX, T, N, K, E, dt, ws, n, s,
+                                                           tuning),
                 dev, stream, out, (T, K), dtype, workspace, lambda: cf_grouped_gemm_workspace_size(T, N, K, E))
 
 
@@ -861,6 +862,6 @@ def gemm_lora(X, W, bias, A, B, offsets, adapters, *, scale=None, out=None, work
     if out is not None:
         _operand("out", out, (T, N), dtype, dev)
     return _run("cf_gemm_lora",
-                lambda Y, ws, n, s: cf_gemm_lora(X, W, bias, A, B, offsets, adapters, scale, Y, T, N, K, S, L, R, dt, ws,
-                                                 n, s, tuning),
+                lambda Y, ws, n, s: cf_gemm_lora(X, W, bias, A, B, offsets, adapters, scale, Y, T, N, K, S, L, R, dt,
+                                                 ws, n, s, tuning),
                 dev, stream, out, (T, N), dtype, workspace, lambda: cf_gemm_lora_workspace_size(T, N, K, S, R))

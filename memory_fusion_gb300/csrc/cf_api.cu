@@ -1344,8 +1344,8 @@ bool make_tmap_features(CUtensorMap *m, int *split, const void *ptr, uint64_t co
                         int blocks) {
     *split = F % 64 != 0;
     // A CTA takes 256 bytes of a row, another one what is next to them, much later: where those 256 bytes are no whole
-    // aligned piece, fetching whole pieces brings up to twice what is used (55 rows over 12 groups of 5464 x 3320: 96 us
-    // with 256-byte fetches, 84 without; of 5464 x 3392: 77 and 64).
+    // aligned piece, fetching whole pieces brings up to twice what is used (55 rows over 12 groups of 5464 x 3320:
+    // 96 us with 256-byte fetches, 84 without; of 5464 x 3392: 77 and 64).
     const bool whole = F % 128 == 0 && reinterpret_cast<uintptr_t>(ptr) % 256 == 0;
     const CUtensorMapL2promotion promotion =
         whole ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE;
@@ -1366,8 +1366,8 @@ bool make_tmap_features_t(CUtensorMap *m, const void *ptr, uint64_t count, uint6
     return make_tmap_nd(m, ptr, 3, dims, strides, box);
 }
 
-// Operand of WGRAD: a row-major [rows, cols] matrix in blocks of 64 rows x 64 columns, `blocks` of them a copy where the
-// rows consist of whole blocks, one otherwise.
+// Operand of WGRAD: a row-major [rows, cols] matrix in blocks of 64 rows x 64 columns, `blocks` of them a copy where
+// the rows consist of whole blocks, one otherwise.
 bool make_tmap_blocks(CUtensorMap *m, int *split, const void *ptr, uint64_t rows, uint64_t cols, uint32_t blocks) {
     *split = cols % 64 != 0;
     if (*split) return make_tmap_bf16(m, ptr, rows, cols, 64, 64);
@@ -1391,10 +1391,11 @@ cf_status grouped_sizes(int64_t T, int64_t N, int64_t K, int64_t groups, int dty
 // minimised over the widths.  Group sizes are device data, so groups are taken as equal, with half a tile of waste
 // where they are wider than a tile.  Measured on a GB300 (about 1.8 GHz under load): an MMA block of n columns takes
 // 2.35 n cycles (600 at 256) and 290 at least (370 in a pair), copies arrive at 75 B per cycle and SM (43 where the
-// matrix's rows are no multiples of 128 bytes: 2048 features 17.4 us, 2056 21.9), HBM gives the chip 3770 B per cycle; an epilogue takes 1500 cycles and 20 a column, 900 more where a pair turns a weight gradient;
-// dividing tiles costs 1500 cycles and 70 a column (writing, adding, finishing), the low-rank product of rows with
-// adapters of their own 1000 cycles for 8 rows and 8 ranks.  Against every width and both CTA counts, timed over 120
-// random sizes, the choice takes 4 % more time than the best one in the geometric mean.
+// matrix's rows are no multiples of 128 bytes: 2048 features 17.4 us, 2056 21.9), HBM gives the chip 3770 B per cycle;
+// an epilogue takes 1500 cycles and 20 a column, 900 more where a pair turns a weight gradient; dividing tiles costs
+// 1500 cycles and 70 a column (writing, adding, finishing), the low-rank product of rows with adapters of their own
+// 1000 cycles for 8 rows and 8 ranks.  Against every width and both CTA counts, timed over 180 random sizes, the choice
+// takes 4 % more time than the best one in the geometric mean.
 // -------------------------------------------------------------------------
 constexpr double kPlanSms = 152;  // a GB300's, whatever device is current: the workspace size follows from this plan
 
@@ -1444,7 +1445,8 @@ double grouped_cycles(const GroupedShape &s, int bn, bool pair) {
     // (where half of the tile's width holds its columns, a copy brings only that half)
     const double copies = copy_cycles(s, !wgrad && 2 * n <= bn ? bn / 2 : bn, pair);
     const double block = std::max(std::max(2.35 * n, pair ? 370.0 : 290.0), copies);
-    const double main = blocks * block + 400, epilogue = 1500 + 20 * n + (wgrad && pair ? 900 : 0) + low, hbm = bytes / 3770;
+    const double main = blocks * block + 400, hbm = bytes / 3770;
+    const double epilogue = 1500 + 20 * n + (wgrad && pair ? 900 : 0) + low;
     // two things that go on at once hardly ever overlap quite
     auto both = [](double a, double b) { return std::max(a, b) + 0.3 * std::min(a, b); };
     const double rounds = std::ceil(tiles / sms - 1e-9);
@@ -1567,16 +1569,18 @@ void grouped_args(cf::GroupedArgs *a, int64_t T, int64_t F, int64_t C, int64_t N
     a->timeout_ns = 1000ull * (t.timeout_us ? t.timeout_us : kDefaultTimeoutUs);
 }
 
-// the rows [T, C] that become accumulator columns, in boxes of what a CTA stages and of half of it
+// the rows [T, C] that become accumulator columns, in boxes of what a CTA stages and of half of it (16 columns are
+// never half full)
 bool make_tmap_rows(cf::GroupedArgs *a, const void *rows, int64_t T, int64_t C) {
     const uint32_t box = staged_columns(*a);
     return make_tmap_bf16(&a->tmap_b, rows, uint64_t(T), uint64_t(C), 64, box) &&
-           make_tmap_bf16(&a->tmap_b2, rows, uint64_t(T), uint64_t(C), 64, box / 2);
+           (a->bn == 16 || make_tmap_bf16(&a->tmap_b2, rows, uint64_t(T), uint64_t(C), 64, box / 2));
 }
 
-// Rows from which a request has tiles of its own, whose low-rank product then runs on the tensor cores.  A row tile more
-// takes 290 cycles a block on its share of the SMs; in a shared tile a row takes about 9 cycles a rank on the CUDA cores.
-// (Geometric mean over 84 batches of 5 to 128 requests: 42.3 us; with 16, 32 or 64 rows for all of them 43.1, 43.9, 42.8.)
+// Rows from which a request has tiles of its own, whose low-rank product then runs on the tensor cores.  A row tile
+// more takes 290 cycles a block on its share of the SMs; in a shared tile a row takes about 9 cycles a rank on the CUDA
+// cores.  (Geometric mean over 84 batches of 5 to 128 requests: 42.3 us; with 16, 32 or 64 rows for all of them 43.1,
+// 43.9 and 42.8.)
 int lora_long_rows(int64_t N, int64_t K, int64_t R) {
     const double share = std::min(1.0, double((N + 127) / 128) / kPlanSms);
     const double rows = double((K + 63) / 64) * 290 * share / (9.0 * double(R));
@@ -1720,7 +1724,8 @@ extern "C" cf_status cf_grouped_gemm_wgrad(const void *X, const void *dY, const 
 // parts of a short request's first contraction: few requests are spread over the SMs
 static int lora_split(int64_t S, int64_t R) {
     const int64_t units = S * ((R + 63) / 64);
-    return int(std::max<int64_t>(1, std::min<int64_t>(cf::kLoraMaxSplit, cf::kGroupedWorkers / std::max<int64_t>(units, 1))));
+    const int64_t parts = cf::kGroupedWorkers / std::max<int64_t>(units, 1);
+    return int(std::max<int64_t>(1, std::min<int64_t>(cf::kLoraMaxSplit, parts)));
 }
 
 // (no parts, no scratch; with parts there are few units)
@@ -1729,8 +1734,8 @@ static size_t lora_part_bytes(int64_t S, int64_t R) {
     return n > 1 ? size_t(S) * size_t((R + 63) / 64) * size_t(n) * cf::kLoraShortRows * 64 * 4 : 0;
 }
 
-// workspace: head; partials of the first product; of the second (which may start while the first ends); H [T, 2, R] 16-bit;
-// parts of the short requests' first product
+// workspace: head; partials of the first product; of the second (which may start while the first ends); H [T, 2, R]
+// 16-bit; parts of the short requests' first product
 extern "C" size_t cf_gemm_lora_workspace_size(int64_t T, int64_t N, int64_t K, int64_t S, int64_t R) {
     if (T < 0 || N <= 0 || K <= 0 || R <= 0 || S <= 0) return kGroupedHead;
     bool pair;
@@ -1776,7 +1781,8 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
         cf_tuning ts = t;
         ts.n_slice = ts.stages = ts.cluster_m = 0;  // the knobs are the main product's
         grouped_args(&sh, T, R, K, 0, S, int(dtype), offsets, workspace, t);
-        st = plan_grouped(cf::GR_SHRINK, T, R, K, 0, S, 0, ts, dev, workspace, 0, part_sh, room_sh, &sh, &sh_ctas, &sh_smem);
+        st = plan_grouped(cf::GR_SHRINK, T, R, K, 0, S, 0, ts, dev, workspace, 0, part_sh, room_sh, &sh, &sh_ctas,
+                          &sh_smem);
         if (st != CF_OK) return st;
         if (!make_tmap_features(&sh.tmap_a, &sh.a_split, A, uint64_t(L), uint64_t(K), uint64_t(R), sh.a_blocks) ||
             !make_tmap_rows(&sh, X, T, K))

@@ -21,9 +21,31 @@
 //    shared memory and walks the same tile list; no host synchronisation.
 //    Offsets that decrease or pass T are clamped and reported
 //    (CF_ERR_DEVICE_BOUNDS), so no read or write leaves its array.
-//  * Warp roles as in the fused GEMM: warp 0 issues TMA loads into a ring,
-//    warp 1 the MMAs into one of two accumulators, warps 2..9 the epilogue of
-//    tile i while tile i + 1 is multiplied; every wait is bounded.
+//  * Warp roles as in the fused GEMM: warp 0 issues TMA loads into a ring, warp
+//    1 the MMAs into one of two accumulators, warps 2..9 the epilogue of tile i
+//    while tile i + 1 is multiplied; every wait is bounded.  The first two run
+//    their loops as whole warps and issue by an elected lane: a loop of one lane
+//    spent some 600 cycles a block on its own control flow (16384 rows over 8
+//    groups of 2048 x 8192: 351 us, now 308 to 320).
+//  * CTA pairs (M = 256, cta_group::2) where there are tiles enough for them:
+//    each CTA stages its own 128 features and half of the rows, so a block costs
+//    an SM 32 KB of copies in place of 48 (single CTAs 356 us there).
+//  * Few tiles with a long contraction are divided among the SMs: pieces of fp32
+//    accumulators in the workspace, added in a fixed order by the last arriver.
+//
+// What bounds each form, and what it measured on a GB300 (in a CUDA graph):
+//     FORWARD  16384 rows, 8 groups of 2048 x 8192, GELU: the tensor pipe, 308 to 320 us (1.72 to 1.78 PFLOP/s);
+//              250 rows, 32 groups of 2048 x 4096: HBM, 72 us (6.6 TB/s); 4099 rows, 64 groups of 1000 x 2056: HBM,
+//              47 us (5.4 TB/s); 2 rows, 8 groups of 1024 x 2048: latency, 7.4 us (launch 2, table 1.5, first copy 1,
+//              16 blocks in pieces 1, joining them 1.5)
+//     DGRAD    16384 rows, 16 groups of 4096 x 2048, GELU': the tensor pipe, 169 to 181 us (1.52 to 1.63 PFLOP/s);
+//              333 rows, 12 groups of 520 x 1032: latency, 7.4 us
+//     WGRAD    16384 rows, 8 groups of 2048 x 8192: the tensor pipe, 325 to 343 us (1.60 to 1.69 PFLOP/s); 1003 rows, 24
+//              groups of 520 x 1032: its 1080 epilogues, 16.3 us (1.8 TB/s)
+//     LORA     with its SHRINK, 8192 rows of 8 requests, 4096 x 4096, rank 64: the tensor pipe, 167 to 171 us (1.65 to
+//              1.68 PFLOP/s); one row, rank 16: 13.3 us, 64 requests of one row: 22.5 us (the chain X . A, join, H . B,
+//              join beside 33 MB of W); 1537 rows of 40 requests, 2048 x 2056, rank 24: 43 us (the chain, then row
+//              tiles that requests do not fill)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -232,8 +254,8 @@ struct Table {
     int *off;   // [groups + 1] first row of each group (LORA: request)
     int *pre;   // [plan groups + 1] tiles of the groups before (WGRAD: blocks of one tile of each)
     int *ad;    // SHRINK, LORA: adapter of each request, -1 for none
-    int *goff;  // LORA: [plan groups + 1] first row of each plan group
-    int *gad;   // LORA: its adapter, -1 none, -2 a run of short requests
+    int *goff;  // LORA: [plan groups + 1] first row of each plan group: a long request, or a run of short ones
+    int *gad;   // LORA: its adapter, -1 none, -2 a run
     int *turn;  // LORA: [groups] changes of the adapter up to each request
     __device__ Table(uint8_t *p, int kind, int groups) {
         plan = reinterpret_cast<Plan *>(p);
@@ -527,8 +549,8 @@ __device__ __forceinline__ void turned(float (&x)[8], const float *stg, int lane
 }
 
 // the pieces of the pre-activation's fragment at column c of the tile (zeros outside)
-__device__ __forceinline__ void load_fragment(uint4 (&z)[4], const GroupedArgs &a, const Tile &w, int c, int q, int lane,
-                                              bool ok) {
+__device__ __forceinline__ void load_fragment(uint4 (&z)[4], const GroupedArgs &a, const Tile &w, int c, int q,
+                                              int lane, bool ok) {
     const int f = w.f0 + q * 32 + (lane & 3) * 8;
     const uint16_t *p = static_cast<const uint16_t *>(a.preact) + size_t(w.col0 + c + (lane >> 2)) * a.F + f;
 #pragma unroll
@@ -663,9 +685,10 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
             const int stretch = max(share, kMinStretch);
             const int rounds = (p.tiles + workers - 1) / workers;
             // WGRAD: of mean tiles, or the longest one
-            const int whole = KIND == GR_WGRAD ? max(rounds * ((units + p.tiles - 1) / p.tiles), longest) : rounds * nkc;
-            // Equal parts of every tile, where there are workers for two at least: a worker then has one piece, not the
-            // end of one tile and the start of another, each of which costs what adding a piece costs.
+            const int mean = KIND == GR_WGRAD ? (units + p.tiles - 1) / p.tiles : nkc;
+            const int whole = max(rounds * mean, longest);
+            // Equal parts of every tile, where there are workers for two at least: a worker then has one piece, not
+            // the end of one tile and the start of another, each of which costs what adding a piece costs.
             const int most = KIND == GR_WGRAD ? 0 : min(workers / p.tiles, nkc / kMinStretch);
             const int n = min(a.bn, (rows_all + ngroups - 1) / ngroups + 15);  // columns of a tile, about
             const int cols = KIND == GR_WGRAD ? a.bn : n;
@@ -694,9 +717,9 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
 
 // A block of the contraction stages 16 KB of the feature operand (8 KB where there are no more than 64 features; what
 // is behind the last feature is zero or stale, in lanes that are never stored) and the tile's columns: one box of rows,
-// of the full width or of half of it.  (An SM takes 75 B of copies a cycle, so a narrow tile that brings a full box pays
-// for it: 120 rows a group at 256 columns took 650 cycles a block, not 440.)  Rows of a box behind the tile's are its
-// neighbour's, in columns that are not multiplied or not stored.  WGRAD: 64-column blocks to fill.
+// of the full width or of half of it.  (An SM takes 75 B of copies a cycle: a group of up to 128 rows at 256 columns
+// takes 440 cycles a block by half boxes, 650 by full ones.)  Rows of a box behind the tile's are its neighbour's, in
+// columns that are not multiplied or not stored.  WGRAD: 64-column blocks to fill.
 template <bool kPair>
 __device__ __forceinline__ bool half_box(const GroupedArgs &a, const Tile &w) {
     return kPair ? w.nm <= a.bn / 2 : 2 * w.nm <= a.bn;
@@ -890,8 +913,8 @@ __device__ __forceinline__ void add_low_rank(float (&x)[8], const GroupedArgs &a
 // sums[row][64].  kFly pieces in flight: one row takes fewer registers for its sums, so more loads (beside the
 // projection, which saturates HBM at the same time, each turn of the loop costs about 2000 cycles).
 template <int kRows, int kFly>
-__device__ __forceinline__ void short_sums(const GroupedArgs &a, const uint16_t *wa, const uint16_t *x, int left, int step,
-                                           int rows, int shift, int lane, float *sums, bool live) {
+__device__ __forceinline__ void short_sums(const GroupedArgs &a, const uint16_t *wa, const uint16_t *x, int left,
+                                           int step, int rows, int shift, int lane, float *sums, bool live) {
     const bool fp16 = a.fp16 != 0;
     float acc[8 * kRows];
 #pragma unroll
@@ -903,7 +926,8 @@ __device__ __forceinline__ void short_sums(const GroupedArgs &a, const uint16_t 
 #pragma unroll
         for (int i = 0; i < kFly; ++i) {
             const bool in = k + i * step < left;
-            w[i] = in ? __ldg(reinterpret_cast<const uint4 *>(wa + size_t(k + i * step) * a.F)) : make_uint4(0u, 0u, 0u, 0u);
+            w[i] = in ? __ldg(reinterpret_cast<const uint4 *>(wa + size_t(k + i * step) * a.F))
+                      : make_uint4(0u, 0u, 0u, 0u);
             xs[i] = in ? __ldg(x + k + i * step) : uint16_t(0);
         }
 #pragma unroll
@@ -963,14 +987,16 @@ __device__ void shrink_short(const GroupedArgs &a, const Table &tab, float *sums
         const int piece = lane & ((1 << shift) - 1);
         const bool live = piece < pieces;
         const int step = (kShortWarps * 32) >> shift;  // rows of A side by side
-        const uint16_t *wa = static_cast<const uint16_t *>(a.lora_a) + size_t(ad) * a.C * a.F + r0 + (live ? piece * 8 : 0);
+        const uint16_t *wa =
+            static_cast<const uint16_t *>(a.lora_a) + size_t(ad) * a.C * a.F + r0 + (live ? piece * 8 : 0);
         const int k_end = min(a.C, (part + 1) * span);
         for (int t0 = 0; t0 < rows; t0 += 4) {
             const uint16_t *x = static_cast<const uint16_t *>(a.x) + size_t(lo + t0) * a.C;
             const int k0 = part * span + (tid >> shift);
             const uint16_t *row = wa + size_t(k0) * a.F;
-            if (rows == 1) short_sums<1, 12>(a, row, x + k0, k_end - k0, step, 1, shift, lane, sums + warp * 256 + piece * 8, live);
-            else short_sums<4, 6>(a, row, x + k0, k_end - k0, step, rows - t0, shift, lane, sums + warp * 256 + piece * 8, live);
+            float *const mine = sums + warp * 256 + piece * 8;
+            if (rows == 1) short_sums<1, 12>(a, row, x + k0, k_end - k0, step, 1, shift, lane, mine, live);
+            else short_sums<4, 6>(a, row, x + k0, k_end - k0, step, rows - t0, shift, lane, mine, live);
             ptx::named_bar_sync(4, kShortWarps * 32);
             for (int i = tid; i < 4 * pieces * 8; i += kShortWarps * 32) {
                 const int j = i / (pieces * 8), r = i - j * pieces * 8;
@@ -978,10 +1004,9 @@ __device__ void shrink_short(const GroupedArgs &a, const Table &tab, float *sums
                     float h = 0.f;
 #pragma unroll
                     for (int g = 0; g < kShortWarps; ++g) h += sums[(g * 4 + j) * 64 + r];
-                    if (a.low_split > 1)
-                        __stcg(a.low_parts + (size_t(uc) * a.low_split + part) * (kShortRows * 64) + (t0 + j) * 64 + r, h);
-                    else
-                        store_low(a, lo + t0 + j, r0 + r, a.scale ? h * __ldg(a.scale + ad) : h);
+                    float *const parts = a.low_parts + (size_t(uc) * a.low_split + part) * (kShortRows * 64);
+                    if (a.low_split > 1) __stcg(parts + (t0 + j) * 64 + r, h);
+                    else store_low(a, lo + t0 + j, r0 + r, a.scale ? h * __ldg(a.scale + ad) : h);
                 }
             }
             ptx::named_bar_sync(4, kShortWarps * 32);
@@ -1041,8 +1066,8 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint64_t ad, uint64_t bd, 
             "add.s64 a, %1, %10;\n\tadd.s64 b, %2, %11;\n\t"
             "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n\t"
             "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], m;\n\t}"
-            ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(bar), "n"(kA), "n"(kB), "n"(2 * kA), "n"(2 * kB),
-            "n"(3 * kA), "n"(3 * kB)
+            ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(bar), "n"(kA), "n"(kB), "n"(2 * kA),
+            "n"(2 * kB), "n"(3 * kA), "n"(3 * kB)
             : "memory");
     } else {
         asm volatile(
@@ -1057,8 +1082,8 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint64_t ad, uint64_t bd, 
             "add.s64 a, %1, %10;\n\tadd.s64 b, %2, %11;\n\t"
             "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
             "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}"
-            ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(bar), "n"(kA), "n"(kB), "n"(2 * kA), "n"(2 * kB),
-            "n"(3 * kA), "n"(3 * kB)
+            ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(bar), "n"(kA), "n"(kB), "n"(2 * kA),
+            "n"(2 * kB), "n"(3 * kA), "n"(3 * kB)
             : "memory");
     }
 }
@@ -1127,8 +1152,9 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint64_
 
 // The producer loop, of a whole warp with an elected lane that issues (as in the MMA loop).
 template <int KIND, bool kPair>
-__device__ __forceinline__ void produce(const GroupedArgs &a, Walk<KIND, kPair> &walk, const GrLayout &L, const GrBars &B,
-                                        uint32_t base, uint32_t crank, uint64_t tmo, volatile uint32_t *abort) {
+__device__ __forceinline__ void produce(const GroupedArgs &a, Walk<KIND, kPair> &walk, const GrLayout &L,
+                                        const GrBars &B, uint32_t base, uint32_t crank, uint64_t tmo,
+                                        volatile uint32_t *abort) {
     const int stages = a.stages;
     const bool leader = crank == 0u;
     const uint32_t full_lead = kPair ? ptx::mapa(B.full0, 0u) : B.full0;
@@ -1318,7 +1344,8 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                         if (!__all_sync(0xffffffffu, ok)) break;
                         ph ^= 1u << at;
                         const int left = w.rows - (w.nk - 1) * kBK;
-                        zero_tail(smem_raw + at * L.stage_bytes, left, (left + 15) / 16, a.a_blocks + (w.nm / 2 + 63) / 64, lane);
+                        zero_tail(smem_raw + at * L.stage_bytes, left, (left + 15) / 16,
+                                  a.a_blocks + (w.nm / 2 + 63) / 64, lane);
                         if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(B.full0 + 8 * at, 0u));
                     }
                     s = (s + uint32_t(w.nk)) % uint32_t(stages);
@@ -1328,8 +1355,9 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
             // The whole warp runs the loop, and one lane of it issues: control flow and descriptors that are the warp's
             // own keep the work between MMA groups short, so that the tensor pipe's queue does not run dry.
             const uint64_t ad0 = kAMn ? sw128_desc(base, 8192, 1024) : sw128_desc(base, 16, 1024);
-            const uint64_t bd0 = kBMn ? sw128_desc(base + L.a_bytes, 8192, 1024) : sw128_desc(base + L.a_bytes, 16, 1024);
-            constexpr int kAStep = kAMn ? 128 : 2, kBStep = kBMn ? 128 : 2;  // of 16 in the contraction, descriptor units
+            const uint64_t bd0 =
+                kBMn ? sw128_desc(base + L.a_bytes, 8192, 1024) : sw128_desc(base + L.a_bytes, 16, 1024);
+            constexpr int kAStep = kAMn ? 128 : 2, kBStep = kBMn ? 128 : 2;  // of 16 in the contraction
             const uint32_t stage_step = L.stage_bytes >> 4;
             const bool elected = ptx::elect_one();  // the same lane as in mma_block: commits cover their thread's MMAs
             uint32_t s = 0, ph = 0;
@@ -1377,7 +1405,8 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                     if (!ok) break;
                     ptx::tc_fence_after();
                     const uint64_t so = uint64_t(s * stage_step);
-                    mma_block<kPair, kAStep, kBStep>(d, ad0 + so, bd0 + so, idesc, kb > kb0 ? 1u : 0u, B.empty0 + 8 * s);
+                    mma_block<kPair, kAStep, kBStep>(d, ad0 + so, bd0 + so, idesc, kb > kb0 ? 1u : 0u,
+                                                     B.empty0 + 8 * s);
                     if (++s == uint32_t(stages)) {
                         s = 0;
                         ph ^= 1u;
@@ -1398,8 +1427,8 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                         const uint64_t so = uint64_t(s * stage_step);
                         if (elected) {
                             for (int k = 0; k < steps; ++k)
-                                issue_mma<kPair>(d, ad0 + so + uint64_t(k * kAStep), bd0 + so + uint64_t(k * kBStep), idesc,
-                                                 whole > kb0 || k > 0 ? 1u : 0u);
+                                issue_mma<kPair>(d, ad0 + so + uint64_t(k * kAStep), bd0 + so + uint64_t(k * kBStep),
+                                                 idesc, whole > kb0 || k > 0 ? 1u : 0u);
                             issue_commit<kPair>(B.empty0 + 8 * s);
                         }
                         __syncwarp();
@@ -1446,7 +1475,8 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                             const int ad = tab.ad[request_of(tab, a.groups, w.col0 + j)];
                             const int f8 = w.f0 + q * 32 + (lane & 3) * 8;
                             if (ad < 0 || f8 >= a.F) continue;
-                            const uint16_t *b = static_cast<const uint16_t *>(a.lora_b) + size_t(ad) * a.rank * a.F + f8;
+                            const uint16_t *b =
+                                static_cast<const uint16_t *>(a.lora_b) + size_t(ad) * a.rank * a.F + f8;
                             for (int r = lane & 3; r < a.rank; r += 4)
                                 ptx::prefetch_l2(b + size_t(r) * a.F - (lane & 3) * 8);
                         }
