@@ -1470,7 +1470,8 @@ int grouped_columns(const GroupedShape &s, bool *pair) {
     }
     int best = 256;
     double cycles = 1e300;
-    for (int bn = 256; bn >= (s.kind == cf::GR_WGRAD ? 64 : 16); bn /= 2) {  // WGRAD stages dY in 64-column blocks
+    // (of equals the narrowest, which leaves shared memory; WGRAD stages dY in 64-column blocks)
+    for (int bn = s.kind == cf::GR_WGRAD ? 64 : 16; bn <= 256; bn *= 2) {
         for (int p = grouped_may_pair(s.kind, bn, s.F) ? 1 : 0; p >= 0; --p) {
             const double c = grouped_cycles(s, bn, p == 1);
             if (c < cycles) {
