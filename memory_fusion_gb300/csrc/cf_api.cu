@@ -1392,7 +1392,7 @@ cf_status grouped_sizes(int64_t T, int64_t N, int64_t K, int64_t groups, int dty
 // where they are wider than a tile.  Measured on a GB300 (about 1.8 GHz under load): an MMA block of n columns takes
 // 2.35 n cycles (600 at 256) and 290 at least (370 in a pair), copies arrive at 75 B per cycle and SM (43 where the
 // matrix's rows are no multiples of 128 bytes: 2048 features 17.4 us, 2056 21.9), HBM gives the chip 3770 B per cycle;
-// an epilogue takes 1500 cycles and 20 a column, 900 more where a pair turns a weight gradient; dividing tiles costs
+// an epilogue takes 1500 cycles and 20 a column, 900 more in a pair; dividing tiles costs
 // 1500 cycles and 70 a column (writing, adding, finishing), the low-rank product of rows with adapters of their own
 // 1000 cycles for 8 rows and 8 ranks.  Against every width and both CTA counts, timed over 180 random sizes, the choice
 // takes 4 % more time than the best one in the geometric mean.
@@ -1409,6 +1409,22 @@ double copy_cycles(const GroupedShape &s, int bn, bool pair) {
     const bool wgrad = s.kind == cf::GR_WGRAD;
     const int64_t a_row = s.kind == cf::GR_DGRAD ? s.C : s.F, b_row = wgrad ? s.N : s.C;
     return 16384 * (a_row % 64 ? 1.75 : 1.0) / 75 + (pair ? 64.0 : 128.0) * bn * (b_row % 64 ? 1.75 : 1.0) / 75;
+}
+
+// accumulator columns of SHRINK's tiles: one tile of features, row tiles for every SM
+int shrink_columns(int64_t T) {
+    int bn = 16;
+    while (bn < 256 && bn * cf::kGroupedWorkers < T) bn *= 2;
+    return bn;
+}
+
+// LORA: cycles from its first copy until H is there (the two launches start together), and the SMs that H keeps busy
+double lora_wait(const GroupedShape &s, double *busy) {
+    const int bn = shrink_columns(s.T);
+    const double blocks = double((s.C + 63) / 64), tiles = double((s.T + bn - 1) / bn);
+    const double ways = std::max(1.0, std::min(std::floor(kPlanSms / tiles), std::floor(blocks / 4)));
+    *busy = std::min(kPlanSms, tiles * ways);
+    return 2500 + blocks / ways * 300 + (ways > 1 ? 2500 : 0) + 1500 + 20 * bn;
 }
 
 double grouped_cycles(const GroupedShape &s, int bn, bool pair) {
@@ -1446,15 +1462,23 @@ double grouped_cycles(const GroupedShape &s, int bn, bool pair) {
     const double copies = copy_cycles(s, !wgrad && 2 * n <= bn ? bn / 2 : bn, pair);
     const double block = std::max(std::max(2.35 * n, pair ? 370.0 : 290.0), copies);
     const double main = blocks * block + 400, hbm = bytes / 3770;
-    const double epilogue = 1500 + 20 * n + (wgrad && pair ? 900 : 0) + low;
+    const double epilogue = 1500 + 20 * n + (pair ? 900 : 0) + low;
+    // no accumulator is complete before H is there, and a CTA whose SM H keeps busy starts then
+    double busy = 0;
+    const double wait = s.kind == cf::GR_LORA ? lora_wait(s, &busy) : 0;
+    auto after = [&](double work, double ctas) {
+        return busy + ctas * (pair ? 2 : 1) > kPlanSms ? wait + work : std::max(wait, work);
+    };
     // two things that go on at once hardly ever overlap quite
     auto both = [](double a, double b) { return std::max(a, b) + 0.3 * std::min(a, b); };
     const double rounds = std::ceil(tiles / sms - 1e-9);
-    const double whole = both(rounds * std::max(main, epilogue) + std::min(main, epilogue), hbm);
+    const double first = after((rounds - 1) * std::max(main, epilogue) + main, std::min(tiles, sms));
+    const double whole = both(first + epilogue, hbm);
     if (pair || tiles > double(cf::kGroupedSplitTiles)) return whole;
     const double each = std::max(tiles * main / sms, 4 * block);
     const double parts = std::max(1.0, sms / tiles);
-    const double split = both(each, hbm) + 1500 + 70 * n + 1500 + 20 * n + low / parts;
+    const double mine = after(each, std::min(sms, tiles * (blocks / 4)));
+    const double split = both(mine, hbm) + 1500 + 70 * n + 1500 + 20 * n + low / parts;
     return std::min(whole, split);
 }
 
@@ -1463,14 +1487,10 @@ bool grouped_may_pair(int kind, int bn, int64_t F) { return kind != cf::GR_SHRIN
 // the tile width where none is asked for, and whether CTA pairs work on it
 int grouped_columns(const GroupedShape &s, bool *pair) {
     *pair = false;
-    if (s.kind == cf::GR_SHRINK) {  // one tile of features: row tiles for every SM
-        int bn = 16;
-        while (bn < 256 && bn * cf::kGroupedWorkers < s.T) bn *= 2;
-        return bn;
-    }
+    if (s.kind == cf::GR_SHRINK) return shrink_columns(s.T);
     int best = 256;
     double cycles = 1e300;
-    // (of equals the narrowest, which leaves shared memory; WGRAD stages dY in 64-column blocks)
+    // (of equals the narrowest; WGRAD stages dY in 64-column blocks)
     for (int bn = s.kind == cf::GR_WGRAD ? 64 : 16; bn <= 256; bn *= 2) {
         for (int p = grouped_may_pair(s.kind, bn, s.F) ? 1 : 0; p >= 0; --p) {
             const double c = grouped_cycles(s, bn, p == 1);
@@ -1520,14 +1540,9 @@ cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int
     if (pair && (kind == cf::GR_SHRINK || bn < 128)) return CF_ERR_UNSUPPORTED;
     const int a_blocks = F <= 64 && kind != cf::GR_DGRAD && !pair ? 1 : 2;
     // (deeper rings of small stages were slower: 250 rows over 32 groups of 2048 x 4096, 12 stages 76.9 us, 8 73.2)
-    int stages = t.stages > 0 ? t.stages : kind == cf::GR_SHRINK ? 12 : 8;
-    // a decode batch's two adapter products share the SMs: the second reads its weights while the first runs
-    const int shrink_room = 98 * 1024, room_smem = bn > 64                ? kMaxSmem
-                                                   : kind == cf::GR_SHRINK ? shrink_room
-                                                   : kind == cf::GR_LORA   ? kMaxSmem - shrink_room - 2048
-                                                                           : kMaxSmem;
+    int stages = t.stages > 0 ? t.stages : 8;
     auto bytes = [&](int n) { return cf::grouped_smem_bytes(kind, pair, n, bn, int(groups), int(rank), a_blocks); };
-    while (stages > 2 && bytes(stages) > room_smem) --stages;
+    while (stages > 2 && bytes(stages) > kMaxSmem) --stages;
     *smem = bytes(stages);
     if (*smem > kMaxSmem || *smem > dev.max_smem_optin) return CF_ERR_UNSUPPORTED;
     const int width = pair ? 2 : 1;
@@ -1544,6 +1559,8 @@ cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int
     a->a_blocks = a_blocks;
     a->stages = stages;
     a->copy_cycles = int(copy_cycles(shape, bn, pair));
+    double busy;
+    a->wait_cycles = kind == cf::GR_LORA ? int(std::min(1e9, lora_wait(shape, &busy))) : 0;
     a->counters = reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(ws) + cf::kErrBytes +
                                                size_t(set) * kGroupedCounterBytes);
     // (a forced tile wider than the workspace was sized for: whole tiles only)

@@ -40,8 +40,8 @@
 //              16 blocks in pieces 1, joining them 1.5)
 //     DGRAD    16384 rows, 16 groups of 4096 x 2048, GELU': the tensor pipe, 169 to 181 us (1.52 to 1.63 PFLOP/s);
 //              333 rows, 12 groups of 520 x 1032: latency, 7.4 us
-//     WGRAD    16384 rows, 8 groups of 2048 x 8192: the tensor pipe, 325 to 343 us (1.60 to 1.69 PFLOP/s); 1003 rows, 24
-//              groups of 520 x 1032: its 1080 epilogues, 16.3 us (1.8 TB/s)
+//     WGRAD    16384 rows, 8 groups of 2048 x 8192: the tensor pipe, 325 to 343 us (1.60 to 1.69 PFLOP/s); 1003 rows,
+//              24 groups of 520 x 1032: its 600 epilogues of 256 columns, 16.3 us (1.8 TB/s)
 //     LORA     with its SHRINK, 8192 rows of 8 requests, 4096 x 4096, rank 64: the tensor pipe, 167 to 171 us (1.65 to
 //              1.68 PFLOP/s); one row, rank 16: 13.3 us, 64 requests of one row: 22.5 us (the chain X . A, join, H . B,
 //              join beside 33 MB of W); 1537 rows of 40 requests, 2048 x 2056, rank 24: 43 us (the chain, then row
@@ -110,13 +110,35 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
-// 8 columns of 32 lanes of tensor memory
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "r"(taddr)
+// 32 columns of 32 lanes of tensor memory in 8 x 8 blocks: of lanes 8b..8b+7 and columns 8k..8k+7, thread t holds lane
+// t / 4 and columns 2 (t % 4) and the next, in v[16 (b / 2) + 4 k + 2 (b % 2)] and the next
+__device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, uint32_t (&v)[32]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(v[16 * h]), "=r"(v[16 * h + 1]), "=r"(v[16 * h + 2]), "=r"(v[16 * h + 3]), "=r"(v[16 * h + 4]),
+              "=r"(v[16 * h + 5]), "=r"(v[16 * h + 6]), "=r"(v[16 * h + 7]), "=r"(v[16 * h + 8]),
+              "=r"(v[16 * h + 9]), "=r"(v[16 * h + 10]), "=r"(v[16 * h + 11]), "=r"(v[16 * h + 12]),
+              "=r"(v[16 * h + 13]), "=r"(v[16 * h + 14]), "=r"(v[16 * h + 15])
+            : "r"(taddr + (uint32_t(16 * h) << 16))
+            : "memory");
+}
+// four 8 x 8 blocks of 16-bit numbers to and from shared memory, transposed: thread t holds row t / 4, columns
+// 2 (t % 4) and the next of each block; thread 8m + j gives the 16 bytes that are column j of block m
+__device__ __forceinline__ void stmatrix4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
                  : "memory");
 }
+__device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+                 : "r"(addr)
+                 : "memory");
+}
+
 // one lane of a converged warp, the same one every time
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
@@ -137,12 +159,14 @@ __device__ __forceinline__ uint32_t idesc_f16(int m, int n, bool fp16, bool a_mn
 
 
 // Epilogue warps, from warp 2 on: two halves of 4 (128 lanes each); SHRINK one, and two more warps that only help
-// with its short requests.  A decode batch's SHRINK and LORA share the SMs, one CTA of each: 256 threads of 96
-// registers and 320 of 128 are what an SM has.
+// with its short requests.
 __host__ __device__ constexpr int epi_warps(int kind) { return kind == GR_SHRINK ? 4 : 8; }
 __host__ __device__ constexpr int threads_of(int kind) { return kind == GR_SHRINK ? 256 : 320; }
-__host__ __device__ constexpr int registers_of(int kind, bool pair) {
-    return kind == GR_SHRINK ? 96 : kind == GR_LORA && !pair ? 128 : 200;
+// Ten warps are three on a quarter of the SM: 168 registers each.  (WGRAD takes 134 of what it is offered; offered 168
+// it was scheduled to take 124 and 1003 rows over 24 groups took 18.1 us, not 16.3.  Fewer, so that a CTA of LORA fits
+// beside one of SHRINK, gained nothing: 64 requests 22.4 us, 21.8 without.)
+__host__ __device__ constexpr int registers_of(int kind) {
+    return kind == GR_SHRINK ? 128 : kind == GR_WGRAD ? 200 : 168;
 }
 constexpr int kShortWarps = 6;
 constexpr int kBK = 64;         // contraction per stage (128 bytes: one swizzle atom)
@@ -179,11 +203,10 @@ __host__ __device__ inline GrLayout gr_layout(int kind, bool pair, int stages, i
     L.table = off;
     off += (32u + uint32_t(table_arrays(kind) * (groups + 1)) * 4u + 15u) & ~15u;
     // per epilogue warp: 16-bit [32 rows][32 features]; LORA: fp32; WGRAD: 16-bit [32 features][64 columns];
-    // SHRINK: the warps' sums of 4 rows x 64 ranks
+    // SHRINK: before that, the warps' sums of 4 rows x 64 ranks
     L.stg = off;
-    off += kind == GR_LORA ? 8u * 4096u
-                           : (kind == GR_FORWARD || kind == GR_DGRAD) ? 8u * 2048u
-           : kind == GR_WGRAD ? 8u * 4096u : uint32_t(kShortWarps) * 4u * 64u * 4u;
+    off += (kind == GR_LORA || kind == GR_WGRAD) ? 8u * 4096u : kind == GR_SHRINK ? 4u * 2048u : 8u * 2048u;
+    static_assert(kShortWarps * 4 * 64 * 4 <= 4 * 2048, "sums of the short requests");
     L.bars = (off + 15u) & ~15u;
     L.total = L.bars + 256u;
     return L;
@@ -225,7 +248,7 @@ struct Tile {
     int extra;  // LORA: blocks of the low-rank product behind the tile's own (pieces: with the last)
     int ad;     // LORA: the adapter of the first nx columns' rows, -1 none
     int nx;     // LORA: columns whose low-rank product runs on the tensor cores: all of the tile (nm), or a long
-                // request's in whole 16s (a pair: 32s)
+                // request's in whole 16s
     bool mixed; // LORA: the columns behind them are of several requests
     int first, last;  // workers that hold pieces of the tile
     int slot;   // which of its two workspace slots this worker's piece goes to
@@ -404,7 +427,7 @@ struct Walk {
             } else {  // requests in a row may share an adapter
                 const int s0 = request_of(tab, a.groups, r.col0), s1 = request_of(tab, a.groups, r.col0 + r.n - 1);
                 r.mixed = tab.turn[s0] != tab.turn[s1];
-                r.nx = r.mixed ? own & ~(kGran - 1) : r.nm;
+                r.nx = r.mixed ? own & ~15 : r.nm;
                 if (r.nx > 0) r.ad = tab.ad[s0];
             }
         }
@@ -464,42 +487,103 @@ __device__ __forceinline__ float from16(uint16_t v, bool fp16) {
     return fp16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(uint32_t(v) << 16);
 }
 
-// 16-bit part of H: rounded; fp16 saturates (an infinity stays one), the rest goes to the other part
-__device__ __forceinline__ uint16_t low_part(float h, bool fp16) {
-    if (fp16 && fabsf(h) > 65504.f && isfinite(h)) h = copysignf(65504.f, h);
-    return to16(h, fp16);
+// two numbers rounded to 16 bits, and back
+template <bool kFp16>
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+    if constexpr (kFp16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+constexpr float kFloatMax = 3.402823466e38f;
+// a finite number, saturated where fp16 is the type
+template <bool kFp16>
+__device__ __forceinline__ float fits(float h) {
+    return kFp16 && fabsf(h) > 65504.f && fabsf(h) <= kFloatMax ? copysignf(65504.f, h) : h;
 }
 
 // H in two 16-bit parts, upper and rest: 16 bits and more of mantissa (fp16: 22, within twice its range, behind which H
-// saturates), so that the second product can run on the tensor cores
+// saturates; an infinity or NaN goes to the upper part), so that the second product can run on the tensor cores
+template <bool kFp16>
+__device__ __forceinline__ void split_pair(uint32_t &up, uint32_t &rest, float lo, float hi) {
+    up = pack_pair<kFp16>(fits<kFp16>(lo), fits<kFp16>(hi));
+    const float rl = lo - from16(uint16_t(up), kFp16), rh = hi - from16(uint16_t(up >> 16), kFp16);
+    rest = pack_pair<kFp16>(fabsf(lo) <= kFloatMax ? fits<kFp16>(rl) : 0.f,
+                            fabsf(hi) <= kFloatMax ? fits<kFp16>(rh) : 0.f);
+}
 __device__ __forceinline__ void store_low(const GroupedArgs &a, int row, int r, float h) {
-    const bool fp16 = a.fp16 != 0;
+    uint32_t up, rest;
+    if (a.fp16) split_pair<true>(up, rest, h, 0.f);
+    else split_pair<false>(up, rest, h, 0.f);
     uint16_t *y = static_cast<uint16_t *>(a.out) + size_t(row) * (2 * a.F) + r;
-    const uint16_t up = low_part(h, fp16);
-    y[0] = up;
-    y[a.F] = isfinite(h) ? low_part(h - from16(up, fp16), fp16) : uint16_t(0);
+    y[0] = uint16_t(up);
+    y[a.F] = uint16_t(rest);
 }
 
-// A warp's fragment, 32 rows x 32 features, in its 2 KB of shared memory (64 bytes a row): lane l holds the 16-byte
-// piece l % 4 of rows l / 4, + 8, + 16, + 24.
+// A warp's fragment, 32 rows of the batch x 32 features, on its way between the accumulator's layout and memory's.  In
+// registers, as tmem_ld_blocks hands it out; in the warp's 2 KB of shared memory 64 bytes a row, its four 16-byte
+// pieces at piece ^ row / 2 % 4, so that neither side meets bank conflicts; lane l then holds piece l % 4 of rows
+// l / 4, + 8, + 16, + 24, and global memory is read and written in 16-byte pieces, 64 bytes a row.  (Turned a 16-bit
+// value at a time, 6792 rows of 55 groups of 96 x 5344 took 54 us, now 49.)
 struct Fragment {
     uint8_t *stg;
     int lane, cols;
     bool live;        // the piece's features exist
     size_t at, step;  // element of the first piece, and from a piece to the next
-    __device__ void put(const uint4 (&z)[4]) const {
+    __device__ uint8_t *piece(int i) const { return stg + i * 512 + ((lane >> 2) * 4 + ((lane ^ lane >> 3) & 3)) * 16; }
+    __device__ uint32_t block(int k) const {
+        return ptx::smem_u32(stg) + uint32_t(k * 512 + ((lane & 7) * 4 + ((lane >> 3 ^ lane >> 1) & 3)) * 16);
+    }
+    // memory's pieces in, the pairs of column block k and feature block b out, at p[4 k + b]
+    __device__ void load(const uint4 (&z)[4], uint32_t (&p)[16]) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(stg + i * 512 + lane * 16) = z[i];
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(piece(i)) = z[i];
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ptx::ldmatrix4_t(block(k), p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
         __syncwarp();
     }
-    __device__ void out(void *p) const {
+    // the same back to memory
+    __device__ void store(void *out, const uint32_t (&p)[16]) const {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ptx::stmatrix4_t(block(k), p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
         __syncwarp();
-        uint16_t *y = static_cast<uint16_t *>(p) + at;
+        uint16_t *y = static_cast<uint16_t *>(out) + at;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (live && (lane >> 2) + 8 * i < cols)
-                *reinterpret_cast<uint4 *>(y + i * step) = *reinterpret_cast<const uint4 *>(stg + i * 512 + lane * 16);
+                *reinterpret_cast<uint4 *>(y + i * step) = *reinterpret_cast<const uint4 *>(piece(i));
         __syncwarp();
+    }
+    // index of the first of the two accumulators that make p[4 k + b]
+    __device__ static constexpr int pair(int k, int b) { return 16 * (b / 2) + 4 * k + 2 * (b % 2); }
+    // the accumulators, rounded
+    template <bool kFp16>
+    __device__ static void pack(uint32_t (&p)[16], const uint32_t (&v)[32]) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int j = pair(i / 4, i % 4);
+            p[i] = pack_pair<kFp16>(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+        }
+    }
+    __device__ void store_rounded(void *out, const uint32_t (&v)[32], bool fp16) const {
+        uint32_t p[16];
+        if (fp16) pack<true>(p, v);
+        else pack<false>(p, v);
+        store(out, p);
+    }
+    // the accumulators times scale, split
+    template <bool kFp16>
+    __device__ static void split(uint32_t (&up)[16], uint32_t (&rest)[16], const uint32_t (&v)[32], float scale) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int j = pair(i / 4, i % 4);
+            split_pair<kFp16>(up[i], rest[i], scale * __uint_as_float(v[j]), scale * __uint_as_float(v[j + 1]));
+        }
     }
 };
 
@@ -686,7 +770,7 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
             const int rounds = (p.tiles + workers - 1) / workers;
             // WGRAD: of mean tiles, or the longest one
             const int mean = KIND == GR_WGRAD ? (units + p.tiles - 1) / p.tiles : nkc;
-            const int whole = max(rounds * mean, longest);
+            const int whole0 = max(rounds * mean, longest);
             // Equal parts of every tile, where there are workers for two at least: a worker then has one piece, not
             // the end of one tile and the start of another, each of which costs what adding a piece costs.
             const int most = KIND == GR_WGRAD ? 0 : min(workers / p.tiles, nkc / kMinStretch);
@@ -694,8 +778,10 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
             const int cols = KIND == GR_WGRAD ? a.bn : n;
             const int block = max(max(47 * cols / 20, 290), a.copy_cycles);
             const int adding = (1500 + 70 * cols) / block + 1;
-            const int even = most >= 2 ? (nkc + most - 1) / most + adding : 1 << 30;
-            const int mixed = stretch + adding + adding / 2;
+            const int least = a.wait_cycles / block;  // no tile can be finished before
+            const int whole = max(whole0, least);
+            const int even = most >= 2 ? max((nkc + most - 1) / most, least) + adding : 1 << 30;
+            const int mixed = max(stretch, least) + adding + adding / 2;
             if (whole > min(even, mixed)) {
                 p.split = 1;
                 p.units = units;
@@ -1244,7 +1330,7 @@ __device__ __forceinline__ void produce(const GroupedArgs &a, Walk<KIND, kPair> 
 }
 
 template <int KIND, bool kPair>
-__global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __grid_constant__ GroupedArgs a) {
+__global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_constant__ GroupedArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = ptx::smem_u32(smem_raw);
     if ((base & 1023u) != 0u) {  // the swizzled operand tiles need it; see the fused GEMM
@@ -1265,7 +1351,7 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
     const uint64_t tmo = a.timeout_ns;
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // one for the warp, and known to be
     const int lane = threadIdx.x & 31;
-    const uint32_t tmem_cols = uint32_t(2 * a.bn);
+    const uint32_t tmem_cols = uint32_t(max(2 * a.bn, 64));  // (a fragment of the second accumulator's is 32 wide)
     // A pair (two CTAs of a cluster) works on one tile of 256 features: the even CTA issues MMAs of M = 256 that
     // read both CTAs' shared memory and write both tensor memories (128 features each).
     const uint32_t crank = kPair ? ptx::cluster_ctarank() : 0u;
@@ -1568,40 +1654,47 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                 }
             }
             if constexpr (KIND == GR_SHRINK) {
-                // (a short loop: this runs once or twice a CTA, and 32 columns' worth of unrolled code took 7000 cycles
-                // to fetch, of a launch of 30000)
                 const float sc = a.scale ? __ldg(a.scale + w.w) : 1.f;
 #pragma unroll 1
-                for (int c = 0; c < w.n; c += 8) {
-                    uint32_t v[8];
-                    ptx::tmem_ld8(tacc + uint32_t(c), v);
+                for (int c = 0; c < w.n; c += 32) {
+                    uint32_t v[32], up[16], rest[16];
+                    ptx::tmem_ld_blocks(tacc + uint32_t(c), v);
                     ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (live && c + j < w.n) store_low(a, w.col0 + c + j, f, sc * __uint_as_float(v[j]));
+                    if (fp16) Fragment::split<true>(up, rest, v, sc);
+                    else Fragment::split<false>(up, rest, v, sc);
+                    const int f8 = w.f0 + q * 32 + (lane & 3) * 8;
+                    const Fragment fr{smem_raw + L.stg + e * 2048, lane, w.n - c, f8 < a.F && ok,
+                                      size_t(w.col0 + c + (lane >> 2)) * (2 * a.F) + f8, size_t(16) * a.F};
+                    fr.store(a.out, up);
+                    fr.store(static_cast<uint16_t *>(a.out) + a.F, rest);
                 }
+            }
+            float bias[4] = {0.f, 0.f, 0.f, 0.f};  // LORA: of a fragment's features in blocks
+            if constexpr (KIND == GR_LORA) {
+                const int fb = w.f0 + q * 32 + (lane >> 2);
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (a.bias && fb + 8 * b < a.F) bias[b] = __ldg(a.bias + fb + 8 * b);
             }
             // (WGRAD: the halves take alternate 64-column blocks)
             for (int c = half * kSpan; KIND != GR_SHRINK && c < w.n; c = next_fragment<kSpan, kHalves>(c)) {
                 uint32_t v[32];
-                if (kPair || KIND != GR_WGRAD || w.whole()) {
+                const int cols = min(32, w.n - c);
+                if constexpr (KIND == GR_WGRAD) {
+                    if (kPair || w.whole()) {
+                        ptx::tmem_ld32(tacc + uint32_t(c), v);
+                        ptx::tmem_ld_wait();
+                    } else {
+                        sum_pieces(v, pieces_of(a, walk, w), c, w.n, q * 32 + lane);
+                    }
+                    store_columns(v, a, w, c, reinterpret_cast<uint4 *>(smem_raw + L.stg + e * 4096), q, lane, ok);
+                } else if (KIND == GR_LORA && parts > 0 && c + 32 > w.nx) {
+                    // rows with adapters of their own
                     ptx::tmem_ld32(tacc + uint32_t(c), v);
                     ptx::tmem_ld_wait();
-                } else {
-                    sum_pieces(v, pieces_of(a, walk, w), c, w.n, q * 32 + lane);
-                }
-                const int cols = min(32, w.n - c);
-                if constexpr (KIND == GR_LORA) {
                     float *const stg = reinterpret_cast<float *>(smem_raw + L.stg) + e * 1024;
                     turn(v, stg, lane);
                     const int f8 = w.f0 + q * 32 + (lane & 3) * 8;
-                    float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    if (a.bias && f8 < a.F) {
-                        const float4 b0 = __ldg(reinterpret_cast<const float4 *>(a.bias + f8));
-                        const float4 b1 = __ldg(reinterpret_cast<const float4 *>(a.bias + f8) + 1);
-                        bias[0] = b0.x, bias[1] = b0.y, bias[2] = b0.z, bias[3] = b0.w;
-                        bias[4] = b1.x, bias[5] = b1.y, bias[6] = b1.z, bias[7] = b1.w;
-                    }
                     uint16_t *y = static_cast<uint16_t *>(a.out) + size_t(w.col0 + c + (lane >> 2)) * a.F + f8;
 #pragma unroll 1
                     for (int i = 0; i < 4; ++i, y += size_t(8) * a.F) {
@@ -1612,51 +1705,58 @@ __global__ void __maxnreg__(registers_of(KIND, kPair)) grouped_kernel(const __gr
                         if (c / 8 + i == early) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k) x[k] += low[k];
-                        } else if (parts > 0 && c + 8 * i >= w.nx) {
+                        } else if (c + 8 * i >= w.nx) {
                             add_low_rank(x, a, tab.ad[request_of(tab, a.groups, row)], row, f8);
+                        }
+                        if (a.bias) {
+                            const float4 b0 = __ldg(reinterpret_cast<const float4 *>(a.bias + f8));
+                            const float4 b1 = __ldg(reinterpret_cast<const float4 *>(a.bias + f8) + 1);
+                            x[0] += b0.x, x[1] += b0.y, x[2] += b0.z, x[3] += b0.w;
+                            x[4] += b1.x, x[5] += b1.y, x[6] += b1.z, x[7] += b1.w;
                         }
                         uint32_t p[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            p[k] = pack16(x[2 * k] + bias[2 * k], x[2 * k + 1] + bias[2 * k + 1], fp16);
+                        for (int k = 0; k < 4; ++k) p[k] = pack16(x[2 * k], x[2 * k + 1], fp16);
                         *reinterpret_cast<uint4 *>(y) = make_uint4(p[0], p[1], p[2], p[3]);
                     }
-                }
-                if constexpr (KIND == GR_FORWARD || KIND == GR_DGRAD) {
-                    // The fragment is turned in shared memory (a lane's feature column in, whole rows out), so that
-                    // global memory is read and written in 16-byte pieces, 64 bytes a row.
-                    uint8_t *const stg = smem_raw + L.stg + e * 2048;
-                    const Fragment fr{stg, lane, cols, (w.f0 + q * 32 + (lane & 3) * 8) < a.F && ok,
+                    __syncwarp();
+                } else {
+                    ptx::tmem_ld_blocks(tacc + uint32_t(c), v);
+                    ptx::tmem_ld_wait();
+                    constexpr uint32_t kStg = KIND == GR_LORA ? 4096u : 2048u;
+                    const Fragment fr{smem_raw + L.stg + e * kStg, lane, cols,
+                                      (w.f0 + q * 32 + (lane & 3) * 8) < a.F && ok,
                                       size_t(w.col0 + c + (lane >> 2)) * a.F + w.f0 + q * 32 + (lane & 3) * 8,
                                       size_t(8) * a.F};
-                    uint16_t *const mine = reinterpret_cast<uint16_t *>(stg) + lane;
                     if constexpr (KIND == GR_DGRAD) {
                         if (a.preact) {
-                            fr.put(zv);
+                            uint32_t z[16];
+                            fr.load(zv, z);
                             if (c + 64 < w.n)  // the next fragment's, while this one is worked on
                                 load_fragment(zv, a, w, c + 64, q, lane, ok);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[j] = __float_as_uint(__uint_as_float(v[j]) * gelu_slope(from16(mine[j * 32], fp16)));
-                            __syncwarp();
+                            for (int i = 0; i < 32; ++i) {
+                                const int j = Fragment::pair(i / 8, i / 2 % 4) + i % 2;
+                                v[j] = __float_as_uint(__uint_as_float(v[j]) *
+                                                       gelu_slope(from16(uint16_t(z[i / 2] >> (i % 2 * 16)), fp16)));
+                            }
                         }
                     }
                     if constexpr (KIND == GR_FORWARD) {
-                        if (a.preact) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) mine[j * 32] = to16(__uint_as_float(v[j]), fp16);
-                            fr.out(a.preact);
-                        }
+                        if (a.preact) fr.store_rounded(a.preact, v, fp16);
                         if (a.act) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(gelu(__uint_as_float(v[j])));
                         }
                     }
+                    if constexpr (KIND == GR_LORA) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) mine[j * 32] = to16(__uint_as_float(v[j]), fp16);
-                    fr.out(a.out);
-                } else if constexpr (KIND == GR_WGRAD) {
-                    store_columns(v, a, w, c, reinterpret_cast<uint4 *>(smem_raw + L.stg + e * 4096), q, lane, ok);
+                        for (int i = 0; i < 32; ++i) {
+                            const int j = Fragment::pair(i / 8, i / 2 % 4) + i % 2;
+                            v[j] = __float_as_uint(__uint_as_float(v[j]) + bias[i / 2 % 4]);
+                        }
+                    }
+                    fr.store_rounded(a.out, v, fp16);
                 }
             }
             ptx::tc_fence_before();

@@ -62,6 +62,7 @@ struct GroupedArgs {
     int bn;                  // columns of one accumulator tile (16, 32, 64, 128 or 256)
     int stages;
     int copy_cycles;         // what a block's copies take
+    int wait_cycles;         // LORA: what H takes, about
     int pair;                // CTA pairs, one cta_group::2 MMA stream over 256 features (not SHRINK)
     int extra_arrivals;      // test hook: arrivals that the accumulator-ready barriers wait for in vain
     unsigned long long timeout_ns;
