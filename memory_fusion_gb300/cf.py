@@ -760,6 +760,8 @@ def _run(what, call, device, stream, out, shape, dtype, workspace, nbytes):
     where none are given; the output."""
     import torch
     index = device.index
+    if workspace is not None and not (workspace.get_device() == index and workspace.is_contiguous()):
+        raise ValueError(f"workspace is not a contiguous tensor on {device}")
     if stream is None and index == torch._C._cuda_getDevice():  # nothing to switch: the decode step's path
         Y = out if out is not None else torch.empty(shape, dtype=dtype, device=device)
         ws = workspace if workspace is not None else new_workspace(nbytes(), device)

@@ -897,7 +897,7 @@ __device__ __forceinline__ void finish_row(const GroupedArgs &a, const Tile &w, 
         for (int i = 0; i < 4; ++i) s[i] *= gelu_slope(from16(uint16_t(zw[i / 2] >> ((i & 1) * 16)), fp16));
     }
     if (KIND == GR_LORA && a.bias) {
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(a.bias + f));
+        const float4 b = __ldcg(reinterpret_cast<const float4 *>(a.bias + f));
         s[0] += b.x, s[1] += b.y, s[2] += b.z, s[3] += b.w;
     }
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
@@ -1396,10 +1396,11 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
         ptx::griddep_launch_dependents();
         if (KIND != GR_LORA || !a.after_shrink) ptx::griddep_wait();
     }
+    // (LORA has not waited itself: nothing that another launch may have written is read through L1 before it has)
     for (int i = threadIdx.x; i <= a.groups; i += kThreads) {
-        tab.off[i] = a.offsets[i];
+        tab.off[i] = __ldcg(a.offsets + i);
         if constexpr (KIND == GR_SHRINK || KIND == GR_LORA)
-            if (i < a.groups) tab.ad[i] = a.windex[i];
+            if (i < a.groups) tab.ad[i] = __ldcg(a.windex + i);
     }
     __syncthreads();
     if (warp == 0) scan_table<KIND, kPair>(tab, a, workers, a.err);
@@ -1674,7 +1675,7 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                 const int fb = w.f0 + q * 32 + (lane >> 2);
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
-                    if (a.bias && fb + 8 * b < a.F) bias[b] = __ldg(a.bias + fb + 8 * b);
+                    if (a.bias && fb + 8 * b < a.F) bias[b] = __ldcg(a.bias + fb + 8 * b);
             }
             // (WGRAD: the halves take alternate 64-column blocks)
             for (int c = half * kSpan; KIND != GR_SHRINK && c < w.n; c = next_fragment<kSpan, kHalves>(c)) {
@@ -1709,8 +1710,8 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                             add_low_rank(x, a, tab.ad[request_of(tab, a.groups, row)], row, f8);
                         }
                         if (a.bias) {
-                            const float4 b0 = __ldg(reinterpret_cast<const float4 *>(a.bias + f8));
-                            const float4 b1 = __ldg(reinterpret_cast<const float4 *>(a.bias + f8) + 1);
+                            const float4 b0 = __ldcg(reinterpret_cast<const float4 *>(a.bias + f8));
+                            const float4 b1 = __ldcg(reinterpret_cast<const float4 *>(a.bias + f8) + 1);
                             x[0] += b0.x, x[1] += b0.y, x[2] += b0.z, x[3] += b0.w;
                             x[4] += b1.x, x[5] += b1.y, x[6] += b1.z, x[7] += b1.w;
                         }

@@ -8,7 +8,8 @@ import pytest
 import oracle
 from memory_fusion_gb300 import cf
 from tests.gpu_util import torch_cuda
-from tests.test_gpu_grouped import (ACC, SENTINEL, TUNINGS, _check, _dev, _host, _i32, _lora_case, _lora_run, _tuning)
+from tests.test_gpu_grouped import (ACC, SENTINEL, TUNINGS, _check, _dev, _host, _i32, _lora_case, _lora_run, _rng,
+                                    _status, _tuning)
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +109,58 @@ def test_same_rows_same_bits_alone_and_in_a_batch_of_copies(tun):
     y = _lora_run(c, "bf16", tuning=_tuning(tun))
     for a in (0, 1):
         assert torch.equal(y[a::2], y[a:a + 1].expand(20, -1))
+
+
+def test_replayed_after_its_inputs_were_written():
+    """A graph that writes offsets, adapters, bias, scale and X and then makes the call, back to back: every replay reads
+    what its own copies wrote, although the call's second launch starts before its first has ended."""
+    torch = torch_cuda()
+    K, N, L, R, S, T = 264, 136, 3, 24, 20, 200
+    rng = _rng(70)
+    W, A, B = (torch.from_numpy(rng.standard_normal(n)).cuda().bfloat16() / 8 for n in ((K, N), (L, K, R), (L, R, N)))
+    sets = []
+    for _ in range(6):
+        cuts = np.sort(rng.integers(0, T + 1, S - 1))
+        sets.append((_i32(np.concatenate([[0], cuts, [T]])), _i32(rng.integers(-1, L, S)),
+                     torch.from_numpy(rng.standard_normal(N)).cuda().float(),
+                     torch.from_numpy(rng.uniform(0.5, 2.0, L)).cuda().float(),
+                     torch.from_numpy(rng.standard_normal((T, K))).cuda().bfloat16()))
+    off, ad, bias, scale, X = (t.clone() for t in sets[0])
+    ws = cf.new_workspace(cf.cf_gemm_lora_workspace_size(T, N, K, S, R))
+    src = [t.clone() for t in sets[0]]
+    out = torch.empty(T, N, dtype=X.dtype, device="cuda")
+
+    def step():
+        for to, of in zip((off, ad, bias, scale, X), src):
+            to.copy_(of)
+        cf.gemm_lora(X, W, bias, A, B, off, ad, scale=scale, out=out, workspace=ws)
+
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step()
+            step()
+        got = []
+        for s in sets * 3:
+            for to, of in zip(src, s):
+                to.copy_(of)
+            graph.replay()
+            got.append(out.clone())
+    torch.cuda.synchronize()
+    for (o, a, b, sc, x), y in zip(sets * 3, got):
+        assert torch.equal(y, cf.gemm_lora(x, W, b, A, B, o, a, scale=sc))
+    _status(ws)
+
+
+def test_workspace_of_another_kind_is_refused():
+    torch = torch_cuda()
+    X = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    W = torch.zeros(2, 64, 128, dtype=torch.bfloat16, device="cuda")
+    n = cf.cf_grouped_gemm_workspace_size(8, 128, 64, 2)
+    for ws in (torch.zeros(n, dtype=torch.uint8), cf.new_workspace(2 * n)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            cf.grouped_gemm(X, W, _i32([0, 4, 8]), workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            cf.grouped_gemm(X, W, _i32([0, 4, 8]), workspace=ws, stream=torch.cuda.Stream())
