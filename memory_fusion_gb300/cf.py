@@ -710,10 +710,41 @@ def cf_gemm_lora(X, W, bias, A, B, offsets, adapters, scale, Y, T, N, K, S, L, R
                               _stream(stream), _tun(tuning))
 
 
+_ACTS = {"none": CF_ACT_NONE, "gelu_tanh": CF_ACT_GELU_TANH}
+_DTYPES = {}  # torch.bfloat16 and float16, once torch is there
+
+
+def _first(name, t, dims):
+    """Sizes, device and dtype of the tensor that the others have to agree with, and the library's name of its dtype."""
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        import torch
+        _DTYPES.update({torch.bfloat16: CF_BF16, torch.float16: CF_FP16})
+        dt = _DTYPES.get(t.dtype)
+    if not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, not on a CUDA device")
+    if dt is None:
+        raise ValueError(f"{name} has dtype {t.dtype}, not bfloat16 or float16")
+    shape = _sizes(name, t, dims)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    return shape, t.device, t.dtype, dt
+
+
+def _sizes(name, t, dims):
+    """The sizes of a tensor that has to have `dims` of them."""
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} has {len(shape)} dimensions, not {dims}")
+    return shape
+
+
 def _operand(name, t, shape, dtype, device):
-    """Check one tensor argument against its whole shape."""
+    """The address of a tensor argument (None: none), checked against its whole shape."""
+    if t is None:
+        return None
     if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
-        return
+        return t.data_ptr()
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if t.dtype != dtype:
@@ -723,22 +754,9 @@ def _operand(name, t, shape, dtype, device):
     raise ValueError(f"{name} is not contiguous")
 
 
-def _sizes(name, t, dims):
-    """The sizes of a tensor that has to have `dims` of them."""
-    if t.dim() != dims:
-        raise ValueError(f"{name} has {t.dim()} dimensions, not {dims}")
-    return t.shape
-
-
-def _grouped_dtype(name, t):
+def _int32():
     import torch
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} is on {t.device}, not on a CUDA device")
-    if t.dtype is torch.bfloat16:
-        return CF_BF16
-    if t.dtype is torch.float16:
-        return CF_FP16
-    raise ValueError(f"{name} has dtype {t.dtype}, not bfloat16 or float16")
+    return torch.int32
 
 
 @contextlib.contextmanager
@@ -755,90 +773,78 @@ def _launch_on(device, stream):
                 yield
 
 
-def _run(what, call, device, stream, out, shape, dtype, workspace, nbytes):
-    """call(out, workspace, its bytes, stream handle) on the operands' device, with the output and the workspace made
-    where none are given; the output."""
+def _run(name, before, between, out, shape, dtype, device, workspace, size, sizes, stream, tuning):
+    """name(*before, out, *between, workspace, its bytes, stream) on the operands' device, with the output and the
+    workspace (size(*sizes) bytes) made where none are given; the output.  (Written for the decode step, whose kernel
+    takes less time than the host does for its call.)"""
     import torch
     index = device.index
     if workspace is not None and not (workspace.get_device() == index and workspace.is_contiguous()):
         raise ValueError(f"workspace is not a contiguous tensor on {device}")
-    if stream is None and index == torch._C._cuda_getDevice():  # nothing to switch: the decode step's path
-        Y = out if out is not None else torch.empty(shape, dtype=dtype, device=device)
-        ws = workspace if workspace is not None else new_workspace(nbytes(), device)
-        check(call(Y, ws, ws.nbytes, torch._C._cuda_getCurrentRawStream(index)), what)
-        return Y
-    with _launch_on(device, stream):
-        Y = out if out is not None else torch.empty(shape, dtype=dtype, device=device)
-        ws = workspace if workspace is not None else new_workspace(nbytes(), device)
-        check(call(Y, ws, ws.nbytes, torch.cuda.current_stream().cuda_stream), what)
-    return Y
+    if stream is not None or index != torch._C._cuda_getDevice():
+        with _launch_on(device, stream):
+            return _run(name, before, between, out, shape, dtype, device, workspace, size, sizes, None, tuning)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+        at = out.data_ptr()
+    else:
+        at = _operand("out", out, shape, dtype, device)
+    if workspace is None:
+        workspace = new_workspace(size(*sizes), device)
+    last = (workspace.data_ptr(), workspace.nbytes, torch._C._cuda_getCurrentRawStream(index))
+    if tuning is None:
+        st = getattr(lib(), name)(*before, at, *between, *last)
+    else:
+        st = getattr(lib(), name + "_ex")(*before, at, *between, *last, ctypes.byref(tuning))
+    if st != CF_OK:
+        raise CfError(st, name)
+    return out
 
 
 def _act(act):
-    acts = {"none": CF_ACT_NONE, "gelu_tanh": CF_ACT_GELU_TANH}
-    if act not in acts:
+    a = _ACTS.get(act)
+    if a is None:
         raise ValueError(f"unknown activation {act!r}")
-    return acts[act]
+    return a
 
 
 def grouped_gemm(X, W, offsets, *, act="none", preact=None, out=None, workspace=None, stream=None, tuning=None):
     """Y[r] = act(X[r] @ W[e]) for the rows r in [offsets[e], offsets[e+1]); X [T, K] and W [E, K, N] bf16 or fp16
     CUDA tensors, offsets int32 [E + 1] on the same device.  `preact` ([T, N]) receives the unactivated product for
     grouped_gemm_dgrad.  Rows of no group are not written: in a new output they hold anything."""
-    import torch
-    dt, dev, dtype = _grouped_dtype("X", X), X.device, X.dtype
+    (T, K), dev, dtype, dt = _first("X", X, 2)
     a = _act(act)
-    T, K = _sizes("X", X, 2)
     E, _, N = _sizes("W", W, 3)
-    _operand("X", X, (T, K), dtype, dev)
-    _operand("W", W, (E, K, N), dtype, dev)
-    _operand("offsets", offsets, (E + 1,), torch.int32, dev)
-    if preact is not None:
-        _operand("preact", preact, (T, N), dtype, dev)
-    if out is not None:
-        _operand("out", out, (T, N), dtype, dev)
-    return _run("cf_grouped_gemm",
-                lambda Y, ws, n, s: cf_grouped_gemm(X, W, offsets, Y, preact, T, N, K, E, dt, a, ws, n, s, tuning),
-                dev, stream, out, (T, N), dtype, workspace, lambda: cf_grouped_gemm_workspace_size(T, N, K, E))
+    before = (X.data_ptr(), _operand("W", W, (E, K, N), dtype, dev),
+              _operand("offsets", offsets, (E + 1,), _int32(), dev))
+    between = (_operand("preact", preact, (T, N), dtype, dev), T, N, K, E, dt, a)
+    return _run("cf_grouped_gemm", before, between, out, (T, N), dtype, dev, workspace,
+                cf_grouped_gemm_workspace_size, (T, N, K, E), stream, tuning)
 
 
 def grouped_gemm_dgrad(dY, W, offsets, *, preact=None, out=None, workspace=None, stream=None, tuning=None):
     """dX[r] = (dY[r] @ W[e].T) * gelu_tanh'(preact[r]) for the rows of each group; dY [T, N], W [E, K, N],
     preact [T, K] or None (no activation before these rows).  out may be preact."""
-    import torch
-    dt, dev, dtype = _grouped_dtype("dY", dY), dY.device, dY.dtype
-    T, N = _sizes("dY", dY, 2)
+    (T, N), dev, dtype, dt = _first("dY", dY, 2)
     E, K, _ = _sizes("W", W, 3)
-    _operand("dY", dY, (T, N), dtype, dev)
-    _operand("W", W, (E, K, N), dtype, dev)
-    _operand("offsets", offsets, (E + 1,), torch.int32, dev)
-    if preact is not None:
-        _operand("preact", preact, (T, K), dtype, dev)
-    if out is not None:
-        _operand("out", out, (T, K), dtype, dev)
-    return _run("cf_grouped_gemm_dgrad",
-                lambda dX, ws, n, s: cf_grouped_gemm_dgrad(dY, W, offsets, preact, dX, T, N, K, E, dt, ws, n, s,
-                                                           tuning),
-                dev, stream, out, (T, K), dtype, workspace, lambda: cf_grouped_gemm_workspace_size(T, N, K, E))
+    before = (dY.data_ptr(), _operand("W", W, (E, K, N), dtype, dev),
+              _operand("offsets", offsets, (E + 1,), _int32(), dev),
+              _operand("preact", preact, (T, K), dtype, dev))
+    return _run("cf_grouped_gemm_dgrad", before, (T, N, K, E, dt), out, (T, K), dtype, dev, workspace,
+                cf_grouped_gemm_workspace_size, (T, N, K, E), stream, tuning)
 
 
 def grouped_gemm_wgrad(X, dY, offsets, *, out=None, workspace=None, stream=None, tuning=None):
     """dW[e] = X[rows of e].T @ dY[rows of e] (zeros for an empty group), [E, K, N]; X [T, K], dY [T, N]."""
-    import torch
-    dt, dev, dtype = _grouped_dtype("X", X), X.device, X.dtype
-    T, K = _sizes("X", X, 2)
+    (T, K), dev, dtype, dt = _first("X", X, 2)
     N = _sizes("dY", dY, 2)[1]
     E = _sizes("offsets", offsets, 1)[0] - 1
     if E < 0:
         raise ValueError("offsets is empty: it has one entry more than there are groups")
-    _operand("X", X, (T, K), dtype, dev)
-    _operand("dY", dY, (T, N), dtype, dev)
-    _operand("offsets", offsets, (E + 1,), torch.int32, dev)
-    if out is not None:
-        _operand("out", out, (E, K, N), dtype, dev)
-    return _run("cf_grouped_gemm_wgrad",
-                lambda dW, ws, n, s: cf_grouped_gemm_wgrad(X, dY, offsets, dW, T, N, K, E, dt, ws, n, s, tuning),
-                dev, stream, out, (E, K, N), dtype, workspace, lambda: cf_grouped_gemm_workspace_size(T, N, K, E))
+    before = (X.data_ptr(), _operand("dY", dY, (T, N), dtype, dev),
+              _operand("offsets", offsets, (E + 1,), _int32(), dev))
+    return _run("cf_grouped_gemm_wgrad", before, (T, N, K, E, dt), out, (E, K, N), dtype, dev, workspace,
+                cf_grouped_gemm_workspace_size, (T, N, K, E), stream, tuning)
 
 
 def gemm_lora(X, W, bias, A, B, offsets, adapters, *, scale=None, out=None, workspace=None, stream=None, tuning=None):
@@ -846,24 +852,14 @@ def gemm_lora(X, W, bias, A, B, offsets, adapters, *, scale=None, out=None, work
     [offsets[s], offsets[s+1]), with a = adapters[s] (-1: no adapter).  X [T, K], W [K, N], A [L, K, R], B [L, R, N]
     bf16 or fp16; bias fp32 [N] or None; offsets int32 [S + 1], adapters int32 [S], scale fp32 [L] or None (1)."""
     import torch
-    dt, dev, dtype = _grouped_dtype("X", X), X.device, X.dtype
-    T, K = _sizes("X", X, 2)
+    (T, K), dev, dtype, dt = _first("X", X, 2)
     N = _sizes("W", W, 2)[1]
     L, _, R = _sizes("A", A, 3)
     S = _sizes("adapters", adapters, 1)[0]
-    _operand("X", X, (T, K), dtype, dev)
-    _operand("W", W, (K, N), dtype, dev)
-    _operand("A", A, (L, K, R), dtype, dev)
-    _operand("B", B, (L, R, N), dtype, dev)
-    _operand("adapters", adapters, (S,), torch.int32, dev)
-    _operand("offsets", offsets, (S + 1,), torch.int32, dev)
-    if bias is not None:
-        _operand("bias", bias, (N,), torch.float32, dev)
-    if scale is not None:
-        _operand("scale", scale, (L,), torch.float32, dev)
-    if out is not None:
-        _operand("out", out, (T, N), dtype, dev)
-    return _run("cf_gemm_lora",
-                lambda Y, ws, n, s: cf_gemm_lora(X, W, bias, A, B, offsets, adapters, scale, Y, T, N, K, S, L, R, dt,
-                                                 ws, n, s, tuning),
-                dev, stream, out, (T, N), dtype, workspace, lambda: cf_gemm_lora_workspace_size(T, N, K, S, R))
+    before = (X.data_ptr(), _operand("W", W, (K, N), dtype, dev), _operand("bias", bias, (N,), torch.float32, dev),
+              _operand("A", A, (L, K, R), dtype, dev), _operand("B", B, (L, R, N), dtype, dev),
+              _operand("offsets", offsets, (S + 1,), torch.int32, dev),
+              _operand("adapters", adapters, (S,), torch.int32, dev),
+              _operand("scale", scale, (L,), torch.float32, dev))
+    return _run("cf_gemm_lora", before, (T, N, K, S, L, R, dt), out, (T, N), dtype, dev, workspace,
+                cf_gemm_lora_workspace_size, (T, N, K, S, R), stream, tuning)
