@@ -40,10 +40,11 @@
 //              16 blocks in pieces 1, joining them 1.5)
 //     DGRAD    16384 rows, 16 groups of 4096 x 2048, GELU': the tensor pipe, 169 to 181 us (1.52 to 1.63 PFLOP/s);
 //              333 rows, 12 groups of 520 x 1032: latency, 7.4 us
-//     WGRAD    16384 rows, 8 groups of 2048 x 8192: the tensor pipe, 325 to 343 us (1.60 to 1.69 PFLOP/s); 1003 rows,
-//              24 groups of 520 x 1032: its 600 epilogues of 256 columns, 16.3 us (1.8 TB/s)
-//     LORA     with its SHRINK, 8192 rows of 8 requests, 4096 x 4096, rank 64: the tensor pipe, 167 to 171 us (1.65 to
-//              1.68 PFLOP/s); one row, rank 16: 13.3 us, 64 requests of one row: 22.5 us (the chain X . A, join, H . B,
+//     WGRAD    16384 rows, 8 groups of 2048 x 8192: the tensor pipe, 318 to 343 us (1.60 to 1.73 PFLOP/s); 1003 rows,
+//              24 groups of 520 x 1032: its 600 epilogues of 256 columns, 13.8 us (2.1 TB/s; 16.2 with 32 columns at a
+//              time out of the accumulator)
+//     LORA     with its SHRINK, 8192 rows of 8 requests, 4096 x 4096, rank 64: the tensor pipe, 160 to 168 us (1.67 to
+//              1.75 PFLOP/s); one row, rank 16: 13.3 us, 64 requests of one row: 22.5 us (the chain X . A, join, H . B,
 //              join beside 33 MB of W); 1537 rows of 40 requests, 2048 x 2056, rank 24: 43 us (the chain, then row
 //              tiles that requests do not fill)
 #include <cuda.h>
@@ -125,6 +126,15 @@ __device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, uint32_t (&v)[32]
             : "r"(taddr + (uint32_t(16 * h) << 16))
             : "memory");
 }
+// the wait for loads into v, which is theirs until then
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                   "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                   "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                   "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
+}
 // four 8 x 8 blocks of 16-bit numbers to and from shared memory, transposed: thread t holds row t / 4, columns
 // 2 (t % 4) and the next of each block; thread 8m + j gives the 16 bytes that are column j of block m
 __device__ __forceinline__ void stmatrix4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -162,12 +172,9 @@ __device__ __forceinline__ uint32_t idesc_f16(int m, int n, bool fp16, bool a_mn
 // with its short requests.
 __host__ __device__ constexpr int epi_warps(int kind) { return kind == GR_SHRINK ? 4 : 8; }
 __host__ __device__ constexpr int threads_of(int kind) { return kind == GR_SHRINK ? 256 : 320; }
-// Ten warps are three on a quarter of the SM: 168 registers each.  (WGRAD takes 134 of what it is offered; offered 168
-// it was scheduled to take 124 and 1003 rows over 24 groups took 18.1 us, not 16.3.  Fewer, so that a CTA of LORA fits
-// beside one of SHRINK, gained nothing: 64 requests 22.4 us, 21.8 without.)
-__host__ __device__ constexpr int registers_of(int kind) {
-    return kind == GR_SHRINK ? 128 : kind == GR_WGRAD ? 200 : 168;
-}
+// Ten warps are three on a quarter of the SM: 168 registers each.  (Fewer, so that a CTA of LORA fits beside one of
+// SHRINK, gained nothing: 64 requests 22.4 us, 21.8 without.)
+__host__ __device__ constexpr int registers_of(int kind) { return kind == GR_SHRINK ? 128 : 168; }
 constexpr int kShortWarps = 6;
 constexpr int kBK = 64;         // contraction per stage (128 bytes: one swizzle atom)
 constexpr int kFB = 128;        // features per tile (accumulator lanes)
@@ -587,26 +594,24 @@ struct Fragment {
     }
 };
 
-// WGRAD: 32 columns of this lane's row of dW.  Rows go out in whole 128 bytes: the first call of a 64-column block
-// (c % 64 == 0) leaves its half in the warp's 4 KB of shared memory, the second sends both (pieces of 16 bytes, at
-// piece ^ row % 8 so that neither side of the turn meets bank conflicts).
-__device__ __forceinline__ void store_columns(const uint32_t (&v)[32], const GroupedArgs &a, const Tile &w, int c,
-                                              uint4 *stg, int q, int lane, bool ok) {
-    const bool fp16 = a.fp16 != 0;
-    const int hi = (c & 32) / 8;  // pieces 0..3 or 4..7 of the block
+// WGRAD: 32 of a 64-column block's columns of this lane's row of dW into the warp's 4 KB of shared memory (16-byte pieces
+// at piece ^ row % 8, so that neither side of the turn meets bank conflicts): the first (hi 0) or the second (4) half
+template <bool kFp16>
+__device__ __forceinline__ void put_columns(const uint32_t (&v)[32], uint4 *stg, int hi, int lane) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         uint32_t p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // an empty group's sum is zero
-            p[i] = w.nk == 0 ? 0u
-                             : pack16(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]), fp16);
+        for (int i = 0; i < 4; ++i)
+            p[i] = pack_pair<kFp16>(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]));
         stg[lane * 8 + ((hi + j) ^ (lane & 7))] = make_uint4(p[0], p[1], p[2], p[3]);
     }
-    if (hi == 0 && c + 32 < w.n) return;
+}
+// ... and the block's rows out of it, 128 bytes each
+__device__ __forceinline__ void store_columns(const GroupedArgs &a, const Tile &w, int c0, const uint4 *stg, int q,
+                                              int lane, bool ok) {
     __syncwarp();
-    const int c0 = c & ~63, piece = lane & 7;
-    const int f0 = w.f0 + q * 32 + (lane >> 3);
+    const int piece = lane & 7, f0 = w.f0 + q * 32 + (lane >> 3);
     uint16_t *y = static_cast<uint16_t *>(a.out) + (size_t(w.g) * a.F + f0) * a.N + w.col0 + c0 + piece * 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -1677,22 +1682,39 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                 for (int b = 0; b < 4; ++b)
                     if (a.bias && fb + 8 * b < a.F) bias[b] = __ldcg(a.bias + fb + 8 * b);
             }
-            // (WGRAD: the halves take alternate 64-column blocks)
-            for (int c = half * kSpan; KIND != GR_SHRINK && c < w.n; c = next_fragment<kSpan, kHalves>(c)) {
+            if constexpr (KIND == GR_WGRAD) {  // the halves take alternate 64-column blocks
+                uint4 *const stg = reinterpret_cast<uint4 *>(smem_raw + L.stg + e * 4096);
+                for (int c = half * 64; c < w.n; c += 128) {
+                    uint32_t v[2][32];
+                    const int two = c + 32 < w.n ? 2 : 1;
+                    if (kPair || w.whole()) {
+                        ptx::tmem_ld32(tacc + uint32_t(c), v[0]);
+                        if (two == 2) ptx::tmem_ld32(tacc + uint32_t(c + 32), v[1]);
+                        ptx::tmem_ld_wait(v[0]);
+                        ptx::tmem_ld_wait(v[1]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (h >= two) break;
+                        if (!kPair && !w.whole()) sum_pieces(v[h], pieces_of(a, walk, w), c + 32 * h, w.n, q * 32 + lane);
+                        if (w.nk == 0) {  // an empty group's sum is zero
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[h][j] = 0u;
+                        }
+                        if (fp16) put_columns<true>(v[h], stg, 4 * h, lane);
+                        else put_columns<false>(v[h], stg, 4 * h, lane);
+                    }
+                    store_columns(a, w, c, stg, q, lane, ok);
+                }
+            }
+            constexpr bool kFragments = KIND == GR_FORWARD || KIND == GR_DGRAD || KIND == GR_LORA;
+            for (int c = half * 32; kFragments && c < w.n; c += 64) {
                 uint32_t v[32];
                 const int cols = min(32, w.n - c);
-                if constexpr (KIND == GR_WGRAD) {
-                    if (kPair || w.whole()) {
-                        ptx::tmem_ld32(tacc + uint32_t(c), v);
-                        ptx::tmem_ld_wait();
-                    } else {
-                        sum_pieces(v, pieces_of(a, walk, w), c, w.n, q * 32 + lane);
-                    }
-                    store_columns(v, a, w, c, reinterpret_cast<uint4 *>(smem_raw + L.stg + e * 4096), q, lane, ok);
-                } else if (KIND == GR_LORA && parts > 0 && c + 32 > w.nx) {
+                if (KIND == GR_LORA && parts > 0 && c + 32 > w.nx) {
                     // rows with adapters of their own
                     ptx::tmem_ld32(tacc + uint32_t(c), v);
-                    ptx::tmem_ld_wait();
+                    ptx::tmem_ld_wait(v);
                     float *const stg = reinterpret_cast<float *>(smem_raw + L.stg) + e * 1024;
                     turn(v, stg, lane);
                     const int f8 = w.f0 + q * 32 + (lane & 3) * 8;
@@ -1723,7 +1745,7 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                     __syncwarp();
                 } else {
                     ptx::tmem_ld_blocks(tacc + uint32_t(c), v);
-                    ptx::tmem_ld_wait();
+                    ptx::tmem_ld_wait(v);
                     constexpr uint32_t kStg = KIND == GR_LORA ? 4096u : 2048u;
                     const Fragment fr{smem_raw + L.stg + e * kStg, lane, cols,
                                       (w.f0 + q * 32 + (lane & 3) * 8) < a.F && ok,
