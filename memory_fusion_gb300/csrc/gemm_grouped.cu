@@ -969,34 +969,40 @@ __device__ __forceinline__ void finish_pieces(const GroupedArgs &a, const Tile &
 // its own adapter's B and nothing of another's, so a NaN in an adapter stays with its requests.
 // x: this lane's 8 features (from f on) of one row; four lanes cover a row's 32 features, eight rows go side by side
 // with an adapter each, and lanes of one adapter read the same addresses.
+template <int kRanks>
+__device__ __forceinline__ void low_rank_step(float (&x)[8], const uint16_t *b, const uint16_t *h, int rank, int step,
+                                              bool fp16) {
+    uint4 bv[kRanks], up[kRanks / 8], rest[kRanks / 8];
+#pragma unroll
+    for (int k = 0; k < kRanks; ++k) bv[k] = __ldg(reinterpret_cast<const uint4 *>(b + size_t(k) * step));
+#pragma unroll
+    for (int g = 0; g < kRanks / 8; ++g) {
+        up[g] = __ldcg(reinterpret_cast<const uint4 *>(h + 8 * g));
+        rest[g] = __ldcg(reinterpret_cast<const uint4 *>(h + rank + 8 * g));
+    }
+#pragma unroll
+    for (int k = 0; k < kRanks; ++k) {
+        const uint4 u = up[k / 8], l = rest[k / 8];
+        const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, lw[4] = {l.x, l.y, l.z, l.w};
+        const float hk = from16(uint16_t(uw[k % 8 / 2] >> ((k & 1) * 16)), fp16) +
+                         from16(uint16_t(lw[k % 8 / 2] >> ((k & 1) * 16)), fp16);
+        const uint32_t w[4] = {bv[k].x, bv[k].y, bv[k].z, bv[k].w};
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+            ptx::fma2(x[2 * p], x[2 * p + 1], hk, hk, from16(uint16_t(w[p]), fp16),
+                      from16(uint16_t(w[p] >> 16), fp16), x[2 * p], x[2 * p + 1]);
+    }
+}
 __device__ __forceinline__ void add_low_rank(float (&x)[8], const GroupedArgs &a, int ad, int row, int f) {
     if (ad < 0) return;
     const int rank = a.rank;
     const bool fp16 = a.fp16 != 0;
     const uint16_t *b = static_cast<const uint16_t *>(a.lora_b) + size_t(ad) * rank * a.F + f;
     const uint16_t *h = static_cast<const uint16_t *>(a.low) + size_t(row) * (2 * rank);
+    int r = 0;
 #pragma unroll 1
-    for (int r = 0; r < rank; r += 8) {
-        uint4 bv[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) bv[k] = __ldg(reinterpret_cast<const uint4 *>(b + size_t(r + k) * a.F));
-        float hk[8];
-        const uint4 up = __ldcg(reinterpret_cast<const uint4 *>(h + r));
-        const uint4 rest = __ldcg(reinterpret_cast<const uint4 *>(h + rank + r));
-        const uint32_t uw[4] = {up.x, up.y, up.z, up.w}, lw[4] = {rest.x, rest.y, rest.z, rest.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            hk[k] = from16(uint16_t(uw[k / 2] >> ((k & 1) * 16)), fp16) +
-                    from16(uint16_t(lw[k / 2] >> ((k & 1) * 16)), fp16);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t w[4] = {bv[k].x, bv[k].y, bv[k].z, bv[k].w};
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-                ptx::fma2(x[2 * p], x[2 * p + 1], hk[k], hk[k], from16(uint16_t(w[p]), fp16),
-                          from16(uint16_t(w[p] >> 16), fp16), x[2 * p], x[2 * p + 1]);
-        }
-    }
+    for (; r + 16 <= rank; r += 16) low_rank_step<16>(x, b + size_t(r) * a.F, h + r, rank, a.F, fp16);
+    if (r < rank) low_rank_step<8>(x, b + size_t(r) * a.F, h + r, rank, a.F, fp16);
 }
 
 // One lane's share of a short request: rows of A (8 ranks, a 16-byte piece) `step` apart, `left` rows until the end,
