@@ -902,7 +902,7 @@ __device__ __forceinline__ void finish_row(const GroupedArgs &a, const Tile &w, 
         for (int i = 0; i < 4; ++i) s[i] *= gelu_slope(from16(uint16_t(zw[i / 2] >> ((i & 1) * 16)), fp16));
     }
     if (KIND == GR_LORA && a.bias) {
-        const float4 b = __ldcg(reinterpret_cast<const float4 *>(a.bias + f));
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(a.bias + f));
         s[0] += b.x, s[1] += b.y, s[2] += b.z, s[3] += b.w;
     }
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
@@ -1000,9 +1000,12 @@ __device__ __forceinline__ void add_low_rank(float (&x)[8], const GroupedArgs &a
     const uint16_t *b = static_cast<const uint16_t *>(a.lora_b) + size_t(ad) * rank * a.F + f;
     const uint16_t *h = static_cast<const uint16_t *>(a.low) + size_t(row) * (2 * rank);
     int r = 0;
+    if (rank >= 32) {
 #pragma unroll 1
-    for (; r + 16 <= rank; r += 16) low_rank_step<16>(x, b + size_t(r) * a.F, h + r, rank, a.F, fp16);
-    if (r < rank) low_rank_step<8>(x, b + size_t(r) * a.F, h + r, rank, a.F, fp16);
+        for (; r + 16 <= rank; r += 16) low_rank_step<16>(x, b + size_t(r) * a.F, h + r, rank, a.F, fp16);
+    }
+#pragma unroll 1
+    for (; r < rank; r += 8) low_rank_step<8>(x, b + size_t(r) * a.F, h + r, rank, a.F, fp16);
 }
 
 // One lane's share of a short request: rows of A (8 ranks, a 16-byte piece) `step` apart, `left` rows until the end,
@@ -1603,6 +1606,7 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
             }
             const bool ok = ptx::mbar_wait_bounded(B.tmem_full0 + 8 * buf, tph, tmo, abort, a.err, kInfoEpi | buf);
             ptx::tc_fence_after();
+            if constexpr (KIND == GR_LORA) ptx::griddep_wait();  // the bias is read through L1
             const uint32_t tacc = tmem_base + (uint32_t(q * 32) << 16) + buf * uint32_t(a.bn);
             const int f = w.f0 + q * 32 + lane;
             const bool live = f < a.F && ok;
@@ -1686,7 +1690,7 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                 const int fb = w.f0 + q * 32 + (lane >> 2);
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
-                    if (a.bias && fb + 8 * b < a.F) bias[b] = __ldcg(a.bias + fb + 8 * b);
+                    if (a.bias && fb + 8 * b < a.F) bias[b] = __ldg(a.bias + fb + 8 * b);
             }
             if constexpr (KIND == GR_WGRAD) {  // the halves take alternate 64-column blocks
                 uint4 *const stg = reinterpret_cast<uint4 *>(smem_raw + L.stg + e * 4096);
@@ -1738,8 +1742,8 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                             add_low_rank(x, a, tab.ad[request_of(tab, a.groups, row)], row, f8);
                         }
                         if (a.bias) {
-                            const float4 b0 = __ldcg(reinterpret_cast<const float4 *>(a.bias + f8));
-                            const float4 b1 = __ldcg(reinterpret_cast<const float4 *>(a.bias + f8) + 1);
+                            const float4 b0 = __ldg(reinterpret_cast<const float4 *>(a.bias + f8));
+                            const float4 b1 = __ldg(reinterpret_cast<const float4 *>(a.bias + f8) + 1);
                             x[0] += b0.x, x[1] += b0.y, x[2] += b0.z, x[3] += b0.w;
                             x[4] += b1.x, x[5] += b1.y, x[6] += b1.z, x[7] += b1.w;
                         }
