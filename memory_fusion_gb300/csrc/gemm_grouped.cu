@@ -911,7 +911,41 @@ __device__ __forceinline__ void finish_row(const GroupedArgs &a, const Tile &w, 
 
 // The pieces of a divided tile added in worker order and finished (all kinds but WGRAD).  A warp takes whole columns,
 // that is rows of the batch: a lane 4 neighbouring features, so the loads are 512 bytes a warp and the stores whole
-// rows, and nothing needs turning.  Four columns of four pieces are in flight.
+// rows, and nothing needs turning.  kCols columns of four pieces are in flight.
+template <int KIND, int kCols>
+__device__ __forceinline__ void finish_columns(const GroupedArgs &a, const Tile &w, const Pieces &pc, int e, int lane) {
+    constexpr int kWarps = epi_warps(KIND), kFly = 4;
+    const int f = w.f0 + 4 * lane;
+    if (f >= a.F) return;
+#pragma unroll 1
+    for (int j = e; j < w.n; j += kCols * kWarps) {
+        const size_t at = size_t(j) * kFB + 4 * lane;
+        float4 s[kCols];
+#pragma unroll
+        for (int h = 0; h < kCols; ++h) s[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int k = 0; k <= pc.more; k += kFly) {
+            float4 x[kFly][kCols];
+#pragma unroll
+            for (int i = 0; i < kFly; ++i) {
+                const float *p = (k + i == 0 ? pc.p0 : pc.p + (k + i - 1) * pc.step) + at;
+#pragma unroll
+                for (int h = 0; h < kCols; ++h)
+                    x[i][h] = k + i <= pc.more && j + h * kWarps < w.n
+                                  ? __ldcg(reinterpret_cast<const float4 *>(p + h * kWarps * kFB))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < kFly; ++i)
+#pragma unroll
+                for (int h = 0; h < kCols; ++h)
+                    s[h].x += x[i][h].x, s[h].y += x[i][h].y, s[h].z += x[i][h].z, s[h].w += x[i][h].w;
+        }
+#pragma unroll
+        for (int h = 0; h < kCols; ++h)
+            if (j + h * kWarps < w.n) finish_row<KIND>(a, w, w.col0 + j + h * kWarps, f, s[h]);
+    }
+}
 template <int KIND>
 __device__ __forceinline__ void finish_pieces(const GroupedArgs &a, const Tile &w, const Pieces &pc, int e, int lane) {
     if constexpr (KIND == GR_SHRINK) {  // few features: lanes go over rows and features alike
@@ -934,35 +968,9 @@ __device__ __forceinline__ void finish_pieces(const GroupedArgs &a, const Tile &
         }
         return;
     }
-    constexpr int kWarps = epi_warps(KIND), kFly = 4, kCols = 4;
-    const int f = w.f0 + 4 * lane;
-    if (f >= a.F) return;
-    for (int j = e; j < w.n; j += kCols * kWarps) {
-        const size_t at = size_t(j) * kFB + 4 * lane;
-        float4 s[kCols];
-#pragma unroll
-        for (int h = 0; h < kCols; ++h) s[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k <= pc.more; k += kFly) {
-            float4 x[kFly][kCols];
-#pragma unroll
-            for (int i = 0; i < kFly; ++i) {
-                const float *p = (k + i == 0 ? pc.p0 : pc.p + (k + i - 1) * pc.step) + at;
-#pragma unroll
-                for (int h = 0; h < kCols; ++h)
-                    x[i][h] = k + i <= pc.more && j + h * kWarps < w.n
-                                  ? __ldcg(reinterpret_cast<const float4 *>(p + h * kWarps * kFB))
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll
-            for (int i = 0; i < kFly; ++i)
-#pragma unroll
-                for (int h = 0; h < kCols; ++h)
-                    s[h].x += x[i][h].x, s[h].y += x[i][h].y, s[h].z += x[i][h].z, s[h].w += x[i][h].w;
-        }
-#pragma unroll
-        for (int h = 0; h < kCols; ++h)
-            if (j + h * kWarps < w.n) finish_row<KIND>(a, w, w.col0 + j + h * kWarps, f, s[h]);
-    }
+    // (as few columns as there are: code that is run once or twice is mostly fetched)
+    if (w.n <= epi_warps(KIND)) finish_columns<KIND, 1>(a, w, pc, e, lane);
+    else finish_columns<KIND, 4>(a, w, pc, e, lane);
 }
 
 // LORA, a tile with rows of several requests: the adapters' second product on the CUDA cores, in fp32.  Each row takes
