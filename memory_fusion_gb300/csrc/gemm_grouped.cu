@@ -751,55 +751,64 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
         ngroups = a.groups;
     }
     if constexpr (KIND == GR_WGRAD) longest = __reduce_max_sync(kAll, longest);
-    if (lane == 0) {
-        tab.pre[0] = 0;
-        const int rows_all = lo_all - first;
-        // Rounds of whole tiles against equal stretches, in blocks; what adding pieces costs is in the host's plan
-        // (grouped_cycles), which chose the tiles.
-        constexpr int kMost = 1 << 20;  // blocks of a contraction, tiles x blocks then fit 30 bits
-        const int per_tile = KIND == GR_WGRAD ? ft * ((a.N + a.bn - 1) >> shift) : 1;
-        const int nkc = (a.C + kBK - 1) / kBK;
-        Plan p;
-        p.split = 0;
-        p.workers = workers;
-        p.tiles = KIND == GR_WGRAD ? ngroups * per_tile : carry;
-        p.units = p.ways = p.base = p.rem = 0;
-        p.groups = ngroups;
-        const bool few = KIND == GR_WGRAD ? ngroups <= kGroupedSplitTiles && per_tile <= kGroupedSplitTiles &&
-                                                p.tiles <= kGroupedSplitTiles && carry <= kMost
-                                          : carry <= kGroupedSplitTiles && nkc <= kMost;
-        if (!kPair && a.partials != nullptr && few && p.tiles > 0) {
-            const int units = KIND == GR_WGRAD ? per_tile * carry : p.tiles * nkc;
-            const int share = (units + workers - 1) / workers;
-            const int stretch = max(share, kMinStretch);
-            const int rounds = (p.tiles + workers - 1) / workers;
-            // WGRAD: of mean tiles, or the longest one
-            const int mean = KIND == GR_WGRAD ? (units + p.tiles - 1) / p.tiles : nkc;
-            const int whole0 = max(rounds * mean, longest);
-            // Equal parts of every tile, where there are workers for two at least: a worker then has one piece, not
-            // the end of one tile and the start of another, each of which costs what adding a piece costs.
-            const int most = KIND == GR_WGRAD ? 0 : min(workers / p.tiles, nkc / kMinStretch);
-            const int n = min(a.bn, (rows_all + ngroups - 1) / ngroups + 15);  // columns of a tile, about
-            const int cols = KIND == GR_WGRAD ? a.bn : n;
-            const int block = max(max(47 * cols / 20, 290), a.copy_cycles);
-            const int adding = (1500 + 70 * cols) / block + 1;
-            const int least = a.wait_cycles / block;  // no tile can be finished before
-            const int whole = max(whole0, least);
-            const int even = most >= 2 ? max((nkc + most - 1) / most, least) + adding : 1 << 30;
-            const int mixed = max(stretch, least) + adding + adding / 2;
-            if (whole > min(even, mixed)) {
-                p.split = 1;
-                p.units = units;
-                if (even <= mixed) {
-                    p.ways = most;
-                    p.workers = p.tiles * most;
-                } else {
-                    p.workers = stretch == share ? workers : max(units / stretch, 1);
-                    p.base = units / p.workers;
-                    p.rem = units - p.base * p.workers;
-                }
+    // Rounds of whole tiles against equal stretches, in blocks; what adding pieces costs is in the host's plan
+    // (grouped_cycles), which chose the tiles.  Every lane decides alike; divisions that do not need one another are
+    // worked out side by side, a lane each (in a row they took 600 cycles of a launch of 10000).
+    const int rows_all = lo_all - first;
+    constexpr int kMost = 1 << 20;  // blocks of a contraction, tiles x blocks then fit 30 bits
+    const int per_tile = KIND == GR_WGRAD ? ft * ((a.N + a.bn - 1) >> shift) : 1;
+    const int nkc = (a.C + kBK - 1) / kBK;
+    Plan p;
+    p.split = 0;
+    p.workers = workers;
+    p.tiles = KIND == GR_WGRAD ? ngroups * per_tile : carry;
+    p.units = p.ways = p.base = p.rem = 0;
+    p.groups = ngroups;
+    const bool few = KIND == GR_WGRAD ? ngroups <= kGroupedSplitTiles && per_tile <= kGroupedSplitTiles &&
+                                            p.tiles <= kGroupedSplitTiles && carry <= kMost
+                                      : carry <= kGroupedSplitTiles && nkc <= kMost;
+    if (!kPair && a.partials != nullptr && few && p.tiles > 0) {
+        auto divide = [&](int n0, int d0, int n1, int d1, int n2, int d2, int n3, int d3) {
+            const int n = lane == 0 ? n0 : lane == 1 ? n1 : lane == 2 ? n2 : n3;
+            const int d = lane == 0 ? d0 : lane == 1 ? d1 : lane == 2 ? d2 : d3;
+            const int q = n / d;
+            return make_int4(__shfl_sync(kAll, q, 0), __shfl_sync(kAll, q, 1), __shfl_sync(kAll, q, 2),
+                             __shfl_sync(kAll, q, 3));
+        };
+        const int units = KIND == GR_WGRAD ? per_tile * carry : p.tiles * nkc;
+        const int4 of = divide(units + workers - 1, workers, p.tiles + workers - 1, workers,
+                               KIND == GR_WGRAD ? units + p.tiles - 1 : workers, p.tiles, rows_all + ngroups - 1,
+                               ngroups);
+        const int share = of.x, rounds = of.y;
+        const int stretch = max(share, kMinStretch);
+        // WGRAD: of mean tiles, or the longest one
+        const int whole0 = max(rounds * (KIND == GR_WGRAD ? of.z : nkc), longest);
+        // Equal parts of every tile, where there are workers for two at least: a worker then has one piece, not the
+        // end of one tile and the start of another, each of which costs what adding a piece costs.
+        const int most = KIND == GR_WGRAD ? 0 : min(of.z, nkc / kMinStretch);
+        const int cols = KIND == GR_WGRAD ? a.bn : min(a.bn, of.w + 15);  // columns of a tile, about
+        const int block = max(max(47 * cols / 20, 290), a.copy_cycles);
+        const int4 in = divide(1500 + 70 * cols, block, a.wait_cycles, block, nkc + most - 1, max(most, 1), units,
+                               stretch);
+        const int adding = in.x + 1, least = in.y;  // no tile can be finished before
+        const int whole = max(whole0, least);
+        const int even = most >= 2 ? max(in.z, least) + adding : 1 << 30;
+        const int mixed = max(stretch, least) + adding + adding / 2;
+        if (whole > min(even, mixed)) {
+            p.split = 1;
+            p.units = units;
+            if (even <= mixed) {
+                p.ways = most;
+                p.workers = p.tiles * most;
+            } else {
+                p.workers = stretch == share ? workers : max(in.w, 1);
+                p.base = units / p.workers;
+                p.rem = units - p.base * p.workers;
             }
         }
+    }
+    if (lane == 0) {
+        tab.pre[0] = 0;
         *tab.plan = p;
     }
     if (__any_sync(kAll, bad) && lane == 0 && blockIdx.x == 0)
