@@ -36,7 +36,7 @@
 // What bounds each form, and what it measured on a GB300 (in a CUDA graph):
 //     FORWARD  16384 rows, 8 groups of 2048 x 8192, GELU: the tensor pipe, 308 to 320 us (1.72 to 1.78 PFLOP/s);
 //              250 rows, 32 groups of 2048 x 4096: HBM, 72 us (6.6 TB/s); 4099 rows, 64 groups of 1000 x 2056: HBM,
-//              47 us (5.4 TB/s); 2 rows, 8 groups of 1024 x 2048: latency, 7.4 us (launch 2, table 1.5, first copy 1,
+//              47 us (5.4 TB/s); 2 rows, 8 groups of 1024 x 2048: latency, 6.8 us (launch 2, table 1.2, first copy 1,
 //              16 blocks in pieces 1, joining them 1.5)
 //     DGRAD    16384 rows, 16 groups of 4096 x 2048, GELU': the tensor pipe, 169 to 181 us (1.52 to 1.63 PFLOP/s);
 //              333 rows, 12 groups of 520 x 1032: latency, 7.4 us
@@ -44,7 +44,7 @@
 //              24 groups of 520 x 1032: its 600 epilogues of 256 columns, 13.8 us (2.1 TB/s; 16.2 with 32 columns at a
 //              time out of the accumulator)
 //     LORA     with its SHRINK, 8192 rows of 8 requests, 4096 x 4096, rank 64: the tensor pipe, 160 to 168 us (1.67 to
-//              1.75 PFLOP/s); one row, rank 16: 13.3 us, 64 requests of one row: 22.5 us (the chain X . A, join, H . B,
+//              1.75 PFLOP/s); one row, rank 16: 13.0 us, 64 requests of one row: 22.5 us (the chain X . A, join, H . B,
 //              join beside 33 MB of W); 1537 rows of 40 requests, 2048 x 2056, rank 24: 43 us (the chain, then row
 //              tiles that requests do not fill)
 #include <cuda.h>
