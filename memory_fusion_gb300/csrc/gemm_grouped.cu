@@ -975,17 +975,17 @@ __device__ __forceinline__ void finish_pieces(const GroupedArgs &a, const Tile &
             }
             finish_row<KIND>(a, w, w.col0 + j, f, s);
         }
-        return;
+    } else {  // (as few columns at a time as there are: code that is run once or twice is mostly fetched)
+        if (w.n <= epi_warps(KIND)) finish_columns<KIND, 1>(a, w, pc, e, lane);
+        else finish_columns<KIND, 4>(a, w, pc, e, lane);
     }
-    // (as few columns as there are: code that is run once or twice is mostly fetched)
-    if (w.n <= epi_warps(KIND)) finish_columns<KIND, 1>(a, w, pc, e, lane);
-    else finish_columns<KIND, 4>(a, w, pc, e, lane);
 }
 
 // LORA, a tile with rows of several requests: the adapters' second product on the CUDA cores, in fp32.  Each row takes
 // its own adapter's B and nothing of another's, so a NaN in an adapter stays with its requests.
 // x: this lane's 8 features (from f on) of one row; four lanes cover a row's 32 features, eight rows go side by side
-// with an adapter each, and lanes of one adapter read the same addresses.
+// with an adapter each, and lanes of one adapter read the same addresses.  L2's latency bounds it, 1000 cycles for 8
+// ranks; from rank 32 on 16 are in flight (13434 rows of 27 requests at rank 64: 67 us, now 58).
 template <int kRanks>
 __device__ __forceinline__ void low_rank_step(float (&x)[8], const uint16_t *b, const uint16_t *h, int rank, int step,
                                               bool fp16) {
