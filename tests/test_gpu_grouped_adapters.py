@@ -164,3 +164,20 @@ def test_workspace_of_another_kind_is_refused():
             cf.grouped_gemm(X, W, _i32([0, 4, 8]), workspace=ws)
         with pytest.raises(ValueError, match="workspace"):
             cf.grouped_gemm(X, W, _i32([0, 4, 8]), workspace=ws, stream=torch.cuda.Stream())
+
+
+@pytest.mark.parametrize("sizes", [[1, 1, 2], [40, 3, 200]])
+def test_a_wait_that_runs_out_is_reported(sizes):
+    """Both launches wait for an arrival that nobody makes: their roles drain, the status is a timeout, and after the
+    workspace is zeroed the next call on it is right."""
+    torch = torch_cuda()
+    c = _lora_case((sizes, 0, 0, 264, 136, 2, 16, [i % 2 for i in range(len(sizes))]), "bf16", seed=80)
+    args = (_dev(c["X"], "bf16"), _dev(c["W"], "bf16"), None, _dev(c["A"], "bf16"), _dev(c["B"], "bf16"),
+            _i32(c["off"]), _i32(c["ad"]))
+    n = cf.cf_gemm_lora_workspace_size(c["T"], c["N"], c["K"], len(sizes), c["R"])
+    ws = cf.new_workspace(n)
+    cf.gemm_lora(*args, workspace=ws, tuning=cf.tuning(extra_arrivals=1, timeout_us=2000))
+    assert cf.cf_get_device_status(ws)[0] == cf.CF_ERR_DEVICE_TIMEOUT
+    cf.cf_workspace_init(ws, n)
+    assert torch.equal(cf.gemm_lora(*args, workspace=ws), cf.gemm_lora(*args))
+    _status(ws)
