@@ -255,7 +255,7 @@ struct Tile {
     int extra;  // LORA: blocks of the low-rank product behind the tile's own (pieces: with the last)
     int ad;     // LORA: the adapter of the first nx columns' rows, -1 none
     int nx;     // LORA: columns whose low-rank product runs on the tensor cores: all of the tile (nm), or a long
-                // request's in whole 16s
+                // request's in whole steps of the MMA's columns
     bool mixed; // LORA: the columns behind them are of several requests
     int first, last;  // workers that hold pieces of the tile
     int slot;   // which of its two workspace slots this worker's piece goes to
@@ -347,8 +347,7 @@ struct Walk {
         }
     }
     static constexpr int kTileF = kPair ? 2 * kFB : kFB;
-    // columns are multiplied in 16s; each half of a pair's in 16s (WGRAD: whole 64-column blocks)
-    static constexpr int kGran = kPair ? (KIND == GR_WGRAD ? 128 : 32) : 16;
+    static constexpr int kGran = grouped_column_step(KIND, kPair);
     __device__ int unit_of(int w) const { return w * plan.base + min(w, plan.rem); }
     __device__ int worker_of(int u) const {
         const int wide = plan.rem * (plan.base + 1);
@@ -434,7 +433,7 @@ struct Walk {
             } else {  // requests in a row may share an adapter
                 const int s0 = request_of(tab, a.groups, r.col0), s1 = request_of(tab, a.groups, r.col0 + r.n - 1);
                 r.mixed = tab.turn[s0] != tab.turn[s1];
-                r.nx = r.mixed ? own & ~15 : r.nm;
+                r.nx = r.mixed ? lora_tensor_columns(own, kPair) : r.nm;
                 if (r.nx > 0) r.ad = tab.ad[s0];
             }
         }

@@ -25,6 +25,17 @@ constexpr int kLoraShortRows = 4;        // rows up to which a request's X . A r
 constexpr int kLoraMaxSplit = 8;         // parts of their contraction
 constexpr int kLoraMaxRank = 128;        // one tile of features in the first product
 
+// Columns that an MMA multiplies come in steps: 16 for one CTA (M = 128), 32 for a pair (M = 256 over two CTAs), each of
+// which stages half of them.  (WGRAD pairs: whole 64-column blocks in either CTA.)
+__host__ __device__ constexpr int grouped_column_step(int kind, bool pair) {
+    return pair ? (kind == GR_WGRAD ? 128 : 32) : 16;
+}
+// LORA, a tile of several requests: of the `own` rows at its start that are one long request's, those whose low-rank
+// product runs on the tensor cores, in whole steps; the rest of them go with the other rows
+__host__ __device__ constexpr int lora_tensor_columns(int own, bool pair) {
+    return own & ~(grouped_column_step(GR_LORA, pair) - 1);
+}
+
 struct GroupedArgs {
     CUtensorMap tmap_a;    // the operand whose features become accumulator lanes: W (WGRAD: X)
     CUtensorMap tmap_b;    // the operand whose rows become accumulator columns: X or dY (WGRAD: dY)

@@ -1,0 +1,49 @@
+"""Columns that the adapters' second product gives to the tensor cores: every width is one that the MMA has, so the rule
+of the kernel (a header function) is compiled and evaluated here, without a GPU."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+SOURCE = r"""
+#include <cstdio>
+#include "grouped_internal.h"
+int main() {
+    for (int pair = 0; pair < 2; ++pair)
+        for (int own = 0; own <= 256; ++own)
+            std::printf("%d %d %d\n", pair, own, cf::lora_tensor_columns(own, pair != 0));
+    for (int kind = cf::GR_FORWARD; kind <= cf::GR_LORA; ++kind)
+        std::printf("step %d %d %d\n", kind, cf::grouped_column_step(kind, false), cf::grouped_column_step(kind, true));
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def lines(tmp_path_factory):
+    d = tmp_path_factory.mktemp("columns")
+    (d / "columns.cpp").write_text(SOURCE)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    gxx = shutil.which("g++")
+    assert gxx, "no g++"
+    subprocess.run([gxx, "-std=c++17", "-I", os.path.join(cuda, "include"), "-I",
+                    os.path.join(ROOT, "memory_fusion_gb300", "csrc"), str(d / "columns.cpp"), "-o", str(d / "columns")],
+                   check=True)
+    return subprocess.run([str(d / "columns")], check=True, capture_output=True, text=True).stdout.splitlines()
+
+
+def test_tensor_core_columns_are_widths_of_the_mma(lines):
+    """N of one CTA's MMA (M = 128) is a multiple of 16, of a pair's (M = 256) one of 32; no row is lost to rounding up."""
+    rows = [tuple(int(v) for v in ln.split()) for ln in lines if not ln.startswith("step")]
+    assert len(rows) == 2 * 257
+    for pair, own, nx in rows:
+        step = 32 if pair else 16
+        assert nx % step == 0 and own - step < nx <= own, (pair, own, nx)
+
+
+def test_steps(lines):
+    for ln in lines:
+        if ln.startswith("step"):
+            single, pair = (int(v) for v in ln.split()[2:])
+            assert single % 16 == 0 and pair % 32 == 0, ln
