@@ -1545,6 +1545,10 @@ cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int
     while (stages > 2 && bytes(stages) > kMaxSmem) --stages;
     *smem = bytes(stages);
     if (*smem > kMaxSmem || *smem > dev.max_smem_optin) return CF_ERR_UNSUPPORTED;
+    // Pairs have their SMs to themselves: of two pairs on the same two SMs, from launches on different streams, each
+    // could hold one SM's tensor memory and wait for the other's without end.  (A ring of the usual depth fills the SM
+    // anyway; this is for shallow ones.)
+    if (pair) *smem = std::min(kMaxSmem, dev.max_smem_optin);
     const int width = pair ? 2 : 1;
     const int64_t tiles = tiles_of(128 * width);
     if (tiles >= (int64_t(1) << 31) - 65536) return CF_ERR_UNSUPPORTED;

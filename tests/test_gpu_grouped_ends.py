@@ -6,8 +6,9 @@ every partial sum is a whole number that fp32 holds."""
 import numpy as np
 import pytest
 
+from memory_fusion_gb300 import cf
 from tests.gpu_util import torch_cuda
-from tests.test_gpu_grouped import SENTINEL, _check, _host, _lora_case, _lora_run, _tuning
+from tests.test_gpu_grouped import SENTINEL, _check, _dev, _host, _i32, _lora_case, _lora_run, _rng, _tuning
 from tests.test_gpu_grouped_adapters import _bounds
 
 pytestmark = pytest.mark.gpu
@@ -25,3 +26,27 @@ def test_a_long_request_shares_its_last_tile(own, tun, dt):
     out = _host(_lora_run(c, dt, tuning=_tuning(tun)))
     _check(out[live], ref[live], slack[live], dt, "Y")
     assert np.all(out[c["off"][-1]:] == SENTINEL)
+
+
+def test_pairs_of_two_streams():
+    """CTA pairs with shallow rings and all of tensor memory, launched on two streams at once: an SM holds one of them,
+    so neither waits for tensor memory that the other holds."""
+    torch = torch_cuda()
+    X, W = _dev(_rng(1).standard_normal((700, 256)), "bf16"), _dev(_rng(2).standard_normal((3, 256, 520)) / 16, "bf16")
+    off, tuning = _i32([0, 300, 301, 700]), cf.tuning(n_slice=256, cluster_m=2, stages=2)
+    want = cf.grouped_gemm(X, W, off, tuning=tuning)
+    dw = cf.grouped_gemm_wgrad(X, want, off, tuning=tuning)
+    torch.cuda.synchronize()
+    jobs = []
+    for _ in range(2):
+        size = cf.cf_grouped_gemm_workspace_size(700, 520, 256, 3)
+        jobs.append((torch.cuda.Stream(), cf.new_workspace(size), torch.zeros_like(want), torch.zeros_like(dw)))
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for s, ws, y, d in jobs:
+            cf.grouped_gemm(X, W, off, out=y, workspace=ws, stream=s, tuning=tuning)
+            cf.grouped_gemm_wgrad(X, y, off, out=d, workspace=ws, stream=s, tuning=tuning)
+    torch.cuda.synchronize()
+    for _, ws, y, d in jobs:
+        assert cf.cf_get_device_status(ws)[0] == cf.CF_OK
+        assert torch.equal(y, want) and torch.equal(d, dw)
