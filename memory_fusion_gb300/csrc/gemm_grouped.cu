@@ -126,7 +126,8 @@ __device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, uint32_t (&v)[32]
             : "r"(taddr + (uint32_t(16 * h) << 16))
             : "memory");
 }
-// the wait for loads into v, which is theirs until then
+// the wait for loads into v, which is theirs until then.  (A wait that does not name them orders memory alone: arithmetic
+// on v may be moved in front of it.)
 __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
@@ -1633,7 +1634,7 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                 for (int c = half * kSpan; c < w.n; c = next_fragment<kSpan, kHalves>(c)) {
                     uint32_t v[32];
                     ptx::tmem_ld32(tacc + uint32_t(c), v);
-                    ptx::tmem_ld_wait();
+                    ptx::tmem_ld_wait(v);
                     const int cols = min(32, w.n - c);
                     if constexpr (KIND == GR_LORA) {
                         if (parts > 0) {
@@ -1691,7 +1692,7 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                 for (int c = 0; c < w.n; c += 32) {
                     uint32_t v[32], up[16], rest[16];
                     ptx::tmem_ld_blocks(tacc + uint32_t(c), v);
-                    ptx::tmem_ld_wait();
+                    ptx::tmem_ld_wait(v);
                     if (fp16) Fragment::split<true>(up, rest, v, sc);
                     else Fragment::split<false>(up, rest, v, sc);
                     const int f8 = w.f0 + q * 32 + (lane & 3) * 8;

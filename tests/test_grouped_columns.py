@@ -1,6 +1,7 @@
 """Columns that the adapters' second product gives to the tensor cores: every width is one that the MMA has, so the rule
 of the kernel (a header function) is compiled and evaluated here, without a GPU."""
 import os
+import re
 import shutil
 import subprocess
 
@@ -47,3 +48,16 @@ def test_steps(lines):
         if ln.startswith("step"):
             single, pair = (int(v) for v in ln.split()[2:])
             assert single % 16 == 0 and pair % 32 == 0, ln
+
+
+def test_every_load_of_tensor_memory_has_a_wait_that_names_its_registers():
+    """A wait without operands does not keep arithmetic on the loaded registers behind it: each load into a register
+    array is followed by a wait that has the array as operand."""
+    with open(os.path.join(ROOT, "memory_fusion_gb300", "csrc", "gemm_grouped.cu")) as f:
+        text = f.read()
+    loads = list(re.finditer(r"ptx::tmem_ld(?:32|_blocks)\([^;]*?, (v(?:\[\d\])?)\);", text))
+    assert len(loads) >= 6
+    for m in loads:
+        wait = re.search(r"ptx::tmem_ld_wait\(" + re.escape(m.group(1)) + r"\);", text[m.end():m.end() + 250])
+        assert wait, text[m.start():m.end() + 80]
+    assert "tmem_ld_wait()" not in text
