@@ -715,7 +715,8 @@ typedef enum { CF_BF16 = 0, CF_FP16 = 1 } cf_dtype;  /* 16-bit operand types */
  * Tuning fields used (_ex): n_slice (accumulator columns: 16, 32, 64, 128, 256;
  * wgrad from 64 on), cluster_m (2: CTA pairs on tiles of 256 features, with
  * n_slice 128 or 256; 1: single CTAs), stages, max_clusters (cap on CTAs or
- * pairs), timeout_us, disable_pdl, extra_arrivals (TEST HOOK: > 0 makes the
+ * pairs), timeout_us (a wait for an accumulator has 4 us more for each 64 of
+ * its contraction), disable_pdl, extra_arrivals (TEST HOOK: > 0 makes the
  * wait for the accumulator run out). */
 CF_API size_t cf_grouped_gemm_workspace_size(int64_t T, int64_t N, int64_t K, int64_t E);
 

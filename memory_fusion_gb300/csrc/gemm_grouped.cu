@@ -187,6 +187,11 @@ constexpr int kMinStretch = 4;   // blocks a worker takes at least
 constexpr int kRunRows = 32;
 constexpr int kShortRows = kLoraShortRows;
 
+// The waits for an accumulator and for a group's last block have this much more time for each 64-deep block before it.
+// (A block takes 0.15 to 0.4 us, 2 where every SM's copies come from HBM at once: a tile that is not divided may sum for
+// seconds.)
+constexpr uint64_t kBlockNs = 4000;
+
 constexpr uint32_t kInfoProducer = 0x10000000u;
 constexpr uint32_t kInfoMma = 0x20000000u;
 constexpr uint32_t kInfoEpi = 0x30000000u;
@@ -755,7 +760,7 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
     // (grouped_cycles), which chose the tiles.  Every lane decides alike; divisions that do not need one another are
     // worked out side by side, a lane each (in a row they took 600 cycles of a launch of 10000).
     const int rows_all = lo_all - first;
-    constexpr int kMost = 1 << 20;  // blocks of a contraction, tiles x blocks then fit 30 bits
+    constexpr long long kMost = 1 << 30;  // blocks of all tiles: sums of them and of the workers then fit an int
     const int per_tile = KIND == GR_WGRAD ? ft * ((a.N + a.bn - 1) >> shift) : 1;
     const int nkc = (a.C + kBK - 1) / kBK;
     Plan p;
@@ -765,8 +770,9 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
     p.units = p.ways = p.base = p.rem = 0;
     p.groups = ngroups;
     const bool few = KIND == GR_WGRAD ? ngroups <= kGroupedSplitTiles && per_tile <= kGroupedSplitTiles &&
-                                            p.tiles <= kGroupedSplitTiles && carry <= kMost
-                                      : carry <= kGroupedSplitTiles && nkc <= kMost;
+                                            p.tiles <= kGroupedSplitTiles &&
+                                            static_cast<long long>(per_tile) * carry <= kMost
+                                      : carry <= kGroupedSplitTiles && static_cast<long long>(p.tiles) * nkc <= kMost;
     if (!kPair && a.partials != nullptr && few && p.tiles > 0) {
         auto divide = [&](int n0, int d0, int n1, int d1, int n2, int d2, int n3, int d3) {
             const int n = lane == 0 ? n0 : lane == 1 ? n1 : lane == 2 ? n2 : n3;
@@ -1457,8 +1463,9 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                 while (walk.next(w)) {
                     if (w.nk > 0 && (w.rows & 15) != 0) {
                         const uint32_t at = (s + uint32_t(w.nk) - 1u) % uint32_t(stages);
-                        const bool ok = ptx::mbar_wait_bounded(B.full0 + 8 * at, (ph >> at) & 1u, tmo, abort, a.err,
-                                                               kInfoMma | 0x200u | at);
+                        const bool ok =
+                            ptx::mbar_wait_bounded(B.full0 + 8 * at, (ph >> at) & 1u, tmo + uint64_t(w.nk) * kBlockNs,
+                                                   abort, a.err, kInfoMma | 0x200u | at);
                         if (!__all_sync(0xffffffffu, ok)) break;
                         ph ^= 1u << at;
                         const int left = w.rows - (w.nk - 1) * kBK;
@@ -1621,7 +1628,8 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                     }
                 }
             }
-            const bool ok = ptx::mbar_wait_bounded(B.tmem_full0 + 8 * buf, tph, tmo, abort, a.err, kInfoEpi | buf);
+            const bool ok = ptx::mbar_wait_bounded(B.tmem_full0 + 8 * buf, tph, tmo + uint64_t(w.kb1 - w.kb0) * kBlockNs,
+                                                   abort, a.err, kInfoEpi | buf);
             ptx::tc_fence_after();
             if constexpr (KIND == GR_LORA) ptx::griddep_wait();  // the bias is read through L1
             const uint32_t tacc = tmem_base + (uint32_t(q * 32) << 16) + buf * uint32_t(a.bn);

@@ -50,3 +50,48 @@ def test_pairs_of_two_streams():
     for _, ws, y, d in jobs:
         assert cf.cf_get_device_status(ws)[0] == cf.CF_OK
         assert torch.equal(y, want) and torch.equal(d, dw)
+
+
+def _counted(rows, K, N, every):
+    """X [rows, K] with a 1 in every `every`-th row of a column, at another row for each column, and `every` rows apart;
+    dY [rows, N] with row r holding 1 + column.  dW[k, n] = (1 + n) * the ones of column k."""
+    torch = torch_cuda()
+    X = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    for k in range(K):
+        X[(k * every) // K::every, k] = 1.0
+    dY = torch.arange(1, N + 1, device="cuda").to(torch.bfloat16).expand(rows, N).contiguous()
+    return X, dY
+
+
+@pytest.mark.parametrize("rows", [2 ** 26 + 5, 2 ** 27])
+def test_weight_gradient_of_very_many_rows(rows):
+    """One group past 2^26 rows (2^20 blocks of the contraction) is divided among the SMs like a shorter one: the sum
+    counts every marked row once, and no wait runs out."""
+    torch = torch_cuda()
+    K = N = 8
+    every = 2 ** 21
+    X, dY = _counted(rows, K, N, every)
+    X[-1] = 64.0  # the last row
+    off = _i32([0, rows])
+    ws = cf.new_workspace(cf.cf_grouped_gemm_workspace_size(rows, N, K, 1))
+    dw = cf.grouped_gemm_wgrad(X, dY, off, workspace=ws)
+    assert cf.cf_get_device_status(ws)[0] == cf.CF_OK
+    ones = (X.float().sum(0)).double()  # whole numbers below 2^24
+    want = ones[:, None] * torch.arange(1, N + 1, device="cuda").double()
+    assert torch.equal(dw[0].double(), want.to(torch.bfloat16).double())
+
+
+def test_a_long_sum_that_is_not_divided_is_waited_for():
+    """A group of very many rows beside a thousand empty ones, more tiles than may be divided: the wait for an
+    accumulator grows with what is summed in it."""
+    torch = torch_cuda()
+    rows, K, N, E = 2_000_003, 136, 136, 1024
+    X, dY = _counted(rows, K, N, 2 ** 15)
+    dY.clamp_(max=8.0)
+    off = _i32([0] * 500 + [rows] * (E + 1 - 500))
+    ws = cf.new_workspace(cf.cf_grouped_gemm_workspace_size(rows, N, K, E))
+    dw = cf.grouped_gemm_wgrad(X, dY, off, workspace=ws, tuning=cf.tuning(timeout_us=1000))
+    assert cf.cf_get_device_status(ws)[0] == cf.CF_OK
+    want = X.float().sum(0).double()[:, None] * dY[0].double()
+    assert torch.equal(dw[499].double(), want.to(torch.bfloat16).double())
+    assert not dw[:499].any() and not dw[500:].any()
