@@ -67,7 +67,8 @@ typedef enum {
     CF_ERR_CUDA = 6,               /* a CUDA runtime call failed (see
                                       cf_last_cuda_error)                        */
     CF_ERR_DEVICE_TIMEOUT = 7,     /* device: a bounded wait ran out             */
-    CF_ERR_DEVICE_BOUNDS = 8,      /* device: an index check failed              */
+    CF_ERR_DEVICE_BOUNDS = 8,      /* device: a check of an index or a range
+                                      failed                                     */
     CF_ERR_NO_DEVICE = 9           /* no sm_103 device is current                */
 } cf_status;
 
@@ -762,7 +763,7 @@ CF_API cf_status cf_grouped_gemm_wgrad_ex(const void *X, const void *dY, const i
  * the projection.  Sums are fp32; the scaled [T, R] product between the two is
  * held as the sum of two `dtype` numbers: to 2^-16 of its value in bf16; in
  * fp16 to 2^-22 or 2^-25, whichever is more, and a finite value beyond
- * +-131,008 counts as that.
+ * +-131,008 counts as that and is reported as CF_ERR_DEVICE_BOUNDS.
  *   X (device) `dtype` [T, K]      W (device) `dtype` [K, N]
  *   bias (device) fp32 [N] or NULL
  *   A (device) `dtype` [L, K, R]   B (device) `dtype` [L, R, N]

@@ -850,7 +850,8 @@ def grouped_gemm_wgrad(X, dY, offsets, *, out=None, workspace=None, stream=None,
 def gemm_lora(X, W, bias, A, B, offsets, adapters, *, scale=None, out=None, workspace=None, stream=None, tuning=None):
     """Y[r] = X[r] @ W + bias + scale[a] * (X[r] @ A[a]) @ B[a] for the rows r of request s,
     [offsets[s], offsets[s+1]), with a = adapters[s] (-1: no adapter).  X [T, K], W [K, N], A [L, K, R], B [L, R, N]
-    bf16 or fp16; bias fp32 [N] or None; offsets int32 [S + 1], adapters int32 [S], scale fp32 [L] or None (1)."""
+    bf16 or fp16; bias fp32 [N] or None; offsets int32 [S + 1], adapters int32 [S], scale fp32 [L] or None (1).
+    fp16: values of scale[a] * X[r] @ A[a] beyond +-131,008 count as that, and the workspace's status says so."""
     import torch
     (T, K), dev, dtype, dt = _first("X", X, 2)
     N = _sizes("W", W, 2)[1]

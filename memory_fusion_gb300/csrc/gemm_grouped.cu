@@ -196,6 +196,7 @@ constexpr uint32_t kInfoProducer = 0x10000000u;
 constexpr uint32_t kInfoMma = 0x20000000u;
 constexpr uint32_t kInfoEpi = 0x30000000u;
 constexpr uint32_t kInfoTable = 0x70000000u;
+constexpr uint32_t kInfoRange = 0x71000000u;
 
 struct GrLayout {
     uint32_t a_bytes, stage_bytes, table, stg, bars, total;
@@ -519,7 +520,8 @@ __device__ __forceinline__ float fits(float h) {
 }
 
 // H in two 16-bit parts, upper and rest: 16 bits and more of mantissa (fp16: 22, within twice its range, behind which H
-// saturates; an infinity or NaN goes to the upper part), so that the second product can run on the tensor cores
+// saturates, which is reported; an infinity or NaN goes to the upper part), so that the second product can run on the
+// tensor cores
 template <bool kFp16>
 __device__ __forceinline__ void split_pair(uint32_t &up, uint32_t &rest, float lo, float hi) {
     up = pack_pair<kFp16>(fits<kFp16>(lo), fits<kFp16>(hi));
@@ -527,7 +529,13 @@ __device__ __forceinline__ void split_pair(uint32_t &up, uint32_t &rest, float l
     rest = pack_pair<kFp16>(fabsf(lo) <= kFloatMax ? fits<kFp16>(rl) : 0.f,
                             fabsf(hi) <= kFloatMax ? fits<kFp16>(rh) : 0.f);
 }
+// fp16: a finite number that its two parts cannot hold
+__device__ __forceinline__ bool beyond_parts(float h) { return fabsf(h) > 131008.f && fabsf(h) <= kFloatMax; }
+__device__ __forceinline__ void report_range(const GroupedArgs &a) {
+    ptx::record_error(a.err, 8u /*CF_ERR_DEVICE_BOUNDS*/, kInfoRange);
+}
 __device__ __forceinline__ void store_low(const GroupedArgs &a, int row, int r, float h) {
+    if (a.fp16 && beyond_parts(h)) report_range(a);
     uint32_t up, rest;
     if (a.fp16) split_pair<true>(up, rest, h, 0.f);
     else split_pair<false>(up, rest, h, 0.f);
@@ -1696,11 +1704,21 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
             }
             if constexpr (KIND == GR_SHRINK) {
                 const float sc = a.scale ? __ldg(a.scale + w.w) : 1.f;
+                bool over = false;
 #pragma unroll 1
                 for (int c = 0; c < w.n; c += 32) {
                     uint32_t v[32], up[16], rest[16];
                     ptx::tmem_ld_blocks(tacc + uint32_t(c), v);
                     ptx::tmem_ld_wait(v);
+                    if (fp16) {  // (of this request's rows and the ranks that there are)
+                        const int fb = w.f0 + q * 32 + (lane >> 2), left = w.n - c - 2 * (lane & 3);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int k = i / 8, b = i / 2 % 4;
+                            over |= beyond_parts(sc * __uint_as_float(v[Fragment::pair(k, b) + i % 2])) &&
+                                    8 * k + i % 2 < left && fb + 8 * b < a.F;
+                        }
+                    }
                     if (fp16) Fragment::split<true>(up, rest, v, sc);
                     else Fragment::split<false>(up, rest, v, sc);
                     const int f8 = w.f0 + q * 32 + (lane & 3) * 8;
@@ -1709,6 +1727,7 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                     fr.store(a.out, up);
                     fr.store(static_cast<uint16_t *>(a.out) + a.F, rest);
                 }
+                if (over && ok) report_range(a);
             }
             float bias[4] = {0.f, 0.f, 0.f, 0.f};  // LORA: of a fragment's features in blocks
             if constexpr (KIND == GR_LORA) {

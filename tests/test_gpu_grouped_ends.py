@@ -95,3 +95,24 @@ def test_a_long_sum_that_is_not_divided_is_waited_for():
     want = X.float().sum(0).double()[:, None] * dY[0].double()
     assert torch.equal(dw[499].double(), want.to(torch.bfloat16).double())
     assert not dw[:499].any() and not dw[500:].any()
+
+
+@pytest.mark.parametrize("sizes,K", [([3, 1], 64), ([2], 4096), ([40], 64), ([100, 2], 64), ([40], 8192)])
+def test_middle_products_beyond_the_parts_are_reported(sizes, K):
+    """fp16: a finite middle value beyond +-131,008 is reported, in short requests, tiles and divided ones; values up to
+    it, infinities, and products of other rows with this adapter are not."""
+    torch = torch_cuda()
+    N, R, T = 64, 8, sum(sizes) + 1
+    X = torch.zeros(T, K, dtype=torch.float16, device="cuda")
+    X[:, K // 2] = 1024.0
+    X[-1] = 60000.0  # a request without an adapter, in the same tile
+    W = torch.zeros(K, N, dtype=torch.float16, device="cuda")
+    A = torch.zeros(5, K, R, dtype=torch.float16, device="cuda")
+    for a, v in enumerate((100.0, 127.9375, 128.0, float("inf"), -1000.0)):
+        A[a, K // 2, R - 1] = v
+    B = torch.full((5, R, N), 2.0 ** -6, dtype=torch.float16, device="cuda")
+    off = _i32(np.concatenate([[0], np.cumsum(sizes), [T]]))
+    ws = cf.new_workspace(cf.cf_gemm_lora_workspace_size(T, N, K, len(sizes) + 1, R))
+    for a, status in enumerate((cf.CF_OK, cf.CF_OK, cf.CF_ERR_DEVICE_BOUNDS, cf.CF_OK, cf.CF_ERR_DEVICE_BOUNDS)):
+        cf.gemm_lora(X, W, None, A, B, off, _i32([a] * len(sizes) + [-1]), workspace=ws)
+        assert cf.cf_get_device_status(ws)[0] == status, a
