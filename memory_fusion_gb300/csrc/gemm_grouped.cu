@@ -513,10 +513,11 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 }
 
 constexpr float kFloatMax = 3.402823466e38f;
-// a finite number, saturated where fp16 is the type
+// a finite number, no larger than the type's largest (bf16: numbers that would round to infinity lie behind that)
 template <bool kFp16>
 __device__ __forceinline__ float fits(float h) {
-    return kFp16 && fabsf(h) > 65504.f && fabsf(h) <= kFloatMax ? copysignf(65504.f, h) : h;
+    constexpr float kMost = kFp16 ? 65504.f : 0x1.fep127f;
+    return fabsf(h) > kMost && fabsf(h) <= kFloatMax ? copysignf(kMost, h) : h;
 }
 
 // H in two 16-bit parts, upper and rest: 16 bits and more of mantissa (fp16: 22, within twice its range, behind which H

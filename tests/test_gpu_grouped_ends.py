@@ -116,3 +116,25 @@ def test_middle_products_beyond_the_parts_are_reported(sizes, K):
     for a, status in enumerate((cf.CF_OK, cf.CF_OK, cf.CF_ERR_DEVICE_BOUNDS, cf.CF_OK, cf.CF_ERR_DEVICE_BOUNDS)):
         cf.gemm_lora(X, W, None, A, B, off, _i32([a] * len(sizes) + [-1]), workspace=ws)
         assert cf.cf_get_device_status(ws)[0] == status, a
+
+
+@pytest.mark.parametrize("sizes,K", [([3, 1], 64), ([40], 64), ([100, 2], 64), ([40], 8192)])
+def test_middle_products_beyond_the_largest_bf16_are_finite(sizes, K):
+    """bf16: a middle value between the largest bf16 and the largest fp32 number is held by the two parts like any other
+    one (the upper part must not round to infinity)."""
+    torch = torch_cuda()
+    N, R, T = 64, 8, sum(sizes)
+    top = torch.finfo(torch.bfloat16).max
+    X = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    X[:, 0], X[:, 1] = 1.0, 3 * 2.0 ** -10
+    W = torch.zeros(K, N, dtype=torch.bfloat16, device="cuda")
+    A = torch.zeros(2, K, R, dtype=torch.bfloat16, device="cuda")
+    A[0, :2, 0], A[1, :2, 0] = top, -top
+    B = torch.full((2, R, N), 2.0 ** -100, dtype=torch.bfloat16, device="cuda")
+    off = _i32(np.concatenate([[0], np.cumsum(sizes)]))
+    h = top * (1 + 3 * 2.0 ** -10)  # closer to the largest fp32 number than to the largest bf16 one
+    assert top < h < torch.finfo(torch.float32).max
+    for a in (0, 1):
+        y = cf.gemm_lora(X, W, None, A, B, off, _i32([a] * len(sizes))).double()
+        want = (h if a == 0 else -h) * 2.0 ** -100
+        assert ((y - want).abs() <= 2.0 ** -8 * abs(want)).all(), (a, y[0, 0].item(), want)
