@@ -768,7 +768,12 @@ def _launch_on(device, stream):
         if stream is None:
             yield
         else:
-            s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+            if not isinstance(stream, int):
+                s = stream
+            elif stream in (0, 1):  # the legacy default stream (torch makes a stream of its own for an external 0)
+                s = torch.cuda.default_stream(device)
+            else:
+                s = torch.cuda.ExternalStream(stream, device=device)
             with torch.cuda.stream(s):
                 yield
 
@@ -781,6 +786,8 @@ def _run(name, before, between, out, shape, dtype, device, workspace, size, size
     index = device.index
     if workspace is not None and not (workspace.get_device() == index and workspace.is_contiguous()):
         raise ValueError(f"workspace is not a contiguous tensor on {device}")
+    if stream is not None and getattr(stream, "device", device) != device:
+        raise ValueError(f"stream is on {stream.device}, not on {device}")
     if stream is not None or index != torch._C._cuda_getDevice():
         with _launch_on(device, stream):
             return _run(name, before, between, out, shape, dtype, device, workspace, size, sizes, None, tuning)

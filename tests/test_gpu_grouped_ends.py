@@ -138,3 +138,40 @@ def test_middle_products_beyond_the_largest_bf16_are_finite(sizes, K):
         y = cf.gemm_lora(X, W, None, A, B, off, _i32([a] * len(sizes))).double()
         want = (h if a == 0 else -h) * 2.0 ** -100
         assert ((y - want).abs() <= 2.0 ** -8 * abs(want)).all(), (a, y[0, 0].item(), want)
+
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_the_default_streams_handle(handle):
+    """0 and 1 are the legacy default stream's handles: the call waits for what is on that stream and what is on it
+    later waits for the call."""
+    torch = torch_cuda()
+    X, W = _dev(_rng(3).standard_normal((300, 256)), "bf16"), _dev(_rng(4).standard_normal((2, 256, 264)) / 16, "bf16")
+    off = _i32([0, 120, 300])
+    want = cf.grouped_gemm(X, W, off)
+    x, a = torch.zeros_like(X), torch.randn(4096, 4096, device="cuda")
+    out = torch.zeros_like(want)
+    with cf._launch_on(X.device, handle):
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    torch.cuda.synchronize()
+    for _ in range(20):  # keeps the stream busy before the input is there
+        a = a @ a * 1e-3
+    x.copy_(X)
+    cf.grouped_gemm(x, W, off, out=out, stream=handle)
+    got = out.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_a_stream_of_another_device_is_refused():
+    torch = torch_cuda()
+
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+
+    X, W = _dev(np.ones((4, 64)), "bf16"), _dev(np.ones((1, 64, 64)), "bf16")
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        cf.grouped_gemm(X, W, _i32([0, 4]), stream=Stream())
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        cf.gemm_lora(X, W[0], None, X.new_zeros(1, 64, 8), X.new_zeros(1, 8, 64), _i32([0, 4]), _i32([0]),
+                     stream=Stream())
