@@ -6,6 +6,7 @@ every partial sum is a whole number that fp32 holds."""
 import numpy as np
 import pytest
 
+import oracle
 from memory_fusion_gb300 import cf
 from tests.gpu_util import torch_cuda
 from tests.test_gpu_grouped import SENTINEL, _check, _dev, _host, _i32, _lora_case, _lora_run, _rng, _tuning
@@ -175,3 +176,120 @@ def test_a_stream_of_another_device_is_refused():
     with pytest.raises(ValueError, match="stream is on cuda:1"):
         cf.gemm_lora(X, W[0], None, X.new_zeros(1, 64, 8), X.new_zeros(1, 8, 64), _i32([0, 4]), _i32([0]),
                      stream=Stream())
+
+
+ENDS = [0.0, 1e-3, 1.0, 3.0, 6.5, 7.0, 8.0, 10.0, 11.75, 12.0, 12.5, 13.0, 100.0, 1000.0, 3e4]
+
+
+def _ends(dt):
+    """Both signs of the activation's interesting arguments and the type's largest, as numbers of the type."""
+    torch = torch_cuda()
+    t = torch.bfloat16 if dt == "bf16" else torch.float16
+    v = torch.tensor(ENDS + [torch.finfo(t).max], device="cuda").to(t)
+    return torch.cat([v, -v]), torch.tensor([float("inf"), float("-inf"), float("nan")] + [1.0] * 5, device="cuda").to(t)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("tun", ["auto", "n64", "pair128"])
+@pytest.mark.parametrize("K,at", [(8, 0), (4096, 2047), (4096, 4095)])
+def test_activation_ends_forward(K, at, tun, dt):
+    """Products that are exactly the ends of the activation: in whole tiles and in ones whose contraction is divided."""
+    torch = torch_cuda()
+    finite, special = _ends(dt)
+    z = torch.cat([finite, special])
+    N, T = z.numel(), 21
+    X = torch.zeros(T, K, dtype=z.dtype, device="cuda")
+    X[:, at] = 1.0
+    W = torch.zeros(2, K, N, dtype=z.dtype, device="cuda")
+    W[0, at] = z
+    pre = torch.full((T, N), SENTINEL, dtype=z.dtype, device="cuda")
+    y = cf.grouped_gemm(X, W, _i32([0, 20, T]), act="gelu_tanh", preact=pre, tuning=_tuning(tun))
+    assert torch.equal(pre[:20].nan_to_num(9.0), z.expand(20, N).nan_to_num(9.0)) and not pre[20].any() and not y[20].any()
+    n = finite.numel()
+    got, want = _host(y[:20, :n]), oracle.gelu_tanh(_host(finite))[None, :].repeat(20, 0)
+    # the function's own error (see test_gpu_grouped): 2^-16 of the value, 1e-10 where the value is below that
+    _check(got, want, 2.0 ** -16 * np.abs(want) + 1e-10, dt, "gelu")
+    assert torch.all(y[:20, n] == float("inf"))
+    assert y[:20, n + 1:n + 3].isnan().all()  # -inf times 0, as x (1 + tanh) / 2 is, and NaN
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("tun", ["auto", "n64", "pair128"])
+@pytest.mark.parametrize("N,at", [(8, 0), (4096, 2047), (4096, 4095)])
+def test_activation_ends_gradient(N, at, tun, dt):
+    """The slope at the ends of the activation, times an input gradient of exactly 1 or -3."""
+    torch = torch_cuda()
+    finite, special = _ends(dt)
+    z = torch.cat([finite, special])
+    K, T = z.numel(), 21
+    dY = torch.zeros(T, N, dtype=z.dtype, device="cuda")
+    dY[:, at] = 1.0
+    dY[1, at] = -3.0
+    W = torch.zeros(1, K, N, dtype=z.dtype, device="cuda")
+    W[0, :, at] = 1.0
+    dx = cf.grouped_gemm_dgrad(dY, W, _i32([0, T]), preact=z.expand(T, K).contiguous(), tuning=_tuning(tun))
+    n = finite.numel()
+    slope = oracle.gelu_tanh_slope(_host(finite))
+    want = slope[None, :] * _host(dY[:, at:at + 1])
+    # p and 2 z p (1 - p) u' are each off by 2^-16 of themselves at most, and 1e-10 where they are below that
+    _check(_host(dx[:, :n]), want, 2.0 ** -16 * (np.abs(want) + 3.0) + 3e-10, dt, "slope")
+    for r, g in ((0, 1.0), (1, -3.0)):  # the slope's limits, 1 and 0
+        assert dx[r, n].item() == g and dx[r, n + 1].item() == 0.0 and dx[r, n + 2].isnan()
+
+
+EXACT_TUNINGS = {"auto": {}, "n256": dict(n_slice=256, cluster_m=1), "n64x5": dict(n_slice=64, cluster_m=1, max_clusters=5),
+                 "n64x37": dict(n_slice=64, cluster_m=1, max_clusters=37), "pair128": dict(n_slice=128, cluster_m=2)}
+
+
+def _whole(seed, dt, *shape):
+    torch = torch_cuda()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(-2, 3, shape, generator=g, device="cuda").to(torch.bfloat16 if dt == "bf16" else torch.float16)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("tun", EXACT_TUNINGS)
+@pytest.mark.parametrize("rows,long,short", [([2, 0, 1], 4096, 136), ([1, 40], 8200, 72), ([130], 5000, 264), ([20, 300], 1992, 128)])
+def test_whole_numbers_are_summed_exactly(rows, long, short, tun, dt):
+    """Operands of -2..2: every partial sum is a whole number below 2^24, so fp32 sums are exact in any order and the
+    result is the exact sum rounded once.  A block lost or counted twice at the border of two pieces shows."""
+    torch = torch_cuda()
+    tuning = cf.tuning(**EXACT_TUNINGS[tun])
+    E, T = len(rows), sum(rows)
+    bounds = np.concatenate([[0], np.cumsum(rows)])
+    off = _i32(bounds)
+    X, W = _whole(1, dt, T, long), _whole(2, dt, E, long, short)
+    want = torch.cat([X[a:b].double() @ W[e].double() for e, (a, b) in enumerate(zip(bounds, bounds[1:]))])
+    assert want.abs().max() < 2 ** 24
+    assert torch.equal(cf.grouped_gemm(X, W, off, tuning=tuning), want.to(X.dtype))
+    dx = cf.grouped_gemm_dgrad(X, W.transpose(1, 2).contiguous(), off, tuning=tuning)
+    assert torch.equal(dx, want.to(X.dtype))
+    # the weight gradient's long sum runs over rows: groups of `long` rows, one row, none, and the rest
+    total = 3 * long
+    A, D = _whole(3, dt, total, 72), _whole(4, dt, total, short)
+    cuts = [0, long, long + 1, long + 1, total - 3]
+    dw = cf.grouped_gemm_wgrad(A, D, _i32(cuts), tuning=tuning)
+    want = torch.stack([A[a:b].double().T @ D[a:b].double() for a, b in zip(cuts, cuts[1:])])
+    assert torch.equal(dw, want.to(A.dtype))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("tun", EXACT_TUNINGS)
+@pytest.mark.parametrize("sizes,K,R", [([1], 4096, 16), ([1, 1, 3, 1], 8200, 24), ([40, 1, 2], 1992, 72), ([300, 2, 17, 64], 136, 8)])
+def test_adapters_of_whole_numbers_are_exact(sizes, K, R, tun, dt):
+    """The same for the adapters: the middle product is a whole number below 2^16, which its two parts hold."""
+    torch = torch_cuda()
+    S, T, N, L = len(sizes), sum(sizes), 264, 3
+    bounds = np.concatenate([[0], np.cumsum(sizes)])
+    X, W, A, B = _whole(5, dt, T, K), _whole(6, dt, K, N), _whole(7, dt, L, K, R), _whole(8, dt, L, R, N)
+    bias, scale = _whole(9, dt, N).float(), torch.tensor([1.0, 2.0, -4.0], device="cuda")
+    ad = [(i * 2 + 1) % (L + 1) - 1 for i in range(S)]
+    y = cf.gemm_lora(X, W, bias, A, B, _i32(bounds), _i32(ad), scale=scale, tuning=cf.tuning(**EXACT_TUNINGS[tun]))
+    want = X.double() @ W.double() + bias.double()
+    for a, lo, hi in zip(ad, bounds, bounds[1:]):
+        if a >= 0:
+            h = scale[a].double() * (X[lo:hi].double() @ A[a].double())
+            assert h.abs().max() < 2 ** 16
+            want[lo:hi] += h @ B[a].double()
+    assert want.abs().max() < 2 ** 24
+    assert torch.equal(y, want.to(X.dtype))
