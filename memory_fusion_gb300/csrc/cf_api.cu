@@ -1389,12 +1389,10 @@ cf_status grouped_sizes(int64_t T, int64_t N, int64_t K, int64_t groups, int dty
 // -------------------------------------------------------------------------
 // Tile width (accumulator columns) and CTA pairs, from the sizes the host knows: a model of a launch's cycles,
 // minimised over the widths.  Group sizes are device data, so groups are taken as equal, with half a tile of waste
-// where they are wider than a tile.  Measured on a GB300 (about 1.8 GHz under load): an MMA block of n columns takes
-// 2.35 n cycles (600 at 256) and 290 at least (370 in a pair), copies arrive at 75 B per cycle and SM (43 where the
-// matrix's rows are no multiples of 128 bytes: 2048 features 17.4 us, 2056 21.9), HBM gives the chip 3770 B per cycle;
-// an epilogue takes 1500 cycles and 20 a column, 900 more in a pair; dividing tiles costs
-// 1500 cycles and 70 a column (writing, adding, finishing), the low-rank product of rows with adapters of their own
-// 1000 cycles for 8 rows and 8 ranks.  Against every width and both CTA counts, timed over 180 random sizes, the choice
+// where they are wider than a tile.  Measured on a GB300 (about 1.8 GHz under load), besides what the device's plan needs
+// too (grouped_internal.h): copies arrive at 75 B per cycle and SM (43 where the matrix's rows are no multiples of 128
+// bytes: 2048 features 17.4 us, 2056 21.9), HBM gives the chip 3770 B per cycle; an epilogue takes 1500 cycles and 20 a
+// column, 900 more in a pair; the low-rank product of rows with adapters of their own 1000 cycles for 8 rows and 8 ranks.  Against every width and both CTA counts, timed over 180 random sizes, the choice
 // takes 4 % more time than the best one in the geometric mean.
 // -------------------------------------------------------------------------
 constexpr double kPlanSms = 152;  // a GB300's, whatever device is current: the workspace size follows from this plan
@@ -1422,7 +1420,7 @@ int shrink_columns(int64_t T) {
 double lora_wait(const GroupedShape &s, double *busy) {
     const int bn = shrink_columns(s.T);
     const double blocks = double((s.C + 63) / 64), tiles = double((s.T + bn - 1) / bn);
-    const double ways = std::max(1.0, std::min(std::floor(kPlanSms / tiles), std::floor(blocks / 4)));
+    const double ways = std::max(1.0, std::min(std::floor(kPlanSms / tiles), std::floor(blocks / cf::kMinStretch)));
     *busy = std::min(kPlanSms, tiles * ways);
     return 2500 + blocks / ways * 300 + (ways > 1 ? 2500 : 0) + 1500 + 20 * bn;
 }
@@ -1460,7 +1458,8 @@ double grouped_cycles(const GroupedShape &s, int bn, bool pair) {
     }
     // (where half of the tile's width holds its columns, a copy brings only that half)
     const double copies = copy_cycles(s, !wgrad && 2 * n <= bn ? bn / 2 : bn, pair);
-    const double block = std::max(std::max(2.35 * n, pair ? 370.0 : 290.0), copies);
+    const double block = std::max(
+        std::max(cf::kMmaCycles20Columns / 20.0 * n, double(pair ? cf::kMmaCyclesLeastPair : cf::kMmaCyclesLeast)), copies);
     const double main = blocks * block + 400, hbm = bytes / 3770;
     const double epilogue = 1500 + 20 * n + (pair ? 900 : 0) + low;
     // no accumulator is complete before H is there, and a CTA whose SM H keeps busy starts then
@@ -1475,10 +1474,11 @@ double grouped_cycles(const GroupedShape &s, int bn, bool pair) {
     const double first = after((rounds - 1) * std::max(main, epilogue) + main, std::min(tiles, sms));
     const double whole = both(first + epilogue, hbm);
     if (pair || tiles > double(cf::kGroupedSplitTiles)) return whole;
-    const double each = std::max(tiles * main / sms, 4 * block);
+    const double each = std::max(tiles * main / sms, cf::kMinStretch * block);
     const double parts = std::max(1.0, sms / tiles);
-    const double mine = after(each, std::min(sms, tiles * (blocks / 4)));
-    const double split = both(mine, hbm) + 1500 + 70 * n + 1500 + 20 * n + low / parts;
+    const double mine = after(each, std::min(sms, tiles * (blocks / cf::kMinStretch)));
+    const double split =
+        both(mine, hbm) + cf::kDivideCycles + cf::kDivideCyclesColumn * n + 1500 + 20 * n + low / parts;
     return std::min(whole, split);
 }
 
@@ -1541,7 +1541,7 @@ cf_status plan_grouped(int kind, int64_t T, int64_t F, int64_t C, int64_t N, int
     const int a_blocks = F <= 64 && kind != cf::GR_DGRAD && !pair ? 1 : 2;
     // (deeper rings of small stages were slower: 250 rows over 32 groups of 2048 x 4096, 12 stages 76.9 us, 8 73.2)
     int stages = t.stages > 0 ? t.stages : 8;
-    auto bytes = [&](int n) { return cf::grouped_smem_bytes(kind, pair, n, bn, int(groups), int(rank), a_blocks); };
+    auto bytes = [&](int n) { return cf::grouped_smem_bytes(kind, pair, n, bn, int(groups), a_blocks); };
     while (stages > 2 && bytes(stages) > kMaxSmem) --stages;
     *smem = bytes(stages);
     if (*smem > kMaxSmem || *smem > dev.max_smem_optin) return CF_ERR_UNSUPPORTED;
@@ -1605,7 +1605,7 @@ bool make_tmap_rows(cf::GroupedArgs *a, const void *rows, int64_t T, int64_t C) 
 // 43.9 and 42.8.)
 int lora_long_rows(int64_t N, int64_t K, int64_t R) {
     const double share = std::min(1.0, double((N + 127) / 128) / kPlanSms);
-    const double rows = double((K + 63) / 64) * 290 * share / (9.0 * double(R));
+    const double rows = double((K + 63) / 64) * cf::kMmaCyclesLeast * share / (9.0 * double(R));
     return int(std::min(128.0, std::max(16.0, 16 * std::ceil(rows / 16))));
 }
 
@@ -1801,7 +1801,7 @@ extern "C" cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *
     int sh_ctas = 0, sh_smem = 0, ctas, smem;
     if (L > 0) {
         cf_tuning ts = t;
-        ts.n_slice = ts.stages = ts.cluster_m = 0;  // the knobs are the main product's
+        ts.n_slice = ts.stages = ts.cluster_m = ts.max_clusters = 0;  // the knobs are the main product's
         grouped_args(&sh, T, R, K, 0, S, int(dtype), offsets, workspace, t);
         st = plan_grouped(cf::GR_SHRINK, T, R, K, 0, S, 0, ts, dev, workspace, 0, part_sh, room_sh, &sh, &sh_ctas,
                           &sh_smem);

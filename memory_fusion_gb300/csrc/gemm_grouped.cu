@@ -180,7 +180,6 @@ constexpr int kShortWarps = 6;
 constexpr int kBK = 64;         // contraction per stage (128 bytes: one swizzle atom)
 constexpr int kFB = 128;        // features per tile (accumulator lanes)
 constexpr int kRasterRows = 16;  // row tiles walked before the next feature tile
-constexpr int kMinStretch = 4;   // blocks a worker takes at least
 // LORA: rows up to which a run of shorter requests joins the long one before it (a run of its own costs a row tile; one
 // that joins ends the tile's part on the tensor cores.  0, 16, 32 and 64 rows: 50.5, 44.3, 44.2 and 44.2 us for 1537
 // rows of 40 requests, 2048 x 2056)
@@ -205,8 +204,7 @@ struct GrLayout {
 // int32 arrays of the group table behind the Plan, groups + 1 long
 __host__ __device__ constexpr int table_arrays(int kind) { return kind == GR_LORA ? 6 : kind == GR_SHRINK ? 3 : 2; }
 
-__host__ __device__ inline GrLayout gr_layout(int kind, bool pair, int stages, int bn, int groups, int rank,
-                                              int a_blocks) {
+__host__ __device__ inline GrLayout gr_layout(int kind, bool pair, int stages, int bn, int groups, int a_blocks) {
     GrLayout L;
     // a CTA of a pair stages its own 128 features and half of the tile's columns
     L.a_bytes = uint32_t(a_blocks) * 8192u;
@@ -278,7 +276,6 @@ struct Plan {
     int split;      // stretches
     int workers;    // that take part
     int tiles;
-    int units;      // split: blocks of all tiles
     int ways;       // split: stretches of each tile, or 0 where they run over tiles:
     int base, rem;  // then a worker's stretch is base blocks, of the first rem workers one more
     int groups;     // LORA: long requests and runs of short ones; else the groups
@@ -776,7 +773,7 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
     p.split = 0;
     p.workers = workers;
     p.tiles = KIND == GR_WGRAD ? ngroups * per_tile : carry;
-    p.units = p.ways = p.base = p.rem = 0;
+    p.ways = p.base = p.rem = 0;
     p.groups = ngroups;
     const bool few = KIND == GR_WGRAD ? ngroups <= kGroupedSplitTiles && per_tile <= kGroupedSplitTiles &&
                                             p.tiles <= kGroupedSplitTiles &&
@@ -802,8 +799,8 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
         // end of one tile and the start of another, each of which costs what adding a piece costs.
         const int most = KIND == GR_WGRAD ? 0 : min(of.z, nkc / kMinStretch);
         const int cols = KIND == GR_WGRAD ? a.bn : min(a.bn, of.w + 15);  // columns of a tile, about
-        const int block = max(max(47 * cols / 20, 290), a.copy_cycles);
-        const int4 in = divide(1500 + 70 * cols, block, a.wait_cycles, block, nkc + most - 1, max(most, 1), units,
+        const int block = max(max(kMmaCycles20Columns * cols / 20, kMmaCyclesLeast), a.copy_cycles);
+        const int4 in = divide(kDivideCycles + kDivideCyclesColumn * cols, block, a.wait_cycles, block, nkc + most - 1, max(most, 1), units,
                                stretch);
         const int adding = in.x + 1, least = in.y;  // no tile can be finished before
         const int whole = max(whole0, least);
@@ -811,7 +808,6 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
         const int mixed = max(stretch, least) + adding + adding / 2;
         if (whole > min(even, mixed)) {
             p.split = 1;
-            p.units = units;
             if (even <= mixed) {
                 p.ways = most;
                 p.workers = p.tiles * most;
@@ -1389,7 +1385,7 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
     constexpr bool kAMn = KIND != GR_DGRAD;  // features contiguous in memory: A is MN-major
     constexpr bool kBMn = KIND == GR_WGRAD;
     const int stages = a.stages;
-    const GrLayout L = gr_layout(KIND, kPair, stages, a.bn, a.groups, a.rank, a.a_blocks);
+    const GrLayout L = gr_layout(KIND, kPair, stages, a.bn, a.groups, a.a_blocks);
     const GrBars B = gr_bars(base + L.bars, stages);
     const Table tab(smem_raw + L.table, KIND, a.groups);
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem_raw + (B.misc - base));
@@ -1871,8 +1867,8 @@ void *kernel_for(int kind) {
 
 }  // namespace
 
-int grouped_smem_bytes(int kind, bool pair, int stages, int bn, int groups, int rank, int a_blocks) {
-    return int(gr_layout(kind, pair, stages, bn, groups, rank, a_blocks).total);
+int grouped_smem_bytes(int kind, bool pair, int stages, int bn, int groups, int a_blocks) {
+    return int(gr_layout(kind, pair, stages, bn, groups, a_blocks).total);
 }
 
 cudaError_t launch_grouped(int kind, const GroupedArgs &a, int ctas, int smem, bool pdl, cudaStream_t stream) {

@@ -21,6 +21,12 @@ constexpr int kGroupedMaxSmem = 232448;   // dynamic shared memory of a CTA (227
 constexpr int kGroupedMaxGroups = 1024;  // the group table lives in shared memory
 constexpr int kGroupedSplitTiles = 1024; // tiles whose contraction may be divided among CTAs
 constexpr int kGroupedWorkers = 160;     // CTAs that may hold a piece of a tile (a GB300 has 152 SMs)
+// Cycles of the cost models that the host's choice of tiles and the device's plan share (about 1.8 GHz under load): an MMA
+// block of 64 in the contraction takes 2.35 a column, and 290 at least (370 in a pair); dividing tiles (writing, adding,
+// finishing pieces) 1500 and 70 a column.
+constexpr int kMmaCycles20Columns = 47, kMmaCyclesLeast = 290, kMmaCyclesLeastPair = 370;
+constexpr int kDivideCycles = 1500, kDivideCyclesColumn = 70;
+constexpr int kMinStretch = 4;           // blocks of 64 that a worker takes at least
 constexpr int kLoraShortRows = 4;        // rows up to which a request's X . A runs on the CUDA cores
 constexpr int kLoraMaxSplit = 8;         // parts of their contraction
 constexpr int kLoraMaxRank = 128;        // one tile of features in the first product
@@ -69,7 +75,7 @@ struct GroupedArgs {
     int rank;                // LORA
     int long_rows;           // LORA: rows from which a request has tiles of its own
     int fp16;                // 16-bit type of every operand: 0 bf16, 1 fp16
-    int act;                 // FORWARD, DGRAD: 1 = GELU(tanh)
+    int act;                 // FORWARD: 1 = GELU(tanh)
     int bn;                  // columns of one accumulator tile (16, 32, 64, 128 or 256)
     int stages;
     int copy_cycles;         // what a block's copies take
@@ -79,7 +85,7 @@ struct GroupedArgs {
     unsigned long long timeout_ns;
 };
 
-int grouped_smem_bytes(int kind, bool pair, int stages, int bn, int groups, int rank, int a_blocks);
+int grouped_smem_bytes(int kind, bool pair, int stages, int bn, int groups, int a_blocks);
 cudaError_t launch_grouped(int kind, const GroupedArgs &a, int ctas, int smem, bool pdl, cudaStream_t stream);
 
 }  // namespace cf
