@@ -179,10 +179,12 @@ __host__ __device__ constexpr int registers_of(int kind) { return kind == GR_SHR
 constexpr int kShortWarps = 6;
 constexpr int kBK = 64;         // contraction per stage (128 bytes: one swizzle atom)
 constexpr int kFB = 128;        // features per tile (accumulator lanes)
-constexpr int kRasterRows = 16;  // row tiles walked before the next feature tile
+// row tiles walked before the next feature tile (the forward and the input gradient of 16384 rows, one after another:
+// 368 and 201 us with 4, 358 and 193 with 16, 359 and 193 with 64)
+constexpr int kRasterRows = 16;
 // LORA: rows up to which a run of shorter requests joins the long one before it (a run of its own costs a row tile; one
-// that joins ends the tile's part on the tensor cores.  0, 16, 32 and 64 rows: 50.5, 44.3, 44.2 and 44.2 us for 1537
-// rows of 40 requests, 2048 x 2056)
+// that joins ends the tile's part on the tensor cores.  Geometric mean over 28 batches with 0, 16, 32 and 64 rows: 31.4,
+// 30.8, 30.7 and 30.8 us; 1537 rows of 40 requests, 2048 x 2056: 52 us with 0, 43 with the others)
 constexpr int kRunRows = 32;
 constexpr int kShortRows = kLoraShortRows;
 
@@ -412,7 +414,7 @@ struct Walk {
                 r.col0 = lo;
                 r.n = rows;
             } else {
-                const int per = ((rows + rt - 1) / rt + kGran - 1) & ~(kGran - 1);
+                const int per = grouped_rows_per_tile(rows, rt, kGran);
                 const int chunk = local / (kRasterRows * ft);
                 const int wide = min(kRasterRows, rt - chunk * kRasterRows);
                 const int in = local - chunk * kRasterRows * ft;
@@ -789,8 +791,8 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
         };
         const int units = KIND == GR_WGRAD ? per_tile * carry : p.tiles * nkc;
         const int4 of = divide(units + workers - 1, workers, p.tiles + workers - 1, workers,
-                               KIND == GR_WGRAD ? units + p.tiles - 1 : workers, p.tiles, rows_all + ngroups - 1,
-                               ngroups);
+                               KIND == GR_WGRAD ? units + p.tiles - 1 : workers, p.tiles,
+                               KIND == GR_WGRAD ? 0 : rows_all + ngroups - 1, ngroups);
         const int share = of.x, rounds = of.y;
         const int stretch = max(share, kMinStretch);
         // WGRAD: of mean tiles, or the longest one

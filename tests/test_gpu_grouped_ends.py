@@ -293,3 +293,37 @@ def test_adapters_of_whole_numbers_are_exact(sizes, K, R, tun, dt):
             want[lo:hi] += h @ B[a].double()
     assert want.abs().max() < 2 ** 24
     assert torch.equal(y, want.to(X.dtype))
+
+
+@pytest.mark.parametrize("tun", [None, dict(n_slice=256, cluster_m=1), dict(n_slice=32)])
+def test_the_most_rows(tun):
+    """2^31 - 512 rows of 8 columns (34 GB each of X and Y) in two groups: rows from everywhere, and the ends."""
+    torch = torch_cuda()
+    T, K, N = 2 ** 31 - 512, 8, 8
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB of free device memory")
+    cut = 2 ** 31 - 2 ** 21
+    X = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    pick = torch.cat([torch.randint(0, T, (4096,), device="cuda", generator=torch.Generator("cuda").manual_seed(1)),
+                      torch.arange(300, device="cuda"), torch.arange(cut - 300, cut + 300, device="cuda"),
+                      torch.arange(T - 300, T - 2, device="cuda")])
+    X[pick] = torch.randint(-2, 3, (pick.numel(), K), device="cuda", generator=torch.Generator("cuda").manual_seed(2)).to(X.dtype)
+    W = _whole(1, "bf16", 2, K, N)
+    Y = torch.full((T, N), SENTINEL, dtype=X.dtype, device="cuda")
+    ws = cf.new_workspace(cf.cf_grouped_gemm_workspace_size(T, N, K, 2))
+    tuning = cf.tuning(**tun) if tun else None
+    cf.grouped_gemm(X, W, _i32([0, cut, T - 2]), out=Y, workspace=ws, tuning=tuning)
+    assert cf.cf_get_device_status(ws)[0] == cf.CF_OK
+    want = torch.where((pick < cut)[:, None], X[pick].double() @ W[0].double(), X[pick].double() @ W[1].double())
+    assert torch.equal(Y[pick].double(), want)
+    assert (Y[T - 2:] == SENTINEL).all()
+    rest = torch.randint(0, T - 2, (100_000,), device="cuda")  # nearly all of them rows of zeros
+    assert torch.equal((Y[rest] != 0).any(1), (X[rest].float() @ W[0].float() != 0).any(1) & (rest < cut)
+                       | (X[rest].float() @ W[1].float() != 0).any(1) & (rest >= cut))
+    if tun is None:
+        dw = cf.grouped_gemm_wgrad(X, Y, _i32([0, cut, T - 2]), workspace=ws)
+        assert cf.cf_get_device_status(ws)[0] == cf.CF_OK
+        one = pick.unique()
+        for e, rows in ((0, one[one < cut]), (1, one[(one >= cut) & (one < T - 2)])):
+            want = X[rows].double().T @ Y[rows].double()
+            assert want.abs().max() < 2 ** 24 and torch.equal(dw[e].double(), want.to(X.dtype).double())

@@ -15,6 +15,14 @@ int main() {
     for (int pair = 0; pair < 2; ++pair)
         for (int own = 0; own <= 256; ++own)
             std::printf("%d %d %d\n", pair, own, cf::lora_tensor_columns(own, pair != 0));
+    const int sizes[] = {17, 33, 255, 257, 1000, 100000, (1 << 30) + 7, 0x7fffffff - (1 << 23), 0x7fffffff - 511};
+    for (int step = 16; step <= 32; step *= 2)
+        for (int bn = step > 16 ? 128 : 16; bn <= 256; bn *= 2)
+            for (int rows : sizes) {
+                const int tiles = int((static_cast<long long>(rows) + bn - 1) / bn);
+                if (tiles > 1)
+                    std::printf("cut %d %d %d %d\n", bn, rows, tiles, cf::grouped_rows_per_tile(rows, tiles, step));
+            }
     for (int kind = cf::GR_FORWARD; kind <= cf::GR_LORA; ++kind)
         std::printf("step %d %d %d\n", kind, cf::grouped_column_step(kind, false), cf::grouped_column_step(kind, true));
 }
@@ -36,7 +44,7 @@ def lines(tmp_path_factory):
 
 def test_tensor_core_columns_are_widths_of_the_mma(lines):
     """N of one CTA's MMA (M = 128) is a multiple of 16, of a pair's (M = 256) one of 32; no row is lost to rounding up."""
-    rows = [tuple(int(v) for v in ln.split()) for ln in lines if not ln.startswith("step")]
+    rows = [tuple(int(v) for v in ln.split()) for ln in lines if ln[0].isdigit()]
     assert len(rows) == 2 * 257
     for pair, own, nx in rows:
         step = 32 if pair else 16
@@ -48,6 +56,15 @@ def test_steps(lines):
         if ln.startswith("step"):
             single, pair = (int(v) for v in ln.split()[2:])
             assert single % 16 == 0 and pair % 32 == 0, ln
+
+
+def test_row_tiles_hold_a_groups_rows(lines):
+    """Tiles of equal size up to the largest number of rows a call may have: none wider than the accumulator, none empty,
+    together all rows."""
+    cuts = [tuple(int(v) for v in ln.split()[1:]) for ln in lines if ln.startswith("cut")]
+    assert len(cuts) >= 50
+    for bn, rows, tiles, per in cuts:
+        assert 0 < per <= bn and per * (tiles - 1) < rows <= per * tiles, (bn, rows, tiles, per)
 
 
 def test_every_load_of_tensor_memory_has_a_wait_that_names_its_registers():
