@@ -707,8 +707,9 @@ typedef enum { CF_BF16 = 0, CF_FP16 = 1 } cf_dtype;  /* 16-bit operand types */
  * Accumulation is fp32 in tensor memory, in an order that depends on the
  * sizes alone: equal calls give equal bits.  An infinity or NaN in one group
  * reaches no other, in rows of no group none.
- * Supported: T >= 0, E in 0..1024 (either 0 is a no-op; wgrad with T = 0
- * writes zeros), N and K positive multiples of 8, no matrix aliasing an input
+ * Supported: T in 0..2^31 - 512, E in 0..1024 (either 0 is a no-op; wgrad with
+ * T = 0 writes zeros), N and K positive multiples of 8 up to 2^24 with
+ * N K < 2^39, less than 2^31 - 65536 tiles, no matrix aliasing an input
  * (but dX = Z); 16-byte aligned matrices and workspace.  Offsets that decrease
  * or leave [0, T] are clamped, and reported as CF_ERR_DEVICE_BOUNDS.
  * workspace (device) >= cf_grouped_gemm_workspace_size() bytes, any of the
@@ -771,9 +772,9 @@ CF_API cf_status cf_grouped_gemm_wgrad_ex(const void *X, const void *dY, const i
  *   adapters (device) int32 [S], each in 0..L-1, or -1 for the projection alone
  *   scale    (device) fp32 [L], or NULL for 1
  *   Y (device) `dtype` [T, N], written; rows of no request are not
- * Supported: T >= 0, S in 0..1024 (either 0 is a no-op), L >= 0, N and K
- * positive multiples of 8, R a multiple of 8 up to 128 (a smaller rank is
- * padded with zeros); Y not an input; 16-byte aligned.  An infinity or NaN in
+ * Supported: T, N, K and S as for cf_grouped_gemm (T or S 0 is a no-op), L in
+ * 0..2^24, R a multiple of 8 up to 128 (a smaller rank is padded with zeros);
+ * Y not an input; 16-byte aligned.  An infinity or NaN in
  * an adapter reaches the rows of its own requests only (an infinity in B as an
  * infinity or a NaN).  Indices outside -1..L-1 are taken as -1 and reported as
  * CF_ERR_DEVICE_BOUNDS, as are bad offsets.  Equal calls give equal bits.

@@ -1392,8 +1392,9 @@ cf_status grouped_sizes(int64_t T, int64_t N, int64_t K, int64_t groups, int dty
 // where they are wider than a tile.  Measured on a GB300 (about 1.8 GHz under load), besides what the device's plan needs
 // too (grouped_internal.h): copies arrive at 75 B per cycle and SM (43 where the matrix's rows are no multiples of 128
 // bytes: 2048 features 17.4 us, 2056 21.9), HBM gives the chip 3770 B per cycle; an epilogue takes 1500 cycles and 20 a
-// column, 900 more in a pair; the low-rank product of rows with adapters of their own 1000 cycles for 8 rows and 8 ranks.  Against every width and both CTA counts, timed over 180 random sizes, the choice
-// takes 4 % more time than the best one in the geometric mean.
+// column, 900 more in a pair; the low-rank product of rows with adapters of their own 1000 cycles for 8 rows and 8 ranks.
+// Against every width and both CTA counts, timed over 180 random sizes, the choice takes 4 % more time than the best one
+// in the geometric mean.
 // -------------------------------------------------------------------------
 constexpr double kPlanSms = 152;  // a GB300's, whatever device is current: the workspace size follows from this plan
 

@@ -26,27 +26,27 @@
 //    while tile i + 1 is multiplied; every wait is bounded.  The first two run
 //    their loops as whole warps and issue by an elected lane: a loop of one lane
 //    spent some 600 cycles a block on its own control flow (16384 rows over 8
-//    groups of 2048 x 8192: 351 us, now 308 to 320).
+//    groups of 2048 x 8192: 351 us, now 317).
 //  * CTA pairs (M = 256, cta_group::2) where there are tiles enough for them:
 //    each CTA stages its own 128 features and half of the rows, so a block costs
 //    an SM 32 KB of copies in place of 48 (single CTAs 356 us there).
 //  * Few tiles with a long contraction are divided among the SMs: pieces of fp32
 //    accumulators in the workspace, added in a fixed order by the last arriver.
 //
-// What bounds each form, and what it measured on a GB300 (in a CUDA graph):
-//     FORWARD  16384 rows, 8 groups of 2048 x 8192, GELU: the tensor pipe, 308 to 320 us (1.72 to 1.78 PFLOP/s);
+// What bounds each form, and what it measured on a GB300 in a CUDA graph, more than twice L2 between two uses of an input
+// (at 2070 MHz; in brackets over two seconds, where the power cap takes the long ones to 1560 MHz):
+//     FORWARD  16384 rows, 8 groups of 2048 x 8192, GELU: the tensor pipe, 317 us (1.73 PFLOP/s) [372, 1.48];
 //              250 rows, 32 groups of 2048 x 4096: HBM, 72 us (6.6 TB/s); 4099 rows, 64 groups of 1000 x 2056: HBM,
-//              47 us (5.4 TB/s); 2 rows, 8 groups of 1024 x 2048: latency, 6.8 us (launch 2, table 1.2, first copy 1,
+//              49 us (5.3 TB/s); 2 rows, 8 groups of 1024 x 2048: latency, 7.1 us (launch 2, table 1.2, first copy 1,
 //              16 blocks in pieces 1, joining them 1.5)
-//     DGRAD    16384 rows, 16 groups of 4096 x 2048, GELU': the tensor pipe, 169 to 181 us (1.52 to 1.63 PFLOP/s);
-//              333 rows, 12 groups of 520 x 1032: latency, 7.4 us
-//     WGRAD    16384 rows, 8 groups of 2048 x 8192: the tensor pipe, 318 to 343 us (1.60 to 1.73 PFLOP/s); 1003 rows,
-//              24 groups of 520 x 1032: its 600 epilogues of 256 columns, 13.8 us (2.1 TB/s; 16.2 with 32 columns at a
-//              time out of the accumulator)
-//     LORA     with its SHRINK, 8192 rows of 8 requests, 4096 x 4096, rank 64: the tensor pipe, 160 to 168 us (1.67 to
-//              1.75 PFLOP/s); one row, rank 16: 13.0 us, 64 requests of one row: 22.5 us (the chain X . A, join, H . B,
-//              join beside 33 MB of W); 1537 rows of 40 requests, 2048 x 2056, rank 24: 43 us (the chain, then row
-//              tiles that requests do not fill)
+//     DGRAD    16384 rows, 16 groups of 4096 x 2048, GELU': the tensor pipe, 191 to 200 us (1.38 to 1.44 PFLOP/s)
+//              [203, 1.36]; 333 rows, 12 groups of 520 x 1032: latency, 7.0 to 7.9 us
+//     WGRAD    16384 rows, 8 groups of 2048 x 8192: the tensor pipe, 326 us (1.69 PFLOP/s) [368, 1.50]; 1003 rows,
+//              24 groups of 520 x 1032: the epilogues of its 600 tiles, 14 us (2.1 TB/s)
+//     LORA     with its SHRINK, 8192 rows of 8 requests, 4096 x 4096, rank 64: the tensor pipe, 165 us (1.72 PFLOP/s)
+//              [184, 1.54]; one row, rank 16: 14.6 us, 64 requests of one row: 25 us (the chain X . A, join, H . B, join
+//              beside 33 MB of W); 1537 rows of 40 requests, 2048 x 2056, rank 24: 43 us (the chain, then row tiles
+//              that requests do not fill)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -802,8 +802,8 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
         const int most = KIND == GR_WGRAD ? 0 : min(of.z, nkc / kMinStretch);
         const int cols = KIND == GR_WGRAD ? a.bn : min(a.bn, of.w + 15);  // columns of a tile, about
         const int block = max(max(kMmaCycles20Columns * cols / 20, kMmaCyclesLeast), a.copy_cycles);
-        const int4 in = divide(kDivideCycles + kDivideCyclesColumn * cols, block, a.wait_cycles, block, nkc + most - 1, max(most, 1), units,
-                               stretch);
+        const int4 in = divide(kDivideCycles + kDivideCyclesColumn * cols, block, a.wait_cycles, block, nkc + most - 1,
+                               max(most, 1), units, stretch);
         const int adding = in.x + 1, least = in.y;  // no tile can be finished before
         const int whole = max(whole0, least);
         const int even = most >= 2 ? max(in.z, least) + adding : 1 << 30;

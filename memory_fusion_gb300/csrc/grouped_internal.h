@@ -21,8 +21,8 @@ constexpr int kGroupedMaxSmem = 232448;   // dynamic shared memory of a CTA (227
 constexpr int kGroupedMaxGroups = 1024;  // the group table lives in shared memory
 constexpr int kGroupedSplitTiles = 1024; // tiles whose contraction may be divided among CTAs
 constexpr int kGroupedWorkers = 160;     // CTAs that may hold a piece of a tile (a GB300 has 152 SMs)
-// Cycles of the cost models that the host's choice of tiles and the device's plan share (about 1.8 GHz under load): an MMA
-// block of 64 in the contraction takes 2.35 a column, and 290 at least (370 in a pair); dividing tiles (writing, adding,
+// Cycles that the host's choice of tiles and the device's plan both count with (about 1.8 GHz under load): an MMA block
+// of 64 in the contraction takes 2.35 a column, and 290 at least (370 in a pair); dividing tiles (writing, adding,
 // finishing pieces) 1500 and 70 a column.
 constexpr int kMmaCycles20Columns = 47, kMmaCyclesLeast = 290, kMmaCyclesLeastPair = 370;
 constexpr int kDivideCycles = 1500, kDivideCyclesColumn = 70;
@@ -40,8 +40,8 @@ constexpr int kLoraMaxRank = 128;        // one tile of features in the first pr
 __host__ __device__ constexpr int grouped_column_step(int kind, bool pair) {
     return pair ? (kind == GR_WGRAD ? 128 : 32) : 16;
 }
-// Rows of each of the `tiles` row tiles (two at least) that a group's rows are cut into evenly, in whole steps.  (Rows plus
-// tiles may pass 2^31.)
+// Rows of each of the `tiles` row tiles (two at least) that a group's rows are cut into evenly, in whole steps.  (Rows
+// plus tiles may pass 2^31.)
 __host__ __device__ constexpr int grouped_rows_per_tile(int rows, int tiles, int step) {
     return ((rows - 1) / tiles + step) & ~(step - 1);
 }
