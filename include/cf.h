@@ -74,7 +74,9 @@ typedef enum {
 
 typedef enum {
     CF_ACT_NONE = 0,
-    CF_ACT_GELU_TANH = 1           /* 0.5 x (1 + tanh(sqrt(2/pi)(x + 0.044715 x^3))) */
+    CF_ACT_GELU_TANH = 1,          /* 0.5 x (1 + tanh(sqrt(2/pi)(x + 0.044715 x^3))) */
+    CF_ACT_SILU = 2,               /* x / (1 + exp(-x)); cf_gemm_linear only */
+    CF_ACT_RELU = 3                /* max(x, 0), slope 0 at 0; cf_gemm_linear only */
 } cf_activation;
 
 /* Human-readable name of a status code (static storage, never NULL). */
@@ -682,7 +684,7 @@ CF_API cf_status cf_unfused_gemm_rowsoftmax(const void *X, const void *W, const 
 /* ------------------------------------------------------------------------ */
 /* Grouped GEMM: every group of rows has its own weights                     */
 /* ------------------------------------------------------------------------ */
-typedef enum { CF_BF16 = 0, CF_FP16 = 1 } cf_dtype;  /* 16-bit operand types */
+typedef enum { CF_BF16 = 0, CF_FP16 = 1, CF_FP32 = 2 } cf_dtype;  /* products: the 16-bit types */
 
 /* Y[r, :] = act(X[r, :] . W[e]) for the rows r in [offsets[e], offsets[e+1])
  *
@@ -793,6 +795,60 @@ CF_API cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *bias
                                  const float *scale, void *Y, int64_t T, int64_t N, int64_t K, int64_t S,
                                  int64_t L, int64_t R, cf_dtype dtype, void *workspace,
                                  size_t workspace_bytes, cf_stream_t stream, const cf_tuning *tuning);
+
+/* ------------------------------------------------------------------------ */
+/* Dense layer: bias, activation and residual in the product's epilogue       */
+/* ------------------------------------------------------------------------ */
+/* Y = act(X . W + bias) + R, the layers of a model that end in no norm.
+ *
+ * The stage-1 nodes of cf_gemm_fused_residual_norm without the reduction behind
+ * them ([sass2mlir] "Epilogue fusion - the core technique"), on the accumulator:
+ * nothing is rounded before Y (and Z) are.
+ *   X    (device) `dtype` [M, K]          W (device) `dtype` [K, N]
+ *   bias (device) fp32 [N] or NULL
+ *   R    (device) `dtype` [M, N] or NULL  added after the activation
+ *   Y    (device) `dtype` [M, N], written (round to nearest even); may be R
+ *   Z    (device) `dtype` [M, N] or NULL: receives X . W + bias, rounded, for
+ *        the gradient; the activation is applied to the unrounded value
+ *   act  CF_ACT_NONE, CF_ACT_GELU_TANH, CF_ACT_SILU or CF_ACT_RELU
+ * cf_gemm_linear_grad: of the gradient dY [M, N] of Y,
+ *   dZ = dY * act'(Z), dX = dZ . W^T [M, K], dW = X^T . dZ [K, N],
+ *   dbias = sum over the rows of dZ (fp32 [N]; of the unrounded dZ)
+ *   (R's is dY itself).  dX, dW and dbias may each be NULL: not wanted (X may
+ *   then be NULL without dW, W without dX).  With an activation Z and dZ
+ *   (`dtype` [M, N], written) are required, and dZ may be Z or dY; without one
+ *   both are NULL.  Up to three launches.
+ * Accumulation is fp32, in an order that depends on the sizes alone: equal
+ * calls give equal bits.
+ * Supported: M in 0..2^31 - 512 (M = 0 is a no-op; dW and dbias are then
+ * zeros), N and K positive multiples of 8 up to 2^24 with N K < 2^39, less than
+ * 2^31 - 65536 tiles; 16-byte aligned; no output aliasing an input but those
+ * named, or another output.
+ * workspace (device) >= cf_gemm_linear_workspace_size() bytes, either
+ * direction; zeroed once, one launch at a time, as for every call.  It may serve
+ * grouped and adapter calls in turn.
+ * Tuning fields used (_ex): those of cf_grouped_gemm_ex (both products of a
+ * gradient take them). */
+CF_API size_t cf_gemm_linear_workspace_size(int64_t M, int64_t N, int64_t K);
+
+CF_API cf_status cf_gemm_linear(const void *X, const void *W, const float *bias, const void *R, void *Y,
+                                void *Z, int64_t M, int64_t N, int64_t K, cf_dtype dtype, cf_activation act,
+                                void *workspace, size_t workspace_bytes, cf_stream_t stream);
+
+CF_API cf_status cf_gemm_linear_ex(const void *X, const void *W, const float *bias, const void *R, void *Y,
+                                   void *Z, int64_t M, int64_t N, int64_t K, cf_dtype dtype,
+                                   cf_activation act, void *workspace, size_t workspace_bytes,
+                                   cf_stream_t stream, const cf_tuning *tuning);
+
+CF_API cf_status cf_gemm_linear_grad(const void *dY, const void *X, const void *W, const void *Z, void *dZ,
+                                     void *dX, void *dW, float *dbias, int64_t M, int64_t N, int64_t K,
+                                     cf_dtype dtype, cf_activation act, void *workspace,
+                                     size_t workspace_bytes, cf_stream_t stream);
+
+CF_API cf_status cf_gemm_linear_grad_ex(const void *dY, const void *X, const void *W, const void *Z, void *dZ,
+                                        void *dX, void *dW, float *dbias, int64_t M, int64_t N, int64_t K,
+                                        cf_dtype dtype, cf_activation act, void *workspace,
+                                        size_t workspace_bytes, cf_stream_t stream, const cf_tuning *tuning);
 
 #ifdef __cplusplus
 }

@@ -28,6 +28,8 @@ CF_ERR_NO_DEVICE = 9
 
 CF_ACT_NONE = 0
 CF_ACT_GELU_TANH = 1
+CF_ACT_SILU = 2
+CF_ACT_RELU = 3
 
 
 class cf_tuning(ctypes.Structure):
@@ -170,6 +172,14 @@ _SIGS = {
                            _SZ, _P]),
     "cf_gemm_lora_ex": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_int,
                               _P, _SZ, _P, ctypes.POINTER(cf_tuning)]),
+    "cf_gemm_linear_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "cf_gemm_linear": (_ST, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _P, _SZ, _P]),
+    "cf_gemm_linear_ex": (_ST, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _P, _SZ, _P,
+                                ctypes.POINTER(cf_tuning)]),
+    "cf_gemm_linear_grad": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _P,
+                                  _SZ, _P]),
+    "cf_gemm_linear_grad_ex": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _P,
+                                     _SZ, _P, ctypes.POINTER(cf_tuning)]),
     "cf_stitch_powadd_softmax": (_ST, [_P, _P, _F, _P, _I64, _I64, _P, _SZ, _P]),
     "cf_stitch_powadd_softmax_ex": (_ST, [_P, _P, _F, _P, _I64, _I64, _P, _SZ, _P, ctypes.POINTER(cf_tuning)]),
 }
@@ -654,6 +664,7 @@ def stitch_powadd_softmax(A, w, p, *, out=None, workspace=None, stream=None, tun
 # ---------------------------------------------------------------------------
 CF_BF16 = 0
 CF_FP16 = 1
+CF_FP32 = 2
 
 
 def cf_grouped_gemm_workspace_size(T, N, K, E) -> int:
@@ -871,3 +882,124 @@ def gemm_lora(X, W, bias, A, B, offsets, adapters, *, scale=None, out=None, work
               _operand("scale", scale, (L,), torch.float32, dev))
     return _run("cf_gemm_lora", before, (T, N, K, S, L, R, dt), out, (T, N), dtype, dev, workspace,
                 cf_gemm_lora_workspace_size, (T, N, K, S, R), stream, tuning)
+
+
+# ---------------------------------------------------------------------------
+# dense layer
+# ---------------------------------------------------------------------------
+def cf_gemm_linear_workspace_size(M, N, K) -> int:
+    return lib().cf_gemm_linear_workspace_size(M, N, K)
+
+
+def cf_gemm_linear(X, W, bias, R, Y, Z, M, N, K, dtype, act, workspace, workspace_bytes, stream=None,
+                   tuning=None) -> int:
+    """Y = act(X . W + bias) + R; Z (or None) receives X . W + bias."""
+    L = lib()
+    if tuning is None:
+        return L.cf_gemm_linear(_ptr(X), _ptr(W), _ptr(bias), _ptr(R), _ptr(Y), _ptr(Z), M, N, K, dtype, act,
+                                _ptr(workspace), workspace_bytes, _stream(stream))
+    return L.cf_gemm_linear_ex(_ptr(X), _ptr(W), _ptr(bias), _ptr(R), _ptr(Y), _ptr(Z), M, N, K, dtype, act,
+                               _ptr(workspace), workspace_bytes, _stream(stream), _tun(tuning))
+
+
+def cf_gemm_linear_grad(dY, X, W, Z, dZ, dX, dW, dbias, M, N, K, dtype, act, workspace, workspace_bytes, stream=None,
+                        tuning=None) -> int:
+    """dZ = dY * act'(Z), dX = dZ . W^T, dW = X^T . dZ, dbias = column sums of dZ (each of the last three or None)."""
+    L = lib()
+    if tuning is None:
+        return L.cf_gemm_linear_grad(_ptr(dY), _ptr(X), _ptr(W), _ptr(Z), _ptr(dZ), _ptr(dX), _ptr(dW), _ptr(dbias),
+                                     M, N, K, dtype, act, _ptr(workspace), workspace_bytes, _stream(stream))
+    return L.cf_gemm_linear_grad_ex(_ptr(dY), _ptr(X), _ptr(W), _ptr(Z), _ptr(dZ), _ptr(dX), _ptr(dW), _ptr(dbias),
+                                    M, N, K, dtype, act, _ptr(workspace), workspace_bytes, _stream(stream),
+                                    _tun(tuning))
+
+
+_LINEAR_ACTS = {"none": CF_ACT_NONE, "gelu_tanh": CF_ACT_GELU_TANH, "silu": CF_ACT_SILU, "relu": CF_ACT_RELU}
+
+
+def _linear_act(act):
+    a = _LINEAR_ACTS.get(act)
+    if a is None:
+        raise ValueError(f"unknown activation {act!r}")
+    return a
+
+
+def _outputs(name, args, device, workspace, size, sizes, stream, tuning):
+    """name(*args(), workspace, its bytes, stream) on the operands' device, where args() makes the outputs that are not
+    given and returns the arguments in front of the workspace with the outputs; the outputs."""
+    import torch
+    index = device.index
+    if workspace is not None and not (workspace.get_device() == index and workspace.is_contiguous()):
+        raise ValueError(f"workspace is not a contiguous tensor on {device}")
+    if stream is not None and getattr(stream, "device", device) != device:
+        raise ValueError(f"stream is on {stream.device}, not on {device}")
+    if stream is not None or index != torch._C._cuda_getDevice():
+        with _launch_on(device, stream):
+            return _outputs(name, args, device, workspace, size, sizes, None, tuning)
+    before, outs = args()
+    if workspace is None:
+        workspace = new_workspace(size(*sizes), device)
+    last = (workspace.data_ptr(), workspace.nbytes, torch._C._cuda_getCurrentRawStream(index))
+    if tuning is None:
+        st = getattr(lib(), name)(*before, *last)
+    else:
+        st = getattr(lib(), name + "_ex")(*before, *last, ctypes.byref(tuning))
+    if st != CF_OK:
+        raise CfError(st, name)
+    return outs
+
+
+def _made(name, t, shape, dtype, device):
+    """An output: the given one, checked, or a new one."""
+    if t is None:
+        import torch
+        return torch.empty(shape, dtype=dtype, device=device)
+    _operand(name, t, shape, dtype, device)
+    return t
+
+
+def gemm_linear(X, W, bias=None, *, act="none", residual=None, preact=None, out=None, workspace=None, stream=None,
+                tuning=None):
+    """Y = act(X @ W + bias) + residual; X [M, K], W [K, N] and residual [M, N] bf16 or fp16 CUDA tensors, bias fp32
+    [N]; act "none", "gelu_tanh", "silu" or "relu".  `preact` ([M, N]) receives X @ W + bias for gemm_linear_grad.
+    out may be residual."""
+    import torch
+    (M, K), dev, dtype, dt = _first("X", X, 2)
+    a = _linear_act(act)
+    N = _sizes("W", W, 2)[1]
+    before = (X.data_ptr(), _operand("W", W, (K, N), dtype, dev), _operand("bias", bias, (N,), torch.float32, dev),
+              _operand("residual", residual, (M, N), dtype, dev))
+    between = (_operand("preact", preact, (M, N), dtype, dev), M, N, K, dt, a)
+    return _run("cf_gemm_linear", before, between, out, (M, N), dtype, dev, workspace, cf_gemm_linear_workspace_size,
+                (M, N, K), stream, tuning)
+
+
+def gemm_linear_grad(dY, X, W, *, act="none", preact=None, input=True, weight=True, bias=True, dz=None, out=None,
+                     workspace=None, stream=None, tuning=None):
+    """(dX, dW, dbias) of Y = act(X @ W + bias) + residual for the gradient dY [M, N] of Y (the residual's own is dY);
+    input, weight and bias say which are wanted (None in the place of the others; X may be None without weight, W
+    without input).  `preact` is what gemm_linear kept, needed with an activation; `dz` ([M, N], made where not given)
+    then receives dY * act'(preact), and may be preact or dY.  dbias is fp32.  `out`: three outputs, None for new ones."""
+    import torch
+    (M, N), dev, dtype, dt = _first("dY", dY, 2)
+    a = _linear_act(act)
+    if X is None and W is None:
+        raise ValueError("neither X nor W is given")
+    K = _sizes("X", X, 2)[1] if X is not None else _sizes("W", W, 2)[0]
+    if (weight and X is None) or (input and W is None):
+        raise ValueError("the weight's gradient needs X, the input's needs W")
+    if (a != CF_ACT_NONE) != (preact is not None) or (a == CF_ACT_NONE and dz is not None):
+        raise ValueError("preact goes with an activation, and so does dz")
+    given = (None, None, None) if out is None else out
+    x, w = _operand("X", X, (M, K), dtype, dev), _operand("W", W, (K, N), dtype, dev)
+    z = _operand("preact", preact, (M, N), dtype, dev)
+
+    def args():
+        dx = _made("out[0]", given[0], (M, K), dtype, dev) if input else None
+        dw = _made("out[1]", given[1], (K, N), dtype, dev) if weight else None
+        db = _made("out[2]", given[2], (N,), torch.float32, dev) if bias else None
+        d = _made("dz", dz, (M, N), dtype, dev) if a != CF_ACT_NONE else None
+        return (dY.data_ptr(), x, w, z, _ptr(d), _ptr(dx), _ptr(dw), _ptr(db), M, N, K, dt, a), (dx, dw, db)
+
+    return _outputs("cf_gemm_linear_grad", args, dev, workspace, cf_gemm_linear_workspace_size, (M, N, K), stream,
+                    tuning)

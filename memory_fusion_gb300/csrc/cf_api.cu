@@ -1855,3 +1855,156 @@ extern "C" cf_status cf_gemm_lora(const void *X, const void *W, const float *bia
     return cf_gemm_lora_ex(X, W, bias, A, B, offsets, adapters, scale, Y, T, N, K, S, L, R, dtype, workspace,
                            workspace_bytes, stream, nullptr);
 }
+
+// -------------------------------------------------------------------------
+// Dense layer: the grouped kernels' forward with one group of all rows, a bias before the activation and a residual
+// behind it; its gradients are dZ = dY * act'(Z) with the column sums, and those kernels' other two directions on dZ.
+// -------------------------------------------------------------------------
+namespace {
+
+cf_status linear_device(cf::DeviceInfo *dev) {
+    if (!cf::current_device_info(dev)) return CF_ERR_NO_DEVICE;
+    return dev->cc_major == 10 && dev->cc_minor == 3 ? CF_OK : CF_ERR_NO_DEVICE;
+}
+
+bool linear_act(int act) { return act >= CF_ACT_NONE && act <= CF_ACT_RELU; }
+
+}  // namespace
+
+extern "C" size_t cf_gemm_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N <= 0 || K <= 0) return kGroupedHead;
+    cf::LinearSumsArgs sums;
+    plan_linear_sums(M, N, int(kPlanSms), &sums);
+    const size_t parts = sums.chunks > 1 ? size_t(sums.chunks) * size_t(N) * 4 : 0;
+    return std::max(cf_grouped_gemm_workspace_size(M, N, K, 1), kGroupedHead + parts);
+}
+
+extern "C" cf_status cf_gemm_linear_ex(const void *X, const void *W, const float *bias, const void *R, void *Y, void *Z,
+                                       int64_t M, int64_t N, int64_t K, cf_dtype dtype, cf_activation act,
+                                       void *workspace, size_t workspace_bytes, cf_stream_t stream,
+                                       const cf_tuning *tuning) {
+    cf_status st = grouped_sizes(M, N, K, 1, int(dtype));
+    if (st != CF_OK) return st;
+    if (!linear_act(int(act)) || !workspace) return CF_ERR_INVALID_ARG;
+    if (M == 0) return CF_OK;
+    if (!X || !W || !Y) return CF_ERR_INVALID_ARG;
+    for (const void *p : {X, W, R, static_cast<const void *>(bias), static_cast<const void *>(Y),
+                          static_cast<const void *>(Z), static_cast<const void *>(workspace)})
+        if (!aligned16(p)) return CF_ERR_MISALIGNED;
+    if (Y == X || Y == W || Z == Y || (Z && (Z == X || Z == W || Z == R))) return CF_ERR_INVALID_ARG;
+    if (workspace_bytes < cf_gemm_linear_workspace_size(M, N, K)) return CF_ERR_WORKSPACE_TOO_SMALL;
+    cf_tuning tz;
+    cf_tuning_default(&tz);
+    const cf_tuning &t = tuning ? *tuning : tz;
+    cf::DeviceInfo dev;
+    st = linear_device(&dev);
+    if (st != CF_OK) return st;
+    cf::GroupedArgs a;
+    grouped_args(&a, M, N, K, 0, 1, int(dtype), nullptr, workspace, t);
+    int ctas, smem;
+    st = plan_grouped(cf::GR_LINEAR, M, N, K, 0, 1, 0, t, dev, workspace, 0,
+                      static_cast<unsigned char *>(workspace) + kGroupedHead, workspace_bytes - kGroupedHead, &a, &ctas,
+                      &smem);
+    if (st != CF_OK) return st;
+    if (!make_tmap_features(&a.tmap_a, &a.a_split, W, 1, uint64_t(K), uint64_t(N), a.a_blocks) ||
+        !make_tmap_rows(&a, X, M, K))
+        return CF_ERR_CUDA;
+    a.bias = bias;
+    a.resid = R;
+    a.out = Y;
+    a.preact = Z;
+    a.act = int(act);
+    return launch_grouped_checked(cf::GR_LINEAR, a, ctas, smem, t, stream);
+}
+
+extern "C" cf_status cf_gemm_linear(const void *X, const void *W, const float *bias, const void *R, void *Y, void *Z,
+                                    int64_t M, int64_t N, int64_t K, cf_dtype dtype, cf_activation act, void *workspace,
+                                    size_t workspace_bytes, cf_stream_t stream) {
+    return cf_gemm_linear_ex(X, W, bias, R, Y, Z, M, N, K, dtype, act, workspace, workspace_bytes, stream, nullptr);
+}
+
+extern "C" cf_status cf_gemm_linear_grad_ex(const void *dY, const void *X, const void *W, const void *Z, void *dZ,
+                                            void *dX, void *dW, float *dbias, int64_t M, int64_t N, int64_t K,
+                                            cf_dtype dtype, cf_activation act, void *workspace, size_t workspace_bytes,
+                                            cf_stream_t stream, const cf_tuning *tuning) {
+    cf_status st = grouped_sizes(M, N, K, 1, int(dtype));
+    if (st != CF_OK) return st;
+    if (!linear_act(int(act)) || !workspace) return CF_ERR_INVALID_ARG;
+    const bool acted = act != CF_ACT_NONE;
+    if (M > 0 && (!dY || (dX && !W) || (dW && !X) || (acted && (!Z || !dZ)))) return CF_ERR_INVALID_ARG;
+    if (!acted && (Z || dZ)) return CF_ERR_INVALID_ARG;  // dZ is dY
+    for (const void *p : {dY, X, W, Z, static_cast<const void *>(dZ), static_cast<const void *>(dX),
+                          static_cast<const void *>(dW), static_cast<const void *>(dbias),
+                          static_cast<const void *>(workspace)})
+        if (!aligned16(p)) return CF_ERR_MISALIGNED;
+    // dZ may take dY's place or Z's; dX and dW are of whole products, whose operands have to stay
+    if (dZ && (dZ == X || dZ == W)) return CF_ERR_INVALID_ARG;
+    for (const void *out : {static_cast<const void *>(dX), static_cast<const void *>(dW)})
+        if (out && (out == dY || out == X || out == W || out == Z || out == dZ)) return CF_ERR_INVALID_ARG;
+    if (dX && dX == dW) return CF_ERR_INVALID_ARG;
+    if (workspace_bytes < cf_gemm_linear_workspace_size(M, N, K)) return CF_ERR_WORKSPACE_TOO_SMALL;
+    cf_tuning tz;
+    cf_tuning_default(&tz);
+    const cf_tuning &t = tuning ? *tuning : tz;
+    cf::DeviceInfo dev;
+    st = linear_device(&dev);
+    if (st != CF_OK) return st;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0) {  // every sum is empty
+        cudaError_t e = cudaSuccess;
+        if (dW) e = cudaMemsetAsync(dW, 0, size_t(K) * size_t(N) * 2, cs);
+        if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, size_t(N) * 4, cs);
+        return e == cudaSuccess ? CF_OK : cuda_fail(e);
+    }
+    unsigned char *const part = static_cast<unsigned char *>(workspace) + kGroupedHead;
+    const size_t room = workspace_bytes - kGroupedHead;
+    // plans first: nothing is launched unless everything can be
+    cf::GroupedArgs gx, gw;
+    int gx_ctas = 0, gx_smem = 0, gw_ctas = 0, gw_smem = 0;
+    const void *g = acted ? dZ : dY;
+    if (dX) {
+        grouped_args(&gx, M, K, N, 0, 1, int(dtype), nullptr, workspace, t);
+        st = plan_grouped(cf::GR_DGRAD, M, K, N, 0, 1, 0, t, dev, workspace, 0, part, room, &gx, &gx_ctas, &gx_smem);
+        if (st != CF_OK) return st;
+        if (!make_tmap_features_t(&gx.tmap_a, W, 1, uint64_t(K), uint64_t(N)) || !make_tmap_rows(&gx, g, M, N))
+            return CF_ERR_CUDA;
+        gx.out = dX;
+    }
+    if (dW) {
+        grouped_args(&gw, M, K, 0, N, 1, int(dtype), nullptr, workspace, t);
+        st = plan_grouped(cf::GR_WGRAD, M, K, 0, N, 1, 0, t, dev, workspace, 0, part, room, &gw, &gw_ctas, &gw_smem);
+        if (st != CF_OK) return st;
+        if (!make_tmap_blocks(&gw.tmap_a, &gw.a_split, X, uint64_t(M), uint64_t(K), uint32_t(gw.a_blocks)) ||
+            !make_tmap_blocks(&gw.tmap_b, &gw.b_split, g, uint64_t(M), uint64_t(N), staged_columns(gw) / 64))
+            return CF_ERR_CUDA;
+        gw.out = dW;
+    }
+    if (acted || dbias) {
+        cf::LinearSumsArgs sums;
+        plan_linear_sums(M, N, std::min(dev.sm_count, int(kPlanSms)), &sums);
+        sums.dy = dY;
+        sums.z = acted ? Z : nullptr;
+        sums.dz = acted ? dZ : nullptr;
+        sums.sums = dbias;
+        sums.partials = reinterpret_cast<float *>(part);
+        sums.counters = reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(workspace) + cf::kErrBytes +
+                                                     2 * kGroupedCounterBytes);
+        sums.fp16 = dtype == CF_FP16;
+        sums.act = int(act);
+        const cudaError_t e = cf::launch_linear_sums(sums, t.disable_pdl == 0, cs);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    if (dX) {
+        st = launch_grouped_checked(cf::GR_DGRAD, gx, gx_ctas, gx_smem, t, stream);
+        if (st != CF_OK) return st;
+    }
+    return dW ? launch_grouped_checked(cf::GR_WGRAD, gw, gw_ctas, gw_smem, t, stream) : CF_OK;
+}
+
+extern "C" cf_status cf_gemm_linear_grad(const void *dY, const void *X, const void *W, const void *Z, void *dZ, void *dX,
+                                         void *dW, float *dbias, int64_t M, int64_t N, int64_t K, cf_dtype dtype,
+                                         cf_activation act, void *workspace, size_t workspace_bytes,
+                                         cf_stream_t stream) {
+    return cf_gemm_linear_grad_ex(dY, X, W, Z, dZ, dX, dW, dbias, M, N, K, dtype, act, workspace, workspace_bytes,
+                                  stream, nullptr);
+}

@@ -4,6 +4,7 @@
 //     WGRAD    dW_g = X_g^T . dY_g            a sum over the group's rows
 //     SHRINK   H = scale[a] * X_g . A[a]      groups are requests, a their adapter
 //     LORA     Y = X . W + bias + H . B[a]    the shared projection with the adapters' second product
+//     LINEAR   Y = act(X . W + bias) + R      one group of all rows: a dense layer
 //
 // Design:
 //  * Features are the accumulator's lanes and rows of the batch its columns:
@@ -56,6 +57,7 @@
 #include <cstdint>
 
 #include "../../include/cf.h"
+#include "activations.cuh"
 #include "cf_internal.h"
 #include "grouped_internal.h"
 #include "ptx.cuh"
@@ -473,22 +475,6 @@ struct Walk {
     __device__ int slot_of(int w, int u0) const { return plan.ways != 0 || unit_of(w) >= u0 ? 0 : 1; }
 };
 
-// GELU in the tanh form is z * p with p = 1 / (1 + exp(-2u)), u = sqrt(2/pi)(z + 0.044715 z^3):
-// no cancellation in the left tail, where 1 + tanh(u) would lose every digit
-__device__ __forceinline__ float gelu_p(float z) {
-    const float u = 0.7978845608028654f * fmaf(0.044715f * z, z * z, z);
-    return __fdividef(1.f, 1.f + ptx::ex2_approx(-2.885390081777927f * u));
-}
-__device__ __forceinline__ float gelu(float z) { return z * gelu_p(z); }
-// d/dz of that: p + 2 z p (1 - p) u'.  Beyond |z| = 12, p is 0 or 1 to fp32 and the second term
-// vanishes; the clamp keeps z^2 finite there (and a NaN stays one)
-__device__ __forceinline__ float gelu_slope(float z) {
-    const float c = fabsf(z) > 12.f ? copysignf(12.f, z) : z;
-    const float p = gelu_p(c);
-    const float du = 0.7978845608028654f * fmaf(0.134145f * c, c, 1.f);
-    return fmaf(2.f * c * p * (1.f - p), du, p);
-}
-
 __device__ __forceinline__ uint16_t to16(float v, bool fp16) {
     return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
@@ -650,11 +636,11 @@ __device__ __forceinline__ void turned(float (&x)[8], const float *stg, int lane
     x[4] = h.x, x[5] = h.y, x[6] = h.z, x[7] = h.w;
 }
 
-// the pieces of the pre-activation's fragment at column c of the tile (zeros outside)
-__device__ __forceinline__ void load_fragment(uint4 (&z)[4], const GroupedArgs &a, const Tile &w, int c, int q,
-                                              int lane, bool ok) {
+// the pieces of a fragment of `from` (laid out as the output) at column c of the tile (zeros outside)
+__device__ __forceinline__ void load_fragment(uint4 (&z)[4], const void *from, const GroupedArgs &a, const Tile &w,
+                                              int c, int q, int lane, bool ok) {
     const int f = w.f0 + q * 32 + (lane & 3) * 8;
-    const uint16_t *p = static_cast<const uint16_t *>(a.preact) + size_t(w.col0 + c + (lane >> 2)) * a.F + f;
+    const uint16_t *p = static_cast<const uint16_t *>(from) + size_t(w.col0 + c + (lane >> 2)) * a.F + f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         z[i] = ok && f < a.F && c + (lane >> 2) + 8 * i < w.n
@@ -910,7 +896,11 @@ __device__ __forceinline__ void finish_row(const GroupedArgs &a, const Tile &w, 
         return;
     }
     const size_t at = size_t(row) * a.F + f;
-    if (KIND == GR_FORWARD && a.preact)
+    if ((KIND == GR_LORA || KIND == GR_LINEAR) && a.bias) {
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(a.bias + f));
+        s[0] += b.x, s[1] += b.y, s[2] += b.z, s[3] += b.w;
+    }
+    if ((KIND == GR_FORWARD || KIND == GR_LINEAR) && a.preact)
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.preact) + at) =
             make_uint2(pack16(s[0], s[1], fp16), pack16(s[2], s[3], fp16));
     if (KIND == GR_FORWARD && a.act) {
@@ -923,9 +913,14 @@ __device__ __forceinline__ void finish_row(const GroupedArgs &a, const Tile &w, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] *= gelu_slope(from16(uint16_t(zw[i / 2] >> ((i & 1) * 16)), fp16));
     }
-    if (KIND == GR_LORA && a.bias) {
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(a.bias + f));
-        s[0] += b.x, s[1] += b.y, s[2] += b.z, s[3] += b.w;
+    if constexpr (KIND == GR_LINEAR) {
+        activate(s, a.act);
+        if (a.resid) {
+            const uint2 r = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.resid) + at);
+            const uint32_t rw[2] = {r.x, r.y};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] += from16(uint16_t(rw[i / 2] >> ((i & 1) * 16)), fp16);
+        }
     }
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
         make_uint2(pack16(s[0], s[1], fp16), pack16(s[2], s[3], fp16));
@@ -1442,7 +1437,7 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
     }
     // (LORA has not waited itself: nothing that another launch may have written is read through L1 before it has)
     for (int i = threadIdx.x; i <= a.groups; i += kThreads) {
-        tab.off[i] = __ldcg(a.offsets + i);
+        tab.off[i] = a.offsets ? __ldcg(a.offsets + i) : i * a.T;  // none: one group of all rows
         if constexpr (KIND == GR_SHRINK || KIND == GR_LORA)
             if (i < a.groups) tab.ad[i] = __ldcg(a.windex + i);
     }
@@ -1590,9 +1585,11 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
         if constexpr (KIND == GR_SHRINK) shrink_short(a, tab, reinterpret_cast<float *>(smem_raw + L.stg), misc + 4);
         for (int tile = 0; e < kEpiWarps && walk.next(w); ++tile) {
             const uint32_t buf = uint32_t(tile & 1), tph = (uint32_t(tile) >> 1) & 1u;
-            uint4 zv[4];  // DGRAD: the next fragment's pre-activations, on their way before the accumulator is ready
+            uint4 zv[4];  // the next fragment's pre-activations (DGRAD) or residuals (LINEAR), on their way before the accumulator is ready
             if constexpr (KIND == GR_DGRAD)
-                if (a.preact && half * 32 < w.n && w.whole()) load_fragment(zv, a, w, half * 32, q, lane, true);
+                if (a.preact && half * 32 < w.n && w.whole()) load_fragment(zv, a.preact, a, w, half * 32, q, lane, true);
+            if constexpr (KIND == GR_LINEAR)
+                if (a.resid && half * 32 < w.n && w.whole()) load_fragment(zv, a.resid, a, w, half * 32, q, lane, true);
             // LORA, a tile of several requests: this worker adds the low-rank product of every parts-th eight rows
             int parts = 0, part = 0;
             if constexpr (KIND == GR_LORA) {
@@ -1728,8 +1725,8 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                 }
                 if (over && ok) report_range(a);
             }
-            float bias[4] = {0.f, 0.f, 0.f, 0.f};  // LORA: of a fragment's features in blocks
-            if constexpr (KIND == GR_LORA) {
+            float bias[4] = {0.f, 0.f, 0.f, 0.f};  // of a fragment's features in blocks
+            if constexpr (KIND == GR_LORA || KIND == GR_LINEAR) {
                 const int fb = w.f0 + q * 32 + (lane >> 2);
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
@@ -1760,7 +1757,7 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                     store_columns(a, w, c, stg, q, lane, ok);
                 }
             }
-            constexpr bool kFragments = KIND == GR_FORWARD || KIND == GR_DGRAD || KIND == GR_LORA;
+            constexpr bool kFragments = KIND == GR_FORWARD || KIND == GR_DGRAD || KIND == GR_LORA || KIND == GR_LINEAR;
             for (int c = half * 32; kFragments && c < w.n; c += 64) {
                 uint32_t v[32];
                 const int cols = min(32, w.n - c);
@@ -1809,7 +1806,7 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                             uint32_t z[16];
                             fr.load(zv, z);
                             if (c + 64 < w.n)  // the next fragment's, while this one is worked on
-                                load_fragment(zv, a, w, c + 64, q, lane, ok);
+                                load_fragment(zv, a.preact, a, w, c + 64, q, lane, ok);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
                                 const int j = Fragment::pair(i / 8, i / 2 % 4) + i % 2;
@@ -1825,11 +1822,27 @@ __global__ void __maxnreg__(registers_of(KIND)) grouped_kernel(const __grid_cons
                             for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(gelu(__uint_as_float(v[j])));
                         }
                     }
-                    if constexpr (KIND == GR_LORA) {
+                    if constexpr (KIND == GR_LORA || KIND == GR_LINEAR) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             const int j = Fragment::pair(i / 8, i / 2 % 4) + i % 2;
                             v[j] = __float_as_uint(__uint_as_float(v[j]) + bias[i / 2 % 4]);
+                        }
+                    }
+                    if constexpr (KIND == GR_LINEAR) {
+                        if (a.preact) fr.store_rounded(a.preact, v, fp16);
+                        activate(v, a.act);
+                        if (a.resid) {
+                            uint32_t r[16];
+                            fr.load(zv, r);
+                            if (c + 64 < w.n)  // the next fragment's, while this one is worked on
+                                load_fragment(zv, a.resid, a, w, c + 64, q, lane, ok);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const int j = Fragment::pair(i / 8, i / 2 % 4) + i % 2;
+                                v[j] = __float_as_uint(__uint_as_float(v[j]) +
+                                                       from16(uint16_t(r[i / 2] >> (i % 2 * 16)), fp16));
+                            }
                         }
                     }
                     fr.store_rounded(a.out, v, fp16);
@@ -1863,6 +1876,7 @@ void *kernel_for(int kind) {
         case GR_WGRAD: return reinterpret_cast<void *>(&grouped_kernel<GR_WGRAD, kPair>);
         case GR_SHRINK: return kPair ? nullptr : reinterpret_cast<void *>(&grouped_kernel<GR_SHRINK, false>);
         case GR_LORA: return reinterpret_cast<void *>(&grouped_kernel<GR_LORA, kPair>);
+        case GR_LINEAR: return reinterpret_cast<void *>(&grouped_kernel<GR_LINEAR, kPair>);
         default: return nullptr;
     }
 }

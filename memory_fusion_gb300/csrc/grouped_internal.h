@@ -15,6 +15,7 @@ enum GroupedKind : int {
     GR_WGRAD = 2,    // dW_g = X_g^T . dY_g
     GR_SHRINK = 3,   // H = scale[a] * X_g . A_a (adapters: groups are requests), as two 16-bit parts
     GR_LORA = 4,     // Y = X . W + bias + H . B_a
+    GR_LINEAR = 5,   // Y = act(X . W + bias) + R: one group of all rows, no offsets
 };
 
 constexpr int kGroupedMaxSmem = 232448;   // dynamic shared memory of a CTA (227 KB)
@@ -59,11 +60,12 @@ struct GroupedArgs {
     CUtensorMap tmap_h;    // LORA: H, as tmap_b
     int a_blocks;          // 64-feature blocks staged: 1 where there are no more than 64 features, else 2
     int a_split, b_split;  // 1: rows of 64-column blocks do not tile the matrix, so one block a copy (a length % 64)
-    const int32_t *offsets;  // [groups + 1] rows of each group (LORA: of each request)
+    const int32_t *offsets;  // [groups + 1] rows of each group (LORA: of each request); null: one group of all rows
     const int32_t *windex;   // SHRINK, LORA: [groups] adapter of each request, -1 for none
     void *out;               // Y / dX / dW / H [T, 2, rank]
-    void *preact;            // FORWARD: Z written; DGRAD: Z read; or null
-    const float *bias;       // LORA: [F] or null
+    void *preact;            // FORWARD, LINEAR: Z written; DGRAD: Z read; or null
+    const void *resid;       // LINEAR: R [T, F] or null
+    const float *bias;       // LORA, LINEAR: [F] or null
     const float *scale;      // SHRINK: [nweights] or null
     const void *low;         // LORA: H [T, 2, rank] 16-bit, upper parts and rests
     int after_shrink;        // LORA: the launch before is the SHRINK that makes H (it waits for what came before it)
@@ -84,7 +86,7 @@ struct GroupedArgs {
     int rank;                // LORA
     int long_rows;           // LORA: rows from which a request has tiles of its own
     int fp16;                // 16-bit type of every operand: 0 bf16, 1 fp16
-    int act;                 // FORWARD: 1 = GELU(tanh)
+    int act;                 // FORWARD, LINEAR: the cf_activation
     int bn;                  // columns of one accumulator tile (16, 32, 64, 128 or 256)
     int stages;
     int copy_cycles;         // what a block's copies take
@@ -96,5 +98,22 @@ struct GroupedArgs {
 
 int grouped_smem_bytes(int kind, bool pair, int stages, int bn, int groups, int a_blocks);
 cudaError_t launch_grouped(int kind, const GroupedArgs &a, int ctas, int smem, bool pdl, cudaStream_t stream);
+
+// dZ = dY * act'(Z) and the column sums of dZ (linear_grad.cu); rows [rows, cols] of 16 bits, cols a multiple of 8
+struct LinearSumsArgs {
+    const void *dy, *z;  // z: null without an activation
+    void *dz;            // null: not wanted (no activation)
+    float *sums;         // [cols] or null
+    float *partials;     // [chunks][cols]
+    uint32_t *counters;  // of each strip: chunks arrived, zero between launches
+    int64_t rows;
+    int cols, fp16, act;
+    int strips, chunks;
+    int64_t rows_per_chunk;
+};
+constexpr int kLinearStrip = 256;  // columns of a strip
+// strips and chunks of rows for a device of `sms` SMs
+void plan_linear_sums(int64_t rows, int64_t cols, int sms, LinearSumsArgs *a);
+cudaError_t launch_linear_sums(const LinearSumsArgs &a, bool pdl, cudaStream_t stream);
 
 }  // namespace cf

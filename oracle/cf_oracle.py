@@ -76,6 +76,15 @@ import math
 import numpy as np
 
 __all__ = [
+    "activation",
+    "activation_slope",
+    "gemm_linear",
+    "gemm_linear_grad",
+    "norm_rows",
+    "block_norms",
+    "block_norms_grad",
+    "logprobs",
+    "logprobs_grad",
     "gelu_tanh_slope",
     "grouped_gemm",
     "grouped_gemm_dgrad",
@@ -497,3 +506,161 @@ def gemm_lora(X, W, bias, A, B, offsets, adapters, scale=None) -> np.ndarray:
         if a >= 0:
             Y[lo:hi] += (1.0 if scale is None else float(scale[a])) * ((X[lo:hi] @ _f64(A[a])) @ _f64(B[a]))
     return Y
+
+
+# ---------------------------------------------------------------------------
+# dense layer
+# ---------------------------------------------------------------------------
+def _logistic(z) -> np.ndarray:
+    return 0.5 * (1.0 + np.tanh(0.5 * _f64(z)))
+
+
+def activation(act: str, z) -> np.ndarray:
+    z = _f64(z)
+    if act == "gelu_tanh":
+        return gelu_tanh(z)
+    if act == "silu":
+        return z * _logistic(z)
+    return np.where(z > 0.0, z, 0.0) if act == "relu" else z.copy()
+
+
+def activation_slope(act: str, z) -> np.ndarray:
+    """d/dz of it; the slope of ReLU at 0 is 0."""
+    z = _f64(z)
+    if act == "gelu_tanh":
+        return gelu_tanh_slope(z)
+    if act == "silu":
+        p = _logistic(z)
+        return p * (1.0 + z * (1.0 - p))
+    return (z > 0.0).astype(np.float64) if act == "relu" else np.ones_like(z)
+
+
+def gemm_linear(X, W, bias=None, *, act: str = "none", residual=None):
+    """(Y, Z) with Z = X.W + bias and Y = act(Z) + residual."""
+    Z = _f64(X) @ _f64(W) + (0.0 if bias is None else _f64(bias))
+    return activation(act, Z) + (0.0 if residual is None else _f64(residual)), Z
+
+
+def gemm_linear_grad(dY, X, W, *, act: str = "none", preact=None):
+    """(dX, dW, dbias): dZ = dY act'(Z), dX = dZ.W^T, dW = X^T.dZ, dbias = sum over the rows of dZ."""
+    dZ = _f64(dY) if act == "none" else _f64(dY) * activation_slope(act, preact)
+    return dZ @ _f64(W).T, _f64(X).T @ dZ, dZ.sum(0)
+
+
+# ---------------------------------------------------------------------------
+# norms before and after a block
+# ---------------------------------------------------------------------------
+def norm_rows(kind: str, t, eps: float):
+    """(normalised rows, 1 / what they were divided by); kind "none", "rms" or "layer"."""
+    t = _f64(t)
+    if kind == "none":
+        return t, np.ones((t.shape[0], 1))
+    c = t - t.mean(1, keepdims=True) if kind == "layer" else t
+    r = 1.0 / np.sqrt((c * c).mean(1, keepdims=True) + float(eps))
+    return c * r, r
+
+
+def _gate_rows(gate, rows: int):
+    return 1.0 if gate is None else np.repeat(_f64(gate), rows // len(gate), axis=0)
+
+
+def _affine(t, weight, bias):
+    return t * (1.0 if weight is None else _f64(weight)) + (0.0 if bias is None else _f64(bias))
+
+
+def block_norms(h, x, *, post="none", post_weight=None, post_bias=None, gate=None, scale=1.0, alpha=1.0, pre="none",
+                pre_weight=None, pre_bias=None, eps: float = 1e-5):
+    """(x', y): x' = alpha x + scale gate Post(h), y = Pre(x'); x may be None (0); gate [G, N], G a divisor of the
+    rows, which share a gate in equal runs."""
+    h = _f64(h)
+    p = _affine(norm_rows(post, h, eps)[0], post_weight, post_bias)
+    out = float(scale) * _gate_rows(gate, len(h)) * p + (0.0 if x is None else float(alpha) * _f64(x))
+    return out, _affine(norm_rows(pre, out, eps)[0], pre_weight, pre_bias)
+
+
+def _norm_grad(kind: str, hat, r, g):
+    if kind == "none":
+        return g
+    d = g - hat * (g * hat).mean(1, keepdims=True)
+    return r * (d - g.mean(1, keepdims=True) if kind == "layer" else d)
+
+
+def block_norms_grad(dy, dx_out, h, x_out, *, post="none", post_weight=None, post_bias=None, gate=None, scale=1.0,
+                     alpha=1.0, pre="none", pre_weight=None, eps: float = 1e-5) -> dict:
+    """Gradients of block_norms for the gradients dy of y and dx_out of x' (either may be None): h, x, gate,
+    post_weight, post_bias, pre_weight, pre_bias."""
+    h, xo = _f64(h), _f64(x_out)
+    rows = len(h)
+    dx = np.zeros_like(xo) if dx_out is None else _f64(dx_out).copy()
+    out = {}
+    if dy is not None:
+        hat, r = norm_rows(pre, xo, eps)
+        out["pre_weight"], out["pre_bias"] = (_f64(dy) * hat).sum(0), _f64(dy).sum(0)
+        dx += _norm_grad(pre, hat, r, _f64(dy) * (1.0 if pre_weight is None else _f64(pre_weight)))
+    out["x"] = float(alpha) * dx
+    hat, r = norm_rows(post, h, eps)
+    dp = float(scale) * dx
+    if gate is not None:
+        out["gate"] = (dp * _affine(hat, post_weight, post_bias)).reshape(len(gate), -1, h.shape[1]).sum(1)
+    dp = dp * _gate_rows(gate, rows)
+    out["post_weight"], out["post_bias"] = (dp * hat).sum(0), dp.sum(0)
+    out["h"] = _norm_grad(post, hat, r, dp * (1.0 if post_weight is None else _f64(post_weight)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# log probabilities of given tokens
+# ---------------------------------------------------------------------------
+def logprobs(logits, targets=None, *, scale: float = 1.0, top: int = 0):
+    """dict of logprob, lse, entropy, top_logprobs, top_ids of softmax(scale logits).
+
+    A target of -1 has logprob 0.  A row of nothing but -inf has lse and logprob -inf and entropy 0; one with a NaN or
+    +inf has NaNs.  The top ids are by logit, equal ones by id; a NaN counts as the largest."""
+    raw = _f64(logits)
+    z = raw * float(scale)
+    rows = np.arange(len(z))
+    with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
+        m = z.max(1, keepdims=True)
+        bad = ~(m < np.inf)[:, 0]
+        none = (m == -np.inf)[:, 0]
+        d = z - np.where(none[:, None], 0.0, m)
+        e = np.exp(d)
+        s = e.sum(1)
+        lse = np.where(none, -np.inf, m[:, 0] + np.log(s))
+        entropy = np.where(none, 0.0, np.log(s) - (e * np.where(e > 0, d, 0.0)).sum(1) / s)
+        logp = np.where(none[:, None], -np.inf, d - np.log(s)[:, None])
+    lse, entropy = (np.where(bad, np.nan, v) for v in (lse, entropy))
+    logp[bad] = np.nan
+    out = {"lse": lse, "entropy": entropy}
+    if targets is not None:
+        t = np.asarray(targets)
+        out["logprob"] = np.where(t < 0, 0.0, logp[rows, np.maximum(t, 0)])
+    if top > 0:
+        order = np.argsort(-np.where(np.isnan(raw), np.inf, raw), axis=1, kind="stable")
+        first = np.argsort(~np.isnan(np.take_along_axis(raw, order, 1)), axis=1, kind="stable")  # NaN before inf
+        ids = np.take_along_axis(order, first, 1)[:, :top]
+        out["top_ids"], out["top_logprobs"] = ids, np.take_along_axis(logp, ids, 1)
+    return out
+
+
+def logprobs_grad(logits, targets=None, *, dlogprob=None, dlse=None, dentropy=None, scale: float = 1.0,
+                  lse=None, entropy=None) -> np.ndarray:
+    """The gradient of the logits; lse and entropy may be given (those of `logprobs` otherwise).  A row of nothing but
+    -inf has none."""
+    raw = _f64(logits)
+    f = logprobs(raw, scale=scale)
+    lse = f["lse"] if lse is None else _f64(lse)
+    entropy = f["entropy"] if entropy is None else _f64(entropy)
+    zero = np.zeros(len(raw))
+    dlp = zero if dlogprob is None or targets is None else np.where(np.asarray(targets) < 0, 0.0, _f64(dlogprob))
+    dl, dh = (zero if v is None else _f64(v) for v in (dlse, dentropy))
+    none = np.all(raw == -np.inf, axis=1)
+    with np.errstate(invalid="ignore"):
+        logp = raw * float(scale) - np.where(none, 0.0, lse)[:, None]
+        p = np.exp(logp)
+        d = p * ((dl - dlp)[:, None] - dh[:, None] * (np.where(p > 0, logp, 0.0) + entropy[:, None]))
+    if targets is not None:
+        t = np.asarray(targets)
+        d[np.arange(len(raw)), np.maximum(t, 0)] += dlp
+    d[none] = 0.0
+    return d * float(scale)
