@@ -352,7 +352,7 @@ CF_API cf_status cf_gemm_fused_rmsnorm_ex(const void *X, const void *W, const fl
 /* ------------------------------------------------------------------------ */
 /* Fused GEMM + bias (+ GELU) + residual + LayerNorm / RMSNorm               */
 /* ------------------------------------------------------------------------ */
-typedef enum { CF_NORM_LAYER = 0, CF_NORM_RMS = 1 } cf_norm;
+typedef enum { CF_NORM_LAYER = 0, CF_NORM_RMS = 1, CF_NORM_NONE = 2 /* cf_stitch_block_norms only */ } cf_norm;
 
 /* Y = Norm(act(alpha * X.W + bias) + R) * gamma (+ beta), Norm = LayerNorm or
  * RMSNorm (`norm`) -- the "add & norm" of a transformer block.
@@ -849,6 +849,84 @@ CF_API cf_status cf_gemm_linear_grad_ex(const void *dY, const void *X, const voi
                                         void *dX, void *dW, float *dbias, int64_t M, int64_t N, int64_t K,
                                         cf_dtype dtype, cf_activation act, void *workspace,
                                         size_t workspace_bytes, cf_stream_t stream, const cf_tuning *tuning);
+
+/* ------------------------------------------------------------------------ */
+/* Norms before and after a block, joined with its gate and residual scale    */
+/* ------------------------------------------------------------------------ */
+/* x_out = alpha * x + scale * gate * Post(h),   y = Pre(x_out)
+ *
+ * h is a block's output, x the residual stream around it, y the next block's
+ * input: two norms (RMSNorm, LayerNorm or none, each with a weight and a bias
+ * or without) and what joins them as one stitched subgraph over rows
+ * ([AStitch] "Four stitching schemes": every value stays in its thread from the
+ * first load to the second norm's store).
+ *   h    (device) `dtype` [rows, cols]
+ *   x    (device) `dtype` [rows, cols], or NULL: x_out = scale * gate * Post(h)
+ *   gate (device) `dtype` [gates, cols], gates a divisor of rows: row r takes
+ *        gate r / (rows / gates) (one for all rows, one for each sample, one for
+ *        each row); NULL with gates = 0: none
+ *   post_weight, post_bias, pre_weight, pre_bias (device) fp32 [cols], each may
+ *        be NULL (1 and 0); NULL where the norm is CF_NORM_NONE
+ *   x_out, y (device) `dtype` [rows, cols], written; either may be NULL, y has to
+ *        be with pre = CF_NORM_NONE.  Each may be h or x.
+ * Mean and biased variance (RMSNorm: the mean square) in fp32, eps inside the
+ * root; nothing is rounded but x_out and y, the second norm taking x_out
+ * unrounded.
+ * cf_stitch_block_norms_grad: of the gradients dy of y and dx_out of x_out (one
+ *   may be NULL: zero), from h and the stored x_out, whose rows' statistics are
+ *   worked out again:
+ *   d = dx_out + (gradient of Pre at x_out), dx = alpha * d,
+ *   dgate = sum over its rows of scale * d * Post(h),
+ *   dh = (gradient of Post at h of scale * gate * d),
+ *   and the column sums that are the weights' and biases' gradients (fp32 [cols]).
+ *   dh (device) `dtype` [rows, cols]; dx and dgate alike, or NULL: not wanted, as
+ *   dpost_weight ... dpre_bias may be.  dh and dx may be dy, dx_out, h or x_out.
+ *   post_bias is read for dgate alone.  Without dy, pre and x_out are not read.
+ * Sums over a row and over rows are fp32, in an order that depends on the sizes
+ * alone: equal calls give equal bits.  NaNs stay in their rows (and their
+ * columns' sums).
+ * Supported: cols in 0..32768, rows in 0..2^31 - 512 (0 of either is a no-op; a
+ * gradient of no rows writes zeros to the sums), dtype bf16, fp16 or fp32,
+ * pointers aligned to their element (16 bytes, with cols a multiple of 8, is
+ * faster).
+ * workspace (device) >= cf_stitch_workspace_size() bytes, the gradient
+ * cf_stitch_block_norms_grad_workspace_size(), 16-byte aligned there; nothing of
+ * it has to be zero.
+ * Tuning fields used (_ex): disable_pdl. */
+CF_API size_t cf_stitch_block_norms_grad_workspace_size(int64_t rows, int64_t cols);
+
+CF_API cf_status cf_stitch_block_norms(const void *h, const void *x, const void *gate, const float *post_weight,
+                                       const float *post_bias, const float *pre_weight, const float *pre_bias,
+                                       void *x_out, void *y, int64_t rows, int64_t cols, int64_t gates,
+                                       cf_norm post, cf_norm pre, float scale, float alpha, float eps,
+                                       cf_dtype dtype, void *workspace, size_t workspace_bytes,
+                                       cf_stream_t stream);
+
+CF_API cf_status cf_stitch_block_norms_ex(const void *h, const void *x, const void *gate,
+                                          const float *post_weight, const float *post_bias,
+                                          const float *pre_weight, const float *pre_bias, void *x_out, void *y,
+                                          int64_t rows, int64_t cols, int64_t gates, cf_norm post, cf_norm pre,
+                                          float scale, float alpha, float eps, cf_dtype dtype, void *workspace,
+                                          size_t workspace_bytes, cf_stream_t stream, const cf_tuning *tuning);
+
+CF_API cf_status cf_stitch_block_norms_grad(const void *dy, const void *dx_out, const void *h, const void *x_out,
+                                            const void *gate, const float *post_weight, const float *post_bias,
+                                            const float *pre_weight, void *dh, void *dx, void *dgate,
+                                            float *dpost_weight, float *dpost_bias, float *dpre_weight,
+                                            float *dpre_bias, int64_t rows, int64_t cols, int64_t gates,
+                                            cf_norm post, cf_norm pre, float scale, float alpha, float eps,
+                                            cf_dtype dtype, void *workspace, size_t workspace_bytes,
+                                            cf_stream_t stream);
+
+CF_API cf_status cf_stitch_block_norms_grad_ex(const void *dy, const void *dx_out, const void *h,
+                                               const void *x_out, const void *gate, const float *post_weight,
+                                               const float *post_bias, const float *pre_weight, void *dh,
+                                               void *dx, void *dgate, float *dpost_weight, float *dpost_bias,
+                                               float *dpre_weight, float *dpre_bias, int64_t rows, int64_t cols,
+                                               int64_t gates, cf_norm post, cf_norm pre, float scale,
+                                               float alpha, float eps, cf_dtype dtype, void *workspace,
+                                               size_t workspace_bytes, cf_stream_t stream,
+                                               const cf_tuning *tuning);
 
 #ifdef __cplusplus
 }

@@ -180,6 +180,14 @@ _SIGS = {
                                   _SZ, _P]),
     "cf_gemm_linear_grad_ex": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, _P,
                                      _SZ, _P, ctypes.POINTER(cf_tuning)]),
+    "cf_stitch_block_norms": (_ST, [_P] * 9 + [_I64] * 3 + [ctypes.c_int] * 2 + [_F] * 3 + [ctypes.c_int, _P, _SZ, _P]),
+    "cf_stitch_block_norms_ex": (_ST, [_P] * 9 + [_I64] * 3 + [ctypes.c_int] * 2 + [_F] * 3 +
+                                 [ctypes.c_int, _P, _SZ, _P, ctypes.POINTER(cf_tuning)]),
+    "cf_stitch_block_norms_grad_workspace_size": (_SZ, [_I64, _I64]),
+    "cf_stitch_block_norms_grad": (_ST, [_P] * 15 + [_I64] * 3 + [ctypes.c_int] * 2 + [_F] * 3 +
+                                   [ctypes.c_int, _P, _SZ, _P]),
+    "cf_stitch_block_norms_grad_ex": (_ST, [_P] * 15 + [_I64] * 3 + [ctypes.c_int] * 2 + [_F] * 3 +
+                                      [ctypes.c_int, _P, _SZ, _P, ctypes.POINTER(cf_tuning)]),
     "cf_stitch_powadd_softmax": (_ST, [_P, _P, _F, _P, _I64, _I64, _P, _SZ, _P]),
     "cf_stitch_powadd_softmax_ex": (_ST, [_P, _P, _F, _P, _I64, _I64, _P, _SZ, _P, ctypes.POINTER(cf_tuning)]),
 }
@@ -317,6 +325,7 @@ def cf_gemm_fused_rmsnorm(X, W, bias, gamma, beta, Y, M, N, K, alpha, eps, act, 
 
 CF_NORM_LAYER = 0
 CF_NORM_RMS = 1
+CF_NORM_NONE = 2
 
 
 def cf_gemm_fused_residual_norm(X, W, bias, R, gamma, beta, Y, M, N, K, alpha, eps, act, norm, workspace,
@@ -1003,3 +1012,130 @@ def gemm_linear_grad(dY, X, W, *, act="none", preact=None, input=True, weight=Tr
 
     return _outputs("cf_gemm_linear_grad", args, dev, workspace, cf_gemm_linear_workspace_size, (M, N, K), stream,
                     tuning)
+
+
+# ---------------------------------------------------------------------------
+# norms before and after a block
+# ---------------------------------------------------------------------------
+def cf_stitch_block_norms(h, x, gate, post_weight, post_bias, pre_weight, pre_bias, x_out, y, rows, cols, gates, post,
+                          pre, scale, alpha, eps, dtype, workspace, workspace_bytes, stream=None, tuning=None) -> int:
+    """x_out = alpha x + scale gate Post(h), y = Pre(x_out)."""
+    L = lib()
+    args = (_ptr(h), _ptr(x), _ptr(gate), _ptr(post_weight), _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias),
+            _ptr(x_out), _ptr(y), rows, cols, gates, post, pre, scale, alpha, eps, dtype, _ptr(workspace),
+            workspace_bytes, _stream(stream))
+    return L.cf_stitch_block_norms(*args) if tuning is None else L.cf_stitch_block_norms_ex(*args, _tun(tuning))
+
+
+def cf_stitch_block_norms_grad_workspace_size(rows, cols) -> int:
+    return lib().cf_stitch_block_norms_grad_workspace_size(rows, cols)
+
+
+def cf_stitch_block_norms_grad(dy, dx_out, h, x_out, gate, post_weight, post_bias, pre_weight, dh, dx, dgate,
+                               dpost_weight, dpost_bias, dpre_weight, dpre_bias, rows, cols, gates, post, pre, scale,
+                               alpha, eps, dtype, workspace, workspace_bytes, stream=None, tuning=None) -> int:
+    L = lib()
+    args = (_ptr(dy), _ptr(dx_out), _ptr(h), _ptr(x_out), _ptr(gate), _ptr(post_weight), _ptr(post_bias),
+            _ptr(pre_weight), _ptr(dh), _ptr(dx), _ptr(dgate), _ptr(dpost_weight), _ptr(dpost_bias),
+            _ptr(dpre_weight), _ptr(dpre_bias), rows, cols, gates, post, pre, scale, alpha, eps, dtype,
+            _ptr(workspace), workspace_bytes, _stream(stream))
+    if tuning is None:
+        return L.cf_stitch_block_norms_grad(*args)
+    return L.cf_stitch_block_norms_grad_ex(*args, _tun(tuning))
+
+
+_NORMS = {"none": CF_NORM_NONE, "rms": CF_NORM_RMS, "layer": CF_NORM_LAYER}
+_ROW_DTYPES = {}  # the 16-bit types and torch.float32, once torch is there
+
+
+def _row_dtype(name, t):
+    """The library's name of a row operand's dtype."""
+    if not _ROW_DTYPES:
+        import torch
+        _ROW_DTYPES.update({torch.bfloat16: CF_BF16, torch.float16: CF_FP16, torch.float32: CF_FP32})
+    if not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, not on a CUDA device")
+    dt = _ROW_DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} has dtype {t.dtype}, not bfloat16, float16 or float32")
+    return dt
+
+
+def _norm(name, kind, *vectors):
+    n = _NORMS.get(kind)
+    if n is None:
+        raise ValueError(f"{name}: unknown norm {kind!r}")
+    if n == CF_NORM_NONE and any(v is not None for v in vectors):
+        raise ValueError(f"{name} is no norm, but has a weight or a bias")
+    return n
+
+
+def _block_norms_operands(h, gate, post, post_weight, post_bias, pre, pre_weight, pre_bias):
+    """What both directions check: sizes, device, dtype, the library's dtype and norms, addresses."""
+    import torch
+    dt = _row_dtype("h", h)
+    rows, cols = _sizes("h", h, 2)
+    dev, dtype, f32 = h.device, h.dtype, torch.float32
+    kinds = _norm("post", post, post_weight, post_bias), _norm("pre", pre, pre_weight, pre_bias)
+    gates = 0
+    if gate is not None:
+        gates = _sizes("gate", gate, 2)[0]
+        if gates == 0 and rows > 0 or gates > 0 and rows % gates:
+            raise ValueError(f"{gates} gates do not divide {rows} rows")
+    addresses = (_operand("h", h, (rows, cols), dtype, dev), _operand("gate", gate, (gates, cols), dtype, dev),
+                 _operand("post_weight", post_weight, (cols,), f32, dev),
+                 _operand("post_bias", post_bias, (cols,), f32, dev),
+                 _operand("pre_weight", pre_weight, (cols,), f32, dev),
+                 _operand("pre_bias", pre_bias, (cols,), f32, dev))
+    return rows, cols, gates, dev, dtype, dt, kinds, addresses
+
+
+def stitch_block_norms(h, x=None, *, post="none", post_weight=None, post_bias=None, gate=None, scale=1.0, alpha=1.0,
+                       pre="none", pre_weight=None, pre_bias=None, eps=1e-5, out=None, norm_out=None, workspace=None,
+                       stream=None, tuning=None):
+    """(x', y): x' = alpha*x + scale*gate*Post(h), y = Pre(x') (None with pre "none"); h and x [T, N] bf16, fp16 or fp32
+    CUDA tensors (x may be None: 0), gate [G, N] of that type, G a divisor of T (row r takes gate r // (T // G)), or
+    None; Post and Pre "rms", "layer" or "none", weights and biases fp32 [N] or None.  `out` and `norm_out` take x'
+    and y; each may be h or x."""
+    rows, cols, gates, dev, dtype, dt, (po, pr), (ph, pg, pw, pb, qw, qb) = _block_norms_operands(
+        h, gate, post, post_weight, post_bias, pre, pre_weight, pre_bias)
+    px = _operand("x", x, (rows, cols), dtype, dev)
+    if pr == CF_NORM_NONE and norm_out is not None:
+        raise ValueError("norm_out is given, but there is no norm before the next block")
+
+    def args():
+        xo = _made("out", out, (rows, cols), dtype, dev)
+        y = None if pr == CF_NORM_NONE else _made("norm_out", norm_out, (rows, cols), dtype, dev)
+        return (ph, px, pg, pw, pb, qw, qb, xo.data_ptr(), _ptr(y), rows, cols, gates, po, pr, scale, alpha, eps,
+                dt), (xo, y)
+
+    return _outputs("cf_stitch_block_norms", args, dev, workspace, cf_stitch_workspace_size, (rows, cols), stream,
+                    tuning)
+
+
+def stitch_block_norms_grad(dy, dx_out, h, x_out, *, post="none", post_weight=None, post_bias=None, gate=None,
+                            scale=1.0, alpha=1.0, pre="none", pre_weight=None, pre_bias=None, eps=1e-5, dx=True,
+                            out=None, workspace=None, stream=None, tuning=None):
+    """(dh, dx, dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias) of stitch_block_norms for the gradients dy of y
+    and dx_out of x' ([T, N]; one may be None: 0): those of what is given there, fp32 for weights and biases, None in
+    the place of the others and, with dx=False, of dx.  h and x_out ([T, N]) are the forward pass's input and output.
+    `out`: seven outputs, None for new ones; dh and dx may be dy, dx_out, h or x_out."""
+    import torch
+    rows, cols, gates, dev, dtype, dt, (po, pr), (ph, pg, pw, pb, qw, _) = _block_norms_operands(
+        h, gate, post, post_weight, post_bias, pre, pre_weight, pre_bias)
+    if (dy is None) == (pr != CF_NORM_NONE):
+        raise ValueError("dy goes with a norm before the next block")
+    given = (None,) * 7 if out is None else out
+    ptrs = [_operand(n, t, (rows, cols), dtype, dev) for n, t in (("dy", dy), ("dx_out", dx_out), ("x_out", x_out))]
+
+    def args():
+        like, wants = (rows, cols), (True, dx, gate is not None, post_weight is not None, post_bias is not None,
+                                     pre_weight is not None, pre_bias is not None)
+        shapes = (like, like, (gates, cols)) + ((cols,),) * 4
+        outs = tuple(_made(f"out[{i}]", given[i], shapes[i], dtype if i < 3 else torch.float32, dev) if w else None
+                     for i, w in enumerate(wants))
+        return (ptrs[0], ptrs[1], ph, ptrs[2], pg, pw, pb, qw, *map(_ptr, outs), rows, cols, gates, po, pr, scale,
+                alpha, eps, dt), outs
+
+    return _outputs("cf_stitch_block_norms_grad", args, dev, workspace, cf_stitch_block_norms_grad_workspace_size,
+                    (rows, cols), stream, tuning)

@@ -15,6 +15,7 @@
 #include <tuple>
 
 #include "../../include/cf.h"
+#include "block_norms.h"
 #include "cf_internal.h"
 #include "grouped_internal.h"
 
@@ -2007,4 +2008,172 @@ extern "C" cf_status cf_gemm_linear_grad(const void *dY, const void *X, const vo
                                          cf_stream_t stream) {
     return cf_gemm_linear_grad_ex(dY, X, W, Z, dZ, dX, dW, dbias, M, N, K, dtype, act, workspace, workspace_bytes,
                                   stream, nullptr);
+}
+
+// -------------------------------------------------------------------------
+// Norms before and after a block
+// -------------------------------------------------------------------------
+namespace {
+
+bool norm_kind(int v) { return v == CF_NORM_LAYER || v == CF_NORM_RMS || v == CF_NORM_NONE; }
+bool aligned_to(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// what both directions check before they look at a pointer
+cf_status block_norms_sizes(int64_t rows, int64_t cols, int64_t gates, const void *gate, cf_norm post, cf_norm pre,
+                            int dtype) {
+    if (rows < 0 || cols < 0 || gates < 0 || !norm_kind(int(post)) || !norm_kind(int(pre))) return CF_ERR_INVALID_ARG;
+    if (dtype != CF_BF16 && dtype != CF_FP16 && dtype != CF_FP32) return CF_ERR_INVALID_ARG;
+    if ((gate != nullptr) != (gates > 0) && rows > 0) return CF_ERR_INVALID_ARG;
+    if (gate && rows % gates != 0) return CF_ERR_INVALID_ARG;
+    if (cols > cf::kBlockNormsMaxCols || rows > (int64_t(1) << 31) - 512) return CF_ERR_UNSUPPORTED;
+    return CF_OK;
+}
+
+}  // namespace
+
+extern "C" cf_status cf_stitch_block_norms_ex(const void *h, const void *x, const void *gate, const float *post_weight,
+                                              const float *post_bias, const float *pre_weight, const float *pre_bias,
+                                              void *x_out, void *y, int64_t rows, int64_t cols, int64_t gates,
+                                              cf_norm post, cf_norm pre, float scale, float alpha, float eps,
+                                              cf_dtype dtype, void *workspace, size_t workspace_bytes,
+                                              cf_stream_t stream, const cf_tuning *tuning) {
+    cf_status st = block_norms_sizes(rows, cols, gates, gate, post, pre, int(dtype));
+    if (st != CF_OK) return st;
+    if (rows == 0 || cols == 0) return CF_OK;
+    if (!workspace || !h || (!x_out && !y)) return CF_ERR_INVALID_ARG;
+    if ((post == CF_NORM_NONE && (post_weight || post_bias)) || (pre == CF_NORM_NONE && (pre_weight || pre_bias || y)))
+        return CF_ERR_INVALID_ARG;
+    const size_t size = dtype == CF_FP32 ? 4 : 2;
+    bool vec = cols % 8 == 0;
+    for (const void *p : {h, x, gate, static_cast<const void *>(x_out), static_cast<const void *>(y)}) {
+        if (!aligned_to(p, size)) return CF_ERR_MISALIGNED;
+        vec = vec && aligned16(p);
+    }
+    for (const float *p : {post_weight, post_bias, pre_weight, pre_bias}) {
+        if (!aligned_to(p, 4)) return CF_ERR_MISALIGNED;
+        vec = vec && aligned16(p);
+    }
+    if (x_out == y || (gate && (gate == x_out || gate == y))) return CF_ERR_INVALID_ARG;
+    if (workspace_bytes < cf_stitch_workspace_size(rows, cols)) return CF_ERR_WORKSPACE_TOO_SMALL;
+    cf::DeviceInfo dev;
+    st = linear_device(&dev);
+    if (st != CF_OK) return st;
+    cf::BlockNormsArgs a{};
+    a.h = h, a.x = x, a.gate = gate;
+    a.post_weight = post_weight, a.post_bias = post_bias, a.pre_weight = pre_weight, a.pre_bias = pre_bias;
+    a.x_out = x_out, a.y = y;
+    a.rows = rows;
+    a.rows_per_gate = uint32_t(gate ? rows / gates : rows);
+    a.cols = int(cols);
+    a.post = int(post), a.pre = int(pre), a.dtype = int(dtype);
+    a.scale = scale, a.alpha = alpha, a.eps = eps;
+    const bool pdl = !tuning || tuning->disable_pdl == 0;
+    const cudaError_t e =
+        cf::launch_block_norms(a, vec, dev.sm_count, pdl, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CF_OK : cuda_fail(e);
+}
+
+extern "C" cf_status cf_stitch_block_norms(const void *h, const void *x, const void *gate, const float *post_weight,
+                                           const float *post_bias, const float *pre_weight, const float *pre_bias,
+                                           void *x_out, void *y, int64_t rows, int64_t cols, int64_t gates,
+                                           cf_norm post, cf_norm pre, float scale, float alpha, float eps,
+                                           cf_dtype dtype, void *workspace, size_t workspace_bytes,
+                                           cf_stream_t stream) {
+    return cf_stitch_block_norms_ex(h, x, gate, post_weight, post_bias, pre_weight, pre_bias, x_out, y, rows, cols,
+                                    gates, post, pre, scale, alpha, eps, dtype, workspace, workspace_bytes, stream,
+                                    nullptr);
+}
+
+// the error word; the sums of the sets, for each of up to four weights and biases; the gates' slots
+static size_t block_norms_partials(const cf::BlockNormsGradPlan &p, int64_t cols) {
+    return cf::align_up(size_t(4) * size_t(p.sets) * size_t(cols) * 4, 256);
+}
+
+extern "C" size_t cf_stitch_block_norms_grad_workspace_size(int64_t rows, int64_t cols) {
+    if (rows <= 0 || cols <= 0 || cols > cf::kBlockNormsMaxCols) return cf::kErrBytes;
+    const cf::BlockNormsGradPlan p = cf::plan_block_norms_grad(rows, cols, int(kPlanSms));
+    return cf::kErrBytes + block_norms_partials(p, cols) + size_t(p.workers) * 2 * size_t(cols) * 4;
+}
+
+extern "C" cf_status cf_stitch_block_norms_grad_ex(
+    const void *dy, const void *dx_out, const void *h, const void *x_out, const void *gate, const float *post_weight,
+    const float *post_bias, const float *pre_weight, void *dh, void *dx, void *dgate, float *dpost_weight,
+    float *dpost_bias, float *dpre_weight, float *dpre_bias, int64_t rows, int64_t cols, int64_t gates, cf_norm post,
+    cf_norm pre, float scale, float alpha, float eps, cf_dtype dtype, void *workspace, size_t workspace_bytes,
+    cf_stream_t stream, const cf_tuning *tuning) {
+    cf_status st = block_norms_sizes(rows, cols, gates, gate, post, pre, int(dtype));
+    if (st != CF_OK) return st;
+    if (!workspace) return CF_ERR_INVALID_ARG;
+    if (cols == 0) return CF_OK;
+    if (rows > 0 && (!h || !dh || (!dy && !dx_out) || (dy && !x_out))) return CF_ERR_INVALID_ARG;
+    if ((post == CF_NORM_NONE && (post_weight || post_bias || dpost_weight || dpost_bias)) ||
+        (pre == CF_NORM_NONE && (dy || pre_weight || dpre_weight || dpre_bias)) || (!gate && dgate && rows > 0))
+        return CF_ERR_INVALID_ARG;
+    if (rows > 0 && !dy && (dpre_weight || dpre_bias)) return CF_ERR_INVALID_ARG;
+    const size_t size = dtype == CF_FP32 ? 4 : 2;
+    bool vec = cols % 8 == 0;
+    for (const void *p : {dy, dx_out, h, x_out, gate, static_cast<const void *>(dh), static_cast<const void *>(dx),
+                          static_cast<const void *>(dgate)}) {
+        if (!aligned_to(p, size)) return CF_ERR_MISALIGNED;
+        vec = vec && aligned16(p);
+    }
+    for (const float *p : {post_weight, post_bias, pre_weight}) {
+        if (!aligned_to(p, 4)) return CF_ERR_MISALIGNED;
+        vec = vec && aligned16(p);
+    }
+    float *const sums[4] = {dpost_weight, dpost_bias, dpre_weight, dpre_bias};
+    for (const float *p : sums)
+        if (!aligned_to(p, 4)) return CF_ERR_MISALIGNED;
+    if (!aligned16(workspace)) return CF_ERR_MISALIGNED;
+    if (rows > 0) {
+        if (dh == dx || dh == gate || (dx && dx == gate)) return CF_ERR_INVALID_ARG;
+        for (const void *p : {dy, dx_out, h, x_out, gate, static_cast<const void *>(dh), static_cast<const void *>(dx)})
+            if (dgate && dgate == p) return CF_ERR_INVALID_ARG;
+    }
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (sums[i] && sums[i] == sums[j]) return CF_ERR_INVALID_ARG;
+    if (workspace_bytes < cf_stitch_block_norms_grad_workspace_size(rows, cols)) return CF_ERR_WORKSPACE_TOO_SMALL;
+    cf::DeviceInfo dev;
+    st = linear_device(&dev);
+    if (st != CF_OK) return st;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (rows == 0) {  // every sum is empty
+        for (float *p : sums) {
+            const cudaError_t e = p ? cudaMemsetAsync(p, 0, size_t(cols) * 4, cs) : cudaSuccess;
+            if (e != cudaSuccess) return cuda_fail(e);
+        }
+        return CF_OK;
+    }
+    const cf::BlockNormsGradPlan p =
+        cf::plan_block_norms_grad(rows, cols, std::min(dev.sm_count, int(kPlanSms)));
+    cf::BlockNormsGradArgs a{};
+    a.dy = dy, a.dx_out = dx_out, a.h = h, a.x_out = x_out, a.gate = gate;
+    a.post_weight = post_weight, a.post_bias = post_bias, a.pre_weight = pre_weight;
+    a.dh = dh, a.dx = dx, a.dgate = dgate;
+    for (int i = 0, n = 0; i < 4; ++i) {
+        a.sum_at[i] = sums[i] ? n++ : -1;
+        a.sum_out[i] = sums[i];
+    }
+    unsigned char *const ws = static_cast<unsigned char *>(workspace) + cf::kErrBytes;
+    a.partials = reinterpret_cast<float *>(ws);
+    a.slots = reinterpret_cast<float *>(ws + block_norms_partials(p, cols));
+    a.rows = rows;
+    a.rows_per_gate = uint32_t(gate ? rows / gates : rows);
+    a.cols = int(cols);
+    a.post = int(post), a.pre = dy ? int(pre) : int(CF_NORM_NONE), a.dtype = int(dtype);
+    a.scale = scale, a.alpha = alpha, a.eps = eps;
+    const cudaError_t e = cf::launch_block_norms_grad(a, p, vec, !tuning || tuning->disable_pdl == 0, cs);
+    return e == cudaSuccess ? CF_OK : cuda_fail(e);
+}
+
+extern "C" cf_status cf_stitch_block_norms_grad(
+    const void *dy, const void *dx_out, const void *h, const void *x_out, const void *gate, const float *post_weight,
+    const float *post_bias, const float *pre_weight, void *dh, void *dx, void *dgate, float *dpost_weight,
+    float *dpost_bias, float *dpre_weight, float *dpre_bias, int64_t rows, int64_t cols, int64_t gates, cf_norm post,
+    cf_norm pre, float scale, float alpha, float eps, cf_dtype dtype, void *workspace, size_t workspace_bytes,
+    cf_stream_t stream) {
+    return cf_stitch_block_norms_grad_ex(dy, dx_out, h, x_out, gate, post_weight, post_bias, pre_weight, dh, dx, dgate,
+                                         dpost_weight, dpost_bias, dpre_weight, dpre_bias, rows, cols, gates, post, pre,
+                                         scale, alpha, eps, dtype, workspace, workspace_bytes, stream, nullptr);
 }
