@@ -928,6 +928,69 @@ CF_API cf_status cf_stitch_block_norms_grad_ex(const void *dy, const void *dx_ou
                                                size_t workspace_bytes, cf_stream_t stream,
                                                const cf_tuning *tuning);
 
+/* ------------------------------------------------------------------------ */
+/* Log probabilities of given tokens, with entropy and top alternatives       */
+/* ------------------------------------------------------------------------ */
+/* Of z = scale * logits[r, :], for every row r:
+ *   lse = log sum exp z,   logprob = z[targets[r]] - lse,
+ *   entropy = -sum p log p with p = exp(z - lse),
+ *   the `top` largest logits' ids (equal ones by id) and log probabilities.
+ *
+ * The row softmax of cf_stitch_rowreduce_broadcast with only what is asked of it
+ * written: one read of the logits.
+ *   logits  (device) `dtype` [rows, vocab], `stride` elements from a row to the
+ *           next (a padded vocabulary's rows; >= vocab)
+ *   targets (device) int64 [rows], each in 0..vocab-1, or -1 for none (logprob
+ *           0); NULL with logprob NULL.  Others are taken as -1 and reported as
+ *           CF_ERR_DEVICE_BOUNDS.
+ *   logprob, lse, entropy (device) fp32 [rows], each may be NULL
+ *   top_logprobs (device) fp32 [rows, top], top_ids (device) int64 [rows, top]:
+ *           one may be NULL, both are with top = 0
+ * A logit of -inf is a token left out.  A row of nothing else has lse and log
+ * probabilities of -inf and entropy 0; one with a NaN or +inf has NaNs (its
+ * largest ids first: NaNs, then +inf).
+ * cf_stitch_logprobs_grad: of the gradients dlogprob, dlse and dentropy (fp32
+ *   [rows], each may be NULL: zero; dlogprob goes with targets, dentropy with
+ *   entropy),
+ *   dlogits = scale * (dlogprob * (1[target] - p) + dlse * p
+ *                      - dentropy * p * (log p + entropy)),  log p = z - lse,
+ *   with the given lse and entropy: p is as good as lse is, which holds fp32's 24
+ *   bits.  A row whose lse is -inf has zeros, a target of -1 no dlogprob.
+ *   dlogits (device) `dtype` [rows, vocab], rows `dstride` apart, written; what
+ *   lies between rows is not.  It may be logits (with the same stride).  The top
+ *   log probabilities have no gradient here.
+ * Sums are fp32, in an order that depends on the sizes (and where in 16 bytes a
+ * row starts) alone: equal calls give equal bits.
+ * Supported: vocab in 0..2^24 (0 with rows > 0: the gradient alone, a no-op),
+ * rows in 0..2^27 (0 is a no-op), stride up to 2^32, top in 0..32 and no more
+ * than vocab, scale > 0, dtype bf16, fp16 or fp32; the gradient rows times
+ * vocabularies of fewer than 2^31 pieces of 16 KB.
+ * workspace (device) >= cf_stitch_workspace_size() bytes: the error word.
+ * Tuning fields used (_ex): disable_pdl. */
+CF_API cf_status cf_stitch_logprobs(const void *logits, const int64_t *targets, float *logprob, float *lse,
+                                    float *entropy, float *top_logprobs, int64_t *top_ids, int64_t rows,
+                                    int64_t vocab, int64_t stride, int64_t top, float scale, cf_dtype dtype,
+                                    void *workspace, size_t workspace_bytes, cf_stream_t stream);
+
+CF_API cf_status cf_stitch_logprobs_ex(const void *logits, const int64_t *targets, float *logprob, float *lse,
+                                       float *entropy, float *top_logprobs, int64_t *top_ids, int64_t rows,
+                                       int64_t vocab, int64_t stride, int64_t top, float scale, cf_dtype dtype,
+                                       void *workspace, size_t workspace_bytes, cf_stream_t stream,
+                                       const cf_tuning *tuning);
+
+CF_API cf_status cf_stitch_logprobs_grad(const void *logits, const int64_t *targets, const float *lse,
+                                         const float *entropy, const float *dlogprob, const float *dlse,
+                                         const float *dentropy, void *dlogits, int64_t rows, int64_t vocab,
+                                         int64_t stride, int64_t dstride, float scale, cf_dtype dtype,
+                                         void *workspace, size_t workspace_bytes, cf_stream_t stream);
+
+CF_API cf_status cf_stitch_logprobs_grad_ex(const void *logits, const int64_t *targets, const float *lse,
+                                            const float *entropy, const float *dlogprob, const float *dlse,
+                                            const float *dentropy, void *dlogits, int64_t rows, int64_t vocab,
+                                            int64_t stride, int64_t dstride, float scale, cf_dtype dtype,
+                                            void *workspace, size_t workspace_bytes, cf_stream_t stream,
+                                            const cf_tuning *tuning);
+
 #ifdef __cplusplus
 }
 #endif

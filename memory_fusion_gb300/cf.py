@@ -188,6 +188,11 @@ _SIGS = {
                                    [ctypes.c_int, _P, _SZ, _P]),
     "cf_stitch_block_norms_grad_ex": (_ST, [_P] * 15 + [_I64] * 3 + [ctypes.c_int] * 2 + [_F] * 3 +
                                       [ctypes.c_int, _P, _SZ, _P, ctypes.POINTER(cf_tuning)]),
+    "cf_stitch_logprobs": (_ST, [_P] * 7 + [_I64] * 4 + [_F, ctypes.c_int, _P, _SZ, _P]),
+    "cf_stitch_logprobs_ex": (_ST, [_P] * 7 + [_I64] * 4 + [_F, ctypes.c_int, _P, _SZ, _P, ctypes.POINTER(cf_tuning)]),
+    "cf_stitch_logprobs_grad": (_ST, [_P] * 8 + [_I64] * 4 + [_F, ctypes.c_int, _P, _SZ, _P]),
+    "cf_stitch_logprobs_grad_ex": (_ST, [_P] * 8 + [_I64] * 4 +
+                                   [_F, ctypes.c_int, _P, _SZ, _P, ctypes.POINTER(cf_tuning)]),
     "cf_stitch_powadd_softmax": (_ST, [_P, _P, _F, _P, _I64, _I64, _P, _SZ, _P]),
     "cf_stitch_powadd_softmax_ex": (_ST, [_P, _P, _F, _P, _I64, _I64, _P, _SZ, _P, ctypes.POINTER(cf_tuning)]),
 }
@@ -1139,3 +1144,98 @@ def stitch_block_norms_grad(dy, dx_out, h, x_out, *, post="none", post_weight=No
 
     return _outputs("cf_stitch_block_norms_grad", args, dev, workspace, cf_stitch_block_norms_grad_workspace_size,
                     (rows, cols), stream, tuning)
+
+
+# ---------------------------------------------------------------------------
+# log probabilities of given tokens
+# ---------------------------------------------------------------------------
+def cf_stitch_logprobs(logits, targets, logprob, lse, entropy, top_logprobs, top_ids, rows, vocab, stride, top, scale,
+                       dtype, workspace, workspace_bytes, stream=None, tuning=None) -> int:
+    L = lib()
+    args = (_ptr(logits), _ptr(targets), _ptr(logprob), _ptr(lse), _ptr(entropy), _ptr(top_logprobs), _ptr(top_ids),
+            rows, vocab, stride, top, scale, dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+    return L.cf_stitch_logprobs(*args) if tuning is None else L.cf_stitch_logprobs_ex(*args, _tun(tuning))
+
+
+def cf_stitch_logprobs_grad(logits, targets, lse, entropy, dlogprob, dlse, dentropy, dlogits, rows, vocab, stride,
+                            dstride, scale, dtype, workspace, workspace_bytes, stream=None, tuning=None) -> int:
+    L = lib()
+    args = (_ptr(logits), _ptr(targets), _ptr(lse), _ptr(entropy), _ptr(dlogprob), _ptr(dlse), _ptr(dentropy),
+            _ptr(dlogits), rows, vocab, stride, dstride, scale, dtype, _ptr(workspace), workspace_bytes,
+            _stream(stream))
+    return L.cf_stitch_logprobs_grad(*args) if tuning is None else L.cf_stitch_logprobs_grad_ex(*args, _tun(tuning))
+
+
+def _rows_apart(name, t, shape=None, dtype=None, device=None):
+    """(rows, columns, elements from a row to the next) of a matrix whose rows are contiguous, checked."""
+    rows, cols = _sizes(name, t, 2)
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name} has rows that are not contiguous or that overlap")
+    return rows, cols, t.stride(0) if rows > 1 else cols
+
+
+def stitch_logprobs(logits, targets=None, *, scale=1.0, top=0, entropy=True, out=None, workspace=None, stream=None,
+                    tuning=None):
+    """(logprob, lse, entropy, top_logprobs, top_ids) of softmax(scale * logits), rows [T, V] of bf16, fp16 or fp32
+    that may lie apart (logits[:, :V] of a padded vocabulary): the log probability of each row's target (int64 [T], -1:
+    none, 0), log-sum-exp and entropy, all fp32 [T], and the `top` (0..32) largest logits' log probabilities and ids
+    [T, top], equal logits by id.  None in the place of what is not asked for.  `out`: five outputs, None for new ones."""
+    import torch
+    dt = _row_dtype("logits", logits)
+    rows, vocab, apart = _rows_apart("logits", logits)
+    dev, f32, i64 = logits.device, torch.float32, torch.int64
+    if not 0 <= top <= min(vocab, 32):
+        raise ValueError(f"top is {top}, not in 0..{min(vocab, 32)}")
+    if not scale > 0:
+        raise ValueError(f"scale is {scale}, not above 0")
+    if vocab == 0 and rows > 0:
+        raise ValueError("logits have no columns")
+    given = (None,) * 5 if out is None else out
+    t = _operand("targets", targets, (rows,), i64, dev)
+
+    def args():
+        want = (targets is not None, True, entropy, top > 0, top > 0)
+        shapes = ((rows,),) * 3 + ((rows, top),) * 2
+        outs = tuple(_made(f"out[{i}]", given[i], shapes[i], f32 if i < 4 else i64, dev) if w else None
+                     for i, w in enumerate(want))
+        return (logits.data_ptr(), t, *map(_ptr, outs), rows, vocab, apart, top, scale, dt), outs
+
+    return _outputs("cf_stitch_logprobs", args, dev, workspace, cf_stitch_workspace_size, (rows, vocab), stream, tuning)
+
+
+def stitch_logprobs_grad(logits, targets, lse, dlogprob=None, *, dlse=None, entropy=None, dentropy=None, scale=1.0,
+                         out=None, workspace=None, stream=None, tuning=None):
+    """The gradient of the logits [T, V] (in their dtype) for the gradients dlogprob, dlse and dentropy (fp32 [T], None:
+    0) of stitch_logprobs' results; lse and, with dentropy, entropy are its results.  `out` may be logits, or rows
+    apart like theirs."""
+    import torch
+    dt = _row_dtype("logits", logits)
+    rows, vocab, apart = _rows_apart("logits", logits)
+    dev, dtype, f32 = logits.device, logits.dtype, torch.float32
+    if not scale > 0:
+        raise ValueError(f"scale is {scale}, not above 0")
+    if (targets is None) != (dlogprob is None):
+        raise ValueError("dlogprob goes with targets")
+    if (entropy is None) != (dentropy is None):
+        raise ValueError("dentropy goes with entropy")
+    if dlogprob is None and dlse is None and dentropy is None:
+        raise ValueError("no gradient is given")
+    before = (logits.data_ptr(), _operand("targets", targets, (rows,), torch.int64, dev),
+              *(_operand(n, t, (rows,), f32, dev) for n, t in (("lse", lse), ("entropy", entropy),
+                                                               ("dlogprob", dlogprob), ("dlse", dlse),
+                                                               ("dentropy", dentropy))))
+    if out is not None:
+        _rows_apart("out", out, (rows, vocab), dtype, dev)
+
+    def args():
+        d = torch.empty((rows, vocab), dtype=dtype, device=dev) if out is None else out
+        return (*before, d.data_ptr(), rows, vocab, apart, d.stride(0) if rows > 1 else vocab, scale, dt), d
+
+    return _outputs("cf_stitch_logprobs_grad", args, dev, workspace, cf_stitch_workspace_size, (rows, vocab), stream,
+                    tuning)

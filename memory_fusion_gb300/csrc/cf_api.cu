@@ -18,6 +18,7 @@
 #include "block_norms.h"
 #include "cf_internal.h"
 #include "grouped_internal.h"
+#include "logprobs.h"
 
 namespace {
 
@@ -2176,4 +2177,111 @@ extern "C" cf_status cf_stitch_block_norms_grad(
     return cf_stitch_block_norms_grad_ex(dy, dx_out, h, x_out, gate, post_weight, post_bias, pre_weight, dh, dx, dgate,
                                          dpost_weight, dpost_bias, dpre_weight, dpre_bias, rows, cols, gates, post, pre,
                                          scale, alpha, eps, dtype, workspace, workspace_bytes, stream, nullptr);
+}
+
+// -------------------------------------------------------------------------
+// Log probabilities of given tokens
+// -------------------------------------------------------------------------
+namespace {
+
+// what both directions check before they look at a pointer
+cf_status logprobs_sizes(int64_t rows, int64_t vocab, int64_t stride, float scale, int dtype) {
+    if (rows < 0 || vocab < 0 || !(scale > 0.f) || !(scale <= 3.4e38f)) return CF_ERR_INVALID_ARG;
+    if (dtype != CF_BF16 && dtype != CF_FP16 && dtype != CF_FP32) return CF_ERR_INVALID_ARG;
+    if (rows > 1 && stride < vocab) return CF_ERR_INVALID_ARG;
+    if (vocab > cf::kLogprobsMaxVocab || rows > (int64_t(1) << 27) || stride > (int64_t(1) << 32))
+        return CF_ERR_UNSUPPORTED;
+    return CF_OK;
+}
+
+}  // namespace
+
+extern "C" cf_status cf_stitch_logprobs_ex(const void *logits, const int64_t *targets, float *logprob, float *lse,
+                                           float *entropy, float *top_logprobs, int64_t *top_ids, int64_t rows,
+                                           int64_t vocab, int64_t stride, int64_t top, float scale, cf_dtype dtype,
+                                           void *workspace, size_t workspace_bytes, cf_stream_t stream,
+                                           const cf_tuning *tuning) {
+    cf_status st = logprobs_sizes(rows, vocab, stride, scale, int(dtype));
+    if (st != CF_OK) return st;
+    if (top < 0 || top > vocab) return CF_ERR_INVALID_ARG;
+    if (top > cf::kLogprobsMaxTop) return CF_ERR_UNSUPPORTED;
+    if (!workspace) return CF_ERR_INVALID_ARG;
+    if (rows == 0) return CF_OK;
+    if (vocab == 0 || !logits || (targets != nullptr) != (logprob != nullptr)) return CF_ERR_INVALID_ARG;
+    if ((top > 0) != (top_ids || top_logprobs)) return CF_ERR_INVALID_ARG;
+    if (!aligned_to(logits, dtype == CF_FP32 ? 4 : 2) || !aligned_to(targets, 8) || !aligned_to(logprob, 4) ||
+        !aligned_to(lse, 4) || !aligned_to(entropy, 4) || !aligned_to(top_logprobs, 4) || !aligned_to(top_ids, 8) ||
+        !aligned_to(workspace, 4))
+        return CF_ERR_MISALIGNED;
+    if (workspace_bytes < cf_stitch_workspace_size(rows, vocab)) return CF_ERR_WORKSPACE_TOO_SMALL;
+    cf::DeviceInfo dev;
+    st = linear_device(&dev);
+    if (st != CF_OK) return st;
+    cf::LogprobsArgs a{};
+    a.logits = logits;
+    a.targets = targets;
+    a.logprob = logprob, a.lse = lse, a.entropy = entropy, a.top_logprobs = top_logprobs, a.top_ids = top_ids;
+    a.err = static_cast<uint32_t *>(workspace);
+    a.rows = rows, a.stride = stride;
+    a.vocab = int(vocab), a.top = int(top), a.dtype = int(dtype);
+    a.scale = scale;
+    const cudaError_t e = cf::launch_logprobs(a, dev.sm_count, !tuning || tuning->disable_pdl == 0,
+                                              reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CF_OK : cuda_fail(e);
+}
+
+extern "C" cf_status cf_stitch_logprobs(const void *logits, const int64_t *targets, float *logprob, float *lse,
+                                        float *entropy, float *top_logprobs, int64_t *top_ids, int64_t rows,
+                                        int64_t vocab, int64_t stride, int64_t top, float scale, cf_dtype dtype,
+                                        void *workspace, size_t workspace_bytes, cf_stream_t stream) {
+    return cf_stitch_logprobs_ex(logits, targets, logprob, lse, entropy, top_logprobs, top_ids, rows, vocab, stride,
+                                 top, scale, dtype, workspace, workspace_bytes, stream, nullptr);
+}
+
+extern "C" cf_status cf_stitch_logprobs_grad_ex(const void *logits, const int64_t *targets, const float *lse,
+                                                const float *entropy, const float *dlogprob, const float *dlse,
+                                                const float *dentropy, void *dlogits, int64_t rows, int64_t vocab,
+                                                int64_t stride, int64_t dstride, float scale, cf_dtype dtype,
+                                                void *workspace, size_t workspace_bytes, cf_stream_t stream,
+                                                const cf_tuning *tuning) {
+    cf_status st = logprobs_sizes(rows, vocab, stride, scale, int(dtype));
+    if (st == CF_OK) st = logprobs_sizes(rows, vocab, dstride, scale, int(dtype));
+    if (st != CF_OK) return st;
+    if (cf::logprobs_grad_ctas(rows, vocab, int(dtype)) > (int64_t(1) << 31) - 1) return CF_ERR_UNSUPPORTED;
+    if (!workspace) return CF_ERR_INVALID_ARG;
+    if (rows == 0 || vocab == 0) return CF_OK;
+    if (!logits || !lse || !dlogits || (targets != nullptr) != (dlogprob != nullptr) ||
+        (entropy != nullptr) != (dentropy != nullptr) || (!dlogprob && !dlse && !dentropy))
+        return CF_ERR_INVALID_ARG;
+    const size_t size = dtype == CF_FP32 ? 4 : 2;
+    if (!aligned_to(logits, size) || !aligned_to(dlogits, size) || !aligned_to(targets, 8) || !aligned_to(lse, 4) ||
+        !aligned_to(entropy, 4) || !aligned_to(dlogprob, 4) || !aligned_to(dlse, 4) || !aligned_to(dentropy, 4) ||
+        !aligned_to(workspace, 4))
+        return CF_ERR_MISALIGNED;
+    if (dlogits == logits && rows > 1 && stride != dstride) return CF_ERR_INVALID_ARG;
+    if (workspace_bytes < cf_stitch_workspace_size(rows, vocab)) return CF_ERR_WORKSPACE_TOO_SMALL;
+    cf::DeviceInfo dev;
+    st = linear_device(&dev);
+    if (st != CF_OK) return st;
+    cf::LogprobsGradArgs a{};
+    a.logits = logits;
+    a.targets = targets;
+    a.lse = lse, a.entropy = entropy, a.dlogprob = dlogprob, a.dlse = dlse, a.dentropy = dentropy;
+    a.dlogits = dlogits;
+    a.err = static_cast<uint32_t *>(workspace);
+    a.rows = rows, a.stride = stride, a.dstride = dstride;
+    a.vocab = int(vocab), a.dtype = int(dtype);
+    a.scale = scale;
+    const cudaError_t e = cf::launch_logprobs_grad(a, !tuning || tuning->disable_pdl == 0,
+                                                   reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CF_OK : cuda_fail(e);
+}
+
+extern "C" cf_status cf_stitch_logprobs_grad(const void *logits, const int64_t *targets, const float *lse,
+                                             const float *entropy, const float *dlogprob, const float *dlse,
+                                             const float *dentropy, void *dlogits, int64_t rows, int64_t vocab,
+                                             int64_t stride, int64_t dstride, float scale, cf_dtype dtype,
+                                             void *workspace, size_t workspace_bytes, cf_stream_t stream) {
+    return cf_stitch_logprobs_grad_ex(logits, targets, lse, entropy, dlogprob, dlse, dentropy, dlogits, rows, vocab,
+                                      stride, dstride, scale, dtype, workspace, workspace_bytes, stream, nullptr);
 }

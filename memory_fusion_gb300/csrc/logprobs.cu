@@ -1,0 +1,475 @@
+// logprobs.cu -- what a model's logits are asked for: of z = scale * logits, a row,
+//     lse      = log sum exp z
+//     logprob  = z[target] - lse
+//     entropy  = lse - sum p z,  p = exp(z - lse)
+//     the top tokens and their log probabilities
+// in one pass over the row, and the gradient
+//     dlogits  = scale (dlogprob (1[target] - p) + dlse p - dentropy p (z - lse + entropy)).
+//
+// HBM bounds both: the logits are read once (the gradient: and written once).  A thread carries the running maximum m of
+// its logits, s = sum 2^d and t = sum d 2^d with d = (z - m) log2 e, so that lse = m + ln s and entropy = ln s - ln2 t / s
+// lose nothing to a large m.  (The difference comes first, the scale second: a row of the type's lowest number does not
+// overflow.)  Where few rows leave SMs idle a cluster of CTAs shares a row.
+//
+// Rows start anywhere: a row is cut at 16-byte boundaries of its memory into windows, the first and last of which may be
+// partial and are read number by number.
+//
+// Top tokens: a thread also remembers its largest logit and the first window that holds it.  The k-th largest of the
+// threads' (largest, window) pairs is a bound below which no top token can lie, and only k threads have anything on the
+// bound or above it; their windows are read again (from L2), and what reaches the bound, little more than k numbers, is
+// ranked by counting.  Pairs order equal logits by window, so equal logits in any number (a masked row) change nothing.
+// Rows made so that more than kCandidates numbers reach the bound are searched once for each of the k.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstddef>
+#include <cstdint>
+
+#include "logprobs.h"
+#include "pieces.cuh"
+#include "ptx.cuh"
+
+namespace cf {
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kLog2E = 1.4426950408889634f, kLn2F = 0.6931471805599453f;
+constexpr int kMaxThreads = 512, kMaxCluster = 8;
+constexpr int kCandidates = 1024;
+constexpr int kFly = 4;  // windows in flight
+constexpr uint32_t kInfoTarget = 0x72000000u;
+
+__device__ __forceinline__ float inf() { return __int_as_float(0x7f800000); }
+// the larger one; a NaN stays one
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// An order of all numbers as unsigned ones: -inf lowest, NaN above everything, the zeros alike.
+__device__ __forceinline__ uint32_t order(float v) {
+    const uint32_t b = __float_as_uint(v + 0.f);
+    if ((b & 0x7fffffffu) > 0x7f800000u) return kAll;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    if (o == kAll) return __uint_as_float(0x7fc00000u);
+    return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+// larger first, of equals the lower index
+__device__ __forceinline__ uint64_t pair_of(uint32_t o, uint32_t index) { return uint64_t(o) << 32 | uint32_t(~index); }
+
+// The windows of a row: 16 bytes of memory each, from the one that holds the row's first number.
+template <int kDt>
+struct Windows {
+    using E = typename Element<kDt>::type;
+    static constexpr int kN = 16 / int(sizeof(E));  // numbers of a window
+    const E *row;
+    int vocab, lead, count;  // lead: numbers of the first window that lie in front of the row
+    __device__ Windows(const E *r, int v) : row(r), vocab(v) {
+        lead = int((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(E));
+        count = int((int64_t(v) + lead + kN - 1) / kN);
+    }
+    __device__ __forceinline__ int first(int w) const { return w * kN - lead; }  // index of its first number
+    // what is not of the row is -inf
+    __device__ __forceinline__ void load(float (&x)[kN], int w) const {
+        const int i0 = first(w);
+        if (w < count && i0 >= 0 && i0 + kN <= vocab) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(row + i0);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                if constexpr (kDt == CF_FP32) x[i] = __uint_as_float(u[i]);
+                else x[i] = to_float<kDt>(uint16_t(u[i / 2] >> (i % 2 * 16)));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                x[i] = w < count && i0 + i >= 0 && i0 + i < vocab ? to_float<kDt>(row[i0 + i]) : -inf();
+        }
+    }
+};
+
+// running maximum, sum and weighted sum (16 bytes: a CTA sends m and s to another one as a pair)
+struct __align__(16) Stats {
+    float m, s, t;
+    __device__ __forceinline__ float ref() const { return m == -inf() ? 0.f : m; }
+    // the same with a larger maximum
+    __device__ __forceinline__ void raise(float to, float s2) {
+        if (to > m) {
+            if (s != 0.f) {
+                // (from 200 on r is 0, and 0 times an infinite d would be a NaN)
+                const float d = fminf((to - m) * s2, 200.f), r = ptx::ex2_approx(-d);
+                t = r * (t - d * s);
+                s *= r;
+            }
+            m = to;
+        }
+    }
+    __device__ __forceinline__ void add(Stats o, float s2) {
+        raise(o.m, s2);
+        o.raise(m, s2);
+        s += o.s;
+        t += o.t;
+    }
+};
+
+// One CTA's view of its share of a row, by whole CTA: the top k pairs (order, index) of it into top[0..k), largest first.
+template <int kDt>
+struct Share {
+    Windows<kDt> w;
+    int part, parts;  // this CTA of the row's
+    __device__ __forceinline__ int window(int step, int t) const {
+        return (step * parts + part) * int(blockDim.x) + t;
+    }
+    __device__ __forceinline__ int steps() const {  // of every thread
+        const int round = parts * int(blockDim.x);
+        return (w.count + round - 1) / round;
+    }
+};
+
+template <int kDt>
+__device__ void search_tops(const Share<kDt> &sh, int k, uint64_t *top, uint64_t *scratch) {
+    // every pair in turn: the largest below the one before
+    uint64_t below = ~uint64_t(0);
+    for (int i = 0; i < k; ++i) {
+        uint64_t best = 0;
+        for (int step = 0; step < sh.steps(); ++step) {
+            const int w = sh.window(step, int(threadIdx.x));
+            if (w >= sh.w.count) break;
+            float x[Windows<kDt>::kN];
+            sh.w.load(x, w);
+#pragma unroll
+            for (int j = 0; j < Windows<kDt>::kN; ++j) {
+                const int at = sh.w.first(w) + j;
+                const uint64_t p = pair_of(order(x[j]), uint32_t(at));
+                if (at >= 0 && at < sh.w.vocab && p < below && p > best) best = p;
+            }
+        }
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) best = max(best, __shfl_xor_sync(kAll, best, d));
+        if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = best;
+        __syncthreads();
+        for (int j = 0; j < int(blockDim.x >> 5); ++j) best = max(best, scratch[j]);
+        if (threadIdx.x == 0) top[i] = best;
+        below = best;
+        __syncthreads();
+    }
+}
+
+// most: the thread's largest logit with its first window, a pair (0: none)
+template <int kDt>
+__device__ void find_tops(const Share<kDt> &sh, uint64_t most, int k, uint64_t *top, uint64_t *pairs, int *chosen,
+                          uint64_t *bound, int *found) {
+    const int tid = int(threadIdx.x), n = int(blockDim.x);
+    pairs[tid] = most;
+    if (tid == 0) {
+        *found = 0;
+        *bound = 0;
+    }
+    if (tid < k) top[tid] = 0;
+    __syncthreads();
+    int rank = 0;
+    for (int i = 0; i < n; ++i) rank += pairs[i] > most;
+    // (threads without a window have no place; where fewer than k have one, everything is a candidate)
+    if (most != 0 && rank < k) chosen[rank] = tid;
+    if (most != 0 && rank == k - 1) *bound = most;
+    const int have = min(k, __syncthreads_count(most != 0));
+    const uint64_t least = *bound;
+    const uint32_t least_order = uint32_t(least >> 32), least_window = uint32_t(~least);
+    const int steps = sh.steps();
+    for (int i = tid; i < have * steps; i += n) {
+        const int who = i / steps, w = sh.window(i - who * steps, chosen[who]);
+        if (w >= sh.w.count) continue;
+        float x[Windows<kDt>::kN];
+        sh.w.load(x, w);
+#pragma unroll
+        for (int j = 0; j < Windows<kDt>::kN; ++j) {
+            const int at = sh.w.first(w) + j;
+            const uint32_t o = order(x[j]);
+            if (at < 0 || at >= sh.w.vocab) continue;
+            if (least == 0 || o > least_order || (o == least_order && uint32_t(w) <= least_window)) {
+                const int slot = atomicAdd(found, 1);
+                if (slot < kCandidates) pairs[slot] = pair_of(o, uint32_t(at));
+            }
+        }
+    }
+    __syncthreads();
+    const int all = *found;
+    if (all > kCandidates) {
+        search_tops(sh, k, top, pairs);
+        return;
+    }
+    for (int c = tid; c < all; c += n) {
+        const uint64_t p = pairs[c];
+        int r = 0;
+        for (int i = 0; i < all; ++i) r += pairs[i] > p;
+        if (r < k) top[r] = p;
+    }
+    __syncthreads();
+}
+
+template <int kDt, bool kEntropy, bool kTop>
+__global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobsArgs a) {
+    __shared__ Stats warp_stats[kMaxThreads / 32];
+    __shared__ Stats cta_stats[kMaxCluster];
+    __shared__ uint64_t pairs[kTop ? kCandidates : 1];
+    __shared__ uint64_t tops[kTop ? kMaxCluster * kLogprobsMaxTop : 1];  // of the row's CTAs, in the first one
+    __shared__ int chosen[kLogprobsMaxTop];
+    __shared__ uint64_t bound;
+    __shared__ int found;
+    static_assert(kCandidates >= kMaxThreads, "one pair a thread");
+    static_assert(sizeof(Stats) == 16 && offsetof(Stats, m) == 0 && offsetof(Stats, s) == 4 && offsetof(Stats, t) == 8,
+                  "sent as a pair and a number");
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    using E = typename Element<kDt>::type;
+    constexpr int kN = Windows<kDt>::kN;
+    const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    const int64_t r = int64_t(blockIdx.x) / a.cluster;
+    const int part = int(int64_t(blockIdx.x) - r * a.cluster);
+    const E *const row = static_cast<const E *>(a.logits) + r * a.stride;
+    const Share<kDt> sh{Windows<kDt>(row, a.vocab), part, a.cluster};
+    const float s2 = a.scale * kLog2E;
+
+    int64_t target = -1;
+    float given = 0.f;
+    if (part == 0 && tid == 0 && a.targets) {
+        target = a.targets[r];
+        if (target < -1 || target >= a.vocab) {
+            ptx::record_error(a.err, 8u /*CF_ERR_DEVICE_BOUNDS*/, kInfoTarget);
+            target = -1;
+        }
+        if (target >= 0) given = to_float<kDt>(row[target]);
+    }
+
+    Stats st{-inf(), 0.f, 0.f};
+    uint64_t most = 0;
+    const int steps = sh.steps();
+#pragma unroll 1
+    for (int step = 0; step < steps; step += kFly) {
+        float x[kFly][kN];
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) sh.w.load(x[i], sh.window(step + i, tid));
+        float high = -inf();
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) {
+            float m = x[i][0];
+#pragma unroll
+            for (int j = 1; j < kN; ++j) m = max_nan(m, x[i][j]);
+            if constexpr (kTop) {
+                const int w = sh.window(step + i, tid);
+                const uint64_t p = pair_of(order(m), uint32_t(w));
+                if (w < sh.w.count && p > most) most = p;
+            }
+            high = fmaxf(high, m);
+        }
+        st.raise(high, s2);
+        const float ref = st.ref();
+#pragma unroll
+        for (int i = 0; i < kFly; ++i)
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                float d = (x[i][j] - ref) * s2;
+                if constexpr (kEntropy) d = max_nan(d, -200.f);  // (of -inf: 2^-200 is 0, and 0 times it)
+                const float e = ptx::ex2_approx(d);
+                st.s += e;
+                if constexpr (kEntropy) st.t = fmaf(e, d, st.t);
+            }
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1)
+        st.add(Stats{__shfl_xor_sync(kAll, st.m, d), __shfl_xor_sync(kAll, st.s, d), __shfl_xor_sync(kAll, st.t, d)}, s2);
+    if (lane == 0) warp_stats[warp] = st;
+    if constexpr (kTop) find_tops(sh, most, a.top, tops + part * kLogprobsMaxTop, pairs, chosen, &bound, &found);
+    __syncthreads();
+    if (tid == 0) {
+        for (int i = 1; i < int(blockDim.x >> 5); ++i) st.add(warp_stats[i], s2);
+        cta_stats[part] = st;
+    }
+    if (a.cluster > 1) {
+        ptx::cluster_sync();  // every CTA has started
+        if (part != 0) {
+            if (tid == 0) {
+                const uint32_t to = ptx::mapa(ptx::smem_u32(cta_stats + part), 0u);
+                ptx::st_cluster_v2f32(to, st.m, st.s);
+                ptx::st_cluster_f32(to + 8, st.t);
+            }
+            if (kTop && tid < a.top) {
+                const uint64_t p = tops[part * kLogprobsMaxTop + tid];
+                ptx::st_cluster_v2f32(ptx::mapa(ptx::smem_u32(tops + part * kLogprobsMaxTop + tid), 0u),
+                                      __uint_as_float(uint32_t(p)), __uint_as_float(uint32_t(p >> 32)));
+            }
+        }
+        ptx::cluster_sync();
+        if (part != 0) return;
+        if (tid == 0)
+            for (int i = 1; i < a.cluster; ++i) st.add(cta_stats[i], s2);
+    }
+    if (tid == 0) {
+        warp_stats[0] = st;
+        const float log_s = logf(st.s);
+        const bool none = st.s == 0.f;  // nothing but -inf
+        if (a.lse) a.lse[r] = none ? -inf() : fmaf(st.ref(), a.scale, log_s);
+        if (a.logprob)
+            a.logprob[r] = target < 0 ? 0.f : none ? -inf() : (given - st.ref()) * a.scale - log_s;
+        if (kEntropy && a.entropy) a.entropy[r] = none ? 0.f : log_s - kLn2F * (st.t / st.s);
+    }
+    if constexpr (kTop) {
+        __syncthreads();
+        st = warp_stats[0];
+        const float log_s = logf(st.s);
+        for (int c = tid; c < a.cluster * a.top; c += int(blockDim.x)) {
+            const int at = c / a.top * kLogprobsMaxTop + c % a.top;
+            const uint64_t p = tops[at];
+            int rank = c % a.top;
+            if (a.cluster > 1) {
+                rank = 0;
+                for (int i = 0; i < a.cluster; ++i)
+                    for (int j = 0; j < a.top; ++j) rank += tops[i * kLogprobsMaxTop + j] > p;
+            }
+            if (p != 0 && rank < a.top) {
+                const size_t out = size_t(r) * a.top + rank;
+                if (a.top_ids) a.top_ids[out] = uint32_t(~p);
+                if (a.top_logprobs)
+                    a.top_logprobs[out] =
+                        st.s == 0.f ? -inf() : (value_of(uint32_t(p >> 32)) - st.ref()) * a.scale - log_s;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// gradient
+// ---------------------------------------------------------------------------
+constexpr int kGradThreads = 256;
+
+template <int kDt, bool kEntropy>
+__global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LogprobsGradArgs a) {
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    using E = typename Element<kDt>::type;
+    constexpr int kN = Windows<kDt>::kN;
+    const int64_t r = int64_t(blockIdx.x) / a.chunks;
+    const int chunk = int(int64_t(blockIdx.x) - r * a.chunks);
+    const Windows<kDt> win(static_cast<const E *>(a.logits) + r * a.stride, a.vocab);
+    E *const out = static_cast<E *>(a.dlogits) + r * a.dstride;
+    const bool same = (reinterpret_cast<uintptr_t>(out) & 15u) == (reinterpret_cast<uintptr_t>(win.row) & 15u);
+    int64_t target = a.targets ? a.targets[r] : -1;
+    if (target < -1 || target >= a.vocab) {
+        if (threadIdx.x == 0) ptx::record_error(a.err, 8u /*CF_ERR_DEVICE_BOUNDS*/, kInfoTarget);
+        target = -1;
+    }
+    const float lse = a.lse[r];
+    const float given = target >= 0 && a.dlogprob ? a.dlogprob[r] : 0.f;
+    const float dh = kEntropy ? a.dentropy[r] : 0.f;
+    // p times (c0 + c1 d), d = z - lse
+    const float c0 = (a.dlse ? a.dlse[r] : 0.f) - given - (kEntropy ? dh * a.entropy[r] : 0.f), c1 = -dh;
+    const bool none = lse == -inf();
+    float x[kFly][kN];
+    const int w0 = chunk * (kFly * kGradThreads) + int(threadIdx.x);
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) win.load(x[i], w0 + i * kGradThreads);
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+        const int w = w0 + i * kGradThreads, i0 = win.first(w);
+        if (w >= win.count) break;
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            float d = fmaf(x[i][j], a.scale, -lse);
+            if constexpr (kEntropy) d = max_nan(d, -200.f);  // (of -inf: 2^-288 is 0, and 0 times it)
+            const float p = ptx::ex2_approx(d * kLog2E);
+            float g = p * (kEntropy ? fmaf(c1, d, c0) : c0);
+            if (i0 + j == target) g += given;
+            x[i][j] = none ? 0.f : g * a.scale;
+        }
+        if (same && i0 >= 0 && i0 + kN <= a.vocab) {
+            uint32_t u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (kDt == CF_FP32) u[j] = __float_as_uint(x[i][j]);
+                else u[j] = uint32_t(from_float<kDt>(x[i][2 * j])) | uint32_t(from_float<kDt>(x[i][2 * j + 1])) << 16;
+            }
+            *reinterpret_cast<uint4 *>(out + i0) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+                if (i0 + j >= 0 && i0 + j < a.vocab) out[i0 + j] = from_float<kDt>(x[i][j]);
+        }
+    }
+}
+
+template <int kDt>
+const void *forward_kernel(bool entropy, bool top) {
+    if (entropy)
+        return top ? reinterpret_cast<const void *>(&logprobs_kernel<kDt, true, true>)
+                   : reinterpret_cast<const void *>(&logprobs_kernel<kDt, true, false>);
+    return top ? reinterpret_cast<const void *>(&logprobs_kernel<kDt, false, true>)
+               : reinterpret_cast<const void *>(&logprobs_kernel<kDt, false, false>);
+}
+template <int kDt>
+const void *grad_kernel(bool entropy) {
+    return entropy ? reinterpret_cast<const void *>(&logprobs_grad_kernel<kDt, true>)
+                   : reinterpret_cast<const void *>(&logprobs_grad_kernel<kDt, false>);
+}
+
+cudaError_t launch(const void *fn, unsigned ctas, int threads, int cluster, bool pdl, cudaStream_t stream, void **args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = unsigned(cluster);
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs(LogprobsArgs a, int sms, bool pdl, cudaStream_t stream) {
+    const int per = 16 / type_bytes(a.dtype);
+    const int64_t windows = (int64_t(a.vocab) + 2 * per - 2) / per;  // the most a row can have
+    int cluster = 1;
+    while (cluster < kMaxCluster && 2 * cluster * a.rows <= 2 * sms && windows > 64 * cluster) cluster *= 2;
+    const int64_t mine = (windows + cluster - 1) / cluster;
+    int threads = 64;
+    while (threads < 256 && threads * kFly < mine) threads *= 2;
+    a.cluster = cluster;
+    const bool entropy = a.entropy != nullptr, top = a.top > 0;
+    const void *fn = a.dtype == CF_BF16   ? forward_kernel<CF_BF16>(entropy, top)
+                     : a.dtype == CF_FP16 ? forward_kernel<CF_FP16>(entropy, top)
+                                          : forward_kernel<CF_FP32>(entropy, top);
+    void *args[] = {&a};
+    return launch(fn, unsigned(a.rows * cluster), threads, cluster, pdl, stream, args);
+}
+
+int64_t logprobs_grad_ctas(int64_t rows, int64_t vocab, int dtype) {
+    const int per = 16 / type_bytes(dtype);
+    const int64_t windows = (vocab + 2 * per - 2) / per;
+    return rows * ((windows + kFly * kGradThreads - 1) / (kFly * kGradThreads));
+}
+
+cudaError_t launch_logprobs_grad(LogprobsGradArgs a, bool pdl, cudaStream_t stream) {
+    const int64_t ctas = logprobs_grad_ctas(a.rows, a.vocab, a.dtype);
+    a.chunks = int(ctas / a.rows);
+    const bool entropy = a.dentropy != nullptr;
+    const void *fn = a.dtype == CF_BF16   ? grad_kernel<CF_BF16>(entropy)
+                     : a.dtype == CF_FP16 ? grad_kernel<CF_FP16>(entropy)
+                                          : grad_kernel<CF_FP32>(entropy);
+    void *args[] = {&a};
+    return launch(fn, unsigned(ctas), kGradThreads, 1, pdl, stream, args);
+}
+
+}  // namespace cf
