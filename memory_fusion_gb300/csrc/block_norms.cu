@@ -39,45 +39,85 @@ struct Group {
     int warp;       // its warp among them
     uint32_t bar;   // named barrier
     uint32_t rank;  // of the CTA in the cluster
-    float2 *slots;  // [2][warps * cluster], one half for every second exchange
+    float *slots;   // two halves of `half` numbers, one for every second exchange
+    int half;
     int turn;
 };
 
-// a and b, each summed over the row; every thread of the row gets the same bits
-template <bool kCluster>
-__device__ __forceinline__ float2 row_sum(Group &g, float a, float b) {
+// v summed over the row (of one CTA); every thread of the row gets the same bits.  The slots behind the last warp's, up
+// to a multiple of four, hold zeros.
+__device__ __forceinline__ float row_sum(Group &g, float v) {
     if (g.lanes >= 32) {
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) {
-            a += __shfl_xor_sync(kAll, a, d);
-            b += __shfl_xor_sync(kAll, b, d);
-        }
+        for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
     } else {
-        for (int d = g.lanes >> 1; d >= 1; d >>= 1) {
-            a += __shfl_xor_sync(kAll, a, d);
-            b += __shfl_xor_sync(kAll, b, d);
-        }
+        for (int d = g.lanes >> 1; d >= 1; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
     }
-    if (g.warps == 1 && !kCluster) return make_float2(a, b);
-    const int all = g.warps * (kCluster ? g.cluster : 1);
-    float2 *const slots = g.slots + (g.turn & 1) * all;
+    if (g.warps == 1) return v;
+    float *const slots = g.slots + (g.turn & 1) * g.half;
     ++g.turn;
-    if constexpr (kCluster) {
-        // lane l tells CTA l of the cluster
-        const int lane = threadIdx.x & 31;
-        if (lane < g.cluster)
-            ptx::st_cluster_v2f32(ptx::mapa(ptx::smem_u32(slots + g.rank * g.warps + g.warp), uint32_t(lane)), a, b);
-        ptx::cluster_sync();
-    } else {
-        if ((threadIdx.x & 31) == 0) slots[g.warp] = make_float2(a, b);
-        ptx::named_bar_sync(g.bar, uint32_t(g.lanes));
-    }
-    float2 s = make_float2(0.f, 0.f);
-    for (int i = 0; i < all; ++i) {
-        const float2 v = slots[i];
-        s.x += v.x, s.y += v.y;
+    if ((threadIdx.x & 31) == 0) slots[g.warp] = v;
+    ptx::named_bar_sync(g.bar, uint32_t(g.lanes));
+    float s = 0.f;
+    for (int i = 0; i < g.warps; i += 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(slots + i);
+        s += (q.x + q.y) + (q.z + q.w);
     }
     return s;
+}
+
+// kV (a power of two) values at once, over a cluster's row too.  In a warp each step halves the values that a lane goes
+// on with (it hands the others to its partner), so eight values take 9 shuffles where one by one they take 40; then lane
+// l holds value place(l % kV) of the warp, and the warps' are added the same way round.
+template <int kV>
+__device__ __forceinline__ constexpr int place(int lane) {
+    int p = 0;
+    for (int k = kV / 2, d = 1; k >= 1; k /= 2, d *= 2) p += lane & d ? k : 0;
+    return p;
+}
+template <int kV, bool kCluster>
+__device__ __forceinline__ void row_sums(Group &g, float (&v)[kV]) {
+    if (!kCluster && g.lanes < 32) {
+        for (int d = g.lanes >> 1; d >= 1; d >>= 1) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) v[i] += __shfl_xor_sync(kAll, v[i], d);
+        }
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    float w[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) w[i] = v[i];
+#pragma unroll
+    for (int k = kV / 2, d = 1; k >= 1; k /= 2, d *= 2) {
+        const bool upper = lane & d;
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+            w[i] = (upper ? w[i + k] : w[i]) + __shfl_xor_sync(kAll, upper ? w[i] : w[i + k], d);
+    }
+#pragma unroll
+    for (int d = kV; d <= 16; d *= 2) w[0] += __shfl_xor_sync(kAll, w[0], d);
+    float s = w[0];
+    if (kCluster || g.warps > 1) {
+        float *const slots = g.slots + (g.turn & 1) * g.half;
+        ++g.turn;
+        const int mine = (kCluster ? int(g.rank) * g.warps : 0) + g.warp;
+        if constexpr (kCluster) {
+            for (int c = lane / kV; c < g.cluster; c += 32 / kV)
+                ptx::st_cluster_f32(ptx::mapa(ptx::smem_u32(slots + mine * kV + lane % kV), uint32_t(c)), s);
+            ptx::cluster_sync();
+        } else {
+            if (lane < kV) slots[mine * kV + lane] = s;
+            ptx::named_bar_sync(g.bar, uint32_t(g.lanes));
+        }
+        const int all = g.warps * (kCluster ? g.cluster : 1);
+        s = 0.f;
+        for (int i = lane / kV; i < all; i += 32 / kV) s += slots[i * kV + lane % kV];
+#pragma unroll
+        for (int d = kV; d <= 16; d *= 2) s += __shfl_xor_sync(kAll, s, d);
+    }
+#pragma unroll
+    for (int i = 0; i < kV; ++i) v[place<kV>(i)] = __shfl_sync(kAll, s, i);
 }
 
 // Columns of a thread's piece p: eight in a row where rows and vectors are 16-byte aligned, else every lanes-th.
@@ -146,7 +186,7 @@ __device__ __forceinline__ float2 spread(Group &g, int norm, const float (&x)[kP
         for (int p = 0; p < kP; ++p)
 #pragma unroll
             for (int j = 0; j < 8; ++j) s += x[p][j];
-        mean = row_sum<false>(g, s, 0.f).x * inv_n;
+        mean = row_sum(g, s) * inv_n;
     }
     float s = 0.f;
 #pragma unroll
@@ -156,12 +196,13 @@ __device__ __forceinline__ float2 spread(Group &g, int norm, const float (&x)[kP
             const float d = cols.live(p, j) ? x[p][j] - mean : 0.f;
             s = fmaf(d, d, s);
         }
-    return make_float2(mean, __frsqrt_rn(fmaf(row_sum<false>(g, s, 0.f).x, inv_n, eps)));
+    return make_float2(mean, __frsqrt_rn(fmaf(row_sum(g, s), inv_n, eps)));
 }
 
 template <int kDt, bool kVec, int kP>
-__global__ void __launch_bounds__(kP == 4 ? 1024 : 512) block_norms_kernel(const BlockNormsArgs a) {
-    __shared__ float2 slots[64];
+__global__ void __launch_bounds__(kP == 4 ? 1024 : 512, kP == 4 ? 1 : 2) block_norms_kernel(const BlockNormsArgs a) {
+    __shared__ __align__(16) float slots[2 * 32 + 8 * 8];  // of each of up to 8 groups of warps, rounded up to four
+    for (int i = threadIdx.x; i < int(sizeof(slots) / 4); i += blockDim.x) slots[i] = 0.f;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     using E = typename Element<kDt>::type;
@@ -174,8 +215,10 @@ __global__ void __launch_bounds__(kP == 4 ? 1024 : 512) block_norms_kernel(const
     g.warp = g.t >> 5;
     g.bar = 1 + uint32_t(group);
     g.rank = 0;
-    g.slots = slots + group * 2 * g.warps;
+    g.half = (g.warps + 3) & ~3;
+    g.slots = slots + group * 2 * g.half;
     g.turn = 0;
+    __syncthreads();
     const Columns<kVec> cols{g.t, a.lanes, 0, a.cols};
     const int groups = int(blockDim.x) / a.lanes;
     const float inv_n = 1.f / float(a.cols);
@@ -227,37 +270,18 @@ __global__ void __launch_bounds__(kP == 4 ? 1024 : 512) block_norms_kernel(const
 // ---------------------------------------------------------------------------
 // gradient
 // ---------------------------------------------------------------------------
-// Means and reciprocal roots of both norms' rows (h and x'), in two exchanges, one without a LayerNorm.
-template <bool kVec, bool kCluster>
-__device__ __forceinline__ void spreads(Group &g, int post, int pre, const float (&h)[8], const float (&x)[8],
-                                        const Columns<kVec> &cols, float inv_n, float eps, float2 &sh, float2 &sx) {
-    sh = sx = make_float2(0.f, 1.f);
-    if (post == CF_NORM_NONE && pre == CF_NORM_NONE) return;
-    if (post == CF_NORM_LAYER || pre == CF_NORM_LAYER) {
-        float a = 0.f, b = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a += h[j], b += x[j];
-        const float2 s = row_sum<kCluster>(g, a, b);
-        if (post == CF_NORM_LAYER) sh.x = s.x * inv_n;
-        if (pre == CF_NORM_LAYER) sx.x = s.y * inv_n;
-    }
-    float a = 0.f, b = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const bool live = cols.live(0, j);
-        const float dh = live ? h[j] - sh.x : 0.f, dx = live ? x[j] - sx.x : 0.f;
-        a = fmaf(dh, dh, a);
-        b = fmaf(dx, dx, b);
-    }
-    const float2 s = row_sum<kCluster>(g, a, b);
-    if (post != CF_NORM_NONE) sh.y = __frsqrt_rn(fmaf(s.x, inv_n, eps));
-    if (pre != CF_NORM_NONE) sx.y = __frsqrt_rn(fmaf(s.y, inv_n, eps));
-}
-
-// kShift: sums for the biases, too.  kGate: a gate, whose rows' sums are closed where the next gate begins.
-template <int kDt, bool kVec, bool kCluster, bool kGate, bool kShift>
+// With hc and xc the rows without their means (RMSNorm: the rows), g2 = dy w2 and w1 = scale gate weight, every sum that
+// the row needs is one over products of what is loaded:
+//     sum g2 x^ = r2 sum g2 xc,
+//     d  = dx' + r2 (g2 - mean(g2) - x^ mean(g2 x^)),
+//     sum w1 d h^ = r1 (sum w1 hc dx' + r2 (sum w1 hc g2 - mean(g2) sum w1 hc - r2 mean(g2 x^) sum w1 hc xc)),
+// so one exchange between the threads serves where three would follow one another (16384 x 4096 bf16: 287 us with
+// three).  A LayerNorm's means come one exchange before.
+// kFull: LayerNorms or biases, too.  kGate: a gate, whose rows' sums are closed where the next gate begins.
+template <int kDt, bool kVec, bool kCluster, bool kGate, bool kFull>
 __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsGradArgs a) {
-    __shared__ float2 slots[2 * 16 * 8];
+    constexpr int kV = kFull ? 16 : 8;
+    __shared__ float slots[2 * 16 * kV * (kCluster ? 8 : 1)];
     __shared__ float sums[kCluster ? 1 : 512 * 8];
     using E = typename Element<kDt>::type;
     ptx::griddep_launch_dependents();
@@ -271,33 +295,36 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
     g.warp = g.t >> 5;
     g.bar = 1 + uint32_t(group);
     g.rank = kCluster ? ptx::cluster_ctarank() : 0u;
-    g.slots = slots + group * 2 * g.warps;
+    g.half = g.warps * kV * (kCluster ? a.cluster : 1);
+    g.slots = slots + group * 2 * g.half;
     g.turn = 0;
     const Columns<kVec> cols{g.t, a.lanes, int(g.rank) * a.lanes * 8, a.cols};
     const int groups = int(blockDim.x) / a.lanes;
     const int set = int(blockIdx.x) / a.cluster, worker = set * groups + group;
     const int64_t first = worker * a.chunk, last = min(a.rows, first + a.chunk);
     const float inv_n = 1.f / float(a.cols);
+    const bool lh = kFull && a.post == CF_NORM_LAYER, lx = kFull && a.pre == CF_NORM_LAYER;
     if constexpr (kCluster) ptx::cluster_sync();  // nobody writes into a CTA that has not started
 
     float w2[8], w1[8];  // Pre's weight; scale * gate * Post's weight
     load_vector<kVec>(w2, a.pre_weight, 1.f, cols, 0);
     load_vector<kVec>(w1, a.post_weight, 1.f, cols, 0);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w1[j] *= a.scale;
+    for (int j = 0; j < 8; ++j) w1[j] = cols.live(0, j) ? w1[j] * a.scale : 0.f;
     float sa[8], sb[8], sc[8], sd[8], ta[8], tb[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) sa[j] = sb[j] = sc[j] = sd[j] = ta[j] = tb[j] = 0.f;
 
     Piece<kDt> gate, next[4];
     int64_t gate_at = 0, gate_end = 0;  // the gate in hand, the first row behind its rows
+    auto gate_of = [&](int j) { return a.gate ? gate.get(j) : 1.f; };
     auto take_gate = [&](int64_t of) {
         gate_at = of;
         gate_end = (of + 1) * int64_t(a.rows_per_gate);
-        load_piece<kDt, kVec>(gate, static_cast<const E *>(a.gate) + size_t(of) * a.cols, cols, 0, true);
+        load_piece<kDt, kVec>(gate, static_cast<const E *>(a.gate) + size_t(of) * a.cols, cols, 0, a.gate != nullptr);
         load_vector<kVec>(w1, a.post_weight, 1.f, cols, 0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w1[j] *= a.scale * gate.get(j);
+        for (int j = 0; j < 8; ++j) w1[j] = cols.live(0, j) ? w1[j] * a.scale * gate_of(j) : 0.f;
     };
     gate.zero();
     if (kGate && first < last) take_gate(uint32_t(first) / a.rows_per_gate);
@@ -313,71 +340,89 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
     for (int64_t i = 0; i < a.chunk; ++i) {
         const int64_t r = first + i;
         const bool on = r < last;
-        float h[8], x[8], dy[8], dx[8];
-        next[0].unpack(h), next[1].unpack(x), next[2].unpack(dy), next[3].unpack(dx);
+        Piece<kDt> hp = next[0], xp = next[1], yp = next[2], dp = next[3];
         fetch(r + 1, r + 1 < last);
         const size_t at = on ? size_t(r) * a.cols : 0;
-        float2 sh, sx;
-        spreads<kVec, kCluster>(g, a.post, a.pre, h, x, cols, inv_n, a.eps, sh, sx);
-        if (!on) sh.y = sx.y = 0.f;  // (an eps of 0 would make a NaN of a row that is not there)
-        if (a.dy) {
-            float s0 = 0.f, s1 = 0.f;
+        float mh = 0.f, mx = 0.f;
+        if (lh || lx) {
+            float v[2] = {0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] = cols.live(0, j) ? (x[j] - sx.x) * sx.y : 0.f;
-                sc[j] = fmaf(dy[j], x[j], sc[j]);
-                if constexpr (kShift) sd[j] += dy[j];
-                dy[j] *= w2[j];
-                s0 += dy[j];
-                s1 = fmaf(dy[j], x[j], s1);
-            }
-            float2 m = make_float2(0.f, 0.f);
-            if (a.pre != CF_NORM_NONE) m = row_sum<kCluster>(g, s0, s1);
-            m.x = a.pre == CF_NORM_LAYER ? m.x * inv_n : 0.f;
-            m.y *= inv_n;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) dx[j] = fmaf(sx.y, dy[j] - m.x - x[j] * m.y, dx[j]);
+            for (int j = 0; j < 8; ++j) v[0] += hp.get(j), v[1] += xp.get(j);
+            row_sums<2, kCluster>(g, v);
+            mh = lh ? v[0] * inv_n : 0.f;
+            mx = lx ? v[1] * inv_n : 0.f;
         }
-        float s0 = 0.f, s1 = 0.f;
+        float v[kV];
+#pragma unroll
+        for (int k = 0; k < kV; ++k) v[k] = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            h[j] = cols.live(0, j) ? (h[j] - sh.x) * sh.y : 0.f;
-            sa[j] = fmaf(dx[j], h[j], sa[j]);
-            if constexpr (kShift) sb[j] += cols.live(0, j) ? dx[j] : 0.f;
-            x[j] = dx[j] * w1[j];
-            s0 += cols.live(0, j) ? x[j] : 0.f;
-            s1 = fmaf(x[j], h[j], s1);
-            dx[j] *= a.alpha;
+            const bool live = !kFull || cols.live(0, j);
+            const float h = live ? hp.get(j) - mh : 0.f, x = live ? xp.get(j) - mx : 0.f;
+            const float g2 = yp.get(j) * w2[j], d = dp.get(j), wh = w1[j] * h;
+            v[0] = fmaf(h, h, v[0]);
+            v[1] = fmaf(x, x, v[1]);
+            v[2] = fmaf(g2, x, v[2]);
+            v[3] = fmaf(wh, d, v[3]);
+            v[4] = fmaf(wh, g2, v[4]);
+            v[5] = fmaf(wh, x, v[5]);
+            if constexpr (kFull) {
+                v[6] += g2;
+                v[7] += wh;
+                v[8] = fmaf(w1[j], d, v[8]);
+                v[9] = fmaf(w1[j], g2, v[9]);
+                v[10] = fmaf(w1[j], x, v[10]);
+                v[11] += w1[j];
+            }
+        }
+        row_sums<kV, kCluster>(g, v);
+        // (an eps of 0 would make a NaN of a row that is not there)
+        const float r1 = a.post == CF_NORM_NONE ? 1.f : on ? __frsqrt_rn(fmaf(v[0], inv_n, a.eps)) : 0.f;
+        const float r2 = a.pre == CF_NORM_NONE ? 1.f : on ? __frsqrt_rn(fmaf(v[1], inv_n, a.eps)) : 0.f;
+        const float ma = lx ? v[kFull ? 6 : 0] * inv_n : 0.f;            // mean(g2)
+        const float mb = a.pre == CF_NORM_NONE ? 0.f : r2 * r2 * (v[2] * inv_n);  // r2 mean(g2 x^)
+        // r1 mean(w1 d h^), mean(w1 d)
+        const float na = a.post == CF_NORM_NONE
+                             ? 0.f
+                             : r1 * r1 * (v[3] + r2 * (v[4] - (kFull ? ma * v[kFull ? 7 : 0] : 0.f) - mb * v[5])) * inv_n;
+        const float nb =
+            lh ? (v[kFull ? 8 : 0] + r2 * (v[kFull ? 9 : 0] - ma * v[kFull ? 11 : 0] - mb * v[kFull ? 10 : 0])) * inv_n
+               : 0.f;
+        float dx[8], dh[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool live = !kFull || cols.live(0, j);
+            const float h = live ? hp.get(j) - mh : 0.f, x = live ? xp.get(j) - mx : 0.f, y = yp.get(j);
+            const float d = live ? fmaf(r2, y * w2[j] - ma - mb * x, dp.get(j)) : 0.f;
+            sc[j] = fmaf(y, r2 * x, sc[j]);
+            sa[j] = fmaf(d, r1 * h, sa[j]);
+            if constexpr (kFull) sd[j] += y, sb[j] += d;
+            dx[j] = d * a.alpha;
+            dh[j] = r1 * (w1[j] * d - nb - na * h);
         }
         if (a.dx) store_piece<kDt, kVec>(static_cast<E *>(a.dx) + at, dx, cols, 0, on);
-        float2 m = make_float2(0.f, 0.f);
-        if (a.post != CF_NORM_NONE) m = row_sum<kCluster>(g, s0, s1);
-        m.x = a.post == CF_NORM_LAYER ? m.x * inv_n : 0.f;
-        m.y *= inv_n;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = sh.y * (x[j] - m.x - h[j] * m.y);
-        store_piece<kDt, kVec>(static_cast<E *>(a.dh) + at, x, cols, 0, on);
+        store_piece<kDt, kVec>(static_cast<E *>(a.dh) + at, dh, cols, 0, on);
         if constexpr (kGate) {
             if (on && (r + 1 == last || r + 1 == gate_end)) {  // its last row here
-                float v[8], w[8], b[8];
+                float w[8], b[8];
                 load_vector<kVec>(w, a.post_weight, 1.f, cols, 0);
-                load_vector<kVec>(b, a.post_bias, 0.f, cols, 0);
+                load_vector<kVec>(b, kFull ? a.post_bias : nullptr, 0.f, cols, 0);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    v[j] = a.scale * fmaf(w[j], sa[j], kShift ? b[j] * sb[j] : 0.f);
-                    const float k = a.scale * gate.get(j);
+                    dx[j] = a.scale * fmaf(w[j], sa[j], b[j] * sb[j]);
+                    const float k = a.scale * gate_of(j);
                     ta[j] = fmaf(k, sa[j], ta[j]);
-                    if constexpr (kShift) tb[j] = fmaf(k, sb[j], tb[j]);
+                    if constexpr (kFull) tb[j] = fmaf(k, sb[j], tb[j]);
                     sa[j] = sb[j] = 0.f;
                 }
                 const int64_t from = gate_end - int64_t(a.rows_per_gate);
                 if (a.dgate && from >= first && gate_end <= last) {
-                    store_piece<kDt, kVec>(static_cast<E *>(a.dgate) + size_t(gate_at) * a.cols, v, cols, 0, true);
+                    store_piece<kDt, kVec>(static_cast<E *>(a.dgate) + size_t(gate_at) * a.cols, dx, cols, 0, true);
                 } else if (a.dgate) {  // slot 0: begun by a worker before; slot 1: here, and goes on
                     float *const slot = a.slots + (size_t(2) * worker + (from >= first ? 1 : 0)) * a.cols;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (cols.live(0, j)) __stcg(slot + cols.at(0, j), v[j]);
+                        if (cols.live(0, j)) __stcg(slot + cols.at(0, j), dx[j]);
                 }
                 if (r + 1 < last) take_gate(gate_at + 1);
             }
@@ -414,9 +459,10 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
     if constexpr (kCluster) ptx::cluster_sync();  // no CTA leaves while its peers may still write to it
 }
 
-// The workers' sums added in order: 32 columns a CTA, a warp every 32nd term, then the warps.
-__global__ void __launch_bounds__(1024) block_norms_sums_kernel(const BlockNormsGradArgs a, int nsums, int gates_first) {
-    __shared__ float part[32][33];
+// The workers' sums added in order: 32 columns a CTA, a warp every kSumWarps-th term, then the warps.
+constexpr int kSumWarps = 8, kSumFly = 8;
+__global__ void __launch_bounds__(kSumWarps * 32) block_norms_sums_kernel(const BlockNormsGradArgs a, int nsums, int gates_first) {
+    __shared__ float part[kSumWarps][32];
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -454,20 +500,20 @@ __global__ void __launch_bounds__(1024) block_norms_sums_kernel(const BlockNorms
         terms = int(last - w);
     }
     float s = head && warp == 0 && live ? __ldcg(head + c) : 0.f;
-    for (int i = warp; i < terms; i += 128) {
-        float x[4];
+    for (int i = warp; i < terms; i += kSumWarps * kSumFly) {
+        float x[kSumFly];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            x[k] = live && i + 32 * k < terms ? __ldcg(from + (i + 32 * k) * step + c) : 0.f;
+        for (int k = 0; k < kSumFly; ++k)
+            x[k] = live && i + kSumWarps * k < terms ? __ldcg(from + (i + kSumWarps * k) * step + c) : 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s += x[k];
+        for (int k = 0; k < kSumFly; ++k) s += x[k];
     }
     part[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || !live) return;
     s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) s += part[k][lane];
+    for (int k = 0; k < kSumWarps; ++k) s += part[k][lane];
     if (of < 0) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -515,19 +561,20 @@ const void *forward_kernel(int pieces) {
            : pieces == 2 ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, kVec, 2>)
                          : reinterpret_cast<const void *>(&block_norms_kernel<kDt, kVec, 4>);
 }
-template <int kDt, bool kVec, bool kCluster>
-const void *grad_kernel(bool gate, bool shift) {
-    if (gate)
-        return shift ? reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, kVec, kCluster, true, true>)
-                     : reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, kVec, kCluster, true, false>);
-    return shift ? reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, kVec, kCluster, false, true>)
-                 : reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, kVec, kCluster, false, false>);
-}
+// (what is rare is compiled in its widest form alone)
 template <int kDt>
-const void *grad_kernel_of(bool vec, bool cluster, bool gate, bool shift) {
+const void *grad_kernel(bool vec, bool cluster, bool gate, bool full) {
+    if (!vec)
+        return cluster ? reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, false, true, true, true>)
+                       : reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, false, false, true, true>);
     if (cluster)
-        return vec ? grad_kernel<kDt, true, true>(gate, shift) : grad_kernel<kDt, false, true>(gate, shift);
-    return vec ? grad_kernel<kDt, true, false>(gate, shift) : grad_kernel<kDt, false, false>(gate, shift);
+        return full ? reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, true, true, true, true>)
+                    : reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, true, true, true, false>);
+    if (gate)
+        return full ? reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, true, false, true, true>)
+                    : reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, true, false, true, false>);
+    return full ? reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, true, false, false, true>)
+                : reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, true, false, false, false>);
 }
 
 }  // namespace
@@ -566,11 +613,12 @@ cudaError_t launch_block_norms_grad(BlockNormsGradArgs a, const BlockNormsGradPl
     a.cluster = p.cluster;
     a.chunk = p.chunk;
     a.sets = p.sets;
-    const bool gate = a.gate != nullptr, shift = a.post_bias || a.sum_at[1] >= 0 || a.sum_at[3] >= 0;
-    const bool cluster = p.cluster > 1;
-    const void *fn = a.dtype == CF_BF16   ? grad_kernel_of<CF_BF16>(vec, cluster, gate, shift)
-                     : a.dtype == CF_FP16 ? grad_kernel_of<CF_FP16>(vec, cluster, gate, shift)
-                                          : grad_kernel_of<CF_FP32>(vec, cluster, gate, shift);
+    const bool gate = a.gate != nullptr, cluster = p.cluster > 1;
+    const bool full = a.post_bias || a.sum_at[1] >= 0 || a.sum_at[3] >= 0 || a.post == CF_NORM_LAYER ||
+                      a.pre == CF_NORM_LAYER;
+    const void *fn = a.dtype == CF_BF16   ? grad_kernel<CF_BF16>(vec, cluster, gate, full)
+                     : a.dtype == CF_FP16 ? grad_kernel<CF_FP16>(vec, cluster, gate, full)
+                                          : grad_kernel<CF_FP32>(vec, cluster, gate, full);
     void *args[] = {&a};
     cudaError_t e = launch(fn, dim3(unsigned(p.sets * p.cluster)), p.threads, p.cluster, pdl, stream, args);
     if (e != cudaSuccess) return e;
@@ -582,7 +630,7 @@ cudaError_t launch_block_norms_grad(BlockNormsGradArgs a, const BlockNormsGradPl
     if (nsums + shared == 0) return cudaSuccess;
     void *args2[] = {&a, &nsums, &gates_first};
     return launch(reinterpret_cast<const void *>(&block_norms_sums_kernel),
-                  dim3(unsigned((a.cols + 31) / 32) * unsigned(nsums + shared)), 1024, 1, pdl, stream, args2);
+                  dim3(unsigned((a.cols + 31) / 32) * unsigned(nsums + shared)), kSumWarps * 32, 1, pdl, stream, args2);
 }
 
 }  // namespace cf
