@@ -143,7 +143,7 @@ __device__ __forceinline__ void load_piece(Piece<kDt> &v, const void *row, const
     }
 }
 template <int kDt, bool kVec>
-__device__ __forceinline__ void store_piece(void *row, const float (&x)[8], const Columns<kVec> &cols, int p, bool on) {
+__device__ __forceinline__ void store_piece(void *row, const Two (&x)[4], const Columns<kVec> &cols, int p, bool on) {
     using E = typename Element<kDt>::type;
     if constexpr (kVec) {
         Piece<kDt> v;
@@ -151,55 +151,66 @@ __device__ __forceinline__ void store_piece(void *row, const float (&x)[8], cons
         if (on && cols.live(p, 0)) v.store(static_cast<E *>(row) + cols.at(p, 0));
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (on && cols.live(p, j)) static_cast<E *>(row)[cols.at(p, j)] = from_float<kDt>(x[j]);
+        for (int j = 0; j < 8; ++j) {
+            const float2 q = x[j / 2].parts();
+            if (on && cols.live(p, j)) static_cast<E *>(row)[cols.at(p, j)] = from_float<kDt>(j % 2 ? q.y : q.x);
+        }
     }
 }
-// a vector's columns, `none` where there is no vector
+// a vector's columns (behind the last one zeros), or `none` where there is no vector
 template <bool kVec>
-__device__ __forceinline__ void load_vector(float (&x)[8], const float *v, float none, const Columns<kVec> &cols,
-                                            int p) {
+__device__ __forceinline__ void load_vector(Two (&x)[4], const float *v, float none, const Columns<kVec> &cols, int p) {
     if (!v) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = none;
+        for (int j = 0; j < 4; ++j) x[j] = Two(none);
     } else if constexpr (kVec) {
         const bool in = cols.live(p, 0);
         const float4 *q = reinterpret_cast<const float4 *>(v + (in ? cols.at(p, 0) : 0));
         const float4 l = in ? __ldg(q) : make_float4(0.f, 0.f, 0.f, 0.f);
         const float4 h = in ? __ldg(q + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-        x[0] = l.x, x[1] = l.y, x[2] = l.z, x[3] = l.w, x[4] = h.x, x[5] = h.y, x[6] = h.z, x[7] = h.w;
+        x[0] = Two(l.x, l.y), x[1] = Two(l.z, l.w), x[2] = Two(h.x, h.y), x[3] = Two(h.z, h.w);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = cols.live(p, j) ? __ldg(v + cols.at(p, j)) : 0.f;
+        for (int j = 0; j < 8; j += 2)
+            x[j / 2] = Two(cols.live(p, j) ? __ldg(v + cols.at(p, j)) : 0.f,
+                           cols.live(p, j + 1) ? __ldg(v + cols.at(p, j + 1)) : 0.f);
     }
 }
+// x with 0 in the place of columns behind the last one
+template <bool kVec>
+__device__ __forceinline__ Two live_two(Two x, const Columns<kVec> &cols, int p, int j) {
+    const float2 q = x.parts();
+    return Two(cols.live(p, 2 * j) ? q.x : 0.f, cols.live(p, 2 * j + 1) ? q.y : 0.f);
+}
 
-// mean and reciprocal root of one norm's row held in x (0 and 1: no norm)
-template <bool kVec, int kP>
-__device__ __forceinline__ float2 spread(Group &g, int norm, const float (&x)[kP][8], const Columns<kVec> &cols,
-                                         float inv_n, float eps) {
-    if (norm == CF_NORM_NONE) return make_float2(0.f, 1.f);
-    float mean = 0.f;
-    if (norm == CF_NORM_LAYER) {
-        float s = 0.f;
+// The reciprocal root of one norm's row held in x (1: no norm), which loses its mean where the norm takes it.
+// kFull: it may be a LayerNorm.
+template <bool kVec, int kP, bool kFull>
+__device__ __forceinline__ float spread(Group &g, int norm, Two (&x)[kP][4], const Columns<kVec> &cols, float inv_n,
+                                        float eps) {
+    if (norm == CF_NORM_NONE) return 1.f;
+    if (kFull && norm == CF_NORM_LAYER) {
+        Two s(0.f);
 #pragma unroll
         for (int p = 0; p < kP; ++p)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s += x[p][j];
-        mean = row_sum(g, s) * inv_n;
+            for (int j = 0; j < 4; ++j) s = s + x[p][j];
+        const Two mean(-row_sum(g, s.sum()) * inv_n);
+#pragma unroll
+        for (int p = 0; p < kP; ++p)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[p][j] = live_two(x[p][j] + mean, cols, p, j);
     }
-    float s = 0.f;
+    Two s(0.f);
 #pragma unroll
     for (int p = 0; p < kP; ++p)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float d = cols.live(p, j) ? x[p][j] - mean : 0.f;
-            s = fmaf(d, d, s);
-        }
-    return make_float2(mean, __frsqrt_rn(fmaf(row_sum(g, s), inv_n, eps)));
+        for (int j = 0; j < 4; ++j) s = fma(x[p][j], x[p][j], s);
+    return __frsqrt_rn(fmaf(row_sum(g, s.sum()), inv_n, eps));
 }
 
-template <int kDt, bool kVec, int kP>
+// kP pieces a thread.  kFull: LayerNorms or biases, too.
+template <int kDt, bool kVec, int kP, bool kFull>
 __global__ void __launch_bounds__(kP == 4 ? 1024 : 512, kP == 4 ? 1 : 2) block_norms_kernel(const BlockNormsArgs a) {
     __shared__ __align__(16) float slots[2 * 32 + 8 * 8];  // of each of up to 8 groups of warps, rounded up to four
     for (int i = threadIdx.x; i < int(sizeof(slots) / 4); i += blockDim.x) slots[i] = 0.f;
@@ -222,6 +233,7 @@ __global__ void __launch_bounds__(kP == 4 ? 1024 : 512, kP == 4 ? 1 : 2) block_n
     const Columns<kVec> cols{g.t, a.lanes, 0, a.cols};
     const int groups = int(blockDim.x) / a.lanes;
     const float inv_n = 1.f / float(a.cols);
+    const Two alpha(a.x ? a.alpha : 0.f);
     // (every thread of a warp makes the same turns)
     for (int64_t r0 = int64_t(blockIdx.x) * groups; r0 < a.rows; r0 += int64_t(gridDim.x) * groups) {
         const int64_t r = r0 + group;
@@ -236,32 +248,51 @@ __global__ void __launch_bounds__(kP == 4 ? 1024 : 512, kP == 4 ? 1 : 2) block_n
         for (int p = 0; p < kP; ++p) load_piece<kDt, kVec>(xp[p], static_cast<const E *>(a.x) + at, cols, p, on && a.x);
 #pragma unroll
         for (int p = 0; p < kP; ++p) load_piece<kDt, kVec>(gp[p], gate, cols, p, on && gate);
-        float x[kP][8];
+        Two x[kP][4];
 #pragma unroll
         for (int p = 0; p < kP; ++p) hp[p].unpack(x[p]);
-        float2 s = spread<kVec, kP>(g, a.post, x, cols, inv_n, a.eps);
+        Two root(a.scale * spread<kVec, kP, kFull>(g, a.post, x, cols, inv_n, a.eps));
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
-            float w[8], b[8];
+            Two w[4], u[4];
             load_vector<kVec>(w, a.post_weight, 1.f, cols, p);
-            load_vector<kVec>(b, a.post_bias, 0.f, cols, p);
+            xp[p].unpack(u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float v = a.scale * fmaf((x[p][j] - s.x) * s.y, w[j], b[j]);
-                const float old = a.x ? a.alpha * xp[p].get(j) : 0.f;
-                x[p][j] = cols.live(p, j) ? (gate ? fmaf(v, gp[p].get(j), old) : v + old) : 0.f;
+            for (int j = 0; j < 4; ++j) x[p][j] = x[p][j] * root;
+            if (kFull && a.post_bias) {  // root has the scale
+                Two b[4];
+                load_vector<kVec>(b, a.post_bias, 0.f, cols, p);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[p][j] = fma(x[p][j], w[j], b[j] * Two(a.scale));
+                    w[j] = Two(1.f);
+                }
+            }
+            if (gate) {
+                Two k[4];
+                gp[p].unpack(k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = w[j] * k[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[p][j] = fma(x[p][j], w[j], u[j] * alpha);
+                // (behind the last column a weight that is not there would be 1, but what it multiplies is 0)
             }
             if (a.x_out) store_piece<kDt, kVec>(static_cast<E *>(a.x_out) + at, x[p], cols, p, on);
         }
         if (a.y == nullptr) continue;
-        s = spread<kVec, kP>(g, a.pre, x, cols, inv_n, a.eps);
+        root = Two(spread<kVec, kP, kFull>(g, a.pre, x, cols, inv_n, a.eps));
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
-            float w[8], b[8];
+            Two w[4], b[4];
             load_vector<kVec>(w, a.pre_weight, 1.f, cols, p);
-            load_vector<kVec>(b, a.pre_bias, 0.f, cols, p);
+            if constexpr (kFull) load_vector<kVec>(b, a.pre_bias, 0.f, cols, p);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[p][j] = fmaf((x[p][j] - s.x) * s.y, w[j], b[j]);
+            for (int j = 0; j < 4; ++j) {
+                x[p][j] = x[p][j] * root;
+                x[p][j] = kFull ? fma(x[p][j], w[j], b[j]) : x[p][j] * w[j];
+            }
             store_piece<kDt, kVec>(static_cast<E *>(a.y) + at, x[p], cols, p, on);
         }
     }
@@ -270,6 +301,18 @@ __global__ void __launch_bounds__(kP == 4 ? 1024 : 512, kP == 4 ? 1 : 2) block_n
 // ---------------------------------------------------------------------------
 // gradient
 // ---------------------------------------------------------------------------
+// a thread's columns of a vector of the workspace
+template <bool kVec>
+__device__ __forceinline__ void store_floats(float *out, const Two (&x)[4], const Columns<kVec> &cols) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const float2 q = x[j / 2].parts();
+        if (kVec && cols.live(0, j)) __stcg(reinterpret_cast<float2 *>(out + cols.at(0, j)), q);
+        if (!kVec && cols.live(0, j)) __stcg(out + cols.at(0, j), q.x);
+        if (!kVec && cols.live(0, j + 1)) __stcg(out + cols.at(0, j + 1), q.y);
+    }
+}
+
 // With hc and xc the rows without their means (RMSNorm: the rows), g2 = dy w2 and w1 = scale gate weight, every sum that
 // the row needs is one over products of what is loaded:
 //     sum g2 x^ = r2 sum g2 xc,
@@ -306,80 +349,93 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
     const bool lh = kFull && a.post == CF_NORM_LAYER, lx = kFull && a.pre == CF_NORM_LAYER;
     if constexpr (kCluster) ptx::cluster_sync();  // nobody writes into a CTA that has not started
 
-    float w2[8], w1[8];  // Pre's weight; scale * gate * Post's weight
+    Two w2[4], w1[4];  // Pre's weight; scale * gate * Post's weight
     load_vector<kVec>(w2, a.pre_weight, 1.f, cols, 0);
-    load_vector<kVec>(w1, a.post_weight, 1.f, cols, 0);
+    Two sa[4], sb[4], sc[4], sd[4], ta[4], tb[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w1[j] = cols.live(0, j) ? w1[j] * a.scale : 0.f;
-    float sa[8], sb[8], sc[8], sd[8], ta[8], tb[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sa[j] = sb[j] = sc[j] = sd[j] = ta[j] = tb[j] = 0.f;
+    for (int j = 0; j < 4; ++j) sa[j] = sb[j] = sc[j] = sd[j] = ta[j] = tb[j] = Two(0.f);
 
     Piece<kDt> gate, next[4];
     int64_t gate_at = 0, gate_end = 0;  // the gate in hand, the first row behind its rows
-    auto gate_of = [&](int j) { return a.gate ? gate.get(j) : 1.f; };
+    auto scaled_gate = [&](int j) {
+        return Two(a.scale) * (a.gate ? Two(gate.get(2 * j), gate.get(2 * j + 1)) : Two(1.f));
+    };
     auto take_gate = [&](int64_t of) {
         gate_at = of;
         gate_end = (of + 1) * int64_t(a.rows_per_gate);
         load_piece<kDt, kVec>(gate, static_cast<const E *>(a.gate) + size_t(of) * a.cols, cols, 0, a.gate != nullptr);
         load_vector<kVec>(w1, a.post_weight, 1.f, cols, 0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w1[j] = cols.live(0, j) ? w1[j] * a.scale * gate_of(j) : 0.f;
+        for (int j = 0; j < 4; ++j) w1[j] = live_two(w1[j] * scaled_gate(j), cols, 0, j);
     };
     gate.zero();
-    if (kGate && first < last) take_gate(uint32_t(first) / a.rows_per_gate);
-    auto fetch = [&](int64_t r, bool on) {
-        const size_t at = on ? size_t(r) * a.cols : 0;
-        load_piece<kDt, kVec>(next[0], static_cast<const E *>(a.h) + at, cols, 0, on);
-        load_piece<kDt, kVec>(next[1], static_cast<const E *>(a.x_out) + at, cols, 0, on && a.dy);
-        load_piece<kDt, kVec>(next[2], static_cast<const E *>(a.dy) + at, cols, 0, on && a.dy);
-        load_piece<kDt, kVec>(next[3], static_cast<const E *>(a.dx_out) + at, cols, 0, on && a.dx_out);
+    if (kGate && first < last) {
+        take_gate(uint32_t(first) / a.rows_per_gate);
+    } else {
+        load_vector<kVec>(w1, a.post_weight, 1.f, cols, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w1[j] = live_two(w1[j] * Two(a.scale), cols, 0, j);
+    }
+    size_t ahead = first < last ? size_t(first) * a.cols : 0;  // where the next row to fetch lies
+    auto fetch = [&](bool on) {
+        load_piece<kDt, kVec>(next[0], static_cast<const E *>(a.h) + ahead, cols, 0, on);
+        load_piece<kDt, kVec>(next[1], static_cast<const E *>(a.x_out) + ahead, cols, 0, on && a.dy);
+        load_piece<kDt, kVec>(next[2], static_cast<const E *>(a.dy) + ahead, cols, 0, on && a.dy);
+        load_piece<kDt, kVec>(next[3], static_cast<const E *>(a.dx_out) + ahead, cols, 0, on && a.dx_out);
+        if (on) ahead += size_t(a.cols);
     };
-    fetch(first, first < last);
+    size_t at = ahead;  // where the row in hand lies
+    fetch(first < last);
     // (every thread of a warp makes the same turns)
     for (int64_t i = 0; i < a.chunk; ++i) {
         const int64_t r = first + i;
         const bool on = r < last;
-        Piece<kDt> hp = next[0], xp = next[1], yp = next[2], dp = next[3];
-        fetch(r + 1, r + 1 < last);
-        const size_t at = on ? size_t(r) * a.cols : 0;
-        float mh = 0.f, mx = 0.f;
+        Two h[4], x[4], y[4], d[4];
+        next[0].unpack(h), next[1].unpack(x), next[2].unpack(y), next[3].unpack(d);
+        fetch(r + 1 < last);
         if (lh || lx) {
-            float v[2] = {0.f, 0.f};
+            Two s(0.f), t(0.f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[0] += hp.get(j), v[1] += xp.get(j);
+            for (int j = 0; j < 4; ++j) s = s + h[j], t = t + x[j];
+            float v[2] = {s.sum(), t.sum()};
             row_sums<2, kCluster>(g, v);
-            mh = lh ? v[0] * inv_n : 0.f;
-            mx = lx ? v[1] * inv_n : 0.f;
+            const Two mh(lh ? -v[0] * inv_n : 0.f), mx(lx ? -v[1] * inv_n : 0.f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = live_two(h[j] + mh, cols, 0, j);
+                x[j] = live_two(x[j] + mx, cols, 0, j);
+            }
+        }
+        constexpr int kSums = kFull ? 12 : 6;
+        Two p[kSums];
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) p[k] = Two(0.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const Two g2 = y[j] * w2[j], wh = w1[j] * h[j];
+            p[0] = fma(h[j], h[j], p[0]);
+            p[1] = fma(x[j], x[j], p[1]);
+            p[2] = fma(g2, x[j], p[2]);
+            p[3] = fma(wh, d[j], p[3]);
+            p[4] = fma(wh, g2, p[4]);
+            p[5] = fma(wh, x[j], p[5]);
+            if constexpr (kFull) {
+                p[6] = p[6] + g2;
+                p[7] = p[7] + wh;
+                p[8] = fma(w1[j], d[j], p[8]);
+                p[9] = fma(w1[j], g2, p[9]);
+                p[10] = fma(w1[j], x[j], p[10]);
+                p[11] = p[11] + w1[j];
+            }
         }
         float v[kV];
 #pragma unroll
-        for (int k = 0; k < kV; ++k) v[k] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bool live = !kFull || cols.live(0, j);
-            const float h = live ? hp.get(j) - mh : 0.f, x = live ? xp.get(j) - mx : 0.f;
-            const float g2 = yp.get(j) * w2[j], d = dp.get(j), wh = w1[j] * h;
-            v[0] = fmaf(h, h, v[0]);
-            v[1] = fmaf(x, x, v[1]);
-            v[2] = fmaf(g2, x, v[2]);
-            v[3] = fmaf(wh, d, v[3]);
-            v[4] = fmaf(wh, g2, v[4]);
-            v[5] = fmaf(wh, x, v[5]);
-            if constexpr (kFull) {
-                v[6] += g2;
-                v[7] += wh;
-                v[8] = fmaf(w1[j], d, v[8]);
-                v[9] = fmaf(w1[j], g2, v[9]);
-                v[10] = fmaf(w1[j], x, v[10]);
-                v[11] += w1[j];
-            }
-        }
+        for (int k = 0; k < kV; ++k) v[k] = k < kSums ? p[k < kSums ? k : 0].sum() : 0.f;
         row_sums<kV, kCluster>(g, v);
         // (an eps of 0 would make a NaN of a row that is not there)
         const float r1 = a.post == CF_NORM_NONE ? 1.f : on ? __frsqrt_rn(fmaf(v[0], inv_n, a.eps)) : 0.f;
         const float r2 = a.pre == CF_NORM_NONE ? 1.f : on ? __frsqrt_rn(fmaf(v[1], inv_n, a.eps)) : 0.f;
-        const float ma = lx ? v[kFull ? 6 : 0] * inv_n : 0.f;            // mean(g2)
+        const float ma = lx ? v[kFull ? 6 : 0] * inv_n : 0.f;                     // mean(g2)
         const float mb = a.pre == CF_NORM_NONE ? 0.f : r2 * r2 * (v[2] * inv_n);  // r2 mean(g2 x^)
         // r1 mean(w1 d h^), mean(w1 d)
         const float na = a.post == CF_NORM_NONE
@@ -388,41 +444,46 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
         const float nb =
             lh ? (v[kFull ? 8 : 0] + r2 * (v[kFull ? 9 : 0] - ma * v[kFull ? 11 : 0] - mb * v[kFull ? 10 : 0])) * inv_n
                : 0.f;
-        float dx[8], dh[8];
+        const Two k1(r1), k2(r2), kb(-r2 * mb), ka(-r2 * ma), kn(-na), km(-r1 * nb);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bool live = !kFull || cols.live(0, j);
-            const float h = live ? hp.get(j) - mh : 0.f, x = live ? xp.get(j) - mx : 0.f, y = yp.get(j);
-            const float d = live ? fmaf(r2, y * w2[j] - ma - mb * x, dp.get(j)) : 0.f;
-            sc[j] = fmaf(y, r2 * x, sc[j]);
-            sa[j] = fmaf(d, r1 * h, sa[j]);
-            if constexpr (kFull) sd[j] += y, sb[j] += d;
-            dx[j] = d * a.alpha;
-            dh[j] = r1 * (w1[j] * d - nb - na * h);
+        for (int j = 0; j < 4; ++j) {
+            d[j] = fma(x[j], kb, fma(y[j] * w2[j], k2, d[j]));
+            if constexpr (kFull) d[j] = d[j] + ka;
+            sc[j] = fma(y[j], x[j] * k2, sc[j]);
+            if constexpr (kFull) sd[j] = sd[j] + y[j], sb[j] = sb[j] + d[j];
+            h[j] = h[j] * k1;
+            sa[j] = fma(d[j], h[j], sa[j]);
+            h[j] = fma(h[j], kn, (w1[j] * d[j]) * k1);
+            if constexpr (kFull) h[j] = h[j] + km;
+            d[j] = d[j] * Two(a.alpha);
         }
-        if (a.dx) store_piece<kDt, kVec>(static_cast<E *>(a.dx) + at, dx, cols, 0, on);
-        store_piece<kDt, kVec>(static_cast<E *>(a.dh) + at, dh, cols, 0, on);
+        if (a.dx) store_piece<kDt, kVec>(static_cast<E *>(a.dx) + at, d, cols, 0, on);
+        store_piece<kDt, kVec>(static_cast<E *>(a.dh) + at, h, cols, 0, on);
+        if (on) at += size_t(a.cols);
         if constexpr (kGate) {
             if (on && (r + 1 == last || r + 1 == gate_end)) {  // its last row here
-                float w[8], b[8];
+                Two w[4], b[4];
                 load_vector<kVec>(w, a.post_weight, 1.f, cols, 0);
-                load_vector<kVec>(b, kFull ? a.post_bias : nullptr, 0.f, cols, 0);
+                if constexpr (kFull) load_vector<kVec>(b, a.post_bias, 0.f, cols, 0);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    dx[j] = a.scale * fmaf(w[j], sa[j], b[j] * sb[j]);
-                    const float k = a.scale * gate_of(j);
-                    ta[j] = fmaf(k, sa[j], ta[j]);
-                    if constexpr (kFull) tb[j] = fmaf(k, sb[j], tb[j]);
-                    sa[j] = sb[j] = 0.f;
+                for (int j = 0; j < 4; ++j) {
+                    const Two k = scaled_gate(j);
+                    ta[j] = fma(k, sa[j], ta[j]);
+                    d[j] = w[j] * sa[j];
+                    if constexpr (kFull) {
+                        d[j] = fma(b[j], sb[j], d[j]);
+                        tb[j] = fma(k, sb[j], tb[j]);
+                        sb[j] = Two(0.f);
+                    }
+                    d[j] = d[j] * Two(a.scale);
+                    sa[j] = Two(0.f);
                 }
                 const int64_t from = gate_end - int64_t(a.rows_per_gate);
                 if (a.dgate && from >= first && gate_end <= last) {
-                    store_piece<kDt, kVec>(static_cast<E *>(a.dgate) + size_t(gate_at) * a.cols, dx, cols, 0, true);
+                    store_piece<kDt, kVec>(static_cast<E *>(a.dgate) + size_t(gate_at) * a.cols, d, cols, 0, true);
                 } else if (a.dgate) {  // slot 0: begun by a worker before; slot 1: here, and goes on
                     float *const slot = a.slots + (size_t(2) * worker + (from >= first ? 1 : 0)) * a.cols;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (cols.live(0, j)) __stcg(slot + cols.at(0, j), dx[j]);
+                    store_floats<kVec>(slot, d, cols);
                 }
                 if (r + 1 < last) take_gate(gate_at + 1);
             }
@@ -433,21 +494,21 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         if (!wanted[k]) continue;
-        float v[8];
+        Two v[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = k == 0 ? (kGate ? ta[j] : a.scale * sa[j])
-                   : k == 1 ? (kGate ? tb[j] : a.scale * sb[j]) : k == 2 ? sc[j] : sd[j];
+        for (int j = 0; j < 4; ++j)
+            v[j] = k == 0 ? (kGate ? ta[j] : Two(a.scale) * sa[j])
+                   : k == 1 ? (kGate ? tb[j] : Two(a.scale) * sb[j]) : k == 2 ? sc[j] : sd[j];
         float *const out = a.partials + (size_t(a.sum_at[k]) * a.sets + set) * a.cols;
         if (kCluster || groups == 1) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (cols.live(0, j)) __stcg(out + cols.at(0, j), v[j]);
+            store_floats<kVec>(out, v, cols);
         } else {
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (cols.live(0, j)) sums[group * a.lanes * 8 + cols.at(0, j)] = v[j];
+            for (int j = 0; j < 8; ++j) {
+                const float2 q = v[j / 2].parts();
+                if (cols.live(0, j)) sums[group * a.lanes * 8 + cols.at(0, j)] = j % 2 ? q.y : q.x;
+            }
             __syncthreads();
             for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
                 float s = 0.f;
@@ -555,11 +616,16 @@ cudaError_t launch(const void *fn, dim3 grid, int threads, int cluster, bool pdl
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-template <int kDt, bool kVec>
+template <int kDt, bool kVec, bool kFull>
 const void *forward_kernel(int pieces) {
-    return pieces == 1   ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, kVec, 1>)
-           : pieces == 2 ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, kVec, 2>)
-                         : reinterpret_cast<const void *>(&block_norms_kernel<kDt, kVec, 4>);
+    return pieces == 1   ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, kVec, 1, kFull>)
+           : pieces == 2 ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, kVec, 2, kFull>)
+                         : reinterpret_cast<const void *>(&block_norms_kernel<kDt, kVec, 4, kFull>);
+}
+template <int kDt>
+const void *forward_kernel(bool vec, bool full, int pieces) {
+    if (!vec) return forward_kernel<kDt, false, true>(pieces);
+    return full ? forward_kernel<kDt, true, true>(pieces) : forward_kernel<kDt, true, false>(pieces);
 }
 // (what is rare is compiled in its widest form alone)
 template <int kDt>
@@ -585,9 +651,10 @@ cudaError_t launch_block_norms(BlockNormsArgs a, bool vec, int sms, bool pdl, cu
     a.lanes = round_lanes((pieces + per - 1) / per);
     const int groups = std::max(1, 256 / a.lanes), threads = groups * a.lanes;
     const int64_t ctas = std::min<int64_t>((a.rows + groups - 1) / groups, int64_t(sms) * (2048 / threads) * 4);
-    const void *fn = a.dtype == CF_BF16   ? (vec ? forward_kernel<CF_BF16, true>(per) : forward_kernel<CF_BF16, false>(per))
-                     : a.dtype == CF_FP16 ? (vec ? forward_kernel<CF_FP16, true>(per) : forward_kernel<CF_FP16, false>(per))
-                                          : (vec ? forward_kernel<CF_FP32, true>(per) : forward_kernel<CF_FP32, false>(per));
+    const bool full = a.post == CF_NORM_LAYER || a.pre == CF_NORM_LAYER || a.post_bias || a.pre_bias;
+    const void *fn = a.dtype == CF_BF16   ? forward_kernel<CF_BF16>(vec, full, per)
+                     : a.dtype == CF_FP16 ? forward_kernel<CF_FP16>(vec, full, per)
+                                          : forward_kernel<CF_FP32>(vec, full, per);
     void *args[] = {&a};
     return launch(fn, dim3(unsigned(ctas)), threads, 1, pdl, stream, args);
 }

@@ -36,6 +36,38 @@ __device__ __forceinline__ typename Element<kDt>::type from_float(float v) {
     else return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// Two fp32 numbers, worked on by one instruction.
+struct Two {
+    uint64_t v;
+    __device__ __forceinline__ Two() {}
+    __device__ __forceinline__ Two(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+    __device__ __forceinline__ explicit Two(float both) : Two(both, both) {}
+    __device__ __forceinline__ float2 parts() const {
+        float2 p;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(p.x), "=f"(p.y) : "l"(v));
+        return p;
+    }
+    __device__ __forceinline__ float sum() const {
+        const float2 p = parts();
+        return p.x + p.y;
+    }
+};
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    Two d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+
 // eight numbers, as stored
 template <int kDt>
 struct Piece {
@@ -50,6 +82,19 @@ struct Piece {
         if constexpr (kDt == CF_FP32) return __uint_as_float(w[j]);
         else if constexpr (kDt == CF_FP16) return __half2float(__ushort_as_half(uint16_t(w[j / 2] >> (j % 2 * 16))));
         else return __uint_as_float(j % 2 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    }
+    __device__ __forceinline__ void unpack(Two (&x)[4]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = Two(get(2 * j), get(2 * j + 1));
+    }
+    __device__ __forceinline__ void pack(const Two (&x)[4]) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 p = x[j].parts();
+            f[2 * j] = p.x, f[2 * j + 1] = p.y;
+        }
+        pack(f);
     }
     __device__ __forceinline__ void unpack(float (&x)[8]) const {
 #pragma unroll
