@@ -19,12 +19,17 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "block_norms.h"
 #include "pieces.cuh"
 #include "ptx.cuh"
 
+#ifndef NREG
+#define NREG 96
+#define NTHR 512
+#endif
 namespace cf {
 namespace {
 
@@ -110,9 +115,13 @@ __device__ __forceinline__ void row_sums(Group &g, float (&v)[kV]) {
             if (lane < kV) slots[mine * kV + lane] = s;
             ptx::named_bar_sync(g.bar, uint32_t(g.lanes));
         }
-        const int all = g.warps * (kCluster ? g.cluster : 1);
         s = 0.f;
-        for (int i = lane / kV; i < all; i += 32 / kV) s += slots[i * kV + lane % kV];
+        if constexpr (kCluster) {
+            for (int i = lane / kV; i < g.warps * g.cluster; i += 32 / kV) s += slots[i * kV + lane % kV];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16 * kV / 32; ++i) s += 32 * i < g.half ? slots[lane + 32 * i] : 0.f;
+        }
 #pragma unroll
         for (int d = kV; d <= 16; d *= 2) s += __shfl_xor_sync(kAll, s, d);
     }
@@ -130,13 +139,14 @@ struct Columns {
     __device__ __forceinline__ bool live(int p, int j) const { return at(p, kVec ? 0 : j) < n; }
 };
 
+// (columns behind the last one stay what they were in v)
 template <int kDt, bool kVec>
 __device__ __forceinline__ void load_piece(Piece<kDt> &v, const void *row, const Columns<kVec> &cols, int p, bool on) {
     using E = typename Element<kDt>::type;
-    v.zero();
     if constexpr (kVec) {
         if (on && cols.live(p, 0)) v.load(static_cast<const E *>(row) + cols.at(p, 0));
     } else {
+        v.zero();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (on && cols.live(p, j)) v.put(j, static_cast<const E *>(row)[cols.at(p, j)]);
@@ -176,11 +186,116 @@ __device__ __forceinline__ void load_vector(Two (&x)[4], const float *v, float n
                            cols.live(p, j + 1) ? __ldg(v + cols.at(p, j + 1)) : 0.f);
     }
 }
+// Rows on their way, in shared memory: a thread fills and reads its own columns alone, so nobody waits for anybody.  The
+// ring has kDepth stages of up to kRows rows (one of each of that many matrices), a row kP pieces a thread.  (16-bit
+// numbers that start anywhere cannot be copied so; theirs are loaded when they are needed.)
+__host__ __device__ constexpr int ring_depth(int dt) { return dt == CF_FP32 ? 2 : 4; }
+__host__ __device__ constexpr bool has_ring(int dt, bool vec, int pieces) { return (vec || dt == CF_FP32) && pieces <= 2; }
+constexpr int kMostSmem = 232448;  // of a CTA (227 KB)
+inline int ring_bytes(int dt, bool vec, int rows, int pieces, int threads) {
+    return has_ring(dt, vec, pieces) ? ring_depth(dt) * rows * threads * pieces * 8 * type_bytes(dt) : 0;
+}
+template <int kDt, bool kVec, int kRows, int kP>
+struct RowRing {
+    using E = typename Element<kDt>::type;
+    static constexpr bool kOn = has_ring(kDt, kVec, kP);
+    static constexpr int kDepth = ring_depth(kDt);
+    static constexpr int kCopies = kVec ? Piece<kDt>::kWords / 4 : 8;  // of a piece
+    static constexpr uint32_t kBytes = kVec ? 16 : 4;                  // of a copy
+    const E *src[kRows];  // this thread's first column of the next row; null: zeros
+    const Columns<kVec> &cols;
+    uint32_t base, step;  // of this thread's copies; from one to the next
+    int rows, stage, left;  // rows: of a stage; left: rows to come
+    size_t apart;
+
+    __device__ __forceinline__ RowRing(const Columns<kVec> &c, uint32_t ring, int rows_, int left_)
+        : cols(c), base(ring + threadIdx.x * kBytes), step(blockDim.x * kBytes), rows(rows_), stage(0), left(left_),
+          apart(size_t(c.n)) {}
+    __device__ __forceinline__ void matrix(int k, const void *m, int64_t row) {
+        src[k] = m ? static_cast<const E *>(m) + (left > 0 ? size_t(row) * apart : 0) +
+                         (cols.at(0, 0) < cols.n ? cols.at(0, 0) : 0)
+                   : nullptr;
+    }
+    // a row of each matrix into stage `to`, if there is one
+    __device__ __forceinline__ void fetch(int to) {
+        if constexpr (kOn) {
+            const bool on = left > 0;
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                if (k >= rows) break;
+                uint32_t dst = base + uint32_t((to * rows + k) * (kP * kCopies)) * step;
+#pragma unroll
+                for (int p = 0; p < kP; ++p)
+#pragma unroll
+                    for (int j = 0; j < kCopies; ++j, dst += step) {
+                        const bool in = on && src[k] != nullptr && cols.live(p, kVec ? 0 : j);
+                        const int d = in ? (kVec ? p * cols.lanes * 8 + j * (16 / int(sizeof(E))) : (p * 8 + j) * cols.lanes)
+                                         : 0;
+                        // (nothing is read where nothing is in)
+                        const E *const from = in ? src[k] + d : src[0];
+                        if constexpr (kVec) ptx::cp_async_16(dst, from, in ? 16u : 0u);
+                        else ptx::cp_async_4(dst, from, in ? 4u : 0u);
+                    }
+                if (on && src[k] != nullptr) src[k] += apart;
+            }
+            --left;
+            ptx::cp_async_commit();
+        }
+    }
+    __device__ __forceinline__ void start() {
+#pragma unroll
+        for (int s = 0; s < kDepth - 1; ++s) fetch(s);
+    }
+    // the row in hand is there, and one more is on its way
+    __device__ __forceinline__ void turn() {
+        fetch(stage == 0 ? kDepth - 1 : stage - 1);
+        if constexpr (kOn) ptx::cp_async_wait<kDepth - 1>();
+    }
+    __device__ __forceinline__ void take(Piece<kDt> &v, int k, int p) {
+        if constexpr (kOn) {
+            uint32_t at = base + uint32_t(((stage * rows + k) * kP + p) * kCopies) * step;
+#pragma unroll
+            for (int j = 0; j < kCopies; ++j, at += step) {
+                if constexpr (kVec) {
+                    const uint4 q = ptx::ld_shared_v4(at);
+                    v.w[4 * j] = q.x, v.w[4 * j + 1] = q.y, v.w[4 * j + 2] = q.z, v.w[4 * j + 3] = q.w;
+                } else {
+                    v.w[j] = ptx::ld_shared_u32(at);
+                }
+            }
+        } else {
+            v.zero();
+            if (left > 0 && src[k] != nullptr) {
+                const E *const row = src[k] - (cols.at(0, 0) < cols.n ? cols.at(0, 0) : 0);
+                load_piece<kDt, kVec>(v, row, cols, p, true);
+            }
+        }
+    }
+    __device__ __forceinline__ void next() {
+        if constexpr (kOn) {
+            stage = stage == kDepth - 1 ? 0 : stage + 1;
+        } else {
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
+                if (left > 0 && src[k] != nullptr) src[k] += apart;
+            --left;
+        }
+    }
+};
+
 // x with 0 in the place of columns behind the last one
 template <bool kVec>
 __device__ __forceinline__ Two live_two(Two x, const Columns<kVec> &cols, int p, int j) {
     const float2 q = x.parts();
     return Two(cols.live(p, 2 * j) ? q.x : 0.f, cols.live(p, 2 * j + 1) ? q.y : 0.f);
+}
+
+// 1 / sqrt(v): the hardware's value and one step of Newton's method, good to 2^-23 or so in a few instructions (the
+// correctly rounded one takes some 25)
+__device__ __forceinline__ float reciprocal_root(float v) {
+    const float r = rsqrtf(v);
+    const float e = fmaf(v * r, -r, 1.f);
+    return fabsf(v) > 1e-30f && v < 1e30f ? fmaf(0.5f * r, e, r) : r;
 }
 
 // The reciprocal root of one norm's row held in x (1: no norm), which loses its mean where the norm takes it.
@@ -206,12 +321,13 @@ __device__ __forceinline__ float spread(Group &g, int norm, Two (&x)[kP][4], con
     for (int p = 0; p < kP; ++p)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s = fma(x[p][j], x[p][j], s);
-    return __frsqrt_rn(fmaf(row_sum(g, s.sum()), inv_n, eps));
+    return reciprocal_root(fmaf(row_sum(g, s.sum()), inv_n, eps));
 }
 
-// kP pieces a thread.  kFull: LayerNorms or biases, too.
+// kP pieces a thread.  kFull: LayerNorms or biases, too.  A worker takes a stretch of neighbouring rows, as in the gradient.
 template <int kDt, bool kVec, int kP, bool kFull>
-__global__ void __launch_bounds__(kP == 4 ? 1024 : 512, kP == 4 ? 1 : 2) block_norms_kernel(const BlockNormsArgs a) {
+__global__ void __maxnreg__(kP == 4 ? 64 : NREG) block_norms_kernel(const BlockNormsArgs a) {
+    extern __shared__ __align__(16) uint8_t ring_smem[];
     __shared__ __align__(16) float slots[2 * 32 + 8 * 8];  // of each of up to 8 groups of warps, rounded up to four
     for (int i = threadIdx.x; i < int(sizeof(slots) / 4); i += blockDim.x) slots[i] = 0.f;
     ptx::griddep_launch_dependents();
@@ -234,67 +350,104 @@ __global__ void __launch_bounds__(kP == 4 ? 1024 : 512, kP == 4 ? 1 : 2) block_n
     const int groups = int(blockDim.x) / a.lanes;
     const float inv_n = 1.f / float(a.cols);
     const Two alpha(a.x ? a.alpha : 0.f);
-    // (every thread of a warp makes the same turns)
-    for (int64_t r0 = int64_t(blockIdx.x) * groups; r0 < a.rows; r0 += int64_t(gridDim.x) * groups) {
-        const int64_t r = r0 + group;
-        const bool on = r < a.rows;
-        const size_t at = on ? size_t(r) * a.cols : 0;
-        Piece<kDt> hp[kP], xp[kP], gp[kP];
-        const E *const gate =
-            a.gate ? static_cast<const E *>(a.gate) + size_t(on ? uint32_t(r) / a.rows_per_gate : 0u) * a.cols : nullptr;
+    const int64_t mine = int64_t(blockIdx.x) * groups + group;
+    const int first = int(min(a.rows, mine * a.chunk)), last = int(min(a.rows, int64_t(first) + a.chunk));
+    // rows that threads of one warp may share a warp's turn with: as many turns as any; else their own
+    const int turns = a.lanes < 32 ? a.chunk : last - first;
+    RowRing<kDt, kVec, 3, kP> ring(cols, ptx::smem_u32(ring_smem), a.gates_along ? 3 : 2, last - first);
+    ring.matrix(0, a.h, first);
+    ring.matrix(1, a.x, first);
+    ring.matrix(2, a.gates_along ? a.gate : nullptr, first);
+    ring.start();
+
+    Two w1[kP][4], w2[kP][4];  // Post's weight times the gate; Pre's
+    int gate_end = 0;          // the first row behind the rows of the gate in w1
+    auto take_gate = [&](int of, bool here) {
+        gate_end = int((uint32_t(of) + 1u) * a.rows_per_gate);
 #pragma unroll
-        for (int p = 0; p < kP; ++p) load_piece<kDt, kVec>(hp[p], static_cast<const E *>(a.h) + at, cols, p, on);
+        for (int p = 0; p < kP; ++p) {
+            load_vector<kVec>(w1[p], a.post_weight, 1.f, cols, p);
+            if (!a.gate) continue;
+            Piece<kDt> q;
+            if (here) {
+                ring.take(q, 2, p);
+            } else {
+                q.zero();
+                load_piece<kDt, kVec>(q, static_cast<const E *>(a.gate) + size_t(of) * a.cols, cols, p, true);
+            }
+            Two k[4];
+            q.unpack(k);
 #pragma unroll
-        for (int p = 0; p < kP; ++p) load_piece<kDt, kVec>(xp[p], static_cast<const E *>(a.x) + at, cols, p, on && a.x);
+            for (int j = 0; j < 4; ++j) w1[p][j] = w1[p][j] * k[j];
+        }
+    };
 #pragma unroll
-        for (int p = 0; p < kP; ++p) load_piece<kDt, kVec>(gp[p], gate, cols, p, on && gate);
+    for (int p = 0; p < kP; ++p) load_vector<kVec>(w2[p], a.pre_weight, 1.f, cols, p);
+    if (!a.gates_along) take_gate(int(uint32_t(first) / a.rows_per_gate < uint32_t(a.gates) ? uint32_t(first) / a.rows_per_gate : 0u), false);
+    E *xo = static_cast<E *>(a.x_out), *yo = static_cast<E *>(a.y);
+    if (xo) xo += size_t(first) * a.cols;
+    if (yo) yo += size_t(first) * a.cols;
+    for (int i = 0; i < turns; ++i) {
+        const bool on = first + i < last;
+        ring.turn();
+        if (a.gates_along) {
+            if (on) take_gate(first + i, true);
+        } else if (on && first + i == gate_end) {
+            take_gate(int(uint32_t(first + i) / a.rows_per_gate), false);
+        }
         Two x[kP][4];
 #pragma unroll
-        for (int p = 0; p < kP; ++p) hp[p].unpack(x[p]);
+        for (int p = 0; p < kP; ++p) {
+            Piece<kDt> q;
+            ring.take(q, 0, p);
+            q.unpack(x[p]);
+        }
         Two root(a.scale * spread<kVec, kP, kFull>(g, a.post, x, cols, inv_n, a.eps));
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
-            Two w[4], u[4];
-            load_vector<kVec>(w, a.post_weight, 1.f, cols, p);
-            xp[p].unpack(u);
+            Two u[4];
+            Piece<kDt> q;
+            ring.take(q, 1, p);
+            q.unpack(u);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[p][j] = x[p][j] * root;
-            if (kFull && a.post_bias) {  // root has the scale
+            for (int j = 0; j < 4; ++j) x[p][j] = fma(x[p][j] * root, w1[p][j], u[j] * alpha);
+            if (kFull && a.post_bias) {  // scale gate bias; the gate from memory again
                 Two b[4];
                 load_vector<kVec>(b, a.post_bias, 0.f, cols, p);
+                if (a.gate) {
+                    if (a.gates_along) {
+                        ring.take(q, 2, p);
+                    } else {
+                        q.zero();
+                        load_piece<kDt, kVec>(
+                            q, static_cast<const E *>(a.gate) + size_t(gate_end / a.rows_per_gate - 1) * a.cols, cols, p,
+                            on);
+                    }
+                    q.unpack(u);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[p][j] = fma(x[p][j], w[j], b[j] * Two(a.scale));
-                    w[j] = Two(1.f);
+                    for (int j = 0; j < 4; ++j) b[j] = b[j] * u[j];
                 }
-            }
-            if (gate) {
-                Two k[4];
-                gp[p].unpack(k);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = w[j] * k[j];
+                for (int j = 0; j < 4; ++j) x[p][j] = fma(b[j], Two(a.scale), x[p][j]);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[p][j] = fma(x[p][j], w[j], u[j] * alpha);
-                // (behind the last column a weight that is not there would be 1, but what it multiplies is 0)
-            }
-            if (a.x_out) store_piece<kDt, kVec>(static_cast<E *>(a.x_out) + at, x[p], cols, p, on);
+            if (xo) store_piece<kDt, kVec>(xo, x[p], cols, p, on);
         }
-        if (a.y == nullptr) continue;
+        ring.next();
+        if (xo) xo += a.cols;
+        if (yo == nullptr) continue;
         root = Two(spread<kVec, kP, kFull>(g, a.pre, x, cols, inv_n, a.eps));
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
-            Two w[4], b[4];
-            load_vector<kVec>(w, a.pre_weight, 1.f, cols, p);
+            Two b[4];
             if constexpr (kFull) load_vector<kVec>(b, a.pre_bias, 0.f, cols, p);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 x[p][j] = x[p][j] * root;
-                x[p][j] = kFull ? fma(x[p][j], w[j], b[j]) : x[p][j] * w[j];
+                x[p][j] = kFull ? fma(x[p][j], w2[p][j], b[j]) : x[p][j] * w2[p][j];
             }
-            store_piece<kDt, kVec>(static_cast<E *>(a.y) + at, x[p], cols, p, on);
+            store_piece<kDt, kVec>(yo, x[p], cols, p, on);
         }
+        yo += a.cols;
     }
 }
 
@@ -320,11 +473,14 @@ __device__ __forceinline__ void store_floats(float *out, const Two (&x)[4], cons
 //     sum w1 d h^ = r1 (sum w1 hc dx' + r2 (sum w1 hc g2 - mean(g2) sum w1 hc - r2 mean(g2 x^) sum w1 hc xc)),
 // so one exchange between the threads serves where three would follow one another (16384 x 4096 bf16: 287 us with
 // three).  A LayerNorm's means come one exchange before.
+// Rows ahead go through a ring in shared memory, of which a thread fills and reads its own columns alone, so nobody waits
+// for anybody: kept in registers on their way, they left no room for the sums (16384 x 4096 bf16: 172 us).
 // kFull: LayerNorms or biases, too.  kGate: a gate, whose rows' sums are closed where the next gate begins.
 template <int kDt, bool kVec, bool kCluster, bool kGate, bool kFull>
 __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsGradArgs a) {
     constexpr int kV = kFull ? 16 : 8;
-    __shared__ float slots[2 * 16 * kV * (kCluster ? 8 : 1)];
+    extern __shared__ __align__(16) uint8_t ring_smem[];
+    __shared__ float slots[2 * (16 * kV + 8 * 32) * (kCluster ? 8 : 1)];  // of up to 8 groups, each rounded up to 32
     __shared__ float sums[kCluster ? 1 : 512 * 8];
     using E = typename Element<kDt>::type;
     ptx::griddep_launch_dependents();
@@ -338,13 +494,21 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
     g.warp = g.t >> 5;
     g.bar = 1 + uint32_t(group);
     g.rank = kCluster ? ptx::cluster_ctarank() : 0u;
-    g.half = g.warps * kV * (kCluster ? a.cluster : 1);
+    // (whole rounds of 32 numbers; what no warp writes stays zero)
+    g.half = (g.warps * kV * (kCluster ? a.cluster : 1) + 31) & ~31;
     g.slots = slots + group * 2 * g.half;
     g.turn = 0;
+    if constexpr (!kCluster) {
+        for (int i = threadIdx.x; i < int(sizeof(slots) / 4); i += blockDim.x) slots[i] = 0.f;
+        __syncthreads();
+    }
     const Columns<kVec> cols{g.t, a.lanes, int(g.rank) * a.lanes * 8, a.cols};
     const int groups = int(blockDim.x) / a.lanes;
     const int set = int(blockIdx.x) / a.cluster, worker = set * groups + group;
-    const int64_t first = worker * a.chunk, last = min(a.rows, first + a.chunk);
+    const int chunk = int(a.chunk);
+    const int first = int(min(a.rows, int64_t(worker) * chunk)), last = int(min(a.rows, int64_t(first) + chunk));
+    // rows that threads of one warp may share a warp's turn with: as many turns as any; else their own
+    const int turns = a.lanes < 32 ? chunk : last - first;
     const float inv_n = 1.f / float(a.cols);
     const bool lh = kFull && a.post == CF_NORM_LAYER, lx = kFull && a.pre == CF_NORM_LAYER;
     if constexpr (kCluster) ptx::cluster_sync();  // nobody writes into a CTA that has not started
@@ -355,44 +519,52 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
 #pragma unroll
     for (int j = 0; j < 4; ++j) sa[j] = sb[j] = sc[j] = sd[j] = ta[j] = tb[j] = Two(0.f);
 
-    Piece<kDt> gate, next[4];
-    int64_t gate_at = 0, gate_end = 0;  // the gate in hand, the first row behind its rows
+    Piece<kDt> gate;
+    int gate_at = 0, gate_end = 0;  // the gate in hand, the first row behind its rows
     auto scaled_gate = [&](int j) {
         return Two(a.scale) * (a.gate ? Two(gate.get(2 * j), gate.get(2 * j + 1)) : Two(1.f));
     };
-    auto take_gate = [&](int64_t of) {
+    auto take_gate = [&](int of, bool here) {  // here: it lies in `gate`
         gate_at = of;
-        gate_end = (of + 1) * int64_t(a.rows_per_gate);
-        load_piece<kDt, kVec>(gate, static_cast<const E *>(a.gate) + size_t(of) * a.cols, cols, 0, a.gate != nullptr);
+        gate_end = int((uint32_t(of) + 1u) * a.rows_per_gate);
+        if (a.gate && !here)
+            load_piece<kDt, kVec>(gate, static_cast<const E *>(a.gate) + size_t(of) * a.cols, cols, 0, true);
         load_vector<kVec>(w1, a.post_weight, 1.f, cols, 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) w1[j] = live_two(w1[j] * scaled_gate(j), cols, 0, j);
     };
     gate.zero();
-    if (kGate && first < last) {
-        take_gate(uint32_t(first) / a.rows_per_gate);
-    } else {
+    const bool gates_along = kGate && RowRing<kDt, kVec, 5, 1>::kOn && a.gate && a.rows_per_gate == 1;
+    if (kGate && !gates_along && first < last) {
+        take_gate(int(uint32_t(first) / a.rows_per_gate), false);
+    } else if (!kGate) {
         load_vector<kVec>(w1, a.post_weight, 1.f, cols, 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) w1[j] = live_two(w1[j] * Two(a.scale), cols, 0, j);
     }
-    size_t ahead = first < last ? size_t(first) * a.cols : 0;  // where the next row to fetch lies
-    auto fetch = [&](bool on) {
-        load_piece<kDt, kVec>(next[0], static_cast<const E *>(a.h) + ahead, cols, 0, on);
-        load_piece<kDt, kVec>(next[1], static_cast<const E *>(a.x_out) + ahead, cols, 0, on && a.dy);
-        load_piece<kDt, kVec>(next[2], static_cast<const E *>(a.dy) + ahead, cols, 0, on && a.dy);
-        load_piece<kDt, kVec>(next[3], static_cast<const E *>(a.dx_out) + ahead, cols, 0, on && a.dx_out);
-        if (on) ahead += size_t(a.cols);
-    };
-    size_t at = ahead;  // where the row in hand lies
-    fetch(first < last);
-    // (every thread of a warp makes the same turns)
-    for (int64_t i = 0; i < a.chunk; ++i) {
-        const int64_t r = first + i;
+
+    RowRing<kDt, kVec, 5, 1> ring(cols, ptx::smem_u32(ring_smem), gates_along ? 5 : 4, last - first);
+    ring.matrix(0, a.h, first);
+    ring.matrix(1, a.dy ? a.x_out : nullptr, first);
+    ring.matrix(2, a.dy, first);
+    ring.matrix(3, a.dx_out, first);
+    ring.matrix(4, gates_along ? a.gate : nullptr, first);
+    ring.start();
+    size_t at = first < last ? size_t(first) * a.cols : 0;  // where the row in hand lies
+    for (int i = 0; i < turns; ++i) {
+        const int r = first + i;
         const bool on = r < last;
+        ring.turn();
+        Piece<kDt> raw[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ring.take(raw[k], k, 0);
+        if (gates_along && on) {
+            ring.take(gate, 4, 0);
+            take_gate(r, true);
+        }
+        ring.next();
         Two h[4], x[4], y[4], d[4];
-        next[0].unpack(h), next[1].unpack(x), next[2].unpack(y), next[3].unpack(d);
-        fetch(r + 1 < last);
+        raw[0].unpack(h), raw[1].unpack(x), raw[2].unpack(y), raw[3].unpack(d);
         if (lh || lx) {
             Two s(0.f), t(0.f);
 #pragma unroll
@@ -433,8 +605,8 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
         for (int k = 0; k < kV; ++k) v[k] = k < kSums ? p[k < kSums ? k : 0].sum() : 0.f;
         row_sums<kV, kCluster>(g, v);
         // (an eps of 0 would make a NaN of a row that is not there)
-        const float r1 = a.post == CF_NORM_NONE ? 1.f : on ? __frsqrt_rn(fmaf(v[0], inv_n, a.eps)) : 0.f;
-        const float r2 = a.pre == CF_NORM_NONE ? 1.f : on ? __frsqrt_rn(fmaf(v[1], inv_n, a.eps)) : 0.f;
+        const float r1 = a.post == CF_NORM_NONE ? 1.f : on ? reciprocal_root(fmaf(v[0], inv_n, a.eps)) : 0.f;
+        const float r2 = a.pre == CF_NORM_NONE ? 1.f : on ? reciprocal_root(fmaf(v[1], inv_n, a.eps)) : 0.f;
         const float ma = lx ? v[kFull ? 6 : 0] * inv_n : 0.f;                     // mean(g2)
         const float mb = a.pre == CF_NORM_NONE ? 0.f : r2 * r2 * (v[2] * inv_n);  // r2 mean(g2 x^)
         // r1 mean(w1 d h^), mean(w1 d)
@@ -478,14 +650,14 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
                     d[j] = d[j] * Two(a.scale);
                     sa[j] = Two(0.f);
                 }
-                const int64_t from = gate_end - int64_t(a.rows_per_gate);
+                const int from = gate_end - int(a.rows_per_gate);
                 if (a.dgate && from >= first && gate_end <= last) {
                     store_piece<kDt, kVec>(static_cast<E *>(a.dgate) + size_t(gate_at) * a.cols, d, cols, 0, true);
                 } else if (a.dgate) {  // slot 0: begun by a worker before; slot 1: here, and goes on
                     float *const slot = a.slots + (size_t(2) * worker + (from >= first ? 1 : 0)) * a.cols;
                     store_floats<kVec>(slot, d, cols);
                 }
-                if (r + 1 < last) take_gate(gate_at + 1);
+                if (r + 1 < last && !gates_along) take_gate(gate_at + 1, false);
             }
         }
     }
@@ -594,8 +766,10 @@ int round_lanes(int64_t threads) {  // of a row: a power of two in a warp, else 
     return p;
 }
 
-cudaError_t launch(const void *fn, dim3 grid, int threads, int cluster, bool pdl, cudaStream_t stream, void **args) {
+cudaError_t launch(const void *fn, dim3 grid, int threads, int cluster, bool pdl, cudaStream_t stream, void **args,
+                   int smem = 0) {
     cudaLaunchConfig_t cfg = {};
+    cfg.dynamicSmemBytes = size_t(smem);
     cfg.gridDim = grid;
     cfg.blockDim = dim3(unsigned(threads));
     cfg.stream = stream;
@@ -614,6 +788,34 @@ cudaError_t launch(const void *fn, dim3 grid, int threads, int cluster, bool pdl
     cfg.attrs = attr;
     cfg.numAttrs = n;
     return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+// Once per device and kernel, to the most a launch may ask for: launches from several threads set the same value, and
+// none is set under a capture later.
+cudaError_t allow_smem(const void *fn) {
+    struct Entry {
+        std::atomic<const void *> fn;
+        std::atomic<uint64_t> devices;
+    };
+    static Entry table[128];  // (51 kernels)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidValue;
+    for (Entry &t : table) {
+        const void *at = t.fn.load(std::memory_order_acquire);
+        if (at == nullptr && t.fn.compare_exchange_strong(at, fn, std::memory_order_acq_rel)) at = fn;
+        if (at != fn) continue;
+        if (t.devices.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, fn);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kMostSmem - int(attr.sharedSizeBytes));
+        if (e == cudaSuccess) t.devices.fetch_or(uint64_t(1) << dev, std::memory_order_acq_rel);
+        return e;
+    }
+    return cudaErrorInvalidValue;
 }
 
 template <int kDt, bool kVec, bool kFull>
@@ -645,18 +847,26 @@ const void *grad_kernel(bool vec, bool cluster, bool gate, bool full) {
 
 }  // namespace
 
+constexpr int kForwardThreads = NTHR;
+
 cudaError_t launch_block_norms(BlockNormsArgs a, bool vec, int sms, bool pdl, cudaStream_t stream) {
     const int pieces = (a.cols + 7) / 8;
-    const int per = pieces <= 32 ? 1 : pieces <= 1024 ? 2 : 4;
+    const int per = pieces <= 32 ? 1 : pieces <= 1024 && (pieces + 63) / 64 * 32 <= 512 ? 2 : 4;
     a.lanes = round_lanes((pieces + per - 1) / per);
     const int groups = std::max(1, 256 / a.lanes), threads = groups * a.lanes;
-    const int64_t ctas = std::min<int64_t>((a.rows + groups - 1) / groups, int64_t(sms) * (2048 / threads) * 4);
+    // CTAs of up to kForwardThreads an SM, of a stretch of rows each
+    int64_t ctas = std::min<int64_t>((a.rows + groups - 1) / groups, int64_t(sms) * std::max(1, kForwardThreads / threads));
+    a.chunk = int((a.rows + ctas * groups - 1) / (ctas * groups));
+    ctas = (a.rows + int64_t(a.chunk) * groups - 1) / (int64_t(a.chunk) * groups);
+    a.gates_along = a.gate && a.rows_per_gate == 1 && has_ring(a.dtype, vec, per);
     const bool full = a.post == CF_NORM_LAYER || a.pre == CF_NORM_LAYER || a.post_bias || a.pre_bias;
     const void *fn = a.dtype == CF_BF16   ? forward_kernel<CF_BF16>(vec, full, per)
                      : a.dtype == CF_FP16 ? forward_kernel<CF_FP16>(vec, full, per)
                                           : forward_kernel<CF_FP32>(vec, full, per);
     void *args[] = {&a};
-    return launch(fn, dim3(unsigned(ctas)), threads, 1, pdl, stream, args);
+    const int smem = ring_bytes(a.dtype, vec, a.gates_along ? 3 : 2, per, threads);
+    const cudaError_t e = allow_smem(fn);
+    return e != cudaSuccess ? e : launch(fn, dim3(unsigned(ctas)), threads, 1, pdl, stream, args, smem);
 }
 
 BlockNormsGradPlan plan_block_norms_grad(int64_t rows, int64_t cols, int sms) {
@@ -687,7 +897,10 @@ cudaError_t launch_block_norms_grad(BlockNormsGradArgs a, const BlockNormsGradPl
                      : a.dtype == CF_FP16 ? grad_kernel<CF_FP16>(vec, cluster, gate, full)
                                           : grad_kernel<CF_FP32>(vec, cluster, gate, full);
     void *args[] = {&a};
-    cudaError_t e = launch(fn, dim3(unsigned(p.sets * p.cluster)), p.threads, p.cluster, pdl, stream, args);
+    const int smem = ring_bytes(a.dtype, vec, a.gate && a.rows_per_gate == 1 ? 5 : 4, 1, p.threads);
+    cudaError_t e = allow_smem(fn);
+    if (e != cudaSuccess) return e;
+    e = launch(fn, dim3(unsigned(p.sets * p.cluster)), p.threads, p.cluster, pdl, stream, args, smem);
     if (e != cudaSuccess) return e;
     int nsums = 0;
     for (int k = 0; k < 4; ++k) nsums += a.sum_at[k] >= 0;

@@ -18,7 +18,8 @@ struct BlockNormsArgs {
     uint32_t rows_per_gate;
     int cols, post, pre, dtype;
     float scale, alpha, eps;
-    int lanes;  // threads of a row (set by the launcher)
+    int gates;
+    int lanes, chunk, gates_along;  // threads of a row, rows of them, a gate with every row (the launcher's)
 };
 // vec: columns a multiple of 8, everything 16-byte aligned
 cudaError_t launch_block_norms(BlockNormsArgs a, bool vec, int sms, bool pdl, cudaStream_t stream);

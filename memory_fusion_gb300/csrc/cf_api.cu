@@ -2064,6 +2064,7 @@ extern "C" cf_status cf_stitch_block_norms_ex(const void *h, const void *x, cons
     a.post_weight = post_weight, a.post_bias = post_bias, a.pre_weight = pre_weight, a.pre_bias = pre_bias;
     a.x_out = x_out, a.y = y;
     a.rows = rows;
+    a.gates = int(gate ? gates : 1);
     a.rows_per_gate = uint32_t(gate ? rows / gates : rows);
     a.cols = int(cols);
     a.post = int(post), a.pre = int(pre), a.dtype = int(dtype);
