@@ -890,9 +890,11 @@ CF_API cf_status cf_gemm_linear_grad_ex(const void *dY, const void *X, const voi
  * pointers aligned to their element (16 bytes, with cols a multiple of 8, is
  * faster).
  * workspace (device) >= cf_stitch_workspace_size() bytes, the gradient
- * cf_stitch_block_norms_grad_workspace_size(), 16-byte aligned there; nothing of
- * it has to be zero.
- * Tuning fields used (_ex): disable_pdl. */
+ * cf_stitch_block_norms_grad_workspace_size(), 16-byte aligned there; zeroed
+ * once, as for every call.
+ * Tuning fields used (_ex): disable_pdl, timeout_us, extra_arrivals (TEST HOOK:
+ * > 0 makes the wait for a row run out, of rows in bulk copies: cols of a
+ * multiple of 8 from 512 to 8192, the gradient from 256 on, all 16-byte aligned). */
 CF_API size_t cf_stitch_block_norms_grad_workspace_size(int64_t rows, int64_t cols);
 
 CF_API cf_status cf_stitch_block_norms(const void *h, const void *x, const void *gate, const float *post_weight,

@@ -26,10 +26,6 @@
 #include "pieces.cuh"
 #include "ptx.cuh"
 
-#ifndef NREG
-#define NREG 96
-#define NTHR 512
-#endif
 namespace cf {
 namespace {
 
@@ -186,30 +182,38 @@ __device__ __forceinline__ void load_vector(Two (&x)[4], const float *v, float n
                            cols.live(p, j + 1) ? __ldg(v + cols.at(p, j + 1)) : 0.f);
     }
 }
-// Rows on their way, in shared memory: a thread fills and reads its own columns alone, so nobody waits for anybody.  The
-// ring has kDepth stages of up to kRows rows (one of each of that many matrices), a row kP pieces a thread.  (16-bit
-// numbers that start anywhere cannot be copied so; theirs are loaded when they are needed.)
+// How rows come in.
+enum RowMode : int {
+    LOOSE = 0,  // numbers that start anywhere: a thread takes every lanes-th, fp32 ones ahead of time, in copies of 4 bytes
+    SHORT = 1,  // 16-byte aligned, few columns: copies of 16 bytes ahead of time, by the thread that needs them
+    WIDE = 2,   // 16-byte aligned, whole warps: bulk copies ahead of time, one a row
+};
+
+constexpr int kMostRingRows = 5;
+
+// Rows on their way, in shared memory, several stages of up to kRows rows (one of each of that many matrices), a row kP
+// pieces a thread.  LOOSE and SHORT: a thread fills and reads its own columns alone, so nobody waits for anybody.
 __host__ __device__ constexpr int ring_depth(int dt) { return dt == CF_FP32 ? 2 : 4; }
-__host__ __device__ constexpr bool has_ring(int dt, bool vec, int pieces) { return (vec || dt == CF_FP32) && pieces <= 2; }
-constexpr int kMostSmem = 232448;  // of a CTA (227 KB)
-inline int ring_bytes(int dt, bool vec, int rows, int pieces, int threads) {
-    return has_ring(dt, vec, pieces) ? ring_depth(dt) * rows * threads * pieces * 8 * type_bytes(dt) : 0;
+__host__ __device__ constexpr bool has_ring(int dt, int mode, int pieces) {
+    return (mode != LOOSE || dt == CF_FP32) && pieces <= 2;
 }
-template <int kDt, bool kVec, int kRows, int kP>
+template <int kDt, int kMode, int kRows, int kP>
 struct RowRing {
     using E = typename Element<kDt>::type;
-    static constexpr bool kOn = has_ring(kDt, kVec, kP);
+    static constexpr bool kVec = kMode != LOOSE;
+    static constexpr bool kOn = has_ring(kDt, kMode, kP);
     static constexpr int kDepth = ring_depth(kDt);
     static constexpr int kCopies = kVec ? Piece<kDt>::kWords / 4 : 8;  // of a piece
-    static constexpr uint32_t kBytes = kVec ? 16 : 4;                  // of a copy
+    static constexpr uint32_t kBytes = kVec ? 16 : 4;                                   // of a copy
     const E *src[kRows];  // this thread's first column of the next row; null: zeros
     const Columns<kVec> &cols;
     uint32_t base, step;  // of this thread's copies; from one to the next
     int rows, stage, left;  // rows: of a stage; left: rows to come
     size_t apart;
 
-    __device__ __forceinline__ RowRing(const Columns<kVec> &c, uint32_t ring, int rows_, int left_)
-        : cols(c), base(ring + threadIdx.x * kBytes), step(blockDim.x * kBytes), rows(rows_), stage(0), left(left_),
+    __device__ __forceinline__ RowRing(const Columns<kVec> &c, const RingArgs &r, uint8_t *ring, const Group &, int rows_,
+                                       int left_, volatile uint32_t *)
+        : cols(c), base(ptx::smem_u32(ring) + threadIdx.x * kBytes), step(blockDim.x * kBytes), rows(rows_), stage(0), left(left_),
           apart(size_t(c.n)) {}
     __device__ __forceinline__ void matrix(int k, const void *m, int64_t row) {
         src[k] = m ? static_cast<const E *>(m) + (left > 0 ? size_t(row) * apart : 0) +
@@ -271,6 +275,7 @@ struct RowRing {
             }
         }
     }
+    // on to the next row
     __device__ __forceinline__ void next() {
         if constexpr (kOn) {
             stage = stage == kDepth - 1 ? 0 : stage + 1;
@@ -280,6 +285,128 @@ struct RowRing {
                 if (left > 0 && src[k] != nullptr) src[k] += apart;
             --left;
         }
+    }
+    __device__ __forceinline__ void release(int) {}
+    __device__ __forceinline__ void finish() {}
+};
+
+// WIDE: the row's first thread asks for whole rows (of the CTA's share) in bulk copies, which complete on an mbarrier a
+// stage, and refills a stage when the exchange of the row's sums has shown that every thread is through with it.  What it
+// alone needs lies in shared memory: the other threads' registers hold the sums.  (With copies by each thread, their
+// addresses and predicates were a fifth of the gradient's instructions.)
+struct RingState {
+    const void *src[kMostRingRows];  // the next row's share of this CTA; null: zeros
+    int left, fill, issued;          // rows to ask for; the stage to fill next; rows asked for
+    uint32_t bytes;                  // of a stage
+};
+constexpr uint32_t kRingHead = 2048;  // of up to 16 groups: 8 mbarriers and the leader's state, 128 bytes
+static_assert(sizeof(RingState) <= 64, "behind the mbarriers");
+template <int kDt, int kRows, int kP>
+struct RowRing<kDt, WIDE, kRows, kP> {
+    using E = typename Element<kDt>::type;
+    static constexpr bool kOn = true;
+    const Columns<true> &cols;
+    const RingArgs &ring;
+    volatile uint32_t *abort;
+    RingState *state;
+    uint32_t bar, at, pitch;  // of the row in hand: its mbarrier, the thread's numbers; from a row to the next
+    int rows, stage;
+    uint32_t phase;
+    bool leader;
+
+    __device__ __forceinline__ RowRing(const Columns<true> &c, const RingArgs &r, uint8_t *smem, const Group &g, int rows_,
+                                       int left, volatile uint32_t *abort_)
+        : cols(c), ring(r), abort(abort_), rows(rows_), stage(0), phase(0), leader(g.t == 0) {
+        const int group = int(threadIdx.x) / c.lanes;
+        pitch = uint32_t(c.lanes) * kP * 8 * sizeof(E);
+        bar = ptx::smem_u32(smem) + uint32_t(group) * 128u;
+        state = reinterpret_cast<RingState *>(smem + group * 128 + 64);
+        at = ptx::smem_u32(smem) + kRingHead + uint32_t(group * r.depth * rows) * pitch + uint32_t(c.c0) * 8 * sizeof(E);
+        if (leader) {
+            for (int s = 0; s < r.depth; ++s) ptx::mbar_init(bar + 8 * s, 1 + r.extra_arrivals);
+            ptx::fence_mbarrier_init_cluster();
+            state->left = left;
+            state->fill = state->issued = 0;
+            state->bytes = 0;
+        }
+    }
+    __device__ __forceinline__ uint32_t share() const {
+        return uint32_t(min(cols.lanes * kP * 8, cols.n - cols.first)) * uint32_t(sizeof(E));
+    }
+    // (what no copy fills is zero)
+    __device__ __forceinline__ void matrix(int k, const void *m, int64_t row) {
+        if (leader) {
+            state->src[k] =
+                m && k < rows ? static_cast<const E *>(m) + (state->left > 0 ? size_t(row) * cols.n + cols.first : 0)
+                              : nullptr;
+            if (m && k < rows) state->bytes += share();
+        }
+        if (k >= rows) return;
+        for (int p = 0; p < kP; ++p)
+            if (!m || !cols.live(p, 0))
+                for (int s = 0; s < ring.depth; ++s)
+                    for (uint32_t b = 0; b < 8 * sizeof(E); b += 4)
+                        ptx::st_shared_u32(at + uint32_t(s * rows + k) * pitch + uint32_t(p * cols.lanes) * 8 * sizeof(E) + b,
+                                           0u);
+    }
+    __device__ __forceinline__ static void issue(RingState *st, const RingArgs &ring, uint32_t bars, uint32_t first,
+                                              uint32_t pitch, int rows, uint32_t share, size_t apart,
+                                              volatile uint32_t *abort, int n) {
+        const uint64_t policy = ptx::policy_evict_first();
+        for (; n > 0; --n) {
+            const int to = st->fill;
+            st->fill = to + 1 == ring.depth ? 0 : to + 1;
+            if (st->left <= 0 || *abort) return;
+            const uint32_t full = bars + 8 * to;
+            ptx::mbar_arrive_expect_tx(full, st->bytes);
+            for (int k = 0; k < rows; ++k) {
+                const uint8_t *const src = static_cast<const uint8_t *>(st->src[k]);
+                if (src == nullptr) continue;
+                ptx::bulk_load_g2s_hint(first + uint32_t(to * rows + k) * pitch, src, share, full, policy);
+                st->src[k] = src + apart;
+            }
+            --st->left;
+            ++st->issued;
+        }
+    }
+    // every thread of the row has taken what it needs of the last n rows.  (Before the first ones: the barriers'
+    // initialisation and the zeros are known to all threads.)
+    __device__ __forceinline__ void release(int n) {
+        if (leader)  // (c0 is 0)
+            issue(state, ring, bar - 8 * stage, at - uint32_t(stage * rows) * pitch, pitch, rows, share(),
+                  size_t(cols.n) * sizeof(E), abort, n);
+        __syncwarp();
+    }
+    __device__ __forceinline__ void start() { release(ring.depth); }
+    __device__ __forceinline__ void turn() {
+        ptx::mbar_wait_bounded(bar, phase, ring.timeout_ns, abort, ring.err, 0x76000000u | uint32_t(stage));
+    }
+    __device__ __forceinline__ void take(Piece<kDt> &v, int k, int p) {
+        const uint32_t from = at + uint32_t(k) * pitch + uint32_t(p * cols.lanes) * 8 * sizeof(E);
+#pragma unroll
+        for (int j = 0; j < Piece<kDt>::kWords / 4; ++j) {
+            const uint4 q = ptx::ld_shared_v4(from + 16 * j);
+            v.w[4 * j] = q.x, v.w[4 * j + 1] = q.y, v.w[4 * j + 2] = q.z, v.w[4 * j + 3] = q.w;
+        }
+    }
+    __device__ __forceinline__ void next() {
+        at += uint32_t(rows) * pitch;
+        bar += 8;
+        if (++stage == ring.depth) {
+            stage = 0;
+            phase ^= 1u;
+            at -= uint32_t(ring.depth * rows) * pitch;
+            bar -= 8 * ring.depth;
+        }
+    }
+    // nothing is on its way when the CTA leaves (after a wait that ran out there might be)
+    __device__ __forceinline__ void finish() {
+        if (!leader) return;
+        volatile uint32_t local = 0;
+        const int issued = state->issued;
+        for (int s = 0; s < ring.depth && s < issued; ++s)
+            ptx::mbar_wait_bounded(bar + 8 * (s - stage), uint32_t((issued - 1 - s) / ring.depth) & 1u, ring.timeout_ns,
+                                   &local, nullptr, 0);
     }
 };
 
@@ -325,9 +452,12 @@ __device__ __forceinline__ float spread(Group &g, int norm, Two (&x)[kP][4], con
 }
 
 // kP pieces a thread.  kFull: LayerNorms or biases, too.  A worker takes a stretch of neighbouring rows, as in the gradient.
-template <int kDt, bool kVec, int kP, bool kFull>
-__global__ void __maxnreg__(kP == 4 ? 64 : NREG) block_norms_kernel(const BlockNormsArgs a) {
-    extern __shared__ __align__(16) uint8_t ring_smem[];
+template <int kDt, int kMode, int kP, bool kFull>
+__global__ void __maxnreg__(kP == 4 ? 64 : 128) block_norms_kernel(const BlockNormsArgs a) {
+    constexpr bool kVec = kMode != LOOSE;
+    extern __shared__ __align__(128) uint8_t ring_smem[];
+    __shared__ uint32_t abort;
+    if (threadIdx.x == 0) abort = 0u;
     __shared__ __align__(16) float slots[2 * 32 + 8 * 8];  // of each of up to 8 groups of warps, rounded up to four
     for (int i = threadIdx.x; i < int(sizeof(slots) / 4); i += blockDim.x) slots[i] = 0.f;
     ptx::griddep_launch_dependents();
@@ -345,7 +475,6 @@ __global__ void __maxnreg__(kP == 4 ? 64 : NREG) block_norms_kernel(const BlockN
     g.half = (g.warps + 3) & ~3;
     g.slots = slots + group * 2 * g.half;
     g.turn = 0;
-    __syncthreads();
     const Columns<kVec> cols{g.t, a.lanes, 0, a.cols};
     const int groups = int(blockDim.x) / a.lanes;
     const float inv_n = 1.f / float(a.cols);
@@ -354,10 +483,11 @@ __global__ void __maxnreg__(kP == 4 ? 64 : NREG) block_norms_kernel(const BlockN
     const int first = int(min(a.rows, mine * a.chunk)), last = int(min(a.rows, int64_t(first) + a.chunk));
     // rows that threads of one warp may share a warp's turn with: as many turns as any; else their own
     const int turns = a.lanes < 32 ? a.chunk : last - first;
-    RowRing<kDt, kVec, 3, kP> ring(cols, ptx::smem_u32(ring_smem), a.gates_along ? 3 : 2, last - first);
+    RowRing<kDt, kMode, 3, kP> ring(cols, a.ring, ring_smem, g, a.gates_along ? 3 : 2, last - first, &abort);
     ring.matrix(0, a.h, first);
     ring.matrix(1, a.x, first);
     ring.matrix(2, a.gates_along ? a.gate : nullptr, first);
+    __syncthreads();
     ring.start();
 
     Two w1[kP][4], w2[kP][4];  // Post's weight times the gate; Pre's
@@ -432,10 +562,17 @@ __global__ void __maxnreg__(kP == 4 ? 64 : NREG) block_norms_kernel(const BlockN
             }
             if (xo) store_piece<kDt, kVec>(xo, x[p], cols, p, on);
         }
-        ring.next();
         if (xo) xo += a.cols;
-        if (yo == nullptr) continue;
+        if (yo == nullptr) {
+            if (g.warps > 1) ptx::named_bar_sync(g.bar, uint32_t(g.lanes));
+            __syncwarp();
+            ring.next();
+            ring.release(1);
+            continue;
+        }
         root = Two(spread<kVec, kP, kFull>(g, a.pre, x, cols, inv_n, a.eps));
+        ring.next();
+        ring.release(1);
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
             Two b[4];
@@ -449,6 +586,7 @@ __global__ void __maxnreg__(kP == 4 ? 64 : NREG) block_norms_kernel(const BlockN
         }
         yo += a.cols;
     }
+    ring.finish();
 }
 
 // ---------------------------------------------------------------------------
@@ -456,14 +594,19 @@ __global__ void __maxnreg__(kP == 4 ? 64 : NREG) block_norms_kernel(const BlockN
 // ---------------------------------------------------------------------------
 // a thread's columns of a vector of the workspace
 template <bool kVec>
-__device__ __forceinline__ void store_floats(float *out, const Two (&x)[4], const Columns<kVec> &cols) {
+__device__ __forceinline__ void store_floats(float *out, const Two (&x)[4], const Columns<kVec> &cols, int p) {
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
         const float2 q = x[j / 2].parts();
-        if (kVec && cols.live(0, j)) __stcg(reinterpret_cast<float2 *>(out + cols.at(0, j)), q);
-        if (!kVec && cols.live(0, j)) __stcg(out + cols.at(0, j), q.x);
-        if (!kVec && cols.live(0, j + 1)) __stcg(out + cols.at(0, j + 1), q.y);
+        if (kVec && cols.live(p, j)) __stcg(reinterpret_cast<float2 *>(out + cols.at(p, j)), q);
+        if (!kVec && cols.live(p, j)) __stcg(out + cols.at(p, j), q.x);
+        if (!kVec && cols.live(p, j + 1)) __stcg(out + cols.at(p, j + 1), q.y);
     }
+}
+
+// Bytes of the sums over all gates that the CTA's threads keep in shared memory.
+__host__ __device__ constexpr int totals_bytes(bool gate, bool full, int pieces, int threads) {
+    return gate ? threads * pieces * 32 * (full ? 2 : 1) : 0;
 }
 
 // With hc and xc the rows without their means (RMSNorm: the rows), g2 = dy w2 and w1 = scale gate weight, every sum that
@@ -473,16 +616,20 @@ __device__ __forceinline__ void store_floats(float *out, const Two (&x)[4], cons
 //     sum w1 d h^ = r1 (sum w1 hc dx' + r2 (sum w1 hc g2 - mean(g2) sum w1 hc - r2 mean(g2 x^) sum w1 hc xc)),
 // so one exchange between the threads serves where three would follow one another (16384 x 4096 bf16: 287 us with
 // three).  A LayerNorm's means come one exchange before.
-// Rows ahead go through a ring in shared memory, of which a thread fills and reads its own columns alone, so nobody waits
-// for anybody: kept in registers on their way, they left no room for the sums (16384 x 4096 bf16: 172 us).
+// (Rows ahead kept in registers left no room for the sums: 16384 x 4096 bf16 172 us, 158 with the ring in shared memory.)
 // kFull: LayerNorms or biases, too.  kGate: a gate, whose rows' sums are closed where the next gate begins.
-template <int kDt, bool kVec, bool kCluster, bool kGate, bool kFull>
+// kP pieces a thread, up to 512 threads an SM with 128 registers: two where those hold them (not with biases' sums), so
+// that a row of 4096 takes half of the SM's threads and the other half, with a row of its own, works while this one
+// exchanges its sums.
+template <int kDt, int kMode, bool kCluster, bool kGate, bool kFull, int kP>
 __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsGradArgs a) {
+    constexpr bool kVec = kMode != LOOSE, kWide = kMode == WIDE;
     constexpr int kV = kFull ? 16 : 8;
-    extern __shared__ __align__(16) uint8_t ring_smem[];
-    __shared__ float slots[2 * (16 * kV + 8 * 32) * (kCluster ? 8 : 1)];  // of up to 8 groups, each rounded up to 32
-    __shared__ float sums[kCluster ? 1 : 512 * 8];
+    extern __shared__ __align__(128) uint8_t smem[];  // the sums over all gates, the ring
+    __shared__ uint32_t abort;
+    __shared__ float slots[kCluster ? 2 * 16 * kV * 8 : 2 * (16 * kV + 8 * 32)];  // (up to 8 groups, each rounded up to 32)
     using E = typename Element<kDt>::type;
+    if (threadIdx.x == 0) abort = 0u;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     Group g;
@@ -502,7 +649,7 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
         for (int i = threadIdx.x; i < int(sizeof(slots) / 4); i += blockDim.x) slots[i] = 0.f;
         __syncthreads();
     }
-    const Columns<kVec> cols{g.t, a.lanes, int(g.rank) * a.lanes * 8, a.cols};
+    const Columns<kVec> cols{g.t, a.lanes, int(g.rank) * a.lanes * kP * 8, a.cols};
     const int groups = int(blockDim.x) / a.lanes;
     const int set = int(blockIdx.x) / a.cluster, worker = set * groups + group;
     const int chunk = int(a.chunk);
@@ -513,97 +660,135 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
     const bool lh = kFull && a.post == CF_NORM_LAYER, lx = kFull && a.pre == CF_NORM_LAYER;
     if constexpr (kCluster) ptx::cluster_sync();  // nobody writes into a CTA that has not started
 
-    Two w2[4], w1[4];  // Pre's weight; scale * gate * Post's weight
-    load_vector<kVec>(w2, a.pre_weight, 1.f, cols, 0);
-    Two sa[4], sb[4], sc[4], sd[4], ta[4], tb[4];
+    Two w2[kP][4], w1[kP][4];  // Pre's weight; scale * gate * Post's weight
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sa[j] = sb[j] = sc[j] = sd[j] = ta[j] = tb[j] = Two(0.f);
+    for (int p = 0; p < kP; ++p) load_vector<kVec>(w2[p], a.pre_weight, 1.f, cols, p);
+    // sums over the rows, those of the gate in hand in sa and sb; in shared memory, which no other thread looks at, those
+    // of all gates
+    Two sa[kP][4], sc[kP][4], sb[kP][4], sd[kP][4];
+    float *const done = reinterpret_cast<float *>(smem) + threadIdx.x * 2;
+    uint8_t *const ring_smem = smem + totals_bytes(kGate, kFull, kP, int(blockDim.x));
+    auto total = [&](int k, int p, int j) -> float2 & {
+        return *reinterpret_cast<float2 *>(done + ((k * kP + p) * 4 + j) * 2 * int(blockDim.x));
+    };
+#pragma unroll
+    for (int p = 0; p < kP; ++p)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sa[p][j] = sb[p][j] = sc[p][j] = sd[p][j] = Two(0.f);
+            if constexpr (kGate) {
+                total(0, p, j) = make_float2(0.f, 0.f);
+                if constexpr (kFull) total(1, p, j) = make_float2(0.f, 0.f);
+            }
+        }
 
-    Piece<kDt> gate;
     int gate_at = 0, gate_end = 0;  // the gate in hand, the first row behind its rows
-    auto scaled_gate = [&](int j) {
-        return Two(a.scale) * (a.gate ? Two(gate.get(2 * j), gate.get(2 * j + 1)) : Two(1.f));
-    };
-    auto take_gate = [&](int of, bool here) {  // here: it lies in `gate`
-        gate_at = of;
-        gate_end = int((uint32_t(of) + 1u) * a.rows_per_gate);
-        if (a.gate && !here)
-            load_piece<kDt, kVec>(gate, static_cast<const E *>(a.gate) + size_t(of) * a.cols, cols, 0, true);
-        load_vector<kVec>(w1, a.post_weight, 1.f, cols, 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w1[j] = live_two(w1[j] * scaled_gate(j), cols, 0, j);
-    };
-    gate.zero();
-    const bool gates_along = kGate && RowRing<kDt, kVec, 5, 1>::kOn && a.gate && a.rows_per_gate == 1;
-    if (kGate && !gates_along && first < last) {
-        take_gate(int(uint32_t(first) / a.rows_per_gate), false);
-    } else if (!kGate) {
-        load_vector<kVec>(w1, a.post_weight, 1.f, cols, 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w1[j] = live_two(w1[j] * Two(a.scale), cols, 0, j);
-    }
-
-    RowRing<kDt, kVec, 5, 1> ring(cols, ptx::smem_u32(ring_smem), gates_along ? 5 : 4, last - first);
+    const bool gates_along = kGate && RowRing<kDt, kMode, 5, kP>::kOn && a.gate && a.rows_per_gate == 1;
+    RowRing<kDt, kMode, 5, kP> ring(cols, a.ring, ring_smem, g, gates_along ? 5 : 4, last - first, &abort);
     ring.matrix(0, a.h, first);
     ring.matrix(1, a.dy ? a.x_out : nullptr, first);
     ring.matrix(2, a.dy, first);
     ring.matrix(3, a.dx_out, first);
     ring.matrix(4, gates_along ? a.gate : nullptr, first);
+    __syncthreads();
     ring.start();
+    // scale * gate, from memory or from the row of gates in hand
+    auto scaled_gate = [&](Two (&k)[4], int of, int p, bool here) {
+        Piece<kDt> q;
+        q.zero();
+        if (here) ring.take(q, 4, p);
+        else if (a.gate) load_piece<kDt, kVec>(q, static_cast<const E *>(a.gate) + size_t(of) * a.cols, cols, p, true);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = Two(a.scale) * (a.gate ? Two(q.get(2 * j), q.get(2 * j + 1)) : Two(1.f));
+    };
+    auto take_gate = [&](int of, bool here) {
+        gate_at = of;
+        gate_end = int((uint32_t(of) + 1u) * a.rows_per_gate);
+#pragma unroll
+        for (int p = 0; p < kP; ++p) {
+            Two k[4];
+            scaled_gate(k, of, p, here);
+            load_vector<kVec>(w1[p], a.post_weight, 1.f, cols, p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w1[p][j] = live_two(w1[p][j] * k[j], cols, p, j);
+        }
+    };
+    if (kGate && first < last) {
+        if (!gates_along) take_gate(int(uint32_t(first) / a.rows_per_gate), false);
+    } else {
+#pragma unroll
+        for (int p = 0; p < kP; ++p) {
+            load_vector<kVec>(w1[p], a.post_weight, 1.f, cols, p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w1[p][j] = live_two(w1[p][j] * Two(a.scale), cols, p, j);
+        }
+    }
     size_t at = first < last ? size_t(first) * a.cols : 0;  // where the row in hand lies
     for (int i = 0; i < turns; ++i) {
         const int r = first + i;
-        const bool on = r < last;
+        const bool on = kWide || r < last;
         ring.turn();
-        Piece<kDt> raw[4];
+        if (gates_along && on) take_gate(r, true);
+        Piece<kDt> raw[4][kP];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ring.take(raw[k], k, 0);
-        if (gates_along && on) {
-            ring.take(gate, 4, 0);
-            take_gate(r, true);
-        }
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int p = 0; p < kP; ++p) ring.take(raw[k][p], k, p);
         ring.next();
-        Two h[4], x[4], y[4], d[4];
-        raw[0].unpack(h), raw[1].unpack(x), raw[2].unpack(y), raw[3].unpack(d);
+        // columns 2j and the next of the k-th matrix's row
+        auto pair = [&](int k, int p, int j) { return Two(raw[k][p].get(2 * j), raw[k][p].get(2 * j + 1)); };
+        Two mh(0.f), mx(0.f);
         if (lh || lx) {
             Two s(0.f), t(0.f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s = s + h[j], t = t + x[j];
+            for (int p = 0; p < kP; ++p)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s = s + pair(0, p, j), t = t + pair(1, p, j);
             float v[2] = {s.sum(), t.sum()};
             row_sums<2, kCluster>(g, v);
-            const Two mh(lh ? -v[0] * inv_n : 0.f), mx(lx ? -v[1] * inv_n : 0.f);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                h[j] = live_two(h[j] + mh, cols, 0, j);
-                x[j] = live_two(x[j] + mx, cols, 0, j);
-            }
+            mh = Two(lh ? -v[0] * inv_n : 0.f);
+            mx = Two(lx ? -v[1] * inv_n : 0.f);
         }
+        auto h_of = [&](int p, int j) { return kFull ? live_two(pair(0, p, j) + mh, cols, p, j) : pair(0, p, j); };
+        auto x_of = [&](int p, int j) { return kFull ? live_two(pair(1, p, j) + mx, cols, p, j) : pair(1, p, j); };
         constexpr int kSums = kFull ? 12 : 6;
-        Two p[kSums];
-#pragma unroll
-        for (int k = 0; k < kSums; ++k) p[k] = Two(0.f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const Two g2 = y[j] * w2[j], wh = w1[j] * h[j];
-            p[0] = fma(h[j], h[j], p[0]);
-            p[1] = fma(x[j], x[j], p[1]);
-            p[2] = fma(g2, x[j], p[2]);
-            p[3] = fma(wh, d[j], p[3]);
-            p[4] = fma(wh, g2, p[4]);
-            p[5] = fma(wh, x[j], p[5]);
-            if constexpr (kFull) {
-                p[6] = p[6] + g2;
-                p[7] = p[7] + wh;
-                p[8] = fma(w1[j], d[j], p[8]);
-                p[9] = fma(w1[j], g2, p[9]);
-                p[10] = fma(w1[j], x[j], p[10]);
-                p[11] = p[11] + w1[j];
-            }
-        }
         float v[kV];
+        {
+            Two s[kSums];
 #pragma unroll
-        for (int k = 0; k < kV; ++k) v[k] = k < kSums ? p[k < kSums ? k : 0].sum() : 0.f;
+            for (int k = 0; k < kSums; ++k) s[k] = Two(0.f);
+#pragma unroll
+            for (int p = 0; p < kP; ++p)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const Two h = h_of(p, j), x = x_of(p, j), d = pair(3, p, j);
+                    const Two g2 = pair(2, p, j) * w2[p][j], wh = w1[p][j] * h;
+                    s[0] = fma(h, h, s[0]);
+                    s[1] = fma(x, x, s[1]);
+                    s[2] = fma(g2, x, s[2]);
+                    s[3] = fma(wh, d, s[3]);
+                    s[4] = fma(wh, g2, s[4]);
+                    s[5] = fma(wh, x, s[5]);
+                    if constexpr (kFull) {
+                        s[6] = s[6] + g2;
+                        s[7] = s[7] + wh;
+                        s[8] = fma(w1[p][j], d, s[8]);
+                        s[9] = fma(w1[p][j], g2, s[9]);
+                        s[10] = fma(w1[p][j], x, s[10]);
+                        s[11] = s[11] + w1[p][j];
+                    }
+                }
+#pragma unroll
+            for (int k = 0; k < kV; ++k) v[k] = k < kSums ? s[k < kSums ? k : 0].sum() : 0.f;
+        }
         row_sums<kV, kCluster>(g, v);
+        ring.release(1);
+        if constexpr (kP == 2) {  // (unpacked once more: held as fp32 over the exchange, they do not fit)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int p = 0; p < kP; ++p) raw[k][p].pin();
+        }
         // (an eps of 0 would make a NaN of a row that is not there)
         const float r1 = a.post == CF_NORM_NONE ? 1.f : on ? reciprocal_root(fmaf(v[0], inv_n, a.eps)) : 0.f;
         const float r2 = a.pre == CF_NORM_NONE ? 1.f : on ? reciprocal_root(fmaf(v[1], inv_n, a.eps)) : 0.f;
@@ -618,73 +803,89 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
                : 0.f;
         const Two k1(r1), k2(r2), kb(-r2 * mb), ka(-r2 * ma), kn(-na), km(-r1 * nb);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            d[j] = fma(x[j], kb, fma(y[j] * w2[j], k2, d[j]));
-            if constexpr (kFull) d[j] = d[j] + ka;
-            sc[j] = fma(y[j], x[j] * k2, sc[j]);
-            if constexpr (kFull) sd[j] = sd[j] + y[j], sb[j] = sb[j] + d[j];
-            h[j] = h[j] * k1;
-            sa[j] = fma(d[j], h[j], sa[j]);
-            h[j] = fma(h[j], kn, (w1[j] * d[j]) * k1);
-            if constexpr (kFull) h[j] = h[j] + km;
-            d[j] = d[j] * Two(a.alpha);
+        for (int p = 0; p < kP; ++p) {
+            Two dx[4], dh[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const Two x = x_of(p, j), y = pair(2, p, j);
+                Two d = fma(x, kb, fma(y * w2[p][j], k2, pair(3, p, j)));
+                if constexpr (kFull) d = d + ka;
+                sc[p][j] = fma(y, x * k2, sc[p][j]);
+                if constexpr (kFull) sd[p][j] = sd[p][j] + y, sb[p][j] = sb[p][j] + d;
+                const Two h = h_of(p, j) * k1;
+                sa[p][j] = fma(d, h, sa[p][j]);
+                dh[j] = fma(h, kn, (w1[p][j] * d) * k1);
+                if constexpr (kFull) dh[j] = dh[j] + km;
+                dx[j] = d * Two(a.alpha);
+            }
+            if (a.dx) store_piece<kDt, kVec>(static_cast<E *>(a.dx) + at, dx, cols, p, on);
+            store_piece<kDt, kVec>(static_cast<E *>(a.dh) + at, dh, cols, p, on);
         }
-        if (a.dx) store_piece<kDt, kVec>(static_cast<E *>(a.dx) + at, d, cols, 0, on);
-        store_piece<kDt, kVec>(static_cast<E *>(a.dh) + at, h, cols, 0, on);
         if (on) at += size_t(a.cols);
         if constexpr (kGate) {
             if (on && (r + 1 == last || r + 1 == gate_end)) {  // its last row here
-                Two w[4], b[4];
-                load_vector<kVec>(w, a.post_weight, 1.f, cols, 0);
-                if constexpr (kFull) load_vector<kVec>(b, a.post_bias, 0.f, cols, 0);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const Two k = scaled_gate(j);
-                    ta[j] = fma(k, sa[j], ta[j]);
-                    d[j] = w[j] * sa[j];
-                    if constexpr (kFull) {
-                        d[j] = fma(b[j], sb[j], d[j]);
-                        tb[j] = fma(k, sb[j], tb[j]);
-                        sb[j] = Two(0.f);
-                    }
-                    d[j] = d[j] * Two(a.scale);
-                    sa[j] = Two(0.f);
-                }
                 const int from = gate_end - int(a.rows_per_gate);
-                if (a.dgate && from >= first && gate_end <= last) {
-                    store_piece<kDt, kVec>(static_cast<E *>(a.dgate) + size_t(gate_at) * a.cols, d, cols, 0, true);
-                } else if (a.dgate) {  // slot 0: begun by a worker before; slot 1: here, and goes on
-                    float *const slot = a.slots + (size_t(2) * worker + (from >= first ? 1 : 0)) * a.cols;
-                    store_floats<kVec>(slot, d, cols);
+#pragma unroll
+                for (int p = 0; p < kP; ++p) {
+                    Two w[4], b[4], d[4], gate[4];
+                    scaled_gate(gate, gate_at, p, false);
+                    load_vector<kVec>(w, a.post_weight, 1.f, cols, p);
+                    if constexpr (kFull) load_vector<kVec>(b, a.post_bias, 0.f, cols, p);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        total(0, p, j) = fma(gate[j], sa[p][j], Two(total(0, p, j))).parts();
+                        d[j] = w[j] * sa[p][j];
+                        if constexpr (kFull) {
+                            d[j] = fma(b[j], sb[p][j], d[j]);
+                            total(1, p, j) = fma(gate[j], sb[p][j], Two(total(1, p, j))).parts();
+                            sb[p][j] = Two(0.f);
+                        }
+                        d[j] = d[j] * Two(a.scale);
+                        sa[p][j] = Two(0.f);
+                    }
+                    if (a.dgate && from >= first && gate_end <= last) {
+                        store_piece<kDt, kVec>(static_cast<E *>(a.dgate) + size_t(gate_at) * a.cols, d, cols, p, true);
+                    } else if (a.dgate) {  // slot 0: begun by a worker before; slot 1: here, and goes on
+                        float *const slot = a.slots + (size_t(2) * worker + (from >= first ? 1 : 0)) * a.cols;
+                        store_floats<kVec>(slot, d, cols, p);
+                    }
                 }
                 if (r + 1 < last && !gates_along) take_gate(gate_at + 1, false);
             }
         }
     }
-    // the CTA's sums: those of its groups of threads are added through shared memory
-    const bool wanted[4] = {a.sum_at[0] >= 0, a.sum_at[1] >= 0, a.sum_at[2] >= 0, a.sum_at[3] >= 0};
+    ring.finish();
+    // the CTA's sums: those of its groups of threads are added through shared memory, which the ring needs no more
+    float *const sums = reinterpret_cast<float *>(ring_smem);
+    const int wide = a.lanes * kP * 8;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        if (!wanted[k]) continue;
-        Two v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v[j] = k == 0 ? (kGate ? ta[j] : Two(a.scale) * sa[j])
-                   : k == 1 ? (kGate ? tb[j] : Two(a.scale) * sb[j]) : k == 2 ? sc[j] : sd[j];
+        if (a.sum_at[k] < 0) continue;
         float *const out = a.partials + (size_t(a.sum_at[k]) * a.sets + set) * a.cols;
-        if (kCluster || groups == 1) {
-            store_floats<kVec>(out, v, cols);
-        } else {
-            __syncthreads();
+        if (groups > 1) __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 q = v[j / 2].parts();
-                if (cols.live(0, j)) sums[group * a.lanes * 8 + cols.at(0, j)] = j % 2 ? q.y : q.x;
+        for (int p = 0; p < kP; ++p) {
+            Two v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = k >= 2                       ? (k == 2 ? sc[p][j] : sd[p][j])
+                       : kGate && (kFull || k == 0) ? Two(total(k, p, j))
+                                                    : Two(a.scale) * (k == 0 ? sa[p][j] : sb[p][j]);
+            if (kCluster || groups == 1) {
+                store_floats<kVec>(out, v, cols, p);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 q = v[j / 2].parts();
+                    if (cols.live(p, j)) sums[group * wide + cols.at(p, j)] = j % 2 ? q.y : q.x;
+                }
             }
+        }
+        if (!kCluster && groups > 1) {
             __syncthreads();
             for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
                 float s = 0.f;
-                for (int i = 0; i < groups; ++i) s += sums[i * a.lanes * 8 + c];
+                for (int i = 0; i < groups; ++i) s += sums[i * wide + c];
                 __stcg(out + c, s);
             }
         }
@@ -792,12 +993,13 @@ cudaError_t launch(const void *fn, dim3 grid, int threads, int cluster, bool pdl
 
 // Once per device and kernel, to the most a launch may ask for: launches from several threads set the same value, and
 // none is set under a capture later.
+constexpr int kMostSmem = 232448;  // of a CTA (227 KB)
 cudaError_t allow_smem(const void *fn) {
     struct Entry {
         std::atomic<const void *> fn;
         std::atomic<uint64_t> devices;
     };
-    static Entry table[128];  // (51 kernels)
+    static Entry table[64];  // (48 kernels)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -818,62 +1020,79 @@ cudaError_t allow_smem(const void *fn) {
     return cudaErrorInvalidValue;
 }
 
-template <int kDt, bool kVec, bool kFull>
-const void *forward_kernel(int pieces) {
-    return pieces == 1   ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, kVec, 1, kFull>)
-           : pieces == 2 ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, kVec, 2, kFull>)
-                         : reinterpret_cast<const void *>(&block_norms_kernel<kDt, kVec, 4, kFull>);
-}
-template <int kDt>
-const void *forward_kernel(bool vec, bool full, int pieces) {
-    if (!vec) return forward_kernel<kDt, false, true>(pieces);
-    return full ? forward_kernel<kDt, true, true>(pieces) : forward_kernel<kDt, true, false>(pieces);
-}
 // (what is rare is compiled in its widest form alone)
 template <int kDt>
-const void *grad_kernel(bool vec, bool cluster, bool gate, bool full) {
-    if (!vec)
-        return cluster ? reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, false, true, true, true>)
-                       : reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, false, false, true, true>);
-    if (cluster)
-        return full ? reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, true, true, true, true>)
-                    : reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, true, true, true, false>);
-    if (gate)
-        return full ? reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, true, false, true, true>)
-                    : reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, true, false, true, false>);
-    return full ? reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, true, false, false, true>)
-                : reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, true, false, false, false>);
+const void *forward_kernel(int mode, bool full, int pieces) {
+    if (mode == LOOSE)
+        return pieces == 1   ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, LOOSE, 1, true>)
+               : pieces == 2 ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, LOOSE, 2, true>)
+                             : reinterpret_cast<const void *>(&block_norms_kernel<kDt, LOOSE, 4, true>);
+    if (mode == SHORT)
+        return pieces == 1 ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, SHORT, 1, true>)
+                           : reinterpret_cast<const void *>(&block_norms_kernel<kDt, SHORT, 4, true>);
+    return full ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, WIDE, 2, true>)
+                : reinterpret_cast<const void *>(&block_norms_kernel<kDt, WIDE, 2, false>);
+}
+template <int kDt, int kMode, bool kCluster, bool kGate, bool kFull, int kP>
+const void *grad_of() {
+    return reinterpret_cast<const void *>(&block_norms_grad_kernel<kDt, kMode, kCluster, kGate, kFull, kP>);
+}
+template <int kDt>
+const void *grad_kernel(int mode, bool cluster, bool gate, bool full, int pieces) {
+    if (mode == LOOSE)
+        return cluster ? grad_of<kDt, LOOSE, true, true, true, 1>() : grad_of<kDt, LOOSE, false, true, true, 1>();
+    if (mode == SHORT) return grad_of<kDt, SHORT, false, true, true, 1>();
+    if (cluster) return full ? grad_of<kDt, WIDE, true, true, true, 1>() : grad_of<kDt, WIDE, true, true, false, 1>();
+    if (full) return gate ? grad_of<kDt, WIDE, false, true, true, 1>() : grad_of<kDt, WIDE, false, false, true, 1>();
+    if (pieces == 2) return gate ? grad_of<kDt, WIDE, false, true, false, 2>() : grad_of<kDt, WIDE, false, false, false, 2>();
+    return grad_of<kDt, WIDE, false, true, false, 1>();
+}
+
+// Shared memory of a launch's ring and, WIDE, its depth: what fits with `ctas` CTAs an SM, up to r->depth stages (0: three; 2, 3, 4
+// and 6 of them, 16384 x 4096 bf16 forward: 97, 93, 95 and 135 us, what they take is missing in L1).
+int plan_ring(RingArgs *r, int dt, int mode, int rows, int pieces, int threads, int ctas, int own) {
+    if (!has_ring(dt, mode, pieces)) return 0;
+    const int stage = rows * threads * pieces * 8 * type_bytes(dt);
+    if (mode != WIDE) return ring_depth(dt) * stage;
+    const int room = std::min(kMostSmem, (kMostSmem + 1024) / ctas - 1024) - own - int(kRingHead);
+    r->depth = std::max(1, std::min(r->depth > 0 ? std::min(r->depth, 8) : 3, room / stage));
+    return int(kRingHead) + r->depth * stage;
 }
 
 }  // namespace
 
-constexpr int kForwardThreads = NTHR;
+constexpr int kForwardThreads = 512;  // an SM, with 96 registers each (16384 x 4096 bf16, copies by each thread: 768 with
+                                      // 80 117 us, 1024 with 64 200 us, 512 with 128 102 us, with 96 95 us)
 
 cudaError_t launch_block_norms(BlockNormsArgs a, bool vec, int sms, bool pdl, cudaStream_t stream) {
     const int pieces = (a.cols + 7) / 8;
-    const int per = pieces <= 32 ? 1 : pieces <= 1024 && (pieces + 63) / 64 * 32 <= 512 ? 2 : 4;
+    // a thread's pieces: two, so that what a row costs besides its numbers is shared by more of them
+    const int per = pieces < 64 ? 1 : pieces <= 1024 ? 2 : 4;
     a.lanes = round_lanes((pieces + per - 1) / per);
+    const int mode = !vec ? LOOSE : per == 2 ? WIDE : SHORT;
     const int groups = std::max(1, 256 / a.lanes), threads = groups * a.lanes;
-    // CTAs of up to kForwardThreads an SM, of a stretch of rows each
-    int64_t ctas = std::min<int64_t>((a.rows + groups - 1) / groups, int64_t(sms) * std::max(1, kForwardThreads / threads));
+    // a stretch of rows for each group of threads
+    const int per_sm = std::max(1, kForwardThreads / threads);
+    int64_t ctas = std::min<int64_t>((a.rows + groups - 1) / groups, int64_t(sms) * per_sm);
     a.chunk = int((a.rows + ctas * groups - 1) / (ctas * groups));
     ctas = (a.rows + int64_t(a.chunk) * groups - 1) / (int64_t(a.chunk) * groups);
-    a.gates_along = a.gate && a.rows_per_gate == 1 && has_ring(a.dtype, vec, per);
+    a.gates_along = a.gate && a.rows_per_gate == 1 && has_ring(a.dtype, mode, per);
     const bool full = a.post == CF_NORM_LAYER || a.pre == CF_NORM_LAYER || a.post_bias || a.pre_bias;
-    const void *fn = a.dtype == CF_BF16   ? forward_kernel<CF_BF16>(vec, full, per)
-                     : a.dtype == CF_FP16 ? forward_kernel<CF_FP16>(vec, full, per)
-                                          : forward_kernel<CF_FP32>(vec, full, per);
+    const void *fn = a.dtype == CF_BF16   ? forward_kernel<CF_BF16>(mode, full, per)
+                     : a.dtype == CF_FP16 ? forward_kernel<CF_FP16>(mode, full, per)
+                                          : forward_kernel<CF_FP32>(mode, full, per);
+    const int smem = plan_ring(&a.ring, a.dtype, mode, a.gates_along ? 3 : 2, per, threads, per_sm, 1024);
     void *args[] = {&a};
-    const int smem = ring_bytes(a.dtype, vec, a.gates_along ? 3 : 2, per, threads);
     const cudaError_t e = allow_smem(fn);
     return e != cudaSuccess ? e : launch(fn, dim3(unsigned(ctas)), threads, 1, pdl, stream, args, smem);
 }
 
-BlockNormsGradPlan plan_block_norms_grad(int64_t rows, int64_t cols, int sms) {
+BlockNormsGradPlan plan_block_norms_grad(int64_t rows, int64_t cols, int sms, bool lean, int dtype) {
     BlockNormsGradPlan p;
-    const int64_t pieces = (cols + 7) / 8;
-    p.cluster = int((pieces + 511) / 512);
-    p.lanes = round_lanes((pieces + p.cluster - 1) / p.cluster);
+    const int64_t n = (cols + 7) / 8;
+    p.pieces = lean && dtype != CF_FP32 && n >= 64 && n <= 1024 ? 2 : 1;  // (of fp32, two are too many registers)
+    p.cluster = int((n + 512 * p.pieces - 1) / (512 * p.pieces));
+    p.lanes = round_lanes((n + p.cluster * p.pieces - 1) / (p.cluster * p.pieces));
     const int groups = p.cluster > 1 ? 1 : std::max(1, 256 / p.lanes);
     p.threads = groups * p.lanes;
     const int64_t most = int64_t(sms) * std::max(1, 512 / p.threads) / p.cluster;
@@ -884,21 +1103,34 @@ BlockNormsGradPlan plan_block_norms_grad(int64_t rows, int64_t cols, int sms) {
     return p;
 }
 
+bool block_norms_grad_lean(const BlockNormsGradArgs &a, bool vec) {
+    return vec && a.post != CF_NORM_LAYER && a.pre != CF_NORM_LAYER && !a.post_bias && a.sum_at[1] < 0 && a.sum_at[3] < 0;
+}
+
 cudaError_t launch_block_norms_grad(BlockNormsGradArgs a, const BlockNormsGradPlan &p, bool vec, bool pdl,
                                     cudaStream_t stream) {
     a.lanes = p.lanes;
     a.cluster = p.cluster;
     a.chunk = p.chunk;
     a.sets = p.sets;
-    const bool gate = a.gate != nullptr, cluster = p.cluster > 1;
-    const bool full = a.post_bias || a.sum_at[1] >= 0 || a.sum_at[3] >= 0 || a.post == CF_NORM_LAYER ||
-                      a.pre == CF_NORM_LAYER;
-    const void *fn = a.dtype == CF_BF16   ? grad_kernel<CF_BF16>(vec, cluster, gate, full)
-                     : a.dtype == CF_FP16 ? grad_kernel<CF_FP16>(vec, cluster, gate, full)
-                                          : grad_kernel<CF_FP32>(vec, cluster, gate, full);
+    const bool gate = a.gate != nullptr, cluster = p.cluster > 1, full = !block_norms_grad_lean(a, vec);
+    const int mode = !vec ? LOOSE : p.lanes < 32 ? SHORT : WIDE;
+    const void *fn = a.dtype == CF_BF16   ? grad_kernel<CF_BF16>(mode, cluster, gate, full, p.pieces)
+                     : a.dtype == CF_FP16 ? grad_kernel<CF_FP16>(mode, cluster, gate, full, p.pieces)
+                                          : grad_kernel<CF_FP32>(mode, cluster, gate, full, p.pieces);
     void *args[] = {&a};
-    const int smem = ring_bytes(a.dtype, vec, a.gate && a.rows_per_gate == 1 ? 5 : 4, 1, p.threads);
-    cudaError_t e = allow_smem(fn);
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, fn);
+    if (e != cudaSuccess) return e;
+    const int rows = a.gate && a.rows_per_gate == 1 ? 5 : 4;
+    // (as grad_kernel chooses: what is rare has its gates' sums anyway)
+    const int totals = totals_bytes(gate || mode != WIDE || cluster || (!full && p.pieces == 1), full || mode != WIDE,
+                                    p.pieces, p.threads);
+    // (the ring's place takes the sums of several groups in the end)
+    const int smem = totals + std::max(plan_ring(&a.ring, a.dtype, mode, rows, p.pieces, p.threads,
+                                                 std::max(1, 512 / p.threads), int(attr.sharedSizeBytes) + totals),
+                                       p.threads == p.lanes ? 0 : p.threads * p.pieces * 8 * 4);
+    e = allow_smem(fn);
     if (e != cudaSuccess) return e;
     e = launch(fn, dim3(unsigned(p.sets * p.cluster)), p.threads, p.cluster, pdl, stream, args, smem);
     if (e != cudaSuccess) return e;

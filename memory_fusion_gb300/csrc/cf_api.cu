@@ -2016,6 +2016,13 @@ extern "C" cf_status cf_gemm_linear_grad(const void *dY, const void *X, const vo
 // -------------------------------------------------------------------------
 namespace {
 
+void ring_args(cf::RingArgs *r, void *workspace, const cf_tuning *t) {
+    r->err = static_cast<uint32_t *>(workspace);
+    r->depth = t && t->stages > 0 ? t->stages : 0;
+    r->timeout_ns = 1000ull * (t && t->timeout_us ? t->timeout_us : kDefaultTimeoutUs);
+    r->extra_arrivals = t && t->extra_arrivals > 0 ? uint32_t(t->extra_arrivals) : 0u;
+}
+
 bool norm_kind(int v) { return v == CF_NORM_LAYER || v == CF_NORM_RMS || v == CF_NORM_NONE; }
 bool aligned_to(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
@@ -2055,6 +2062,7 @@ extern "C" cf_status cf_stitch_block_norms_ex(const void *h, const void *x, cons
         vec = vec && aligned16(p);
     }
     if (x_out == y || (gate && (gate == x_out || gate == y))) return CF_ERR_INVALID_ARG;
+    if (!aligned_to(workspace, 4)) return CF_ERR_MISALIGNED;
     if (workspace_bytes < cf_stitch_workspace_size(rows, cols)) return CF_ERR_WORKSPACE_TOO_SMALL;
     cf::DeviceInfo dev;
     st = linear_device(&dev);
@@ -2069,6 +2077,7 @@ extern "C" cf_status cf_stitch_block_norms_ex(const void *h, const void *x, cons
     a.cols = int(cols);
     a.post = int(post), a.pre = int(pre), a.dtype = int(dtype);
     a.scale = scale, a.alpha = alpha, a.eps = eps;
+    ring_args(&a.ring, workspace, tuning);
     const bool pdl = !tuning || tuning->disable_pdl == 0;
     const cudaError_t e =
         cf::launch_block_norms(a, vec, dev.sm_count, pdl, reinterpret_cast<cudaStream_t>(stream));
@@ -2093,8 +2102,12 @@ static size_t block_norms_partials(const cf::BlockNormsGradPlan &p, int64_t cols
 
 extern "C" size_t cf_stitch_block_norms_grad_workspace_size(int64_t rows, int64_t cols) {
     if (rows <= 0 || cols <= 0 || cols > cf::kBlockNormsMaxCols) return cf::kErrBytes;
-    const cf::BlockNormsGradPlan p = cf::plan_block_norms_grad(rows, cols, int(kPlanSms));
-    return cf::kErrBytes + block_norms_partials(p, cols) + size_t(p.workers) * 2 * size_t(cols) * 4;
+    size_t most = 0;
+    for (bool lean : {false, true}) {
+        const cf::BlockNormsGradPlan p = cf::plan_block_norms_grad(rows, cols, int(kPlanSms), lean, CF_BF16);
+        most = std::max(most, block_norms_partials(p, cols) + size_t(p.workers) * 2 * size_t(cols) * 4);
+    }
+    return cf::kErrBytes + most;
 }
 
 extern "C" cf_status cf_stitch_block_norms_grad_ex(
@@ -2147,8 +2160,6 @@ extern "C" cf_status cf_stitch_block_norms_grad_ex(
         }
         return CF_OK;
     }
-    const cf::BlockNormsGradPlan p =
-        cf::plan_block_norms_grad(rows, cols, std::min(dev.sm_count, int(kPlanSms)));
     cf::BlockNormsGradArgs a{};
     a.dy = dy, a.dx_out = dx_out, a.h = h, a.x_out = x_out, a.gate = gate;
     a.post_weight = post_weight, a.post_bias = post_bias, a.pre_weight = pre_weight;
@@ -2157,14 +2168,17 @@ extern "C" cf_status cf_stitch_block_norms_grad_ex(
         a.sum_at[i] = sums[i] ? n++ : -1;
         a.sum_out[i] = sums[i];
     }
+    a.post = int(post), a.pre = dy ? int(pre) : int(CF_NORM_NONE), a.dtype = int(dtype);
+    const cf::BlockNormsGradPlan p = cf::plan_block_norms_grad(rows, cols, std::min(dev.sm_count, int(kPlanSms)),
+                                                               cf::block_norms_grad_lean(a, vec), int(dtype));
     unsigned char *const ws = static_cast<unsigned char *>(workspace) + cf::kErrBytes;
     a.partials = reinterpret_cast<float *>(ws);
     a.slots = reinterpret_cast<float *>(ws + block_norms_partials(p, cols));
     a.rows = rows;
     a.rows_per_gate = uint32_t(gate ? rows / gates : rows);
     a.cols = int(cols);
-    a.post = int(post), a.pre = dy ? int(pre) : int(CF_NORM_NONE), a.dtype = int(dtype);
     a.scale = scale, a.alpha = alpha, a.eps = eps;
+    ring_args(&a.ring, workspace, tuning);
     const cudaError_t e = cf::launch_block_norms_grad(a, p, vec, !tuning || tuning->disable_pdl == 0, cs);
     return e == cudaSuccess ? CF_OK : cuda_fail(e);
 }

@@ -38,35 +38,17 @@ __device__ __forceinline__ typename Element<kDt>::type from_float(float v) {
 
 // Two fp32 numbers, worked on by one instruction.
 struct Two {
-    uint64_t v;
+    float2 v;
     __device__ __forceinline__ Two() {}
-    __device__ __forceinline__ Two(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
-    __device__ __forceinline__ explicit Two(float both) : Two(both, both) {}
-    __device__ __forceinline__ float2 parts() const {
-        float2 p;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(p.x), "=f"(p.y) : "l"(v));
-        return p;
-    }
-    __device__ __forceinline__ float sum() const {
-        const float2 p = parts();
-        return p.x + p.y;
-    }
+    __device__ __forceinline__ explicit Two(float2 p) : v(p) {}
+    __device__ __forceinline__ Two(float lo, float hi) : v(make_float2(lo, hi)) {}
+    __device__ __forceinline__ explicit Two(float both) : v(make_float2(both, both)) {}
+    __device__ __forceinline__ float2 parts() const { return v; }
+    __device__ __forceinline__ float sum() const { return v.x + v.y; }
 };
-__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
-    Two d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return d;
-}
-__device__ __forceinline__ Two operator*(Two a, Two b) {
-    Two d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-    return d;
-}
-__device__ __forceinline__ Two operator+(Two a, Two b) {
-    Two d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-    return d;
-}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) { return Two(__ffma2_rn(a.v, b.v, c.v)); }
+__device__ __forceinline__ Two operator*(Two a, Two b) { return Two(__fmul2_rn(a.v, b.v)); }
+__device__ __forceinline__ Two operator+(Two a, Two b) { return Two(__fadd2_rn(a.v, b.v)); }
 
 // eight numbers, as stored
 template <int kDt>
@@ -74,6 +56,11 @@ struct Piece {
     static constexpr int kWords = kDt == CF_FP32 ? 8 : 4;
     uint32_t w[kWords];
 
+    // what was worked out from the words before is worked out again behind this
+    __device__ __forceinline__ void pin() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) asm volatile("" : "+r"(w[i]));
+    }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[i] = 0u;
