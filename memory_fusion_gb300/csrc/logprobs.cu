@@ -14,6 +14,11 @@
 // Rows start anywhere: a row is cut at 16-byte boundaries of its memory into windows, the first and last of which may be
 // partial and are read number by number.
 //
+// What stands between the loads and HBM's rate is the instructions: 17 a number at first (322 us for 4096 x 128000 bf16).
+// So numbers are worked on in pairs, maxima are taken of 16-bit pairs as they are, and -inf, whose 0 times -inf would be a
+// NaN in the entropy, is raised to a low finite number as a pair too, where the running maximum shows that this changes
+// nothing; elsewhere (rows of nothing but masks) number by number.
+//
 // Top tokens: a thread also remembers its largest logit and the first window that holds it.  The k-th largest of the
 // threads' (largest, window) pairs is a bound below which no top token can lie, and only k threads have anything on the
 // bound or above it; their windows are read again (from L2), and what reaches the bound, little more than k numbers, is
@@ -60,6 +65,66 @@ __device__ __forceinline__ float value_of(uint32_t o) {
 // larger first, of equals the lower index
 __device__ __forceinline__ uint64_t pair_of(uint32_t o, uint32_t index) { return uint64_t(o) << 32 | uint32_t(~index); }
 
+// 16 bytes of numbers
+template <int kDt>
+struct Pack {
+    static constexpr int kN = kDt == CF_FP32 ? 4 : 8;
+    uint32_t u[4];
+
+    __device__ __forceinline__ float get(int j) const {
+        if constexpr (kDt == CF_FP32) return __uint_as_float(u[j]);
+        else if constexpr (kDt == CF_FP16) return __half2float(__ushort_as_half(uint16_t(u[j / 2] >> (j % 2 * 16))));
+        else return __uint_as_float(j % 2 ? u[j / 2] & 0xffff0000u : u[j / 2] << 16);
+    }
+    __device__ __forceinline__ void set(int j, float v) {
+        if constexpr (kDt == CF_FP32) {
+            u[j] = __float_as_uint(v);
+        } else {
+            const uint32_t h = from_float<kDt>(v);
+            u[j / 2] = j % 2 ? (u[j / 2] & 0xffffu) | h << 16 : (u[j / 2] & 0xffff0000u) | h;
+        }
+    }
+    __device__ __forceinline__ Two pair(int j) const { return Two(get(2 * j), get(2 * j + 1)); }
+    __device__ __forceinline__ void set_pair(int j, Two v) {
+        const float2 p = v.parts();
+        if constexpr (kDt == CF_FP32) {
+            u[2 * j] = __float_as_uint(p.x), u[2 * j + 1] = __float_as_uint(p.y);
+        } else if constexpr (kDt == CF_FP16) {
+            const __half2 h = __floats2half2_rn(p.x, p.y);
+            u[j] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            u[j] = ptx::pack_bf16x2(p.x, p.y);
+        }
+    }
+    // the larger ones of two words' numbers; NaNs stay
+    __device__ __forceinline__ static uint32_t larger(uint32_t a, uint32_t b) {
+        uint32_t r;
+        if constexpr (kDt == CF_FP32) asm("max.NaN.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        else if constexpr (kDt == CF_FP16) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    __device__ __forceinline__ float largest() const {
+        Pack m;
+        m.u[0] = larger(larger(u[0], u[1]), larger(u[2], u[3]));
+        return kDt == CF_FP32 ? m.get(0) : max_nan(m.get(0), m.get(1));
+    }
+    __device__ __forceinline__ void raise(uint32_t low) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = larger(u[i], low);
+    }
+    // What -inf is raised to, as a word; and the sizes that m and m + the distance to it must keep to for this to be
+    // right: above `least`, which is so far above it that what it stands for counts 0, and below `most`, so that m s2 is
+    // finite.
+    __device__ __forceinline__ static uint32_t low() {
+        return kDt == CF_FP32 ? 0xf2fc6f7cu /* -1e31 */ : kDt == CF_FP16 ? 0xfbfffbffu /* -65504 */ : 0xf2fcf2fcu;
+    }
+    __device__ __forceinline__ static float least(float s2) {
+        return (kDt == CF_FP16 ? -65504.f : kDt == CF_FP32 ? -1e31f : __uint_as_float(0xf2fc0000u)) + 160.f / s2;
+    }
+    __device__ __forceinline__ static float most(float s2) { return s2 < 1e7f ? 1e30f : 0.f; }
+};
+
 // The windows of a row: 16 bytes of memory each, from the one that holds the row's first number.
 template <int kDt>
 struct Windows {
@@ -72,22 +137,21 @@ struct Windows {
         count = int((int64_t(v) + lead + kN - 1) / kN);
     }
     __device__ __forceinline__ int first(int w) const { return w * kN - lead; }  // index of its first number
-    // what is not of the row is -inf
-    __device__ __forceinline__ void load(float (&x)[kN], int w) const {
+    __device__ __forceinline__ int full0() const { return lead > 0 ? 1 : 0; }    // the first whole window
+    __device__ __forceinline__ int full1() const { return (vocab + lead) / kN; }  // the one behind the last whole window
+    __device__ __forceinline__ Pack<kDt> whole(int w) const {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(row + first(w)));
+        return Pack<kDt>{{v.x, v.y, v.z, v.w}};
+    }
+    // any window, and none; what is not of the row is -inf
+    __device__ __forceinline__ Pack<kDt> any(int w) const {
+        if (w >= full0() && w < full1()) return whole(w);
+        Pack<kDt> p{};
         const int i0 = first(w);
-        if (w < count && i0 >= 0 && i0 + kN <= vocab) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(row + i0);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                if constexpr (kDt == CF_FP32) x[i] = __uint_as_float(u[i]);
-                else x[i] = to_float<kDt>(uint16_t(u[i / 2] >> (i % 2 * 16)));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kN; ++i)
-                x[i] = w < count && i0 + i >= 0 && i0 + i < vocab ? to_float<kDt>(row[i0 + i]) : -inf();
-        }
+        for (int i = 0; i < kN; ++i)
+            p.set(i, w < count && i0 + i >= 0 && i0 + i < vocab ? to_float<kDt>(row[i0 + i]) : -inf());
+        return p;
     }
 };
 
@@ -115,18 +179,17 @@ struct __align__(16) Stats {
     }
 };
 
-// One CTA's view of its share of a row, by whole CTA: the top k pairs (order, index) of it into top[0..k), largest first.
+// One CTA's share of a row: window 0, where it is partial, is the first thread's of the first CTA; the others go round.
 template <int kDt>
 struct Share {
     Windows<kDt> w;
     int part, parts;  // this CTA of the row's
-    __device__ __forceinline__ int window(int step, int t) const {
-        return (step * parts + part) * int(blockDim.x) + t;
+    __device__ __forceinline__ int round() const { return parts * int(blockDim.x); }  // windows from a step to the next
+    __device__ __forceinline__ int window(int step, int t) const {  // step -1: the partial one
+        if (step < 0) return part == 0 && t == 0 && w.full0() > 0 ? 0 : w.count;
+        return w.full0() + (step * parts + part) * int(blockDim.x) + t;
     }
-    __device__ __forceinline__ int steps() const {  // of every thread
-        const int round = parts * int(blockDim.x);
-        return (w.count + round - 1) / round;
-    }
+    __device__ __forceinline__ int steps() const { return (w.count - w.full0() + round() - 1) / round(); }  // of any thread
 };
 
 template <int kDt>
@@ -135,15 +198,14 @@ __device__ void search_tops(const Share<kDt> &sh, int k, uint64_t *top, uint64_t
     uint64_t below = ~uint64_t(0);
     for (int i = 0; i < k; ++i) {
         uint64_t best = 0;
-        for (int step = 0; step < sh.steps(); ++step) {
+        for (int step = -1; step < sh.steps(); ++step) {
             const int w = sh.window(step, int(threadIdx.x));
-            if (w >= sh.w.count) break;
-            float x[Windows<kDt>::kN];
-            sh.w.load(x, w);
+            if (w >= sh.w.count) continue;
+            const Pack<kDt> x = sh.w.any(w);
 #pragma unroll
             for (int j = 0; j < Windows<kDt>::kN; ++j) {
                 const int at = sh.w.first(w) + j;
-                const uint64_t p = pair_of(order(x[j]), uint32_t(at));
+                const uint64_t p = pair_of(order(x.get(j)), uint32_t(at));
                 if (at >= 0 && at < sh.w.vocab && p < below && p > best) best = p;
             }
         }
@@ -178,16 +240,15 @@ __device__ void find_tops(const Share<kDt> &sh, uint64_t most, int k, uint64_t *
     const int have = min(k, __syncthreads_count(most != 0));
     const uint64_t least = *bound;
     const uint32_t least_order = uint32_t(least >> 32), least_window = uint32_t(~least);
-    const int steps = sh.steps();
+    const int steps = sh.steps() + 1;
     for (int i = tid; i < have * steps; i += n) {
-        const int who = i / steps, w = sh.window(i - who * steps, chosen[who]);
+        const int who = i / steps, w = sh.window(i - who * steps - 1, chosen[who]);
         if (w >= sh.w.count) continue;
-        float x[Windows<kDt>::kN];
-        sh.w.load(x, w);
+        const Pack<kDt> x = sh.w.any(w);
 #pragma unroll
         for (int j = 0; j < Windows<kDt>::kN; ++j) {
             const int at = sh.w.first(w) + j;
-            const uint32_t o = order(x[j]);
+            const uint32_t o = order(x.get(j));
             if (at < 0 || at >= sh.w.vocab) continue;
             if (least == 0 || o > least_order || (o == least_order && uint32_t(w) <= least_window)) {
                 const int slot = atomicAdd(found, 1);
@@ -245,39 +306,94 @@ __global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobsArg
     }
 
     Stats st{-inf(), 0.f, 0.f};
-    uint64_t most = 0;
-    const int steps = sh.steps();
-#pragma unroll 1
-    for (int step = 0; step < steps; step += kFly) {
-        float x[kFly][kN];
-#pragma unroll
-        for (int i = 0; i < kFly; ++i) sh.w.load(x[i], sh.window(step + i, tid));
+    uint32_t most_order = 0, most_window = 0;  // (no order is 0)
+    using P = Pack<kDt>;
+    const uint32_t low = P::low();
+    const float least = P::least(s2), beyond = P::most(s2);
+    // n windows from w on, `step` apart
+    auto take = [&](P (&x)[kFly], int n, int w, int step) {
         float high = -inf();
 #pragma unroll
         for (int i = 0; i < kFly; ++i) {
-            float m = x[i][0];
-#pragma unroll
-            for (int j = 1; j < kN; ++j) m = max_nan(m, x[i][j]);
+            if (i >= n) break;
+            const float m = x[i].largest();
             if constexpr (kTop) {
-                const int w = sh.window(step + i, tid);
-                const uint64_t p = pair_of(order(m), uint32_t(w));
-                if (w < sh.w.count && p > most) most = p;
+                const uint32_t o = order(m);
+                if (o > most_order) {
+                    most_order = o;
+                    most_window = uint32_t(w + i * step);
+                }
             }
             high = fmaxf(high, m);
         }
         st.raise(high, s2);
-        const float ref = st.ref();
+        if (st.m > least && fabsf(st.m) < beyond) {
+            const Two k(s2), c(-st.m);
+            Two sum(0.f), weighted(0.f);
 #pragma unroll
-        for (int i = 0; i < kFly; ++i)
+            for (int i = 0; i < kFly; ++i) {
+                if (i >= n) break;
+                if constexpr (kEntropy) x[i].raise(low);
 #pragma unroll
-            for (int j = 0; j < kN; ++j) {
-                float d = (x[i][j] - ref) * s2;
-                if constexpr (kEntropy) d = max_nan(d, -200.f);  // (of -inf: 2^-200 is 0, and 0 times it)
-                const float e = ptx::ex2_approx(d);
-                st.s += e;
-                if constexpr (kEntropy) st.t = fmaf(e, d, st.t);
+                for (int j = 0; j < kN / 2; ++j) {
+                    const Two d = (x[i].pair(j) + c) * k;  // (the difference first: m s2 would be rounded)
+                    const float2 p = d.parts();
+                    const Two e(ptx::ex2_approx(p.x), ptx::ex2_approx(p.y));
+                    sum = sum + e;
+                    if constexpr (kEntropy) weighted = fma(e, d, weighted);
+                }
             }
+            st.s += sum.sum();
+            if constexpr (kEntropy) st.t += weighted.sum();
+        } else {
+            const float ref = st.ref();
+#pragma unroll 1
+            for (int i = 0; i < n; ++i)
+#pragma unroll
+                for (int j = 0; j < kN; ++j) {
+                    float v = x[0].get(j);
+#pragma unroll
+                    for (int q = 1; q < kFly; ++q) v = i == q ? x[q].get(j) : v;
+                    const float d = max_nan((v - ref) * s2, -200.f);  // (of -inf: 2^-200 is 0, and 0 times it)
+                    const float e = ptx::ex2_approx(d);
+                    st.s += e;
+                    st.t = fmaf(e, d, st.t);
+                }
+        }
+    };
+    const int round = sh.round(), w0 = sh.window(0, tid);
+    P x[kFly];
+    if (sh.window(-1, tid) == 0) {
+        x[0] = sh.w.any(0);
+        take(x, 1, 0, 0);
     }
+    // windows that are whole for every thread of the CTA, kFly at a time, the next ones on their way
+    int w = w0, g = 0;
+    const int whole = (sh.w.full1() - (w0 - tid) - int(blockDim.x) + round) / round;  // steps whose last thread's is whole
+    const int turns = max(0, whole) / kFly;
+    if (turns > 0) {
+        P next[kFly];
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) next[i] = sh.w.whole(w + i * round);
+#pragma unroll 1
+        for (; g < turns; ++g, w += kFly * round) {
+#pragma unroll
+            for (int i = 0; i < kFly; ++i) x[i] = next[i];
+            if (g + 1 < turns) {
+#pragma unroll
+                for (int i = 0; i < kFly; ++i) next[i] = sh.w.whole(w + (kFly + i) * round);
+            }
+            take(x, kFly, w, round);
+        }
+    }
+#pragma unroll 1
+    for (; w < sh.w.count; w += kFly * round) {
+#pragma unroll
+        for (int i = 0; i < kFly; ++i) x[i] = sh.w.any(w + i * round);
+        const int n = min(kFly, (sh.w.count - w + round - 1) / round);
+        take(x, n, w, round);
+    }
+    const uint64_t most = most_order == 0 ? 0 : pair_of(most_order, most_window);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1)
         st.add(Stats{__shfl_xor_sync(kAll, st.m, d), __shfl_xor_sync(kAll, st.s, d), __shfl_xor_sync(kAll, st.t, d)}, s2);
@@ -350,52 +466,79 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const Logpr
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     using E = typename Element<kDt>::type;
-    constexpr int kN = Windows<kDt>::kN;
+    using P = Pack<kDt>;
+    constexpr int kN = P::kN;
     const int64_t r = int64_t(blockIdx.x) / a.chunks;
     const int chunk = int(int64_t(blockIdx.x) - r * a.chunks);
     const Windows<kDt> win(static_cast<const E *>(a.logits) + r * a.stride, a.vocab);
     E *const out = static_cast<E *>(a.dlogits) + r * a.dstride;
     const bool same = (reinterpret_cast<uintptr_t>(out) & 15u) == (reinterpret_cast<uintptr_t>(win.row) & 15u);
+    int w = chunk * (a.turns * kFly * kGradThreads) + int(threadIdx.x);
+    const int end = min(win.count, (chunk + 1) * (a.turns * kFly * kGradThreads));
+    P next[kFly];
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) next[i] = win.any(w + i * kGradThreads);
     int64_t target = a.targets ? a.targets[r] : -1;
     if (target < -1 || target >= a.vocab) {
         if (threadIdx.x == 0) ptx::record_error(a.err, 8u /*CF_ERR_DEVICE_BOUNDS*/, kInfoTarget);
         target = -1;
     }
     const float lse = a.lse[r];
-    const float given = target >= 0 && a.dlogprob ? a.dlogprob[r] : 0.f;
-    const float dh = kEntropy ? a.dentropy[r] : 0.f;
+    const float given = target >= 0 && a.dlogprob ? a.dlogprob[r] * a.scale : 0.f;
+    const float dh = kEntropy ? a.dentropy[r] * a.scale : 0.f;
     // p times (c0 + c1 d), d = z - lse
-    const float c0 = (a.dlse ? a.dlse[r] : 0.f) - given - (kEntropy ? dh * a.entropy[r] : 0.f), c1 = -dh;
+    const float c0 = (a.dlse ? a.dlse[r] * a.scale : 0.f) - given - (kEntropy ? dh * a.entropy[r] : 0.f);
     const bool none = lse == -inf();
-    float x[kFly][kN];
-    const int w0 = chunk * (kFly * kGradThreads) + int(threadIdx.x);
+    // -inf may count as a low finite number (see Pack) where its distance from lse is large, and finite
+    const float least = P::least(a.scale * kLog2E) * a.scale;
+    const bool plain = lse > least && fabsf(lse) < P::most(a.scale) && !none;
+    const uint32_t low = P::low();
+    const Two scale(a.scale), shift(-lse), log2e(kLog2E), k0(c0), k1(-dh);
+#pragma unroll 1
+    for (; w < end; w += kFly * kGradThreads) {
+        P x[kFly];
 #pragma unroll
-    for (int i = 0; i < kFly; ++i) win.load(x[i], w0 + i * kGradThreads);
+        for (int i = 0; i < kFly; ++i) x[i] = next[i];
+        if (w + kFly * kGradThreads < end) {
 #pragma unroll
-    for (int i = 0; i < kFly; ++i) {
-        const int w = w0 + i * kGradThreads, i0 = win.first(w);
-        if (w >= win.count) break;
-#pragma unroll
-        for (int j = 0; j < kN; ++j) {
-            float d = fmaf(x[i][j], a.scale, -lse);
-            if constexpr (kEntropy) d = max_nan(d, -200.f);  // (of -inf: 2^-288 is 0, and 0 times it)
-            const float p = ptx::ex2_approx(d * kLog2E);
-            float g = p * (kEntropy ? fmaf(c1, d, c0) : c0);
-            if (i0 + j == target) g += given;
-            x[i][j] = none ? 0.f : g * a.scale;
+            for (int i = 0; i < kFly; ++i) next[i] = win.any(w + (kFly + i) * kGradThreads);
         }
-        if (same && i0 >= 0 && i0 + kN <= a.vocab) {
-            uint32_t u[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (kDt == CF_FP32) u[j] = __float_as_uint(x[i][j]);
-                else u[j] = uint32_t(from_float<kDt>(x[i][2 * j])) | uint32_t(from_float<kDt>(x[i][2 * j + 1])) << 16;
+        for (int i = 0; i < kFly; ++i) {
+            const int v = w + i * kGradThreads, i0 = win.first(v);
+            if (v >= end) break;
+            if (plain) {
+                if constexpr (kEntropy) x[i].raise(low);
+#pragma unroll
+                for (int j = 0; j < kN / 2; ++j) {
+                    const Two d = fma(x[i].pair(j), scale, shift);
+                    const float2 q = (d * log2e).parts();
+                    const Two p(ptx::ex2_approx(q.x), ptx::ex2_approx(q.y));
+                    Two g = p * (kEntropy ? fma(k1, d, k0) : k0);
+                    const int at = i0 + 2 * j;
+                    if (uint32_t(int(target) - at) < 2u) {
+                        const float2 h = g.parts();
+                        g = int(target) == at ? Two(h.x + given, h.y) : Two(h.x, h.y + given);
+                    }
+                    x[i].set_pair(j, g);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kN; ++j) {
+                    float d = fmaf(x[i].get(j), a.scale, -lse);
+                    if constexpr (kEntropy) d = max_nan(d, -200.f);  // (of -inf: 2^-288 is 0, and 0 times it)
+                    float g = ptx::ex2_approx(d * kLog2E) * (kEntropy ? fmaf(-dh, d, c0) : c0);
+                    if (i0 + j == target) g += given;
+                    x[i].set(j, none ? 0.f : g);
+                }
             }
-            *reinterpret_cast<uint4 *>(out + i0) = make_uint4(u[0], u[1], u[2], u[3]);
-        } else {
+            if (same && i0 >= 0 && i0 + kN <= a.vocab) {
+                __stcs(reinterpret_cast<uint4 *>(out + i0), make_uint4(x[i].u[0], x[i].u[1], x[i].u[2], x[i].u[3]));
+            } else {
 #pragma unroll
-            for (int j = 0; j < kN; ++j)
-                if (i0 + j >= 0 && i0 + j < a.vocab) out[i0 + j] = from_float<kDt>(x[i][j]);
+                for (int j = 0; j < kN; ++j)
+                    if (i0 + j >= 0 && i0 + j < a.vocab) out[i0 + j] = from_float<kDt>(x[i].get(j));
+            }
         }
     }
 }
@@ -455,15 +598,27 @@ cudaError_t launch_logprobs(LogprobsArgs a, int sms, bool pdl, cudaStream_t stre
     return launch(fn, unsigned(a.rows * cluster), threads, cluster, pdl, stream, args);
 }
 
-int64_t logprobs_grad_ctas(int64_t rows, int64_t vocab, int dtype) {
+// turns of kFly windows that a thread of the gradient takes: few where there are few CTAs, else up to eight
+static int grad_turns(int64_t rows, int64_t windows) {
+    int turns = 1;
+    while (turns < 8 && rows * ((windows + 2 * turns * kFly * kGradThreads - 1) / (2 * turns * kFly * kGradThreads)) >= 1216)
+        turns *= 2;
+    return turns;
+}
+static int64_t grad_windows(int64_t vocab, int dtype) {
     const int per = 16 / type_bytes(dtype);
-    const int64_t windows = (vocab + 2 * per - 2) / per;
-    return rows * ((windows + kFly * kGradThreads - 1) / (kFly * kGradThreads));
+    return (vocab + 2 * per - 2) / per;  // the most a row can have
+}
+
+int64_t logprobs_grad_ctas(int64_t rows, int64_t vocab, int dtype) {
+    const int64_t windows = grad_windows(vocab, dtype), each = int64_t(grad_turns(rows, windows)) * kFly * kGradThreads;
+    return rows * ((windows + each - 1) / each);
 }
 
 cudaError_t launch_logprobs_grad(LogprobsGradArgs a, bool pdl, cudaStream_t stream) {
     const int64_t ctas = logprobs_grad_ctas(a.rows, a.vocab, a.dtype);
     a.chunks = int(ctas / a.rows);
+    a.turns = grad_turns(a.rows, grad_windows(a.vocab, a.dtype));
     const bool entropy = a.dentropy != nullptr;
     const void *fn = a.dtype == CF_BF16   ? grad_kernel<CF_BF16>(entropy)
                      : a.dtype == CF_FP16 ? grad_kernel<CF_FP16>(entropy)

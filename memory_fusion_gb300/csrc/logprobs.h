@@ -33,7 +33,7 @@ struct LogprobsGradArgs {
     int64_t rows, stride, dstride;
     int vocab, dtype;
     float scale;
-    int chunks;              // CTAs of a row (the launcher's)
+    int chunks, turns;       // CTAs of a row, and turns of a CTA's loop (the launcher's)
 };
 cudaError_t launch_logprobs_grad(LogprobsGradArgs a, bool pdl, cudaStream_t stream);
 // CTAs that a gradient takes
