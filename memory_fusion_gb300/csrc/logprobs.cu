@@ -39,7 +39,7 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2E = 1.4426950408889634f, kLn2F = 0.6931471805599453f;
-constexpr int kMaxThreads = 512, kMaxCluster = 8;
+constexpr int kMaxThreads = 256, kMaxCluster = 8;
 constexpr int kCandidates = 1024;
 constexpr int kFly = 4;  // windows in flight
 constexpr uint32_t kInfoTarget = 0x72000000u;
@@ -223,21 +223,48 @@ __device__ void search_tops(const Share<kDt> &sh, int k, uint64_t *top, uint64_t
 // most: the thread's largest logit with its first window, a pair (0: none)
 template <int kDt>
 __device__ void find_tops(const Share<kDt> &sh, uint64_t most, int k, uint64_t *top, uint64_t *pairs, int *chosen,
-                          uint64_t *bound, int *found) {
+                          uint64_t *bound, int *found, int *many) {
     const int tid = int(threadIdx.x), n = int(blockDim.x);
     pairs[tid] = most;
-    if (tid == 0) {
-        *found = 0;
-        *bound = 0;
-    }
+    if (tid == 0) *found = 0;
     if (tid < k) top[tid] = 0;
     __syncthreads();
-    int rank = 0;
-    for (int i = 0; i < n; ++i) rank += pairs[i] > most;
-    // (threads without a window have no place; where fewer than k have one, everything is a candidate)
-    if (most != 0 && rank < k) chosen[rank] = tid;
-    if (most != 0 && rank == k - 1) *bound = most;
-    const int have = min(k, __syncthreads_count(most != 0));
+    // The k largest in turn, by one warp: the largest order of all, of those that have it the lowest window.  (Every
+    // thread counting the pairs above its own took a sixth of the kernel's instructions.  Threads without a window have
+    // no pair; where fewer than k have one, everything is a candidate.)
+    if (tid < 32) {
+        uint64_t mine[kMaxThreads / 32], best = 0;
+#pragma unroll
+        for (int i = 0; i < kMaxThreads / 32; ++i) {
+            mine[i] = tid + 32 * i < n ? pairs[tid + 32 * i] : 0;
+            best = max(best, mine[i]);
+        }
+        int i = 0;
+        uint64_t last = 0;
+        for (; i < k; ++i) {
+            const uint32_t o = __reduce_max_sync(kAll, uint32_t(best >> 32));
+            if (o == 0) break;
+            const uint32_t at = __reduce_max_sync(kAll, uint32_t(best >> 32) == o ? uint32_t(best) : 0u);
+            last = uint64_t(o) << 32 | at;
+            if (best == last) {
+                best = 0;
+#pragma unroll
+                for (int j = 0; j < kMaxThreads / 32; ++j) {
+                    if (mine[j] == last) {
+                        mine[j] = 0;
+                        chosen[i] = tid + 32 * j;
+                    }
+                    best = max(best, mine[j]);
+                }
+            }
+        }
+        if (tid == 0) {
+            *bound = i == k ? last : 0;
+            *many = i;
+        }
+    }
+    __syncthreads();
+    const int have = *many;
     const uint64_t least = *bound;
     const uint32_t least_order = uint32_t(least >> 32), least_window = uint32_t(~least);
     const int steps = sh.steps() + 1;
@@ -279,7 +306,7 @@ __global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobsArg
     __shared__ uint64_t tops[kTop ? kMaxCluster * kLogprobsMaxTop : 1];  // of the row's CTAs, in the first one
     __shared__ int chosen[kLogprobsMaxTop];
     __shared__ uint64_t bound;
-    __shared__ int found;
+    __shared__ int found, many;
     static_assert(kCandidates >= kMaxThreads, "one pair a thread");
     static_assert(sizeof(Stats) == 16 && offsetof(Stats, m) == 0 && offsetof(Stats, s) == 4 && offsetof(Stats, t) == 8,
                   "sent as a pair and a number");
@@ -306,7 +333,10 @@ __global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobsArg
     }
 
     Stats st{-inf(), 0.f, 0.f};
-    uint32_t most_order = 0, most_window = 0;  // (no order is 0)
+    // the largest logit, in an order of signed numbers (a maximum's NaN is a positive one, so it is above everything; no
+    // logit has the lowest number), and its first window
+    int most_order = int(0x80000000u);
+    uint32_t most_window = 0;
     using P = Pack<kDt>;
     const uint32_t low = P::low();
     const float least = P::least(s2), beyond = P::most(s2);
@@ -318,7 +348,7 @@ __global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobsArg
             if (i >= n) break;
             const float m = x[i].largest();
             if constexpr (kTop) {
-                const uint32_t o = order(m);
+                const int bits = __float_as_int(m + 0.f), o = bits ^ (bits >> 31 & 0x7fffffff);
                 if (o > most_order) {
                     most_order = o;
                     most_window = uint32_t(w + i * step);
@@ -372,18 +402,28 @@ __global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobsArg
     const int whole = (sh.w.full1() - (w0 - tid) - int(blockDim.x) + round) / round;  // steps whose last thread's is whole
     const int turns = max(0, whole) / kFly;
     if (turns > 0) {
-        P next[kFly];
+        // (two sets of registers that take turns: moving one to the other costs half an instruction a number)
+        const uint4 *from = reinterpret_cast<const uint4 *>(sh.w.row + sh.w.first(w));
+        auto fetch = [&](P (&to)[kFly]) {
 #pragma unroll
-        for (int i = 0; i < kFly; ++i) next[i] = sh.w.whole(w + i * round);
-#pragma unroll 1
-        for (; g < turns; ++g, w += kFly * round) {
-#pragma unroll
-            for (int i = 0; i < kFly; ++i) x[i] = next[i];
-            if (g + 1 < turns) {
-#pragma unroll
-                for (int i = 0; i < kFly; ++i) next[i] = sh.w.whole(w + (kFly + i) * round);
+            for (int i = 0; i < kFly; ++i) {
+                const uint4 v = __ldcs(from + i * round);
+                to[i] = P{{v.x, v.y, v.z, v.w}};
             }
+            from += kFly * round;
+        };
+        P y[kFly];
+        fetch(x);
+#pragma unroll 1
+        for (;;) {
+            if (g + 1 < turns) fetch(y);
             take(x, kFly, w, round);
+            w += kFly * round;
+            if (++g >= turns) break;
+            if (g + 1 < turns) fetch(x);
+            take(y, kFly, w, round);
+            w += kFly * round;
+            if (++g >= turns) break;
         }
     }
 #pragma unroll 1
@@ -393,12 +433,15 @@ __global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobsArg
         const int n = min(kFly, (sh.w.count - w + round - 1) / round);
         take(x, n, w, round);
     }
-    const uint64_t most = most_order == 0 ? 0 : pair_of(most_order, most_window);
+    const uint64_t most =
+        most_order == int(0x80000000u)
+            ? 0
+            : pair_of(order(__int_as_float(most_order ^ (most_order >> 31 & 0x7fffffff))), most_window);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1)
         st.add(Stats{__shfl_xor_sync(kAll, st.m, d), __shfl_xor_sync(kAll, st.s, d), __shfl_xor_sync(kAll, st.t, d)}, s2);
     if (lane == 0) warp_stats[warp] = st;
-    if constexpr (kTop) find_tops(sh, most, a.top, tops + part * kLogprobsMaxTop, pairs, chosen, &bound, &found);
+    if constexpr (kTop) find_tops(sh, most, a.top, tops + part * kLogprobsMaxTop, pairs, chosen, &bound, &found, &many);
     __syncthreads();
     if (tid == 0) {
         for (int i = 1; i < int(blockDim.x >> 5); ++i) st.add(warp_stats[i], s2);
