@@ -931,43 +931,52 @@ def cf_gemm_linear_grad(dY, X, W, Z, dZ, dX, dW, dbias, M, N, K, dtype, act, wor
 _LINEAR_ACTS = {"none": CF_ACT_NONE, "gelu_tanh": CF_ACT_GELU_TANH, "silu": CF_ACT_SILU, "relu": CF_ACT_RELU}
 
 
-def _linear_act(act):
-    a = _LINEAR_ACTS.get(act)
-    if a is None:
-        raise ValueError(f"unknown activation {act!r}")
-    return a
+# (The calls below are written for the decode step, whose kernels take less time than the host does for a call: torch and
+# the library's functions are looked up once, and what a call needs on another stream or device it does in a call of its
+# own.)
+_torch = None
+_entries = {}
 
 
-def _outputs(name, args, device, workspace, size, sizes, stream, tuning):
-    """name(*args(), workspace, its bytes, stream) on the operands' device, where args() makes the outputs that are not
-    given and returns the arguments in front of the workspace with the outputs; the outputs."""
+def _the_torch():
+    global _torch
     import torch
-    index = device.index
-    if workspace is not None and not (workspace.get_device() == index and workspace.is_contiguous()):
-        raise ValueError(f"workspace is not a contiguous tensor on {device}")
-    if stream is not None and getattr(stream, "device", device) != device:
+    _torch = torch
+    return torch
+
+
+def _away(device, stream):
+    """Whether the call is for another stream or device than the current ones."""
+    if stream is None:
+        return device.index != _torch._C._cuda_getDevice()
+    if getattr(stream, "device", device) != device:
         raise ValueError(f"stream is on {stream.device}, not on {device}")
-    if stream is not None or index != torch._C._cuda_getDevice():
-        with _launch_on(device, stream):
-            return _outputs(name, args, device, workspace, size, sizes, None, tuning)
-    before, outs = args()
+    return True
+
+
+def _launch(name, args, device, workspace, size, sizes, tuning):
+    """name(*args, workspace, its bytes, the current stream), the workspace (size(*sizes) bytes) made if there is none."""
+    index = device.index
     if workspace is None:
         workspace = new_workspace(size(*sizes), device)
-    last = (workspace.data_ptr(), workspace.nbytes, torch._C._cuda_getCurrentRawStream(index))
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace is not a contiguous tensor on {device}")
     if tuning is None:
-        st = getattr(lib(), name)(*before, *last)
+        f = _entries.get(name)
+        if f is None:
+            f = _entries[name] = getattr(lib(), name)
+        st = f(*args, workspace.data_ptr(), workspace.nbytes, _torch._C._cuda_getCurrentRawStream(index))
     else:
-        st = getattr(lib(), name + "_ex")(*before, *last, ctypes.byref(tuning))
+        st = getattr(lib(), name + "_ex")(*args, workspace.data_ptr(), workspace.nbytes,
+                                          _torch._C._cuda_getCurrentRawStream(index), ctypes.byref(tuning))
     if st != CF_OK:
         raise CfError(st, name)
-    return outs
 
 
 def _made(name, t, shape, dtype, device):
     """An output: the given one, checked, or a new one."""
     if t is None:
-        import torch
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty(shape, dtype=dtype, device=device)
     _operand(name, t, shape, dtype, device)
     return t
 
@@ -977,15 +986,23 @@ def gemm_linear(X, W, bias=None, *, act="none", residual=None, preact=None, out=
     """Y = act(X @ W + bias) + residual; X [M, K], W [K, N] and residual [M, N] bf16 or fp16 CUDA tensors, bias fp32
     [N]; act "none", "gelu_tanh", "silu" or "relu".  `preact` ([M, N]) receives X @ W + bias for gemm_linear_grad.
     out may be residual."""
-    import torch
+    f32 = (_torch or _the_torch()).float32
     (M, K), dev, dtype, dt = _first("X", X, 2)
-    a = _linear_act(act)
+    if _away(dev, stream):
+        with _launch_on(dev, stream):
+            return gemm_linear(X, W, bias, act=act, residual=residual, preact=preact, out=out, workspace=workspace,
+                               tuning=tuning)
+    a = _LINEAR_ACTS.get(act)
+    if a is None:
+        raise ValueError(f"unknown activation {act!r}")
     N = _sizes("W", W, 2)[1]
-    before = (X.data_ptr(), _operand("W", W, (K, N), dtype, dev), _operand("bias", bias, (N,), torch.float32, dev),
-              _operand("residual", residual, (M, N), dtype, dev))
-    between = (_operand("preact", preact, (M, N), dtype, dev), M, N, K, dt, a)
-    return _run("cf_gemm_linear", before, between, out, (M, N), dtype, dev, workspace, cf_gemm_linear_workspace_size,
-                (M, N, K), stream, tuning)
+    like = (M, N)
+    w, b = _operand("W", W, (K, N), dtype, dev), _operand("bias", bias, (N,), f32, dev)
+    r, z = _operand("residual", residual, like, dtype, dev), _operand("preact", preact, like, dtype, dev)
+    y = _made("out", out, like, dtype, dev)
+    _launch("cf_gemm_linear", (X.data_ptr(), w, b, r, y.data_ptr(), z, M, N, K, dt, a), dev, workspace,
+            cf_gemm_linear_workspace_size, (M, N, K), tuning)
+    return y
 
 
 def gemm_linear_grad(dY, X, W, *, act="none", preact=None, input=True, weight=True, bias=True, dz=None, out=None,
@@ -994,9 +1011,15 @@ def gemm_linear_grad(dY, X, W, *, act="none", preact=None, input=True, weight=Tr
     input, weight and bias say which are wanted (None in the place of the others; X may be None without weight, W
     without input).  `preact` is what gemm_linear kept, needed with an activation; `dz` ([M, N], made where not given)
     then receives dY * act'(preact), and may be preact or dY.  dbias is fp32.  `out`: three outputs, None for new ones."""
-    import torch
+    f32 = (_torch or _the_torch()).float32
     (M, N), dev, dtype, dt = _first("dY", dY, 2)
-    a = _linear_act(act)
+    if _away(dev, stream):
+        with _launch_on(dev, stream):
+            return gemm_linear_grad(dY, X, W, act=act, preact=preact, input=input, weight=weight, bias=bias, dz=dz,
+                                    out=out, workspace=workspace, tuning=tuning)
+    a = _LINEAR_ACTS.get(act)
+    if a is None:
+        raise ValueError(f"unknown activation {act!r}")
     if X is None and W is None:
         raise ValueError("neither X nor W is given")
     K = _sizes("X", X, 2)[1] if X is not None else _sizes("W", W, 2)[0]
@@ -1004,19 +1027,16 @@ def gemm_linear_grad(dY, X, W, *, act="none", preact=None, input=True, weight=Tr
         raise ValueError("the weight's gradient needs X, the input's needs W")
     if (a != CF_ACT_NONE) != (preact is not None) or (a == CF_ACT_NONE and dz is not None):
         raise ValueError("preact goes with an activation, and so does dz")
-    given = (None, None, None) if out is None else out
     x, w = _operand("X", X, (M, K), dtype, dev), _operand("W", W, (K, N), dtype, dev)
     z = _operand("preact", preact, (M, N), dtype, dev)
-
-    def args():
-        dx = _made("out[0]", given[0], (M, K), dtype, dev) if input else None
-        dw = _made("out[1]", given[1], (K, N), dtype, dev) if weight else None
-        db = _made("out[2]", given[2], (N,), torch.float32, dev) if bias else None
-        d = _made("dz", dz, (M, N), dtype, dev) if a != CF_ACT_NONE else None
-        return (dY.data_ptr(), x, w, z, _ptr(d), _ptr(dx), _ptr(dw), _ptr(db), M, N, K, dt, a), (dx, dw, db)
-
-    return _outputs("cf_gemm_linear_grad", args, dev, workspace, cf_gemm_linear_workspace_size, (M, N, K), stream,
-                    tuning)
+    given = (None, None, None) if out is None else out
+    dx = _made("out[0]", given[0], (M, K), dtype, dev) if input else None
+    dw = _made("out[1]", given[1], (K, N), dtype, dev) if weight else None
+    db = _made("out[2]", given[2], (N,), f32, dev) if bias else None
+    d = _made("dz", dz, (M, N), dtype, dev) if a != CF_ACT_NONE else None
+    _launch("cf_gemm_linear_grad", (dY.data_ptr(), x, w, z, _ptr(d), _ptr(dx), _ptr(dw), _ptr(db), M, N, K, dt, a), dev,
+            workspace, cf_gemm_linear_workspace_size, (M, N, K), tuning)
+    return dx, dw, db
 
 
 # ---------------------------------------------------------------------------
@@ -1055,44 +1075,34 @@ _ROW_DTYPES = {}  # the 16-bit types and torch.float32, once torch is there
 
 def _row_dtype(name, t):
     """The library's name of a row operand's dtype."""
+    dt = _ROW_DTYPES.get(t.dtype)
+    if dt is not None and t.is_cuda:
+        return dt
     if not _ROW_DTYPES:
-        import torch
+        torch = _torch or _the_torch()
         _ROW_DTYPES.update({torch.bfloat16: CF_BF16, torch.float16: CF_FP16, torch.float32: CF_FP32})
+        return _row_dtype(name, t)
     if not t.is_cuda:
         raise ValueError(f"{name} is on {t.device}, not on a CUDA device")
-    dt = _ROW_DTYPES.get(t.dtype)
-    if dt is None:
-        raise ValueError(f"{name} has dtype {t.dtype}, not bfloat16, float16 or float32")
-    return dt
+    raise ValueError(f"{name} has dtype {t.dtype}, not bfloat16, float16 or float32")
 
 
-def _norm(name, kind, *vectors):
+def _norm(name, kind, weight, bias):
     n = _NORMS.get(kind)
     if n is None:
         raise ValueError(f"{name}: unknown norm {kind!r}")
-    if n == CF_NORM_NONE and any(v is not None for v in vectors):
+    if n == CF_NORM_NONE and not (weight is None and bias is None):
         raise ValueError(f"{name} is no norm, but has a weight or a bias")
     return n
 
 
-def _block_norms_operands(h, gate, post, post_weight, post_bias, pre, pre_weight, pre_bias):
-    """What both directions check: sizes, device, dtype, the library's dtype and norms, addresses."""
-    import torch
-    dt = _row_dtype("h", h)
-    rows, cols = _sizes("h", h, 2)
-    dev, dtype, f32 = h.device, h.dtype, torch.float32
-    kinds = _norm("post", post, post_weight, post_bias), _norm("pre", pre, pre_weight, pre_bias)
-    gates = 0
-    if gate is not None:
-        gates = _sizes("gate", gate, 2)[0]
-        if gates == 0 and rows > 0 or gates > 0 and rows % gates:
-            raise ValueError(f"{gates} gates do not divide {rows} rows")
-    addresses = (_operand("h", h, (rows, cols), dtype, dev), _operand("gate", gate, (gates, cols), dtype, dev),
-                 _operand("post_weight", post_weight, (cols,), f32, dev),
-                 _operand("post_bias", post_bias, (cols,), f32, dev),
-                 _operand("pre_weight", pre_weight, (cols,), f32, dev),
-                 _operand("pre_bias", pre_bias, (cols,), f32, dev))
-    return rows, cols, gates, dev, dtype, dt, kinds, addresses
+def _gates(gate, rows):
+    if gate is None:
+        return 0
+    gates = _sizes("gate", gate, 2)[0]
+    if gates == 0 and rows > 0 or gates > 0 and rows % gates:
+        raise ValueError(f"{gates} gates do not divide {rows} rows")
+    return gates
 
 
 def stitch_block_norms(h, x=None, *, post="none", post_weight=None, post_bias=None, gate=None, scale=1.0, alpha=1.0,
@@ -1102,20 +1112,33 @@ def stitch_block_norms(h, x=None, *, post="none", post_weight=None, post_bias=No
     CUDA tensors (x may be None: 0), gate [G, N] of that type, G a divisor of T (row r takes gate r // (T // G)), or
     None; Post and Pre "rms", "layer" or "none", weights and biases fp32 [N] or None.  `out` and `norm_out` take x'
     and y; each may be h or x."""
-    rows, cols, gates, dev, dtype, dt, (po, pr), (ph, pg, pw, pb, qw, qb) = _block_norms_operands(
-        h, gate, post, post_weight, post_bias, pre, pre_weight, pre_bias)
-    px = _operand("x", x, (rows, cols), dtype, dev)
-    if pr == CF_NORM_NONE and norm_out is not None:
+    torch = _torch or _the_torch()
+    dt, dev, dtype, f32 = _row_dtype("h", h), h.device, h.dtype, torch.float32
+    if _away(dev, stream):
+        with _launch_on(dev, stream):
+            return stitch_block_norms(h, x, post=post, post_weight=post_weight, post_bias=post_bias, gate=gate,
+                                      scale=scale, alpha=alpha, pre=pre, pre_weight=pre_weight, pre_bias=pre_bias,
+                                      eps=eps, out=out, norm_out=norm_out, workspace=workspace, tuning=tuning)
+    like = h.shape
+    rows, cols = _sizes("h", h, 2)
+    po, pr = _norm("post", post, post_weight, post_bias), _norm("pre", pre, pre_weight, pre_bias)
+    gates, vector = _gates(gate, rows), (cols,)
+    ph, px = _operand("h", h, like, dtype, dev), _operand("x", x, like, dtype, dev)
+    pg = None if gate is None else _operand("gate", gate, (gates, cols), dtype, dev)
+    pw = None if post_weight is None else _operand("post_weight", post_weight, vector, f32, dev)
+    pb = None if post_bias is None else _operand("post_bias", post_bias, vector, f32, dev)
+    qw = None if pre_weight is None else _operand("pre_weight", pre_weight, vector, f32, dev)
+    qb = None if pre_bias is None else _operand("pre_bias", pre_bias, vector, f32, dev)
+    y = None
+    if pr != CF_NORM_NONE:
+        y = torch.empty_like(h) if norm_out is None else _made("norm_out", norm_out, like, dtype, dev)
+    elif norm_out is not None:
         raise ValueError("norm_out is given, but there is no norm before the next block")
-
-    def args():
-        xo = _made("out", out, (rows, cols), dtype, dev)
-        y = None if pr == CF_NORM_NONE else _made("norm_out", norm_out, (rows, cols), dtype, dev)
-        return (ph, px, pg, pw, pb, qw, qb, xo.data_ptr(), _ptr(y), rows, cols, gates, po, pr, scale, alpha, eps,
-                dt), (xo, y)
-
-    return _outputs("cf_stitch_block_norms", args, dev, workspace, cf_stitch_workspace_size, (rows, cols), stream,
-                    tuning)
+    xo = torch.empty_like(h) if out is None else _made("out", out, like, dtype, dev)
+    _launch("cf_stitch_block_norms", (ph, px, pg, pw, pb, qw, qb, xo.data_ptr(), None if y is None else y.data_ptr(), rows,
+                                      cols, gates, po, pr, scale, alpha, eps, dt), dev, workspace,
+            cf_stitch_workspace_size, (rows, cols), tuning)
+    return xo, y
 
 
 def stitch_block_norms_grad(dy, dx_out, h, x_out, *, post="none", post_weight=None, post_bias=None, gate=None,
@@ -1125,25 +1148,44 @@ def stitch_block_norms_grad(dy, dx_out, h, x_out, *, post="none", post_weight=No
     and dx_out of x' ([T, N]; one may be None: 0): those of what is given there, fp32 for weights and biases, None in
     the place of the others and, with dx=False, of dx.  h and x_out ([T, N]) are the forward pass's input and output.
     `out`: seven outputs, None for new ones; dh and dx may be dy, dx_out, h or x_out."""
-    import torch
-    rows, cols, gates, dev, dtype, dt, (po, pr), (ph, pg, pw, pb, qw, _) = _block_norms_operands(
-        h, gate, post, post_weight, post_bias, pre, pre_weight, pre_bias)
+    torch = _torch or _the_torch()
+    dt, dev, dtype, f32 = _row_dtype("h", h), h.device, h.dtype, torch.float32
+    if _away(dev, stream):
+        with _launch_on(dev, stream):
+            return stitch_block_norms_grad(dy, dx_out, h, x_out, post=post, post_weight=post_weight, post_bias=post_bias,
+                                           gate=gate, scale=scale, alpha=alpha, pre=pre, pre_weight=pre_weight,
+                                           pre_bias=pre_bias, eps=eps, dx=dx, out=out, workspace=workspace,
+                                           tuning=tuning)
+    like = h.shape
+    rows, cols = _sizes("h", h, 2)
+    po, pr = _norm("post", post, post_weight, post_bias), _norm("pre", pre, pre_weight, pre_bias)
     if (dy is None) == (pr != CF_NORM_NONE):
         raise ValueError("dy goes with a norm before the next block")
+    gates, vector = _gates(gate, rows), (cols,)
+    ph, pxo = _operand("h", h, like, dtype, dev), _operand("x_out", x_out, like, dtype, dev)
+    pdy, pdx = _operand("dy", dy, like, dtype, dev), _operand("dx_out", dx_out, like, dtype, dev)
+    pg = None if gate is None else _operand("gate", gate, (gates, cols), dtype, dev)
     given = (None,) * 7 if out is None else out
-    ptrs = [_operand(n, t, (rows, cols), dtype, dev) for n, t in (("dy", dy), ("dx_out", dx_out), ("x_out", x_out))]
 
-    def args():
-        like, wants = (rows, cols), (True, dx, gate is not None, post_weight is not None, post_bias is not None,
-                                     pre_weight is not None, pre_bias is not None)
-        shapes = (like, like, (gates, cols)) + ((cols,),) * 4
-        outs = tuple(_made(f"out[{i}]", given[i], shapes[i], dtype if i < 3 else torch.float32, dev) if w else None
-                     for i, w in enumerate(wants))
-        return (ptrs[0], ptrs[1], ph, ptrs[2], pg, pw, pb, qw, *map(_ptr, outs), rows, cols, gates, po, pr, scale,
-                alpha, eps, dt), outs
+    def result(i, wanted, shape=vector, kind=f32):
+        return _made(f"out[{i}]", given[i], shape, kind, dev) if wanted else None
 
-    return _outputs("cf_stitch_block_norms_grad", args, dev, workspace, cf_stitch_block_norms_grad_workspace_size,
-                    (rows, cols), stream, tuning)
+    dh = torch.empty_like(h) if given[0] is None else _made("out[0]", given[0], like, dtype, dev)
+    outs = [dh, result(1, dx, like, dtype), result(2, gate is not None, (gates, cols), dtype)]
+    vectors = []
+    for i, (name, v) in enumerate((("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
+                                   ("pre_bias", pre_bias))):
+        if v is None:
+            vectors.append(None)
+            outs.append(None)
+        else:
+            vectors.append(_operand(name, v, vector, f32, dev))
+            outs.append(result(3 + i, True))
+    _launch("cf_stitch_block_norms_grad", (pdy, pdx, ph, pxo, pg, vectors[0], vectors[1], vectors[2],
+                                           *[None if t is None else t.data_ptr() for t in outs], rows, cols, gates, po, pr,
+                                           scale, alpha, eps, dt), dev, workspace,
+            cf_stitch_block_norms_grad_workspace_size, (rows, cols), tuning)
+    return tuple(outs)
 
 
 # ---------------------------------------------------------------------------
@@ -1186,27 +1228,30 @@ def stitch_logprobs(logits, targets=None, *, scale=1.0, top=0, entropy=True, out
     that may lie apart (logits[:, :V] of a padded vocabulary): the log probability of each row's target (int64 [T], -1:
     none, 0), log-sum-exp and entropy, all fp32 [T], and the `top` (0..32) largest logits' log probabilities and ids
     [T, top], equal logits by id.  None in the place of what is not asked for.  `out`: five outputs, None for new ones."""
-    import torch
-    dt = _row_dtype("logits", logits)
+    torch = _torch or _the_torch()
+    dt, dev, f32, i64 = _row_dtype("logits", logits), logits.device, torch.float32, torch.int64
+    if _away(dev, stream):
+        with _launch_on(dev, stream):
+            return stitch_logprobs(logits, targets, scale=scale, top=top, entropy=entropy, out=out, workspace=workspace,
+                                   tuning=tuning)
     rows, vocab, apart = _rows_apart("logits", logits)
-    dev, f32, i64 = logits.device, torch.float32, torch.int64
     if not 0 <= top <= min(vocab, 32):
         raise ValueError(f"top is {top}, not in 0..{min(vocab, 32)}")
     if not scale > 0:
         raise ValueError(f"scale is {scale}, not above 0")
     if vocab == 0 and rows > 0:
         raise ValueError("logits have no columns")
-    given = (None,) * 5 if out is None else out
     t = _operand("targets", targets, (rows,), i64, dev)
-
-    def args():
-        want = (targets is not None, True, entropy, top > 0, top > 0)
-        shapes = ((rows,),) * 3 + ((rows, top),) * 2
-        outs = tuple(_made(f"out[{i}]", given[i], shapes[i], f32 if i < 4 else i64, dev) if w else None
-                     for i, w in enumerate(want))
-        return (logits.data_ptr(), t, *map(_ptr, outs), rows, vocab, apart, top, scale, dt), outs
-
-    return _outputs("cf_stitch_logprobs", args, dev, workspace, cf_stitch_workspace_size, (rows, vocab), stream, tuning)
+    given = (None,) * 5 if out is None else out
+    lse = _made("out[1]", given[1], (rows,), f32, dev)
+    logprob = None if t is None and targets is None else _made("out[0]", given[0], (rows,), f32, dev)
+    h = _made("out[2]", given[2], (rows,), f32, dev) if entropy else None
+    tl = _made("out[3]", given[3], (rows, top), f32, dev) if top else None
+    ti = _made("out[4]", given[4], (rows, top), i64, dev) if top else None
+    _launch("cf_stitch_logprobs", (logits.data_ptr(), t, _ptr(logprob), lse.data_ptr(), _ptr(h), _ptr(tl), _ptr(ti), rows,
+                                   vocab, apart, top, scale, dt), dev, workspace, cf_stitch_workspace_size, (rows, vocab),
+            tuning)
+    return logprob, lse, h, tl, ti
 
 
 def stitch_logprobs_grad(logits, targets, lse, dlogprob=None, *, dlse=None, entropy=None, dentropy=None, scale=1.0,
@@ -1214,10 +1259,13 @@ def stitch_logprobs_grad(logits, targets, lse, dlogprob=None, *, dlse=None, entr
     """The gradient of the logits [T, V] (in their dtype) for the gradients dlogprob, dlse and dentropy (fp32 [T], None:
     0) of stitch_logprobs' results; lse and, with dentropy, entropy are its results.  `out` may be logits, or rows
     apart like theirs."""
-    import torch
-    dt = _row_dtype("logits", logits)
+    torch = _torch or _the_torch()
+    dt, dev, dtype, f32 = _row_dtype("logits", logits), logits.device, logits.dtype, torch.float32
+    if _away(dev, stream):
+        with _launch_on(dev, stream):
+            return stitch_logprobs_grad(logits, targets, lse, dlogprob, dlse=dlse, entropy=entropy, dentropy=dentropy,
+                                        scale=scale, out=out, workspace=workspace, tuning=tuning)
     rows, vocab, apart = _rows_apart("logits", logits)
-    dev, dtype, f32 = logits.device, logits.dtype, torch.float32
     if not scale > 0:
         raise ValueError(f"scale is {scale}, not above 0")
     if (targets is None) != (dlogprob is None):
@@ -1226,16 +1274,14 @@ def stitch_logprobs_grad(logits, targets, lse, dlogprob=None, *, dlse=None, entr
         raise ValueError("dentropy goes with entropy")
     if dlogprob is None and dlse is None and dentropy is None:
         raise ValueError("no gradient is given")
-    before = (logits.data_ptr(), _operand("targets", targets, (rows,), torch.int64, dev),
-              *(_operand(n, t, (rows,), f32, dev) for n, t in (("lse", lse), ("entropy", entropy),
-                                                               ("dlogprob", dlogprob), ("dlse", dlse),
-                                                               ("dentropy", dentropy))))
-    if out is not None:
-        _rows_apart("out", out, (rows, vocab), dtype, dev)
-
-    def args():
-        d = torch.empty((rows, vocab), dtype=dtype, device=dev) if out is None else out
-        return (*before, d.data_ptr(), rows, vocab, apart, d.stride(0) if rows > 1 else vocab, scale, dt), d
-
-    return _outputs("cf_stitch_logprobs_grad", args, dev, workspace, cf_stitch_workspace_size, (rows, vocab), stream,
-                    tuning)
+    row = (rows,)
+    args = (logits.data_ptr(), _operand("targets", targets, row, torch.int64, dev), _operand("lse", lse, row, f32, dev),
+            _operand("entropy", entropy, row, f32, dev), _operand("dlogprob", dlogprob, row, f32, dev),
+            _operand("dlse", dlse, row, f32, dev), _operand("dentropy", dentropy, row, f32, dev))
+    if out is None:
+        out, between = torch.empty((rows, vocab), dtype=dtype, device=dev), vocab
+    else:
+        between = _rows_apart("out", out, (rows, vocab), dtype, dev)[2]
+    _launch("cf_stitch_logprobs_grad", (*args, out.data_ptr(), rows, vocab, apart, between, scale, dt), dev, workspace,
+            cf_stitch_workspace_size, (rows, vocab), tuning)
+    return out

@@ -994,10 +994,11 @@ cudaError_t launch(const void *fn, dim3 grid, int threads, int cluster, bool pdl
 // Once per device and kernel, to the most a launch may ask for: launches from several threads set the same value, and
 // none is set under a capture later.
 constexpr int kMostSmem = 232448;  // of a CTA (227 KB)
-cudaError_t allow_smem(const void *fn) {
+cudaError_t allow_smem(const void *fn, int *own) {  // own: the kernel's static shared memory
     struct Entry {
         std::atomic<const void *> fn;
         std::atomic<uint64_t> devices;
+        std::atomic<int> own;
     };
     static Entry table[64];  // (48 kernels)
     int dev = 0;
@@ -1008,14 +1009,18 @@ cudaError_t allow_smem(const void *fn) {
         const void *at = t.fn.load(std::memory_order_acquire);
         if (at == nullptr && t.fn.compare_exchange_strong(at, fn, std::memory_order_acq_rel)) at = fn;
         if (at != fn) continue;
-        if (t.devices.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
-        cudaFuncAttributes attr;
-        e = cudaFuncGetAttributes(&attr, fn);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kMostSmem - int(attr.sharedSizeBytes));
-        if (e == cudaSuccess) t.devices.fetch_or(uint64_t(1) << dev, std::memory_order_acq_rel);
-        return e;
+        if (!(t.devices.load(std::memory_order_acquire) >> dev & 1)) {
+            cudaFuncAttributes attr;
+            e = cudaFuncGetAttributes(&attr, fn);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kMostSmem - int(attr.sharedSizeBytes));
+            if (e != cudaSuccess) return e;
+            t.own.store(int(attr.sharedSizeBytes), std::memory_order_release);
+            t.devices.fetch_or(uint64_t(1) << dev, std::memory_order_acq_rel);
+        }
+        *own = t.own.load(std::memory_order_acquire);
+        return cudaSuccess;
     }
     return cudaErrorInvalidValue;
 }
@@ -1081,10 +1086,12 @@ cudaError_t launch_block_norms(BlockNormsArgs a, bool vec, int sms, bool pdl, cu
     const void *fn = a.dtype == CF_BF16   ? forward_kernel<CF_BF16>(mode, full, per)
                      : a.dtype == CF_FP16 ? forward_kernel<CF_FP16>(mode, full, per)
                                           : forward_kernel<CF_FP32>(mode, full, per);
-    const int smem = plan_ring(&a.ring, a.dtype, mode, a.gates_along ? 3 : 2, per, threads, per_sm, 1024);
+    int own;
+    const cudaError_t e = allow_smem(fn, &own);
+    if (e != cudaSuccess) return e;
+    const int smem = plan_ring(&a.ring, a.dtype, mode, a.gates_along ? 3 : 2, per, threads, per_sm, own);
     void *args[] = {&a};
-    const cudaError_t e = allow_smem(fn);
-    return e != cudaSuccess ? e : launch(fn, dim3(unsigned(ctas)), threads, 1, pdl, stream, args, smem);
+    return launch(fn, dim3(unsigned(ctas)), threads, 1, pdl, stream, args, smem);
 }
 
 BlockNormsGradPlan plan_block_norms_grad(int64_t rows, int64_t cols, int sms, bool lean, int dtype) {
@@ -1119,8 +1126,8 @@ cudaError_t launch_block_norms_grad(BlockNormsGradArgs a, const BlockNormsGradPl
                      : a.dtype == CF_FP16 ? grad_kernel<CF_FP16>(mode, cluster, gate, full, p.pieces)
                                           : grad_kernel<CF_FP32>(mode, cluster, gate, full, p.pieces);
     void *args[] = {&a};
-    cudaFuncAttributes attr;
-    cudaError_t e = cudaFuncGetAttributes(&attr, fn);
+    int own;
+    cudaError_t e = allow_smem(fn, &own);
     if (e != cudaSuccess) return e;
     const int rows = a.gate && a.rows_per_gate == 1 ? 5 : 4;
     // (as grad_kernel chooses: what is rare has its gates' sums anyway)
@@ -1128,10 +1135,8 @@ cudaError_t launch_block_norms_grad(BlockNormsGradArgs a, const BlockNormsGradPl
                                     p.pieces, p.threads);
     // (the ring's place takes the sums of several groups in the end)
     const int smem = totals + std::max(plan_ring(&a.ring, a.dtype, mode, rows, p.pieces, p.threads,
-                                                 std::max(1, 512 / p.threads), int(attr.sharedSizeBytes) + totals),
+                                                 std::max(1, 512 / p.threads), own + totals),
                                        p.threads == p.lanes ? 0 : p.threads * p.pieces * 8 * 4);
-    e = allow_smem(fn);
-    if (e != cudaSuccess) return e;
     e = launch(fn, dim3(unsigned(p.sets * p.cluster)), p.threads, p.cluster, pdl, stream, args, smem);
     if (e != cudaSuccess) return e;
     int nsums = 0;
