@@ -1869,6 +1869,48 @@ cf_status linear_device(cf::DeviceInfo *dev) {
     return dev->cc_major == 10 && dev->cc_minor == 3 ? CF_OK : CF_ERR_NO_DEVICE;
 }
 
+// One group, whose rows the host knows: CTA pairs with tiles of as many rows as fill their last round best.  (8192 rows of
+// 2048 x 8192, the input's gradient: 201 us with single CTAs and divided tiles, 173 with pairs and tiles of 256 rows, four
+// rounds of which the last is 37 % full.)  Single CTAs stay where the model of cycles sees them a fifth ahead: few tiles.
+void plan_linear_tiles(int kind, int64_t M, int64_t F, int64_t C, cf_tuning *t, int *tile_rows) {
+    *tile_rows = 0;
+    if (t->n_slice != 0 || t->cluster_m != 0) return;
+    const GroupedShape shape{kind, M, F, C, 0, 1, 0};
+    bool pair;
+    const int bn = grouped_columns(shape, &pair);
+    if (!pair) {
+        if (!grouped_may_pair(kind, 256, F) ||
+            grouped_cycles(shape, 256, true) > 1.2 * grouped_cycles(shape, bn, false))
+            return;
+    }
+    const int step = cf::grouped_column_step(kind, true);
+    const int64_t ft = (F + 255) / 256, pairs = int64_t(kPlanSms) / 2;
+    int best = 256;
+    double least = 1e300;
+    for (int rows = 256; rows >= 128; rows -= step) {
+        const int64_t rounds = (ft * ((M + rows - 1) / rows) + pairs - 1) / pairs;
+        const double block =
+            std::max(std::max(cf::kMmaCycles20Columns / 20.0 * rows, double(cf::kMmaCyclesLeastPair)),
+                     copy_cycles(shape, 256, true));
+        const double cycles = double(rounds) * (double((C + 63) / 64) * block + 400);
+        if (cycles < 0.98 * least) {
+            least = cycles;
+            best = rows;
+        }
+    }
+    t->n_slice = 256;
+    t->cluster_m = 2;
+    *tile_rows = best;
+}
+
+// the pairs that a plan with tiles of tile_rows rows keeps busy
+int linear_pairs(int64_t M, int64_t F, int tile_rows, const cf_tuning &t, const cf::DeviceInfo &dev) {
+    const int64_t tiles = (F + 255) / 256 * ((M + tile_rows - 1) / tile_rows);
+    int64_t c = std::min<int64_t>(tiles, std::min(dev.sm_count, cf::kGroupedWorkers) / 2);
+    if (t.max_clusters > 0) c = std::min<int64_t>(c, t.max_clusters);
+    return int(std::max<int64_t>(c, 1)) * 2;
+}
+
 bool linear_act(int act) { return act >= CF_ACT_NONE && act <= CF_ACT_RELU; }
 
 }  // namespace
@@ -1903,11 +1945,15 @@ extern "C" cf_status cf_gemm_linear_ex(const void *X, const void *W, const float
     if (st != CF_OK) return st;
     cf::GroupedArgs a;
     grouped_args(&a, M, N, K, 0, 1, int(dtype), nullptr, workspace, t);
-    int ctas, smem;
-    st = plan_grouped(cf::GR_LINEAR, M, N, K, 0, 1, 0, t, dev, workspace, 0,
+    int ctas, smem, tile_rows;
+    cf_tuning tl = t;
+    plan_linear_tiles(cf::GR_LINEAR, M, N, K, &tl, &tile_rows);
+    st = plan_grouped(cf::GR_LINEAR, M, N, K, 0, 1, 0, tl, dev, workspace, 0,
                       static_cast<unsigned char *>(workspace) + kGroupedHead, workspace_bytes - kGroupedHead, &a, &ctas,
                       &smem);
     if (st != CF_OK) return st;
+    a.tile_rows = tile_rows;
+    if (tile_rows) ctas = linear_pairs(M, N, tile_rows, t, dev);
     if (!make_tmap_features(&a.tmap_a, &a.a_split, W, 1, uint64_t(K), uint64_t(N), a.a_blocks) ||
         !make_tmap_rows(&a, X, M, K))
         return CF_ERR_CUDA;
@@ -1966,8 +2012,13 @@ extern "C" cf_status cf_gemm_linear_grad_ex(const void *dY, const void *X, const
     const void *g = acted ? dZ : dY;
     if (dX) {
         grouped_args(&gx, M, K, N, 0, 1, int(dtype), nullptr, workspace, t);
-        st = plan_grouped(cf::GR_DGRAD, M, K, N, 0, 1, 0, t, dev, workspace, 0, part, room, &gx, &gx_ctas, &gx_smem);
+        int tile_rows;
+        cf_tuning tl = t;
+        plan_linear_tiles(cf::GR_DGRAD, M, K, N, &tl, &tile_rows);
+        st = plan_grouped(cf::GR_DGRAD, M, K, N, 0, 1, 0, tl, dev, workspace, 0, part, room, &gx, &gx_ctas, &gx_smem);
         if (st != CF_OK) return st;
+        gx.tile_rows = tile_rows;
+        if (tile_rows) gx_ctas = linear_pairs(M, K, tile_rows, t, dev);
         if (!make_tmap_features_t(&gx.tmap_a, W, 1, uint64_t(K), uint64_t(N)) || !make_tmap_rows(&gx, g, M, N))
             return CF_ERR_CUDA;
         gx.out = dX;

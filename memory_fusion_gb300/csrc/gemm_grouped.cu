@@ -248,6 +248,15 @@ __device__ __forceinline__ int feature_tiles(const GroupedArgs &a) {
     return kPair ? (a.F + 2 * kFB - 1) / (2 * kFB) : (a.F + kFB - 1) / kFB;
 }
 
+// Kinds that may have no offsets: the host knows the rows of their one group, and how many of them a tile should take.
+__host__ __device__ constexpr bool one_group(int kind) { return kind == GR_LINEAR || kind == GR_DGRAD; }
+// row tiles of a group
+template <int KIND>
+__device__ __forceinline__ int row_tiles(const GroupedArgs &a, int rows, int shift) {
+    if (one_group(KIND) && a.tile_rows) return (rows - 1) / a.tile_rows + (rows > 0 ? 1 : 0);
+    return (rows + a.bn - 1) >> shift;
+}
+
 // one piece of work: a tile, or the part of its contraction that falls to this CTA
 struct Tile {
     int id;     // tile number
@@ -410,13 +419,13 @@ struct Walk {
             r.nk = (rows + kBK - 1) / kBK;
             blocks = max(r.nk, 1);
         } else {
-            const int rt = (rows + a.bn - 1) >> shift;  // row tiles of the group, cut evenly
+            const int rt = row_tiles<KIND>(a, rows, shift);  // of the group, cut evenly
             if (rt == 1) {
                 r.f0 = local * kTileF + half;
                 r.col0 = lo;
                 r.n = rows;
             } else {
-                const int per = grouped_rows_per_tile(rows, rt, kGran);
+                const int per = one_group(KIND) && a.tile_rows ? a.tile_rows : grouped_rows_per_tile(rows, rt, kGran);
                 const int chunk = local / (kRasterRows * ft);
                 const int wide = min(kRasterRows, rt - chunk * kRasterRows);
                 const int in = local - chunk * kRasterRows * ft;
@@ -688,7 +697,7 @@ __device__ void scan_table(const Table &tab, const GroupedArgs &a, int workers, 
             count = in ? max((rows + kBK - 1) / kBK, 1) : 0;
             longest = max(longest, count);
         } else {
-            count = ft * ((rows + a.bn - 1) >> shift);
+            count = ft * row_tiles<KIND>(a, rows, shift);
         }
         if constexpr (KIND == GR_SHRINK || KIND == GR_LORA) {
             int w = tab.ad[at];

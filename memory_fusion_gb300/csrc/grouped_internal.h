@@ -88,6 +88,7 @@ struct GroupedArgs {
     int fp16;                // 16-bit type of every operand: 0 bf16, 1 fp16
     int act;                 // FORWARD, LINEAR: the cf_activation
     int bn;                  // columns of one accumulator tile (16, 32, 64, 128 or 256)
+    int tile_rows;           // LINEAR, DGRAD without offsets: rows of a tile, in whole column steps; 0: as many as fit
     int stages;
     int copy_cycles;         // what a block's copies take
     int wait_cycles;         // LORA: what H takes, about

@@ -6,8 +6,6 @@
 // of them, a 16-byte piece) and a chunk of the rows, a warp every eighth row and four of them in flight; the warps' sums
 // meet in shared memory, the chunks' in the workspace, where the last CTA of a strip to arrive adds them in order, so
 // that equal calls give equal bits.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -15,6 +13,7 @@
 
 #include "activations.cuh"
 #include "grouped_internal.h"
+#include "pieces.cuh"
 #include "ptx.cuh"
 
 namespace cf {
@@ -22,36 +21,22 @@ namespace {
 
 constexpr int kWarps = 8, kFly = 4;
 
+// numbers of 16 bits kept within +-end (a word of two); NaNs stay
 template <bool kFp16>
-__device__ __forceinline__ void unpack8(float (&x)[8], uint4 v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (kFp16) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            x[2 * i] = f.x, x[2 * i + 1] = f.y;
-        } else {
-            x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+__device__ __forceinline__ uint32_t within(uint32_t v, uint32_t end) {
+    uint32_t r;
+    if constexpr (kFp16) {
+        asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(end));
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(end ^ 0x80008000u));
+    } else {
+        asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(end));
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(end ^ 0x80008000u));
     }
-}
-template <bool kFp16>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (kFp16) {
-            const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
-        } else {
-            w[i] = ptx::pack_bf16x2(x[2 * i], x[2 * i + 1]);
-        }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return r;
 }
 
 template <bool kFp16>
-__global__ void __launch_bounds__(kWarps * 32) linear_sums_kernel(const LinearSumsArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 4) linear_sums_kernel(const LinearSumsArgs a) {
     __shared__ float part[kWarps][kLinearStrip];
     __shared__ uint32_t last;
     ptx::griddep_launch_dependents();
@@ -61,38 +46,53 @@ __global__ void __launch_bounds__(kWarps * 32) linear_sums_kernel(const LinearSu
     const int c = strip * kLinearStrip + lane * 8;
     const bool live = c < a.cols;  // cols is a multiple of 8
     const int64_t r1 = min(a.rows, (chunk + 1) * a.rows_per_chunk);
-    float sum[8];
+    constexpr int kDt = kFp16 ? CF_FP16 : CF_BF16;
+    using P = Piece<kDt>;
+    Two sum[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+    for (int j = 0; j < 4; ++j) sum[j] = Two(0.f);
+    const uint32_t end16 = from_float<kDt>(slope_end(a.act)), end = end16 | end16 << 16;
     const uint16_t *dy = static_cast<const uint16_t *>(a.dy), *z = static_cast<const uint16_t *>(a.z);
 #pragma unroll 1
     for (int64_t r = chunk * a.rows_per_chunk + warp; live && r < r1; r += kFly * kWarps) {
-        uint4 g[kFly], p[kFly];
+        P g[kFly], p[kFly];
 #pragma unroll
         for (int i = 0; i < kFly; ++i) {
-            const bool in = r + i * kWarps < r1;
             const size_t at = size_t(r + i * kWarps) * a.cols + c;
-            g[i] = in ? *reinterpret_cast<const uint4 *>(dy + at) : make_uint4(0u, 0u, 0u, 0u);
-            p[i] = in && z ? *reinterpret_cast<const uint4 *>(z + at) : make_uint4(0u, 0u, 0u, 0u);
+            g[i].zero();
+            p[i].zero();
+            if (r + i * kWarps < r1) {
+                g[i].load(dy + at);
+                if (z) p[i].load(z + at);
+            }
         }
 #pragma unroll
         for (int i = 0; i < kFly; ++i) {
-            float x[8], y[8];
-            unpack8<kFp16>(x, g[i]);
+            Two x[4], y[4];
+            g[i].unpack(x);
             if (z) {
-                unpack8<kFp16>(y, p[i]);
-                times_slope(x, y, a.act);
+                if (a.act != 3) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) p[i].w[j] = within<kFp16>(p[i].w[j], end);
+                }
+                p[i].unpack(y);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = times_slope(x[j], y[j], a.act);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += x[j];
-            if (a.dz && r + i * kWarps < r1)
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dz) + size_t(r + i * kWarps) * a.cols + c) =
-                    pack8<kFp16>(x);
+            for (int j = 0; j < 4; ++j) sum[j] = sum[j] + x[j];
+            if (a.dz && r + i * kWarps < r1) {
+                g[i].pack(x);
+                g[i].store(static_cast<uint16_t *>(a.dz) + size_t(r + i * kWarps) * a.cols + c);
+            }
         }
     }
     if (!a.sums) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) part[warp][lane * 8 + j] = sum[j];
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = sum[j].parts();
+        part[warp][lane * 8 + 2 * j] = v.x, part[warp][lane * 8 + 2 * j + 1] = v.y;
+    }
     __syncthreads();
     const int col = strip * kLinearStrip + int(threadIdx.x);
     float total = 0.f;
