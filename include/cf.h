@@ -891,7 +891,8 @@ CF_API cf_status cf_gemm_linear_grad_ex(const void *dY, const void *X, const voi
  * faster).
  * workspace (device) >= cf_stitch_workspace_size() bytes, the gradient
  * cf_stitch_block_norms_grad_workspace_size(), 16-byte aligned there; zeroed
- * once, as for every call.
+ * once, as for every call.  One workspace may serve these calls, the dense
+ * layer's, the grouped ones' and the log probabilities' in turn.
  * Tuning fields used (_ex): disable_pdl, timeout_us, extra_arrivals (TEST HOOK:
  * > 0 makes the wait for a row run out, of rows in bulk copies: cols of a
  * multiple of 8 from 512 to 8192, the gradient from 256 on, all 16-byte aligned). */

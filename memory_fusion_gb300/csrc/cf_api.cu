@@ -2146,19 +2146,20 @@ extern "C" cf_status cf_stitch_block_norms(const void *h, const void *x, const v
                                     nullptr);
 }
 
-// the error word; the sums of the sets, for each of up to four weights and biases; the gates' slots
+// the head that the grouped calls have, whose counters stay zero, so that one workspace may serve both; the sums of the
+// sets, for each of up to four weights and biases; the gates' slots
 static size_t block_norms_partials(const cf::BlockNormsGradPlan &p, int64_t cols) {
     return cf::align_up(size_t(4) * size_t(p.sets) * size_t(cols) * 4, 256);
 }
 
 extern "C" size_t cf_stitch_block_norms_grad_workspace_size(int64_t rows, int64_t cols) {
-    if (rows <= 0 || cols <= 0 || cols > cf::kBlockNormsMaxCols) return cf::kErrBytes;
+    if (rows <= 0 || cols <= 0 || cols > cf::kBlockNormsMaxCols) return kGroupedHead;
     size_t most = 0;
     for (bool lean : {false, true}) {
         const cf::BlockNormsGradPlan p = cf::plan_block_norms_grad(rows, cols, int(kPlanSms), lean, CF_BF16);
         most = std::max(most, block_norms_partials(p, cols) + size_t(p.workers) * 2 * size_t(cols) * 4);
     }
-    return cf::kErrBytes + most;
+    return kGroupedHead + most;
 }
 
 extern "C" cf_status cf_stitch_block_norms_grad_ex(
@@ -2222,7 +2223,7 @@ extern "C" cf_status cf_stitch_block_norms_grad_ex(
     a.post = int(post), a.pre = dy ? int(pre) : int(CF_NORM_NONE), a.dtype = int(dtype);
     const cf::BlockNormsGradPlan p = cf::plan_block_norms_grad(rows, cols, std::min(dev.sm_count, int(kPlanSms)),
                                                                cf::block_norms_grad_lean(a, vec), int(dtype));
-    unsigned char *const ws = static_cast<unsigned char *>(workspace) + cf::kErrBytes;
+    unsigned char *const ws = static_cast<unsigned char *>(workspace) + kGroupedHead;
     a.partials = reinterpret_cast<float *>(ws);
     a.slots = reinterpret_cast<float *>(ws + block_norms_partials(p, cols));
     a.rows = rows;
