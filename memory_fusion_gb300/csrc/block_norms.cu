@@ -187,7 +187,10 @@ enum RowMode : int {
     LOOSE = 0,  // numbers that start anywhere: a thread takes every lanes-th, fp32 ones ahead of time, in copies of 4 bytes
     SHORT = 1,  // 16-byte aligned, few columns: copies of 16 bytes ahead of time, by the thread that needs them
     WIDE = 2,   // 16-byte aligned, whole warps: bulk copies ahead of time, one a row
+    SHIFTED = 3,  // numbers that start anywhere, whole warps: bulk copies of the 16-byte pieces that hold a row
 };
+__host__ __device__ constexpr bool is_vec(int mode) { return mode == SHORT || mode == WIDE; }
+__host__ __device__ constexpr bool is_bulk(int mode) { return mode == WIDE || mode == SHIFTED; }
 
 constexpr int kMostRingRows = 5;
 
@@ -195,12 +198,12 @@ constexpr int kMostRingRows = 5;
 // pieces a thread.  LOOSE and SHORT: a thread fills and reads its own columns alone, so nobody waits for anybody.
 __host__ __device__ constexpr int ring_depth(int dt) { return dt == CF_FP32 ? 2 : 4; }
 __host__ __device__ constexpr bool has_ring(int dt, int mode, int pieces) {
-    return (mode != LOOSE || dt == CF_FP32) && pieces <= 2;
+    return is_bulk(mode) || ((mode == SHORT || dt == CF_FP32) && pieces <= 2);
 }
 template <int kDt, int kMode, int kRows, int kP>
 struct RowRing {
     using E = typename Element<kDt>::type;
-    static constexpr bool kVec = kMode != LOOSE;
+    static constexpr bool kVec = is_vec(kMode);
     static constexpr bool kOn = has_ring(kDt, kMode, kP);
     static constexpr int kDepth = ring_depth(kDt);
     static constexpr int kCopies = kVec ? Piece<kDt>::kWords / 4 : 8;  // of a piece
@@ -215,7 +218,7 @@ struct RowRing {
                                        int left_, volatile uint32_t *)
         : cols(c), base(ptx::smem_u32(ring) + threadIdx.x * kBytes), step(blockDim.x * kBytes), rows(rows_), stage(0), left(left_),
           apart(size_t(c.n)) {}
-    __device__ __forceinline__ void matrix(int k, const void *m, int64_t row) {
+    __device__ __forceinline__ void matrix(int k, const void *m, int64_t row, int64_t) {
         src[k] = m ? static_cast<const E *>(m) + (left > 0 ? size_t(row) * apart : 0) +
                          (cols.at(0, 0) < cols.n ? cols.at(0, 0) : 0)
                    : nullptr;
@@ -294,34 +297,44 @@ struct RowRing {
 // stage, and refills a stage when the exchange of the row's sums has shown that every thread is through with it.  What it
 // alone needs lies in shared memory: the other threads' registers hold the sums.  (With copies by each thread, their
 // addresses and predicates were a fifth of the gradient's instructions.)
+// SHIFTED: a row's 16-byte pieces, the first and last of which hold a neighbour's numbers, too; where they would reach
+// out of the matrix (its first and last row) the leader brings those few numbers itself.  A thread reads its numbers one
+// by one, behind the row's start in its first piece.
 struct RingState {
-    const void *src[kMostRingRows];  // the next row's share of this CTA; null: zeros
-    int left, fill, issued;          // rows to ask for; the stage to fill next; rows asked for
-    uint32_t bytes;                  // of a stage
+    const uint8_t *src[kMostRingRows];                      // the next row's share of this CTA; null: zeros
+    const uint8_t *lo[kMostRingRows], *hi[kMostRingRows];  // SHIFTED: the matrix's ends
+    int left, fill, issued;  // rows to ask for; the stage to fill next; rows asked for
+    uint32_t bytes;          // WIDE: of a stage
 };
-constexpr uint32_t kRingHead = 2048;  // of up to 16 groups: 8 mbarriers and the leader's state, 128 bytes
-static_assert(sizeof(RingState) <= 64, "behind the mbarriers");
-template <int kDt, int kRows, int kP>
-struct RowRing<kDt, WIDE, kRows, kP> {
+constexpr uint32_t kRingHead = 2048;  // of up to 8 groups: 8 mbarriers and the leader's state, 256 bytes
+static_assert(sizeof(RingState) <= 192, "behind the mbarriers");
+// bytes of a row of a ring's stage
+__host__ __device__ constexpr int ring_pitch(int dt, int mode, int pieces, int lanes) {
+    return lanes * pieces * 8 * type_bytes(dt) + (mode == SHIFTED ? 32 : 0);
+}
+template <int kDt, int kMode, int kRows, int kP>
+struct BulkRing {
     using E = typename Element<kDt>::type;
-    static constexpr bool kOn = true;
-    const Columns<true> &cols;
+    static constexpr bool kOn = true, kVec = kMode == WIDE;
+    const Columns<kVec> &cols;
     const RingArgs &ring;
     volatile uint32_t *abort;
     RingState *state;
     uint32_t bar, at, pitch;  // of the row in hand: its mbarrier, the thread's numbers; from a row to the next
+    uint32_t lead[kVec ? 1 : kRows];  // SHIFTED: of each matrix's row in hand, bytes in front of it in its first piece
     int rows, stage;
     uint32_t phase;
     bool leader;
 
-    __device__ __forceinline__ RowRing(const Columns<true> &c, const RingArgs &r, uint8_t *smem, const Group &g, int rows_,
-                                       int left, volatile uint32_t *abort_)
+    __device__ __forceinline__ BulkRing(const Columns<kVec> &c, const RingArgs &r, uint8_t *smem, const Group &g, int rows_,
+                                        int left, volatile uint32_t *abort_)
         : cols(c), ring(r), abort(abort_), rows(rows_), stage(0), phase(0), leader(g.t == 0) {
         const int group = int(threadIdx.x) / c.lanes;
-        pitch = uint32_t(c.lanes) * kP * 8 * sizeof(E);
-        bar = ptx::smem_u32(smem) + uint32_t(group) * 128u;
-        state = reinterpret_cast<RingState *>(smem + group * 128 + 64);
-        at = ptx::smem_u32(smem) + kRingHead + uint32_t(group * r.depth * rows) * pitch + uint32_t(c.c0) * 8 * sizeof(E);
+        pitch = uint32_t(ring_pitch(kDt, kMode, kP, c.lanes));
+        bar = ptx::smem_u32(smem) + uint32_t(group) * 256u;
+        state = reinterpret_cast<RingState *>(smem + group * 256 + 64);
+        at = ptx::smem_u32(smem) + kRingHead + uint32_t(group * r.depth * rows) * pitch +
+             uint32_t(c.c0) * (kVec ? 8 : 1) * sizeof(E);
         if (leader) {
             for (int s = 0; s < r.depth; ++s) ptx::mbar_init(bar + 8 * s, 1 + r.extra_arrivals);
             ptx::fence_mbarrier_init_cluster();
@@ -334,40 +347,95 @@ struct RowRing<kDt, WIDE, kRows, kP> {
         return uint32_t(min(cols.lanes * kP * 8, cols.n - cols.first)) * uint32_t(sizeof(E));
     }
     // (what no copy fills is zero)
-    __device__ __forceinline__ void matrix(int k, const void *m, int64_t row) {
+    __device__ __forceinline__ void matrix(int k, const void *m, int64_t row, int64_t all) {
+        m = k < rows ? m : nullptr;
+        const size_t row_bytes = size_t(cols.n) * sizeof(E);
+        const uint8_t *const first = static_cast<const uint8_t *>(m) + size_t(row) * row_bytes + cols.first * sizeof(E);
         if (leader) {
-            state->src[k] =
-                m && k < rows ? static_cast<const E *>(m) + (state->left > 0 ? size_t(row) * cols.n + cols.first : 0)
-                              : nullptr;
-            if (m && k < rows) state->bytes += share();
+            state->src[k] = m && state->left > 0 ? first : nullptr;
+            if (m) state->bytes += share();
+            state->lo[k] = static_cast<const uint8_t *>(m);
+            state->hi[k] = static_cast<const uint8_t *>(m) + size_t(all) * row_bytes;
         }
+        if constexpr (!kVec) lead[k] = uint32_t(reinterpret_cast<uintptr_t>(first)) & 15u;
         if (k >= rows) return;
-        for (int p = 0; p < kP; ++p)
-            if (!m || !cols.live(p, 0))
-                for (int s = 0; s < ring.depth; ++s)
-                    for (uint32_t b = 0; b < 8 * sizeof(E); b += 4)
-                        ptx::st_shared_u32(at + uint32_t(s * rows + k) * pitch + uint32_t(p * cols.lanes) * 8 * sizeof(E) + b,
-                                           0u);
+        if constexpr (kVec) {
+            for (int p = 0; p < kP; ++p)
+                if (!m || !cols.live(p, 0))
+                    for (int s = 0; s < ring.depth; ++s)
+                        for (uint32_t b = 0; b < 8 * sizeof(E); b += 4)
+                            ptx::st_shared_u32(
+                                at + uint32_t(s * rows + k) * pitch + uint32_t(p * cols.lanes) * 8 * sizeof(E) + b, 0u);
+        } else if (!m) {
+            for (int s = 0; s < ring.depth; ++s)
+                for (uint32_t b = uint32_t(cols.c0) * 4; b < pitch; b += uint32_t(cols.lanes) * 4)
+                    ptx::st_shared_u32(at - uint32_t(cols.c0) * sizeof(E) + uint32_t(s * rows + k) * pitch + b, 0u);
+        }
     }
     __device__ __forceinline__ static void issue(RingState *st, const RingArgs &ring, uint32_t bars, uint32_t first,
-                                              uint32_t pitch, int rows, uint32_t share, size_t apart,
-                                              volatile uint32_t *abort, int n) {
+                                                 uint32_t pitch, int rows, uint32_t share, size_t apart,
+                                                 volatile uint32_t *abort, int n) {
         const uint64_t policy = ptx::policy_evict_first();
         for (; n > 0; --n) {
             const int to = st->fill;
             st->fill = to + 1 == ring.depth ? 0 : to + 1;
             if (st->left <= 0 || *abort) return;
             const uint32_t full = bars + 8 * to;
-            ptx::mbar_arrive_expect_tx(full, st->bytes);
+            if constexpr (!kVec) {
+                for (int k = 0; k < rows; ++k)
+                    if (st->src[k] != nullptr) inner(st, k, share, first + uint32_t(to * rows + k) * pitch);
+            }
+            if constexpr (kVec) {
+                ptx::mbar_arrive_expect_tx(full, st->bytes);
+            } else {
+                uint32_t bytes = 0;
+                for (int k = 0; k < rows; ++k) bytes += st->src[k] == nullptr ? 0u : inner(st, k, share, 0u);
+                ptx::mbar_arrive_expect_tx(full, bytes);  // (after the leader's own numbers)
+            }
             for (int k = 0; k < rows; ++k) {
-                const uint8_t *const src = static_cast<const uint8_t *>(st->src[k]);
+                const uint8_t *const src = st->src[k];
                 if (src == nullptr) continue;
-                ptx::bulk_load_g2s_hint(first + uint32_t(to * rows + k) * pitch, src, share, full, policy);
+                uint32_t dst = first + uint32_t(to * rows + k) * pitch, size = share;
+                const uint8_t *from = src;
+                if constexpr (!kVec) {
+                    size = inner(st, k, share, 0u);
+                    from = reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15));
+                    if (at_end(st, k, share)) {
+                        const uint8_t *const piece = from;
+                        from = reinterpret_cast<const uint8_t *>((reinterpret_cast<uintptr_t>(src) + 15) & ~uintptr_t(15));
+                        dst += uint32_t(from - piece);
+                    }
+                }
+                if (size > 0) ptx::bulk_load_g2s_hint(dst, from, size, full, policy);
                 st->src[k] = src + apart;
             }
             --st->left;
             ++st->issued;
         }
+    }
+    // SHIFTED: whether the row's first or last piece reaches out of the matrix
+    __device__ __forceinline__ static bool at_end(const RingState *st, int k, uint32_t share) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(st->src[k]), e = a + share;
+        return (a & ~uintptr_t(15)) < reinterpret_cast<uintptr_t>(st->lo[k]) ||
+               ((e + 15) & ~uintptr_t(15)) > reinterpret_cast<uintptr_t>(st->hi[k]);
+    }
+    // Bytes of the row's pieces; where they would reach out of the matrix, of those inside it, and the numbers outside
+    // them are brought to `to`, where the row's first piece begins (0: they are not).
+    __device__ __forceinline__ static uint32_t inner(const RingState *st, int k, uint32_t share, uint32_t to) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(st->src[k]), e = a + share;
+        if (!at_end(st, k, share)) return uint32_t(((e + 15) & ~uintptr_t(15)) - (a & ~uintptr_t(15)));
+        const uintptr_t a0 = (a + 15) & ~uintptr_t(15), a1 = max(a0, e & ~uintptr_t(15));
+        if (to != 0u) {
+            for (uintptr_t b = a; b < min(a0, e); b += sizeof(E))
+                put(to + uint32_t(b - (a & ~uintptr_t(15))), *reinterpret_cast<const E *>(b));
+            for (uintptr_t b = a1; b < e; b += sizeof(E))
+                put(to + uint32_t(b - (a & ~uintptr_t(15))), *reinterpret_cast<const E *>(b));
+        }
+        return uint32_t(a1 - a0);
+    }
+    __device__ __forceinline__ static void put(uint32_t addr, E v) {
+        if constexpr (sizeof(E) == 4) ptx::st_shared_u32(addr, __float_as_uint(v));
+        else ptx::st_shared_u16(addr, v);
     }
     // every thread of the row has taken what it needs of the last n rows.  (Before the first ones: the barriers'
     // initialisation and the zeros are known to all threads.)
@@ -382,16 +450,31 @@ struct RowRing<kDt, WIDE, kRows, kP> {
         ptx::mbar_wait_bounded(bar, phase, ring.timeout_ns, abort, ring.err, 0x76000000u | uint32_t(stage));
     }
     __device__ __forceinline__ void take(Piece<kDt> &v, int k, int p) {
-        const uint32_t from = at + uint32_t(k) * pitch + uint32_t(p * cols.lanes) * 8 * sizeof(E);
+        if constexpr (kVec) {
+            const uint32_t from = at + uint32_t(k) * pitch + uint32_t(p * cols.lanes) * 8 * sizeof(E);
 #pragma unroll
-        for (int j = 0; j < Piece<kDt>::kWords / 4; ++j) {
-            const uint4 q = ptx::ld_shared_v4(from + 16 * j);
-            v.w[4 * j] = q.x, v.w[4 * j + 1] = q.y, v.w[4 * j + 2] = q.z, v.w[4 * j + 3] = q.w;
+            for (int j = 0; j < Piece<kDt>::kWords / 4; ++j) {
+                const uint4 q = ptx::ld_shared_v4(from + 16 * j);
+                v.w[4 * j] = q.x, v.w[4 * j + 1] = q.y, v.w[4 * j + 2] = q.z, v.w[4 * j + 3] = q.w;
+            }
+        } else {
+            uint32_t from = at + uint32_t(k) * pitch + lead[k] + uint32_t(p * 8 * cols.lanes) * sizeof(E);
+            v.zero();
+#pragma unroll
+            for (int j = 0; j < 8; ++j, from += uint32_t(cols.lanes) * sizeof(E)) {
+                if constexpr (sizeof(E) == 4) v.w[j] = cols.live(p, j) ? ptx::ld_shared_u32(from) : 0u;
+                else v.put(j, cols.live(p, j) ? ptx::ld_shared_u16(from) : uint16_t(0));
+            }
         }
     }
     __device__ __forceinline__ void next() {
         at += uint32_t(rows) * pitch;
         bar += 8;
+        if constexpr (!kVec) {
+            const uint32_t row = uint32_t(cols.n) * uint32_t(sizeof(E));
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) lead[k] = (lead[k] + row) & 15u;
+        }
         if (++stage == ring.depth) {
             stage = 0;
             phase ^= 1u;
@@ -408,6 +491,14 @@ struct RowRing<kDt, WIDE, kRows, kP> {
             ptx::mbar_wait_bounded(bar + 8 * (s - stage), uint32_t((issued - 1 - s) / ring.depth) & 1u, ring.timeout_ns,
                                    &local, nullptr, 0);
     }
+};
+template <int kDt, int kRows, int kP>
+struct RowRing<kDt, WIDE, kRows, kP> : BulkRing<kDt, WIDE, kRows, kP> {
+    using BulkRing<kDt, WIDE, kRows, kP>::BulkRing;
+};
+template <int kDt, int kRows, int kP>
+struct RowRing<kDt, SHIFTED, kRows, kP> : BulkRing<kDt, SHIFTED, kRows, kP> {
+    using BulkRing<kDt, SHIFTED, kRows, kP>::BulkRing;
 };
 
 // x with 0 in the place of columns behind the last one
@@ -454,7 +545,7 @@ __device__ __forceinline__ float spread(Group &g, int norm, Two (&x)[kP][4], con
 // kP pieces a thread.  kFull: LayerNorms or biases, too.  A worker takes a stretch of neighbouring rows, as in the gradient.
 template <int kDt, int kMode, int kP, bool kFull>
 __global__ void __maxnreg__(kP == 4 ? 64 : 128) block_norms_kernel(const BlockNormsArgs a) {
-    constexpr bool kVec = kMode != LOOSE;
+    constexpr bool kVec = is_vec(kMode);
     extern __shared__ __align__(128) uint8_t ring_smem[];
     __shared__ uint32_t abort;
     if (threadIdx.x == 0) abort = 0u;
@@ -484,9 +575,9 @@ __global__ void __maxnreg__(kP == 4 ? 64 : 128) block_norms_kernel(const BlockNo
     // rows that threads of one warp may share a warp's turn with: as many turns as any; else their own
     const int turns = a.lanes < 32 ? a.chunk : last - first;
     RowRing<kDt, kMode, 3, kP> ring(cols, a.ring, ring_smem, g, a.gates_along ? 3 : 2, last - first, &abort);
-    ring.matrix(0, a.h, first);
-    ring.matrix(1, a.x, first);
-    ring.matrix(2, a.gates_along ? a.gate : nullptr, first);
+    ring.matrix(0, a.h, first, a.rows);
+    ring.matrix(1, a.x, first, a.rows);
+    ring.matrix(2, a.gates_along ? a.gate : nullptr, first, a.rows);
     __syncthreads();
     ring.start();
 
@@ -604,9 +695,10 @@ __device__ __forceinline__ void store_floats(float *out, const Two (&x)[4], cons
     }
 }
 
-// Bytes of the sums over all gates that the CTA's threads keep in shared memory.
-__host__ __device__ constexpr int totals_bytes(bool gate, bool full, int pieces, int threads) {
-    return gate ? threads * pieces * 32 * (full ? 2 : 1) : 0;
+// Bytes of what the CTA's threads keep in shared memory, each for itself: the sums over all gates and, with two pieces a
+// thread, Post's weight (in registers, what did not fit took the gradient of 16384 x 4096 from 154 to 175 us).
+__host__ __device__ constexpr int kept_bytes(bool gate, bool full, int pieces, int threads) {
+    return threads * pieces * 32 * ((gate ? (full ? 2 : 1) : 0) + (pieces == 2 ? 1 : 0));
 }
 
 // With hc and xc the rows without their means (RMSNorm: the rows), g2 = dy w2 and w1 = scale gate weight, every sum that
@@ -623,9 +715,9 @@ __host__ __device__ constexpr int totals_bytes(bool gate, bool full, int pieces,
 // exchanges its sums.
 template <int kDt, int kMode, bool kCluster, bool kGate, bool kFull, int kP>
 __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsGradArgs a) {
-    constexpr bool kVec = kMode != LOOSE, kWide = kMode == WIDE;
+    constexpr bool kVec = is_vec(kMode), kWide = is_bulk(kMode);
     constexpr int kV = kFull ? 16 : 8;
-    extern __shared__ __align__(128) uint8_t smem[];  // the sums over all gates, the ring
+    extern __shared__ __align__(128) uint8_t smem[];  // what is kept there, the ring
     __shared__ uint32_t abort;
     __shared__ float slots[kCluster ? 2 * 16 * kV * 8 : 2 * (16 * kV + 8 * 32)];  // (up to 8 groups, each rounded up to 32)
     using E = typename Element<kDt>::type;
@@ -660,14 +752,15 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
     const bool lh = kFull && a.post == CF_NORM_LAYER, lx = kFull && a.pre == CF_NORM_LAYER;
     if constexpr (kCluster) ptx::cluster_sync();  // nobody writes into a CTA that has not started
 
-    Two w2[kP][4], w1[kP][4];  // Pre's weight; scale * gate * Post's weight
+    constexpr bool kAside = kP == 2;
+    Two w2[kP][4], w1[kAside ? 1 : kP][4];  // Pre's weight; scale * gate * Post's weight
 #pragma unroll
     for (int p = 0; p < kP; ++p) load_vector<kVec>(w2[p], a.pre_weight, 1.f, cols, p);
     // sums over the rows, those of the gate in hand in sa and sb; in shared memory, which no other thread looks at, those
     // of all gates
     Two sa[kP][4], sc[kP][4], sb[kP][4], sd[kP][4];
     float *const done = reinterpret_cast<float *>(smem) + threadIdx.x * 2;
-    uint8_t *const ring_smem = smem + totals_bytes(kGate, kFull, kP, int(blockDim.x));
+    uint8_t *const ring_smem = smem + kept_bytes(kGate, kFull, kP, int(blockDim.x));
     auto total = [&](int k, int p, int j) -> float2 & {
         return *reinterpret_cast<float2 *>(done + ((k * kP + p) * 4 + j) * 2 * int(blockDim.x));
     };
@@ -682,14 +775,21 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
             }
         }
 
+    auto w1_at = [&](int p, int j) -> float2 & { return total(kGate ? (kFull ? 2 : 1) : 0, p, j); };
+    auto w1_of = [&](int p, int j) { return kAside ? Two(w1_at(p, j)) : w1[kAside ? 0 : p][j]; };
+    auto set_w1 = [&](int p, int j, Two v) {
+        if constexpr (kAside) w1_at(p, j) = v.parts();
+        else w1[p][j] = v;
+    };
+
     int gate_at = 0, gate_end = 0;  // the gate in hand, the first row behind its rows
     const bool gates_along = kGate && RowRing<kDt, kMode, 5, kP>::kOn && a.gate && a.rows_per_gate == 1;
     RowRing<kDt, kMode, 5, kP> ring(cols, a.ring, ring_smem, g, gates_along ? 5 : 4, last - first, &abort);
-    ring.matrix(0, a.h, first);
-    ring.matrix(1, a.dy ? a.x_out : nullptr, first);
-    ring.matrix(2, a.dy, first);
-    ring.matrix(3, a.dx_out, first);
-    ring.matrix(4, gates_along ? a.gate : nullptr, first);
+    ring.matrix(0, a.h, first, a.rows);
+    ring.matrix(1, a.dy ? a.x_out : nullptr, first, a.rows);
+    ring.matrix(2, a.dy, first, a.rows);
+    ring.matrix(3, a.dx_out, first, a.rows);
+    ring.matrix(4, gates_along ? a.gate : nullptr, first, a.rows);
     __syncthreads();
     ring.start();
     // scale * gate, from memory or from the row of gates in hand
@@ -706,11 +806,11 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
         gate_end = int((uint32_t(of) + 1u) * a.rows_per_gate);
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
-            Two k[4];
+            Two k[4], w[4];
             scaled_gate(k, of, p, here);
-            load_vector<kVec>(w1[p], a.post_weight, 1.f, cols, p);
+            load_vector<kVec>(w, a.post_weight, 1.f, cols, p);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w1[p][j] = live_two(w1[p][j] * k[j], cols, p, j);
+            for (int j = 0; j < 4; ++j) set_w1(p, j, live_two(w[j] * k[j], cols, p, j));
         }
     };
     if (kGate && first < last) {
@@ -718,9 +818,10 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
     } else {
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
-            load_vector<kVec>(w1[p], a.post_weight, 1.f, cols, p);
+            Two w[4];
+            load_vector<kVec>(w, a.post_weight, 1.f, cols, p);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w1[p][j] = live_two(w1[p][j] * Two(a.scale), cols, p, j);
+            for (int j = 0; j < 4; ++j) set_w1(p, j, live_two(w[j] * Two(a.scale), cols, p, j));
         }
     }
     size_t at = first < last ? size_t(first) * a.cols : 0;  // where the row in hand lies
@@ -762,7 +863,7 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const Two h = h_of(p, j), x = x_of(p, j), d = pair(3, p, j);
-                    const Two g2 = pair(2, p, j) * w2[p][j], wh = w1[p][j] * h;
+                    const Two w = w1_of(p, j), g2 = pair(2, p, j) * w2[p][j], wh = w * h;
                     s[0] = fma(h, h, s[0]);
                     s[1] = fma(x, x, s[1]);
                     s[2] = fma(g2, x, s[2]);
@@ -772,10 +873,10 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
                     if constexpr (kFull) {
                         s[6] = s[6] + g2;
                         s[7] = s[7] + wh;
-                        s[8] = fma(w1[p][j], d, s[8]);
-                        s[9] = fma(w1[p][j], g2, s[9]);
-                        s[10] = fma(w1[p][j], x, s[10]);
-                        s[11] = s[11] + w1[p][j];
+                        s[8] = fma(w, d, s[8]);
+                        s[9] = fma(w, g2, s[9]);
+                        s[10] = fma(w, x, s[10]);
+                        s[11] = s[11] + w;
                     }
                 }
 #pragma unroll
@@ -814,7 +915,7 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
                 if constexpr (kFull) sd[p][j] = sd[p][j] + y, sb[p][j] = sb[p][j] + d;
                 const Two h = h_of(p, j) * k1;
                 sa[p][j] = fma(d, h, sa[p][j]);
-                dh[j] = fma(h, kn, (w1[p][j] * d) * k1);
+                dh[j] = fma(h, kn, (w1_of(p, j) * d) * k1);
                 if constexpr (kFull) dh[j] = dh[j] + km;
                 dx[j] = d * Two(a.alpha);
             }
@@ -827,22 +928,26 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
                 const int from = gate_end - int(a.rows_per_gate);
 #pragma unroll
                 for (int p = 0; p < kP; ++p) {
-                    Two w[4], b[4], d[4], gate[4];
-                    scaled_gate(gate, gate_at, p, false);
+                    Two w[4], b[4], d[4];
                     load_vector<kVec>(w, a.post_weight, 1.f, cols, p);
                     if constexpr (kFull) load_vector<kVec>(b, a.post_bias, 0.f, cols, p);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        total(0, p, j) = fma(gate[j], sa[p][j], Two(total(0, p, j))).parts();
                         d[j] = w[j] * sa[p][j];
-                        if constexpr (kFull) {
-                            d[j] = fma(b[j], sb[p][j], d[j]);
-                            total(1, p, j) = fma(gate[j], sb[p][j], Two(total(1, p, j))).parts();
-                            sb[p][j] = Two(0.f);
-                        }
+                        if constexpr (kFull) d[j] = fma(b[j], sb[p][j], d[j]);
                         d[j] = d[j] * Two(a.scale);
-                        sa[p][j] = Two(0.f);
                     }
+                    if (a.sum_at[0] >= 0 || a.sum_at[1] >= 0) {
+                        Two gate[4];
+                        scaled_gate(gate, gate_at, p, false);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            total(0, p, j) = fma(gate[j], sa[p][j], Two(total(0, p, j))).parts();
+                            if constexpr (kFull) total(1, p, j) = fma(gate[j], sb[p][j], Two(total(1, p, j))).parts();
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sa[p][j] = sb[p][j] = Two(0.f);
                     if (a.dgate && from >= first && gate_end <= last) {
                         store_piece<kDt, kVec>(static_cast<E *>(a.dgate) + size_t(gate_at) * a.cols, d, cols, p, true);
                     } else if (a.dgate) {  // slot 0: begun by a worker before; slot 1: here, and goes on
@@ -893,8 +998,9 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
     if constexpr (kCluster) ptx::cluster_sync();  // no CTA leaves while its peers may still write to it
 }
 
-// The workers' sums added in order: 32 columns a CTA, a warp every kSumWarps-th term, then the warps.
-constexpr int kSumWarps = 8, kSumFly = 8;
+// The workers' sums added in order: 32 columns a CTA, a warp every so many-th term, then the warps.  (335 terms of 1111
+// columns by eight warps 10.5 us, which is the loads one after another.)
+constexpr int kSumWarps = 32, kSumFly = 8;
 __global__ void __launch_bounds__(kSumWarps * 32) block_norms_sums_kernel(const BlockNormsGradArgs a, int nsums, int gates_first) {
     __shared__ float part[kSumWarps][32];
     ptx::griddep_launch_dependents();
@@ -934,11 +1040,12 @@ __global__ void __launch_bounds__(kSumWarps * 32) block_norms_sums_kernel(const 
         terms = int(last - w);
     }
     float s = head && warp == 0 && live ? __ldcg(head + c) : 0.f;
-    for (int i = warp; i < terms; i += kSumWarps * kSumFly) {
+    const int warps = int(blockDim.x) / 32;
+    for (int i = warp; i < terms; i += warps * kSumFly) {
         float x[kSumFly];
 #pragma unroll
         for (int k = 0; k < kSumFly; ++k)
-            x[k] = live && i + kSumWarps * k < terms ? __ldcg(from + (i + kSumWarps * k) * step + c) : 0.f;
+            x[k] = live && i + warps * k < terms ? __ldcg(from + (i + warps * k) * step + c) : 0.f;
 #pragma unroll
         for (int k = 0; k < kSumFly; ++k) s += x[k];
     }
@@ -946,8 +1053,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) block_norms_sums_kernel(const 
     __syncthreads();
     if (warp != 0 || !live) return;
     s = 0.f;
-#pragma unroll
-    for (int k = 0; k < kSumWarps; ++k) s += part[k][lane];
+    for (int k = 0; k < warps; ++k) s += part[k][lane];
     if (of < 0) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -1030,8 +1136,8 @@ template <int kDt>
 const void *forward_kernel(int mode, bool full, int pieces) {
     if (mode == LOOSE)
         return pieces == 1   ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, LOOSE, 1, true>)
-               : pieces == 2 ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, LOOSE, 2, true>)
                              : reinterpret_cast<const void *>(&block_norms_kernel<kDt, LOOSE, 4, true>);
+    if (mode == SHIFTED) return reinterpret_cast<const void *>(&block_norms_kernel<kDt, SHIFTED, 2, true>);
     if (mode == SHORT)
         return pieces == 1 ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, SHORT, 1, true>)
                            : reinterpret_cast<const void *>(&block_norms_kernel<kDt, SHORT, 4, true>);
@@ -1044,21 +1150,24 @@ const void *grad_of() {
 }
 template <int kDt>
 const void *grad_kernel(int mode, bool cluster, bool gate, bool full, int pieces) {
-    if (mode == LOOSE)
-        return cluster ? grad_of<kDt, LOOSE, true, true, true, 1>() : grad_of<kDt, LOOSE, false, true, true, 1>();
+    if (mode == LOOSE) return grad_of<kDt, LOOSE, false, true, true, 1>();
+    if (mode == SHIFTED)
+        return cluster ? grad_of<kDt, SHIFTED, true, true, true, 1>() : grad_of<kDt, SHIFTED, false, true, true, 1>();
     if (mode == SHORT) return grad_of<kDt, SHORT, false, true, true, 1>();
     if (cluster) return full ? grad_of<kDt, WIDE, true, true, true, 1>() : grad_of<kDt, WIDE, true, true, false, 1>();
     if (full) return gate ? grad_of<kDt, WIDE, false, true, true, 1>() : grad_of<kDt, WIDE, false, false, true, 1>();
-    if (pieces == 2) return gate ? grad_of<kDt, WIDE, false, true, false, 2>() : grad_of<kDt, WIDE, false, false, false, 2>();
+    if constexpr (kDt != CF_FP32)
+        if (pieces == 2)
+            return gate ? grad_of<kDt, WIDE, false, true, false, 2>() : grad_of<kDt, WIDE, false, false, false, 2>();
     return grad_of<kDt, WIDE, false, true, false, 1>();
 }
 
-// Shared memory of a launch's ring and, WIDE, its depth: what fits with `ctas` CTAs an SM, up to r->depth stages (0: three; 2, 3, 4
+// Shared memory of a launch's ring and, in bulk copies, its depth: what fits with `ctas` CTAs an SM, up to r->depth stages (0: three; 2, 3, 4
 // and 6 of them, 16384 x 4096 bf16 forward: 97, 93, 95 and 135 us, what they take is missing in L1).
-int plan_ring(RingArgs *r, int dt, int mode, int rows, int pieces, int threads, int ctas, int own) {
+int plan_ring(RingArgs *r, int dt, int mode, int rows, int pieces, int lanes, int threads, int ctas, int own) {
     if (!has_ring(dt, mode, pieces)) return 0;
-    const int stage = rows * threads * pieces * 8 * type_bytes(dt);
-    if (mode != WIDE) return ring_depth(dt) * stage;
+    const int stage = rows * (threads / lanes) * ring_pitch(dt, mode, pieces, lanes);
+    if (!is_bulk(mode)) return ring_depth(dt) * stage;
     const int room = std::min(kMostSmem, (kMostSmem + 1024) / ctas - 1024) - own - int(kRingHead);
     r->depth = std::max(1, std::min(r->depth > 0 ? std::min(r->depth, 8) : 3, room / stage));
     return int(kRingHead) + r->depth * stage;
@@ -1074,7 +1183,7 @@ cudaError_t launch_block_norms(BlockNormsArgs a, bool vec, int sms, bool pdl, cu
     // a thread's pieces: two, so that what a row costs besides its numbers is shared by more of them
     const int per = pieces < 64 ? 1 : pieces <= 1024 ? 2 : 4;
     a.lanes = round_lanes((pieces + per - 1) / per);
-    const int mode = !vec ? LOOSE : per == 2 ? WIDE : SHORT;
+    const int mode = per == 2 ? (vec ? WIDE : SHIFTED) : vec ? SHORT : LOOSE;
     const int groups = std::max(1, 256 / a.lanes), threads = groups * a.lanes;
     // a stretch of rows for each group of threads
     const int per_sm = std::max(1, kForwardThreads / threads);
@@ -1089,7 +1198,7 @@ cudaError_t launch_block_norms(BlockNormsArgs a, bool vec, int sms, bool pdl, cu
     int own;
     const cudaError_t e = allow_smem(fn, &own);
     if (e != cudaSuccess) return e;
-    const int smem = plan_ring(&a.ring, a.dtype, mode, a.gates_along ? 3 : 2, per, threads, per_sm, own);
+    const int smem = plan_ring(&a.ring, a.dtype, mode, a.gates_along ? 3 : 2, per, a.lanes, threads, per_sm, own);
     void *args[] = {&a};
     return launch(fn, dim3(unsigned(ctas)), threads, 1, pdl, stream, args, smem);
 }
@@ -1121,7 +1230,7 @@ cudaError_t launch_block_norms_grad(BlockNormsGradArgs a, const BlockNormsGradPl
     a.chunk = p.chunk;
     a.sets = p.sets;
     const bool gate = a.gate != nullptr, cluster = p.cluster > 1, full = !block_norms_grad_lean(a, vec);
-    const int mode = !vec ? LOOSE : p.lanes < 32 ? SHORT : WIDE;
+    const int mode = p.lanes < 32 ? (vec ? SHORT : LOOSE) : vec ? WIDE : SHIFTED;
     const void *fn = a.dtype == CF_BF16   ? grad_kernel<CF_BF16>(mode, cluster, gate, full, p.pieces)
                      : a.dtype == CF_FP16 ? grad_kernel<CF_FP16>(mode, cluster, gate, full, p.pieces)
                                           : grad_kernel<CF_FP32>(mode, cluster, gate, full, p.pieces);
@@ -1131,11 +1240,11 @@ cudaError_t launch_block_norms_grad(BlockNormsGradArgs a, const BlockNormsGradPl
     if (e != cudaSuccess) return e;
     const int rows = a.gate && a.rows_per_gate == 1 ? 5 : 4;
     // (as grad_kernel chooses: what is rare has its gates' sums anyway)
-    const int totals = totals_bytes(gate || mode != WIDE || cluster || (!full && p.pieces == 1), full || mode != WIDE,
+    const int kept = kept_bytes(gate || mode != WIDE || cluster || (!full && p.pieces == 1), full || mode != WIDE,
                                     p.pieces, p.threads);
     // (the ring's place takes the sums of several groups in the end)
-    const int smem = totals + std::max(plan_ring(&a.ring, a.dtype, mode, rows, p.pieces, p.threads,
-                                                 std::max(1, 512 / p.threads), own + totals),
+    const int smem = kept + std::max(plan_ring(&a.ring, a.dtype, mode, rows, p.pieces, p.lanes, p.threads,
+                                                 std::max(1, 512 / p.threads), own + kept),
                                        p.threads == p.lanes ? 0 : p.threads * p.pieces * 8 * 4);
     e = launch(fn, dim3(unsigned(p.sets * p.cluster)), p.threads, p.cluster, pdl, stream, args, smem);
     if (e != cudaSuccess) return e;
@@ -1147,7 +1256,8 @@ cudaError_t launch_block_norms_grad(BlockNormsGradArgs a, const BlockNormsGradPl
     if (nsums + shared == 0) return cudaSuccess;
     void *args2[] = {&a, &nsums, &gates_first};
     return launch(reinterpret_cast<const void *>(&block_norms_sums_kernel),
-                  dim3(unsigned((a.cols + 31) / 32) * unsigned(nsums + shared)), kSumWarps * 32, 1, pdl, stream, args2);
+                  dim3(unsigned((a.cols + 31) / 32) * unsigned(nsums + shared)),
+                  p.workers > 8 * kSumFly * 3 ? kSumWarps * 32 : 256, 1, pdl, stream, args2);
 }
 
 }  // namespace cf

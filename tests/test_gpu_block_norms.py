@@ -281,6 +281,37 @@ def test_no_rows_and_no_columns():
     assert cf.stitch_block_norms(n, n, pre="rms")[1].shape == (3, 0)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("N", [64, 1024, 9000])
+@pytest.mark.parametrize("shift", [1, 3, 7])
+def test_gradient_of_unaligned_rows(N, dt, shift):
+    """Tensors that start anywhere in memory, each elsewhere."""
+    torch = torch_cuda()
+    c, v, gate, kw = _case((30, N), dt, "rms", "rms", 3, False)
+    dv = {k: _dev(a) for k, a in v.items()}
+
+    def odd(a, by):
+        t = _dev(a, dt)
+        out = torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")[by % 8:by % 8 + t.numel()].view(t.shape)
+        return out.copy_(t)
+
+    r = _rng(3)
+    dy, dxo = _round(r.standard_normal((30, N)), dt), _round(r.standard_normal((30, N)), dt)
+    xo = _round(oracle.block_norms(c["h"], c["x"], gate=gate, **v, **kw)[0], dt)
+    args = [odd(a, shift * (i + 1)) for i, a in enumerate((dy, dxo, c["h"], xo))]
+    got = cf.stitch_block_norms_grad(*args, gate=odd(gate, 5), **dv, **kw)
+    ref = oracle.block_norms_grad(dy, dxo, c["h"], xo, gate=gate, **v, **kw)
+    bounds = _grad_bounds(dy, dxo, c, xo, v, gate, kw)
+    for k, t in zip(KEYS, got):
+        if t is not None:
+            _check(t, ref[k], bounds[k], dt if k in ("h", "x", "gate") else "fp32", k)
+    out, y = cf.stitch_block_norms(args[2], odd(c["x"], 2), gate=odd(gate, 5), **dv, **kw)
+    ref_x, ref_y = oracle.block_norms(c["h"], c["x"], gate=gate, **v, **kw)
+    e = _forward_bounds(c, v, gate, kw)
+    _check(out, ref_x, e, dt, "x_out")
+    _check(y, ref_y, _normed("rms", ref_x, v["pre_weight"], None, e) + 2 * U * np.abs(ref_y), dt, "y")
+
+
 def test_unaligned_rows():
     """Tensors that start anywhere in memory."""
     torch = torch_cuda()
