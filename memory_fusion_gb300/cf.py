@@ -981,6 +981,18 @@ def _made(name, t, shape, dtype, device):
     return t
 
 
+def _made_like(name, t, like):
+    """An output of an operand's shape and type, which takes less time to make."""
+    if t is None:
+        return _torch.empty_like(like)
+    _operand(name, t, like.shape, like.dtype, like.device)
+    return t
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 def gemm_linear(X, W, bias=None, *, act="none", residual=None, preact=None, out=None, workspace=None, stream=None,
                 tuning=None):
     """Y = act(X @ W + bias) + residual; X [M, K], W [K, N] and residual [M, N] bf16 or fp16 CUDA tensors, bias fp32
@@ -1030,11 +1042,16 @@ def gemm_linear_grad(dY, X, W, *, act="none", preact=None, input=True, weight=Tr
     x, w = _operand("X", X, (M, K), dtype, dev), _operand("W", W, (K, N), dtype, dev)
     z = _operand("preact", preact, (M, N), dtype, dev)
     given = (None, None, None) if out is None else out
-    dx = _made("out[0]", given[0], (M, K), dtype, dev) if input else None
-    dw = _made("out[1]", given[1], (K, N), dtype, dev) if weight else None
-    db = _made("out[2]", given[2], (N,), f32, dev) if bias else None
-    d = _made("dz", dz, (M, N), dtype, dev) if a != CF_ACT_NONE else None
-    _launch("cf_gemm_linear_grad", (dY.data_ptr(), x, w, z, _ptr(d), _ptr(dx), _ptr(dw), _ptr(db), M, N, K, dt, a), dev,
+    dx = dw = db = d = None
+    if input:
+        dx = _made("out[0]", given[0], (M, K), dtype, dev) if X is None else _made_like("out[0]", given[0], X)
+    if weight:
+        dw = _made("out[1]", given[1], (K, N), dtype, dev) if W is None else _made_like("out[1]", given[1], W)
+    if bias:
+        db = _made("out[2]", given[2], (N,), f32, dev)
+    if a != CF_ACT_NONE:
+        d = _made_like("dz", dz, dY)
+    _launch("cf_gemm_linear_grad", (dY.data_ptr(), x, w, z, _at(d), _at(dx), _at(dw), _at(db), M, N, K, dt, a), dev,
             workspace, cf_gemm_linear_workspace_size, (M, N, K), tuning)
     return dx, dw, db
 
@@ -1164,28 +1181,26 @@ def stitch_block_norms_grad(dy, dx_out, h, x_out, *, post="none", post_weight=No
     gates, vector = _gates(gate, rows), (cols,)
     ph, pxo = _operand("h", h, like, dtype, dev), _operand("x_out", x_out, like, dtype, dev)
     pdy, pdx = _operand("dy", dy, like, dtype, dev), _operand("dx_out", dx_out, like, dtype, dev)
-    pg = None if gate is None else _operand("gate", gate, (gates, cols), dtype, dev)
     given = (None,) * 7 if out is None else out
-
-    def result(i, wanted, shape=vector, kind=f32):
-        return _made(f"out[{i}]", given[i], shape, kind, dev) if wanted else None
-
-    dh = torch.empty_like(h) if given[0] is None else _made("out[0]", given[0], like, dtype, dev)
-    outs = [dh, result(1, dx, like, dtype), result(2, gate is not None, (gates, cols), dtype)]
-    vectors = []
-    for i, (name, v) in enumerate((("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
-                                   ("pre_bias", pre_bias))):
-        if v is None:
-            vectors.append(None)
-            outs.append(None)
-        else:
-            vectors.append(_operand(name, v, vector, f32, dev))
-            outs.append(result(3 + i, True))
-    _launch("cf_stitch_block_norms_grad", (pdy, pdx, ph, pxo, pg, vectors[0], vectors[1], vectors[2],
-                                           *[None if t is None else t.data_ptr() for t in outs], rows, cols, gates, po, pr,
-                                           scale, alpha, eps, dt), dev, workspace,
-            cf_stitch_block_norms_grad_workspace_size, (rows, cols), tuning)
-    return tuple(outs)
+    dh = _made_like("out[0]", given[0], h)
+    dx = _made_like("out[1]", given[1], h) if dx else None
+    pg = pw = pb = qw = dg = dpw = dpb = dqw = dqb = None
+    if gate is not None:
+        pg, dg = _operand("gate", gate, (gates, cols), dtype, dev), _made_like("out[2]", given[2], gate)
+    if post_weight is not None:
+        pw = _operand("post_weight", post_weight, vector, f32, dev)
+        dpw = _made_like("out[3]", given[3], post_weight)
+    if post_bias is not None:
+        pb, dpb = _operand("post_bias", post_bias, vector, f32, dev), _made_like("out[4]", given[4], post_bias)
+    if pre_weight is not None:
+        qw, dqw = _operand("pre_weight", pre_weight, vector, f32, dev), _made_like("out[5]", given[5], pre_weight)
+    if pre_bias is not None:
+        _operand("pre_bias", pre_bias, vector, f32, dev)
+        dqb = _made_like("out[6]", given[6], pre_bias)
+    _launch("cf_stitch_block_norms_grad", (pdy, pdx, ph, pxo, pg, pw, pb, qw, dh.data_ptr(), _at(dx), _at(dg), _at(dpw),
+                                           _at(dpb), _at(dqw), _at(dqb), rows, cols, gates, po, pr, scale, alpha, eps, dt),
+            dev, workspace, cf_stitch_block_norms_grad_workspace_size, (rows, cols), tuning)
+    return dh, dx, dg, dpw, dpb, dqw, dqb
 
 
 # ---------------------------------------------------------------------------
@@ -1244,11 +1259,11 @@ def stitch_logprobs(logits, targets=None, *, scale=1.0, top=0, entropy=True, out
     t = _operand("targets", targets, (rows,), i64, dev)
     given = (None,) * 5 if out is None else out
     lse = _made("out[1]", given[1], (rows,), f32, dev)
-    logprob = None if t is None and targets is None else _made("out[0]", given[0], (rows,), f32, dev)
-    h = _made("out[2]", given[2], (rows,), f32, dev) if entropy else None
+    logprob = None if targets is None else _made_like("out[0]", given[0], lse)
+    h = _made_like("out[2]", given[2], lse) if entropy else None
     tl = _made("out[3]", given[3], (rows, top), f32, dev) if top else None
     ti = _made("out[4]", given[4], (rows, top), i64, dev) if top else None
-    _launch("cf_stitch_logprobs", (logits.data_ptr(), t, _ptr(logprob), lse.data_ptr(), _ptr(h), _ptr(tl), _ptr(ti), rows,
+    _launch("cf_stitch_logprobs", (logits.data_ptr(), t, _at(logprob), lse.data_ptr(), _at(h), _at(tl), _at(ti), rows,
                                    vocab, apart, top, scale, dt), dev, workspace, cf_stitch_workspace_size, (rows, vocab),
             tuning)
     return logprob, lse, h, tl, ti

@@ -1488,9 +1488,8 @@ double grouped_cycles(const GroupedShape &s, int bn, bool pair) {
 bool grouped_may_pair(int kind, int bn, int64_t F) { return kind != cf::GR_SHRINK && bn >= 128 && F > 128; }
 
 // the tile width where none is asked for, and whether CTA pairs work on it
-int grouped_columns(const GroupedShape &s, bool *pair) {
+int choose_columns(const GroupedShape &s, bool *pair) {
     *pair = false;
-    if (s.kind == cf::GR_SHRINK) return shrink_columns(s.T);
     int best = 256;
     double cycles = 1e300;
     // (of equals the narrowest; WGRAD stages dY in 64-column blocks)
@@ -1505,6 +1504,28 @@ int grouped_columns(const GroupedShape &s, bool *pair) {
         }
     }
     return best;
+}
+// ... which follows from the sizes alone, so a thread keeps what it has worked out for the last few: a call asks for it
+// once for the workspace and once for each launch, and a small call takes the host longer than the GPU.
+int grouped_columns(const GroupedShape &s, bool *pair) {
+    *pair = false;
+    if (s.kind == cf::GR_SHRINK) return shrink_columns(s.T);
+    struct Known {
+        GroupedShape s{-1, 0, 0, 0, 0, 0, 0};
+        int bn = 0;
+        bool pair = false;
+    };
+    thread_local Known known[16];
+    const uint64_t h = (uint64_t(s.T) * 31 + uint64_t(s.F)) * 1000003u + uint64_t(s.C) * 17 + uint64_t(s.N) * 7 +
+                       uint64_t(s.groups) * 3 + uint64_t(s.rank) + uint64_t(s.kind) * 5;
+    Known &k = known[(h ^ h >> 7) & 15];
+    if (k.s.kind != s.kind || k.s.T != s.T || k.s.F != s.F || k.s.C != s.C || k.s.N != s.N || k.s.groups != s.groups ||
+        k.s.rank != s.rank) {
+        k.bn = choose_columns(s, &k.pair);
+        k.s = s;
+    }
+    *pair = k.pair;
+    return k.bn;
 }
 
 // pieces of tiles: two for each CTA
