@@ -1000,7 +1000,7 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
 
 // The workers' sums added in order: 32 columns a CTA, a warp every so many-th term, then the warps.  (335 terms of 1111
 // columns by eight warps 10.5 us, which is the loads one after another.)
-constexpr int kSumWarps = 32, kSumFly = 8;
+constexpr int kSumWarps = 32, kSumFly = 8, kSumSms = 152;
 __global__ void __launch_bounds__(kSumWarps * 32) block_norms_sums_kernel(const BlockNormsGradArgs a, int nsums, int gates_first) {
     __shared__ float part[kSumWarps][32];
     ptx::griddep_launch_dependents();
@@ -1254,10 +1254,14 @@ cudaError_t launch_block_norms_grad(BlockNormsGradArgs a, const BlockNormsGradPl
     int gates_first = gates <= p.workers;
     const int shared = gate && a.dgate && a.rows_per_gate > 1 ? int(std::min<int64_t>(gates, p.workers)) : 0;
     if (nsums + shared == 0) return cudaSuccess;
+    // as many warps a CTA as there is room for all CTAs at once (eight: 335 terms of 1111 columns 10.5 us, 32: 6.6; 304 of
+    // 4096 columns and eight gates the other way round)
+    const int64_t blocks = int64_t((a.cols + 31) / 32) * (nsums + shared);
+    int warps = 8;
+    while (warps < kSumWarps && blocks * warps * 2 <= int64_t(kSumSms) * 64) warps *= 2;
     void *args2[] = {&a, &nsums, &gates_first};
     return launch(reinterpret_cast<const void *>(&block_norms_sums_kernel),
-                  dim3(unsigned((a.cols + 31) / 32) * unsigned(nsums + shared)),
-                  p.workers > 8 * kSumFly * 3 ? kSumWarps * 32 : 256, 1, pdl, stream, args2);
+                  dim3(unsigned((a.cols + 31) / 32) * unsigned(nsums + shared)), warps * 32, 1, pdl, stream, args2);
 }
 
 }  // namespace cf
