@@ -19,10 +19,10 @@
 // NaN in the entropy, is raised to a low finite number as a pair too, where the running maximum shows that this changes
 // nothing; elsewhere (rows of nothing but masks) number by number.
 //
-// Top tokens: a thread also remembers its largest logit and the first window that holds it.  The k-th largest of the
-// threads' (largest, window) pairs is a bound below which no top token can lie, and only k threads have anything on the
-// bound or above it; their windows are read again (from L2), and what reaches the bound, little more than k numbers, is
-// ranked by counting.  Pairs order equal logits by window, so equal logits in any number (a masked row) change nothing.
+// Top tokens: a thread also remembers its largest logit and the first window that holds it.  A bound that k of the
+// threads' (largest, window) pairs reach is one below which no top token can lie, and where hardly more than k reach it,
+// only those threads have anything on the bound or above it: in that one window, or, where the largest of the others shows
+// it, in any.  These windows are read again, and what reaches the bound, little more than k numbers, is ranked by counting.  Pairs order equal logits by window, so equal logits in any number (a masked row) change nothing.
 // Rows made so that more than kCandidates numbers reach the bound are searched once for each of the k.
 #include <cuda_runtime.h>
 
@@ -41,6 +41,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2E = 1.4426950408889634f, kLn2F = 0.6931471805599453f;
 constexpr int kMaxThreads = 256, kMaxCluster = 8;
 constexpr int kCandidates = 1024;
+constexpr int kSlack = 8;  // threads more than top tokens that may be looked at again
 constexpr int kFly = 4;  // windows in flight
 constexpr uint32_t kInfoTarget = 0x72000000u;
 
@@ -220,56 +221,105 @@ __device__ void search_tops(const Share<kDt> &sh, int k, uint64_t *top, uint64_t
     }
 }
 
-// most: the thread's largest logit with its first window, a pair (0: none)
+// most: the thread's largest logit with its first window, a pair (0: none); second: the order of its other windows' largest
 template <int kDt>
-__device__ void find_tops(const Share<kDt> &sh, uint64_t most, int k, uint64_t *top, uint64_t *pairs, int *chosen,
-                          uint64_t *bound, int *found, int *many) {
+__device__ void find_tops(const Share<kDt> &sh, uint64_t most, uint32_t second, int k, uint64_t *top, uint64_t *pairs,
+                          uint32_t *seconds, int *chosen, uint64_t *bound, int *found, int *many) {
     const int tid = int(threadIdx.x), n = int(blockDim.x);
     pairs[tid] = most;
+    seconds[tid] = second;
     if (tid == 0) *found = 0;
     if (tid < k) top[tid] = 0;
     __syncthreads();
-    // The k largest in turn, by one warp: the largest order of all, of those that have it the lowest window.  (Every
-    // thread counting the pairs above its own took a sixth of the kernel's instructions.  Threads without a window have
-    // no pair; where fewer than k have one, everything is a candidate.)
+    // One warp looks for an order that at least k pairs reach and hardly more, halving the range that is left; where many
+    // are on the bound itself, so it does for their window.  (The k largest in turn were 3.4 us for each of the k for
+    // 4096 x 128000 bf16; every thread counting the pairs above its own took a sixth of the kernel's instructions.
+    // Threads without a window have no pair; where fewer than k have one, everything is a candidate.)
+    constexpr int kShift = kDt == CF_FP32 ? 0 : kDt == CF_FP16 ? 13 : 16;  // an order's bits that are always the same
     if (tid < 32) {
-        uint64_t mine[kMaxThreads / 32], best = 0;
+        uint32_t order_of[kMaxThreads / 32], window_of[kMaxThreads / 32], low = kAll, high = 0;
+        int have = 0;
 #pragma unroll
         for (int i = 0; i < kMaxThreads / 32; ++i) {
-            mine[i] = tid + 32 * i < n ? pairs[tid + 32 * i] : 0;
-            best = max(best, mine[i]);
+            const uint64_t p = tid + 32 * i < n ? pairs[tid + 32 * i] : 0;
+            order_of[i] = uint32_t(p >> 32) >> kShift;
+            window_of[i] = uint32_t(~p);
+            if (p == 0) continue;
+            ++have;
+            low = min(low, order_of[i]);
+            high = max(high, order_of[i]);
         }
-        int i = 0;
-        uint64_t last = 0;
-        for (; i < k; ++i) {
-            const uint32_t o = __reduce_max_sync(kAll, uint32_t(best >> 32));
-            if (o == 0) break;
-            const uint32_t at = __reduce_max_sync(kAll, uint32_t(best >> 32) == o ? uint32_t(best) : 0u);
-            last = uint64_t(o) << 32 | at;
-            if (best == last) {
-                best = 0;
+        have = __reduce_add_sync(kAll, have);
+        low = __reduce_min_sync(kAll, low);
+        high = __reduce_max_sync(kAll, high);
+        // pairs that have an order above o, or o itself and a window of at most w
+        auto count = [&](uint32_t o, uint32_t w) {
+            int c = 0;
 #pragma unroll
-                for (int j = 0; j < kMaxThreads / 32; ++j) {
-                    if (mine[j] == last) {
-                        mine[j] = 0;
-                        chosen[i] = tid + 32 * j;
+            for (int i = 0; i < kMaxThreads / 32; ++i) c += order_of[i] > o || (order_of[i] == o && window_of[i] <= w);
+            return __reduce_add_sync(kAll, c);
+        };
+        uint32_t last = kAll;
+        if (have < k) {
+            low = 0;
+        } else if (have > k + kSlack) {
+            while (low < high) {
+                const uint32_t mid = low + (high - low + 1) / 2;
+                const int c = count(mid, kAll);
+                if (c < k) {
+                    high = mid - 1;
+                } else {
+                    low = mid;
+                    have = c;
+                    if (c <= k + kSlack) break;
+                }
+            }
+            if (have > k + kSlack) {
+                uint32_t from = 0;
+                last = uint32_t(sh.w.count);
+                while (from < last) {
+                    const uint32_t mid = from + (last - from) / 2;
+                    const int c = count(low, mid);
+                    if (c < k) {
+                        from = mid + 1;
+                    } else {
+                        last = mid;
+                        if (c <= k + kSlack) break;
                     }
-                    best = max(best, mine[j]);
                 }
             }
         }
+        // from the front the windows of those that have no other one of interest, from the back the others' threads
+        int front = 0, back = 0;
+#pragma unroll
+        for (int i = 0; i < kMaxThreads / 32; ++i) {
+            const bool on = order_of[i] != 0 && (order_of[i] > low || (order_of[i] == low && window_of[i] <= last));
+            const bool more = on && seconds[tid + 32 * i] >> kShift >= low;
+            const uint32_t one = __ballot_sync(kAll, on && !more), all = __ballot_sync(kAll, more);
+            const uint32_t before = (1u << tid) - 1u;
+            if (on && !more) chosen[front + __popc(one & before)] = int(window_of[i]);
+            if (more) chosen[kLogprobsMaxTop + kSlack - 1 - back - __popc(all & before)] = tid + 32 * i;
+            front += __popc(one);
+            back += __popc(all);
+        }
         if (tid == 0) {
-            *bound = i == k ? last : 0;
-            *many = i;
+            *bound = uint64_t(low) << 32 | last;
+            many[0] = front;
+            many[1] = back;
         }
     }
     __syncthreads();
-    const int have = *many;
-    const uint64_t least = *bound;
-    const uint32_t least_order = uint32_t(least >> 32), least_window = uint32_t(~least);
+    const int ones = many[0];
+    const uint32_t least = uint32_t(*bound >> 32), last = uint32_t(*bound);
     const int steps = sh.steps() + 1;
-    for (int i = tid; i < have * steps; i += n) {
-        const int who = i / steps, w = sh.window(i - who * steps - 1, chosen[who]);
+    for (int i = tid; i < ones + many[1] * steps; i += n) {
+        int w;
+        if (i < ones) {
+            w = chosen[i];
+        } else {
+            const int who = (i - ones) / steps;
+            w = sh.window(i - ones - who * steps - 1, chosen[kLogprobsMaxTop + kSlack - 1 - who]);
+        }
         if (w >= sh.w.count) continue;
         const Pack<kDt> x = sh.w.any(w);
 #pragma unroll
@@ -277,7 +327,7 @@ __device__ void find_tops(const Share<kDt> &sh, uint64_t most, int k, uint64_t *
             const int at = sh.w.first(w) + j;
             const uint32_t o = order(x.get(j));
             if (at < 0 || at >= sh.w.vocab) continue;
-            if (least == 0 || o > least_order || (o == least_order && uint32_t(w) <= least_window)) {
+            if (o >> kShift > least || (o >> kShift == least && uint32_t(w) <= last)) {
                 const int slot = atomicAdd(found, 1);
                 if (slot < kCandidates) pairs[slot] = pair_of(o, uint32_t(at));
             }
@@ -299,14 +349,15 @@ __device__ void find_tops(const Share<kDt> &sh, uint64_t most, int k, uint64_t *
 }
 
 template <int kDt, bool kEntropy, bool kTop>
-__global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobsArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 4) logprobs_kernel(const LogprobsArgs a) {
     __shared__ Stats warp_stats[kMaxThreads / 32];
     __shared__ Stats cta_stats[kMaxCluster];
     __shared__ uint64_t pairs[kTop ? kCandidates : 1];
     __shared__ uint64_t tops[kTop ? kMaxCluster * kLogprobsMaxTop : 1];  // of the row's CTAs, in the first one
-    __shared__ int chosen[kLogprobsMaxTop];
+    __shared__ int chosen[kLogprobsMaxTop + kSlack];
     __shared__ uint64_t bound;
-    __shared__ int found, many;
+    __shared__ uint32_t seconds[kTop ? kMaxThreads : 1];
+    __shared__ int found, many[2];
     static_assert(kCandidates >= kMaxThreads, "one pair a thread");
     static_assert(sizeof(Stats) == 16 && offsetof(Stats, m) == 0 && offsetof(Stats, s) == 4 && offsetof(Stats, t) == 8,
                   "sent as a pair and a number");
@@ -335,7 +386,7 @@ __global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobsArg
     Stats st{-inf(), 0.f, 0.f};
     // the largest logit, in an order of signed numbers (a maximum's NaN is a positive one, so it is above everything; no
     // logit has the lowest number), and its first window
-    int most_order = int(0x80000000u);
+    int most_order = int(0x80000000u), second_order = int(0x80000000u);
     uint32_t most_window = 0;
     using P = Pack<kDt>;
     const uint32_t low = P::low();
@@ -349,6 +400,7 @@ __global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobsArg
             const float m = x[i].largest();
             if constexpr (kTop) {
                 const int bits = __float_as_int(m + 0.f), o = bits ^ (bits >> 31 & 0x7fffffff);
+                second_order = max(second_order, min(most_order, o));
                 if (o > most_order) {
                     most_order = o;
                     most_window = uint32_t(w + i * step);
@@ -433,15 +485,16 @@ __global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobsArg
         const int n = min(kFly, (sh.w.count - w + round - 1) / round);
         take(x, n, w, round);
     }
-    const uint64_t most =
-        most_order == int(0x80000000u)
-            ? 0
-            : pair_of(order(__int_as_float(most_order ^ (most_order >> 31 & 0x7fffffff))), most_window);
+    auto unsigned_order = [](int o) {
+        return o == int(0x80000000u) ? 0u : order(__int_as_float(o ^ (o >> 31 & 0x7fffffff)));
+    };
+    const uint64_t most = most_order == int(0x80000000u) ? 0 : pair_of(unsigned_order(most_order), most_window);
+    const uint32_t second = unsigned_order(second_order);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1)
         st.add(Stats{__shfl_xor_sync(kAll, st.m, d), __shfl_xor_sync(kAll, st.s, d), __shfl_xor_sync(kAll, st.t, d)}, s2);
     if (lane == 0) warp_stats[warp] = st;
-    if constexpr (kTop) find_tops(sh, most, a.top, tops + part * kLogprobsMaxTop, pairs, chosen, &bound, &found, &many);
+    if constexpr (kTop) find_tops(sh, most, second, a.top, tops + part * kLogprobsMaxTop, pairs, seconds, chosen, &bound, &found, many);
     __syncthreads();
     if (tid == 0) {
         for (int i = 1; i < int(blockDim.x >> 5); ++i) st.add(warp_stats[i], s2);
@@ -632,6 +685,12 @@ cudaError_t launch_logprobs(LogprobsArgs a, int sms, bool pdl, cudaStream_t stre
     const int64_t mine = (windows + cluster - 1) / cluster;
     int threads = 64;
     while (threads < 256 && threads * kFly < mine) threads *= 2;
+    // Fewer where that still fills the SMs (1024 threads each, at 64 registers): what a row costs besides its numbers, the
+    // waits of one row, then goes beside more rows' reading (4096 rows bf16, 8 top tokens: of 10000 logits 64 us with 256
+    // threads and 36 with 64, of 32003 95 and, with 128, 78).  Not below two threads for each of a thread's windows, or
+    // more threads have several windows of interest (128000 logits: 201 us with 256 threads, 243 with 64).
+    while (threads > 64 && a.rows * cluster * (threads / 2) * 5 >= int64_t(sms) * 1024 * 4 && mine <= threads / 2 * (threads / 4))
+        threads /= 2;
     a.cluster = cluster;
     const bool entropy = a.entropy != nullptr, top = a.top > 0;
     const void *fn = a.dtype == CF_BF16   ? forward_kernel<CF_BF16>(entropy, top)
