@@ -43,17 +43,25 @@ struct Group {
     float *slots;   // two halves of `half` numbers, one for every second exchange
     int half;
     int turn;
+    float4 *means;             // LayerNorm in the forward pass: its warps' statistics, two halves
+    float n_warp, inv_warp;  // and the columns that the warp has
 };
 
-// v summed over the row (of one CTA); every thread of the row gets the same bits.  The slots behind the last warp's, up
-// to a multiple of four, hold zeros.
-__device__ __forceinline__ float row_sum(Group &g, float v) {
+// v summed over the threads of the row in this warp
+__device__ __forceinline__ float warp_sum(const Group &g, float v) {
     if (g.lanes >= 32) {
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
     } else {
         for (int d = g.lanes >> 1; d >= 1; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
     }
+    return v;
+}
+
+// v summed over the row (of one CTA); every thread of the row gets the same bits.  The slots behind the last warp's, up
+// to a multiple of four, hold zeros.
+__device__ __forceinline__ float row_sum(Group &g, float v) {
+    v = warp_sum(g, v);
     if (g.warps == 1) return v;
     float *const slots = g.slots + (g.turn & 1) * g.half;
     ++g.turn;
@@ -516,39 +524,90 @@ __device__ __forceinline__ float reciprocal_root(float v) {
     return fabsf(v) > 1e-30f && v < 1e30f ? fmaf(0.5f * r, e, r) : r;
 }
 
+// c added to the columns that there are, the others are zero
+template <bool kVec, int kP>
+__device__ __forceinline__ void add_live(Two (&x)[kP][4], float c, const Columns<kVec> &cols) {
+    const Two k(c);
+#pragma unroll
+    for (int p = 0; p < kP; ++p)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[p][j] = x[p][j] + k;
+    if (cols.live(kP - 1, 7)) return;
+#pragma unroll
+    for (int p = 0; p < kP; ++p)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[p][j] = live_two(x[p][j], cols, p, j);
+}
+
 // The reciprocal root of one norm's row held in x (1: no norm), which loses its mean where the norm takes it.
-// kFull: it may be a LayerNorm.
+// kFull: it may be a LayerNorm.  Its squares are taken about the mean of the warp's columns, and one exchange brings every
+// warp's mean and squares: with n of them, sums s and q, about the mean c of the first warp
+//     sum (x - m)^2 = sum q + n (s / n - c)^2  -  N (m - c)^2,
+// where the first sum is at most N / n times the difference (the first warp's n), so no more is lost than that of 2^-24.
+// (A mean first, then the squares, two exchanges: 8192 x 4096 bf16 with two LayerNorms 75 us.)
 template <bool kVec, int kP, bool kFull>
 __device__ __forceinline__ float spread(Group &g, int norm, Two (&x)[kP][4], const Columns<kVec> &cols, float inv_n,
                                         float eps) {
     if (norm == CF_NORM_NONE) return 1.f;
+    float mean = 0.f;
     if (kFull && norm == CF_NORM_LAYER) {
         Two s(0.f);
 #pragma unroll
         for (int p = 0; p < kP; ++p)
 #pragma unroll
             for (int j = 0; j < 4; ++j) s = s + x[p][j];
-        const Two mean(-row_sum(g, s.sum()) * inv_n);
-#pragma unroll
-        for (int p = 0; p < kP; ++p)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[p][j] = live_two(x[p][j] + mean, cols, p, j);
+        mean = warp_sum(g, s.sum()) * g.inv_warp;
+        add_live<kVec, kP>(x, -mean, cols);
     }
     Two s(0.f);
 #pragma unroll
     for (int p = 0; p < kP; ++p)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s = fma(x[p][j], x[p][j], s);
-    return reciprocal_root(fmaf(row_sum(g, s.sum()), inv_n, eps));
+    float q = s.sum();
+    if (kFull && norm == CF_NORM_LAYER) {
+        q = warp_sum(g, q);
+        if (g.warps > 1) {
+            float4 *const slots = g.means + (g.turn & 1) * g.warps;
+            ++g.turn;
+            if ((threadIdx.x & 31) == 0) slots[g.warp] = make_float4(mean, q, g.n_warp, 0.f);
+            ptx::named_bar_sync(g.bar, uint32_t(g.lanes));
+            const float c = slots[0].x;
+            float off = 0.f;  // N (m - c)
+            q = 0.f;
+#pragma unroll 4
+            for (int i = 0; i < g.warps; ++i) {
+                const float4 w = slots[i];
+                const float d = w.x - c;
+                off = fmaf(w.z, d, off);
+                q += fmaf(w.z * d, d, w.y);
+            }
+            off *= inv_n;
+            q = fmaf(-off * off, 1.f / inv_n, q);
+            q = q < 0.f ? 0.f : q;  // (a NaN stays)
+            add_live<kVec, kP>(x, mean - (c + off), cols);
+        }
+    } else {
+        q = row_sum(g, q);
+    }
+    return reciprocal_root(fmaf(q, inv_n, eps));
+}
+
+// Bytes of what the forward pass's threads keep in shared memory
+__host__ __device__ constexpr int forward_kept_bytes(bool bias, int pieces, int threads) {
+    return threads * pieces * 32 * (pieces == 4 ? 1 : bias ? 2 : 0);
 }
 
 // kP pieces a thread.  kFull: LayerNorms or biases, too.  A worker takes a stretch of neighbouring rows, as in the gradient.
 template <int kDt, int kMode, int kP, bool kFull>
-__global__ void __maxnreg__(kP == 4 ? 64 : 128) block_norms_kernel(const BlockNormsArgs a) {
+__global__ void __maxnreg__(kP == 4 && !is_bulk(kMode) ? 64 : 128) block_norms_kernel(const BlockNormsArgs a) {
     constexpr bool kVec = is_vec(kMode);
-    extern __shared__ __align__(128) uint8_t ring_smem[];
+    constexpr bool kAside = kP == 4;
+    extern __shared__ __align__(128) uint8_t smem[];  // what is kept there, the ring
+    uint8_t *const ring_smem = smem + forward_kept_bytes(a.post_bias || a.pre_bias, kP, int(blockDim.x));
     __shared__ uint32_t abort;
     if (threadIdx.x == 0) abort = 0u;
+    __shared__ float4 means[kFull ? 2 * 32 : 1];           // of up to 32 warps in all
     __shared__ __align__(16) float slots[2 * 32 + 8 * 8];  // of each of up to 8 groups of warps, rounded up to four
     for (int i = threadIdx.x; i < int(sizeof(slots) / 4); i += blockDim.x) slots[i] = 0.f;
     ptx::griddep_launch_dependents();
@@ -566,9 +625,19 @@ __global__ void __maxnreg__(kP == 4 ? 64 : 128) block_norms_kernel(const BlockNo
     g.half = (g.warps + 3) & ~3;
     g.slots = slots + group * 2 * g.half;
     g.turn = 0;
+    g.means = means + (kFull ? group * 2 * g.warps : 0);
     const Columns<kVec> cols{g.t, a.lanes, 0, a.cols};
     const int groups = int(blockDim.x) / a.lanes;
     const float inv_n = 1.f / float(a.cols);
+    if constexpr (kFull) {
+        float n_warp = 0.f;
+#pragma unroll
+        for (int p = 0; p < kP; ++p)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) n_warp += cols.live(p, j) ? 1.f : 0.f;
+        g.n_warp = warp_sum(g, n_warp);
+        g.inv_warp = 1.f / fmaxf(g.n_warp, 1.f);
+    }
     const Two alpha(a.x ? a.alpha : 0.f);
     const int64_t mine = int64_t(blockIdx.x) * groups + group;
     const int first = int(min(a.rows, mine * a.chunk)), last = int(min(a.rows, int64_t(first) + a.chunk));
@@ -581,29 +650,74 @@ __global__ void __maxnreg__(kP == 4 ? 64 : 128) block_norms_kernel(const BlockNo
     __syncthreads();
     ring.start();
 
-    Two w1[kP][4], w2[kP][4];  // Post's weight times the gate; Pre's
-    int gate_end = 0;          // the first row behind the rows of the gate in w1
+    Two w1[kAside ? 1 : kP][4], w2[kP][4];  // Post's weight times the gate; Pre's
+    int gate_end = 0;                       // the first row behind the rows of the gate in w1
+    // Kept in shared memory, which no other thread looks at: with four pieces a thread w1, else the biases, Post's times
+    // scale and gate (read from memory at each row, 8192 x 4096 bf16 took 89 us).
+    float4 *const kept = reinterpret_cast<float4 *>(smem) + threadIdx.x;
+    auto keep = [&](int k, int p, const Two (&v)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            const float2 l = v[j].parts(), h = v[j + 1].parts();
+            kept[((k * kP + p) * 2 + j / 2) * int(blockDim.x)] = make_float4(l.x, l.y, h.x, h.y);
+        }
+    };
+    auto get_kept = [&](int k, int p, Two (&v)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            const float4 q = kept[((k * kP + p) * 2 + j / 2) * int(blockDim.x)];
+            v[j] = Two(q.x, q.y), v[j + 1] = Two(q.z, q.w);
+        }
+    };
     auto take_gate = [&](int of, bool here) {
         gate_end = int((uint32_t(of) + 1u) * a.rows_per_gate);
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
-            load_vector<kVec>(w1[p], a.post_weight, 1.f, cols, p);
-            if (!a.gate) continue;
-            Piece<kDt> q;
-            if (here) {
-                ring.take(q, 2, p);
-            } else {
-                q.zero();
-                load_piece<kDt, kVec>(q, static_cast<const E *>(a.gate) + size_t(of) * a.cols, cols, p, true);
-            }
-            Two k[4];
-            q.unpack(k);
+            Two w[4], k[4];
+            load_vector<kVec>(w, a.post_weight, 1.f, cols, p);
+            if (a.gate) {
+                Piece<kDt> q;
+                if (here) {
+                    ring.take(q, 2, p);
+                } else {
+                    q.zero();
+                    load_piece<kDt, kVec>(q, static_cast<const E *>(a.gate) + size_t(of) * a.cols, cols, p, true);
+                }
+                q.unpack(k);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w1[p][j] = w1[p][j] * k[j];
+                for (int j = 0; j < 4; ++j) w[j] = w[j] * k[j];
+            }
+            if constexpr (kAside) {
+                keep(0, p, w);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w1[p][j] = w[j];
+                if (kFull && a.post_bias && !here) {
+                    load_vector<kVec>(w, a.post_bias, 0.f, cols, p);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = w[j] * Two(a.scale) * (a.gate ? k[j] : Two(1.f));
+                    keep(0, p, w);
+                }
+            }
         }
     };
 #pragma unroll
-    for (int p = 0; p < kP; ++p) load_vector<kVec>(w2[p], a.pre_weight, 1.f, cols, p);
+    for (int p = 0; p < kP; ++p) {
+        load_vector<kVec>(w2[p], a.pre_weight, 1.f, cols, p);
+        if (kFull && !kAside) {
+            Two b[4];
+            if (a.pre_bias) {
+                load_vector<kVec>(b, a.pre_bias, 0.f, cols, p);
+                keep(1, p, b);
+            }
+            if (a.post_bias && a.gates_along) {  // (the gate is in the ring, row by row)
+                load_vector<kVec>(b, a.post_bias, 0.f, cols, p);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] = b[j] * Two(a.scale);
+                keep(0, p, b);
+            }
+        }
+    }
     if (!a.gates_along) take_gate(int(uint32_t(first) / a.rows_per_gate < uint32_t(a.gates) ? uint32_t(first) / a.rows_per_gate : 0u), false);
     E *xo = static_cast<E *>(a.x_out), *yo = static_cast<E *>(a.y);
     if (xo) xo += size_t(first) * a.cols;
@@ -631,11 +745,17 @@ __global__ void __maxnreg__(kP == 4 ? 64 : 128) block_norms_kernel(const BlockNo
             ring.take(q, 1, p);
             q.unpack(u);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[p][j] = fma(x[p][j] * root, w1[p][j], u[j] * alpha);
-            if (kFull && a.post_bias) {  // scale gate bias; the gate from memory again
-                Two b[4];
-                load_vector<kVec>(b, a.post_bias, 0.f, cols, p);
-                if (a.gate) {
+            for (int j = 0; j < 4; ++j) u[j] = u[j] * alpha;
+            if (kFull && a.post_bias) {  // scale gate bias
+                Two b[4], k[4];
+                if constexpr (kAside) {  // (the bias, and a gate that is not in the ring, from memory again)
+                    load_vector<kVec>(b, a.post_bias, 0.f, cols, p);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) b[j] = b[j] * Two(a.scale);
+                } else {
+                    get_kept(0, p, b);
+                }
+                if (a.gate && (kAside || a.gates_along)) {
                     if (a.gates_along) {
                         ring.take(q, 2, p);
                     } else {
@@ -644,12 +764,21 @@ __global__ void __maxnreg__(kP == 4 ? 64 : 128) block_norms_kernel(const BlockNo
                             q, static_cast<const E *>(a.gate) + size_t(gate_end / a.rows_per_gate - 1) * a.cols, cols, p,
                             on);
                     }
-                    q.unpack(u);
+                    q.unpack(k);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) b[j] = b[j] * u[j];
+                    for (int j = 0; j < 4; ++j) b[j] = b[j] * k[j];
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[p][j] = fma(b[j], Two(a.scale), x[p][j]);
+                for (int j = 0; j < 4; ++j) u[j] = u[j] + b[j];
+            }
+            if constexpr (kAside) {
+                Two w[4];
+                get_kept(0, p, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[p][j] = fma(x[p][j] * root, w[j], u[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[p][j] = fma(x[p][j] * root, w1[p][j], u[j]);
             }
             if (xo) store_piece<kDt, kVec>(xo, x[p], cols, p, on);
         }
@@ -666,12 +795,14 @@ __global__ void __maxnreg__(kP == 4 ? 64 : 128) block_norms_kernel(const BlockNo
         ring.release(1);
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
-            Two b[4];
-            if constexpr (kFull) load_vector<kVec>(b, a.pre_bias, 0.f, cols, p);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[p][j] = x[p][j] * root;
-                x[p][j] = kFull ? fma(x[p][j], w2[p][j], b[j]) : x[p][j] * w2[p][j];
+            for (int j = 0; j < 4; ++j) x[p][j] = x[p][j] * root * w2[p][j];
+            if (kFull && a.pre_bias) {
+                Two b[4];
+                if constexpr (kAside) load_vector<kVec>(b, a.pre_bias, 0.f, cols, p);
+                else get_kept(1, p, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[p][j] = x[p][j] + b[j];
             }
             store_piece<kDt, kVec>(yo, x[p], cols, p, on);
         }
@@ -1135,12 +1266,15 @@ cudaError_t allow_smem(const void *fn, int *own) {  // own: the kernel's static 
 template <int kDt>
 const void *forward_kernel(int mode, bool full, int pieces) {
     if (mode == LOOSE)
-        return pieces == 1   ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, LOOSE, 1, true>)
-                             : reinterpret_cast<const void *>(&block_norms_kernel<kDt, LOOSE, 4, true>);
-    if (mode == SHIFTED) return reinterpret_cast<const void *>(&block_norms_kernel<kDt, SHIFTED, 2, true>);
+        return pieces == 1 ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, LOOSE, 1, true>)
+                           : reinterpret_cast<const void *>(&block_norms_kernel<kDt, LOOSE, 4, true>);
+    if (mode == SHIFTED)
+        return pieces == 2 ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, SHIFTED, 2, true>)
+                           : reinterpret_cast<const void *>(&block_norms_kernel<kDt, SHIFTED, 4, true>);
     if (mode == SHORT)
         return pieces == 1 ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, SHORT, 1, true>)
                            : reinterpret_cast<const void *>(&block_norms_kernel<kDt, SHORT, 4, true>);
+    if (pieces == 4) return reinterpret_cast<const void *>(&block_norms_kernel<kDt, WIDE, 4, true>);
     return full ? reinterpret_cast<const void *>(&block_norms_kernel<kDt, WIDE, 2, true>)
                 : reinterpret_cast<const void *>(&block_norms_kernel<kDt, WIDE, 2, false>);
 }
@@ -1154,7 +1288,11 @@ const void *grad_kernel(int mode, bool cluster, bool gate, bool full, int pieces
     if (mode == SHIFTED)
         return cluster ? grad_of<kDt, SHIFTED, true, true, true, 1>() : grad_of<kDt, SHIFTED, false, true, true, 1>();
     if (mode == SHORT) return grad_of<kDt, SHORT, false, true, true, 1>();
-    if (cluster) return full ? grad_of<kDt, WIDE, true, true, true, 1>() : grad_of<kDt, WIDE, true, true, false, 1>();
+    if (cluster) {
+        if constexpr (kDt != CF_FP32)
+            if (pieces == 2) return grad_of<kDt, WIDE, true, true, false, 2>();
+        return full ? grad_of<kDt, WIDE, true, true, true, 1>() : grad_of<kDt, WIDE, true, true, false, 1>();
+    }
     if (full) return gate ? grad_of<kDt, WIDE, false, true, true, 1>() : grad_of<kDt, WIDE, false, false, true, 1>();
     if constexpr (kDt != CF_FP32)
         if (pieces == 2)
@@ -1183,14 +1321,18 @@ cudaError_t launch_block_norms(BlockNormsArgs a, bool vec, int sms, bool pdl, cu
     // a thread's pieces: two, so that what a row costs besides its numbers is shared by more of them
     const int per = pieces < 64 ? 1 : pieces <= 1024 ? 2 : 4;
     a.lanes = round_lanes((pieces + per - 1) / per);
-    const int mode = per == 2 ? (vec ? WIDE : SHIFTED) : vec ? SHORT : LOOSE;
+    // (above 16384 columns it takes 1024 threads, which have 64 registers, and no ring fits)
+    const bool bulk = per > 1 && a.lanes <= 512;
+    const int mode = vec ? (bulk ? WIDE : SHORT) : bulk ? SHIFTED : LOOSE;
     const int groups = std::max(1, 256 / a.lanes), threads = groups * a.lanes;
     // a stretch of rows for each group of threads
     const int per_sm = std::max(1, kForwardThreads / threads);
     int64_t ctas = std::min<int64_t>((a.rows + groups - 1) / groups, int64_t(sms) * per_sm);
     a.chunk = int((a.rows + ctas * groups - 1) / (ctas * groups));
     ctas = (a.rows + int64_t(a.chunk) * groups - 1) / (int64_t(a.chunk) * groups);
-    a.gates_along = a.gate && a.rows_per_gate == 1 && has_ring(a.dtype, mode, per);
+    const int kept = forward_kept_bytes(a.post_bias || a.pre_bias, per, threads);
+    // (of fp32, three rows of more than 8192 columns do not fit)
+    a.gates_along = a.gate && a.rows_per_gate == 1 && has_ring(a.dtype, mode, per) && !(per == 4 && a.dtype == CF_FP32);
     const bool full = a.post == CF_NORM_LAYER || a.pre == CF_NORM_LAYER || a.post_bias || a.pre_bias;
     const void *fn = a.dtype == CF_BF16   ? forward_kernel<CF_BF16>(mode, full, per)
                      : a.dtype == CF_FP16 ? forward_kernel<CF_FP16>(mode, full, per)
@@ -1198,7 +1340,8 @@ cudaError_t launch_block_norms(BlockNormsArgs a, bool vec, int sms, bool pdl, cu
     int own;
     const cudaError_t e = allow_smem(fn, &own);
     if (e != cudaSuccess) return e;
-    const int smem = plan_ring(&a.ring, a.dtype, mode, a.gates_along ? 3 : 2, per, a.lanes, threads, per_sm, own);
+    const int smem =
+        kept + plan_ring(&a.ring, a.dtype, mode, a.gates_along ? 3 : 2, per, a.lanes, threads, per_sm, own + kept);
     void *args[] = {&a};
     return launch(fn, dim3(unsigned(ctas)), threads, 1, pdl, stream, args, smem);
 }
@@ -1206,7 +1349,9 @@ cudaError_t launch_block_norms(BlockNormsArgs a, bool vec, int sms, bool pdl, cu
 BlockNormsGradPlan plan_block_norms_grad(int64_t rows, int64_t cols, int sms, bool lean, int dtype) {
     BlockNormsGradPlan p;
     const int64_t n = (cols + 7) / 8;
-    p.pieces = lean && dtype != CF_FP32 && n >= 64 && n <= 1024 ? 2 : 1;  // (of fp32, two are too many registers)
+    // (of fp32, two are too many registers; where a cluster has one row at most, more CTAs finish sooner: 1 x 16384 bf16
+    // 10 us with one, 14 with two, 2048 x 16384 239 and 109)
+    p.pieces = lean && dtype != CF_FP32 && n >= 64 && (n <= 1024 || rows * ((n + 511) / 512) > sms) ? 2 : 1;
     p.cluster = int((n + 512 * p.pieces - 1) / (512 * p.pieces));
     p.lanes = round_lanes((n + p.cluster * p.pieces - 1) / (p.cluster * p.pieces));
     const int groups = p.cluster > 1 ? 1 : std::max(1, 256 / p.lanes);
