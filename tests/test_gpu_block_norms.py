@@ -235,6 +235,59 @@ def test_gradient(shape, norms, dt):
         assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, same))
 
 
+# more rows than CTAs, of more than 8192 columns: several rows of a ring for each of them
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("norms", [("rms", "rms"), ("layer", "layer")], ids="-".join)
+@pytest.mark.parametrize("shape", [(400, 8200), (330, 10001)], ids=str)
+def test_wide_rows(shape, norms, dt):
+    ws = cf.new_workspace(cf.cf_stitch_block_norms_grad_workspace_size(*shape))
+    for gates, shift in ((0, False), (shape[0], True), (shape[0] // 10, False), (1, True)):
+        c, v, gate, kw = _case(shape, dt, *norms, gates, shift)
+        dv, g = {k: _dev(a) for k, a in v.items()}, _dev(gate, dt)
+        xo, y = cf.stitch_block_norms(_dev(c["h"], dt), _dev(c["x"], dt), gate=g, **dv, **kw)
+        ref_x, ref_y = oracle.block_norms(c["h"], c["x"], gate=gate, **v, **kw)
+        e = _forward_bounds(c, v, gate, kw)
+        _check(xo, ref_x, e, dt, "x_out")
+        _check(y, ref_y, _normed(norms[1], ref_x, v.get("pre_weight"), v.get("pre_bias"), e) + 2 * U * np.abs(ref_y), dt,
+               "y")
+        x16 = _round(ref_x, dt)
+        dy = _round(_rng(5).standard_normal(shape), dt)
+        got = cf.stitch_block_norms_grad(_dev(dy, dt), None, _dev(c["h"], dt), _dev(x16, dt), gate=g, **dv, **kw,
+                                         workspace=ws)
+        okw = {k: a for k, a in v.items() if k != "pre_bias"}
+        ref = oracle.block_norms_grad(dy, None, c["h"], x16, gate=gate, **okw, **kw)
+        bounds = _grad_bounds(dy, None, c, x16, v, gate, kw)
+        for k, t in zip(KEYS, got):
+            if t is not None:
+                _check(t, ref[k], bounds[k], dt if k in ("h", "x", "gate") else "fp32", f"d{k} {gates} {shift}")
+
+
+# A LayerNorm whose mean is far from zero, whose parts have means of their own, and whose first part lies far from the
+# others: squares about the mean of a part, put together, lose nothing of the small ones.
+@pytest.mark.parametrize("N", [64, 300, 2056, 4096, 8192, 9999, 16384, 32768])
+def test_means_of_parts(N):
+    r = _rng(N)
+    h = r.standard_normal((12, N))
+    h[0] += 1000.0
+    h[1] += 100.0 * (np.arange(N) // 256)
+    h[2, :min(512, N // 2)] += 3000.0
+    h[3, -min(512, N // 2):] -= 3000.0
+    h[4] = 5.0 + 1e-3 * h[4]
+    h[5, 0] = 1e4
+    h[6, -1] = 1e4
+    h[7] *= 1e-4
+    h = h.astype(np.float32)
+    x = np.zeros_like(h)
+    w, b = r.standard_normal((2, N)).astype(np.float32)
+    xo, y = cf.stitch_block_norms(_dev(h), _dev(x), post_weight=_dev(w), post_bias=_dev(b), pre_weight=_dev(w),
+                                  pre_bias=_dev(b), post="layer", pre="layer", eps=EPS)
+    ref_x, ref_y = oracle.block_norms(h, x, post_weight=w, post_bias=b, pre_weight=w, pre_bias=b, post="layer",
+                                      pre="layer", eps=EPS)
+    e = _normed("layer", h, w, b, 0.0) + 4 * U * np.abs(ref_x)
+    _check(xo, ref_x, e, "fp32", "x_out")
+    _check(y, ref_y, _normed("layer", ref_x, w, b, e) + 2 * U * np.abs(ref_y), "fp32", "y")
+
+
 def test_nans_stay_in_their_rows():
     torch = torch_cuda()
     c, v, gate, kw = _case((40, 200), "bf16", "layer", "rms", 8, True)

@@ -197,6 +197,24 @@ def test_gradient(shape, dt, act):
         assert torch.equal(part[i], got[i]) and sum(p is not None for p in part) == 1
 
 
+# many rows: tiles of CTA pairs that are cut to fill the last round
+@pytest.mark.parametrize("shape", [(8191, 128, 2048), (5003, 520, 2056), (8191, 2048, 128)], ids=str)
+def test_many_rows(shape):
+    X, W, b, R = _case(shape, "bf16")
+    torch = torch_cuda()
+    z = torch.empty(R.shape, dtype=torch.bfloat16, device="cuda")
+    y = _forward(X, W, b, R, "silu", "bf16", preact=z)
+    _check_forward(y, z, X, W, b, R, "silu", "bf16")
+    X, W, Z, dY = _grad_case(shape, "bf16")
+    M, K, N = shape
+    dX, dW, db = cf.gemm_linear_grad(_dev(dY, "bf16"), _dev(X, "bf16"), _dev(W, "bf16"))
+    rX, rW, rb = oracle.gemm_linear_grad(dY, X, W)
+    size = np.abs(dY)
+    _check(_host(dX), rX, N * ACC * (size @ np.abs(W).T), HALF["bf16"], TINY["bf16"], "dX")
+    _check(_host(dW), rW, M * ACC * (np.abs(X).T @ size), HALF["bf16"], TINY["bf16"], "dW")
+    _check(_host(db), rb, M * ACC * size.sum(0), 2.0 ** -24, 0.0, "dbias")
+
+
 def test_no_rows():
     torch = torch_cuda()
     X, W = torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(64, 72, dtype=torch.bfloat16,

@@ -190,6 +190,35 @@ def test_large_logits_in_few_threads(top):
         _check([None if g is None else g[pick] for g in got], zr[pick], None, 1.0, top, dt)
 
 
+# enough rows to fill the SMs with few threads each
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("kind", ["plain", "masked", "coarse"])
+@pytest.mark.parametrize("shape", [(4200, 70, 0), (2500, 4001, 0), (1100, 9003, 5), (1000, 30000, 0)], ids=str)
+def test_many_rows(shape, kind, dt):
+    z, t = _case(shape, dt, kind)
+    for top in (1, 6, 32):
+        _check(cf.stitch_logprobs(_dev(z, dt, shape[2]), _i64(t), top=top), z, t, 1.0, top, f"{top}")
+
+
+# The threads that hold the top tokens have several windows of them, or as many others as good lie behind them.
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("top", [1, 4, 5, 32])
+def test_equal_logits_on_the_bound(top, dt):
+    r = _rng(top)
+    z = _round(r.standard_normal((6, 20011)), dt)
+    z[0, r.permutation(20011)[:700]] = 9.0
+    z[1, ::977] = 9.0
+    z[1, 5::977] = 9.5
+    z[2, 8000:8000 + 64] = 9.0
+    z[3, r.permutation(20011)[:2500]] = 9.0
+    z[4] = -5.0
+    z[4, -1] = -4.0
+    z[5] = -np.inf
+    z[5, 19990:19990 + top] = -1.0
+    t = r.integers(0, 20011, 6)
+    _check(cf.stitch_logprobs(_dev(z, dt), _i64(t), top=top), z, t, 1.0, top)
+
+
 def test_targets_out_of_range():
     z, _ = _case((4, 100, 0), "fp32", "plain")
     ws = cf.new_workspace(cf.cf_stitch_workspace_size(4, 100))
