@@ -893,9 +893,10 @@ CF_API cf_status cf_gemm_linear_grad_ex(const void *dY, const void *X, const voi
  * cf_stitch_block_norms_grad_workspace_size(), 16-byte aligned there; zeroed
  * once, as for every call.  One workspace may serve these calls, the dense
  * layer's, the grouped ones' and the log probabilities' in turn.
- * Tuning fields used (_ex): disable_pdl, timeout_us, extra_arrivals (TEST HOOK:
- * > 0 makes the wait for a row run out, of rows in bulk copies: cols of a
- * multiple of 8 from 512 to 8192, the gradient from 256 on, all 16-byte aligned). */
+ * Tuning fields used (_ex): disable_pdl, timeout_us, stages (rows on their way in
+ * shared memory, 1 to 8, fewer where they do not fit; 0: three), extra_arrivals
+ * (TEST HOOK: > 0 makes the wait for a row run out, of rows in bulk copies: cols
+ * from 505 to 16384, the gradient from 129 on). */
 CF_API size_t cf_stitch_block_norms_grad_workspace_size(int64_t rows, int64_t cols);
 
 CF_API cf_status cf_stitch_block_norms(const void *h, const void *x, const void *gate, const float *post_weight,

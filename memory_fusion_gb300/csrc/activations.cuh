@@ -29,12 +29,6 @@ __device__ __forceinline__ float gelu_slope(float z) {
 // and so p; an infinite z times p = 0 would be a NaN where the limit is 0.)
 __device__ __forceinline__ float silu_p(float z) { return __fdividef(1.f, 1.f + ptx::ex2_approx(-1.4426950408889634f * z)); }
 __device__ __forceinline__ float silu(float z) { return z < -120.f ? 0.f : z * silu_p(z); }
-__device__ __forceinline__ float silu_slope(float z) {
-    const float c = fabsf(z) > 120.f ? copysignf(120.f, z) : z;
-    const float p = silu_p(c);
-    return fmaf(c * p, 1.f - p, p);
-}
-
 // act (cf_activation) of every value of an array, floats or their bits; one branch for all of them
 __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(uint32_t v) { return __uint_as_float(v); }

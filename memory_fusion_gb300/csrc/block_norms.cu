@@ -10,7 +10,11 @@
 // writes dh and dx.  A row is held in registers by as many threads as it has pieces of 8 columns (the forward pass: or
 // half or a quarter as many); short rows share a warp, wide ones in the gradient are split over a cluster's CTAs.  Sums
 // over a row go by shuffles, then through shared memory, of every CTA of the cluster where there are several.  A norm's
-// mean is taken before its squares, so nothing cancels.
+// squares are taken about a mean, never about zero, so nothing cancels.
+// 16384 x 4096 bf16, RMSNorms, eight gates: forward 94 us (5.7 TB/s), gradient 147 (5.5; 138 and 9 for the sums).  What is
+// left are the waits of a row's exchanges, one after another, and the instructions between them.  With LayerNorms and biases
+// 1.6 times that.  Rows that start anywhere (odd widths of 16-bit numbers) are read from shared memory and stored number
+// by number: about 2 times (forward) and 2.8 times (gradient) what aligned ones take.
 //
 // The gradients of the weights are sums over all rows: a thread keeps its columns' sums in registers over a stretch of
 // neighbouring rows, and a second, small launch adds the stretches in order (so equal calls give equal bits).  A gate

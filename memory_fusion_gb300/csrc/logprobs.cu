@@ -14,7 +14,8 @@
 // Rows start anywhere: a row is cut at 16-byte boundaries of its memory into windows, the first and last of which may be
 // partial and are read number by number.
 //
-// What stands between the loads and HBM's rate is the instructions: 17 a number at first (322 us for 4096 x 128000 bf16).
+// What stands between the loads and HBM's rate is the instructions: 17 a number at first (322 us for 4096 x 128000 bf16), 10
+// now (200 us with eight top tokens, 5.2 TB/s; without top tokens 163, 6.4 TB/s; the gradient 308, the copy's rate).
 // So numbers are worked on in pairs, maxima are taken of 16-bit pairs as they are, and -inf, whose 0 times -inf would be a
 // NaN in the entropy, is raised to a low finite number as a pair too, where the running maximum shows that this changes
 // nothing; elsewhere (rows of nothing but masks) number by number.

@@ -83,10 +83,6 @@ struct Piece {
         }
         pack(f);
     }
-    __device__ __forceinline__ void unpack(float (&x)[8]) const {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = get(j);
-    }
     __device__ __forceinline__ void pack(const float (&x)[8]) {
 #pragma unroll
         for (int j = 0; j < 8; j += (kDt == CF_FP32 ? 1 : 2)) {
