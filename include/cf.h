@@ -883,8 +883,8 @@ CF_API cf_status cf_gemm_linear_grad_ex(const void *dY, const void *X, const voi
  *   dpost_weight ... dpre_bias may be.  dh and dx may be dy, dx_out, h or x_out.
  *   post_bias is read for dgate alone.  Without dy, pre and x_out are not read.
  * Sums over a row and over rows are fp32, in an order that depends on the sizes
- * alone: equal calls give equal bits.  NaNs stay in their rows (and their
- * columns' sums).
+ * and on whether all pointers are 16-byte aligned: equal calls give equal bits.
+ * NaNs stay in their rows (and their columns' sums).
  * Supported: cols in 0..32768, rows in 0..2^31 - 512 (0 of either is a no-op; a
  * gradient of no rows writes zeros to the sums), dtype bf16, fp16 or fp32,
  * pointers aligned to their element (16 bytes, with cols a multiple of 8, is

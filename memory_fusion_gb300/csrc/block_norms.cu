@@ -842,7 +842,7 @@ __host__ __device__ constexpr int kept_bytes(bool gate, bool full, int pieces, i
 //     d  = dx' + r2 (g2 - mean(g2) - x^ mean(g2 x^)),
 //     sum w1 d h^ = r1 (sum w1 hc dx' + r2 (sum w1 hc g2 - mean(g2) sum w1 hc - r2 mean(g2 x^) sum w1 hc xc)),
 // so one exchange between the threads serves where three would follow one another (16384 x 4096 bf16: 287 us with
-// three).  A LayerNorm's means come one exchange before.
+// three).  A LayerNorm's means come one exchange before: that of the row before, where the ring holds two rows.
 // (Rows ahead kept in registers left no room for the sums: 16384 x 4096 bf16 172 us, 158 with the ring in shared memory.)
 // kFull: LayerNorms or biases, too.  kGate: a gate, whose rows' sums are closed where the next gate begins.
 // kP pieces a thread, up to 512 threads an SM with 128 registers: two where those hold them (not with biases' sums), so
@@ -960,6 +960,9 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
         }
     }
     size_t at = first < last ? size_t(first) * a.cols : 0;  // where the row in hand lies
+    constexpr bool kAhead = kFull && kMode == WIDE;
+    const bool ahead = kAhead && a.ring.depth >= 2 && (lh || lx);
+    Two mh(0.f), mx(0.f);  // less the LayerNorms' means
     for (int i = 0; i < turns; ++i) {
         const int r = first + i;
         const bool on = kWide || r < last;
@@ -973,8 +976,8 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
         ring.next();
         // columns 2j and the next of the k-th matrix's row
         auto pair = [&](int k, int p, int j) { return Two(raw[k][p].get(2 * j), raw[k][p].get(2 * j + 1)); };
-        Two mh(0.f), mx(0.f);
-        if (lh || lx) {
+        if constexpr (!kAhead) mh = mx = Two(0.f);  // (nothing is kept from a row to the next)
+        if ((lh || lx) && (!ahead || i == 0)) {
             Two s(0.f), t(0.f);
 #pragma unroll
             for (int p = 0; p < kP; ++p)
@@ -1017,6 +1020,21 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
 #pragma unroll
             for (int k = 0; k < kV; ++k) v[k] = k < kSums ? s[k < kSums ? k : 0].sum() : 0.f;
         }
+        if (kAhead && ahead && i + 1 < turns) {
+            Two s(0.f), t(0.f);
+            ring.turn();
+#pragma unroll
+            for (int p = 0; p < kP; ++p) {
+                Piece<kDt> q;
+                ring.take(q, 0, p);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s = s + Two(q.get(2 * j), q.get(2 * j + 1));
+                ring.take(q, 1, p);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) t = t + Two(q.get(2 * j), q.get(2 * j + 1));
+            }
+            v[kV - 2] = s.sum(), v[kV - 1] = t.sum();
+        }
         row_sums<kV, kCluster>(g, v);
         ring.release(1);
         if constexpr (kP == 2) {  // (unpacked once more: held as fp32 over the exchange, they do not fit)
@@ -1056,6 +1074,10 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
             }
             if (a.dx) store_piece<kDt, kVec>(static_cast<E *>(a.dx) + at, dx, cols, p, on);
             store_piece<kDt, kVec>(static_cast<E *>(a.dh) + at, dh, cols, p, on);
+        }
+        if (kAhead && ahead) {
+            mh = Two(lh ? -v[kV - 2] * inv_n : 0.f);
+            mx = Two(lx ? -v[kV - 1] * inv_n : 0.f);
         }
         if (on) at += size_t(a.cols);
         if constexpr (kGate) {

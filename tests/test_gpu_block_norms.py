@@ -238,7 +238,7 @@ def test_gradient(shape, norms, dt):
 # more rows than CTAs, of more than 8192 columns: several rows of a ring for each of them
 @pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("norms", [("rms", "rms"), ("layer", "layer")], ids="-".join)
-@pytest.mark.parametrize("shape", [(400, 8200), (330, 10001)], ids=str)
+@pytest.mark.parametrize("shape", [(400, 8200), (330, 10001), (310, 16384)], ids=str)
 def test_wide_rows(shape, norms, dt):
     ws = cf.new_workspace(cf.cf_stitch_block_norms_grad_workspace_size(*shape))
     for gates, shift in ((0, False), (shape[0], True), (shape[0] // 10, False), (1, True)):
