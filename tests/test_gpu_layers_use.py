@@ -269,3 +269,34 @@ def test_depth_of_the_ring():
         got = cf.stitch_block_norms(h, h, post="layer", pre="rms", tuning=t)
         d = cf.stitch_block_norms_grad(h, h, h, want[0], post="rms", pre="rms", tuning=t)
         assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(d[0], dwant[0])
+
+
+@pytest.mark.parametrize("shape", [(700, 1024), (170, 8200), (320, 4095)], ids=str)
+def test_depth_of_the_ring_with_means(shape):
+    """A LayerNorm's means come with the row before where the ring holds two rows, and by themselves where it holds one;
+    a row that never arrives ends both."""
+    c, v, gate, kw = bn._case(shape, "bf16", "layer", "layer", 1, True)
+    r = bn._rng(5)
+    dy, dxo = (bn._round(r.standard_normal(shape), "bf16") for _ in range(2))
+    xo = bn._round(oracle.block_norms(c["h"], c["x"], gate=gate, **v, **kw)[0], "bf16")
+    args = [bn._dev(a, "bf16") for a in (dy, dxo, c["h"], xo)]
+    dv, g = {k: bn._dev(a) for k, a in v.items()}, bn._dev(gate, "bf16")
+    ref = oracle.block_norms_grad(dy, dxo, c["h"], xo, gate=gate, **{k: a for k, a in v.items() if k != "pre_bias"}, **kw)
+    bounds = bn._grad_bounds(dy, dxo, c, xo, v, gate, kw)
+    ws = cf.new_workspace(cf.cf_stitch_block_norms_grad_workspace_size(*shape))
+    for n in (1, 2, 3, 8):
+        got = cf.stitch_block_norms_grad(*args, gate=g, **dv, **kw, workspace=ws, tuning=cf.tuning(stages=n))
+        assert cf.cf_get_device_status(ws)[0] == cf.CF_OK
+        for k, t in zip(bn.KEYS, got):
+            bn._check(t, ref[k], bounds[k], "bf16" if k in ("h", "x", "gate") else "fp32", f"d{k} {n} stages")
+    for n in (1, 2):
+        t = cf.tuning(stages=n, extra_arrivals=1, timeout_us=2000)
+        cf.stitch_block_norms_grad(*args, gate=g, **dv, **kw, workspace=ws, tuning=t)
+        assert cf.cf_get_device_status(ws)[0] == cf.CF_ERR_DEVICE_TIMEOUT
+        ws.zero_()
+        cf.stitch_block_norms(args[2], args[3], gate=g, **dv, **kw, workspace=ws, tuning=t)
+        assert cf.cf_get_device_status(ws)[0] == cf.CF_ERR_DEVICE_TIMEOUT
+        ws.zero_()
+    again = cf.stitch_block_norms_grad(*args, gate=g, **dv, **kw, workspace=ws)
+    assert cf.cf_get_device_status(ws)[0] == cf.CF_OK
+    bn._check(again[0], ref["h"], bounds["h"], "bf16", "dh")
