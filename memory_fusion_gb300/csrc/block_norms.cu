@@ -1157,7 +1157,8 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
 
 // The workers' sums added in order: 32 columns a CTA, a warp every so many-th term, then the warps.  (335 terms of 1111
 // columns by eight warps 10.5 us, which is the loads one after another.)
-constexpr int kSumWarps = 32, kSumFly = 8, kSumSms = 152;
+// Of many terms (a gate that thousands of workers share), kSumLong are in flight.
+constexpr int kSumWarps = 32, kSumFly = 8, kSumLong = 32, kSumSms = 152;
 __global__ void __launch_bounds__(kSumWarps * 32) block_norms_sums_kernel(const BlockNormsGradArgs a, int nsums, int gates_first) {
     __shared__ float part[kSumWarps][32];
     ptx::griddep_launch_dependents();
@@ -1198,7 +1199,15 @@ __global__ void __launch_bounds__(kSumWarps * 32) block_norms_sums_kernel(const 
     }
     float s = head && warp == 0 && live ? __ldcg(head + c) : 0.f;
     const int warps = int(blockDim.x) / 32;
-    for (int i = warp; i < terms; i += warps * kSumFly) {
+    int i = warp;
+    for (; i + warps * (kSumLong - 1) < terms; i += warps * kSumLong) {
+        float x[kSumLong];
+#pragma unroll
+        for (int k = 0; k < kSumLong; ++k) x[k] = live ? __ldcg(from + (i + warps * k) * step + c) : 0.f;
+#pragma unroll
+        for (int k = 0; k < kSumLong; ++k) s += x[k];
+    }
+    for (; i < terms; i += warps * kSumFly) {
         float x[kSumFly];
 #pragma unroll
         for (int k = 0; k < kSumFly; ++k)
