@@ -196,8 +196,10 @@ __device__ __forceinline__ void load_vector(Two (&x)[4], const float *v, float n
 }
 // How rows come in.
 enum RowMode : int {
-    LOOSE = 0,  // numbers that start anywhere: a thread takes every lanes-th, fp32 ones ahead of time, in copies of 4 bytes
-    SHORT = 1,  // 16-byte aligned, few columns: copies of 16 bytes ahead of time, by the thread that needs them
+    LOOSE = 0,  // numbers that start anywhere, few columns or, forward, over 16384: a thread takes every lanes-th, fp32
+                // ones ahead of time, in copies of 4 bytes
+    SHORT = 1,  // 16-byte aligned, few columns (copies of 16 bytes ahead of time, by the thread that needs them) or, forward,
+                // over 16384 (loads)
     WIDE = 2,   // 16-byte aligned, whole warps: bulk copies ahead of time, one a row
     SHIFTED = 3,  // numbers that start anywhere, whole warps: bulk copies of the 16-byte pieces that hold a row
 };
@@ -1272,7 +1274,7 @@ cudaError_t allow_smem(const void *fn, int *own) {  // own: the kernel's static 
         std::atomic<uint64_t> devices;
         std::atomic<int> own;
     };
-    static Entry table[64];  // (48 kernels)
+    static Entry table[96];  // (60 kernels)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
