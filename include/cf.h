@@ -886,9 +886,9 @@ CF_API cf_status cf_gemm_linear_grad_ex(const void *dY, const void *X, const voi
  * and on whether all pointers are 16-byte aligned: equal calls give equal bits.
  * NaNs stay in their rows (and their columns' sums).
  * Supported: cols in 0..32768, rows in 0..2^31 - 512 (0 of either is a no-op; a
- * gradient of no rows writes zeros to the sums), dtype bf16, fp16 or fp32,
- * pointers aligned to their element (16 bytes, with cols a multiple of 8, is
- * faster).
+ * gradient of no rows writes zeros to the sums and to dgate), dtype bf16, fp16
+ * or fp32, pointers aligned to their element (16 bytes, with cols a multiple of
+ * 8, is faster).
  * workspace (device) >= cf_stitch_workspace_size() bytes, the gradient
  * cf_stitch_block_norms_grad_workspace_size(), 16-byte aligned there; zeroed
  * once, as for every call.  One workspace may serve these calls, the dense

@@ -2213,9 +2213,10 @@ extern "C" cf_status cf_stitch_block_norms_grad_ex(
     for (const float *p : sums)
         if (!aligned_to(p, 4)) return CF_ERR_MISALIGNED;
     if (!aligned16(workspace)) return CF_ERR_MISALIGNED;
+    if (dgate && dgate == gate) return CF_ERR_INVALID_ARG;
     if (rows > 0) {
         if (dh == dx || dh == gate || (dx && dx == gate)) return CF_ERR_INVALID_ARG;
-        for (const void *p : {dy, dx_out, h, x_out, gate, static_cast<const void *>(dh), static_cast<const void *>(dx)})
+        for (const void *p : {dy, dx_out, h, x_out, static_cast<const void *>(dh), static_cast<const void *>(dx)})
             if (dgate && dgate == p) return CF_ERR_INVALID_ARG;
     }
     for (int i = 0; i < 4; ++i)
@@ -2227,11 +2228,10 @@ extern "C" cf_status cf_stitch_block_norms_grad_ex(
     if (st != CF_OK) return st;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (rows == 0) {  // every sum is empty
-        for (float *p : sums) {
-            const cudaError_t e = p ? cudaMemsetAsync(p, 0, size_t(cols) * 4, cs) : cudaSuccess;
-            if (e != cudaSuccess) return cuda_fail(e);
-        }
-        return CF_OK;
+        cudaError_t e = dgate && gates > 0 ? cudaMemsetAsync(dgate, 0, size_t(gates) * size_t(cols) * size, cs) : cudaSuccess;
+        for (float *p : sums)
+            if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, size_t(cols) * 4, cs);
+        return e == cudaSuccess ? CF_OK : cuda_fail(e);
     }
     cf::BlockNormsGradArgs a{};
     a.dy = dy, a.dx_out = dx_out, a.h = h, a.x_out = x_out, a.gate = gate;

@@ -71,3 +71,8 @@ def test_wrapper_refusals():
     for f in (lambda: cf.stitch_block_norms(h, h), lambda: cf.stitch_block_norms_grad(h, h, h, h, pre="rms")):
         with pytest.raises(ValueError, match="CUDA"):
             f()
+
+
+def test_gradient_of_no_rows_spares_the_gate():
+    """It writes zeros to dgate, which is then no input either."""
+    assert _grad(rows=0, gate=9 * P, gates=2, dg=9 * P) == cf.CF_ERR_INVALID_ARG
