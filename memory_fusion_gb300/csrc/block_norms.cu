@@ -304,7 +304,11 @@ struct RowRing {
         }
     }
     __device__ __forceinline__ void release(int) {}
-    __device__ __forceinline__ void finish() {}
+    // Behind the last row the copies write zeros: they have all arrived before the ring's place takes the CTA's sums (a
+    // __syncthreads alone does not wait for them), and before the CTA leaves.
+    __device__ __forceinline__ void finish() {
+        if constexpr (kOn) ptx::cp_async_wait<0>();
+    }
 };
 
 // WIDE: the row's first thread asks for whole rows (of the CTA's share) in bulk copies, which complete on an mbarrier a

@@ -1,8 +1,11 @@
 """The norms around a block at the ends of what their calls allow: gradients of no
-rows."""
+rows, and of short rows, several of which a worker takes in turn from its ring.
+
+Bounds are those of the other parity files."""
 import numpy as np
 import pytest
 
+import oracle
 from memory_fusion_gb300 import cf
 from tests import test_gpu_block_norms as bn
 from tests.gpu_util import torch_cuda
@@ -22,3 +25,34 @@ def test_gradient_of_no_rows(gates, dt):
     assert d[0].shape == d[1].shape == (0, 64)
     for want, got in zip(out[2:], d[2:]):
         assert got is want and not got.any()
+
+
+# (workers of 152 SMs: 9728 for 37, 40 and 64 columns, 4864 for 128, 77824 for 1, 1216 for 333: 2 to 4 rows each)
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("shape,gates", [((20000, 40), (1, 400, 20000)), ((20000, 37), (8, 20000)), ((15000, 64), (0, 5)),
+                                         ((12000, 128), (0, 12000)), ((80000, 1), (0, 2)), ((4000, 333), (5, 4000))], ids=str)
+@pytest.mark.parametrize("norms,shift", [(("rms", "rms"), False), (("layer", "layer"), True)], ids=str)
+def test_gradients_of_several_rows_a_worker(shape, gates, norms, shift, dt):
+    """Every sum over the rows, which the groups of a CTA add in the place where their rings were."""
+    torch = torch_cuda()
+    ws = cf.new_workspace(cf.cf_stitch_block_norms_grad_workspace_size(*shape))
+    for n in gates:
+        c, v, gate, kw = bn._case(shape, dt, *norms, n, shift)
+        r = bn._rng(5)
+        dy, dxo = bn._round(r.standard_normal(shape), dt), bn._round(r.standard_normal(shape), dt)
+        xo = bn._round(oracle.block_norms(c["h"], c["x"], gate=gate, **v, **kw)[0], dt)
+        args = [bn._dev(a, dt) for a in (dy, dxo, c["h"], xo)]
+        dv, g = {k: bn._dev(a) for k, a in v.items()}, bn._dev(gate, dt)
+        got = cf.stitch_block_norms_grad(*args, gate=g, **dv, **kw, workspace=ws)
+        ref = oracle.block_norms_grad(dy, dxo, c["h"], xo, gate=gate, **{k: a for k, a in v.items() if k != "pre_bias"}, **kw)
+        bounds = bn._grad_bounds(dy, dxo, c, xo, v, gate, kw)
+        for k, t in zip(bn.KEYS, got):
+            assert (t is not None) == (k in ("h", "x") or k in v or (k == "gate" and n > 0)), k
+            if t is not None:
+                bn._check(t, ref[k], bounds[k], dt if k in ("h", "x", "gate") else "fp32", f"d{k} {n}")
+        for _ in range(10):
+            again = cf.stitch_block_norms_grad(*args, gate=g, **dv, **kw, workspace=ws)
+            assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, again))
+        out, _ = cf.stitch_block_norms(args[2], bn._dev(c["x"], dt), gate=g, **dv, **kw)
+        bn._check(out, oracle.block_norms(c["h"], c["x"], gate=gate, **v, **kw)[0], bn._forward_bounds(c, v, gate, kw), dt,
+                  f"x_out {n}")
