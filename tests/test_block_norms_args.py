@@ -76,3 +76,10 @@ def test_wrapper_refusals():
 def test_gradient_of_no_rows_spares_the_gate():
     """It writes zeros to dgate, which is then no input either."""
     assert _grad(rows=0, gate=9 * P, gates=2, dg=9 * P) == cf.CF_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("call", [_fwd, _grad])
+def test_a_gate_of_no_rows(call):
+    """A gate goes with a number of gates, whatever the number of rows: nothing is divided by none."""
+    for rows in (0, 8):
+        assert call(rows=rows, gate=9 * P, gates=0) == cf.CF_ERR_INVALID_ARG
