@@ -2103,8 +2103,9 @@ cf_status block_norms_sizes(int64_t rows, int64_t cols, int64_t gates, const voi
                             int dtype) {
     if (rows < 0 || cols < 0 || gates < 0 || !norm_kind(int(post)) || !norm_kind(int(pre))) return CF_ERR_INVALID_ARG;
     if (dtype != CF_BF16 && dtype != CF_FP16 && dtype != CF_FP32) return CF_ERR_INVALID_ARG;
-    if ((gate && gates == 0) || (!gate && gates > 0 && rows > 0)) return CF_ERR_INVALID_ARG;
-    if (gate && rows % gates != 0) return CF_ERR_INVALID_ARG;
+    // (a gate of no columns may have no address)
+    if (cols > 0 && ((gate && gates == 0) || (!gate && gates > 0 && rows > 0))) return CF_ERR_INVALID_ARG;
+    if (gates > 0 && rows % gates != 0) return CF_ERR_INVALID_ARG;
     if (cols > cf::kBlockNormsMaxCols || rows > (int64_t(1) << 31) - 512) return CF_ERR_UNSUPPORTED;
     return CF_OK;
 }

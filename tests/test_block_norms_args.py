@@ -83,3 +83,11 @@ def test_a_gate_of_no_rows(call):
     """A gate goes with a number of gates, whatever the number of rows: nothing is divided by none."""
     for rows in (0, 8):
         assert call(rows=rows, gate=9 * P, gates=0) == cf.CF_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("call", [_fwd, _grad])
+def test_no_columns_with_gates(call):
+    """A tensor of no columns has no address; the call has nothing to do."""
+    assert call(cols=0, gate=None, gates=2) == cf.CF_OK
+    assert call(cols=0, gate=9 * P, gates=2) == cf.CF_OK
+    assert call(cols=0, gate=None, gates=3) == cf.CF_ERR_INVALID_ARG  # of 8 rows

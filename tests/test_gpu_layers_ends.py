@@ -1,5 +1,5 @@
 """The norms around a block at the ends of what their calls allow: gradients of no
-rows, and of short rows, several of which a worker takes in turn from its ring.
+rows and of no columns, and of short rows, several of which a worker takes in turn from its ring.
 
 Bounds are those of the other parity files."""
 import numpy as np
@@ -25,6 +25,18 @@ def test_gradient_of_no_rows(gates, dt):
     assert d[0].shape == d[1].shape == (0, 64)
     for want, got in zip(out[2:], d[2:]):
         assert got is want and not got.any()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_no_columns_with_gates(dt):
+    torch = torch_cuda()
+    n, g, w = (bn._dev(np.ones(s), t) for s, t in (((6, 0), dt), ((3, 0), dt), ((0,), "fp32")))
+    kw = dict(post="rms", pre="rms", gate=g, post_weight=w, pre_weight=w)
+    xo, y = cf.stitch_block_norms(n, n, **kw)
+    assert xo.shape == y.shape == (6, 0)
+    d = cf.stitch_block_norms_grad(n, n, n, xo, **kw)
+    assert d[0].shape == (6, 0) and d[2].shape == (3, 0) and d[3].shape == d[5].shape == (0,)
+    torch.cuda.synchronize()
 
 
 # (workers of 152 SMs: 9728 for 37, 40 and 64 columns, 4864 for 128, 77824 for 1, 1216 for 333: 2 to 4 rows each)
