@@ -588,8 +588,11 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const Logpr
     const bool none = lse == -inf();
     // -inf may count as a low finite number (see Pack) where its distance from lse is large, and finite
     const float least = P::least(a.scale * kLog2E) * a.scale;
-    const bool plain = lse > least && fabsf(lse) < P::most(a.scale) && !none;
     const uint32_t low = P::low();
+    // (... and where c0 + c1 d, too, is finite there, or 0 times it would be a NaN)
+    const float lowest = P{{low, low, low, low}}.get(0);
+    const bool finite = !kEntropy || fabsf(fmaf(-dh, fmaf(lowest, a.scale, -lse), c0)) < 3e38f;
+    const bool plain = lse > least && fabsf(lse) < P::most(a.scale) && !none && finite;
     const Two scale(a.scale), shift(-lse), log2e(kLog2E), k0(c0), k1(-dh);
 #pragma unroll 1
     for (; w < end; w += kFly * kGradThreads) {

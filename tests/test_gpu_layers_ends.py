@@ -1,5 +1,7 @@
-"""The norms around a block at the ends of what their calls allow: gradients of no
-rows and of no columns, and of short rows, several of which a worker takes in turn from its ring.
+"""The norms around a block and the log probabilities at the ends of what their
+calls allow: gradients of no rows and of no columns, and of short rows, several of
+which a worker takes in turn from its ring; entropy gradients so large that one
+times a masked token's distance leaves fp32's range.
 
 Bounds are those of the other parity files."""
 import numpy as np
@@ -8,6 +10,7 @@ import pytest
 import oracle
 from memory_fusion_gb300 import cf
 from tests import test_gpu_block_norms as bn
+from tests import test_gpu_logprobs as lp
 from tests.gpu_util import torch_cuda
 
 pytestmark = pytest.mark.gpu
@@ -68,3 +71,27 @@ def test_gradients_of_several_rows_a_worker(shape, gates, norms, shift, dt):
         out, _ = cf.stitch_block_norms(args[2], bn._dev(c["x"], dt), gate=g, **dv, **kw)
         bn._check(out, oracle.block_norms(c["h"], c["x"], gate=gate, **v, **kw)[0], bn._forward_bounds(c, v, gate, kw), dt,
                   f"x_out {n}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("scale,size", [(1.0, 2.0 ** 28), (1000.0, 64.0), (2.0 ** -10, 2.0 ** 40)], ids=str)
+def test_large_entropy_gradients(scale, size, dt):
+    """A masked token's probability is 0, and so is its gradient, whatever the loss is scaled by."""
+    T, V = 9, 1003
+    r = lp._rng(11)
+    z = r.standard_normal((T, V)) * (2.5 / scale)
+    mask = r.random((T, V)) < 0.5
+    mask[0] = False
+    mask[1, :] = np.arange(V) != 500
+    t = r.integers(0, V, T)
+    mask[np.arange(T), t] = False
+    z[mask] = -np.inf
+    z = lp._round(z, dt)
+    zd, td = lp._dev(z, dt), lp._i64(t)
+    f = cf.stitch_logprobs(zd, td, scale=scale)
+    lse, ent = lp._host(f[1]), lp._host(f[2])
+    dlp, dh = (size * r.standard_normal((2, T))).astype(np.float32)
+    got = cf.stitch_logprobs_grad(zd, td, f[1], lp._dev(dlp), entropy=f[2], dentropy=lp._dev(dh), scale=scale)
+    ref = oracle.logprobs_grad(z, t, dlogprob=dlp, dentropy=dh, scale=scale, lse=lse, entropy=ent)
+    assert not lp._host(got)[mask].any()
+    lp._within(got, ref, lp._grad_bound(z, t, scale, lse, ent, dlp, None, dh, dt, ref), f"{scale} {size}")
