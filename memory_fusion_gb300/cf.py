@@ -1162,9 +1162,10 @@ def stitch_block_norms_grad(dy, dx_out, h, x_out, *, post="none", post_weight=No
                             scale=1.0, alpha=1.0, pre="none", pre_weight=None, pre_bias=None, eps=1e-5, dx=True,
                             out=None, workspace=None, stream=None, tuning=None):
     """(dh, dx, dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias) of stitch_block_norms for the gradients dy of y
-    and dx_out of x' ([T, N]; one may be None: 0): those of what is given there, fp32 for weights and biases, None in
-    the place of the others and, with dx=False, of dx.  h and x_out ([T, N]) are the forward pass's input and output.
-    `out`: seven outputs, None for new ones; dh and dx may be dy, dx_out, h or x_out."""
+    and dx_out of x' ([T, N]): those of what is given there, fp32 for weights and biases, None in the place of the others
+    and, with dx=False, of dx.  dy goes with a Pre norm, dx_out may then be None (0); where only x' was used, the call is
+    one with pre "none" (dy None, x_out not read, no gradients of Pre's weight and bias).  h and x_out ([T, N]) are the
+    forward pass's input and output.  `out`: seven outputs, None for new ones; dh and dx may be dy, dx_out, h or x_out."""
     torch = _torch or _the_torch()
     dt, dev, dtype, f32 = _row_dtype("h", h), h.device, h.dtype, torch.float32
     if _away(dev, stream):
@@ -1177,7 +1178,7 @@ def stitch_block_norms_grad(dy, dx_out, h, x_out, *, post="none", post_weight=No
     rows, cols = _sizes("h", h, 2)
     po, pr = _norm("post", post, post_weight, post_bias), _norm("pre", pre, pre_weight, pre_bias)
     if (dy is None) == (pr != CF_NORM_NONE):
-        raise ValueError("dy goes with a norm before the next block")
+        raise ValueError("dy goes with a norm before the next block (pre \"none\" where only x' was used)")
     gates, vector = _gates(gate, rows), (cols,)
     ph, pxo = _operand("h", h, like, dtype, dev), _operand("x_out", x_out, like, dtype, dev)
     pdy, pdx = _operand("dy", dy, like, dtype, dev), _operand("dx_out", dx_out, like, dtype, dev)

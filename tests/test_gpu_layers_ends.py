@@ -73,6 +73,23 @@ def test_gradients_of_several_rows_a_worker(shape, gates, norms, shift, dt):
                   f"x_out {n}")
 
 
+@pytest.mark.parametrize("shape", [(24, 200), (6, 1111), (10, 4096)], ids=str)
+def test_gradient_where_only_the_stream_was_used(shape):
+    """y had no part in the loss: the call with pre "none", which reads neither x' nor Pre's weight, is the one of zeros
+    for dy."""
+    torch = torch_cuda()
+    c, v, gate, kw = bn._case(shape, "bf16", "rms", "rms", 2, False)
+    h, dxo, g, w = bn._dev(c["h"], "bf16"), bn._dev(c["x"], "bf16"), bn._dev(gate, "bf16"), bn._dev(v["post_weight"])
+    kw = dict(kw, post_weight=w, gate=g)
+    got = cf.stitch_block_norms_grad(None, dxo, h, None, **dict(kw, pre="none"))
+    want = cf.stitch_block_norms_grad(torch.zeros_like(h), dxo, h, dxo, pre_weight=bn._dev(v["pre_weight"]), **kw)
+    assert got[4:] == (None, None, None) and not want[5].any()
+    for a, b in zip(got[:4], want[:4]):
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError, match="pre"):
+        cf.stitch_block_norms_grad(None, dxo, h, None, **kw)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 @pytest.mark.parametrize("scale,size", [(1.0, 2.0 ** 28), (1000.0, 64.0), (2.0 ** -10, 2.0 ** 40)], ids=str)
 def test_large_entropy_gradients(scale, size, dt):
