@@ -733,7 +733,7 @@ __global__ void __maxnreg__(kP == 4 && !is_bulk(kMode) ? 64 : 128) block_norms_k
     if (xo) xo += size_t(first) * a.cols;
     if (yo) yo += size_t(first) * a.cols;
     for (int i = 0; i < turns; ++i) {
-        const bool on = first + i < last;
+        const bool on = i < last - first;  // (behind the last row first + i may pass 2^31)
         ring.turn();
         if (a.gates_along) {
             if (on) take_gate(first + i, true);
@@ -970,8 +970,8 @@ __global__ void __launch_bounds__(512) block_norms_grad_kernel(const BlockNormsG
     const bool ahead = kAhead && a.ring.depth >= 2 && (lh || lx);
     Two mh(0.f), mx(0.f);  // less the LayerNorms' means
     for (int i = 0; i < turns; ++i) {
-        const int r = first + i;
-        const bool on = kWide || r < last;
+        const bool on = kWide || i < last - first;
+        const int r = on ? first + i : last;  // (behind the last row first + i may pass 2^31)
         ring.turn();
         if (gates_along && on) take_gate(r, true);
         Piece<kDt> raw[4][kP];

@@ -90,6 +90,40 @@ def test_gradient_where_only_the_stream_was_used(shape):
         cf.stitch_block_norms_grad(None, dxo, h, None, **kw)
 
 
+@pytest.mark.parametrize("N", [1, 8])
+def test_most_rows(N):
+    """The largest number of rows: workers without rows, or with fewer than others, write nothing behind the last one."""
+    torch = torch_cuda()
+    T, guard = 2 ** 31 - 512, 1 << 20
+    if torch.cuda.mem_get_info()[0] < 4 * 2 * T * N + (8 << 30):
+        pytest.skip("too little device memory")
+
+    def rows():
+        t = torch.full((T * N + guard,), 3.0, dtype=torch.bfloat16, device="cuda")
+        return t, t[:T * N].view(T, N)
+
+    def check(base, t, scale):
+        assert (base[T * N:] == 3.0).all()
+        for lo in range(0, T, 1 << 27):
+            assert torch.equal(t[lo:lo + (1 << 27)], h[lo:lo + (1 << 27)] * scale)
+
+    _, h = rows()
+    h.view(-1)[:] = torch.randn(1 << 16, device="cuda").bfloat16().repeat(T * N // (1 << 16) + 1)[:T * N]
+    base, out = rows()
+    cf.stitch_block_norms(h, None, scale=2.0, out=out)
+    check(base, out, 2.0)
+    base.fill_(3.0)
+    cf.stitch_block_norms(h, None, pre="rms", out=out, norm_out=(more := rows())[1])
+    check(base, out, 1.0)
+    x = h[-4096:].double()
+    bound = bn.HALF["bf16"] + bn.K
+    want = x * torch.rsqrt(x.square().mean(1, keepdim=True) + 1e-5)
+    assert (more[0][T * N:] == 3.0).all() and ((more[1][-4096:].double() - want).abs() <= bound * want.abs()).all()
+    base.fill_(3.0)
+    cf.stitch_block_norms_grad(None, h, h, None, scale=0.5, out=[out] + [None] * 6, dx=False)
+    check(base, out, 0.5)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 @pytest.mark.parametrize("scale,size", [(1.0, 2.0 ** 28), (1000.0, 64.0), (2.0 ** -10, 2.0 ** 40)], ids=str)
 def test_large_entropy_gradients(scale, size, dt):
