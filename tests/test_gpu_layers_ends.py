@@ -124,6 +124,35 @@ def test_most_rows(N):
     check(base, out, 0.5)
 
 
+def test_dense_layer_of_most_rows():
+    """The largest number of rows, whole numbers: equal to the call of its last rows, and nothing behind them."""
+    torch = torch_cuda()
+    M, tail, guard = 2 ** 31 - 512, 2000, 1 << 20
+    if torch.cuda.mem_get_info()[0] < 110 << 30:
+        pytest.skip("too little device memory")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    few = torch.randint(-2, 3, (1 << 16, 8), generator=g, device="cuda").bfloat16()
+    W = torch.randint(-2, 3, (8, 8), generator=g, device="cuda").bfloat16()
+    b = torch.randint(-2, 3, (8,), generator=g, device="cuda").float()
+    X = torch.empty(M, 8, dtype=torch.bfloat16, device="cuda")
+    for lo in range(0, M, 1 << 16):
+        X[lo:lo + (1 << 16)] = few[:min(1 << 16, M - lo)]
+    base = torch.full((M * 8 + guard,), 3.0, dtype=torch.bfloat16, device="cuda")
+    Y = base[:M * 8].view(M, 8)
+    cf.gemm_linear(X, W, b, act="relu", out=Y)
+    want = cf.gemm_linear(few, W, b, act="relu")
+    for lo in (0, M // (1 << 17) << 16, M >> 16 << 16):
+        n = min(1 << 16, M - lo)
+        assert torch.equal(Y[lo:lo + n], want[:n])
+    assert (base[M * 8:] == 3.0).all()
+    Y.zero_()
+    Y[-tail:] = torch.randint(-2, 3, (tail, 8), generator=g, device="cuda").bfloat16()
+    dx, dw, db = cf.gemm_linear_grad(Y, X, W)
+    wx, ww, wb = cf.gemm_linear_grad(Y[-tail:].clone(), X[-tail:].clone(), W)
+    assert torch.equal(dx[-tail:], wx) and not dx[:M - tail].any()
+    assert torch.equal(dw, ww) and torch.equal(db, wb)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 @pytest.mark.parametrize("scale,size", [(1.0, 2.0 ** 28), (1000.0, 64.0), (2.0 ** -10, 2.0 ** 40)], ids=str)
 def test_large_entropy_gradients(scale, size, dt):
@@ -146,3 +175,37 @@ def test_large_entropy_gradients(scale, size, dt):
     ref = oracle.logprobs_grad(z, t, dlogprob=dlp, dentropy=dh, scale=scale, lse=lse, entropy=ent)
     assert not lp._host(got)[mask].any()
     lp._within(got, ref, lp._grad_bound(z, t, scale, lse, ent, dlp, None, dh, dt, ref), f"{scale} {size}")
+
+
+def test_log_probabilities_of_most_rows():
+    torch = torch_cuda()
+    T, V, n = 2 ** 27, 5, 1 << 14
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("too little device memory")
+    few, t = lp._case((n, V, 0), "bf16", "masked")
+    zf, tf = lp._dev(few, "bf16"), lp._i64(t)
+    z, td = zf.repeat(T // n, 1), tf.repeat(T // n)
+    got = cf.stitch_logprobs(z, td, top=2)
+    want = cf.stitch_logprobs(zf, tf, top=2)
+    lp._check(want, few, t, 1.0, 2)
+    one = torch.ones(T, device="cuda")
+    d = cf.stitch_logprobs_grad(z, td, got[1], one, entropy=got[2], dentropy=one)
+    for lo in (0, T // 2, T - n):
+        assert all(torch.equal(a[lo:lo + n], b) for a, b in zip(got, want))
+    assert torch.equal(d[T - n:], cf.stitch_logprobs_grad(zf, tf, want[1], one[:n], entropy=want[2], dentropy=one[:n]))
+    ref = oracle.logprobs_grad(few, t, dlogprob=np.ones(n), dentropy=np.ones(n), lse=lp._host(want[1]),
+                               entropy=lp._host(want[2]))
+    bound = lp._grad_bound(few, t, 1.0, lp._host(want[1]), lp._host(want[2]), np.ones(n), None, np.ones(n), "bf16", ref)
+    lp._within(d[T - n:], ref, bound, "gradient")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_log_probabilities_of_the_largest_vocabulary(dt):
+    z, t = lp._case((2, 2 ** 24, 0), dt, "masked")
+    t = np.array([2 ** 24 - 1, 0])
+    z[[0, 1], t] = 12.0
+    got = cf.stitch_logprobs(lp._dev(z, dt), lp._i64(t), top=32)
+    lp._check(got, z, t, 1.0, 32)
+    d = cf.stitch_logprobs_grad(lp._dev(z, dt), lp._i64(t), got[1], lp._dev(np.ones(2)))
+    ref = oracle.logprobs_grad(z, t, dlogprob=np.ones(2), lse=lp._host(got[1]))
+    lp._within(d, ref, lp._grad_bound(z, t, 1.0, lp._host(got[1]), None, np.ones(2, np.float32), None, None, dt, ref), "gradient")
