@@ -500,7 +500,8 @@ struct BulkRing {
             bar -= 8 * ring.depth;
         }
     }
-    // nothing is on its way when the CTA leaves (after a wait that ran out there might be)
+    // Nothing is on its way when the CTA leaves (after a wait that ran out there might be), and the place is free for the
+    // CTA's sums.  (The row's other threads are through with the barriers: each row's exchange is behind its wait.)
     __device__ __forceinline__ void finish() {
         if (!leader) return;
         volatile uint32_t local = 0;
@@ -508,6 +509,7 @@ struct BulkRing {
         for (int s = 0; s < ring.depth && s < issued; ++s)
             ptx::mbar_wait_bounded(bar + 8 * (s - stage), uint32_t((issued - 1 - s) / ring.depth) & 1u, ring.timeout_ns,
                                    &local, nullptr, 0);
+        for (int s = 0; s < ring.depth; ++s) ptx::mbar_inval(bar + 8 * (s - stage));
     }
 };
 template <int kDt, int kRows, int kP>
