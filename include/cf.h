@@ -814,7 +814,8 @@ CF_API cf_status cf_gemm_lora_ex(const void *X, const void *W, const float *bias
  * cf_gemm_linear_grad: of the gradient dY [M, N] of Y,
  *   dZ = dY * act'(Z), dX = dZ . W^T [M, K], dW = X^T . dZ [K, N],
  *   dbias = sum over the rows of dZ (fp32 [N]; of the unrounded dZ)
- *   (R's is dY itself).  dX, dW and dbias may each be NULL: not wanted (X may
+ *   (R's is dY itself).  The two products take dZ as it is stored, rounded to
+ *   `dtype`.  dX, dW and dbias may each be NULL: not wanted (X may
  *   then be NULL without dW, W without dX).  With an activation Z and dZ
  *   (`dtype` [M, N], written) are required, and dZ may be Z or dY; without one
  *   both are NULL.  Up to three launches.
@@ -959,10 +960,13 @@ CF_API cf_status cf_stitch_block_norms_grad_ex(const void *dy, const void *dx_ou
  *   dlogits = scale * (dlogprob * (1[target] - p) + dlse * p
  *                      - dentropy * p * (log p + entropy)),  log p = z - lse,
  *   with the given lse and entropy: p is as good as lse is, which holds fp32's 24
- *   bits.  A row whose lse is -inf has zeros, a target of -1 no dlogprob.
+ *   bits; one below 2^-126 counts as 0.  A row whose lse is -inf has zeros, a
+ *   target of -1 no dlogprob.
  *   dlogits (device) `dtype` [rows, vocab], rows `dstride` apart, written; what
- *   lies between rows is not.  It may be logits (with the same stride).  The top
- *   log probabilities have no gradient here.
+ *   lies between rows is not.  It may be logits (with the same stride).  Rows that
+ *   start where the logits' do, modulo 16 bytes, are written 16 bytes at a time
+ *   (the same stride and base alignment); others number by number, up to four
+ *   times slower.  The top log probabilities have no gradient here.
  * Sums are fp32, in an order that depends on the sizes (and where in 16 bytes a
  * row starts) alone: equal calls give equal bits.
  * Supported: vocab in 0..2^24 (0 with rows > 0: the gradient alone, a no-op),

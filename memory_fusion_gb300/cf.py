@@ -1022,7 +1022,8 @@ def gemm_linear_grad(dY, X, W, *, act="none", preact=None, input=True, weight=Tr
     """(dX, dW, dbias) of Y = act(X @ W + bias) + residual for the gradient dY [M, N] of Y (the residual's own is dY);
     input, weight and bias say which are wanted (None in the place of the others; X may be None without weight, W
     without input).  `preact` is what gemm_linear kept, needed with an activation; `dz` ([M, N], made where not given)
-    then receives dY * act'(preact), and may be preact or dY.  dbias is fp32.  `out`: three outputs, None for new ones."""
+    then receives dY * act'(preact), which the two products take rounded to dY's dtype, and may be preact or dY.  dbias is
+    fp32, of the unrounded values.  `out`: three outputs, None for new ones."""
     f32 = (_torch or _the_torch()).float32
     (M, N), dev, dtype, dt = _first("dY", dY, 2)
     if _away(dev, stream):
@@ -1274,7 +1275,8 @@ def stitch_logprobs_grad(logits, targets, lse, dlogprob=None, *, dlse=None, entr
                          out=None, workspace=None, stream=None, tuning=None):
     """The gradient of the logits [T, V] (in their dtype) for the gradients dlogprob, dlse and dentropy (fp32 [T], None:
     0) of stitch_logprobs' results; lse and, with dentropy, entropy are its results.  `out` may be logits, or rows
-    apart like theirs."""
+    apart like theirs, which is up to four times faster than the contiguous one that is made without it where logits' rows
+    lie apart and are of no whole 16 bytes."""
     torch = _torch or _the_torch()
     dt, dev, dtype, f32 = _row_dtype("logits", logits), logits.device, logits.dtype, torch.float32
     if _away(dev, stream):

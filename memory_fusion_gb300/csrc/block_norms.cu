@@ -12,9 +12,10 @@
 // over a row go by shuffles, then through shared memory, of every CTA of the cluster where there are several.  A norm's
 // squares are taken about a mean, never about zero, so nothing cancels.
 // 16384 x 4096 bf16, RMSNorms, eight gates: forward 94 us (5.7 TB/s), gradient 147 (5.5; 138 and 9 for the sums).  What is
-// left are the waits of a row's exchanges, one after another, and the instructions between them.  With LayerNorms and biases
-// 1.6 times that.  Rows that start anywhere (odd widths of 16-bit numbers) are read from shared memory and stored number
-// by number: about 2 times (forward) and 2.8 times (gradient) what aligned ones take.
+// left are the waits of a row's exchanges, one after another, and the instructions between them.  8192 x 4096 bf16 with
+// LayerNorms and biases: forward 83 us, gradient 135, 1.75 and 1.85 times what RMSNorms take of half as many rows as above.
+// Rows that start anywhere are read from shared memory and stored number by number: 8192 x 4095 bf16 with RMSNorms 98 and
+// 222 us, 2.1 and 3.0 times what aligned ones take; with LayerNorms and biases 133 and 251, 1.6 and 1.9 times.
 //
 // The gradients of the weights are sums over all rows: a thread keeps its columns' sums in registers over a stretch of
 // neighbouring rows, and a second, small launch adds the stretches in order (so equal calls give equal bits).  A gate
@@ -850,7 +851,8 @@ __host__ __device__ constexpr int kept_bytes(bool gate, bool full, int pieces, i
 //     d  = dx' + r2 (g2 - mean(g2) - x^ mean(g2 x^)),
 //     sum w1 d h^ = r1 (sum w1 hc dx' + r2 (sum w1 hc g2 - mean(g2) sum w1 hc - r2 mean(g2 x^) sum w1 hc xc)),
 // so one exchange between the threads serves where three would follow one another (16384 x 4096 bf16: 287 us with
-// three).  A LayerNorm's means come one exchange before: that of the row before, where the ring holds two rows.
+// three; fp32 gradients are 1.4e-7 off, where sums one after another in fp32 leave 1.2e-7).  A LayerNorm's means come one
+// exchange before: that of the row before, where the ring holds two rows.
 // (Rows ahead kept in registers left no room for the sums: 16384 x 4096 bf16 172 us, 158 with the ring in shared memory.)
 // kFull: LayerNorms or biases, too.  kGate: a gate, whose rows' sums are closed where the next gate begins.
 // kP pieces a thread, up to 512 threads an SM with 128 registers: two where those hold them (not with biases' sums), so

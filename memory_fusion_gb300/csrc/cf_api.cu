@@ -1893,6 +1893,8 @@ cf_status linear_device(cf::DeviceInfo *dev) {
 // One group, whose rows the host knows: CTA pairs with tiles of as many rows as fill their last round best.  (8192 rows of
 // 2048 x 8192, the input's gradient: 201 us with single CTAs and divided tiles, 173 with pairs and tiles of 256 rows, four
 // rounds of which the last is 37 % full.)  Single CTAs stay where the model of cycles sees them a fifth ahead: few tiles.
+// Against every width and both CTA counts over 120 random sizes the choice takes 3.1 % (LINEAR) and 3.6 % (DGRAD) more time
+// than the best one in the geometric mean, where pairs of 128 columns would serve some hundred rows best up to 1.6 times.
 void plan_linear_tiles(int kind, int64_t M, int64_t F, int64_t C, cf_tuning *t, int *tile_rows) {
     *tile_rows = 0;
     if (t->n_slice != 0 || t->cluster_m != 0) return;

@@ -48,11 +48,12 @@
 //              [184, 1.54]; one row, rank 16: 14.6 us, 64 requests of one row: 25 us (the chain X . A, join, H . B, join
 //              beside 33 MB of W); 1537 rows of 40 requests, 2048 x 2056, rank 24: 43 us (the chain, then row tiles
 //              that requests do not fill)
-//     LINEAR   16384 rows, 2048 x 8192, bias, GELU, pre-activation kept: the tensor pipe (90 % active), 300 us (1.83
-//              PFLOP/s); one row, 4096 x 4096, bias and residual: latency, 11.6 us (launch 2, table 1, 33 MB of W at
-//              6 TB/s, joining the pieces 1.5)
+//     LINEAR   16384 rows, 2048 x 8192, bias, GELU, pre-activation kept: the tensor pipe (90 % active), 300 to 311 us
+//              (1.77 to 1.83 PFLOP/s); one row, 4096 x 4096, bias and residual: latency, 11.6 us (launch 2, table 1,
+//              33 MB of W at 6 TB/s, joining the pieces 1.5)
 // With one group of all rows (LINEAR, and DGRAD without offsets) the rows are cut into equal tiles of the height, from 128
-// to 256, that fills the last round of CTA pairs best: DGRAD of 8192 rows, 2048 from 8192, 148 us with 224 rows, 174 with 256.
+// to 256, that fills the last round of CTA pairs best: DGRAD of 8192 rows, 2048 from 8192, 159 us with 224 rows, 169 with
+// 256 (another time 148 and 174); WGRAD of that size, whose tiles are not cut, 182.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -12,10 +12,15 @@
 // overflow.)  Where few rows leave SMs idle a cluster of CTAs shares a row.
 //
 // Rows start anywhere: a row is cut at 16-byte boundaries of its memory into windows, the first and last of which may be
-// partial and are read number by number.
+// partial and are read number by number.  The gradient's windows are the logits': into rows that start elsewhere in 16
+// bytes it stores number by number (4096 x 32003 bf16 of rows 32064 apart: into rows as far apart 82 us, into contiguous
+// ones 310; fp32 into contiguous ones 178, floor 156).
 //
 // What stands between the loads and HBM's rate is the instructions: 17 a number at first (322 us for 4096 x 128000 bf16), 10
-// now (200 us with eight top tokens, 5.2 TB/s; without top tokens 163, 6.4 TB/s; the gradient 308, the copy's rate).
+// now (200 us with eight top tokens, 5.2 TB/s; without top tokens 163, 6.4 TB/s; without the entropy either 158; the
+// gradient 308, the copy's rate, without the entropy's 305).
+// d is the difference times scale log2 e, a factor rounded once, and 2^d the hardware's: two steps of fp32 (2^-22) and 3
+// half steps of |d| ln 2 of each term, which is what the log probabilities are off by (some 8e-8 of their size).
 // So numbers are worked on in pairs, maxima are taken of 16-bit pairs as they are, and -inf, whose 0 times -inf would be a
 // NaN in the entropy, is raised to a low finite number as a pair too, where the running maximum shows that this changes
 // nothing; elsewhere (rows of nothing but masks) number by number.
