@@ -960,7 +960,9 @@ CF_API cf_status cf_stitch_block_norms_grad_ex(const void *dy, const void *dx_ou
  *   dlogits = scale * (dlogprob * (1[target] - p) + dlse * p
  *                      - dentropy * p * (log p + entropy)),  log p = z - lse,
  *   with the given lse and entropy: p is as good as lse is, which holds fp32's 24
- *   bits; one below 2^-126 counts as 0.  A row whose lse is -inf has zeros, a
+ *   bits (off by 2^-24 |lse| of itself; a row of logits of the type's lowest
+ *   number alone has an lse that says nothing of their count, and no gradient of
+ *   use); one below 2^-126 counts as 0.  A row whose lse is -inf has zeros, a
  *   target of -1 no dlogprob.
  *   dlogits (device) `dtype` [rows, vocab], rows `dstride` apart, written; what
  *   lies between rows is not.  It may be logits (with the same stride).  Rows that

@@ -1274,7 +1274,8 @@ def stitch_logprobs(logits, targets=None, *, scale=1.0, top=0, entropy=True, out
 def stitch_logprobs_grad(logits, targets, lse, dlogprob=None, *, dlse=None, entropy=None, dentropy=None, scale=1.0,
                          out=None, workspace=None, stream=None, tuning=None):
     """The gradient of the logits [T, V] (in their dtype) for the gradients dlogprob, dlse and dentropy (fp32 [T], None:
-    0) of stitch_logprobs' results; lse and, with dentropy, entropy are its results.  `out` may be logits, or rows
+    0) of stitch_logprobs' results; lse and, with dentropy, entropy are its results: probabilities are off by 2^-24 |lse| of
+    themselves, so a row that a mask of the type's lowest number leaves nothing of has no gradient of use.  `out` may be logits, or rows
     apart like theirs, which is up to four times faster than the contiguous one that is made without it where logits' rows
     lie apart and are of no whole 16 bytes."""
     torch = _torch or _the_torch()
